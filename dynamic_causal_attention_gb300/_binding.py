@@ -49,12 +49,31 @@ EXPORTED = (
     "saf_trace_count",
     "saf_trace_get",
     "saf_debug_forward_hold",
+    "saf_cache_layer_layout",
+    "saf_cache_append",
+    "saf_cache_attn_workspace_size",
+    "saf_cache_attn",
+    "saf_cache_fork",
+    "saf_cache_pages_workspace_size",
+    "saf_cache_grow",
+    "saf_cache_compact",
 )
 
 
 class saf_attn_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
                 ("d_h", ctypes.c_int), ("dtype", ctypes.c_int), ("H_kv", ctypes.c_int)]
+
+
+class saf_cache_dims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int),
+                ("d_h", ctypes.c_int), ("page_stride", ctypes.c_size_t)]
+
+
+class saf_cache_layout(ctypes.Structure):
+    _fields_ = [("H_k", ctypes.c_int), ("v", ctypes.c_size_t), ("k_scale", ctypes.c_size_t),
+                ("v_scale", ctypes.c_size_t), ("bytes", ctypes.c_size_t)]
 
 
 class SafError(RuntimeError):
@@ -123,6 +142,25 @@ _lib.saf_trace_get.argtypes = [_i, ctypes.POINTER(ctypes.c_char_p), ctypes.POINT
 _lib.saf_trace_get.restype = _i
 _lib.saf_debug_forward_hold.argtypes = [_i]
 _lib.saf_debug_forward_hold.restype = _i
+_cd = ctypes.POINTER(saf_cache_dims)
+_lib.saf_cache_layer_layout.argtypes = [_cd, ctypes.c_char_p, ctypes.POINTER(saf_cache_layout)]
+_lib.saf_cache_layer_layout.restype = _i
+_lib.saf_cache_append.argtypes = [_cd, ctypes.c_char_p, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp]
+_lib.saf_cache_append.restype = _i
+_lib.saf_cache_attn_workspace_size.argtypes = [_cd, _i]
+_lib.saf_cache_attn_workspace_size.restype = _sz
+_lib.saf_cache_attn.argtypes = [_cd, ctypes.c_char_p, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _sz, _vp]
+_lib.saf_cache_attn.restype = _i
+_lib.saf_cache_fork.argtypes = [_cd, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.saf_cache_fork.restype = _i
+_lib.saf_cache_pages_workspace_size.argtypes = [_cd]
+_lib.saf_cache_pages_workspace_size.restype = _sz
+_lib.saf_cache_grow.argtypes = [_cd, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _sz, _vp]
+_lib.saf_cache_grow.restype = _i
+_lib.saf_cache_compact.argtypes = [_cd, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.saf_cache_compact.restype = _i
 
 
 def lib():
@@ -236,3 +274,54 @@ def saf_get_device_status(workspace_or_handle, is_calib_handle, stream):
     st = _lib.saf_get_device_status(workspace_or_handle, int(is_calib_handle),
                                     ctypes.byref(site), stream)
     return st, site.value
+
+
+def _cache_dims(n_seqs, max_pages, n_pages, page_size, H, H_kv, d_h, page_stride):
+    return saf_cache_dims(int(n_seqs), int(max_pages), int(n_pages), int(page_size), int(H),
+                          int(H_kv), int(d_h), int(page_stride))
+
+
+def saf_cache_layer_layout(dims, head_is_static: bytes):
+    layout = saf_cache_layout()
+    st = _lib.saf_cache_layer_layout(ctypes.byref(dims), head_is_static, ctypes.byref(layout))
+    return st, layout
+
+
+def saf_cache_append(dims, head_is_static: bytes, layer, K, V, dtype, n_q, n_new, seq_len,
+                     page_table, stream) -> int:
+    return _lib.saf_cache_append(ctypes.byref(dims), head_is_static, layer, K, V, dtype, n_q,
+                                 n_new, seq_len, page_table, stream)
+
+
+def saf_cache_attn_workspace_size(dims, n_q) -> int:
+    return _lib.saf_cache_attn_workspace_size(ctypes.byref(dims), int(n_q))
+
+
+def saf_cache_attn(dims, head_is_static: bytes, layer, Q, alpha, rho, T_pat, n_q, n_new, seq_len,
+                   page_table, out, lse, workspace, ws_bytes, stream) -> int:
+    return _lib.saf_cache_attn(ctypes.byref(dims), head_is_static, layer, Q, alpha, rho, T_pat,
+                               n_q, n_new, seq_len, page_table, out, lse, workspace, ws_bytes,
+                               stream)
+
+
+def saf_cache_fork(dims, parent, page_table, seq_len, ref, page_table_out, seq_len_out, ref_out,
+                   stream) -> int:
+    return _lib.saf_cache_fork(ctypes.byref(dims), parent, page_table, seq_len, ref,
+                               page_table_out, seq_len_out, ref_out, stream)
+
+
+def saf_cache_pages_workspace_size(dims) -> int:
+    return _lib.saf_cache_pages_workspace_size(ctypes.byref(dims))
+
+
+def saf_cache_grow(dims, pool, page_bytes, n_new, page_table, seq_len, ref, page_table_out,
+                   seq_len_out, ref_out, granted, n_short, workspace, ws_bytes, stream) -> int:
+    return _lib.saf_cache_grow(ctypes.byref(dims), pool, page_bytes, n_new, page_table, seq_len,
+                               ref, page_table_out, seq_len_out, ref_out, granted, n_short,
+                               workspace, ws_bytes, stream)
+
+
+def saf_cache_compact(dims, pool, page_bytes, page_table, ref, page_table_out, ref_out, n_used,
+                      workspace, ws_bytes, stream) -> int:
+    return _lib.saf_cache_compact(ctypes.byref(dims), pool, page_bytes, page_table, ref,
+                                  page_table_out, ref_out, n_used, workspace, ws_bytes, stream)

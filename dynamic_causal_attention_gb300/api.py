@@ -12,7 +12,8 @@ import torch
 
 from . import _binding as B
 
-__all__ = ["HybridAttention", "Calibration", "fit_compact", "num_select", "SafError"]
+__all__ = ["HybridAttention", "Calibration", "PagedCache", "fit_compact", "num_select",
+           "SafError"]
 
 SafError = B.SafError
 
@@ -147,6 +148,198 @@ class Calibration:
             self.close()
         except Exception:
             pass
+
+
+class PagedCache:
+    """Keys and values of past tokens in pages of a pool, held in 8 bits, for serving the
+    hybrid layers token by token.
+
+    ``layers`` has one list of host booleans of length H for each layer: its frozen heads.
+    ``H_kv`` < H groups the K/V heads as in HybridAttention.  The cache has ``n_seqs`` slots
+    (rows of ``page_table`` [n_seqs, max_pages], int32), ``n_pages`` pages of ``page_size``
+    tokens each, a token count for each slot (``seq_len``) and a count of the rows that hold
+    each page (``ref``); all live on the GPU and may be given by the caller.  A page holds its
+    tokens of every layer: ``pool`` is [n_pages, bytes of a page].
+
+    One step of serving::
+
+        granted, n_short = cache.grow(n_new)         # pages for the tokens to come
+        for layer ...:
+            cache.append(layer, k, v, n_new=granted)
+            out, lse = cache.attend(layer, q, alpha, rho, n_new=granted)
+
+    ``fork`` copies, reorders and frees slots, ``compact`` moves the used pages together.
+    Nothing synchronises, and every call can be captured in a CUDA graph.  ``max_new`` is the
+    largest number of rows for each slot that ``attend`` will be given; calls on one cache share
+    its workspace, so they belong on one stream at a time.
+    """
+
+    def __init__(self, layers, H: int, d_h: int, *, n_seqs: int, max_pages: int, n_pages: int,
+                 page_size: int = 64, H_kv=None, max_new: int = 1, device="cuda", pool=None,
+                 page_table=None, seq_len=None, ref=None):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.H, self.d_h, self.H_kv = H, d_h, H if H_kv is None else H_kv
+        self.n_seqs, self.max_pages, self.n_pages = n_seqs, max_pages, n_pages
+        self.page_size, self.max_new = page_size, max_new
+        self.layouts, self.offsets, self._static = [], [], []
+        geometry = (n_seqs, max_pages, n_pages, page_size, H, self.H_kv, d_h)
+        at = 0
+        for mask in layers:
+            m = bytes(int(bool(x)) for x in mask)
+            if len(m) != H:
+                raise B.SafError(B.SAF_ERR_INVALID_ARG, f"PagedCache: a mask of {len(m)} heads")
+            st, layout = B.saf_cache_layer_layout(B._cache_dims(*geometry, 0), m)
+            _check(st, "saf_cache_layer_layout")
+            self._static.append(m)
+            self.layouts.append(layout)
+            self.offsets.append(at)
+            at += layout.bytes
+        self.page_bytes = at
+        new = lambda shape, fill: torch.full(shape, fill, dtype=torch.int32, device=self.device)
+        if pool is None:
+            pool = torch.zeros((n_pages, at), dtype=torch.uint8, device=self.device)
+        self.page_table = new((n_seqs, max_pages), -1) if page_table is None else page_table
+        self.seq_len = new((n_seqs,), 0) if seq_len is None else seq_len
+        self.ref = new((n_pages,), 0) if ref is None else ref
+        if not (pool.dim() == 2 and pool.shape == (n_pages, at) and pool.stride(1) == 1
+                and pool.dtype == torch.uint8 and pool.device == self.device):
+            raise B.SafError(B.SAF_ERR_INVALID_ARG, f"PagedCache: pool is not [{n_pages}, {at}] bytes")
+        self.pool = pool
+        self._table_like((self.page_table, self.seq_len, self.ref), "PagedCache")
+        # a pool of one page may report any stride
+        self.dims = B._cache_dims(*geometry, pool.stride(0) if n_pages > 1 else at)
+        with torch.cuda.device(self.device):
+            attn = B.saf_cache_attn_workspace_size(self.dims, max_new)
+            pages = B.saf_cache_pages_workspace_size(self.dims)
+        if attn == 0 or pages == 0:
+            raise B.SafError(B.SAF_ERR_UNSUPPORTED, "saf_cache_attn_workspace_size")
+        self.ws_bytes, self._pages_bytes = attn, pages
+        self.workspace = torch.empty(attn, dtype=torch.uint8, device=self.device)
+        self._pages_ws = torch.empty(pages, dtype=torch.uint8, device=self.device)
+
+    # ---- checks
+    def _need(self, t, shape, dtype, what):
+        if (t.shape != shape or t.dtype != dtype or t.device != self.device
+                or not t.is_contiguous()):
+            raise B.SafError(B.SAF_ERR_INVALID_ARG,
+                             f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def _table_like(self, three, what):
+        shapes = ((self.n_seqs, self.max_pages), (self.n_seqs,), (self.n_pages,))
+        return [self._need(t, s, torch.int32, what) for t, s in zip(three, shapes)]
+
+    def _per_slot(self, t, what):
+        return None if t is None else self._need(t, (self.n_seqs,), torch.int32, what)
+
+    def _call(self, name, *args):
+        """The C entry on this cache's device and its current stream."""
+        if torch.cuda.current_device() == self.device.index:
+            st = getattr(B, name)(*args, _stream(self.device))
+        else:
+            with torch.cuda.device(self.device):
+                st = getattr(B, name)(*args, _stream(self.device))
+        if st != B.SAF_OK:
+            raise B.SafError(st, name)
+
+    # ---- tokens
+    def append(self, layer: int, k, v, n_new=None):
+        """Quantise new rows k, v [n_seqs, H_kv, n, d_h] (bf16 or fp32) into the pages of
+        ``layer``: the last n_new[s] (None: n) tokens of each slot, as counted by seq_len.
+        k may be None where the layer stores no K."""
+        n = v.shape[2] if v.dim() == 4 else -1
+        shape = (self.n_seqs, self.H_kv, n, self.d_h)
+        if v.dtype not in (torch.bfloat16, torch.float32):
+            raise B.SafError(B.SAF_ERR_UNSUPPORTED, "append: v is neither bf16 nor fp32")
+        pv = self._need(v, shape, v.dtype, "append: v")
+        pk = None if k is None else self._need(k, shape, v.dtype, "append: k")
+        self._call("saf_cache_append", self.dims, self._static[layer],
+                   self.pool.data_ptr() + self.offsets[layer], pk, pv,
+                   B.SAF_F32 if v.dtype == torch.float32 else B.SAF_BF16, n,
+                   self._per_slot(n_new, "append: n_new"), self.seq_len.data_ptr(),
+                   self.page_table.data_ptr())
+
+    def attend(self, layer: int, q, alpha=None, rho=None, n_new=None, out=None, lse=None):
+        """The hybrid attention of q [n_seqs, H, n, d_h] (bf16), the last n_new[s] (None: n)
+        tokens of each slot, over the cache.  alpha, rho [H, T] are needed where the layer has
+        frozen heads.  Returns (out, lse); rows behind n_new are left as they were."""
+        n = q.shape[2] if q.dim() == 4 else -1
+        shape = (self.n_seqs, self.H, n, self.d_h)
+        pq = self._need(q, shape, torch.bfloat16, "attend: q")
+        if n > self.max_new:
+            raise B.SafError(B.SAF_ERR_INVALID_ARG, f"attend: {n} rows, max_new is {self.max_new}")
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
+        pa = pr = None
+        T = 0
+        if alpha is not None:
+            T = alpha.shape[-1]
+            pa = self._need(alpha, (self.H, T), torch.float32, "attend: alpha")
+            pr = None if rho is None else self._need(rho, (self.H, T), torch.float32, "attend: rho")
+        if any(self._static[layer]) and (alpha is None or rho is None):
+            raise B.SafError(B.SAF_ERR_INVALID_ARG, "attend: frozen heads need alpha and rho")
+        self._call("saf_cache_attn", self.dims, self._static[layer],
+                   self.pool.data_ptr() + self.offsets[layer], pq, pa, pr, T, n,
+                   self._per_slot(n_new, "attend: n_new"), self.seq_len.data_ptr(),
+                   self.page_table.data_ptr(),
+                   self._need(out, shape, torch.bfloat16, "attend: out"),
+                   self._need(lse, shape[:3], torch.float32, "attend: lse"),
+                   self.workspace.data_ptr(), self.ws_bytes)
+        return out, lse
+
+    def views(self, layer: int):
+        """(K codes, V codes, K scales, V scales) of a layer as views of the pool: codes
+        [n_pages, heads, page_size, d_h] e4m3, scales [n_pages, heads] fp32."""
+        L, n, d = self.layouts[layer], self.n_pages, self.d_h
+        rec = self.pool[:, self.offsets[layer]:self.offsets[layer] + L.bytes]
+        part = lambda a, b, h: rec[:, a:b].view(n, h, self.page_size, d).view(torch.float8_e4m3fn)
+        return (part(0, L.v, L.H_k), part(L.v, L.k_scale, self.H_kv),
+                rec[:, L.k_scale:L.v_scale].view(torch.float32),
+                rec[:, L.v_scale:L.v_scale + 4 * self.H_kv].view(torch.float32))
+
+    # ---- pages
+    def grow(self, n_new, into=None):
+        """Room for n_new[s] more tokens in every slot (copying a last page that is shared);
+        seq_len advances.  Returns (granted [n_seqs], n_short [1]): what each slot got, all zero
+        when n_short pages are missing.  ``into``: (page_table, seq_len, ref) to write instead of
+        the cache's own."""
+        mine = self._table_like((self.page_table, self.seq_len, self.ref), "grow")
+        to = mine if into is None else self._table_like(into, "grow: into")
+        granted = torch.empty(self.n_seqs, dtype=torch.int32, device=self.device)
+        n_short = torch.empty(1, dtype=torch.int32, device=self.device)
+        if self.n_seqs == 0:
+            n_short.zero_()
+        self._call("saf_cache_grow", self.dims, self.pool.data_ptr(), self.page_bytes,
+                   self._per_slot(n_new, "grow: n_new"), *mine, *to, granted.data_ptr(),
+                   n_short.data_ptr(), self._pages_ws.data_ptr(), self._pages_bytes)
+        return granted, n_short
+
+    def fork(self, parent, into=None):
+        """Slot s takes over the pages and length of slot parent[s] (int32 [n_seqs]); a parent
+        outside [0, n_seqs) frees it.  ``into`` as in grow."""
+        mine = self._table_like((self.page_table, self.seq_len, self.ref), "fork")
+        to = mine if into is None else self._table_like(into, "fork: into")
+        self._call("saf_cache_fork", self.dims, self._per_slot(parent, "fork: parent"), *mine, *to)
+
+    def compact(self, into=None):
+        """Move the used pages into the lowest page numbers.  Returns their number (int32 [1]).
+        ``into``: (page_table, ref) to write instead of the cache's own."""
+        table, _, ref = self._table_like((self.page_table, self.seq_len, self.ref), "compact")
+        to = (table, ref)
+        if into is not None:
+            to = (self._need(into[0], (self.n_seqs, self.max_pages), torch.int32, "compact: into"),
+                  self._need(into[1], (self.n_pages,), torch.int32, "compact: into"))
+        n_used = torch.empty(1, dtype=torch.int32, device=self.device)
+        self._call("saf_cache_compact", self.dims, self.pool.data_ptr(), self.page_bytes, table, ref,
+                   *to, n_used.data_ptr(), self._pages_ws.data_ptr(), self._pages_bytes)
+        return n_used
+
+    def device_status(self):
+        return B.saf_get_device_status(_ptr(self.workspace), 0, _stream(self.device))
 
 
 def fit_compact(A_hat, candidates, k, kl_max=0.2, steps=400, lr=1e-2):

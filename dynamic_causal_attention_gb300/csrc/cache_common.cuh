@@ -1,0 +1,102 @@
+// cache_common.cuh — the paged 8-bit cache as its kernels see it: the layout
+// of a layer's record in a page, the rows of one call, and the pieces of PTX
+// that only these kernels use.
+//
+// A page holds `page_size` tokens of every layer; one layer's record in it is
+//   K codes [H_k, page, d] | V codes [H_kv, page, d] | K scales | V scales
+// with e4m3 codes and one fp32 scale for each (page, head).  K is stored for
+// the H_k heads that serve at least one dynamic query head.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace saf {
+
+// ------------------------------------------------------------ PTX
+// 16-byte asynchronous copy global -> shared; `bytes` (0..16) are read, the
+// rest of the destination is zero-filled.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two e4m3 codes (low and high byte of v) as packed f16: exact (f16 holds
+// every e4m3 value); the NaN code becomes NaN.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint16_t a, b;
+  asm("mov.b32 {%0, %1}, %2;" : "=h"(a), "=h"(b) : "r"(w));
+  lo = e4m3x2_f16x2(a);
+  hi = e4m3x2_f16x2(b);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// D += A B: 16 x 16 by 16 x 8, f16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2^e as fp32 for e in [-126, 127].
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// ------------------------------------------------------------ the rows of a call
+// Slot b takes n_new(b) of the n_q rows that the call holds for each slot;
+// row t stands at position seq_len - n_new + t.  Lengths beyond the page
+// table are cut to it: no page can hold what lies behind.
+struct Rows {
+  int n_new;  // rows of this slot
+  int base;   // position of row 0 (negative: the first rows see nothing)
+  int cap;    // keys that exist for the slot
+};
+__device__ __forceinline__ Rows slot_rows(const CacheCall& c, int b) {
+  Rows r;
+  const int len = c.seq_len[b];
+  int n = c.n_new ? c.n_new[b] : c.n_q;
+  n = n < 0 ? 0 : (n > c.n_q ? c.n_q : n);
+  r.n_new = n;
+  // a negative length counts as zero; len - n cannot overflow (len >= 0, n >= 0)
+  const int l = len < 0 ? 0 : len;
+  r.base = l - n;
+  const int room = c.max_pages << c.page_shift;  // fits: checked on the host
+  r.cap = l < room ? l : room;
+  return r;
+}
+
+// The page of table row b, column col; -1 where the entry names no page of
+// the pool (a hole: its tokens weigh nothing).
+__device__ __forceinline__ int page_at(const CacheCall& c, int b, int col) {
+  const int p = __ldg(c.page_table + (size_t)b * c.max_pages + col);
+  return (unsigned)p < (unsigned)c.n_pages ? p : -1;
+}
+
+}  // namespace saf

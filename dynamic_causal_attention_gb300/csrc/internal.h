@@ -108,4 +108,66 @@ cudaError_t launch_restage_rows(const void* src, bool src_f32, void* dst, bool d
 cudaError_t launch_restage_vec(const float* src, float* dst, size_t n_rows, int T_src, int T_dst,
                                float fill, cudaStream_t s);
 
+// ------------------------------------------------------------ paged 8-bit cache
+// One call on one layer of the cache (see cache_common.cuh for the layout).
+struct CacheCall {
+  uint8_t* layer;            // the layer's record in page 0
+  size_t page_stride;        // bytes from one page to the next
+  size_t off_v, off_ks, off_vs;  // V codes, K scales, V scales in the record
+  const int32_t* page_table; // [n_seqs, max_pages]
+  const int32_t* seq_len;    // [n_seqs], the new tokens among them
+  const int32_t* n_new;      // [n_seqs] or null: n_q rows for every slot
+  int n_seqs, max_pages, n_pages, page_shift;
+  int H, H_kv, group, n_q;   // group = H / H_kv
+  int H_k;                   // K heads that are stored
+  int16_t k_of[kMaxHeads];   // [H_kv] index among the stored K heads, or -1
+  uint8_t is_static[kMaxHeads];
+};
+
+struct CacheAppend {
+  CacheCall c;
+  const void *K, *V;  // [n_seqs, H_kv, n_q, d]
+  bool f32;
+  int16_t kv_of[kMaxHeads];  // [H_k] the K/V head of a stored K head
+};
+cudaError_t launch_cache_append(const CacheAppend& p, int d_h, cudaStream_t s);
+
+struct CacheAttn {
+  CacheCall c;
+  const uint16_t* Q;  // bf16 [n_seqs, H, n_q, d]
+  const float *alpha, *rho;  // [H, T_pat]
+  int T_pat;
+  uint16_t* out;  // bf16 [n_seqs, H, n_q, d]
+  float* lse;     // [n_seqs, H, n_q] or null
+  // scratch: see cache_attn_ws
+  int* status;
+  int4* join;     // [n_ctas] the unit that a CTA leaves to its successors, or none
+  float* ml;      // [2 n_ctas, rows, 2]
+  float* acc;     // [2 n_ctas, rows, d]
+};
+struct CacheAttnWs {
+  size_t status, join, ml, acc, total;
+};
+CacheAttnWs cache_attn_ws(int d_h, int n_sms);
+cudaError_t launch_cache_attn(const CacheAttn& p, int d_h, int n_sms, cudaStream_t s);
+
+// Page tables and reference counts (cache_pages.cu); a page is page_bytes
+// long, every page_stride bytes.
+struct CachePages {
+  int n_seqs, max_pages, n_pages, page_shift;
+  uint8_t* pool;
+  size_t page_stride, page_bytes;
+  const int32_t *table, *seq_len, *ref;
+  int32_t *table_out, *seq_len_out, *ref_out;
+  const int32_t* parent;   // fork: [n_seqs]
+  const int32_t* n_new;    // grow: [n_seqs]
+  int32_t* granted;        // grow: [n_seqs]
+  int32_t* count;          // grow: pages short; compact: pages in use
+  int32_t* scratch;
+};
+size_t cache_pages_scratch_words(int n_seqs, int n_pages);
+cudaError_t launch_cache_fork(const CachePages& p, cudaStream_t s);
+cudaError_t launch_cache_grow(const CachePages& p, int n_sms, cudaStream_t s);
+cudaError_t launch_cache_compact(const CachePages& p, int n_sms, cudaStream_t s);
+
 }  // namespace saf

@@ -283,6 +283,157 @@ SAF_API saf_status saf_calib_reset(void* handle);
 /* Free the state (synchronises the device first).  NULL is accepted. */
 SAF_API saf_status saf_calib_destroy(void* handle);
 
+/* ------------------------------------------------------------------------
+ * The paged 8-bit cache: serving the hybrid layer token by token.
+ *
+ * Keys and values of past tokens lie in pages of a pool.  A page holds
+ * `page_size` consecutive tokens of one sequence, for every layer; row s of
+ * `page_table` ([n_seqs, max_pages] int32) lists the pages of slot s, and
+ * seq_len[s] counts its tokens.  Pages may be shared between rows; ref[p]
+ * counts the rows that hold page p (0: free).  An entry of the table outside
+ * [0, n_pages) is a hole: its tokens weigh nothing in the attention, and
+ * appending there writes nothing.
+ *
+ * One layer's record in a page is
+ *     K codes [H_k, page_size, d_h] | V codes [H_kv, page_size, d_h]
+ *   | K scales [H_k] | V scales [H_kv]
+ * with one-byte e4m3 codes and fp32 scales, one for each block of a page's
+ * tokens and head: the value is code * scale.  H_k counts the K/V heads that
+ * serve at least one dynamic query head; a frozen head's weights come from
+ * alpha and rho, so the K of a group that is frozen whole is never stored.
+ * saf_cache_layer_layout gives the offsets.  Several layers lie behind one
+ * another in the page; a call on a layer takes the address of its record in
+ * page 0 and dims->page_stride.
+ *
+ * Arrays of int32 are 16-byte aligned device arrays unless a call says
+ * otherwise.  No call allocates, synchronises or reads device memory on the
+ * host; all can be captured in a CUDA graph. */
+typedef struct saf_cache_dims {
+  int n_seqs;         /* slots: rows of page_table, 0..32768               */
+  int max_pages;      /* columns of page_table; max_pages * page_size < 2^31 */
+  int n_pages;        /* pages of the pool, >= 1                           */
+  int page_size;      /* tokens of a page: 16, 32, 64 or 128               */
+  int H;              /* query heads, 1..256                               */
+  int H_kv;           /* K/V heads: a divisor of H                         */
+  int d_h;            /* head dimension: 32, 64 or 128                     */
+  size_t page_stride; /* bytes from one page to the next, a multiple of 16 */
+} saf_cache_dims;
+
+typedef struct saf_cache_layout {
+  int H_k;            /* K heads that are stored                           */
+  size_t v;           /* offset of the V codes (the K codes lie at 0)      */
+  size_t k_scale;     /* offset of the K scales                            */
+  size_t v_scale;     /* offset of the V scales                            */
+  size_t bytes;       /* length of the record, a multiple of 128           */
+} saf_cache_layout;
+
+/* The record of a layer whose frozen heads are marked in head_is_static
+ * (host [H]).  dims->page_stride is not looked at beyond its alignment. */
+SAF_API saf_status saf_cache_layer_layout(const saf_cache_dims* dims,
+                                  const uint8_t* head_is_static, saf_cache_layout* layout);
+
+/* Writes new K/V rows into the pages, quantised.
+ *
+ *   layer       the layer's record in page 0 (16-byte aligned).
+ *   K, V        [n_seqs, H_kv, n_q, d_h] bf16 or fp32 per `dtype`; K rows of
+ *               heads that are not stored are never read (K may be NULL when
+ *               H_k = 0).
+ *   n_new       [n_seqs] or NULL (4-byte aligned): rows of each slot, cut to
+ *               0..n_q; NULL means n_q for every slot.  Rows behind are never
+ *               read.
+ *   seq_len     [n_seqs] (4-byte aligned): tokens of each slot, the new ones
+ *               among them: row t goes to position seq_len - n_new + t.  Rows
+ *               at negative positions, in holes or behind the page table are
+ *               dropped.
+ *
+ * The scale of a block (a page's tokens under one K or V head) is the least
+ * power of two s >= 2^-64 with 448 s >= |x| for every finite x in it, and the
+ * codes are x / s rounded to the nearest e4m3 value, ties to even.  When new
+ * tokens raise the scale of a block that older tokens began, the older codes
+ * are rounded again under the new scale, which changes only those that sink
+ * below e4m3's normal range; an older block's scale must be a power of two
+ * (this call writes no other).  Position 0 of a page starts its block over.
+ * Infinities are stored as the largest value of the block's scale (448 s), NaN
+ * as NaN.  Writing the same rows to the same positions again changes nothing.
+ *
+ * No two slots may write the same page in one call (saf_cache_grow gives a
+ * slot a copy of a shared last page). */
+SAF_API saf_status saf_cache_append(const saf_cache_dims* dims, const uint8_t* head_is_static,
+                            void* layer, const void* K, const void* V, saf_dtype dtype,
+                            int n_q, const int32_t* n_new, const int32_t* seq_len,
+                            const int32_t* page_table, void* stream);
+
+/* Bytes of device workspace for saf_cache_attn with these dims and n_q rows
+ * for each slot; 0 for dims that it does not take. */
+SAF_API size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q);
+
+/* The hybrid layer's forward for the newest n_new tokens of each slot over
+ * what the cache holds, the new tokens included (append them first).  Row t
+ * of slot b stands at position i = seq_len - n_new + t and sees the keys
+ * j <= i that lie on a page:
+ *   dynamic head: softmax_j(q . k_j / sqrt(d_h)) over the dequantised K, V;
+ *   frozen head:  weights exp(alpha(j) + rho(i - j)) / Z(i).
+ *
+ *   Q           bf16 [n_seqs, H, n_q, d_h]; rows of frozen heads and rows
+ *               t >= n_new are never read (Q may be NULL when H_k = 0).
+ *   alpha, rho  fp32 [H, T_pat]; only rows of frozen heads are read.  Keys and
+ *               distances at or behind T_pat count as -inf.
+ *   n_new, seq_len, page_table: as in saf_cache_append.  Scales must be
+ *               positive and finite.
+ *   out         bf16 [n_seqs, H, n_q, d_h]; lse fp32 [n_seqs, H, n_q] or NULL:
+ *               log sum_j exp(.).  A row that sees no key, or none of nonzero
+ *               weight, gets out = 0 and lse = -inf.  Rows t >= n_new are left
+ *               as they were.
+ *   workspace   256-byte aligned; saf_get_device_status reads its status.
+ * What lies on a page behind a slot's last token, or at keys that a row does
+ * not see, has no part in the row's result, NaN codes included.  Results do
+ * not depend on timing: the same call gives the same bits. */
+SAF_API saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_static,
+                          const void* layer, const void* Q, const float* alpha,
+                          const float* rho, int T_pat, int n_q, const int32_t* n_new,
+                          const int32_t* seq_len, const int32_t* page_table, void* out,
+                          float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* Pages of the cache.  The calls below take the page table, lengths and
+ * reference counts and write the changed ones; an output may be its input
+ * (updated in place) but must not overlap another array of the call.  H, H_kv
+ * and d_h of dims are checked but play no part; page_bytes <= page_stride (a
+ * multiple of 16) are the bytes of a page that are copied. */
+
+/* Every slot s takes over the pages and the length that slot parent[s] had
+ * before the call; a parent outside [0, n_seqs) frees the slot (entries -1,
+ * length 0).  parent[s] = s keeps a slot, parent[s] = q forks q, a permutation
+ * reorders.  Pages are shared, not copied; ref follows the rows. */
+SAF_API saf_status saf_cache_fork(const saf_cache_dims* dims, const int32_t* parent,
+                          const int32_t* page_table, const int32_t* seq_len,
+                          const int32_t* ref, int32_t* page_table_out, int32_t* seq_len_out,
+                          int32_t* ref_out, void* stream);
+
+SAF_API size_t saf_cache_pages_workspace_size(const saf_cache_dims* dims);
+
+/* Makes room for n_new[s] more tokens in every slot and advances seq_len.
+ * Free pages (ref <= 0) are taken lowest first, slot by slot; a slot whose
+ * last page is begun and shared (ref > 1 before the call) first gets a copy of
+ * it.  granted[s] receives the tokens that slot s may append: n_new[s], or 0
+ * where they would pass the end of the page table (the slot is left alone) or
+ * n_new[s] <= 0.  When the pool has too few free pages nothing changes, every
+ * granted[s] is 0 and n_short [1] says how many are missing; otherwise it is
+ * 0.  granted is what saf_cache_append and saf_cache_attn take as n_new. */
+SAF_API saf_status saf_cache_grow(const saf_cache_dims* dims, void* pool, size_t page_bytes,
+                          const int32_t* n_new, const int32_t* page_table,
+                          const int32_t* seq_len, const int32_t* ref,
+                          int32_t* page_table_out, int32_t* seq_len_out, int32_t* ref_out,
+                          int32_t* granted, int32_t* n_short, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/* Moves the used pages (ref > 0) into the lowest page numbers: with n of them,
+ * the k-th used page behind n moves to the k-th free page before n.  Table
+ * entries and ref follow; n_used [1] receives n. */
+SAF_API saf_status saf_cache_compact(const saf_cache_dims* dims, void* pool, size_t page_bytes,
+                             const int32_t* page_table, const int32_t* ref,
+                             int32_t* page_table_out, int32_t* ref_out, int32_t* n_used,
+                             void* workspace, size_t ws_bytes, void* stream);
+
 /* Reads (and clears) the device status word kept in an attention workspace
  * (`is_calib_handle` = 0) or in a calibration handle (`is_calib_handle` = 1).
  * Every saf_hybrid_attn_fwd / _bwd call clears the word of its workspace when

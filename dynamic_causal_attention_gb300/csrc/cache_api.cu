@@ -85,6 +85,15 @@ saf_status make_call(const saf_cache_dims& d, const uint8_t* head_is_static, con
   return SAF_OK;
 }
 
+// The scratch of an attention call and the kernel that takes it: up to 16 rows
+// for each slot and K/V head go to the kernel made for single tokens.
+bool many_rows(const saf_cache_dims& d, int n_q) {
+  return (long long)n_q * (d.H / d.H_kv) > 16;
+}
+CacheAttnWs attn_ws(const saf_cache_dims& d, int n_q) {
+  return many_rows(d, n_q) ? cache_chunk_ws(d.d_h, sm_count()) : cache_attn_ws(d.d_h, sm_count());
+}
+
 saf_status status_of(cudaError_t e) { return e == cudaSuccess ? SAF_OK : SAF_ERR_CUDA; }
 
 saf_status make_pages(const saf_cache_dims& d, const int32_t* const (&words)[3],
@@ -147,7 +156,10 @@ saf_status saf_cache_append(const saf_cache_dims* dims, const uint8_t* head_is_s
 
 size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q) {
   if (check_cache(dims) != SAF_OK || n_q < 0) return 0;
-  return cache_attn_ws(dims->d_h, sm_count()).total;
+  // calls with fewer rows may take either kernel
+  const size_t few = cache_attn_ws(dims->d_h, sm_count()).total;
+  const size_t all = attn_ws(*dims, n_q).total;
+  return few > all ? few : all;
 }
 
 saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_static,
@@ -172,7 +184,7 @@ saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_sta
   if (any_static && T_pat > 0 && (bad16(alpha) || bad16(rho))) return SAF_ERR_INVALID_ARG;
   if (bad16(out) || (lse && !aligned16(lse)) || !workspace) return SAF_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SAF_ERR_INVALID_ARG;
-  const CacheAttnWs w = cache_attn_ws(dims->d_h, sm_count());
+  const CacheAttnWs w = attn_ws(*dims, n_q);
   if (ws_bytes < w.total) return SAF_ERR_INVALID_ARG;
   p.Q = static_cast<const uint16_t*>(Q);
   p.alpha = alpha;
@@ -185,7 +197,8 @@ saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_sta
   p.join = reinterpret_cast<int4*>(ws + w.join);
   p.ml = reinterpret_cast<float*>(ws + w.ml);
   p.acc = reinterpret_cast<float*>(ws + w.acc);
-  return status_of(launch_cache_attn(p, dims->d_h, sm_count(), static_cast<cudaStream_t>(stream)));
+  return status_of((many_rows(*dims, n_q) ? launch_cache_chunk : launch_cache_attn)(
+      p, dims->d_h, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 
 saf_status saf_cache_fork(const saf_cache_dims* dims, const int32_t* parent,

@@ -4,14 +4,17 @@
 // accumulators in TMEM.
 //
 // A unit is (slot, class, row pair): a class is the dynamic or the frozen
-// query heads of one K/V head, its rows are r = t * heads + index, and a unit
+// query heads of one K/V head; its rows are r = t * heads + index (dynamic: the
+// last key that a unit sees is then as early as can be) or r = index * n_new + t
+// (frozen: a warp's rows share alpha and read rho side by side), and a unit
 // takes 256 of them as two tiles of 128, against the keys up to the last
 // position among them in tiles of 128.  Splitting a group by kind keeps every
 // warp uniform and spares frozen rows the Q K product.  All tiles of all
 // units are cut into equal shares, one for each CTA (one per SM), as in
 // cache_attn.cu.
 //
-// Warp roles (416 threads):
+// Warp roles (512 threads; registers move from the last two warpgroups to the
+// first two):
 //   warps 0-3, 4-7   the softmax of row tile 0 and 1: one row per thread.  They
 //                    also stage Q (scaled into f16) and write the results.
 //   warps 8-11       turn e4m3 codes into f16 tiles in shared memory (K: K-major,
@@ -36,7 +39,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 256;     // query rows of a unit
 constexpr int kTile = 128;     // keys of a tile
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
+// registers of a thread after the split: 2 * 176 + 112 + 48 = 4 * 128
+constexpr int kRegsSoftmax = 176, kRegsConvert = 112, kRegsIssue = 48;
 constexpr long long kMinTiles = 1;
 
 enum : int { kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree };
@@ -50,58 +55,104 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
 __device__ __forceinline__ int pairs_of(const Rows& r, int gk) {
   return (int)(((long long)r.n_new * gk + kRows - 1) / kRows);
 }
-__device__ __forceinline__ int pair_extent(const Rows& r, int pair, int gk) {
-  int t_hi = (pair * kRows + kRows - 1) / gk + 1;
-  if (t_hi > r.n_new) t_hi = r.n_new;
-  const int e = r.base + t_hi;
+// The tokens [lo, hi) of a unit's rows.
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span pair_span(const Rows& r, int pair, int gk, bool ice) {
+  Span s;
+  if (ice) {
+    const int at = pair * kRows;
+    s.lo = at % r.n_new;
+    s.hi = s.lo + kRows;
+    if (s.hi > r.n_new) {  // the rows may go on with the next head's first token
+      const bool next = (long long)at + r.n_new - s.lo < (long long)r.n_new * gk;
+      if (next) s.lo = 0;
+      s.hi = r.n_new;
+    }
+    return s;
+  }
+  s.lo = pair * kRows / gk;
+  s.hi = min((pair * kRows + kRows - 1) / gk + 1, r.n_new);
+  return s;
+}
+__device__ __forceinline__ int pair_extent(const Rows& r, int pair, int gk, bool ice) {
+  const int e = r.base + pair_span(r, pair, gk, ice).hi;
   return e < 0 ? 0 : (e < r.cap ? e : r.cap);
 }
-__device__ __forceinline__ int pair_tiles(const Rows& r, int pair, int gk) {
-  const int n = (pair_extent(r, pair, gk) + kTile - 1) / kTile;
+__device__ __forceinline__ int pair_tiles(const Rows& r, int pair, int gk, bool ice) {
+  const int n = (pair_extent(r, pair, gk, ice) + kTile - 1) / kTile;
   return n < 1 ? 1 : n;  // rows that see nothing are written too
 }
+// Row `rr` of a class as (token, index of the head).
+__device__ __forceinline__ void row_of(const Rows& r, int rr, int gk, bool ice, int& t, int& idx) {
+  if (ice) {
+    idx = rr / r.n_new;
+    t = rr - idx * r.n_new;
+  } else {
+    t = rr / gk;
+    idx = rr - t * gk;
+  }
+}
 
-// Walks the units in order: slots, then classes of equal width, row pairs,
-// classes.
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// Walks the units in order: slots, then groups of classes (equal width and
+// kind), row pairs, classes.  seek() and the sums are taken by whole warps.
 struct Walk {
   const CacheChunk& p;
   Rows rows;
   int b, group, pair, cls, ut;
   __device__ __forceinline__ explicit Walk(const CacheChunk& q) : p(q) {}
   __device__ __forceinline__ int gk() const { return p.group_width[group]; }
-  __device__ long long group_tiles(const Rows& r, int g) const {
-    long long sum = 0;
-    const int w = p.group_width[g], n = pairs_of(r, w);
-    for (int i = 0; i < n; ++i) sum += pair_tiles(r, i, w);
-    return sum * (p.group_first[g + 1] - p.group_first[g]);
+  __device__ __forceinline__ bool ice() const { return p.group_static[group]; }
+  __device__ __forceinline__ int classes(int g) const {
+    return p.group_first[g + 1] - p.group_first[g];
   }
   __device__ long long slot_tiles(int slot) const {
     const Rows r = slot_rows(p.a.c, slot);
+    const int lane = threadIdx.x & 31;
     long long sum = 0;
-    for (int g = 0; g < p.n_groups; ++g) sum += group_tiles(r, g);
-    return sum;
+    for (int g = 0; g < p.n_groups; ++g) {
+      long long mine = 0;
+      const int w = p.group_width[g], n = pairs_of(r, w);
+      for (int i = lane; i < n; i += 32) mine += pair_tiles(r, i, w, p.group_static[g]);
+      sum += mine * classes(g);
+    }
+    return warp_sum(sum);
   }
   // to the unit that holds tile `at` of slot `slot`; returns the tile in it
   __device__ int seek(int slot, long long at) {
+    const int lane = threadIdx.x & 31;
     b = slot;
     rows = slot_rows(p.a.c, b);
-    group = 0;
-    while (group < p.n_groups - 1) {
-      const long long n = group_tiles(rows, group);
-      if (at < n) break;
-      at -= n;
-      ++group;
+    for (group = 0;; ++group) {
+      const int n = pairs_of(rows, gk()), n_cls = classes(group);
+      for (pair = 0; pair < n; pair += 32) {
+        const int i = pair + lane;
+        const int mine = i < n ? pair_tiles(rows, i, gk(), ice()) : 0;
+        long long upto = (long long)mine * n_cls;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(~0u, upto, o);
+          if (lane >= o) upto += y;
+        }
+        const unsigned over = __ballot_sync(~0u, at < upto);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          pair += l;
+          ut = __shfl_sync(~0u, mine, l);
+          at -= __shfl_sync(~0u, upto, l) - (long long)ut * n_cls;
+          cls = p.group_first[group] + (int)(at / ut);
+          return (int)(at % ut);
+        }
+        at -= __shfl_sync(~0u, upto, 31);
+      }
     }
-    pair = 0;
-    const int n_cls = p.group_first[group + 1] - p.group_first[group];
-    ut = pair_tiles(rows, 0, gk());
-    while (at >= (long long)ut * n_cls) {
-      at -= (long long)ut * n_cls;
-      ++pair;
-      ut = pair_tiles(rows, pair, gk());
-    }
-    cls = p.group_first[group] + (int)(at / ut);
-    return (int)(at % ut);
   }
   __device__ void next() {
     if (++cls == p.group_first[group + 1]) {
@@ -115,7 +166,7 @@ struct Walk {
         }
       }
       cls = p.group_first[group];
-      ut = pair_tiles(rows, pair, gk());
+      ut = pair_tiles(rows, pair, gk(), ice());
     }
   }
 };
@@ -124,29 +175,29 @@ struct Share {
   long long size, begin, end, in_slot;
   int b;
 };
-// As in cache_attn.cu: a run of slots for each thread, one block scan.
-__device__ Share find_share(const CacheChunk& p, long long* scan /* [threads + 4] */) {
+// Every CTA finds its share: each warp sums a run of slots, the sums of the
+// warps before give a run's first tile, and the warp whose run holds the
+// share's first tile walks it.
+__device__ Share find_share(const CacheChunk& p, long long* scan /* [20] */) {
   const Walk w(p);
-  const int n = blockDim.x, tid = threadIdx.x, n_seqs = p.a.c.n_seqs;
-  const int per = (n_seqs + n - 1) / n;
-  const int b0 = min(tid * per, n_seqs), b1 = min(b0 + per, n_seqs);
+  constexpr int kN = kThreads / 32;
+  const int warp = threadIdx.x >> 5, n_seqs = p.a.c.n_seqs;
+  const int per = (n_seqs + kN - 1) / kN;
+  const int b0 = min(warp * per, n_seqs), b1 = min(b0 + per, n_seqs);
   long long sum = 0;
   for (int b = b0; b < b1; ++b) sum += w.slot_tiles(b);
-  scan[tid] = sum;
+  scan[warp] = sum;
   __syncthreads();
-  for (int o = 1; o < n; o <<= 1) {
-    const long long x = tid >= o ? scan[tid - o] : 0;
-    __syncthreads();
-    scan[tid] += x;
-    __syncthreads();
+  long long total = 0, mine = 0;
+  for (int i = 0; i < kN; ++i) {
+    if (i == warp) mine = total;
+    total += scan[i];
   }
   Share s;
-  const long long total = scan[n - 1];
   s.size = (total + gridDim.x - 1) / gridDim.x;
   if (s.size < kMinTiles) s.size = kMinTiles;
   s.begin = min(s.size * blockIdx.x, total);
   s.end = min(s.begin + s.size, total);
-  const long long mine = scan[tid] - sum;
   if (s.begin < s.end && mine <= s.begin && s.begin < mine + sum) {
     long long at = mine;
     int b = b0;
@@ -155,12 +206,12 @@ __device__ Share find_share(const CacheChunk& p, long long* scan /* [threads + 4
       if (s.begin < at + t) break;
       at += t;
     }
-    scan[n] = b;
-    scan[n + 1] = s.begin - at;
+    scan[kN] = b;
+    scan[kN + 1] = s.begin - at;
   }
   __syncthreads();
-  s.b = (int)scan[n];
-  s.in_slot = scan[n + 1];
+  s.b = (int)scan[kN];
+  s.in_slot = scan[kN + 1];
   return s;
 }
 
@@ -172,7 +223,7 @@ struct Smem {
   static constexpr int OFF_V = 4 * TILE;      // two stages
   static constexpr int OFF_META = 6 * TILE;   // 4 tiles x 8 groups of 16 keys x 16 bytes
   static constexpr int OFF_SCAN = OFF_META + 4 * 8 * 16;
-  static constexpr int OFF_BAR = OFF_SCAN + (kThreads + 4) * 8;
+  static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
   static constexpr int NBAR = 2 + 4 + 4 + 4 + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 32;
@@ -250,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long at = sh.begin;
     if (warp < 8) {
       // ------------------------------------------------------------ softmax
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
       const int g = warp >> 2, r = threadIdx.x & 127;
       const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_col = trow + kS + g * 128, o_col = trow + kO + g * 128;
@@ -257,47 +309,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int seg = 0;; ++seg) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
         const int gk = w.gk(), kv = p.cls_kv[w.cls];
-        const bool ice = p.cls_static[w.cls];
+        const bool ice = w.ice();
         const int n_rows = (int)min((long long)kRows,
                                     (long long)w.rows.n_new * gk - (long long)w.pair * kRows);
         if (g * 128 < n_rows) {
           const bool live = g * 128 + r < n_rows;
           const int rr = w.pair * kRows + g * 128 + r;
-          const int t = live ? rr / gk : 0;
-          const int h = p.order[p.cls_first[w.cls] + (live ? rr - t * gk : 0)];
+          int t = 0, idx = 0;
+          if (live) row_of(w.rows, rr, gk, ice, t, idx);
+          const int h = p.order[p.cls_first[w.cls] + idx];
           const int pos = live ? w.rows.base + t : -1;
           const int lim_all = min(pos + 1, w.rows.cap);  // keys below it are seen
           const size_t row = ((size_t)w.b * c.H + h) * c.n_q + t;
           const bool warp_live = g * 128 + (warp & 3) * 32 < n_rows;
           float fac = 1.f;
           if (!ice) {
-            // the row of Q, scaled by a power of two so that its largest
-            // component lies in [2^14, 2^15)
-            uint4 q[D / 8];
-            float amax = 0.f;
-#pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
-              q[u] = live ? __ldg(reinterpret_cast<const uint4*>(p.a.Q + row * D) + u)
-                          : make_uint4(0, 0, 0, 0);
-              const uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            // rows of Q, each scaled by a power of two so that its largest
+            // component lies in [2^14, 2^15): kL lanes take a row
+            constexpr int kL = D / 8, kR = 32 / kL;
+            const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
+            const uint16_t* qb = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
+#pragma unroll 4
+            for (int i = 0; i < 32; i += kR) {
+              const int rl = i + lane / kL, u = lane % kL;  // row of the warp, 16-byte unit
+              const int src = __shfl_sync(~0u, mine, rl);
+              const uint4 q = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                             qb + (size_t)(unsigned)src * D) + u)
+                                       : make_uint4(0, 0, 0, 0);
+              const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+              float amax = 0.f;
 #pragma unroll
               for (int v = 0; v < 4; ++v)
                 amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[v] << 16)),
                                          fabsf(__uint_as_float(x[v] & 0xffff0000u))));
-            }
-            int e = (__float_as_int(amax) >> 23) - 127 - 14;
-            e = amax > 0.f ? max(-126, min(112, e)) : 0;
-            const float down = pow2f(-e);
-            fac = pow2f(e) * (rsqrtf((float)D) * kLog2e);
 #pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
-              const uint32_t x[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+              for (int o = kL / 2; o; o >>= 1)
+                amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+              int e = (__float_as_int(amax) >> 23) - 127 - 14;
+              e = amax > 0.f ? max(-126, min(112, e)) : 0;
+              const float down = pow2f(-e);
               uint32_t y[4];
 #pragma unroll
               for (int v = 0; v < 4; ++v)
                 y[v] = pack_f16x2(__uint_as_float(x[v] << 16) * down,
                                   __uint_as_float(x[v] & 0xffff0000u) * down);
-              st_shared_v4(sQ + g * L::TILE + unit_at<D>(r, u), y[0], y[1], y[2], y[3]);
+              st_shared_v4(sQ + g * L::TILE + unit_at<D>((warp & 3) * 32 + rl, u), y[0], y[1],
+                           y[2], y[3]);
+              const int back = __shfl_sync(~0u, e, (lane - i) * kL & 31);
+              if (lane >= i && lane < i + kR) fac = pow2f(back) * (rsqrtf((float)D) * kLog2e);
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full + g);
@@ -318,58 +377,62 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int j0 = i * kTile;
               const int lim = lim_all - j0;  // columns below it are seen
               const bool edge = __any_sync(~0u, lim < kTile);
-              float gm[8];
+              uint32_t s[128];
+              if (!ice) {
+                uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
+                uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
+                uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 64);
+                uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 96);
+                tmem_ld_x32(s_col, s0);
+                tmem_ld_x32(s_col + 32, s1);
+                tmem_ld_x32(s_col + 64, s2);
+                tmem_ld_x32(s_col + 96, s3);
+                tmem_wait_ld(s0);
+                tmem_wait_ld(s1);
+                tmem_wait_ld(s2);
+                tmem_wait_ld(s3);
+              } else {
+                const float* al = p.a.alpha + (size_t)h * p.a.T_pat + j0;
+                const int d0 = pos - j0;  // distance of column 0
+                const float* rh = p.a.rho + (size_t)h * p.a.T_pat + d0;
+                // inside the vectors for every column of the warp's rows?
+                const bool in = j0 + kTile <= p.a.T_pat && d0 < p.a.T_pat && d0 >= kTile - 1;
+                if (__all_sync(~0u, in && (reinterpret_cast<uintptr_t>(al) & 15) == 0)) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t s[32];
-                if (!ice) {
-                  tmem_ld_x32(s_col + 32 * q, s);
-                  tmem_wait_ld(s);
-                } else {
-                  const float* al = p.a.alpha + (size_t)h * p.a.T_pat + j0 + 32 * q;
-                  const float* rh = p.a.rho + (size_t)h * p.a.T_pat + (pos - j0 - 32 * q);
-                  // inside the vectors for every column of the warp's rows?
-                  const int d0 = pos - j0 - 32 * q;
-                  const bool in = j0 + 32 * q + 31 < p.a.T_pat && d0 < p.a.T_pat && d0 >= 31;
-                  if (__all_sync(~0u, in)) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                      s[k] = __float_as_uint((__ldg(al + k) + __ldg(rh - k)) * kLog2e);
-                  } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                      const bool ok = j0 + 32 * q + k < p.a.T_pat && d0 - k >= 0 &&
-                                      d0 - k < p.a.T_pat;
-                      s[k] = __float_as_uint(
-                          ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
-                    }
+                  for (int k = 0; k < kTile; k += 4) {
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(al + k));
+                    s[k] = __float_as_uint((x.x + __ldg(rh - k)) * kLog2e);
+                    s[k + 1] = __float_as_uint((x.y + __ldg(rh - k - 1)) * kLog2e);
+                    s[k + 2] = __float_as_uint((x.z + __ldg(rh - k - 2)) * kLog2e);
+                    s[k + 3] = __float_as_uint((x.w + __ldg(rh - k - 3)) * kLog2e);
                   }
-                  uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(s);
-                  uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(s + 16);
-                  tmem_st_x16(s_col + 32 * q, lo);
-                  tmem_st_x16(s_col + 32 * q + 16, hi);
-                }
-                if (edge) {
+                } else {
 #pragma unroll
-                  for (int k = 0; k < 32; ++k)
-                    if (32 * q + k >= lim) s[k] = 0xff800000u;
+                  for (int k = 0; k < kTile; ++k) {
+                    const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
+                    s[k] = __float_as_uint(
+                        ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
+                  }
                 }
+              }
+              if (edge) {
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                  float x = fmax3(__uint_as_float(s[16 * hh]), __uint_as_float(s[16 * hh + 1]),
-                                  __uint_as_float(s[16 * hh + 2]));
-#pragma unroll
-                  for (int k = 3; k < 15; k += 2)
-                    x = fmax3(x, __uint_as_float(s[16 * hh + k]),
-                              __uint_as_float(s[16 * hh + k + 1]));
-                  gm[2 * q + hh] = fmaxf(x, __uint_as_float(s[16 * hh + 15]));
-                }
+                for (int k = 0; k < kTile; ++k)
+                  if (k >= lim) s[k] = 0xff800000u;
               }
               float top = -CUDART_INF_F;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 mt = lds_f32x4(meta + 16 * k);
-                top = fmaxf(top, fmaf(gm[k], ice ? 1.f : fac * mt.x, mt.y));
+              for (int q = 0; q < 8; ++q) {  // groups of 16 keys: one page, one scale
+                float x = fmax3(__uint_as_float(s[16 * q]), __uint_as_float(s[16 * q + 1]),
+                                __uint_as_float(s[16 * q + 2]));
+#pragma unroll
+                for (int k = 3; k < 15; k += 2)
+                  x = fmax3(x, __uint_as_float(s[16 * q + k]), __uint_as_float(s[16 * q + k + 1]));
+                x = fmaxf(x, __uint_as_float(s[16 * q + 15]));
+                const uint64_t mt = lds_f32x2(meta + 16 * q);
+                float ks, lv;
+                f2_unpack(mt, ks, lv);
+                top = fmaxf(top, fmaf(x, ice ? 1.f : fac * ks, lv));
               }
               // the maximum moves only when it would grow by more than 2^8:
               // weights up to 2^8 fit f16 as well
@@ -380,53 +443,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l *= corr;
                 if (i > tile) {
 #pragma unroll 1
-                  for (int q = 0; q < D; q += 32) {
-                    uint32_t o[32];
-                    tmem_ld_x32(o_col + q, o);
+                  for (int q = 0; q < D; q += 16) {
+                    uint32_t o[16];
+                    tmem_ld_x16(o_col + q, o);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
+                    for (int k = 0; k < 16; ++k)
                       o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                    tmem_st_x16(o_col + q, *reinterpret_cast<uint32_t(*)[16]>(o));
-                    tmem_st_x16(o_col + q + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                    tmem_st_x16(o_col + q, o);
                   }
                 }
               }
               const float base = m == -CUDART_INF_F ? 0.f : m;
-              if (ice) tmem_wait_st();
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t s[32], pk[16];
-                tmem_ld_x32(s_col + 32 * q, s);
-                tmem_wait_ld(s);
-                if (edge) {
+              for (int q = 0; q < 8; ++q) {
+                const float4 mt = lds_f32x4(meta + 16 * q);
+                const float a = ice ? 1.f : fac * mt.x, b = mt.y - base;
+                const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
+                uint64_t sum = 0;
+                uint32_t pk[8];
 #pragma unroll
-                  for (int k = 0; k < 32; ++k)
-                    if (32 * q + k >= lim) s[k] = 0xff800000u;
-                }
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                  const float4 mt = lds_f32x4(meta + 16 * (2 * q + hh));
-                  const float a = ice ? 1.f : fac * mt.x, b = mt.y - base;
-                  const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
-                  uint64_t sum = 0;
-#pragma unroll
-                  for (int k = 0; k < 16; k += 2) {
-                    float x, y;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[16 * hh + k]),
-                                             __uint_as_float(s[16 * hh + k + 1])),
-                                     a2, b2),
-                              x, y);
-                    x = fast_exp2(x);
-                    y = fast_exp2(y);
-                    sum = f2_add(sum, f2_pack(x, y));
-                    pk[8 * hh + k / 2] = pack_f16x2(x, y);
-                  }
+                for (int k = 0; k < 16; k += 2) {
                   float x, y;
-                  f2_unpack(sum, x, y);
-                  l = fmaf(x + y, mt.z, l);
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[16 * q + k]),
+                                           __uint_as_float(s[16 * q + k + 1])),
+                                   a2, b2),
+                            x, y);
+                  x = fast_exp2(x);
+                  y = fast_exp2(y);
+                  sum = f2_add(sum, f2_pack(x, y));
+                  pk[k / 2] = pack_f16x2(x, y);
                 }
-                tmem_st_x16(s_col + 16 * q, pk);
+                float x, y;
+                f2_unpack(sum, x, y);
+                l = fmaf(x + y, mt.z, l);
+                tmem_st_x8(s_col + 8 * q, pk);
               }
               tmem_wait_st();
             }
@@ -445,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < D / 32; ++q) nan[q] = 0;
             if (nan_seg[seg & 3] == seg + 1) {
               // V holds NaN at a key of an edge tile: rows that see it take it
-              const int first = max(0, (w.rows.base + w.pair * kRows / gk) / kTile * kTile);
+              const int lo = w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo;
+              const int first = max(0, lo / kTile * kTile);
               for (int j = max(first, tile * kTile); j < min(lim_all, tile_end * kTile); ++j) {
                 const int page = page_at(c, w.b, j >> c.page_shift);
                 if (page < 0) continue;
@@ -458,8 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const size_t part =
-                ((size_t)(2 * blockIdx.x + (at == sh.begin ? 0 : 1)) * kRows + g * 128 + r);
+            // partial sums: [D / 4][row][4], so that a warp's stores are contiguous
+            const size_t part = (size_t)(2 * blockIdx.x + (at == sh.begin ? 0 : 1)) * kRows;
+            const int pr = g * 128 + r;
+            // results go through the row tile's Q buffer (its products are done)
+            const uint32_t stage = sQ + g * L::TILE;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
               uint32_t o[32];
@@ -470,25 +525,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
                 if (nan[q] >> k & 1) o[k] = 0x7fc00000u;
               }
-              if (live && whole) {
-                uint4* dst = reinterpret_cast<uint4*>(p.a.out + row * D + 32 * q);
+              if (whole) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
-                  dst[k / 8] = make_uint4(
-                      pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
-                      pack_bf16x2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
-                      pack_bf16x2(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
-                      pack_bf16x2(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
+                  st_shared_v4(stage + unit_at<D>(r, 4 * q + k / 8),
+                               pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
+                               pack_bf16x2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
+                               pack_bf16x2(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
+                               pack_bf16x2(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
               } else if (live) {
-                uint4* dst = reinterpret_cast<uint4*>(p.a.acc + part * D + 32 * q);
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
-                  dst[k / 4] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                  *reinterpret_cast<uint4*>(p.a.acc + part * D +
+                                            ((size_t)(8 * q + k / 4) * kRows + pr) * 4) =
+                      make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
               }
+            }
+            if (whole) {
+              __syncwarp();
+              constexpr int kL = D / 8, kR = 32 / kL;
+              const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
+              uint16_t* ob = p.a.out + (size_t)w.b * c.H * c.n_q * D;
+#pragma unroll 4
+              for (int i = 0; i < 32; i += kR) {
+                const int rl = i + lane / kL, u = lane % kL;
+                const int dst = __shfl_sync(~0u, mine, rl);
+                const float4 x = lds_f32x4(stage + unit_at<D>((warp & 3) * 32 + rl, u));
+                if (dst >= 0)
+                  *(reinterpret_cast<float4*>(ob + (size_t)(unsigned)dst * D) + u) = x;
+              }
+              __syncwarp();
             }
             if (live && whole && p.a.lse) p.a.lse[row] = (m + log2f(l)) * kLn2;
             if (live && !whole)
-              *reinterpret_cast<float2*>(p.a.ml + part * 2) = make_float2(m, l);
+              *reinterpret_cast<float2*>(p.a.ml + (part + pr) * 2) = make_float2(m, l);
           }
         }
         if (threadIdx.x == 0 && tile == 0 && tile_end < w.ut) {
@@ -505,75 +575,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp < 12) {
       // ------------------------------------------------------------ codes -> f16
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
       const int tid = threadIdx.x - 256;
       constexpr int kCh = D / 16;              // 16-byte chunks of a row of codes
       constexpr int kN = kTile * kCh / 128;    // chunks of a thread in a tile
       constexpr int kStep = 128 / kCh;         // rows between a thread's chunks
-      const int ch = tid % kCh, row0 = tid / kCh;
+      // a row's upper chunks go with its neighbour's lower ones (d_h = 128), so
+      // that the stores of 8 lanes touch every bank
+      const int ch = tid % kCh, row0 = (tid / kCh) ^ (D == 128 ? ch >> 2 : 0);
+      const int in_page = (1 << c.page_shift) - 1;
       uint4 kx[kN], vx[kN];
       float meta_k = 1.f, meta_v = 1.f;  // scales of group tid (tid < 8)
-      bool meta_there = false;
       // the tile being fetched, ahead of the one being converted
       Walk f = w;
       int f_tile = tile, f_end = 0;
       long long f_at = at;
       bool f_more = true;
       int f_ext = 0, f_kv = 0, f_kh = -1;
+      int f_page = -1;  // the page of group lane % 8 of the tile
+      int ahead = -1;   // ... of the tile after it, if it is of the same unit
+      int page_now = -1;  // ... of the tile being converted
+      auto look_up = [&](int tl) {
+        const int j = tl * kTile + 16 * (lane & 7);
+        return f_more && tl < f_end && j < f_ext ? page_at(c, f.b, j >> c.page_shift) : -1;
+      };
       auto open = [&]() {
         f_end = (int)min((long long)f.ut, f_tile + (sh.end - f_at));
-        f_ext = pair_extent(f.rows, f.pair, f.gk());
+        f_ext = pair_extent(f.rows, f.pair, f.gk(), f.ice());
         f_kv = p.cls_kv[f.cls];
-        f_kh = p.cls_static[f.cls] ? -1 : c.k_of[f_kv];
+        f_kh = f.ice() ? -1 : c.k_of[f_kv];
       };
       open();
-      auto address = [&](int key, int head, size_t off, bool& ok) {
-        const int j = f_tile * kTile + key;
-        ok = f_more && j < f_ext;
-        const int page = ok ? page_at(c, f.b, j >> c.page_shift) : -1;
-        ok = page >= 0;
-        return c.layer + (size_t)(ok ? page : 0) * c.page_stride + off +
-               (((size_t)head << c.page_shift) + (j & ((1 << c.page_shift) - 1))) * D + 16 * ch;
-      };
-      auto fetch_k = [&]() {
+      f_page = look_up(f_tile);
+      ahead = look_up(f_tile + 1);
+      auto fetch = [&](uint4(&x)[kN], int head, size_t off) {
+        const uint8_t* base = c.layer + off + (((size_t)head << c.page_shift) + row0) * D + 16 * ch;
+        const int left = f_ext - f_tile * kTile - row0;  // > n * kStep: the key exists
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-          bool ok = false;
-          const uint8_t* a = nullptr;
-          if (f_kh >= 0) a = address(row0 + n * kStep, f_kh, 0, ok);
-          kx[n] = ok ? __ldg(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
+          // the chunk's key is row0 + n * kStep; groups and pages are whole multiples of 16
+          const int key = row0 + n * kStep;
+          const int page = __shfl_sync(~0u, f_page, key >> 4);
+          const bool ok = page >= 0 && head >= 0 && n * kStep < left;
+          const uint8_t* a =
+              base + (size_t)(unsigned)page * c.page_stride + ((key & in_page) - row0) * D;
+          x[n] = ok ? __ldg(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
         }
       };
+      auto fetch_k = [&]() { fetch(kx, f_kh, 0); };
       auto fetch_v = [&]() {
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          bool ok;
-          const uint8_t* a = address(row0 + n * kStep, f_kv, c.off_v, ok);
-          vx[n] = ok ? __ldg(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
-        }
-        if (tid < 8) {
-          const int j = f_tile * kTile + 16 * tid;
-          const int page = f_more && j < f_ext ? page_at(c, f.b, j >> c.page_shift) : -1;
-          meta_there = page >= 0;
-          if (meta_there) {
-            const uint8_t* rec = c.layer + (size_t)page * c.page_stride;
-            meta_v = __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + f_kv);
-            meta_k = f_kh >= 0 ? __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + f_kh) : 1.f;
-          }
+        fetch(vx, f_kv, c.off_v);
+        page_now = f_page;
+        if (tid < 8 && f_page >= 0) {
+          const uint8_t* rec = c.layer + (size_t)f_page * c.page_stride;
+          meta_v = __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + f_kv);
+          meta_k = f_kh >= 0 ? __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + f_kh) : 1.f;
         }
       };
       auto fetch_next = [&]() {  // moves on to the next tile of the CTA
-        if (++f_tile < f_end) return;
-        f_at += f_end - (f_at == sh.begin ? tile : 0);
-        if (f_at >= sh.end) {
-          f_more = false;
-          return;
+        f_page = ahead;
+        if (++f_tile >= f_end) {
+          f_at += f_end - (f_at == sh.begin ? tile : 0);
+          f_more = f_at < sh.end;
+          if (f_more) {
+            f_tile = 0;
+            f.next();
+            open();
+          }
+          f_page = look_up(f_tile);
         }
-        f_tile = 0;
-        f.next();
-        open();
+        ahead = look_up(f_tile + 1);
       };
-      // one chunk of 16 codes as two units of 8 f16; lanes of the upper half of
-      // a row store their second unit first, so that 8 lanes touch every bank
+      // one chunk of 16 codes as two units of 8 f16
       auto store = [&](uint32_t base, int row, const uint4& x, bool clean, bool& bad) {
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
         uint32_t y[8];
@@ -588,19 +661,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             y[i] &= ok;
           }
         }
-        const bool up = ch * 2 >= kCh;
-        const uint32_t a0 = base + unit_at<D>(row, 2 * ch + (up ? 1 : 0));
-        const uint32_t a1 = base + unit_at<D>(row, 2 * ch + (up ? 0 : 1));
-        st_shared_v4(a0, up ? y[4] : y[0], up ? y[5] : y[1], up ? y[6] : y[2], up ? y[7] : y[3]);
-        st_shared_v4(a1, up ? y[0] : y[4], up ? y[1] : y[5], up ? y[2] : y[6], up ? y[3] : y[7]);
+        st_shared_v4(base + unit_at<D>(row, 2 * ch), y[0], y[1], y[2], y[3]);
+        st_shared_v4(base + unit_at<D>(row, 2 * ch + 1), y[4], y[5], y[6], y[7]);
       };
       uint32_t kc = 0, vc = 0;
       fetch_k();
       fetch_v();
       for (int seg = 0;; ++seg) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
-        const bool ice = p.cls_static[w.cls];
-        const int pos_lo = w.rows.base + w.pair * kRows / w.gk();  // the row that sees least
+        const bool ice = w.ice();
+        const int pos_lo = w.rows.base + pair_span(w.rows, w.pair, w.gk(), ice).lo;  // the row that sees least
         for (int i = tile; i < tile_end; ++i) {
           bool bad = false;
           fetch_next();
@@ -626,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (bad) nan_seg[seg & 3] = seg + 1;
           if (tid < 8) {
             // a group without a page: every logit -inf
-            const float lv = meta_there ? __log2f(meta_v) : -CUDART_INF_F;
+            const bool there = page_now >= 0;
+            const float lv = there ? __log2f(meta_v) : -CUDART_INF_F;
             *reinterpret_cast<float4*>(smem + L::OFF_META + (vc & 3) * 128 + tid * 16) =
-                make_float4(meta_there ? meta_k : 1.f, lv,
-                            meta_there ? __fdividef(1.f, meta_v) : 1.f, 0.f);
+                make_float4(there ? meta_k : 1.f, lv, there ? __fdividef(1.f, meta_v) : 1.f, 0.f);
           }
           mbar_arrive(m_full + (vc & 3));
           fetch_v();
@@ -642,23 +712,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile = 0;
         w.next();
       }
-    } else if (lane == 0) {
+    } else {
       // ------------------------------------------------------------ products
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+      if (warp == 12 && lane == 0) {
       constexpr uint32_t id_s = idesc_f16(128, kTile, false, false);
       constexpr uint32_t id_o = idesc_f16(128, D, false, true);
       uint32_t kc = 0, vc = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
       for (;;) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
         const int gk = w.gk();
-        const bool ice = p.cls_static[w.cls];
+        const bool ice = w.ice();
         const int n_g =
             (long long)w.rows.n_new * gk - (long long)w.pair * kRows > 128 ? 2 : 1;
         auto issue_s = [&](int g) {
-          const uint32_t kt = sK + (kc & 1) * L::TILE, qt = sQ + g * L::TILE;
-#pragma unroll
-          for (int kk = 0; kk < G::KSTEPS; ++kk)
-            mma_bf16_ss(tmem + kS + g * 128, G::kmajor_desc(qt, kk), G::kmajor_desc(kt, kk), id_s,
-                        kk > 0);
+          // the descriptors' start address is their lowest field: steps add to it
+          const uint64_t kt = G::kmajor_desc(sK + (kc & 1) * L::TILE, 0);
+          const uint64_t qt = G::kmajor_desc(sQ + g * L::TILE, 0);
+          constexpr int per = G::CHUNK / 16;
+#pragma unroll 1
+          for (int kk = 0; kk < G::KSTEPS; ++kk) {
+            const uint32_t step = ((kk / per) * G::CHUNK_BYTES + (kk % per) * 32) >> 4;
+            mma_bf16_ss(tmem + kS + g * 128, qt + step, kt + step, id_s, kk > 0);
+          }
           mma_commit(s_full + g);
         };
         if (!ice) {
@@ -675,14 +751,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = tile; i < tile_end; ++i) {
           const bool more = !ice && i + 1 < tile_end;
           mbar_wait(v_full + (vc & 1), (vc >> 1) & 1, wc, kSiteV);
-          const uint32_t vt = sV + (vc & 1) * L::TILE;
+          const uint64_t vt = G::mnmajor_desc(sV + (vc & 1) * L::TILE, 0);
+#pragma unroll 1
           for (int g = 0; g < n_g; ++g) {
             mbar_wait(p_full + g, n_p[g] & 1, wc, kSiteP);
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < kTile / 16; ++kk)
               mma_bf16_ts(tmem + kO + g * 128, tmem + kS + g * 128 + 8 * kk,
-                          G::mnmajor_desc(vt, kk), id_o, (i > tile || kk > 0));
+                          vt + (uint32_t)(kk * 16 * G::SWZ >> 4), id_o, (i > tile || kk > 0));
             mma_commit(o_done + g);
             if (more) {
               if (g == 0) mbar_wait(k_full + (kc & 1), (kc >> 1) & 1, wc, kSiteK);
@@ -708,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every product has completed before TMEM is freed
       mma_commit(drained);
       mbar_drain(drained, 0);
+      }
     }
   }
   __syncwarp();
@@ -732,12 +810,17 @@ __global__ void __launch_bounds__(256)
   const int first = 2 * blockIdx.x + (u.w >> 30 & 1);
   const Rows rows = slot_rows(c, b);
   int gk = 0;
+  bool ice = false;
   for (int g = 0; g < p.n_groups; ++g)
-    if (cls >= p.group_first[g]) gk = p.group_width[g];
+    if (cls >= p.group_first[g]) {
+      gk = p.group_width[g];
+      ice = p.group_static[g];
+    }
   const int n_rows =
       (int)min((long long)kRows, (long long)rows.n_new * gk - (long long)pair * kRows);
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < n_rows * (D / 4); i += gridDim.y * 256) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < kRows * (D / 4); i += gridDim.y * 256) {
+    const int r = i % kRows, d = i / kRows * 4;
+    if (r >= n_rows) continue;
     auto ml = [&](int part) {
       return *reinterpret_cast<const float2*>(p.a.ml + ((size_t)part * kRows + r) * 2);
     };
@@ -750,13 +833,16 @@ __global__ void __launch_bounds__(256)
       const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(x.x - mx);
       sum = fmaf(f, x.y, sum);
       const float4 v =
-          *reinterpret_cast<const float4*>(p.a.acc + ((size_t)part * kRows + r) * D + d);
+          *reinterpret_cast<const float4*>(p.a.acc + (size_t)part * kRows * D +
+                                           ((size_t)(d / 4) * kRows + r) * 4);
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);
       o.z = fmaf(f, v.z, o.z);
       o.w = fmaf(f, v.w, o.w);
     }
-    const int rr = pair * kRows + r, t = rr / gk, h = p.order[p.cls_first[cls] + rr - t * gk];
+    int t, idx;
+    row_of(rows, pair * kRows + r, gk, ice, t, idx);
+    const int h = p.order[p.cls_first[cls] + idx];
     const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2*>(p.a.out + row * D + d) =
@@ -829,21 +915,21 @@ cudaError_t launch_cache_chunk(const CacheAttn& a, int d_h, int n_sms, cudaStrea
         }
     }
   }
-  for (int w = c.group; w >= 1; --w) {
-    const int before = n;
-    for (int kind = 0; kind < 2; ++kind)
+  for (int w = c.group; w >= 1; --w)
+    for (int kind = 0; kind < 2; ++kind) {
+      const int before = n;
       for (int kv = 0; kv < c.H_kv; ++kv)
         if (width[kind][kv] == w) {
           p.cls_kv[n] = (uint8_t)kv;
-          p.cls_static[n] = (uint8_t)kind;
           p.cls_first[n] = (int16_t)(kv * c.group + (kind ? width[0][kv] : 0));
           ++n;
         }
-    if (n > before) {
-      p.group_width[p.n_groups] = w;
-      p.group_first[p.n_groups++] = before;
+      if (n > before) {
+        p.group_width[p.n_groups] = w;
+        p.group_static[p.n_groups] = kind;
+        p.group_first[p.n_groups++] = before;
+      }
     }
-  }
   p.group_first[p.n_groups] = n;
   switch (d_h) {
     case 32: return launch<32>(p, n_sms, s);

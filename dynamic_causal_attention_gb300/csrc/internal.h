@@ -152,14 +152,15 @@ CacheAttnWs cache_attn_ws(int d_h, int n_sms);
 cudaError_t launch_cache_attn(const CacheAttn& p, int d_h, int n_sms, cudaStream_t s);
 
 // Many rows (cache_chunk.cu): a class is the dynamic or the frozen query heads
-// of a K/V head; classes of equal width form a group.
+// of a K/V head; classes of equal width and kind form a group.
 struct CacheChunk {
   CacheAttn a;
   int n_groups;
   int group_width[kMaxHeads];       // heads of each class of the group
+  uint8_t group_static[kMaxHeads];
   int group_first[kMaxHeads + 1];   // its first class
   int16_t cls_first[kMaxHeads];     // a class's heads: order[cls_first ...]
-  uint8_t cls_kv[kMaxHeads], cls_static[kMaxHeads], order[kMaxHeads];
+  uint8_t cls_kv[kMaxHeads], order[kMaxHeads];
 };
 CacheAttnWs cache_chunk_ws(int d_h, int n_sms);
 cudaError_t launch_cache_chunk(const CacheAttn& p, int d_h, int n_sms, cudaStream_t s);

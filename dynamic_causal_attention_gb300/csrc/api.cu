@@ -136,6 +136,26 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, int d) {
   return r == CUDA_SUCCESS;
 }
 
+// 4-D view [n_pages, heads, page, d] of the codes of a cache layer, box of one
+// page's block of one head; a page number outside the pool reads zeros.
+bool encode_pages(CUtensorMap* m, const void* base, int d, int page, int heads, int n_pages,
+                  size_t page_stride) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads,
+                              (cuuint64_t)n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)d * page, (cuuint64_t)page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)page, 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUtensorMapSwizzle swz = d == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                 : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                           : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 // 2-D view [rows, d] of an fp32 tensor, box of 128 rows x 32 columns (128 B,
 // 128-byte swizzle): the staging layout of the backward's dQ reduction.

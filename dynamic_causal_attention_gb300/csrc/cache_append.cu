@@ -39,13 +39,6 @@ __device__ __forceinline__ void load8(const void* base, size_t off, bool f32, fl
   }
 }
 
-// e4m3 of two values, saturating; the NaN code for NaN
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The exponent of the least scale that holds amax (finite, >= 0).
 __device__ __forceinline__ int scale_exponent(float amax) {
   const int bits = __float_as_int(amax);

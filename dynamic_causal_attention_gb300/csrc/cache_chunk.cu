@@ -17,20 +17,31 @@
 // first two):
 //   warps 0-3, 4-7   the softmax of row tile 0 and 1: one row per thread.  They
 //                    also stage Q (scaled into f16) and write the results.
-//   warps 8-11       turn e4m3 codes into f16 tiles in shared memory (K: K-major,
-//                    V: MN-major, 128-byte swizzle); each thread holds the next
-//                    tile's codes in registers while it converts this one.
+//   warps 8-11       turn V's e4m3 codes into f16 tiles in shared memory.
 //   warp 12          allocates TMEM; one lane issues every product.
+//   warp 13          looks up pages, fetches K and V codes by TMA (a page that is
+//                    missing reads as zeros) and writes the scales of each tile.
+//
+// K needs no conversion: Q K^T runs on e4m3 operands at twice f16's rate, with
+// the row of q split into two e4m3 parts, q = hi + lo.  The row is scaled by a
+// power of two into e4m3's range; hi is q rounded to 4 bits, and what is left
+// of a bf16 value (8 bits) has at most 4: the sum is exact for components down
+// to 2^-10 of the row's largest, and below them it is off by at most 2^-18 of
+// the largest.  V is turned into f16 (exact): splitting the 256 x 128 weights
+// of a tile in its place would take six times the arithmetic of converting V's
+// 128 x d_h codes.
 //
 // TMEM: S of the two row tiles (128 columns each), then their O.  P, as packed
 // f16, overwrites the first half of its own S, so the next S of a row tile
 // waits for the product that reads P; the other row tile's products and
 // softmax run meanwhile.  A frozen row writes its logits into S itself.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
 #include "attn_common.cuh"
 #include "cache_common.cuh"
+#include "host_common.h"
 
 namespace saf {
 namespace {
@@ -40,16 +51,24 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 256;     // query rows of a unit
 constexpr int kTile = 128;     // keys of a tile
 constexpr int kThreads = 512;
-// registers of a thread after the split: 2 * 176 + 112 + 48 = 4 * 128
-constexpr int kRegsSoftmax = 176, kRegsConvert = 112, kRegsIssue = 48;
+// registers of a thread after the split: 2 * 176 + 80 + 80 = 4 * 128
+constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsIssue = 80;
 constexpr long long kMinTiles = 1;
 
-enum : int { kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree };
+enum : int {
+  kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree,
+  kSiteRaw, kSiteRawFree
+};
 
 // Instruction descriptor with f16 operands and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// ... with e4m3 operands (K-major both).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 __device__ __forceinline__ int pairs_of(const Rows& r, int gk) {
@@ -217,19 +236,31 @@ __device__ Share find_share(const CacheChunk& p, long long* scan /* [20] */) {
 
 template <int D>
 struct Smem {
-  static constexpr int TILE = kTile * D * 2;  // f16
+  static constexpr int CODES = kTile * D;     // e4m3
+  static constexpr int TILE = 2 * CODES;      // f16, or Q's two parts
+  static constexpr int KST = 3, RST = 2;      // stages of K codes and of V codes
   static constexpr int OFF_Q = 0;             // two row tiles
-  static constexpr int OFF_K = 2 * TILE;      // two stages
-  static constexpr int OFF_V = 4 * TILE;      // two stages
-  static constexpr int OFF_META = 6 * TILE;   // 4 tiles x 8 groups of 16 keys x 16 bytes
+  static constexpr int OFF_V = 2 * TILE;      // two stages of f16 V
+  static constexpr int OFF_K = 4 * TILE;
+  static constexpr int OFF_R = OFF_K + KST * CODES;
+  static constexpr int OFF_META = OFF_R + RST * CODES;  // 4 tiles x 8 groups of 16 keys x 16 bytes
   static constexpr int OFF_SCAN = OFF_META + 4 * 8 * 16;
   static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
-  static constexpr int NBAR = 2 + 4 + 4 + 4 + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 32;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
   static_assert(ALLOC <= 232448, "shared memory budget exceeded");
 };
+
+// Byte offset of 16-byte chunk ch of row r of a [128 x D] tile of codes: rows
+// of D bytes, swizzled over D bytes.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(uint32_t r, uint32_t ch) {
+  if (D == 128) return r * 128 + ((ch ^ (r & 7)) << 4);
+  if (D == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  return r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
+}
 
 // Byte offset of 16-byte unit u of row r of a [128 x D] f16 tile.
 template <int D>
@@ -240,7 +271,9 @@ __device__ __forceinline__ uint32_t unit_at(uint32_t r, uint32_t u) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    cache_chunk_kernel(const __grid_constant__ CacheChunk p) {
+    cache_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CacheChunk p) {
   using G = TileGeom<D>;
   using L = Smem<D>;
   const CacheCall& c = p.a.c;
@@ -249,15 +282,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_full = bars;          // [2] Q staged (128 arrivals)
-  uint64_t* k_full = q_full + 2;    // [2] stage converted (128)
-  uint64_t* k_empty = k_full + 2;   // [2] its products done
-  uint64_t* v_full = k_empty + 2;   // [2]
-  uint64_t* v_empty = v_full + 2;   // [2]
-  uint64_t* m_full = v_empty + 2;   // [4] a tile's scales (128)
-  uint64_t* s_full = m_full + 4;    // [2] S of a row tile done
-  uint64_t* p_full = s_full + 2;    // [2] P written, O rescaled (128)
-  uint64_t* o_done = p_full + 2;    // [2] a tile's P V done
-  uint64_t* drained = o_done + 2;   // every product done
+  uint64_t* k_full = q_full + 2;          // [KST] codes of K have landed
+  uint64_t* k_empty = k_full + L::KST;    // [KST] their products done
+  uint64_t* r_full = k_empty + L::KST;    // [RST] codes of V have landed
+  uint64_t* r_empty = r_full + L::RST;    // [RST] converted (128 arrivals)
+  uint64_t* v_full = r_empty + L::RST;    // [2] f16 V written (128)
+  uint64_t* v_empty = v_full + 2;         // [2] its products done
+  uint64_t* m_full = v_empty + 2;         // [4] a tile's scales (8)
+  uint64_t* s_full = m_full + 4;          // [2] S of a row tile done
+  uint64_t* p_full = s_full + 2;          // [2] P written, O rescaled (128)
+  // a tile's P V done: its products, and the issuing thread itself, which has
+  // seen v_full: what the converting warps wrote before is then visible
+  uint64_t* o_done = p_full + 2;          // [2] (2)
+  uint64_t* drained = o_done + 2;         // every product done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [4]
@@ -267,15 +304,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 128);
-      mbar_init(k_full + i, 128);
-      mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 128);
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 128);
-      mbar_init(o_done + i, 1);
+      mbar_init(o_done + i, 2);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(m_full + i, 128);
+    for (int i = 0; i < L::KST; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < L::RST; ++i) {
+      mbar_init(r_full + i, 1);
+      mbar_init(r_empty + i, 128);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(m_full + i, 8);
     mbar_init(drained, 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_seg[i] = 0;
@@ -292,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t sQ = smem_u32(smem + L::OFF_Q), sK = smem_u32(smem + L::OFF_K),
-                 sV = smem_u32(smem + L::OFF_V), sM = smem_u32(smem + L::OFF_META);
+                 sV = smem_u32(smem + L::OFF_V), sR = smem_u32(smem + L::OFF_R),
+                 sM = smem_u32(smem + L::OFF_META);
   constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S of row tile g at 128 g, O at 256 + 128 g
 
   if (sh.begin < sh.end) {
@@ -324,37 +368,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool warp_live = g * 128 + (warp & 3) * 32 < n_rows;
           float fac = 1.f;
           if (!ice) {
-            // rows of Q, each scaled by a power of two so that its largest
-            // component lies in [2^14, 2^15): kL lanes take a row
+            // rows of Q: scaled by the least 2^-e that brings the row within
+            // e4m3's range, split into hi + lo; kL lanes take a row
             constexpr int kL = D / 8, kR = 32 / kL;
             const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
             const uint16_t* qb = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
 #pragma unroll 4
             for (int i = 0; i < 32; i += kR) {
-              const int rl = i + lane / kL, u = lane % kL;  // row of the warp, 16-byte unit
+              const int rl = i + lane / kL, u = lane % kL;  // row of the warp, 8 components
               const int src = __shfl_sync(~0u, mine, rl);
               const uint4 q = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(
                                              qb + (size_t)(unsigned)src * D) + u)
                                        : make_uint4(0, 0, 0, 0);
               const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-              float amax = 0.f;
+              float y[8], amax = 0.f;
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[v] << 16)),
-                                         fabsf(__uint_as_float(x[v] & 0xffff0000u))));
+              for (int v = 0; v < 8; ++v) {
+                y[v] = __uint_as_float(v & 1 ? x[v / 2] & 0xffff0000u : x[v / 2] << 16);
+                amax = fmaxf(amax, fabsf(y[v]));
+              }
 #pragma unroll
               for (int o = kL / 2; o; o >>= 1)
                 amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-              int e = (__float_as_int(amax) >> 23) - 127 - 14;
-              e = amax > 0.f ? max(-126, min(112, e)) : 0;
+              const int bits = __float_as_int(amax);
+              int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+              e = amax > 0.f ? max(-126, min(120, e)) : 0;
               const float down = pow2f(-e);
-              uint32_t y[4];
+              uint32_t hi[2], lo[2];
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                y[v] = pack_f16x2(__uint_as_float(x[v] << 16) * down,
-                                  __uint_as_float(x[v] & 0xffff0000u) * down);
-              st_shared_v4(sQ + g * L::TILE + unit_at<D>((warp & 3) * 32 + rl, u), y[0], y[1],
-                           y[2], y[3]);
+              for (int v = 0; v < 2; ++v) {
+                float z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  z[k] = y[4 * v + k] * down;
+                  // e4m3 has no infinity: the row becomes NaN, as its softmax would
+                  if (fabsf(z[k]) == CUDART_INF_F) z[k] = CUDART_NAN_F;
+                }
+                hi[v] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
+                uint32_t a, b;
+                e4m3x4_f16x4(hi[v], a, b);
+                const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+                const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                lo[v] = e4m3x2(z[0] - fa.x, z[1] - fa.y) | e4m3x2(z[2] - fb.x, z[3] - fb.y) << 16;
+              }
+              const uint32_t at8 =
+                  sQ + g * L::TILE + code_at<D>((warp & 3) * 32 + rl, u >> 1) + (u & 1) * 8;
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8), "r"(hi[0]), "r"(hi[1])
+                           : "memory");
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8 + L::CODES), "r"(lo[0]),
+                           "r"(lo[1])
+                           : "memory");
               const int back = __shfl_sync(~0u, e, (lane - i) * kL & 31);
               if (lane >= i && lane < i + kR) fac = pow2f(back) * (rsqrtf((float)D) * kLog2e);
             }
@@ -574,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.next();
       }
     } else if (warp < 12) {
-      // ------------------------------------------------------------ codes -> f16
+      // ------------------------------------------------------------ V: codes -> f16
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
       const int tid = threadIdx.x - 256;
       constexpr int kCh = D / 16;              // 16-byte chunks of a row of codes
@@ -583,128 +646,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a row's upper chunks go with its neighbour's lower ones (d_h = 128), so
       // that the stores of 8 lanes touch every bank
       const int ch = tid % kCh, row0 = (tid / kCh) ^ (D == 128 ? ch >> 2 : 0);
-      const int in_page = (1 << c.page_shift) - 1;
-      uint4 kx[kN], vx[kN];
-      float meta_k = 1.f, meta_v = 1.f;  // scales of group tid (tid < 8)
-      // the tile being fetched, ahead of the one being converted
-      Walk f = w;
-      int f_tile = tile, f_end = 0;
-      long long f_at = at;
-      bool f_more = true;
-      int f_ext = 0, f_kv = 0, f_kh = -1;
-      int f_page = -1;  // the page of group lane % 8 of the tile
-      int ahead = -1;   // ... of the tile after it, if it is of the same unit
-      int page_now = -1;  // ... of the tile being converted
-      auto look_up = [&](int tl) {
-        const int j = tl * kTile + 16 * (lane & 7);
-        return f_more && tl < f_end && j < f_ext ? page_at(c, f.b, j >> c.page_shift) : -1;
-      };
-      auto open = [&]() {
-        f_end = (int)min((long long)f.ut, f_tile + (sh.end - f_at));
-        f_ext = pair_extent(f.rows, f.pair, f.gk(), f.ice());
-        f_kv = p.cls_kv[f.cls];
-        f_kh = f.ice() ? -1 : c.k_of[f_kv];
-      };
-      open();
-      f_page = look_up(f_tile);
-      ahead = look_up(f_tile + 1);
-      auto fetch = [&](uint4(&x)[kN], int head, size_t off) {
-        const uint8_t* base = c.layer + off + (((size_t)head << c.page_shift) + row0) * D + 16 * ch;
-        const int left = f_ext - f_tile * kTile - row0;  // > n * kStep: the key exists
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          // the chunk's key is row0 + n * kStep; groups and pages are whole multiples of 16
-          const int key = row0 + n * kStep;
-          const int page = __shfl_sync(~0u, f_page, key >> 4);
-          const bool ok = page >= 0 && head >= 0 && n * kStep < left;
-          const uint8_t* a =
-              base + (size_t)(unsigned)page * c.page_stride + ((key & in_page) - row0) * D;
-          x[n] = ok ? __ldg(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto fetch_k = [&]() { fetch(kx, f_kh, 0); };
-      auto fetch_v = [&]() {
-        fetch(vx, f_kv, c.off_v);
-        page_now = f_page;
-        if (tid < 8 && f_page >= 0) {
-          const uint8_t* rec = c.layer + (size_t)f_page * c.page_stride;
-          meta_v = __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + f_kv);
-          meta_k = f_kh >= 0 ? __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + f_kh) : 1.f;
-        }
-      };
-      auto fetch_next = [&]() {  // moves on to the next tile of the CTA
-        f_page = ahead;
-        if (++f_tile >= f_end) {
-          f_at += f_end - (f_at == sh.begin ? tile : 0);
-          f_more = f_at < sh.end;
-          if (f_more) {
-            f_tile = 0;
-            f.next();
-            open();
-          }
-          f_page = look_up(f_tile);
-        }
-        ahead = look_up(f_tile + 1);
-      };
-      // one chunk of 16 codes as two units of 8 f16
-      auto store = [&](uint32_t base, int row, const uint4& x, bool clean, bool& bad) {
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e4m3x4_f16x4(in[i], y[2 * i], y[2 * i + 1]);
-        if (clean) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const __half2 z = *reinterpret_cast<const __half2*>(&y[i]);
-            const uint32_t ok = __heq2_mask(z, z);
-            bad |= ok != ~0u;
-            y[i] &= ok;
-          }
-        }
-        st_shared_v4(base + unit_at<D>(row, 2 * ch), y[0], y[1], y[2], y[3]);
-        st_shared_v4(base + unit_at<D>(row, 2 * ch + 1), y[4], y[5], y[6], y[7]);
-      };
-      uint32_t kc = 0, vc = 0;
-      fetch_k();
-      fetch_v();
+      uint32_t vc = 0;
       for (int seg = 0;; ++seg) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
-        const bool ice = w.ice();
-        const int pos_lo = w.rows.base + pair_span(w.rows, w.pair, w.gk(), ice).lo;  // the row that sees least
+        // keys that not every row sees, and what lies behind the last key, may
+        // hold NaN: 0 * NaN must not reach the other rows
+        const int sure = min(w.rows.base + pair_span(w.rows, w.pair, w.gk(), w.ice()).lo + 1,
+                             pair_extent(w.rows, w.pair, w.gk(), w.ice()));
         for (int i = tile; i < tile_end; ++i) {
-          bool bad = false;
-          fetch_next();
-          if (!ice) {
-            const int st = kc & 1;
-            mbar_wait(k_empty + st, ((kc >> 1) & 1) ^ 1, wc, kSiteKFree);
+          const uint32_t rs = vc % L::RST, st = vc & 1;
+          mbar_wait(r_full + rs, (vc / L::RST) & 1, wc, kSiteRaw);
+          uint4 x[kN];
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
-              store(sK + st * L::TILE, row0 + n * kStep, kx[n], false, bad);
-            fetch_k();
-            fence_proxy_async_smem();
-            mbar_arrive(k_full + st);
-            ++kc;
-          } else {
-            fetch_k();
+          for (int n = 0; n < kN; ++n) {
+            const float4 y = lds_f32x4(sR + rs * L::CODES + code_at<D>(row0 + n * kStep, ch));
+            x[n] = *reinterpret_cast<const uint4*>(&y);
           }
-          const int st = vc & 1;
           mbar_wait(v_empty + st, ((vc >> 1) & 1) ^ 1, wc, kSiteVFree);
-          const bool clean = i * kTile + kTile - 1 > pos_lo;  // keys that not every row sees
+          const bool clean = (i + 1) * kTile > sure;
+          bool bad = false;
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
-            store(sV + st * L::TILE, row0 + n * kStep, vx[n], clean, bad);
-          if (bad) nan_seg[seg & 3] = seg + 1;
-          if (tid < 8) {
-            // a group without a page: every logit -inf
-            const bool there = page_now >= 0;
-            const float lv = there ? __log2f(meta_v) : -CUDART_INF_F;
-            *reinterpret_cast<float4*>(smem + L::OFF_META + (vc & 3) * 128 + tid * 16) =
-                make_float4(there ? meta_k : 1.f, lv, there ? __fdividef(1.f, meta_v) : 1.f, 0.f);
+          for (int n = 0; n < kN; ++n) {
+            const uint32_t in[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e4m3x4_f16x4(in[k], y[2 * k], y[2 * k + 1]);
+            if (clean) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const __half2 z = *reinterpret_cast<const __half2*>(&y[k]);
+                const uint32_t ok = __heq2_mask(z, z);
+                bad |= ok != ~0u;
+                y[k] &= ok;
+              }
+            }
+            const uint32_t to = sV + st * L::TILE, row = row0 + n * kStep;
+            st_shared_v4(to + unit_at<D>(row, 2 * ch), y[0], y[1], y[2], y[3]);
+            st_shared_v4(to + unit_at<D>(row, 2 * ch + 1), y[4], y[5], y[6], y[7]);
           }
-          mbar_arrive(m_full + (vc & 3));
-          fetch_v();
+          if (bad) nan_seg[seg & 3] = seg + 1;
           fence_proxy_async_smem();
           mbar_arrive(v_full + st);
+          mbar_arrive(r_empty + rs);
           ++vc;
         }
         at += tile_end - tile;
@@ -716,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ products
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
       if (warp == 12 && lane == 0) {
-      constexpr uint32_t id_s = idesc_f16(128, kTile, false, false);
+      constexpr uint32_t id_s = idesc_e4m3(128, kTile);
       constexpr uint32_t id_o = idesc_f16(128, D, false, true);
       uint32_t kc = 0, vc = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
       for (;;) {
@@ -726,26 +709,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_g =
             (long long)w.rows.n_new * gk - (long long)w.pair * kRows > 128 ? 2 : 1;
         auto issue_s = [&](int g) {
-          // the descriptors' start address is their lowest field: steps add to it
-          const uint64_t kt = G::kmajor_desc(sK + (kc & 1) * L::TILE, 0);
-          const uint64_t qt = G::kmajor_desc(sQ + g * L::TILE, 0);
-          constexpr int per = G::CHUNK / 16;
+          // the descriptors' start address is their lowest field: steps of 32
+          // codes add to it
+          const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES, 16, 8 * D, swizzle_layout_code(D));
+          const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
 #pragma unroll 1
-          for (int kk = 0; kk < G::KSTEPS; ++kk) {
-            const uint32_t step = ((kk / per) * G::CHUNK_BYTES + (kk % per) * 32) >> 4;
-            mma_bf16_ss(tmem + kS + g * 128, qt + step, kt + step, id_s, kk > 0);
-          }
+          for (int part = 0; part < 2; ++part)
+#pragma unroll 1
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8_ss(tmem + kS + g * 128, qt + (part * L::CODES + kk * 32 >> 4),
+                        kt + (kk * 32 >> 4), id_s, part + kk > 0);
           mma_commit(s_full + g);
         };
         if (!ice) {
-          mbar_wait(k_full + (kc & 1), (kc >> 1) & 1, wc, kSiteK);
+          mbar_wait(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK);
           for (int g = 0; g < n_g; ++g) {
             mbar_wait(q_full + g, n_q[g] & 1, wc, kSiteQ);
             ++n_q[g];
             tc_fence_after();
             issue_s(g);
           }
-          mma_commit(k_empty + (kc & 1));
+          mma_commit(k_empty + kc % L::KST);
           ++kc;
         }
         for (int i = tile; i < tile_end; ++i) {
@@ -761,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_bf16_ts(tmem + kO + g * 128, tmem + kS + g * 128 + 8 * kk,
                           vt + (uint32_t)(kk * 16 * G::SWZ >> 4), id_o, (i > tile || kk > 0));
             mma_commit(o_done + g);
+            mbar_arrive(o_done + g);
             if (more) {
-              if (g == 0) mbar_wait(k_full + (kc & 1), (kc >> 1) & 1, wc, kSiteK);
+              if (g == 0) mbar_wait(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK);
               // S takes the columns of the P that this product reads
               mbar_wait(o_done + g, n_p[g] & 1, wc, kSiteO);
               tc_fence_after();
@@ -773,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(v_empty + (vc & 1));
           ++vc;
           if (more) {
-            mma_commit(k_empty + (kc & 1));
+            mma_commit(k_empty + kc % L::KST);
             ++kc;
           }
         }
@@ -785,6 +770,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every product has completed before TMEM is freed
       mma_commit(drained);
       mbar_drain(drained, 0);
+      } else if (warp == 13) {
+        // ---------------------------------------------------------- codes and scales
+        uint32_t kc = 0, vc = 0;
+        const int per = c.page_shift > 4 ? 1 << (c.page_shift - 4) : 1;  // groups of a page
+        for (;;) {
+          const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+          const int kv = p.cls_kv[w.cls], kh = w.ice() ? -1 : c.k_of[kv];
+          const int ext = pair_extent(w.rows, w.pair, w.gk(), w.ice());
+          // lane % 8: its group's page, two tiles ahead, and scales, one ahead
+          auto look_up = [&](int tl) {
+            const int j = tl * kTile + 16 * (lane & 7);
+            return tl < tile_end && j < ext ? page_at(c, w.b, j >> c.page_shift) : -1;
+          };
+          auto scales = [&](int page) {
+            if (page < 0) return make_float2(1.f, -1.f);
+            const uint8_t* rec = c.layer + (size_t)page * c.page_stride;
+            return make_float2(
+                kh >= 0 ? __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + kh) : 1.f,
+                __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + kv));
+          };
+          int page = look_up(tile), page1 = look_up(tile + 1);
+          float2 sc = scales(page);
+          for (int i = tile; i < tile_end; ++i) {
+            const int page2 = look_up(i + 2);
+            const float2 sc1 = scales(page1);
+            if (kh >= 0) {
+              const uint32_t st = kc % L::KST;
+              mbar_wait(k_empty + st, ((kc / L::KST) & 1) ^ 1, wc, kSiteKFree);
+              if (lane == 0) mbar_arrive_expect_tx(k_full + st, L::CODES);
+              for (int g = 0; g < 8; g += per) {
+                const int pg = __shfl_sync(~0u, page, g);
+                if (lane == 0)
+                  tma_load_4d(smem + L::OFF_K + st * L::CODES + g * 16 * D, &tm_k, k_full + st, kh,
+                              pg);
+              }
+              ++kc;
+            }
+            const uint32_t st = vc % L::RST;
+            mbar_wait(r_empty + st, ((vc / L::RST) & 1) ^ 1, wc, kSiteRawFree);
+            if (lane < 8) {
+              // a group without a page: every logit -inf
+              const bool there = page >= 0;
+              *reinterpret_cast<float4*>(smem + L::OFF_META + (vc & 3) * 128 + lane * 16) =
+                  make_float4(sc.x, there ? __log2f(sc.y) : -CUDART_INF_F,
+                              there ? __fdividef(1.f, sc.y) : 1.f, 0.f);
+              mbar_arrive(m_full + (vc & 3));
+            }
+            if (lane == 0) mbar_arrive_expect_tx(r_full + st, L::CODES);
+            for (int g = 0; g < 8; g += per) {
+              const int pg = __shfl_sync(~0u, page, g);
+              if (lane == 0)
+                tma_load_4d(smem + L::OFF_R + st * L::CODES + g * 16 * D, &tm_v, r_full + st, kv,
+                            pg);
+            }
+            ++vc;
+            page = page1;
+            page1 = page2;
+            sc = sc1;
+          }
+          at += tile_end - tile;
+          if (at >= sh.end) break;
+          tile = 0;
+          w.next();
+        }
+        // every copy has landed before the CTA ends
+        for (uint32_t s = 0; s < L::KST; ++s)
+          if (kc > s) mbar_drain(k_full + (kc - 1 - s) % L::KST, ((kc - 1 - s) / L::KST) & 1);
+        for (uint32_t s = 0; s < L::RST; ++s)
+          if (vc > s) mbar_drain(r_full + (vc - 1 - s) % L::RST, ((vc - 1 - s) / L::RST) & 1);
       }
     }
   }
@@ -858,7 +912,15 @@ cudaError_t launch(const CacheChunk& p, int n_sms, cudaStream_t s) {
   e = set_max_dynamic_smem(reinterpret_cast<const void*>(cache_chunk_kernel<D>), Smem<D>::ALLOC);
   if (e != cudaSuccess) return e;
   trace_begin(s);
-  cache_chunk_kernel<D><<<n_sms, kThreads, Smem<D>::ALLOC, s>>>(p);
+  const CacheCall& c = p.a.c;
+  CUtensorMap tm_k, tm_v;
+  const uint8_t* v = c.layer + c.off_v;
+  // without stored K heads its map stands for V's and is never used
+  if (!encode_pages(&tm_v, v, D, 1 << c.page_shift, c.H_kv, c.n_pages, c.page_stride) ||
+      !encode_pages(&tm_k, c.H_k ? c.layer : v, D, 1 << c.page_shift, c.H_k ? c.H_k : c.H_kv,
+                    c.n_pages, c.page_stride))
+    return cudaErrorInvalidValue;
+  cache_chunk_kernel<D><<<n_sms, kThreads, Smem<D>::ALLOC, s>>>(tm_k, tm_v, p);
   trace_end(s, "cache_chunk");
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -50,4 +50,9 @@ void fill_fwd_params(FwdParams& p, const saf_attn_dims& d, const HeadSplit& hs,
 // 2-D view [rows, d] of a bf16 tensor, box of 128 rows x one swizzle chunk.
 bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, int d);
 
+// 4-D view [n_pages, heads, page, d] of the codes of a cache layer, box of one
+// page's block of one head.
+bool encode_pages(CUtensorMap* m, const void* base, int d, int page, int heads, int n_pages,
+                  size_t page_stride);
+
 }  // namespace saf

@@ -18,7 +18,8 @@
 //   warps 0-3, 4-7   the softmax of row tile 0 and 1: one row per thread.  They
 //                    also stage Q (scaled into f16) and write the results.
 //   warps 8-11       turn V's e4m3 codes into f16 tiles in shared memory.
-//   warp 12          allocates TMEM; one lane issues every product.
+//   warps 12, 14     issue the products of row tile 0 and 1 (one lane each); 12
+//                    allocates TMEM.
 //   warp 13          looks up pages, fetches K and V codes by TMA (a page that is
 //                    missing reads as zeros) and writes the scales of each tile.
 //
@@ -64,6 +65,55 @@ enum : int {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// A chain of products into one accumulator from one statement: k-step after
+// k-step with the descriptors advanced by adds.  One issuing thread then gets a
+// product through in about 75 cycles in place of about 160.
+template <int N, int STEP>  // S += hi K^T, then lo K^T: N steps of 32 codes each
+__device__ __forceinline__ void issue_codes(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+#define SAF_MMA8 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, "
+#define SAF_NEXT "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+#define SAF_HEAD                                                                              \
+  "{\n\t.reg .pred f, t;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 t, 0, 0;\n\tmov.pred f, t;\n\t"    \
+  "not.pred t, f;\n\tmov.b64 a, %1;\n\tmov.b64 b, %2;\n\t"
+#define SAF_LOW "add.s64 a, %1, %4;\n\tmov.b64 b, %2;\n\t"
+  if constexpr (N == 1)
+    asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_LOW SAF_MMA8 "t;\n\t}" ::"r"(d), "l"(q), "l"(k),
+                 "r"(idesc), "n"(STEP)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_LOW SAF_MMA8
+                 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t}" ::"r"(d),
+                 "l"(q), "l"(k), "r"(idesc), "n"(STEP)
+                 : "memory");
+  else
+    asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8
+                 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_LOW SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8
+                 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t}" ::"r"(d),
+                 "l"(q), "l"(k), "r"(idesc), "n"(STEP)
+                 : "memory");
+#undef SAF_MMA8
+#undef SAF_NEXT
+#undef SAF_HEAD
+#undef SAF_LOW
+}
+// O (+)= P V for 64 keys: 4 steps of 16, P in TMEM (8 columns a step), V's
+// descriptor advanced by STEP.
+template <int STEP>
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc,
+                                         uint32_t accumulate) {
+#define SAF_MMA "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, "
+#define SAF_NEXT "add.s32 a, a, 8;\n\tadd.s64 b, b, %5;\n\t"
+  asm volatile(
+      "{\n\t.reg .pred f, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\tsetp.ne.b32 f, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\tmov.b32 a, %1;\n\tmov.b64 b, %2;\n\t" SAF_MMA "f;\n\t" SAF_NEXT
+      SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t}" ::"r"(d),
+      "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "n"(STEP)
+      : "memory");
+#undef SAF_MMA
+#undef SAF_NEXT
 }
 
 // ... with e4m3 operands (K-major both).
@@ -246,7 +296,7 @@ struct Smem {
   static constexpr int OFF_META = OFF_R + RST * CODES;  // 4 tiles x 8 groups of 16 keys x 16 bytes
   static constexpr int OFF_SCAN = OFF_META + 4 * 8 * 16;
   static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
-  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 4 + 2 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 32;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
@@ -290,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_empty = v_full + 2;         // [2] its products done
   uint64_t* m_full = v_empty + 2;         // [4] a tile's scales (8)
   uint64_t* s_full = m_full + 4;          // [2] S of a row tile done
-  uint64_t* p_full = s_full + 2;          // [2] P written, O rescaled (128)
+  uint64_t* p_full = s_full + 2;          // [2][2] half of P written, O rescaled (128)
   // a tile's P V done: its products, and the issuing thread itself, which has
   // seen v_full: what the converting warps wrote before is then visible
-  uint64_t* o_done = p_full + 2;          // [2] (2)
-  uint64_t* drained = o_done + 2;         // every product done
+  uint64_t* o_done = p_full + 4;          // [2] (2)
+  uint64_t* drained = o_done + 2;         // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [4]
@@ -305,14 +355,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 128);
       mbar_init(v_full + i, 128);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, 2);  // both issuers
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 128);
+      mbar_init(p_full + 2 * i, 128);
+      mbar_init(p_full + 2 * i + 1, 128);
       mbar_init(o_done + i, 2);
     }
     for (int i = 0; i < L::KST; ++i) {
       mbar_init(k_full + i, 1);
-      mbar_init(k_empty + i, 1);
+      mbar_init(k_empty + i, 2);
     }
     for (int i = 0; i < L::RST; ++i) {
       mbar_init(r_full + i, 1);
@@ -320,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) mbar_init(m_full + i, 8);
     mbar_init(drained, 1);
+    mbar_init(drained + 1, 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_seg[i] = 0;
     fence_barrier_init();
@@ -541,11 +593,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_unpack(sum, x, y);
                 l = fmaf(x + y, mt.z, l);
                 tmem_st_x8(s_col + 8 * q, pk);
+                if (q == 3) {  // the first half's product may start
+                  tmem_wait_st();
+                  tc_fence_before();
+                  mbar_arrive(p_full + 2 * g);
+                }
               }
               tmem_wait_st();
+            } else {
+              tc_fence_before();
+              mbar_arrive(p_full + 2 * g);
             }
             tc_fence_before();
-            mbar_arrive(p_full + g);
+            mbar_arrive(p_full + 2 * g + 1);
             ++n_p;
           }
           // ---- results
@@ -698,78 +758,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------ products
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-      if (warp == 12 && lane == 0) {
-      constexpr uint32_t id_s = idesc_e4m3(128, kTile);
-      constexpr uint32_t id_o = idesc_f16(128, D, false, true);
-      uint32_t kc = 0, vc = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-      for (;;) {
-        const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
-        const int gk = w.gk();
-        const bool ice = w.ice();
-        const int n_g =
-            (long long)w.rows.n_new * gk - (long long)w.pair * kRows > 128 ? 2 : 1;
-        auto issue_s = [&](int g) {
-          // the descriptors' start address is their lowest field: steps of 32
-          // codes add to it
-          const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES, 16, 8 * D, swizzle_layout_code(D));
-          const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part)
-#pragma unroll 1
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8_ss(tmem + kS + g * 128, qt + (part * L::CODES + kk * 32 >> 4),
-                        kt + (kk * 32 >> 4), id_s, part + kk > 0);
-          mma_commit(s_full + g);
-        };
-        if (!ice) {
-          mbar_wait(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK);
-          for (int g = 0; g < n_g; ++g) {
-            mbar_wait(q_full + g, n_q[g] & 1, wc, kSiteQ);
-            ++n_q[g];
+      if ((warp == 12 || warp == 14) && lane == 0) {
+        const int g = (warp - 12) >> 1;
+        constexpr uint32_t id_s = idesc_e4m3(128, kTile);
+        constexpr uint32_t id_o = idesc_f16(128, D, false, true);
+        const uint32_t s_col = tmem + kS + g * 128, o_col = tmem + kO + g * 128;
+        const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
+        uint32_t kc = 0, vc = 0, n_q = 0, n_p = 0;
+        for (;;) {
+          const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+          const bool ice = w.ice();
+          const bool mine =
+              (long long)w.rows.n_new * w.gk() - (long long)w.pair * kRows > g * 128;
+          auto issue_s = [&]() {  // the next tile's S; the stage is free when it is done
+            const uint32_t st = kc % L::KST;
+            mbar_poll(k_full + st, (kc / L::KST) & 1, wc, kSiteK);
             tc_fence_after();
-            issue_s(g);
-          }
-          mma_commit(k_empty + kc % L::KST);
-          ++kc;
-        }
-        for (int i = tile; i < tile_end; ++i) {
-          const bool more = !ice && i + 1 < tile_end;
-          mbar_wait(v_full + (vc & 1), (vc >> 1) & 1, wc, kSiteV);
-          const uint64_t vt = G::mnmajor_desc(sV + (vc & 1) * L::TILE, 0);
-#pragma unroll 1
-          for (int g = 0; g < n_g; ++g) {
-            mbar_wait(p_full + g, n_p[g] & 1, wc, kSiteP);
-            tc_fence_after();
-#pragma unroll 1
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_bf16_ts(tmem + kO + g * 128, tmem + kS + g * 128 + 8 * kk,
-                          vt + (uint32_t)(kk * 16 * G::SWZ >> 4), id_o, (i > tile || kk > 0));
-            mma_commit(o_done + g);
-            mbar_arrive(o_done + g);
-            if (more) {
-              if (g == 0) mbar_wait(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK);
-              // S takes the columns of the P that this product reads
-              mbar_wait(o_done + g, n_p[g] & 1, wc, kSiteO);
-              tc_fence_after();
-              issue_s(g);
+            if (mine) {
+              const uint64_t kt = sdesc(sK + st * L::CODES, 16, 8 * D, swizzle_layout_code(D));
+              issue_codes<D / 32, (L::CODES >> 4)>(s_col, qt, kt, id_s);
+              mma_commit(k_empty + st);
+              mma_commit(s_full + g);
+            } else {
+              mbar_arrive(k_empty + st);
             }
-            ++n_p[g];
-          }
-          mma_commit(v_empty + (vc & 1));
-          ++vc;
-          if (more) {
-            mma_commit(k_empty + kc % L::KST);
             ++kc;
+          };
+          if (!ice) {
+            if (mine) mbar_poll(q_full + g, n_q++ & 1, wc, kSiteQ);
+            issue_s();
           }
+          for (int i = tile; i < tile_end; ++i) {
+            const uint32_t st = vc & 1;
+            mbar_poll(v_full + st, (vc >> 1) & 1, wc, kSiteV);
+            ++vc;
+            if (mine) {
+              const uint64_t vt = G::mnmajor_desc(sV + st * L::TILE, 0);
+              constexpr int kVStep = 16 * G::SWZ >> 4;
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                mbar_poll(p_full + 2 * g + half, n_p & 1, wc, kSiteP);
+                tc_fence_after();
+                issue_pv<kVStep>(o_col, s_col + 32 * half, vt + 4 * kVStep * half, id_o,
+                                 i > tile || half);
+              }
+              mma_commit(v_empty + st);
+              mma_commit(o_done + g);
+              mbar_arrive(o_done + g);
+              // S takes the columns of the P that these products read
+              if (!ice && i + 1 < tile_end) {
+                mbar_poll(o_done + g, n_p & 1, wc, kSiteO);
+                tc_fence_after();
+              }
+              ++n_p;
+            } else {
+              mbar_arrive(v_empty + st);
+            }
+            if (!ice && i + 1 < tile_end) issue_s();
+          }
+          at += tile_end - tile;
+          if (at >= sh.end) break;
+          tile = 0;
+          w.next();
         }
-        at += tile_end - tile;
-        if (at >= sh.end) break;
-        tile = 0;
-        w.next();
-      }
-      // every product has completed before TMEM is freed
-      mma_commit(drained);
-      mbar_drain(drained, 0);
+        // every product has completed before TMEM is freed
+        mma_commit(drained + g);
+        mbar_drain(drained + g, 0);
       } else if (warp == 13) {
         // ---------------------------------------------------------- codes and scales
         uint32_t kc = 0, vc = 0;

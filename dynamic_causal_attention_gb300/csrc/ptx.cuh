@@ -95,6 +95,38 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// mbar_wait for a thread that a whole CTA waits on: it polls (test_wait) and
+// is not suspended, so it sees the phase sooner.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const WaitCtl& w,
+                                          int site) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test_wait(a, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_test_wait(a, parity)) return true;
+    if (*w.abort) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+      wait_timed_out(w, site);
+      return false;
+    }
+  }
+}
+
 // Bounded wait that ignores the abort flag (used to drain copies in flight
 // before the CTA exits).
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {

@@ -21,7 +21,8 @@ saf_status check_cache(const saf_cache_dims* d) {
     return SAF_ERR_UNSUPPORTED;
   if (d->d_h != 32 && d->d_h != 64 && d->d_h != 128) return SAF_ERR_UNSUPPORTED;
   if (d->H > kMaxHeads || d->n_seqs > kMaxSlots) return SAF_ERR_UNSUPPORTED;
-  if ((long long)d->max_pages * d->page_size >= (1ll << 31)) return SAF_ERR_UNSUPPORTED;
+  // the kernels step past the last key by less than a tile
+  if ((long long)d->max_pages * d->page_size > (1ll << 31) - 1024) return SAF_ERR_UNSUPPORTED;
   if (d->page_stride % 16 != 0) return SAF_ERR_INVALID_ARG;
   return SAF_OK;
 }

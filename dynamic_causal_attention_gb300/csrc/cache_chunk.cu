@@ -6,21 +6,21 @@
 // A unit is (slot, class, row pair): a class is the dynamic or the frozen
 // query heads of one K/V head; its rows are r = t * heads + index (dynamic: the
 // last key that a unit sees is then as early as can be) or r = index * n_new + t
-// (frozen: a warp's rows share alpha and read rho side by side), and a unit
-// takes 256 of them as two tiles of 128, against the keys up to the last
+// (frozen: a warp's rows share alpha and read rho side by side; from 128 new
+// tokens on each head begins a unit of its own), and a unit takes 256 of them as two tiles of 128, against the keys up to the last
 // position among them in tiles of 128.  Splitting a group by kind keeps every
 // warp uniform and spares frozen rows the Q K product.  All tiles of all
 // units are cut into equal shares, one for each CTA (one per SM), as in
 // cache_attn.cu.
 //
-// Warp roles (512 threads; registers move from the last two warpgroups to the
-// first two):
-//   warps 0-3, 4-7   the softmax of row tile 0 and 1: one row per thread.  They
-//                    also stage Q (scaled into f16) and write the results.
-//   warps 8-11       turn V's e4m3 codes into f16 tiles in shared memory.
-//   warps 12, 14     issue the products of row tile 0 and 1 (one lane each); 12
+// Warp roles (768 threads; registers move to the softmax):
+//   warps 0-15       the softmax: row tile g = warp / 8, two threads to a row,
+//                    one for each half of the 128 key columns.  They also stage
+//                    Q and write the results.
+//   warps 16-19      turn V's e4m3 codes into f16 tiles in shared memory.
+//   warps 20, 22     issue the products of row tile 0 and 1 (one lane each); 20
 //                    allocates TMEM.
-//   warp 13          looks up pages, fetches K and V codes by TMA (a page that is
+//   warp 21          looks up pages, fetches K and V codes by TMA (a page that is
 //                    missing reads as zeros) and writes the scales of each tile.
 //
 // K needs no conversion: Q K^T runs on e4m3 operands at twice f16's rate, with
@@ -33,7 +33,7 @@
 // 128 x d_h codes.
 //
 // TMEM: S of the two row tiles (128 columns each), then their O.  P, as packed
-// f16, overwrites the first half of its own S, so the next S of a row tile
+// f16, overwrites half of the S columns that its thread has read, so the next S of a row tile
 // waits for the product that reads P; the other row tile's products and
 // softmax run meanwhile.  A frozen row writes its logits into S itself.
 #include <cuda.h>
@@ -51,15 +51,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 256;     // query rows of a unit
 constexpr int kTile = 128;     // keys of a tile
-constexpr int kThreads = 512;
-// registers of a thread after the split: 2 * 176 + 80 + 80 = 4 * 128
-constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsIssue = 80;
+constexpr int kThreads = 768;
+// registers of a thread after the split: 4 * 96 + 48 + 48 = 6 * 80
+constexpr int kRegsSoftmax = 96, kRegsConvert = 48, kRegsIssue = 48;
 constexpr long long kMinTiles = 1;
 
 enum : int {
   kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree,
   kSiteRaw, kSiteRawFree
 };
+
+constexpr int kBarTurn = 1;  // named barriers 1 and 2: row tile 0's and 1's turn
+constexpr int kBarPair = 3;  // 3-10: the two warps that share 32 rows
 
 // Instruction descriptor with f16 operands and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -121,28 +124,46 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ int pairs_of(const Rows& r, int gk) {
+// The rows of a class fall into units of up to 256.  Frozen heads with many
+// new tokens do not share a unit.
+__device__ __forceinline__ bool by_head(const Rows& r, bool ice) { return ice && r.n_new >= 128; }
+__device__ __forceinline__ int pairs_of(const Rows& r, int gk, bool ice) {
+  if (by_head(r, ice)) return (r.n_new + kRows - 1) / kRows * gk;
   return (int)(((long long)r.n_new * gk + kRows - 1) / kRows);
+}
+struct UnitRows {
+  int first, n;  // rows [first, first + n) of the class
+};
+__device__ __forceinline__ UnitRows unit_rows(const Rows& r, int pair, int gk, bool ice) {
+  UnitRows u;
+  if (by_head(r, ice)) {
+    const int per = (r.n_new + kRows - 1) / kRows, idx = pair / per, at = (pair - idx * per) * kRows;
+    u.first = idx * r.n_new + at;
+    u.n = min(kRows, r.n_new - at);
+  } else {
+    u.first = pair * kRows;
+    u.n = min(kRows, r.n_new * gk - u.first);
+  }
+  return u;
 }
 // The tokens [lo, hi) of a unit's rows.
 struct Span {
   int lo, hi;
 };
 __device__ __forceinline__ Span pair_span(const Rows& r, int pair, int gk, bool ice) {
+  const UnitRows u = unit_rows(r, pair, gk, ice);
   Span s;
   if (ice) {
-    const int at = pair * kRows;
-    s.lo = at % r.n_new;
-    s.hi = s.lo + kRows;
-    if (s.hi > r.n_new) {  // the rows may go on with the next head's first token
-      const bool next = (long long)at + r.n_new - s.lo < (long long)r.n_new * gk;
-      if (next) s.lo = 0;
+    s.lo = u.first % r.n_new;
+    s.hi = s.lo + u.n;
+    if (s.hi > r.n_new) {  // the rows go on with the next head's first token
+      s.lo = 0;
       s.hi = r.n_new;
     }
-    return s;
+  } else {
+    s.lo = u.first / gk;
+    s.hi = (u.first + u.n - 1) / gk + 1;
   }
-  s.lo = pair * kRows / gk;
-  s.hi = min((pair * kRows + kRows - 1) / gk + 1, r.n_new);
   return s;
 }
 __device__ __forceinline__ int pair_extent(const Rows& r, int pair, int gk, bool ice) {
@@ -152,6 +173,10 @@ __device__ __forceinline__ int pair_extent(const Rows& r, int pair, int gk, bool
 __device__ __forceinline__ int pair_tiles(const Rows& r, int pair, int gk, bool ice) {
   const int n = (pair_extent(r, pair, gk, ice) + kTile - 1) / kTile;
   return n < 1 ? 1 : n;  // rows that see nothing are written too
+}
+// Whether a unit's rows are of one frozen head.
+__device__ __forceinline__ bool one_head(const Rows& r, const UnitRows& u) {
+  return u.first / r.n_new == (u.first + u.n - 1) / r.n_new;
 }
 // Row `rr` of a class as (token, index of the head).
 __device__ __forceinline__ void row_of(const Rows& r, int rr, int gk, bool ice, int& t, int& idx) {
@@ -188,7 +213,7 @@ struct Walk {
     long long sum = 0;
     for (int g = 0; g < p.n_groups; ++g) {
       long long mine = 0;
-      const int w = p.group_width[g], n = pairs_of(r, w);
+      const int w = p.group_width[g], n = pairs_of(r, w, p.group_static[g]);
       for (int i = lane; i < n; i += 32) mine += pair_tiles(r, i, w, p.group_static[g]);
       sum += mine * classes(g);
     }
@@ -200,7 +225,7 @@ struct Walk {
     b = slot;
     rows = slot_rows(p.a.c, b);
     for (group = 0;; ++group) {
-      const int n = pairs_of(rows, gk()), n_cls = classes(group);
+      const int n = pairs_of(rows, gk(), ice()), n_cls = classes(group);
       for (pair = 0; pair < n; pair += 32) {
         const int i = pair + lane;
         const int mine = i < n ? pair_tiles(rows, i, gk(), ice()) : 0;
@@ -225,7 +250,7 @@ struct Walk {
   }
   __device__ void next() {
     if (++cls == p.group_first[group + 1]) {
-      if (++pair >= pairs_of(rows, gk())) {
+      if (++pair >= pairs_of(rows, gk(), ice())) {
         pair = 0;
         if (++group == p.n_groups) {
           do {
@@ -247,7 +272,7 @@ struct Share {
 // Every CTA finds its share: each warp sums a run of slots, the sums of the
 // warps before give a run's first tile, and the warp whose run holds the
 // share's first tile walks it.
-__device__ Share find_share(const CacheChunk& p, long long* scan /* [20] */) {
+__device__ Share find_share(const CacheChunk& p, long long* scan /* [warps + 2] */) {
   const Walk w(p);
   constexpr int kN = kThreads / 32;
   const int warp = threadIdx.x >> 5, n_seqs = p.a.c.n_seqs;
@@ -294,9 +319,15 @@ struct Smem {
   static constexpr int OFF_K = 4 * TILE;
   static constexpr int OFF_R = OFF_K + KST * CODES;
   static constexpr int OFF_META = OFF_R + RST * CODES;  // 4 tiles x 8 groups of 16 keys x 16 bytes
-  static constexpr int OFF_SCAN = OFF_META + 4 * 8 * 16;
-  static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
-  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 4 + 2 + 2;
+  // frozen rows of one head: 128 alphas and the 384 rhos of a tile, times
+  // log2(e), for 4 tiles
+  static constexpr int OFF_PAT = OFF_META + 4 * 8 * 16;
+  // row maxima [2 tiles][2 row tiles][2 halves][128]; between the tiles of a
+  // segment the same place carries Q's factors and the sums
+  static constexpr int OFF_X = OFF_PAT + 4 * 2048;
+  static constexpr int OFF_SCAN = OFF_X + 4096;
+  static constexpr int OFF_BAR = OFF_SCAN + (kThreads / 32 + 4) * 8;
+  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 2 + 2 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 32;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
@@ -331,19 +362,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* q_full = bars;          // [2] Q staged (128 arrivals)
+  uint64_t* q_full = bars;          // [2] Q staged (256 arrivals)
   uint64_t* k_full = q_full + 2;          // [KST] codes of K have landed
   uint64_t* k_empty = k_full + L::KST;    // [KST] their products done
   uint64_t* r_full = k_empty + L::KST;    // [RST] codes of V have landed
   uint64_t* r_empty = r_full + L::RST;    // [RST] converted (128 arrivals)
   uint64_t* v_full = r_empty + L::RST;    // [2] f16 V written (128)
   uint64_t* v_empty = v_full + 2;         // [2] its products done
-  uint64_t* m_full = v_empty + 2;         // [4] a tile's scales (8)
+  uint64_t* m_full = v_empty + 2;         // [4] a tile's scales and pattern (32)
   uint64_t* s_full = m_full + 4;          // [2] S of a row tile done
-  uint64_t* p_full = s_full + 2;          // [2][2] half of P written, O rescaled (128)
+  uint64_t* p_full = s_full + 2;          // [2] P written, O rescaled (256)
   // a tile's P V done: its products, and the issuing thread itself, which has
   // seen v_full: what the converting warps wrote before is then visible
-  uint64_t* o_done = p_full + 4;          // [2] (2)
+  uint64_t* o_done = p_full + 2;          // [2] (2)
   uint64_t* drained = o_done + 2;         // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -353,12 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 128);
+      mbar_init(q_full + i, 256);
       mbar_init(v_full + i, 128);
       mbar_init(v_empty + i, 2);  // both issuers
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + 2 * i, 128);
-      mbar_init(p_full + 2 * i + 1, 128);
+      mbar_init(p_full + i, 256);
       mbar_init(o_done + i, 2);
     }
     for (int i = 0; i < L::KST; ++i) {
@@ -369,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(r_full + i, 1);
       mbar_init(r_empty + i, 128);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(m_full + i, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(m_full + i, 32);
     mbar_init(drained, 1);
     mbar_init(drained + 1, 1);
     *abort_flag = 0;
@@ -377,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     p.a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -395,44 +425,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w(p);
     int tile = w.seek(sh.b, sh.in_slot);
     long long at = sh.begin;
-    if (warp < 8) {
+    if (warp < 16) {
       // ------------------------------------------------------------ softmax
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      const int g = warp >> 2, r = threadIdx.x & 127;
-      const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t s_col = trow + kS + g * 128, o_col = trow + kO + g * 128;
+      const int g = warp >> 3, hf = (warp >> 2) & 1, q4 = warp & 3, r = q4 * 32 + lane;
+      const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+      const uint32_t s_col = trow + kS + g * 128 + 64 * hf, o_col = trow + kO + g * 128;
+      constexpr int DH = D / 2;  // columns of O that this thread rescales and writes
+      const int pair_bar = kBarPair + g * 4 + q4;
+      float* xch = reinterpret_cast<float*>(smem + L::OFF_X) + g * 256 + r;  // + 512 parity + 128 half
       uint32_t n_tile = 0, n_s = 0, n_p = 0;  // tiles of the CTA; S and P of this row tile
       for (int seg = 0;; ++seg) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
         const int gk = w.gk(), kv = p.cls_kv[w.cls];
         const bool ice = w.ice();
-        const int n_rows = (int)min((long long)kRows,
-                                    (long long)w.rows.n_new * gk - (long long)w.pair * kRows);
-        if (g * 128 < n_rows) {
-          const bool live = g * 128 + r < n_rows;
-          const int rr = w.pair * kRows + g * 128 + r;
+        const UnitRows unit = unit_rows(w.rows, w.pair, gk, ice);
+        if (g * 128 < unit.n) {
+          const bool live = g * 128 + r < unit.n;
           int t = 0, idx = 0;
-          if (live) row_of(w.rows, rr, gk, ice, t, idx);
+          if (live) row_of(w.rows, unit.first + g * 128 + r, gk, ice, t, idx);
           const int h = p.order[p.cls_first[w.cls] + idx];
           const int pos = live ? w.rows.base + t : -1;
           const int lim_all = min(pos + 1, w.rows.cap);  // keys below it are seen
-          const size_t row = ((size_t)w.b * c.H + h) * c.n_q + t;
-          const bool warp_live = g * 128 + (warp & 3) * 32 < n_rows;
+          // row of Q, out and lse, counted from the slot's first
+          const int row = live ? h * c.n_q + t : -1;
+          const size_t slot0 = (size_t)w.b * c.H * c.n_q;
+          const bool warp_live = g * 128 + q4 * 32 < unit.n;
           float fac = 1.f;
           if (!ice) {
-            // rows of Q: scaled by the least 2^-e that brings the row within
-            // e4m3's range, split into hi + lo; kL lanes take a row
+            // rows of Q (16 for each warp): scaled by the least 2^-e that brings
+            // the row within e4m3's range, split into hi + lo; kL lanes take a row
             constexpr int kL = D / 8, kR = 32 / kL;
-            const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
-            const uint16_t* qb = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
-#pragma unroll 4
-            for (int i = 0; i < 32; i += kR) {
-              const int rl = i + lane / kL, u = lane % kL;  // row of the warp, 8 components
-              const int src = __shfl_sync(~0u, mine, rl);
-              const uint4 q = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                             qb + (size_t)(unsigned)src * D) + u)
-                                       : make_uint4(0, 0, 0, 0);
-              const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+            const int u = lane % kL;  // 8 components of a row
+            uint4 q[16 / kR];
+#pragma unroll
+            for (int i = 0; i < 16; i += kR) {
+              const int src = __shfl_sync(~0u, row, 16 * hf + i + lane / kL);
+              q[i / kR] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                               p.a.Q + (slot0 + (unsigned)src) * D) + u)
+                                   : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += kR) {
+              const int rl = q4 * 32 + 16 * hf + i + lane / kL;  // row of the tile
+              const uint32_t x[4] = {q[i / kR].x, q[i / kR].y, q[i / kR].z, q[i / kR].w};
               float y[8], amax = 0.f;
 #pragma unroll
               for (int v = 0; v < 8; ++v) {
@@ -463,20 +499,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
                 lo[v] = e4m3x2(z[0] - fa.x, z[1] - fa.y) | e4m3x2(z[2] - fb.x, z[3] - fb.y) << 16;
               }
-              const uint32_t at8 =
-                  sQ + g * L::TILE + code_at<D>((warp & 3) * 32 + rl, u >> 1) + (u & 1) * 8;
+              const uint32_t at8 = sQ + g * L::TILE + code_at<D>(rl, u >> 1) + (u & 1) * 8;
               asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8), "r"(hi[0]), "r"(hi[1])
                            : "memory");
               asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8 + L::CODES), "r"(lo[0]),
                            "r"(lo[1])
                            : "memory");
-              const int back = __shfl_sync(~0u, e, (lane - i) * kL & 31);
-              if (lane >= i && lane < i + kR) fac = pow2f(back) * (rsqrtf((float)D) * kLog2e);
+              if (u == 0) xch[rl - r] = pow2f(e) * (rsqrtf((float)D) * kLog2e);
             }
             fence_proxy_async_smem();
+            named_bar_sync(pair_bar, 64);
+            fac = xch[0];
+            named_bar_sync(pair_bar, 64);  // read before the maxima overwrite it
             mbar_arrive(q_full + g);
           }
           float m = -CUDART_INF_F, l = 0.f;
+          // The two row tiles take turns at the exponentials: each then has the
+          // special-function units to itself, and one's products run under the
+          // other's softmax.
+          const bool turns = unit.n > 128;
+          const bool windowed = ice && one_head(w.rows, unit);
+          if (turns && g == 1) named_bar_arrive(kBarTurn, 512);
           for (int i = tile; i < tile_end; ++i) {
             const uint32_t nt = n_tile + (i - tile);
             mbar_wait(m_full + (nt & 3), (nt >> 2) & 1, wc, kSiteMeta);
@@ -487,57 +530,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n_p > 0) mbar_wait(o_done + g, (n_p - 1) & 1, wc, kSiteO);
             __syncwarp();
             tc_fence_after();
+            const bool pass_on = turns && (g == 0 || i + 1 < tile_end);
             if (warp_live) {
-              const uint32_t meta = sM + (nt & 3) * 128;
-              const int j0 = i * kTile;
+              const uint32_t meta = sM + (nt & 3) * 128 + 64 * hf;
+              const int j0 = i * kTile + 64 * hf;
               const int lim = lim_all - j0;  // columns below it are seen
-              const bool edge = __any_sync(~0u, lim < kTile);
-              uint32_t s[128];
+              const bool edge = __any_sync(~0u, lim < 64);
+              uint32_t s[64];
               if (!ice) {
                 uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
                 uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
-                uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 64);
-                uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 96);
                 tmem_ld_x32(s_col, s0);
                 tmem_ld_x32(s_col + 32, s1);
-                tmem_ld_x32(s_col + 64, s2);
-                tmem_ld_x32(s_col + 96, s3);
                 tmem_wait_ld(s0);
                 tmem_wait_ld(s1);
-                tmem_wait_ld(s2);
-                tmem_wait_ld(s3);
+              } else if (windowed) {
+                // distance of (row, column k): entry (row of the unit) - k + 127
+                const float* pat =
+                    reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
+                const float* win = pat + 128 + g * 128 + r + 127 - 128 * hf;
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                  const float4 x = *reinterpret_cast<const float4*>(pat + k);
+                  s[k] = __float_as_uint(x.x + win[-k]);
+                  s[k + 1] = __float_as_uint(x.y + win[-k - 1]);
+                  s[k + 2] = __float_as_uint(x.z + win[-k - 2]);
+                  s[k + 3] = __float_as_uint(x.w + win[-k - 3]);
+                }
               } else {
                 const float* al = p.a.alpha + (size_t)h * p.a.T_pat + j0;
                 const int d0 = pos - j0;  // distance of column 0
                 const float* rh = p.a.rho + (size_t)h * p.a.T_pat + d0;
-                // inside the vectors for every column of the warp's rows?
-                const bool in = j0 + kTile <= p.a.T_pat && d0 < p.a.T_pat && d0 >= kTile - 1;
-                if (__all_sync(~0u, in && (reinterpret_cast<uintptr_t>(al) & 15) == 0)) {
 #pragma unroll
-                  for (int k = 0; k < kTile; k += 4) {
-                    const float4 x = __ldg(reinterpret_cast<const float4*>(al + k));
-                    s[k] = __float_as_uint((x.x + __ldg(rh - k)) * kLog2e);
-                    s[k + 1] = __float_as_uint((x.y + __ldg(rh - k - 1)) * kLog2e);
-                    s[k + 2] = __float_as_uint((x.z + __ldg(rh - k - 2)) * kLog2e);
-                    s[k + 3] = __float_as_uint((x.w + __ldg(rh - k - 3)) * kLog2e);
-                  }
-                } else {
-#pragma unroll
-                  for (int k = 0; k < kTile; ++k) {
-                    const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
-                    s[k] = __float_as_uint(
-                        ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
-                  }
+                for (int k = 0; k < 64; ++k) {
+                  const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
+                  s[k] = __float_as_uint(
+                      ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
                 }
               }
               if (edge) {
 #pragma unroll
-                for (int k = 0; k < kTile; ++k)
+                for (int k = 0; k < 64; ++k)
                   if (k >= lim) s[k] = 0xff800000u;
               }
               float top = -CUDART_INF_F;
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {  // groups of 16 keys: one page, one scale
+              for (int q = 0; q < 4; ++q) {  // groups of 16 keys: one page, one scale
                 float x = fmax3(__uint_as_float(s[16 * q]), __uint_as_float(s[16 * q + 1]),
                                 __uint_as_float(s[16 * q + 2]));
 #pragma unroll
@@ -549,6 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_unpack(mt, ks, lv);
                 top = fmaxf(top, fmaf(x, ice ? 1.f : fac * ks, lv));
               }
+              float* mine = xch + 512 * (nt & 1);
+              mine[128 * hf] = top;
+              named_bar_sync(pair_bar, 64);
+              top = fmaxf(top, mine[128 * (hf ^ 1)]);
               // the maximum moves only when it would grow by more than 2^8:
               // weights up to 2^8 fit f16 as well
               const bool need = top > m + 8.f;
@@ -558,20 +600,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l *= corr;
                 if (i > tile) {
 #pragma unroll 1
-                  for (int q = 0; q < D; q += 16) {
+                  for (int q = 0; q < DH; q += 16) {
                     uint32_t o[16];
-                    tmem_ld_x16(o_col + q, o);
+                    tmem_ld_x16(o_col + hf * DH + q, o);
                     tmem_wait_ld(o);
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                       o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                    tmem_st_x16(o_col + q, o);
+                    tmem_st_x16(o_col + hf * DH + q, o);
                   }
                 }
               }
               const float base = m == -CUDART_INF_F ? 0.f : m;
+              if (turns) named_bar_sync(kBarTurn + g, 512);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
+              for (int q = 0; q < 4; ++q) {
                 const float4 mt = lds_f32x4(meta + 16 * q);
                 const float a = ice ? 1.f : fac * mt.x, b = mt.y - base;
                 const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
@@ -593,19 +636,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_unpack(sum, x, y);
                 l = fmaf(x + y, mt.z, l);
                 tmem_st_x8(s_col + 8 * q, pk);
-                if (q == 3) {  // the first half's product may start
-                  tmem_wait_st();
-                  tc_fence_before();
-                  mbar_arrive(p_full + 2 * g);
-                }
               }
+              if (pass_on) named_bar_arrive(kBarTurn + 1 - g, 512);
               tmem_wait_st();
-            } else {
-              tc_fence_before();
-              mbar_arrive(p_full + 2 * g);
+            } else if (turns) {
+              named_bar_sync(kBarTurn + g, 512);
+              if (pass_on) named_bar_arrive(kBarTurn + 1 - g, 512);
             }
             tc_fence_before();
-            mbar_arrive(p_full + 2 * g + 1);
+            mbar_arrive(p_full + g);
             ++n_p;
           }
           // ---- results
@@ -613,10 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_fence_after();
           const bool whole = tile == 0 && tile_end == w.ut;
+          named_bar_sync(pair_bar, 64);  // the last maxima are read
+          xch[128 * hf] = l;
+          named_bar_sync(pair_bar, 64);
+          l = xch[0] + xch[128];
           if (warp_live && !__any_sync(~0u, *abort_flag)) {
-            uint32_t nan[D / 32];
+            uint32_t nan[(DH + 31) / 32];
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) nan[q] = 0;
+            for (int q = 0; q < (DH + 31) / 32; ++q) nan[q] = 0;
             if (nan_seg[seg & 3] == seg + 1) {
               // V holds NaN at a key of an edge tile: rows that see it take it
               const int lo = w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo;
@@ -624,12 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = max(first, tile * kTile); j < min(lim_all, tile_end * kTile); ++j) {
                 const int page = page_at(c, w.b, j >> c.page_shift);
                 if (page < 0) continue;
-                const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                    c.layer + (size_t)page * c.page_stride + c.off_v +
-                    (((size_t)kv << c.page_shift) + (j & ((1 << c.page_shift) - 1))) * D);
-                for (int q = 0; q < D / 4; ++q)
-                  for (int k = 0; k < 4; ++k)
-                    if ((v[q] >> (8 * k) & 0x7f) == 0x7f) nan[q / 8] |= 1u << (q % 8 * 4 + k);
+                const uint8_t* v = c.layer + (size_t)page * c.page_stride + c.off_v +
+                                   (((size_t)kv << c.page_shift) +
+                                    (j & ((1 << c.page_shift) - 1))) * D + hf * DH;
+#pragma unroll
+                for (int q = 0; q < DH; ++q)
+                  if ((v[q] & 0x7f) == 0x7f) nan[q / 32] |= 1u << (q % 32);
               }
             }
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -639,50 +682,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             // results go through the row tile's Q buffer (its products are done)
             const uint32_t stage = sQ + g * L::TILE;
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld_x32(o_col + 32 * q, o);
+            for (int q = 0; q < DH / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld_x16(o_col + hf * DH + 16 * q, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
+              for (int k = 0; k < 16; ++k) {
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
-                if (nan[q] >> k & 1) o[k] = 0x7fc00000u;
+                if (nan[q / 2] >> (16 * (q & 1) + k) & 1) o[k] = 0x7fc00000u;
               }
               if (whole) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                  st_shared_v4(stage + unit_at<D>(r, 4 * q + k / 8),
+                for (int k = 0; k < 16; k += 8)
+                  st_shared_v4(stage + unit_at<D>(r, (hf * DH + 16 * q + k) / 8),
                                pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
                                pack_bf16x2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
                                pack_bf16x2(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
                                pack_bf16x2(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
               } else if (live) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                  *reinterpret_cast<uint4*>(p.a.acc + part * D +
-                                            ((size_t)(8 * q + k / 4) * kRows + pr) * 4) =
+                for (int k = 0; k < 16; k += 4)
+                  *reinterpret_cast<uint4*>(
+                      p.a.acc + part * D +
+                      ((size_t)((hf * DH + 16 * q + k) / 4) * kRows + pr) * 4) =
                       make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
               }
             }
-            if (whole) {
-              __syncwarp();
-              constexpr int kL = D / 8, kR = 32 / kL;
-              const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
-              uint16_t* ob = p.a.out + (size_t)w.b * c.H * c.n_q * D;
-#pragma unroll 4
-              for (int i = 0; i < 32; i += kR) {
-                const int rl = i + lane / kL, u = lane % kL;
-                const int dst = __shfl_sync(~0u, mine, rl);
-                const float4 x = lds_f32x4(stage + unit_at<D>((warp & 3) * 32 + rl, u));
-                if (dst >= 0)
-                  *(reinterpret_cast<float4*>(ob + (size_t)(unsigned)dst * D) + u) = x;
-              }
-              __syncwarp();
+            if (live && hf == 0) {
+              if (whole && p.a.lse) p.a.lse[slot0 + (unsigned)row] = (m + log2f(l)) * kLn2;
+              if (!whole) *reinterpret_cast<float2*>(p.a.ml + (part + pr) * 2) = make_float2(m, l);
             }
-            if (live && whole && p.a.lse) p.a.lse[row] = (m + log2f(l)) * kLn2;
-            if (live && !whole)
-              *reinterpret_cast<float2*>(p.a.ml + (part + pr) * 2) = make_float2(m, l);
           }
+          named_bar_sync(pair_bar, 64);
+          if (whole && warp_live && !__any_sync(~0u, *abort_flag)) {
+            constexpr int kL = D / 8, kR = 32 / kL;
+            const int u = lane % kL;
+#pragma unroll
+            for (int i = 0; i < 16; i += kR) {
+              const int rl = 16 * hf + i + lane / kL;
+              const int dst = __shfl_sync(~0u, row, rl);
+              const float4 x = lds_f32x4(sQ + g * L::TILE + unit_at<D>(q4 * 32 + rl, u));
+              if (dst >= 0)
+                *(reinterpret_cast<float4*>(p.a.out + (slot0 + (unsigned)dst) * D) + u) = x;
+            }
+          }
+          named_bar_sync(pair_bar, 64);  // Q's buffer and the exchange are free again
         }
         if (threadIdx.x == 0 && tile == 0 && tile_end < w.ut) {
           // the unit begins here and ends in CTA `last`
@@ -696,10 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile = 0;
         w.next();
       }
-    } else if (warp < 12) {
+    } else if (warp < 20) {
       // ------------------------------------------------------------ V: codes -> f16
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-      const int tid = threadIdx.x - 256;
+      const int tid = threadIdx.x - 512;
       constexpr int kCh = D / 16;              // 16-byte chunks of a row of codes
       constexpr int kN = kTile * kCh / 128;    // chunks of a thread in a tile
       constexpr int kStep = 128 / kCh;         // rows between a thread's chunks
@@ -758,8 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------ products
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-      if ((warp == 12 || warp == 14) && lane == 0) {
-        const int g = (warp - 12) >> 1;
+      if ((warp == 20 || warp == 22) && lane == 0) {
+        const int g = (warp - 20) >> 1;
         constexpr uint32_t id_s = idesc_e4m3(128, kTile);
         constexpr uint32_t id_o = idesc_f16(128, D, false, true);
         const uint32_t s_col = tmem + kS + g * 128, o_col = tmem + kO + g * 128;
@@ -768,13 +812,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (;;) {
           const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
           const bool ice = w.ice();
-          const bool mine =
-              (long long)w.rows.n_new * w.gk() - (long long)w.pair * kRows > g * 128;
-          auto issue_s = [&]() {  // the next tile's S; the stage is free when it is done
-            const uint32_t st = kc % L::KST;
-            mbar_poll(k_full + st, (kc / L::KST) & 1, wc, kSiteK);
-            tc_fence_after();
+          const bool mine = unit_rows(w.rows, w.pair, w.gk(), ice).n > g * 128;
+          // K of the next S; waited for ahead of the softmax, so that the wait
+          // is not part of the row tile's chain
+          auto wait_k = [&]() { mbar_poll(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK); };
+          auto issue_s = [&]() {
+            const uint32_t st = kc++ % L::KST;
             if (mine) {
+              tc_fence_after();
               const uint64_t kt = sdesc(sK + st * L::CODES, 16, 8 * D, swizzle_layout_code(D));
               issue_codes<D / 32, (L::CODES >> 4)>(s_col, qt, kt, id_s);
               mma_commit(k_empty + st);
@@ -782,39 +827,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               mbar_arrive(k_empty + st);
             }
-            ++kc;
           };
           if (!ice) {
+            wait_k();
             if (mine) mbar_poll(q_full + g, n_q++ & 1, wc, kSiteQ);
             issue_s();
           }
           for (int i = tile; i < tile_end; ++i) {
+            const bool more = !ice && i + 1 < tile_end;
             const uint32_t st = vc & 1;
             mbar_poll(v_full + st, (vc >> 1) & 1, wc, kSiteV);
             ++vc;
+            if (more) wait_k();
             if (mine) {
               const uint64_t vt = G::mnmajor_desc(sV + st * L::TILE, 0);
               constexpr int kVStep = 16 * G::SWZ >> 4;
-#pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
-                mbar_poll(p_full + 2 * g + half, n_p & 1, wc, kSiteP);
-                tc_fence_after();
-                issue_pv<kVStep>(o_col, s_col + 32 * half, vt + 4 * kVStep * half, id_o,
-                                 i > tile || half);
-              }
-              mma_commit(v_empty + st);
+              mbar_poll(p_full + g, n_p & 1, wc, kSiteP);
+              tc_fence_after();
+              issue_pv<kVStep>(o_col, s_col, vt, id_o, i > tile);
+              issue_pv<kVStep>(o_col, s_col + 64, vt + 4 * kVStep, id_o, 1);
               mma_commit(o_done + g);
               mbar_arrive(o_done + g);
+              mma_commit(v_empty + st);
               // S takes the columns of the P that these products read
-              if (!ice && i + 1 < tile_end) {
+              if (more) {
                 mbar_poll(o_done + g, n_p & 1, wc, kSiteO);
-                tc_fence_after();
+                issue_s();
               }
               ++n_p;
             } else {
               mbar_arrive(v_empty + st);
+              if (more) issue_s();
             }
-            if (!ice && i + 1 < tile_end) issue_s();
           }
           at += tile_end - tile;
           if (at >= sh.end) break;
@@ -824,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every product has completed before TMEM is freed
         mma_commit(drained + g);
         mbar_drain(drained + g, 0);
-      } else if (warp == 13) {
+      } else if (warp == 21) {
         // ---------------------------------------------------------- codes and scales
         uint32_t kc = 0, vc = 0;
         const int per = c.page_shift > 4 ? 1 << (c.page_shift - 4) : 1;  // groups of a page
@@ -844,8 +888,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 kh >= 0 ? __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + kh) : 1.f,
                 __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + kv));
           };
+          // frozen rows of one head: the lane's 4 alphas and 12 rhos of a tile
+          const UnitRows unit = unit_rows(w.rows, w.pair, w.gk(), w.ice());
+          const bool windowed = w.ice() && one_head(w.rows, unit);
+          const float *al = nullptr, *rh = nullptr;
+          int d_lo = 0;  // distance of the window's first entry, plus the tile's first key
+          if (windowed) {
+            int t0, idx;
+            row_of(w.rows, unit.first, w.gk(), true, t0, idx);
+            const size_t h = (size_t)p.order[p.cls_first[w.cls] + idx] * p.a.T_pat;
+            al = p.a.alpha + h;
+            rh = p.a.rho + h;
+            d_lo = w.rows.base + t0 - 127;
+          }
+          float pat[16];
+          auto fetch_pattern = [&](int tl) {
+            if (!windowed || tl >= tile_end) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = tl * kTile + lane + 32 * k;
+              pat[k] = j < p.a.T_pat ? __ldg(al + j) * kLog2e : -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int k = 0; k < 12; ++k) {
+              const int d = d_lo - tl * kTile + lane + 32 * k;
+              pat[4 + k] = d >= 0 && d < p.a.T_pat ? __ldg(rh + d) * kLog2e : -CUDART_INF_F;
+            }
+          };
           int page = look_up(tile), page1 = look_up(tile + 1);
           float2 sc = scales(page);
+          fetch_pattern(tile);
           for (int i = tile; i < tile_end; ++i) {
             const int page2 = look_up(i + 2);
             const float2 sc1 = scales(page1);
@@ -869,8 +941,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<float4*>(smem + L::OFF_META + (vc & 3) * 128 + lane * 16) =
                   make_float4(sc.x, there ? __log2f(sc.y) : -CUDART_INF_F,
                               there ? __fdividef(1.f, sc.y) : 1.f, 0.f);
-              mbar_arrive(m_full + (vc & 3));
             }
+            if (windowed) {
+              float* to = reinterpret_cast<float*>(smem + L::OFF_PAT + (vc & 3) * 2048) + lane;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) to[32 * k] = pat[k];
+            }
+            mbar_arrive(m_full + (vc & 3));
+            fetch_pattern(i + 1);
             if (lane == 0) mbar_arrive_expect_tx(r_full + st, L::CODES);
             for (int g = 0; g < 8; g += per) {
               const int pg = __shfl_sync(~0u, page, g);
@@ -899,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -924,11 +1002,10 @@ __global__ void __launch_bounds__(256)
       gk = p.group_width[g];
       ice = p.group_static[g];
     }
-  const int n_rows =
-      (int)min((long long)kRows, (long long)rows.n_new * gk - (long long)pair * kRows);
+  const UnitRows unit = unit_rows(rows, pair, gk, ice);
   for (int i = blockIdx.y * 256 + threadIdx.x; i < kRows * (D / 4); i += gridDim.y * 256) {
     const int r = i % kRows, d = i / kRows * 4;
-    if (r >= n_rows) continue;
+    if (r >= unit.n) continue;
     auto ml = [&](int part) {
       return *reinterpret_cast<const float2*>(p.a.ml + ((size_t)part * kRows + r) * 2);
     };
@@ -949,7 +1026,7 @@ __global__ void __launch_bounds__(256)
       o.w = fmaf(f, v.w, o.w);
     }
     int t, idx;
-    row_of(rows, pair * kRows + r, gk, ice, t, idx);
+    row_of(rows, unit.first + r, gk, ice, t, idx);
     const int h = p.order[p.cls_first[cls] + idx];
     const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

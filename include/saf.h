@@ -310,7 +310,7 @@ SAF_API saf_status saf_calib_destroy(void* handle);
  * host; all can be captured in a CUDA graph. */
 typedef struct saf_cache_dims {
   int n_seqs;         /* slots: rows of page_table, 0..32768               */
-  int max_pages;      /* columns of page_table; max_pages * page_size < 2^31 */
+  int max_pages;      /* columns; max_pages * page_size <= 2^31 - 1024    */
   int n_pages;        /* pages of the pool, >= 1                           */
   int page_size;      /* tokens of a page: 16, 32, 64 or 128               */
   int H;              /* query heads, 1..256                               */

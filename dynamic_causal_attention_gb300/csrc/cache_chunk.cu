@@ -13,14 +13,13 @@
 // units are cut into equal shares, one for each CTA (one per SM), as in
 // cache_attn.cu.
 //
-// Warp roles (768 threads; registers move to the softmax):
-//   warps 0-15       the softmax: row tile g = warp / 8, two threads to a row,
-//                    one for each half of the 128 key columns.  They also stage
-//                    Q and write the results.
-//   warps 16-19      turn V's e4m3 codes into f16 tiles in shared memory.
-//   warps 20, 22     issue the products of row tile 0 and 1 (one lane each); 20
+// Warp roles (512 threads; registers move to the softmax):
+//   warps 0-3, 4-7   the softmax of row tile 0 and 1: one row per thread.  They
+//                    also stage Q and write the results.
+//   warps 8-11       turn V's e4m3 codes into f16 tiles in shared memory.
+//   warps 12, 14     issue the products of row tile 0 and 1 (one lane each); 12
 //                    allocates TMEM.
-//   warp 21          looks up pages, fetches K and V codes by TMA (a page that is
+//   warp 13          looks up pages, fetches K and V codes by TMA (a page that is
 //                    missing reads as zeros) and writes the scales of each tile.
 //
 // K needs no conversion: Q K^T runs on e4m3 operands at twice f16's rate, with
@@ -33,7 +32,7 @@
 // 128 x d_h codes.
 //
 // TMEM: S of the two row tiles (128 columns each), then their O.  P, as packed
-// f16, overwrites half of the S columns that its thread has read, so the next S of a row tile
+// f16, overwrites the first half of its own S, so the next S of a row tile
 // waits for the product that reads P; the other row tile's products and
 // softmax run meanwhile.  A frozen row writes its logits into S itself.
 #include <cuda.h>
@@ -51,9 +50,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 256;     // query rows of a unit
 constexpr int kTile = 128;     // keys of a tile
-constexpr int kThreads = 768;
-// registers of a thread after the split: 4 * 96 + 48 + 48 = 6 * 80
-constexpr int kRegsSoftmax = 96, kRegsConvert = 48, kRegsIssue = 48;
+constexpr int kThreads = 512;
+// registers of a thread after the split: 2 * 176 + 80 + 80 = 4 * 128
+constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsIssue = 80;
 constexpr long long kMinTiles = 1;
 
 enum : int {
@@ -62,7 +61,6 @@ enum : int {
 };
 
 constexpr int kBarTurn = 1;  // named barriers 1 and 2: row tile 0's and 1's turn
-constexpr int kBarPair = 3;  // 3-10: the two warps that share 32 rows
 
 // Instruction descriptor with f16 operands and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -322,12 +320,9 @@ struct Smem {
   // frozen rows of one head: 128 alphas and the 384 rhos of a tile, times
   // log2(e), for 4 tiles
   static constexpr int OFF_PAT = OFF_META + 4 * 8 * 16;
-  // row maxima [2 tiles][2 row tiles][2 halves][128]; between the tiles of a
-  // segment the same place carries Q's factors and the sums
-  static constexpr int OFF_X = OFF_PAT + 4 * 2048;
-  static constexpr int OFF_SCAN = OFF_X + 4096;
+  static constexpr int OFF_SCAN = OFF_PAT + 4 * 2048;
   static constexpr int OFF_BAR = OFF_SCAN + (kThreads / 32 + 4) * 8;
-  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 2 + 2 + 2;
+  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 4 + 2 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 32;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
@@ -362,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* q_full = bars;          // [2] Q staged (256 arrivals)
+  uint64_t* q_full = bars;          // [2] Q staged (128 arrivals)
   uint64_t* k_full = q_full + 2;          // [KST] codes of K have landed
   uint64_t* k_empty = k_full + L::KST;    // [KST] their products done
   uint64_t* r_full = k_empty + L::KST;    // [RST] codes of V have landed
@@ -371,10 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_empty = v_full + 2;         // [2] its products done
   uint64_t* m_full = v_empty + 2;         // [4] a tile's scales and pattern (32)
   uint64_t* s_full = m_full + 4;          // [2] S of a row tile done
-  uint64_t* p_full = s_full + 2;          // [2] P written, O rescaled (256)
+  uint64_t* p_full = s_full + 2;          // [2][2] half of P written, O rescaled (128)
   // a tile's P V done: its products, and the issuing thread itself, which has
   // seen v_full: what the converting warps wrote before is then visible
-  uint64_t* o_done = p_full + 2;          // [2] (2)
+  uint64_t* o_done = p_full + 4;          // [2] (2)
   uint64_t* drained = o_done + 2;         // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -384,11 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 256);
+      mbar_init(q_full + i, 128);
       mbar_init(v_full + i, 128);
       mbar_init(v_empty + i, 2);  // both issuers
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 256);
+      mbar_init(p_full + 2 * i, 128);
+      mbar_init(p_full + 2 * i + 1, 128);
       mbar_init(o_done + i, 2);
     }
     for (int i = 0; i < L::KST; ++i) {
@@ -407,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     p.a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
-  if (warp == 20) {
+  if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -425,15 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w(p);
     int tile = w.seek(sh.b, sh.in_slot);
     long long at = sh.begin;
-    if (warp < 16) {
+    if (warp < 8) {
       // ------------------------------------------------------------ softmax
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      const int g = warp >> 3, hf = (warp >> 2) & 1, q4 = warp & 3, r = q4 * 32 + lane;
-      const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-      const uint32_t s_col = trow + kS + g * 128 + 64 * hf, o_col = trow + kO + g * 128;
-      constexpr int DH = D / 2;  // columns of O that this thread rescales and writes
-      const int pair_bar = kBarPair + g * 4 + q4;
-      float* xch = reinterpret_cast<float*>(smem + L::OFF_X) + g * 256 + r;  // + 512 parity + 128 half
+      const int g = warp >> 2, r = threadIdx.x & 127;
+      const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t s_col = trow + kS + g * 128, o_col = trow + kO + g * 128;
       uint32_t n_tile = 0, n_s = 0, n_p = 0;  // tiles of the CTA; S and P of this row tile
       for (int seg = 0;; ++seg) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
@@ -447,27 +440,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int h = p.order[p.cls_first[w.cls] + idx];
           const int pos = live ? w.rows.base + t : -1;
           const int lim_all = min(pos + 1, w.rows.cap);  // keys below it are seen
-          // row of Q, out and lse, counted from the slot's first
-          const int row = live ? h * c.n_q + t : -1;
-          const size_t slot0 = (size_t)w.b * c.H * c.n_q;
-          const bool warp_live = g * 128 + q4 * 32 < unit.n;
+          const size_t row = ((size_t)w.b * c.H + h) * c.n_q + t;
+          const bool warp_live = g * 128 + (warp & 3) * 32 < unit.n;
           float fac = 1.f;
           if (!ice) {
-            // rows of Q (16 for each warp): scaled by the least 2^-e that brings
-            // the row within e4m3's range, split into hi + lo; kL lanes take a row
+            // rows of Q: scaled by the least 2^-e that brings the row within
+            // e4m3's range, split into hi + lo; kL lanes take a row
             constexpr int kL = D / 8, kR = 32 / kL;
+            const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
+            const uint16_t* qb = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
             const int u = lane % kL;  // 8 components of a row
-            uint4 q[16 / kR];
+            uint4 q[kL];
 #pragma unroll
-            for (int i = 0; i < 16; i += kR) {
-              const int src = __shfl_sync(~0u, row, 16 * hf + i + lane / kL);
+            for (int i = 0; i < 32; i += kR) {
+              const int src = __shfl_sync(~0u, mine, i + lane / kL);
               q[i / kR] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                               p.a.Q + (slot0 + (unsigned)src) * D) + u)
+                                               qb + (size_t)(unsigned)src * D) + u)
                                    : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int i = 0; i < 16; i += kR) {
-              const int rl = q4 * 32 + 16 * hf + i + lane / kL;  // row of the tile
+            for (int i = 0; i < 32; i += kR) {
+              const int rl = i + lane / kL;  // row of the warp
               const uint32_t x[4] = {q[i / kR].x, q[i / kR].y, q[i / kR].z, q[i / kR].w};
               float y[8], amax = 0.f;
 #pragma unroll
@@ -499,18 +492,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
                 lo[v] = e4m3x2(z[0] - fa.x, z[1] - fa.y) | e4m3x2(z[2] - fb.x, z[3] - fb.y) << 16;
               }
-              const uint32_t at8 = sQ + g * L::TILE + code_at<D>(rl, u >> 1) + (u & 1) * 8;
+              const uint32_t at8 =
+                  sQ + g * L::TILE + code_at<D>((warp & 3) * 32 + rl, u >> 1) + (u & 1) * 8;
               asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8), "r"(hi[0]), "r"(hi[1])
                            : "memory");
               asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8 + L::CODES), "r"(lo[0]),
                            "r"(lo[1])
                            : "memory");
-              if (u == 0) xch[rl - r] = pow2f(e) * (rsqrtf((float)D) * kLog2e);
+              const int back = __shfl_sync(~0u, e, (lane - i) * kL & 31);
+              if (lane >= i && lane < i + kR) fac = pow2f(back) * (rsqrtf((float)D) * kLog2e);
             }
             fence_proxy_async_smem();
-            named_bar_sync(pair_bar, 64);
-            fac = xch[0];
-            named_bar_sync(pair_bar, 64);  // read before the maxima overwrite it
             mbar_arrive(q_full + g);
           }
           float m = -CUDART_INF_F, l = 0.f;
@@ -519,38 +511,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           // other's softmax.
           const bool turns = unit.n > 128;
           const bool windowed = ice && one_head(w.rows, unit);
-          if (turns && g == 1) named_bar_arrive(kBarTurn, 512);
+          if (turns && g == 1) named_bar_arrive(kBarTurn, 256);
           for (int i = tile; i < tile_end; ++i) {
             const uint32_t nt = n_tile + (i - tile);
             mbar_wait(m_full + (nt & 3), (nt >> 2) & 1, wc, kSiteMeta);
+            // the P V of the tile before is done as well: this S was issued after it
             if (!ice) {
               mbar_wait(s_full + g, n_s & 1, wc, kSiteS);
               ++n_s;
+            } else if (n_p > 0) {
+              mbar_wait(o_done + g, (n_p - 1) & 1, wc, kSiteO);
             }
-            if (n_p > 0) mbar_wait(o_done + g, (n_p - 1) & 1, wc, kSiteO);
             __syncwarp();
             tc_fence_after();
-            const bool pass_on = turns && (g == 0 || i + 1 < tile_end);
             if (warp_live) {
-              const uint32_t meta = sM + (nt & 3) * 128 + 64 * hf;
-              const int j0 = i * kTile + 64 * hf;
+              const uint32_t meta = sM + (nt & 3) * 128;
+              const int j0 = i * kTile;
               const int lim = lim_all - j0;  // columns below it are seen
-              const bool edge = __any_sync(~0u, lim < 64);
-              uint32_t s[64];
+              const bool edge = __any_sync(~0u, lim < kTile);
+              uint32_t s[128];
               if (!ice) {
                 uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
                 uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
+                uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 64);
+                uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 96);
                 tmem_ld_x32(s_col, s0);
                 tmem_ld_x32(s_col + 32, s1);
+                tmem_ld_x32(s_col + 64, s2);
+                tmem_ld_x32(s_col + 96, s3);
                 tmem_wait_ld(s0);
                 tmem_wait_ld(s1);
+                tmem_wait_ld(s2);
+                tmem_wait_ld(s3);
               } else if (windowed) {
                 // distance of (row, column k): entry (row of the unit) - k + 127
                 const float* pat =
-                    reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
-                const float* win = pat + 128 + g * 128 + r + 127 - 128 * hf;
+                    reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048);
+                const float* win = pat + 128 + g * 128 + r + 127;
 #pragma unroll
-                for (int k = 0; k < 64; k += 4) {
+                for (int k = 0; k < kTile; k += 4) {
                   const float4 x = *reinterpret_cast<const float4*>(pat + k);
                   s[k] = __float_as_uint(x.x + win[-k]);
                   s[k + 1] = __float_as_uint(x.y + win[-k - 1]);
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int d0 = pos - j0;  // distance of column 0
                 const float* rh = p.a.rho + (size_t)h * p.a.T_pat + d0;
 #pragma unroll
-                for (int k = 0; k < 64; ++k) {
+                for (int k = 0; k < kTile; ++k) {
                   const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
                   s[k] = __float_as_uint(
                       ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
@@ -570,12 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (edge) {
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
+                for (int k = 0; k < kTile; ++k)
                   if (k >= lim) s[k] = 0xff800000u;
               }
               float top = -CUDART_INF_F;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {  // groups of 16 keys: one page, one scale
+              for (int q = 0; q < 8; ++q) {  // groups of 16 keys: one page, one scale
                 float x = fmax3(__uint_as_float(s[16 * q]), __uint_as_float(s[16 * q + 1]),
                                 __uint_as_float(s[16 * q + 2]));
 #pragma unroll
@@ -587,10 +586,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_unpack(mt, ks, lv);
                 top = fmaxf(top, fmaf(x, ice ? 1.f : fac * ks, lv));
               }
-              float* mine = xch + 512 * (nt & 1);
-              mine[128 * hf] = top;
-              named_bar_sync(pair_bar, 64);
-              top = fmaxf(top, mine[128 * (hf ^ 1)]);
               // the maximum moves only when it would grow by more than 2^8:
               // weights up to 2^8 fit f16 as well
               const bool need = top > m + 8.f;
@@ -600,21 +595,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l *= corr;
                 if (i > tile) {
 #pragma unroll 1
-                  for (int q = 0; q < DH; q += 16) {
+                  for (int q = 0; q < D; q += 16) {
                     uint32_t o[16];
-                    tmem_ld_x16(o_col + hf * DH + q, o);
+                    tmem_ld_x16(o_col + q, o);
                     tmem_wait_ld(o);
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                       o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                    tmem_st_x16(o_col + hf * DH + q, o);
+                    tmem_st_x16(o_col + q, o);
                   }
                 }
               }
               const float base = m == -CUDART_INF_F ? 0.f : m;
-              if (turns) named_bar_sync(kBarTurn + g, 512);
+              if (turns) named_bar_sync(kBarTurn + g, 256);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 8; ++q) {
                 const float4 mt = lds_f32x4(meta + 16 * q);
                 const float a = ice ? 1.f : fac * mt.x, b = mt.y - base;
                 const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
@@ -636,15 +631,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_unpack(sum, x, y);
                 l = fmaf(x + y, mt.z, l);
                 tmem_st_x8(s_col + 8 * q, pk);
+                if (q == 3) {  // the first half's product may start
+                  tmem_wait_st();
+                  tc_fence_before();
+                  mbar_arrive(p_full + 2 * g);
+                }
               }
-              if (pass_on) named_bar_arrive(kBarTurn + 1 - g, 512);
+              if (turns && (g == 0 || i + 1 < tile_end)) named_bar_arrive(kBarTurn + 1 - g, 256);
               tmem_wait_st();
-            } else if (turns) {
-              named_bar_sync(kBarTurn + g, 512);
-              if (pass_on) named_bar_arrive(kBarTurn + 1 - g, 512);
+            } else {
+              if (turns) {
+                named_bar_sync(kBarTurn + g, 256);
+                if (g == 0 || i + 1 < tile_end) named_bar_arrive(kBarTurn + 1 - g, 256);
+              }
+              tc_fence_before();
+              mbar_arrive(p_full + 2 * g);
             }
             tc_fence_before();
-            mbar_arrive(p_full + g);
+            mbar_arrive(p_full + 2 * g + 1);
             ++n_p;
           }
           // ---- results
@@ -652,14 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_fence_after();
           const bool whole = tile == 0 && tile_end == w.ut;
-          named_bar_sync(pair_bar, 64);  // the last maxima are read
-          xch[128 * hf] = l;
-          named_bar_sync(pair_bar, 64);
-          l = xch[0] + xch[128];
           if (warp_live && !__any_sync(~0u, *abort_flag)) {
-            uint32_t nan[(DH + 31) / 32];
+            uint32_t nan[D / 32];
 #pragma unroll
-            for (int q = 0; q < (DH + 31) / 32; ++q) nan[q] = 0;
+            for (int q = 0; q < D / 32; ++q) nan[q] = 0;
             if (nan_seg[seg & 3] == seg + 1) {
               // V holds NaN at a key of an edge tile: rows that see it take it
               const int lo = w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo;
@@ -667,12 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = max(first, tile * kTile); j < min(lim_all, tile_end * kTile); ++j) {
                 const int page = page_at(c, w.b, j >> c.page_shift);
                 if (page < 0) continue;
-                const uint8_t* v = c.layer + (size_t)page * c.page_stride + c.off_v +
-                                   (((size_t)kv << c.page_shift) +
-                                    (j & ((1 << c.page_shift) - 1))) * D + hf * DH;
-#pragma unroll
-                for (int q = 0; q < DH; ++q)
-                  if ((v[q] & 0x7f) == 0x7f) nan[q / 32] |= 1u << (q % 32);
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                    c.layer + (size_t)page * c.page_stride + c.off_v +
+                    (((size_t)kv << c.page_shift) + (j & ((1 << c.page_shift) - 1))) * D);
+                for (int q = 0; q < D / 4; ++q)
+                  for (int k = 0; k < 4; ++k)
+                    if ((v[q] >> (8 * k) & 0x7f) == 0x7f) nan[q / 8] |= 1u << (q % 8 * 4 + k);
               }
             }
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -682,51 +682,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             // results go through the row tile's Q buffer (its products are done)
             const uint32_t stage = sQ + g * L::TILE;
 #pragma unroll
-            for (int q = 0; q < DH / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld_x16(o_col + hf * DH + 16 * q, o);
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld_x32(o_col + 32 * q, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
+              for (int k = 0; k < 32; ++k) {
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
-                if (nan[q / 2] >> (16 * (q & 1) + k) & 1) o[k] = 0x7fc00000u;
+                if (nan[q] >> k & 1) o[k] = 0x7fc00000u;
               }
               if (whole) {
 #pragma unroll
-                for (int k = 0; k < 16; k += 8)
-                  st_shared_v4(stage + unit_at<D>(r, (hf * DH + 16 * q + k) / 8),
+                for (int k = 0; k < 32; k += 8)
+                  st_shared_v4(stage + unit_at<D>(r, 4 * q + k / 8),
                                pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
                                pack_bf16x2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
                                pack_bf16x2(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
                                pack_bf16x2(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
               } else if (live) {
 #pragma unroll
-                for (int k = 0; k < 16; k += 4)
-                  *reinterpret_cast<uint4*>(
-                      p.a.acc + part * D +
-                      ((size_t)((hf * DH + 16 * q + k) / 4) * kRows + pr) * 4) =
+                for (int k = 0; k < 32; k += 4)
+                  *reinterpret_cast<uint4*>(p.a.acc + part * D +
+                                            ((size_t)(8 * q + k / 4) * kRows + pr) * 4) =
                       make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
               }
             }
-            if (live && hf == 0) {
-              if (whole && p.a.lse) p.a.lse[slot0 + (unsigned)row] = (m + log2f(l)) * kLn2;
-              if (!whole) *reinterpret_cast<float2*>(p.a.ml + (part + pr) * 2) = make_float2(m, l);
+            if (whole) {
+              __syncwarp();
+              constexpr int kL = D / 8, kR = 32 / kL;
+              const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
+              uint16_t* ob = p.a.out + (size_t)w.b * c.H * c.n_q * D;
+#pragma unroll 4
+              for (int i = 0; i < 32; i += kR) {
+                const int rl = i + lane / kL, u = lane % kL;
+                const int dst = __shfl_sync(~0u, mine, rl);
+                const float4 x = lds_f32x4(stage + unit_at<D>((warp & 3) * 32 + rl, u));
+                if (dst >= 0)
+                  *(reinterpret_cast<float4*>(ob + (size_t)(unsigned)dst * D) + u) = x;
+              }
+              __syncwarp();
             }
+            if (live && whole && p.a.lse) p.a.lse[row] = (m + log2f(l)) * kLn2;
+            if (live && !whole)
+              *reinterpret_cast<float2*>(p.a.ml + (part + pr) * 2) = make_float2(m, l);
           }
-          named_bar_sync(pair_bar, 64);
-          if (whole && warp_live && !__any_sync(~0u, *abort_flag)) {
-            constexpr int kL = D / 8, kR = 32 / kL;
-            const int u = lane % kL;
-#pragma unroll
-            for (int i = 0; i < 16; i += kR) {
-              const int rl = 16 * hf + i + lane / kL;
-              const int dst = __shfl_sync(~0u, row, rl);
-              const float4 x = lds_f32x4(sQ + g * L::TILE + unit_at<D>(q4 * 32 + rl, u));
-              if (dst >= 0)
-                *(reinterpret_cast<float4*>(p.a.out + (slot0 + (unsigned)dst) * D) + u) = x;
-            }
-          }
-          named_bar_sync(pair_bar, 64);  // Q's buffer and the exchange are free again
         }
         if (threadIdx.x == 0 && tile == 0 && tile_end < w.ut) {
           // the unit begins here and ends in CTA `last`
@@ -740,10 +739,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile = 0;
         w.next();
       }
-    } else if (warp < 20) {
+    } else if (warp < 12) {
       // ------------------------------------------------------------ V: codes -> f16
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-      const int tid = threadIdx.x - 512;
+      const int tid = threadIdx.x - 256;
       constexpr int kCh = D / 16;              // 16-byte chunks of a row of codes
       constexpr int kN = kTile * kCh / 128;    // chunks of a thread in a tile
       constexpr int kStep = 128 / kCh;         // rows between a thread's chunks
@@ -802,8 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------ products
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-      if ((warp == 20 || warp == 22) && lane == 0) {
-        const int g = (warp - 20) >> 1;
+      if ((warp == 12 || warp == 14) && lane == 0) {
+        const int g = (warp - 12) >> 1;
         constexpr uint32_t id_s = idesc_e4m3(128, kTile);
         constexpr uint32_t id_o = idesc_f16(128, D, false, true);
         const uint32_t s_col = tmem + kS + g * 128, o_col = tmem + kO + g * 128;
@@ -842,10 +841,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine) {
               const uint64_t vt = G::mnmajor_desc(sV + st * L::TILE, 0);
               constexpr int kVStep = 16 * G::SWZ >> 4;
-              mbar_poll(p_full + g, n_p & 1, wc, kSiteP);
-              tc_fence_after();
-              issue_pv<kVStep>(o_col, s_col, vt, id_o, i > tile);
-              issue_pv<kVStep>(o_col, s_col + 64, vt + 4 * kVStep, id_o, 1);
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                mbar_poll(p_full + 2 * g + half, n_p & 1, wc, kSiteP);
+                tc_fence_after();
+                issue_pv<kVStep>(o_col, s_col + 32 * half, vt + 4 * kVStep * half, id_o,
+                                 i > tile || half);
+              }
               mma_commit(o_done + g);
               mbar_arrive(o_done + g);
               mma_commit(v_empty + st);
@@ -868,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every product has completed before TMEM is freed
         mma_commit(drained + g);
         mbar_drain(drained + g, 0);
-      } else if (warp == 21) {
+      } else if (warp == 13) {
         // ---------------------------------------------------------- codes and scales
         uint32_t kc = 0, vc = 0;
         const int per = c.page_shift > 4 ? 1 << (c.page_shift - 4) : 1;  // groups of a page
@@ -977,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 20) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

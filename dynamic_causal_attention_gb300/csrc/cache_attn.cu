@@ -11,6 +11,17 @@
 // softmax is sum_j p_j / s_v.  So a weight is rounded to f16 relative to the
 // largest contribution to `out`, whatever the scales of the blocks.
 //
+// This file: up to 16 query rows for each slot and K/V head (single tokens and
+// short drafts; more rows go to cache_chunk.cu).  Such calls are bound by the
+// bytes of the codes, so the kernel is built around reading them with few
+// instructions: codes go from global memory straight into the registers of the
+// matrix fragments, 16 bytes a lane, one step ahead.  Both products are formed
+// transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and the columns
+// of V fill the 16 rows of a fragment and the few query rows its 8 columns.
+// Which key or which component of d a slot of a fragment stands for is free as
+// long as both operands agree; it is chosen so that a lane's slots are
+// consecutive bytes.
+//
 // Both products run in f16 with fp32 sums: f16 holds every e4m3 value; a row
 // of q is scaled by a power of two into f16's range, which loses bits only of
 // components 2^-28 below the row's largest.
@@ -25,38 +36,32 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 4;
 
 // ------------------------------------------------------------ work split
-// A unit is (slot b, row tile, K/V head): rows [16 tile, 16 tile + 16) of the
-// slot's n_new * group query rows (row r = t * group + h) against the keys up
-// to the last position among them, in tiles of kTile keys.  All tiles of all
-// units, in that order, are cut into equal shares, one for each CTA; a unit
-// that is cut leaves partial sums, joined by a second kernel in the order of
-// the CTAs.  Nothing depends on timing.
-constexpr int kMR = 16;      // query rows of a unit
-constexpr int kTile = 64;    // keys of a tile: 16 for each warp
-constexpr int kWarps = 4;
-constexpr int kMinTiles = 4; // least share of a CTA
+// A unit is (slot b, K/V head): the slot's n_new * group query rows (row
+// r = t * group + h) against all its keys, in tiles of kTile keys.  All tiles of
+// all units, in that order, are cut into equal shares, one for each CTA; a
+// unit that is cut leaves partial sums, joined by a second kernel in the order
+// of the CTAs.  Nothing depends on timing.  Where no slot can have more than
+// kWholeKeys keys, each unit is one CTA's instead: no search for a share and no
+// second kernel.
+constexpr int kMinTiles = 4;     // least share of a CTA
+constexpr int kWholeKeys = 512;
 
-__device__ __forceinline__ int unit_extent(const Rows& r, int rt, int group) {
-  int t_hi = (rt * kMR + kMR - 1) / group + 1;
-  if (t_hi > r.n_new) t_hi = r.n_new;
-  const int e = r.base + t_hi;
-  return e < 0 ? 0 : (e < r.cap ? e : r.cap);
-}
-__device__ __forceinline__ int unit_tiles(const Rows& r, int rt, int group) {
-  const int n = (unit_extent(r, rt, group) + kTile - 1) / kTile;
-  return n < 1 ? 1 : n;  // rows that see nothing are written too
-}
-__device__ __forceinline__ int slot_row_tiles(const Rows& r, int group) {
-  return (int)(((long long)r.n_new * group + kMR - 1) / kMR);
-}
-__device__ __forceinline__ long long slot_tiles(const CacheCall& c, int b) {
+template <int D>
+struct Geo {
+  static constexpr int kGroups = 128 / D;           // groups of 16 keys in a warp's step: 4 KB of codes
+  static constexpr int kStep = 16 * kGroups;        // keys of a step
+  static constexpr int kTile = kWarps * kStep;      // keys of a tile
+};
+
+template <int TILE>
+__device__ __forceinline__ int slot_tiles(const CacheCall& c, int b) {
   const Rows r = slot_rows(c, b);
-  const int n = slot_row_tiles(r, c.group);
-  long long sum = 0;
-  for (int i = 0; i < n; ++i) sum += unit_tiles(r, i, c.group);
-  return sum * c.H_kv;
+  if (r.n_new == 0) return 0;
+  const int n = (r.cap + TILE - 1) / TILE;
+  return n < 1 ? 1 : n;  // rows that see nothing are written too
 }
 
 struct Share {
@@ -68,144 +73,216 @@ struct Share {
 // Every CTA finds its share: each thread sums a run of slots, a block scan
 // gives the runs' first tiles, and the thread whose run holds the share's
 // first tile walks it.
-__device__ Share find_share(const CacheCall& c, long long* scan /* [threads + 4] */) {
-  const int n = blockDim.x, tid = threadIdx.x;
+template <int TILE>
+__device__ Share find_share(const CacheCall& c, long long* scan /* [kWarps + 2] */) {
+  constexpr int n = kWarps * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (c.n_seqs + n - 1) / n;
   const int b0 = min(tid * per, c.n_seqs), b1 = min(b0 + per, c.n_seqs);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += slot_tiles(c, b);
-  scan[tid] = sum;
+  for (int b = b0; b < b1; ++b) sum += slot_tiles<TILE>(c, b);
+  sum *= c.H_kv;
+  long long upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) scan[warp] = upto;
   __syncthreads();
-  for (int o = 1; o < n; o <<= 1) {
-    const long long x = tid >= o ? scan[tid - o] : 0;
-    __syncthreads();
-    scan[tid] += x;
-    __syncthreads();
+  long long total = 0, mine = upto - sum;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) mine += scan[i];
+    total += scan[i];
   }
   Share s;
-  const long long total = scan[n - 1];
   s.size = (total + gridDim.x - 1) / gridDim.x;
   if (s.size < kMinTiles) s.size = kMinTiles;
   s.begin = min(s.size * blockIdx.x, total);
   s.end = min(s.begin + s.size, total);
-  const long long mine = scan[tid] - sum;
   if (s.begin < s.end && mine <= s.begin && s.begin < mine + sum) {
     long long at = mine;
     int b = b0;
     for (; b < b1 - 1; ++b) {
-      const long long t = slot_tiles(c, b);
+      const long long t = (long long)slot_tiles<TILE>(c, b) * c.H_kv;
       if (s.begin < at + t) break;
       at += t;
     }
-    scan[n] = b;
-    scan[n + 1] = s.begin - at;
+    scan[kWarps] = b;
+    scan[kWarps + 1] = s.begin - at;
   }
   __syncthreads();
-  s.b = (int)scan[n];
-  s.in_slot = scan[n + 1];
+  s.b = (int)scan[kWarps];
+  s.in_slot = scan[kWarps + 1];
   return s;
 }
 
-// ------------------------------------------------------------ shared memory
-// One step of a warp is 16 keys of one page: K codes, V codes, the two scales
-// and the number of keys there.  16-byte chunks are placed so that the reads
-// of both products touch every bank once: a product's reads take the keys
-// {c, c + 4} and {c + 8, c + 12} for lane % 4 = c.
-template <int D>
-__device__ __forceinline__ uint32_t chunk_at(int key, int ch) {
-  if (D == 128) {
-    const int f = (((key & 3) << 1) | ((key >> 1) & 1)) ^ (key & 4);
-    return key * 128 + ((ch ^ f) << 4);
-  }
-  if (D == 64) {
-    const int half = (key & 1) ^ ((key >> 2) & 1);
-    return (key >> 1) * 128 + half * 64 + ((ch ^ (((key >> 1) & 1) << 1)) << 4);
-  }
-  return (key >> 2) * 128 + (((key & 3) ^ (((key >> 2) & 1) << 1)) << 5) + (ch << 4);
+// Codes of the cache: read once, so not kept in L1.
+__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
+}
+__device__ __forceinline__ void load_codes(uint32_t (&w)[2], const uint8_t* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+               : "=r"(w[0]), "=r"(w[1])
+               : "l"(p));
+}
+__device__ __forceinline__ void load_codes(uint32_t (&w)[1], const uint8_t* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
 }
 
-template <int D>
-struct Geo {
-  static constexpr int kCodes = 16 * D;               // bytes of K or V codes of a step
-  static constexpr int kStep = 2 * kCodes + 16;       // + K scale, V scale, key count
-  static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 6 : 10);
-  static constexpr int kRing = (kStages * kStep + 127) / 128 * 128;
-  static constexpr int kMerge = kWarps * kMR * (D + 2) * 4;
-  static constexpr int kSmem = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
-};
+// The 8 x 8 block of 16-bit values of a warp (lane: row lane / 4, columns
+// 2 (lane % 4) and the next), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
-    cache_attn_kernel(const __grid_constant__ CacheAttn p) {
-  using G = Geo<D>;
-  constexpr int kKS = D / 16;  // steps of 16 along d
-  constexpr int kNT = D / 8;   // output tiles of 8 columns
-  constexpr int kVB = D / 8;   // bytes of a V row that a lane takes
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long scan[kWarps * 32 + 4];
+template <int D, int NT>  // NT: 8 query rows each
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
+    cache_attn_kernel(const __grid_constant__ CacheAttn p, bool whole_units) {
+  constexpr int kMR = 8 * NT;
+  constexpr int kG = Geo<D>::kGroups, kStep = Geo<D>::kStep, kTile = Geo<D>::kTile;
+  constexpr int kKS = D / 16;            // steps of 16 along d
+  constexpr int kKW = D / 16;            // words of a K row that a lane takes
+  constexpr int kVW = D / 32;            // words of a V row that a lane takes
+  constexpr int kKL = kKW < 4 ? kKW : 4; // words of one load
+  constexpr int kVB = D / 8;             // bytes of a V row that a lane takes
+  __shared__ __align__(16) float merge[kWarps * kMR * (D + 2)];
+  __shared__ long long scan[kWarps + 2];
   const CacheCall& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, cc = lane & 3;
 
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits without end
-  const Share sh = find_share(c, scan);
-  if (threadIdx.x == 0) p.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (sh.begin >= sh.end) return;
-
-  const uint32_t ring = smem_u32(smem) + warp * G::kRing;
-  int b = sh.b;
-  Rows rows = slot_rows(c, b);
-  int rt = 0;
-  long long in_slot = sh.in_slot;
-  int ut = unit_tiles(rows, 0, c.group);
-  while (in_slot >= (long long)ut * c.H_kv) {
-    in_slot -= (long long)ut * c.H_kv;
-    ++rt;
-    ut = unit_tiles(rows, rt, c.group);
+  Share sh;
+  if (whole_units) {
+    sh.b = blockIdx.x / c.H_kv;
+    const int n = slot_tiles<kTile>(c, sh.b);
+    if (n == 0) return;
+    sh.in_slot = (long long)n * (blockIdx.x - sh.b * c.H_kv);
+    sh.begin = 0;
+    sh.end = sh.size = n;
+  } else {
+    sh = find_share<kTile>(c, scan);
+    if (threadIdx.x == 0) p.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (sh.begin >= sh.end) return;
   }
-  int kv = (int)(in_slot / ut), tile = (int)(in_slot % ut);
+
+  int b = sh.b, ut = slot_tiles<kTile>(c, b);
+  Rows rows = slot_rows(c, b);
+  int kv = (int)(sh.in_slot / ut), tile = (int)(sh.in_slot % ut);
   long long at = sh.begin;
 
   while (true) {
-    // ---- this segment: tiles [tile, tile_end) of unit (b, rt, kv)
+    // ---- this segment: tiles [tile, tile_end) of unit (b, kv)
     const int tile_end = (int)min((long long)ut, tile + (sh.end - at));
-    const int ext = unit_extent(rows, rt, c.group);
-    const int n_rows = min(kMR, rows.n_new * c.group - rt * kMR);
+    const int ext = rows.cap;
+    const int n_rows = rows.n_new * c.group;
     const int steps = tile_end - tile;
     const int k_head = c.k_of[kv];
+    const bool any_dyn = k_head >= 0;  // a dynamic head in the group
+    const int key_w = tile * kTile + warp * kStep;  // first key of this warp's step 0
 
-    // rows of this lane: quad and quad + 8
-    int pos[2], head[2];
-    bool ice[2];
-    const uint16_t* qrow[2];
+    // ---- codes: pages are looked up 32 groups ahead, one for each lane
+    int pages = -1;
+    uint32_t kw[kG][2][kKW], vw[kG][4][kVW];
+    float ks[kG], vs[kG];
+    int there[kG];  // keys of the group
+    auto group_key = [&](int s, int g) { return key_w + s * kTile + 16 * g; };
+    auto look_up = [&](int s) {  // the pages of steps s .. s + 32 / kG - 1
+      const int st = s + lane / kG, key = group_key(st, lane % kG);
+      pages = st < steps && key < ext ? page_at(c, b, key >> c.page_shift) : -1;
+    };
+    const int in_page = (1 << c.page_shift) - 1;
+    auto record = [&](int s, int g, int& n) {
+      const int page = __shfl_sync(~0u, pages, (s * kG + g) & 31);
+      const int key = group_key(s, g);
+      n = page < 0 || s >= steps ? 0 : min(16, ext - key);
+      return c.layer + (size_t)(n > 0 ? page : 0) * c.page_stride;
+    };
+    auto fetch_k = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = rt * kMR + quad + 8 * i;
-      const bool live = quad + 8 * i < n_rows;
-      const int t = live ? r / c.group : 0, hh = live ? r - t * c.group : 0;
-      head[i] = kv * c.group + hh;
-      pos[i] = live ? rows.base + t : -1;
-      ice[i] = live && c.is_static[head[i]];
-      qrow[i] = live && !ice[i] ? p.Q + (((size_t)b * c.H + head[i]) * c.n_q + t) * D : nullptr;
-    }
-    bool any_dyn = k_head >= 0;  // a dynamic head in the group
-    const int pos_lo = rows.base + rt * kMR / c.group;  // the row that sees least
+      for (int g = 0; g < kG; ++g) {
+        const uint8_t* rec = record(s, g, there[g]);
+        if (!any_dyn || there[g] == 0) continue;
+        const uint8_t* src =
+            rec + (((size_t)k_head << c.page_shift) + (group_key(s, g) & in_page) + quad) * D +
+            cc * 4 * kKL;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)  // keys quad and quad + 8
+#pragma unroll
+          for (int i = 0; i < kKW / kKL; ++i) {
+            uint32_t(&w)[kKL] = *reinterpret_cast<uint32_t(*)[kKL]>(kw[g][h] + kKL * i);
+            // keys behind the last one lie on the page as well
+            load_codes(w, src + h * 8 * D + i * 64);
+          }
+        ks[g] = __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + k_head);
+      }
+    };
+    auto fetch_v = [&](int s) {
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        int n;
+        const uint8_t* rec = record(s, g, n);
+        if (n == 0) continue;
+        const uint8_t* src =
+            rec + c.off_v + (((size_t)kv << c.page_shift) + (group_key(s, g) & in_page)) * D +
+            quad * kVB;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9
+          const int key = 2 * cc + (u & 1) + 8 * (u >> 1);
+          load_codes(vw[g][u], src + key * D);
+        }
+        vs[g] = __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + kv);
+      }
+    };
+    look_up(0);
+    fetch_k(0);
+    fetch_v(0);
 
-    // ---- Q fragments: lane takes d = 16 c .. 16 c + 15 (and + 64) of its rows
-    uint32_t qf[kKS][4];
-    float fac[2];
+    // ---- the rows of this lane: 8 nt + 2c and the next
+    int pos[NT][2], head[NT][2];
+    bool ice[NT][2];
+    bool any_ice = false;
+    const int pos_lo = rows.base;  // the row that sees least
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * nt + 2 * cc + i;
+        const bool live = r < n_rows;
+        const int t = live ? r / c.group : 0, hh = live ? r - t * c.group : 0;
+        head[nt][i] = kv * c.group + hh;
+        pos[nt][i] = live ? rows.base + t : -1;
+        ice[nt][i] = live && c.is_static[head[nt][i]];
+        any_ice |= ice[nt][i];
+      }
+
+    // ---- Q^T fragments: lane takes components 16 c .. 16 c + 15 (and + 64; 8 c ..
+    // for d_h = 32) of row 8 nt + quad
+    uint32_t qf[NT][kKS][2];
+    float fac[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + quad;
+      const uint16_t* qrow = nullptr;
+      if (r < n_rows && any_dyn) {
+        const int t = r / c.group, h = kv * c.group + r - t * c.group;
+        if (!c.is_static[h]) qrow = p.Q + (((size_t)b * c.H + h) * c.n_q + t) * D;
+      }
       float x[D / 4];
       float amax = 0.f;
 #pragma unroll
       for (int blk = 0; blk < (D + 63) / 64; ++blk) {
-        constexpr int kW = D >= 64 ? 16 : 8;  // d's of a lane in a block
+        constexpr int kW = D >= 64 ? 16 : 8;  // components of a lane in a block
 #pragma unroll
         for (int u = 0; u < kW / 8; ++u) {
           uint4 w = make_uint4(0, 0, 0, 0);
-          if (qrow[i])
-            w = __ldg(reinterpret_cast<const uint4*>(qrow[i] + 64 * blk + kW * cc + 8 * u));
+          if (qrow) w = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * blk + kW * cc + 8 * u));
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
@@ -222,199 +299,161 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
       int e = (__float_as_int(amax) >> 23) - 127 - 14;
       e = amax > 0.f ? max(-126, min(112, e)) : 0;
       const float down = pow2f(-e);
-      fac[i] = pow2f(e) * (rsqrtf((float)D) * kLog2e);
+      const float f = pow2f(e) * (rsqrtf((float)D) * kLog2e);
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        // the lane's 4 values of step ks: slots 2c, 2c+1 (lo) and 2c+8, 2c+9 (hi)
-        const int o = ks * 4;
-        qf[ks][i] = pack_f16x2(x[o] * down, x[o + 1] * down);
-        qf[ks][2 + i] = pack_f16x2(x[o + 2] * down, x[o + 3] * down);
+      for (int i = 0; i < 2; ++i)  // of rows 2c, 2c + 1: held by quads 2c, 2c + 1
+        fac[nt][i] = __shfl_sync(~0u, f, 4 * (2 * cc + i));
+#pragma unroll
+      for (int s = 0; s < kKS; ++s) {
+        qf[nt][s][0] = pack_f16x2(x[4 * s] * down, x[4 * s + 1] * down);
+        qf[nt][s][1] = pack_f16x2(x[4 * s + 2] * down, x[4 * s + 3] * down);
       }
     }
 
-    // ---- the ring: page numbers are fetched 32 steps ahead by lane
-    int pages = -1;
-    const int key_w = tile * kTile + warp * 16;  // first key of this warp's step 0
-    auto load_pages = [&](int s0) {
-      const int key = key_w + (s0 + lane) * kTile;
-      pages = key < ext && s0 + lane < steps ? page_at(c, b, key >> c.page_shift) : -1;
-    };
-    auto issue = [&](int s) {
-      if (s < steps) {
-        if ((s & 31) == 0) load_pages(s);
-        const int page = __shfl_sync(~0u, pages, s & 31);
-        const int key0 = key_w + s * kTile;
-        const int n = page < 0 ? 0 : min(16, ext - key0);
-        const uint32_t st = ring + (s % G::kStages) * G::kStep;
-        const uint8_t* rec = c.layer + (size_t)(page < 0 ? 0 : page) * c.page_stride;
-        const int slot = key0 & ((1 << c.page_shift) - 1);
-        const uint8_t* src_v = rec + c.off_v + (((size_t)kv << c.page_shift) + slot) * D;
+    // logits of the frozen rows for one step, fetched a step ahead
+    float pat[NT][2][2 * kG];
+    auto fetch_pattern = [&](int s) {
+      if (!any_ice || s >= steps) return;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int ch = (lane + 32 * i) % (D / 16), key = (lane + 32 * i) / (D / 16);
-          cp_async16(st + G::kCodes + chunk_at<D>(key, ch), src_v + key * D + ch * 16,
-                     key < n ? 16 : 0);
-        }
-        if (any_dyn) {
-          const uint8_t* src_k = rec + (((size_t)k_head << c.page_shift) + slot) * D;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const int ch = (lane + 32 * i) % (D / 16), key = (lane + 32 * i) / (D / 16);
-            cp_async16(st + chunk_at<D>(key, ch), src_k + key * D + ch * 16, key < n ? 16 : 0);
+        for (int i = 0; i < 2; ++i)
+          if (ice[nt][i]) {
+#pragma unroll
+            for (int u = 0; u < 2 * kG; ++u) {
+              const int j = group_key(s, u >> 1) + quad + 8 * (u & 1);
+              const int dist = pos[nt][i] - j;
+              float a = -CUDART_INF_F;
+              if (dist >= 0 && j < p.T_pat && dist < p.T_pat)
+                a = __ldg(p.alpha + (size_t)head[nt][i] * p.T_pat + j) +
+                    __ldg(p.rho + (size_t)head[nt][i] * p.T_pat + dist);
+              pat[nt][i][u] = a * kLog2e;
+            }
           }
-        }
-        if (lane == 0) {
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + 2 * G::kCodes + 8), "r"(n) : "memory");
-          if (n > 0) {
-            if (any_dyn)
-              cp_async4(st + 2 * G::kCodes, rec + c.off_ks + 4 * (size_t)k_head);
-            cp_async4(st + 2 * G::kCodes + 4, rec + c.off_vs + 4 * (size_t)kv);
+    };
+    fetch_pattern(0);
+
+    float acc[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[nt][j][u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[nt][i] = -CUDART_INF_F;
+        l[nt][i] = 0.f;
+      }
+    }
+    bool v_nan = false;  // a NaN in V at a key that not every row sees
+
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+      // S^T of the step, [group][row pair][key quad: 2 rows | key quad + 8: 2 rows]
+      float sc[kG][NT][4];
+      int n[kG];
+      float kscale[kG];
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        n[g] = there[g];
+        kscale[g] = ks[g];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) sc[g][nt][u] = 0.f;
+        if (any_dyn && n[g] > 0) {
+#pragma unroll
+          for (int i = 0; i < kKS; ++i) {
+            uint32_t a[4];
+            e4m3x4_f16x4(kw[g][0][i], a[0], a[2]);
+            e4m3x4_f16x4(kw[g][1][i], a[1], a[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(sc[g][nt], a, qf[nt][i][0], qf[nt][i][1]);
           }
         }
       }
-      cp_async_commit();
-    };
+      // the lookup of the next pages lies between the last use of the old ones
+      // (V of this step was fetched) and K of the next step
+      if (((s + 1) * kG & 31) == 0) look_up(s + 1);
+      fetch_k(s + 1);
 
-    // values of the frozen rows for one step, fetched a step ahead
-    float pat[2][4];
-    auto fetch_pattern = [&](int s) {
+      // y = x log2(e) + log2(s_v); keys that a row does not see: -inf
+      bool grow = false;
+      float inv[kG];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (ice[i] && s < steps) {
+      for (int g = 0; g < kG; ++g) {
+        if (n[g] == 0) continue;
+        const int key0 = group_key(s, g);
+        const float lv = __log2f(vs[g]);
+        inv[g] = __fdividef(1.f, vs[g]);
+        const bool edge = n[g] < 16 || key0 + 15 > pos_lo;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int j = key_w + s * kTile + cc + 4 * u;  // u: keys c, c+4, c+8, c+12
-            const int dist = pos[i] - j;
-            float a = -CUDART_INF_F;
-            if (dist >= 0 && j < p.T_pat && dist < p.T_pat)
-              a = __ldg(p.alpha + (size_t)head[i] * p.T_pat + j) +
-                  __ldg(p.rho + (size_t)head[i] * p.T_pat + dist);
-            pat[i][u] = a * kLog2e;
+            const int i = u & 1, k = quad + 8 * (u >> 1);
+            float& y = sc[g][nt][u];
+            y = fmaf(y, fac[nt][i] * kscale[g], lv);
+            if (any_ice && ice[nt][i]) y = pat[nt][i][2 * g + (u >> 1)] + lv;
+            if (edge && (k >= n[g] || key0 + k > pos[nt][i])) y = -CUDART_INF_F;
+            // the maximum moves only when it would grow by more than 2^8:
+            // weights up to 2^8 fit f16 as well
+            grow |= y > m[nt][i] + 8.f;
           }
-        }
-    };
-
-    float acc[kNT][4];
+      }
+      if (__any_sync(~0u, grow)) {
 #pragma unroll
-    for (int t = 0; t < kNT; ++t)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) acc[t][u] = 0.f;
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
-    bool v_nan = false;  // a NaN in V at a key that not every row sees
-
-    __syncwarp();
-#pragma unroll
-    for (int s = 0; s < G::kStages - 1; ++s) issue(s);
-    fetch_pattern(0);
-#pragma unroll 1
-    for (int s = 0; s < steps; ++s) {
-      cp_async_wait<G::kStages - 2>();
-      __syncwarp();
-      const uint32_t st = ring + (s % G::kStages) * G::kStep;
-      const int n = __float_as_int(lds_f32(st + 2 * G::kCodes + 8));
-      const int key0 = key_w + s * kTile;
-      if (n > 0) {
-        const float ks = lds_f32(st + 2 * G::kCodes), vs = lds_f32(st + 2 * G::kCodes + 4);
-        float sc[2][4];  // [8-key half][row quad: 2 keys | row quad + 8: 2 keys]
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) sc[h][u] = 0.f;
-        if (any_dyn) {
-          const int key = (quad >> 1) + 4 * (quad & 1);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[kKS];
-            if (D == 32) {
-              const uint32_t a = st + chunk_at<D>(key + 8 * h, cc >> 1) + (cc & 1) * 8;
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
-            } else {
-#pragma unroll
-              for (int blk = 0; blk < D / 64; ++blk)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[4 * blk]), "=r"(w[4 * blk + 1]), "=r"(w[4 * blk + 2]),
-                               "=r"(w[4 * blk + 3])
-                             : "r"(st + chunk_at<D>(key + 8 * h, cc + 4 * blk)));
-            }
-#pragma unroll
-            for (int i = 0; i < kKS; ++i) {
-              uint32_t b0, b1;
-              e4m3x4_f16x4(w[i], b0, b1);
-              mma_f16_16816(sc[h], qf[i], b0, b1);
-            }
-          }
-        }
-        // y = x log2(e) + log2(s_v); keys that a row does not see: -inf
-        const float lv = __log2f(vs), inv = __fdividef(1.f, vs);
-        const bool edge = n < 16 || key0 + 15 > pos_lo;
-        float top[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float f = fac[i] * ks;
-          top[i] = -CUDART_INF_F;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {  // keys c + 4 u: half u >> 1, column u & 1
-            float& y = sc[u >> 1][2 * i + (u & 1)];
-            y = ice[i] ? pat[i][u] + lv : fmaf(y, f, lv);
-            if (edge && (cc + 4 * u >= n || key0 + cc + 4 * u > pos[i])) y = -CUDART_INF_F;
-            top[i] = fmaxf(top[i], y);
-          }
-          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 1));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 2));
-        }
-        if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
-          float corr[2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float mn = fmaxf(m[i], top[i]);
-            corr[i] = mn == -CUDART_INF_F ? 1.f : fast_exp2(m[i] - mn);
-            m[i] = mn;
-            l[i] *= corr[i];
+            float top = m[nt][i];
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+              if (n[g] > 0) top = fmaxf(top, fmaxf(sc[g][nt][i], sc[g][nt][2 + i]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            const float corr = top == -CUDART_INF_F ? 1.f : fast_exp2(m[nt][i] - top);
+            m[nt][i] = top;
+            l[nt][i] *= corr;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              acc[nt][j][i] *= corr;
+              acc[nt][j][2 + i] *= corr;
+            }
+          }
+      }
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        if (n[g] == 0) continue;
+        const bool edge = n[g] < 16 || group_key(s, g) + 15 > pos_lo;
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float base = m[nt][u & 1] == -CUDART_INF_F ? 0.f : m[nt][u & 1];
+            w[u] = fast_exp2(sc[g][nt][u] - base);
           }
 #pragma unroll
-          for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) acc[t][u] *= corr[u >> 1];
-        }
-        uint32_t pf[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float base = m[i] == -CUDART_INF_F ? 0.f : m[i];
-          float sum = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p0 = fast_exp2(sc[h][2 * i] - base);
-            const float p1 = fast_exp2(sc[h][2 * i + 1] - base);
-            sum += p0 + p1;
-            pf[2 * h + i] = pack_f16x2(p0, p1);
+          for (int i = 0; i < 2; ++i) {
+            l[nt][i] = fmaf(w[i] + w[2 + i], inv[g], l[nt][i]);
+            pf[nt][i] = transpose8(pack_f16x2(w[2 * i], w[2 * i + 1]));
           }
-          l[i] = fmaf(sum, inv, l[i]);
         }
-        // V: keys c, c + 4 (slots 2c, 2c+1) and c + 8, c + 12 (slots 2c+8, 2c+9)
-        uint32_t w[4][(kVB + 3) / 4];
+        // V^T: a lane's words hold 4 components of one key; pairs of keys side by side
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t a = st + G::kCodes + chunk_at<D>(cc + 4 * u, quad * kVB >> 4) +
-                             (quad * kVB & 15);
-          if (D == 128)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[u][0]), "=r"(w[u][1 % (kVB / 4)]), "=r"(w[u][2 % (kVB / 4)]),
-                           "=r"(w[u][3 % (kVB / 4)])
-                         : "r"(a));
-          else if (D == 64)
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(w[u][0]), "=r"(w[u][1 % (kVB / 4)])
-                         : "r"(a));
-          else
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[u][0]) : "r"(a));
-        }
-#pragma unroll
-        for (int i = 0; i < kVB / 4; ++i) {
-          uint32_t f[2][4];  // [slots lo, hi][column of the word]
+        for (int i = 0; i < kVW; ++i) {
+          uint32_t f[2][4];  // [keys 2c, 2c + 1 | 2c + 8, 2c + 9][component of the word]
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            e4m3x4_f16x4(__byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x5140), f[h][0], f[h][1]);
-            e4m3x4_f16x4(__byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x7362), f[h][2], f[h][3]);
+            e4m3x4_f16x4(__byte_perm(vw[g][2 * h][i], vw[g][2 * h + 1][i], 0x5140), f[h][0],
+                         f[h][1]);
+            e4m3x4_f16x4(__byte_perm(vw[g][2 * h][i], vw[g][2 * h + 1][i], 0x7362), f[h][2],
+                         f[h][3]);
           }
           if (edge) {  // 0 * NaN would reach rows that do not see the key
 #pragma unroll
@@ -428,61 +467,60 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
               }
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mma_f16_16816(acc[4 * i + u], pf, f[0][u], f[1][u]);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(acc[nt][2 * i + j], a, pf[nt][0], pf[nt][1]);
+          }
         }
       }
+      fetch_v(s + 1);
       fetch_pattern(s + 1);
-      __syncwarp();
-      issue(s + G::kStages - 1);
     }
-    cp_async_wait<0>();
 
     if (__any_sync(~0u, v_nan)) {
       // rows that do see a key whose V holds NaN take it
-      for (int s = 0; s < steps; ++s) {
-        const int key0 = key_w + s * kTile;
-        for (int k = 0; k < 16; ++k) {
-          const int j = key0 + k;
+      for (int s = 0; s < steps; ++s)
+        for (int k = 0; k < kStep; ++k) {
+          const int j = group_key(s, 0) + k, key0 = j & ~15;
           if (j >= ext || (ext - key0 >= 16 && key0 + 15 <= pos_lo)) continue;
           const int page = page_at(c, b, j >> c.page_shift);
           if (page < 0) continue;
           const uint8_t* v = c.layer + (size_t)page * c.page_stride + c.off_v +
-                             (((size_t)kv << c.page_shift) + (j & ((1 << c.page_shift) - 1))) * D;
+                             (((size_t)kv << c.page_shift) + (j & in_page)) * D + quad * kVB;
 #pragma unroll
-          for (int t = 0; t < kNT; ++t)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (j <= pos[u >> 1] && (v[(2 * cc + (u & 1)) * kVB + t] & 0x7f) == 0x7f)
-                acc[t][u] = CUDART_NAN_F;
+            for (int t = 0; t < kVB; ++t)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (j <= pos[nt][i] && (v[t] & 0x7f) == 0x7f)
+                  acc[nt][t / 2][2 * (t & 1) + i] = CUDART_NAN_F;
         }
-      }
     }
 
     // ---- join the warps: [warp][row][D] sums, then [warp][row][2] of (m, l)
+    float* mm = merge + kWarps * kMR * D;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(~0u, l[i], 1);
-      l[i] += __shfl_xor_sync(~0u, l[i], 2);
-    }
-    __syncthreads();  // every warp has read its ring
-    float* mo = reinterpret_cast<float*>(smem);
-    float* mm = mo + kWarps * kMR * D;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = quad + 8 * i;
-      if (r < n_rows) {
-        float* dst = mo + ((size_t)warp * kMR + r) * D;
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-          dst[2 * cc * kVB + t] = acc[t][2 * i];
-          dst[(2 * cc + 1) * kVB + t] = acc[t][2 * i + 1];
-        }
-        if (cc == 0) {
-          mm[(warp * kMR + r) * 2] = m[i];
-          mm[(warp * kMR + r) * 2 + 1] = l[i];
+        for (int o = 4; o < 32; o <<= 1) l[nt][i] += __shfl_xor_sync(~0u, l[nt][i], o);
+        const int r = 8 * nt + 2 * cc + i;
+        if (r < n_rows) {
+          float* dst = merge + (warp * kMR + r) * D + quad * kVB;
+#pragma unroll
+          for (int t = 0; t < kVB; t += 4)
+            *reinterpret_cast<float4*>(dst + t) =
+                make_float4(acc[nt][t / 2][i], acc[nt][t / 2][2 + i], acc[nt][t / 2 + 1][i],
+                            acc[nt][t / 2 + 1][2 + i]);
+          if (quad == 0)
+            *reinterpret_cast<float2*>(mm + (warp * kMR + r) * 2) =
+                make_float2(m[nt][i], l[nt][i]);
         }
       }
-    }
     __syncthreads();
     const bool whole = tile == 0 && tile_end == ut;
     const int part = 2 * blockIdx.x + (at == sh.begin ? 0 : 1);
@@ -497,14 +535,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
         const float mw = mm[(w * kMR + r) * 2];
         const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(mw - mx);
         sum = fmaf(f, mm[(w * kMR + r) * 2 + 1], sum);
-        const float4 x = *reinterpret_cast<const float4*>(mo + ((size_t)w * kMR + r) * D + d);
+        const float4 x = *reinterpret_cast<const float4*>(merge + (w * kMR + r) * D + d);
         o.x = fmaf(f, x.x, o.x);
         o.y = fmaf(f, x.y, o.y);
         o.z = fmaf(f, x.z, o.z);
         o.w = fmaf(f, x.w, o.w);
       }
       if (whole) {
-        const int rr = rt * kMR + r, t = rr / c.group, h = kv * c.group + rr - t * c.group;
+        const int t = r / c.group, h = kv * c.group + r - t * c.group;
         const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: 0
         *reinterpret_cast<uint2*>(p.out + row * D + d) =
@@ -516,41 +554,38 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 3 : 4)
           *reinterpret_cast<float2*>(p.ml + ((size_t)part * kMR + r) * 2) = make_float2(mx, sum);
       }
     }
-    if (tile == 0 && tile_end < ut && threadIdx.x == 0) {
+    if (!whole && tile == 0 && threadIdx.x == 0) {
       // the unit begins here and ends in CTA `last`
       const int last = (int)((at + ut - 1) / sh.size);
-      p.join[blockIdx.x] = make_int4(b, rt, kv, last | (at == sh.begin ? 0 : 1 << 30));
+      p.join[blockIdx.x] = make_int4(b, kv, last, at == sh.begin ? 0 : 1);
     }
-    __syncthreads();  // the merge buffer is the ring again
 
     // ---- the next unit
     at += tile_end - tile;
     if (at >= sh.end) break;
+    __syncthreads();  // the merge buffer is free again
     tile = 0;
     if (++kv == c.H_kv) {
       kv = 0;
-      ++rt;
-      while (rt >= slot_row_tiles(rows, c.group)) {
-        rows = slot_rows(c, ++b);
-        rt = 0;
-      }
-      ut = unit_tiles(rows, rt, c.group);
+      do {
+        ut = slot_tiles<kTile>(c, ++b);
+      } while (ut == 0);
+      rows = slot_rows(c, b);
     }
   }
 }
 
 // Joins the parts of a unit that was cut: CTA x takes the unit that CTA x of
 // the first kernel left to its successors; y splits the rows.
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttn p) {
+  constexpr int kMR = 8 * NT;
   const CacheCall& c = p.c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 u = p.join[blockIdx.x];
   if (u.x < 0) return;
-  const int b = u.x, rt = u.y, kv = u.z, last = u.w & ~(1 << 30);
-  const int first = 2 * blockIdx.x + (u.w >> 30 & 1);
-  const Rows rows = slot_rows(c, b);
-  const int n_rows = min(kMR, rows.n_new * c.group - rt * kMR);
+  const int b = u.x, kv = u.y, last = u.z, first = 2 * blockIdx.x + u.w;
+  const int n_rows = slot_rows(c, b).n_new * c.group;
   for (int i = blockIdx.y * 128 + threadIdx.x; i < n_rows * (D / 4); i += gridDim.y * 128) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     auto ml = [&](int part) {
@@ -571,7 +606,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
       o.z = fmaf(f, x.z, o.z);
       o.w = fmaf(f, x.w, o.w);
     }
-    const int rr = rt * kMR + r, t = rr / c.group, h = kv * c.group + rr - t * c.group;
+    const int t = r / c.group, h = kv * c.group + r - t * c.group;
     const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2*>(p.out + row * D + d) =
@@ -580,33 +615,36 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   }
 }
 
-int n_ctas(int d_h, int n_sms) { return n_sms * (d_h == 128 ? 3 : 4); }
+int n_ctas(int nt, int n_sms) { return n_sms * (nt == 1 ? 4 : 3); }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
-  const int grid = n_ctas(D, n_sms);
-  cudaError_t e =
-      set_max_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<D>), Geo<D>::kSmem);
-  if (e != cudaSuccess) return e;
+  const bool whole = (long long)p.c.max_pages << p.c.page_shift <= kWholeKeys;
+  const int grid = whole ? p.c.n_seqs * p.c.H_kv : n_ctas(NT, n_sms);
   trace_begin(s);
-  cache_attn_kernel<D><<<grid, kWarps * 32, Geo<D>::kSmem, s>>>(p);
+  cache_attn_kernel<D, NT><<<grid, kWarps * 32, 0, s>>>(p, whole);
   trace_end(s, "cache_attn");
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || whole) return e;
   // launched while the first kernel runs; waits for its end before it reads
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 4);
+  cfg.gridDim = dim3(grid, 2);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   trace_begin(s);
-  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p);
+  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, p);
   trace_end(s, "cache_join");
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
+  return p.c.n_q * p.c.group <= 8 ? launch<D, 1>(p, n_sms, s) : launch<D, 2>(p, n_sms, s);
 }
 
 }  // namespace
@@ -619,11 +657,12 @@ CacheAttnWs cache_attn_ws(int d_h, int n_sms) {
     off = (off + bytes + 255) & ~(size_t)255;
     return o;
   };
-  const size_t n = (size_t)n_ctas(d_h, n_sms);
+  // the larger of both row counts
+  const size_t n = (size_t)n_ctas(1, n_sms), rows = 2 * (n * 8 > (size_t)n_ctas(2, n_sms) * 16 ? n * 8 : (size_t)n_ctas(2, n_sms) * 16);
   w.status = take(256);
   w.join = take(n * sizeof(int4));
-  w.ml = take(2 * n * kMR * 2 * 4);
-  w.acc = take(2 * n * kMR * d_h * 4);
+  w.ml = take(rows * 2 * 4);
+  w.acc = take(rows * d_h * 4);
   w.total = off;
   return w;
 }

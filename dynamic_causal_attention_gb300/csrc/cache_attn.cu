@@ -13,14 +13,15 @@
 //
 // This file: up to 16 query rows for each slot and K/V head (single tokens and
 // short drafts; more rows go to cache_chunk.cu).  Such calls are bound by the
-// bytes of the codes, so the kernel is built around reading them with few
-// instructions: codes go from global memory straight into the registers of the
-// matrix fragments, 16 bytes a lane, one step ahead.  Both products are formed
-// transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and the columns
-// of V fill the 16 rows of a fragment and the few query rows its 8 columns.
-// Which key or which component of d a slot of a fragment stands for is free as
-// long as both operands agree; it is chosen so that a lane's slots are
-// consecutive bytes.
+// bytes of the codes, so the kernel is built around keeping many of them in
+// flight for few instructions: each warp has a ring of its own in shared
+// memory, filled by asynchronous copies several steps ahead (a step is 4 KB:
+// 16 keys of K and V at d_h = 128), and waits for nobody else.  Both products
+// are formed transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys and
+// the columns of V fill the 16 rows of a fragment and the few query rows its 8
+// columns.  Which key or which component of d a slot of a fragment stands for
+// is free as long as both operands agree; it is chosen so that a lane's slots
+// are consecutive bytes, read 16 at a time without bank conflicts.
 //
 // Both products run in f16 with fp32 sums: f16 holds every e4m3 value; a row
 // of q is scaled by a power of two into f16's range, which loses bits only of
@@ -54,7 +55,28 @@ struct Geo {
   static constexpr int kGroups = 128 / D;           // groups of 16 keys in a warp's step: 4 KB of codes
   static constexpr int kStep = 16 * kGroups;        // keys of a step
   static constexpr int kTile = kWarps * kStep;      // keys of a tile
+  // ring of a warp: K codes, V codes, then for each group K scale, V scale and
+  // the number of keys
+  static constexpr int kCodes = kStep * D;
+  static constexpr int kMeta = 16 * kGroups;
+  static constexpr int kStage = 2 * kCodes + (kMeta + 127) / 128 * 128;
 };
+
+// Where 16-byte chunk `ch` of key `key` of a group lies.  A fragment's reads
+// take keys (n / 2) + 4 (n % 2) for n = lane / 4, or the keys lane % 4 and the
+// one 4 behind; either way 8 lanes touch every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int key, int ch) {
+  if (D == 128) {
+    const int f = (((key & 3) << 1) | ((key >> 1) & 1)) ^ (key & 4);
+    return key * 128 + ((ch ^ f) << 4);
+  }
+  if (D == 64) {
+    const int half = (key & 1) ^ ((key >> 2) & 1);
+    return (key >> 1) * 128 + half * 64 + ((ch ^ (((key >> 1) & 1) << 1)) << 4);
+  }
+  return (key >> 2) * 128 + (((key & 3) ^ (((key >> 2) & 1) << 1)) << 5) + (ch << 4);
+}
 
 template <int TILE>
 __device__ __forceinline__ int slot_tiles(const CacheCall& c, int b) {
@@ -118,19 +140,17 @@ __device__ Share find_share(const CacheCall& c, long long* scan /* [kWarps + 2] 
   return s;
 }
 
-// Codes of the cache: read once, so not kept in L1.
-__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "l"(p));
-}
-__device__ __forceinline__ void load_codes(uint32_t (&w)[2], const uint8_t* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
-               : "=r"(w[0]), "=r"(w[1])
-               : "l"(p));
-}
-__device__ __forceinline__ void load_codes(uint32_t (&w)[1], const uint8_t* p) {
-  asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
 // The 8 x 8 block of 16-bit values of a warp (lane: row lane / 4, columns
@@ -141,8 +161,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
+// CTAs on an SM, and stages of a ring: together about 190 KB.
+template <int NT>
+constexpr int kCtas = NT == 1 ? 4 : 3;
+template <int NT>
+constexpr int kStages = NT == 1 ? 3 : 4;
+template <int D, int NT>
+constexpr int smem_bytes() {
+  const int ring = kWarps * kStages<NT> * Geo<D>::kStage, merge = kWarps * 8 * NT * (D + 2) * 4;
+  return ring > merge ? ring : merge;
+}
+
 template <int D, int NT>  // NT: 8 query rows each
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     cache_attn_kernel(const __grid_constant__ CacheAttn p, bool whole_units) {
   constexpr int kMR = 8 * NT;
   constexpr int kG = Geo<D>::kGroups, kStep = Geo<D>::kStep, kTile = Geo<D>::kTile;
@@ -151,11 +182,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
   constexpr int kVW = D / 32;            // words of a V row that a lane takes
   constexpr int kKL = kKW < 4 ? kKW : 4; // words of one load
   constexpr int kVB = D / 8;             // bytes of a V row that a lane takes
-  __shared__ __align__(16) float merge[kWarps * kMR * (D + 2)];
+  using G = Geo<D>;
+  constexpr int kS = kStages<NT>;
+  extern __shared__ __align__(128) uint8_t smem[];  // the rings; then the warps' sums
+  float* merge = reinterpret_cast<float*>(smem);
   __shared__ long long scan[kWarps + 2];
   const CacheCall& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, cc = lane & 3;
+  const int kq = (quad >> 1) + 4 * (quad & 1);  // key of the lane's rows of S^T (and kq + 8)
 
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits without end
   Share sh;
@@ -187,62 +222,50 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     const bool any_dyn = k_head >= 0;  // a dynamic head in the group
     const int key_w = tile * kTile + warp * kStep;  // first key of this warp's step 0
 
-    // ---- codes: pages are looked up 32 groups ahead, one for each lane
-    int pages = -1;
-    uint32_t kw[kG][2][kKW], vw[kG][4][kVW];
-    float ks[kG], vs[kG];
-    int there[kG];  // keys of the group
-    auto group_key = [&](int s, int g) { return key_w + s * kTile + 16 * g; };
-    auto look_up = [&](int s) {  // the pages of steps s .. s + 32 / kG - 1
-      const int st = s + lane / kG, key = group_key(st, lane % kG);
-      pages = st < steps && key < ext ? page_at(c, b, key >> c.page_shift) : -1;
-    };
+    // ---- the ring: pages are looked up 32 groups ahead, one for each lane
+    const uint32_t ring = smem_u32(smem) + warp * kS * G::kStage;
     const int in_page = (1 << c.page_shift) - 1;
-    auto record = [&](int s, int g, int& n) {
-      const int page = __shfl_sync(~0u, pages, (s * kG + g) & 31);
-      const int key = group_key(s, g);
-      n = page < 0 || s >= steps ? 0 : min(16, ext - key);
-      return c.layer + (size_t)(n > 0 ? page : 0) * c.page_stride;
-    };
-    auto fetch_k = [&](int s) {
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        const uint8_t* rec = record(s, g, there[g]);
-        if (!any_dyn || there[g] == 0) continue;
-        const uint8_t* src =
-            rec + (((size_t)k_head << c.page_shift) + (group_key(s, g) & in_page) + quad) * D +
-            cc * 4 * kKL;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)  // keys quad and quad + 8
-#pragma unroll
-          for (int i = 0; i < kKW / kKL; ++i) {
-            uint32_t(&w)[kKL] = *reinterpret_cast<uint32_t(*)[kKL]>(kw[g][h] + kKL * i);
-            // keys behind the last one lie on the page as well
-            load_codes(w, src + h * 8 * D + i * 64);
-          }
-        ks[g] = __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + k_head);
-      }
-    };
-    auto fetch_v = [&](int s) {
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        int n;
-        const uint8_t* rec = record(s, g, n);
-        if (n == 0) continue;
-        const uint8_t* src =
-            rec + c.off_v + (((size_t)kv << c.page_shift) + (group_key(s, g) & in_page)) * D +
-            quad * kVB;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9
-          const int key = 2 * cc + (u & 1) + 8 * (u >> 1);
-          load_codes(vw[g][u], src + key * D);
+    int pages = -1;
+    auto group_key = [&](int s, int g) { return key_w + s * kTile + 16 * g; };
+    auto issue = [&](int s, uint32_t st) {
+      if (s < steps) {
+        if ((s * kG & 31) == 0) {  // the pages of steps s .. s + 32 / kG - 1
+          const int at_s = s + lane / kG, key = group_key(at_s, lane % kG);
+          pages = at_s < steps && key < ext ? page_at(c, b, key >> c.page_shift) : -1;
         }
-        vs[g] = __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + kv);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          const int page = __shfl_sync(~0u, pages, (s * kG + g) & 31);
+          const int key = group_key(s, g);
+          if (lane == 0)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + 2 * G::kCodes + 16 * g + 8),
+                         "r"(page < 0 ? 0 : min(16, ext - key))
+                         : "memory");
+          if (page < 0) continue;
+          // the 16 keys of a group are contiguous; those behind the last one lie
+          // on the page as well
+          const uint8_t* rec = c.layer + (size_t)page * c.page_stride;
+          const size_t in_rec = (size_t)(key & in_page) * D + lane * 16;
+          const uint8_t* src_v = rec + c.off_v + (((size_t)kv << c.page_shift) * D) + in_rec;
+          const uint8_t* src_k =
+              rec + (((size_t)(any_dyn ? k_head : 0) << c.page_shift) * D) + in_rec;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const int q = lane + 32 * i;
+            const uint32_t to = st + g * 16 * D + chunk_at<D>(q / (D / 16), q % (D / 16));
+            cp_async16(to + G::kCodes, src_v + i * 512, 16);
+            if (any_dyn) cp_async16(to, src_k + i * 512, 16);
+          }
+          if (lane == 0 && any_dyn)
+            cp_async4(st + 2 * G::kCodes + 16 * g, rec + c.off_ks + 4 * (size_t)k_head);
+          if (lane == 1)
+            cp_async4(st + 2 * G::kCodes + 16 * g + 4, rec + c.off_vs + 4 * (size_t)kv);
+        }
       }
+      cp_async_commit();
     };
-    look_up(0);
-    fetch_k(0);
-    fetch_v(0);
+#pragma unroll
+    for (int i = 0; i < kS - 1; ++i) issue(i, ring + i * G::kStage);
 
     // ---- the rows of this lane: 8 nt + 2c and the next
     int pos[NT][2], head[NT][2];
@@ -310,26 +333,26 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
       }
     }
 
-    // logits of the frozen rows for one step, fetched a step ahead
-    float pat[NT][2][2 * kG];
+    // alpha and rho of the frozen rows for one step, fetched a step ahead
+    float pa[NT][2][2 * kG], pr[NT][2][2 * kG];
     auto fetch_pattern = [&](int s) {
       if (!any_ice || s >= steps) return;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (ice[nt][i]) {
+        for (int i = 0; i < 2; ++i) {
+          const float* al = p.alpha + (size_t)head[nt][i] * p.T_pat;
+          const float* rh = p.rho + (size_t)head[nt][i] * p.T_pat;
 #pragma unroll
-            for (int u = 0; u < 2 * kG; ++u) {
-              const int j = group_key(s, u >> 1) + quad + 8 * (u & 1);
-              const int dist = pos[nt][i] - j;
-              float a = -CUDART_INF_F;
-              if (dist >= 0 && j < p.T_pat && dist < p.T_pat)
-                a = __ldg(p.alpha + (size_t)head[nt][i] * p.T_pat + j) +
-                    __ldg(p.rho + (size_t)head[nt][i] * p.T_pat + dist);
-              pat[nt][i][u] = a * kLog2e;
-            }
+          for (int u = 0; u < 2 * kG; ++u) {
+            const int j = group_key(s, u >> 1) + kq + 8 * (u & 1);
+            const int dist = pos[nt][i] - j;
+            const bool ok = ice[nt][i] && dist >= 0 && j < p.T_pat && dist < p.T_pat;
+            // (p.alpha and p.rho have an entry wherever a frozen row exists)
+            pa[nt][i][u] = ok ? __ldg(al + j) : -CUDART_INF_F;
+            pr[nt][i][u] = ok ? __ldg(rh + dist) : 0.f;
           }
+        }
     };
     fetch_pattern(0);
 
@@ -349,36 +372,48 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     }
     bool v_nan = false;  // a NaN in V at a key that not every row sees
 
+    uint32_t st = ring, st_next = ring + (kS - 1) * G::kStage;  // stages of steps s and s + kS - 1
 #pragma unroll 1
     for (int s = 0; s < steps; ++s) {
-      // S^T of the step, [group][row pair][key quad: 2 rows | key quad + 8: 2 rows]
+      cp_async_wait<kS - 2>();
+      __syncwarp();
+      // S^T of the step, [group][row pair][key kq: 2 rows | key kq + 8: 2 rows]
       float sc[kG][NT][4];
       int n[kG];
-      float kscale[kG];
+      float ks[kG], vs[kG];
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        n[g] = there[g];
-        kscale[g] = ks[g];
+        const float4 mt = lds_f32x4(st + 2 * G::kCodes + 16 * g);
+        ks[g] = mt.x;
+        vs[g] = mt.y;
+        n[g] = __float_as_int(mt.z);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int u = 0; u < 4; ++u) sc[g][nt][u] = 0.f;
         if (any_dyn && n[g] > 0) {
+          uint32_t kw[2][kKW];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kKW / kKL; ++i) {
+              uint32_t(&w)[kKL] = *reinterpret_cast<uint32_t(*)[kKL]>(kw[h] + kKL * i);
+              const uint32_t a = st + g * 16 * D +
+                                 (D == 32 ? chunk_at<D>(kq + 8 * h, cc >> 1) + (cc & 1) * 8
+                                          : chunk_at<D>(kq + 8 * h, cc + 4 * i));
+              lds_words(w, a);
+            }
 #pragma unroll
           for (int i = 0; i < kKS; ++i) {
             uint32_t a[4];
-            e4m3x4_f16x4(kw[g][0][i], a[0], a[2]);
-            e4m3x4_f16x4(kw[g][1][i], a[1], a[3]);
+            e4m3x4_f16x4(kw[0][i], a[0], a[2]);
+            e4m3x4_f16x4(kw[1][i], a[1], a[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_f16_16816(sc[g][nt], a, qf[nt][i][0], qf[nt][i][1]);
           }
         }
       }
-      // the lookup of the next pages lies between the last use of the old ones
-      // (V of this step was fetched) and K of the next step
-      if (((s + 1) * kG & 31) == 0) look_up(s + 1);
-      fetch_k(s + 1);
 
       // y = x log2(e) + log2(s_v); keys that a row does not see: -inf
       bool grow = false;
@@ -394,10 +429,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int i = u & 1, k = quad + 8 * (u >> 1);
+            const int i = u & 1, k = kq + 8 * (u >> 1);
             float& y = sc[g][nt][u];
-            y = fmaf(y, fac[nt][i] * kscale[g], lv);
-            if (any_ice && ice[nt][i]) y = pat[nt][i][2 * g + (u >> 1)] + lv;
+            y = fmaf(y, fac[nt][i] * ks[g], lv);
+            if (any_ice && ice[nt][i])
+              y = fmaf(pa[nt][i][2 * g + (u >> 1)] + pr[nt][i][2 * g + (u >> 1)], kLog2e, lv);
             if (edge && (k >= n[g] || key0 + k > pos[nt][i])) y = -CUDART_INF_F;
             // the maximum moves only when it would grow by more than 2^8:
             // weights up to 2^8 fit f16 as well
@@ -444,15 +480,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
             pf[nt][i] = transpose8(pack_f16x2(w[2 * i], w[2 * i + 1]));
           }
         }
-        // V^T: a lane's words hold 4 components of one key; pairs of keys side by side
+        // V^T: a lane's words hold 4 components of one of the keys c, c + 4, c + 8,
+        // c + 12; pairs of keys side by side
+        uint32_t vw[4][kVW];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          lds_words(vw[u], st + G::kCodes + g * 16 * D +
+                               chunk_at<D>(cc + 4 * u, quad * kVB >> 4) + (quad * kVB & 15));
 #pragma unroll
         for (int i = 0; i < kVW; ++i) {
-          uint32_t f[2][4];  // [keys 2c, 2c + 1 | 2c + 8, 2c + 9][component of the word]
+          uint32_t f[2][4];  // [keys c, c + 4 | c + 8, c + 12][component of the word]
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            e4m3x4_f16x4(__byte_perm(vw[g][2 * h][i], vw[g][2 * h + 1][i], 0x5140), f[h][0],
+            e4m3x4_f16x4(__byte_perm(vw[2 * h][i], vw[2 * h + 1][i], 0x5140), f[h][0],
                          f[h][1]);
-            e4m3x4_f16x4(__byte_perm(vw[g][2 * h][i], vw[g][2 * h + 1][i], 0x7362), f[h][2],
+            e4m3x4_f16x4(__byte_perm(vw[2 * h][i], vw[2 * h + 1][i], 0x7362), f[h][2],
                          f[h][3]);
           }
           if (edge) {  // 0 * NaN would reach rows that do not see the key
@@ -475,9 +517,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
           }
         }
       }
-      fetch_v(s + 1);
       fetch_pattern(s + 1);
+      __syncwarp();
+      issue(s + kS - 1, st_next);
+      st_next = st;
+      st = st + G::kStage == ring + kS * G::kStage ? ring : st + G::kStage;
     }
+    cp_async_wait<0>();
 
     if (__any_sync(~0u, v_nan)) {
       // rows that do see a key whose V holds NaN take it
@@ -500,6 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         }
     }
 
+    __syncthreads();  // every warp has read its ring
     // ---- join the warps: [warp][row][D] sums, then [warp][row][2] of (m, l)
     float* mm = merge + kWarps * kMR * D;
 #pragma unroll
@@ -615,16 +662,19 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   }
 }
 
-int n_ctas(int nt, int n_sms) { return n_sms * (nt == 1 ? 4 : 3); }
+int n_ctas(int nt, int n_sms) { return n_sms * (nt == 1 ? kCtas<1> : kCtas<2>); }
 
 template <int D, int NT>
 cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   const bool whole = (long long)p.c.max_pages << p.c.page_shift <= kWholeKeys;
   const int grid = whole ? p.c.n_seqs * p.c.H_kv : n_ctas(NT, n_sms);
+  cudaError_t e = set_max_dynamic_smem(
+      reinterpret_cast<const void*>(cache_attn_kernel<D, NT>), smem_bytes<D, NT>());
+  if (e != cudaSuccess) return e;
   trace_begin(s);
-  cache_attn_kernel<D, NT><<<grid, kWarps * 32, 0, s>>>(p, whole);
+  cache_attn_kernel<D, NT><<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, whole);
   trace_end(s, "cache_attn");
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
   // launched while the first kernel runs; waits for its end before it reads
   cudaLaunchAttribute attr[1];

@@ -24,6 +24,7 @@ saf_status check_cache(const saf_cache_dims* d) {
   // the kernels step past the last key by less than a tile
   if ((long long)d->max_pages * d->page_size > (1ll << 31) - 1024) return SAF_ERR_UNSUPPORTED;
   if (d->page_stride % 16 != 0) return SAF_ERR_INVALID_ARG;
+  if (d->page_stride >= (1ull << 32)) return SAF_ERR_UNSUPPORTED;
   return SAF_OK;
 }
 

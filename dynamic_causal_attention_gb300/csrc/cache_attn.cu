@@ -59,7 +59,8 @@ struct Geo {
   // the number of keys
   static constexpr int kCodes = kStep * D;
   static constexpr int kMeta = 16 * kGroups;
-  static constexpr int kStage = 2 * kCodes + (kMeta + 127) / 128 * 128;
+  static constexpr int kStage = 2 * kCodes + 128;
+  static_assert(kMeta <= 64, "half a stage holds V codes and the scales");
 };
 
 // Where 16-byte chunk `ch` of key `key` of a group lies.  A fragment's reads
@@ -192,6 +193,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
   const int quad = lane >> 2, cc = lane & 3;
   const int kq = (quad >> 1) + 4 * (quad & 1);  // key of the lane's rows of S^T (and kq + 8)
 
+  // the joining kernel may be set up meanwhile; it waits for this one's end
+  if (!whole_units) asm volatile("griddepcontrol.launch_dependents;");
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits without end
   Share sh;
   if (whole_units) {
@@ -222,11 +225,51 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     const bool any_dyn = k_head >= 0;  // a dynamic head in the group
     const int key_w = tile * kTile + warp * kStep;  // first key of this warp's step 0
 
-    // ---- the ring: pages are looked up 32 groups ahead, one for each lane
+    // ---- Q: the lane's components 16 c .. 16 c + 15 (and + 64; 8 c .. for d_h = 32)
+    // of row 8 nt + quad, on their way while the ring starts
+    constexpr int kQW = D >= 64 ? 2 : 1;  // 16-byte words of a block of 64 components
+    constexpr int kQB = D == 128 ? 2 : 1;
+    uint4 qw[NT][kQB][kQW];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + quad;
+      const uint16_t* qrow = nullptr;
+      if (r < n_rows && any_dyn) {
+        const int t = r / c.group, h = kv * c.group + r - t * c.group;
+        if (!c.is_static[h]) qrow = p.Q + (((size_t)b * c.H + h) * c.n_q + t) * D;
+      }
+#pragma unroll
+      for (int blk = 0; blk < kQB; ++blk)
+#pragma unroll
+        for (int u = 0; u < kQW; ++u) {
+          qw[nt][blk][u] = make_uint4(0, 0, 0, 0);
+          if (qrow)
+            qw[nt][blk][u] =
+                __ldg(reinterpret_cast<const uint4*>(qrow + 64 * blk + 8 * kQW * cc + 8 * u));
+        }
+    }
+
+    // ---- the ring: pages are looked up 32 groups ahead, one for each lane.
+    // Without K a stage is half as long and the ring has twice as many, so that as
+    // many bytes are in flight.
     const uint32_t ring = smem_u32(smem) + warp * kS * G::kStage;
+    const uint32_t stage = any_dyn ? G::kStage : G::kStage / 2;
+    const uint32_t off_v = any_dyn ? G::kCodes : 0, off_m = off_v + G::kCodes;
+    const int ahead = any_dyn ? kS - 1 : 2 * kS - 1;  // steps in flight
     const int in_page = (1 << c.page_shift) - 1;
     int pages = -1;
     auto group_key = [&](int s, int g) { return key_w + s * kTile + 16 * g; };
+    // what does not change from step to step: the lane's chunks in a stage (the
+    // third and fourth of d_h = 128 lie 8 keys = 1024 bytes behind the first two),
+    // its places in the record, and where its scale comes from (lane 0: K, 1: V)
+    constexpr int kChunks = D / 32;  // of a lane in 16 keys of K or V
+    const uint32_t to0 = chunk_at<D>(lane / (D / 16), lane % (D / 16));
+    const uint32_t to1 = chunk_at<D>(lane / (D / 16) + 512 / D, lane % (D / 16));
+    const uint8_t* lane_v = c.layer + c.off_v + (((size_t)kv << c.page_shift) * D) + lane * 16;
+    const uint8_t* lane_k = c.layer + (((size_t)(any_dyn ? k_head : 0) << c.page_shift) * D) + lane * 16;
+    const uint8_t* lane_m =
+        c.layer + (lane == 0 && any_dyn ? c.off_ks + 4 * (size_t)k_head : c.off_vs + 4 * (size_t)kv);
+    const uint32_t page_stride = (uint32_t)c.page_stride;  // below 2^32: checked on the host
     auto issue = [&](int s, uint32_t st) {
       if (s < steps) {
         if ((s * kG & 31) == 0) {  // the pages of steps s .. s + 32 / kG - 1
@@ -237,40 +280,38 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
         for (int g = 0; g < kG; ++g) {
           const int page = __shfl_sync(~0u, pages, (s * kG + g) & 31);
           const int key = group_key(s, g);
-          if (lane == 0)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + 2 * G::kCodes + 16 * g + 8),
+          const uint32_t meta = st + off_m + 16 * g;
+          if (lane == 2)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(meta + 8),
                          "r"(page < 0 ? 0 : min(16, ext - key))
                          : "memory");
           if (page < 0) continue;
           // the 16 keys of a group are contiguous; those behind the last one lie
           // on the page as well
-          const uint8_t* rec = c.layer + (size_t)page * c.page_stride;
-          const size_t in_rec = (size_t)(key & in_page) * D + lane * 16;
-          const uint8_t* src_v = rec + c.off_v + (((size_t)kv << c.page_shift) * D) + in_rec;
-          const uint8_t* src_k =
-              rec + (((size_t)(any_dyn ? k_head : 0) << c.page_shift) * D) + in_rec;
+          const uint64_t rec = (uint64_t)(uint32_t)page * page_stride;
+          const uint64_t in_rec = rec + (uint32_t)((key & in_page) * D);
+          const uint32_t to = st + g * 16 * D;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const int q = lane + 32 * i;
-            const uint32_t to = st + g * 16 * D + chunk_at<D>(q / (D / 16), q % (D / 16));
-            cp_async16(to + G::kCodes, src_v + i * 512, 16);
-            if (any_dyn) cp_async16(to, src_k + i * 512, 16);
+          for (int i = 0; i < kChunks; ++i)
+            cp_async16(to + off_v + (i & 1 ? to1 : to0) + (i >> 1) * 1024, lane_v + in_rec + i * 512,
+                       16);
+          if (any_dyn) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+              cp_async16(to + (i & 1 ? to1 : to0) + (i >> 1) * 1024, lane_k + in_rec + i * 512, 16);
           }
-          if (lane == 0 && any_dyn)
-            cp_async4(st + 2 * G::kCodes + 16 * g, rec + c.off_ks + 4 * (size_t)k_head);
-          if (lane == 1)
-            cp_async4(st + 2 * G::kCodes + 16 * g + 4, rec + c.off_vs + 4 * (size_t)kv);
+          if (lane < 2) cp_async4(meta + 4 * lane, lane_m + rec);
         }
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kS - 1; ++i) issue(i, ring + i * G::kStage);
+    for (int i = 0; i < ahead; ++i) issue(i, ring + i * stage);
 
     // ---- the rows of this lane: 8 nt + 2c and the next
     int pos[NT][2], head[NT][2];
     bool ice[NT][2];
-    bool any_ice = false;
+    const bool odd_rows = n_rows > 1;  // a single row leaves every lane's second one empty
+    unsigned frozen = 0;               // bit 2 nt + i: row i of pair nt is frozen in some lane
     const int pos_lo = rows.base;  // the row that sees least
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -282,38 +323,28 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
         head[nt][i] = kv * c.group + hh;
         pos[nt][i] = live ? rows.base + t : -1;
         ice[nt][i] = live && c.is_static[head[nt][i]];
-        any_ice |= ice[nt][i];
+        frozen |= (__any_sync(~0u, ice[nt][i]) ? 1u : 0u) << (2 * nt + i);
       }
 
-    // ---- Q^T fragments: lane takes components 16 c .. 16 c + 15 (and + 64; 8 c ..
-    // for d_h = 32) of row 8 nt + quad
+    // ---- Q^T fragments
     uint32_t qf[NT][kKS][2];
     float fac[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = 8 * nt + quad;
-      const uint16_t* qrow = nullptr;
-      if (r < n_rows && any_dyn) {
-        const int t = r / c.group, h = kv * c.group + r - t * c.group;
-        if (!c.is_static[h]) qrow = p.Q + (((size_t)b * c.H + h) * c.n_q + t) * D;
-      }
       float x[D / 4];
       float amax = 0.f;
 #pragma unroll
-      for (int blk = 0; blk < (D + 63) / 64; ++blk) {
-        constexpr int kW = D >= 64 ? 16 : 8;  // components of a lane in a block
+      for (int blk = 0; blk < kQB; ++blk)
 #pragma unroll
-        for (int u = 0; u < kW / 8; ++u) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (qrow) w = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * blk + kW * cc + 8 * u));
+        for (int u = 0; u < kQW; ++u) {
+          const uint4 w = qw[nt][blk][u];
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            x[blk * kW + 8 * u + 2 * v] = __uint_as_float(ww[v] << 16);
-            x[blk * kW + 8 * u + 2 * v + 1] = __uint_as_float(ww[v] & 0xffff0000u);
+            x[8 * (kQW * blk + u) + 2 * v] = __uint_as_float(ww[v] << 16);
+            x[8 * (kQW * blk + u) + 2 * v + 1] = __uint_as_float(ww[v] & 0xffff0000u);
           }
         }
-      }
 #pragma unroll
       for (int v = 0; v < D / 4; ++v) amax = fmaxf(amax, fabsf(x[v]));
       amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
@@ -333,26 +364,36 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       }
     }
 
-    // alpha and rho of the frozen rows for one step, fetched a step ahead
+    // alpha and rho of the frozen rows for one step, fetched a step ahead.  Keys
+    // [lo, lo + len) have both, counted from the lane's first key.
     float pa[NT][2][2 * kG], pr[NT][2][2 * kG];
+    const float *al[NT][2], *rh[NT][2];
+    int lo[NT][2], len[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int first = key_w + kq, x = pos[nt][i];
+        const int j0 = max(0, x - p.T_pat + 1), j1 = min(x + 1, p.T_pat);
+        al[nt][i] = p.alpha + (size_t)head[nt][i] * p.T_pat + first;
+        rh[nt][i] = p.rho + (size_t)head[nt][i] * p.T_pat + (x - first);
+        lo[nt][i] = j0 - first;
+        len[nt][i] = ice[nt][i] ? max(0, j1 - j0) : 0;
+      }
     auto fetch_pattern = [&](int s) {
-      if (!any_ice || s >= steps) return;
+      if (frozen == 0 || s >= steps) return;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float* al = p.alpha + (size_t)head[nt][i] * p.T_pat;
-          const float* rh = p.rho + (size_t)head[nt][i] * p.T_pat;
+        for (int i = 0; i < 2; ++i)
+          if (frozen >> (2 * nt + i) & 1)
 #pragma unroll
           for (int u = 0; u < 2 * kG; ++u) {
-            const int j = group_key(s, u >> 1) + kq + 8 * (u & 1);
-            const int dist = pos[nt][i] - j;
-            const bool ok = ice[nt][i] && dist >= 0 && j < p.T_pat && dist < p.T_pat;
-            // (p.alpha and p.rho have an entry wherever a frozen row exists)
-            pa[nt][i][u] = ok ? __ldg(al + j) : -CUDART_INF_F;
-            pr[nt][i][u] = ok ? __ldg(rh + dist) : 0.f;
+            const int j = s * kTile + 8 * u;  // 16 (u / 2) + 8 (u % 2)
+            const bool ok = (unsigned)(j - lo[nt][i]) < (unsigned)len[nt][i];
+            pa[nt][i][u] = ok ? __ldg(al[nt][i] + j) : -CUDART_INF_F;
+            pr[nt][i][u] = ok ? __ldg(rh[nt][i] - j) : 0.f;
           }
-        }
     };
     fetch_pattern(0);
 
@@ -372,10 +413,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     }
     bool v_nan = false;  // a NaN in V at a key that not every row sees
 
-    uint32_t st = ring, st_next = ring + (kS - 1) * G::kStage;  // stages of steps s and s + kS - 1
+    uint32_t st = ring, st_next = ring + ahead * stage;  // stages of steps s and s + ahead
 #pragma unroll 1
     for (int s = 0; s < steps; ++s) {
-      cp_async_wait<kS - 2>();
+      if (any_dyn)
+        cp_async_wait<kS - 2>();
+      else
+        cp_async_wait<2 * kS - 2>();
       __syncwarp();
       // S^T of the step, [group][row pair][key kq: 2 rows | key kq + 8: 2 rows]
       float sc[kG][NT][4];
@@ -383,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       float ks[kG], vs[kG];
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        const float4 mt = lds_f32x4(st + 2 * G::kCodes + 16 * g);
+        const float4 mt = lds_f32x4(st + off_m + 16 * g);
         ks[g] = mt.x;
         vs[g] = mt.y;
         n[g] = __float_as_int(mt.z);
@@ -422,8 +466,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       for (int g = 0; g < kG; ++g) {
         if (n[g] == 0) continue;
         const int key0 = group_key(s, g);
-        const float lv = __log2f(vs[g]);
-        inv[g] = __fdividef(1.f, vs[g]);
+        const float lv = fast_log2(vs[g]);
+        inv[g] = fast_rcp(vs[g]);
         const bool edge = n[g] < 16 || key0 + 15 > pos_lo;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -431,8 +475,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
           for (int u = 0; u < 4; ++u) {
             const int i = u & 1, k = kq + 8 * (u >> 1);
             float& y = sc[g][nt][u];
+            if (i == 1 && !odd_rows) {
+              y = -CUDART_INF_F;
+              continue;
+            }
             y = fmaf(y, fac[nt][i] * ks[g], lv);
-            if (any_ice && ice[nt][i])
+            if ((frozen >> (2 * nt + i) & 1) && ice[nt][i])
               y = fmaf(pa[nt][i][2 * g + (u >> 1)] + pr[nt][i][2 * g + (u >> 1)], kLog2e, lv);
             if (edge && (k >= n[g] || key0 + k > pos[nt][i])) y = -CUDART_INF_F;
             // the maximum moves only when it would grow by more than 2^8:
@@ -472,7 +520,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const float base = m[nt][u & 1] == -CUDART_INF_F ? 0.f : m[nt][u & 1];
-            w[u] = fast_exp2(sc[g][nt][u] - base);
+            w[u] = (u & 1) && !odd_rows ? 0.f : fast_exp2(sc[g][nt][u] - base);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -485,7 +533,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
         uint32_t vw[4][kVW];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          lds_words(vw[u], st + G::kCodes + g * 16 * D +
+          lds_words(vw[u], st + off_v + g * 16 * D +
                                chunk_at<D>(cc + 4 * u, quad * kVB >> 4) + (quad * kVB & 15));
 #pragma unroll
         for (int i = 0; i < kVW; ++i) {
@@ -519,9 +567,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       }
       fetch_pattern(s + 1);
       __syncwarp();
-      issue(s + kS - 1, st_next);
+      issue(s + ahead, st_next);
       st_next = st;
-      st = st + G::kStage == ring + kS * G::kStage ? ring : st + G::kStage;
+      st += stage;
+      if (st == ring + (ahead + 1) * stage) st = ring;
     }
     cp_async_wait<0>();
 
@@ -638,20 +687,40 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     auto ml = [&](int part) {
       return *reinterpret_cast<const float2*>(p.ml + ((size_t)part * kMR + r) * 2);
     };
-    float mx = ml(first).x, sum = 0.f;
-    for (int k = blockIdx.x + 1; k <= last; ++k) mx = fmaxf(mx, ml(2 * k).x);
+    // parts 0 .. n - 1, in the order of the CTAs; eight at a time are in flight
+    const int n = last - blockIdx.x + 1;
+    auto part = [&](int k) { return k == 0 ? first : 2 * ((int)blockIdx.x + k); };
+    float mx = -CUDART_INF_F, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = blockIdx.x; k <= last; ++k) {
-      const int part = k == (int)blockIdx.x ? first : 2 * k;
-      const float2 w = ml(part);
-      const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(w.x - mx);
-      sum = fmaf(f, w.y, sum);
-      const float4 x =
-          *reinterpret_cast<const float4*>(p.acc + ((size_t)part * kMR + r) * D + d);
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float2 w[8];
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < n) {
+          w[k] = ml(part(k0 + k));
+          x[k] = *reinterpret_cast<const float4*>(p.acc +
+                                                  ((size_t)part(k0 + k) * kMR + r) * D + d);
+        }
+      float top = mx;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < n) top = fmaxf(top, w[k].x);
+      if (top == -CUDART_INF_F) continue;  // nothing of weight yet
+      const float f0 = fast_exp2(mx - top);
+      mx = top;
+      sum *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < n) {
+          const float f = fast_exp2(w[k].x - mx);
+          sum = fmaf(f, w[k].y, sum);
+          o.x = fmaf(f, x[k].x, o.x);
+          o.y = fmaf(f, x[k].y, o.y);
+          o.z = fmaf(f, x[k].z, o.z);
+          o.w = fmaf(f, x[k].w, o.w);
+        }
     }
     const int t = r / c.group, h = kv * c.group + r - t * c.group;
     const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
@@ -681,7 +750,7 @@ cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 2);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = attr;

@@ -316,7 +316,8 @@ typedef struct saf_cache_dims {
   int H;              /* query heads, 1..256                               */
   int H_kv;           /* K/V heads: a divisor of H                         */
   int d_h;            /* head dimension: 32, 64 or 128                     */
-  size_t page_stride; /* bytes from one page to the next, a multiple of 16 */
+  size_t page_stride; /* bytes from one page to the next: a multiple of 16, *
+                       * below 2^32                                        */
 } saf_cache_dims;
 
 typedef struct saf_cache_layout {
@@ -379,7 +380,7 @@ SAF_API size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q
  *   alpha, rho  fp32 [H, T_pat]; only rows of frozen heads are read.  Keys and
  *               distances at or behind T_pat count as -inf.
  *   n_new, seq_len, page_table: as in saf_cache_append.  Scales must be
- *               positive and finite.
+ *               positive normal numbers.
  *   out         bf16 [n_seqs, H, n_q, d_h]; lse fp32 [n_seqs, H, n_q] or NULL:
  *               log sum_j exp(.).  A row that sees no key, or none of nonzero
  *               weight, gets out = 0 and lse = -inf.  Rows t >= n_new are left

@@ -89,8 +89,9 @@ saf_status make_call(const saf_cache_dims& d, const uint8_t* head_is_static, con
 
 // The scratch of an attention call and the kernel that takes it: up to 16 rows
 // for each slot and K/V head go to the kernel made for single tokens.
+constexpr int kFewRows = 16;
 bool many_rows(const saf_cache_dims& d, int n_q) {
-  return (long long)n_q * (d.H / d.H_kv) > 16;
+  return (long long)n_q * (d.H / d.H_kv) > kFewRows;
 }
 CacheAttnWs attn_ws(const saf_cache_dims& d, int n_q) {
   return many_rows(d, n_q) ? cache_chunk_ws(d.d_h, sm_count()) : cache_attn_ws(d.d_h, sm_count());

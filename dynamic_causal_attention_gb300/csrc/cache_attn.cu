@@ -11,7 +11,7 @@
 // softmax is sum_j p_j / s_v.  So a weight is rounded to f16 relative to the
 // largest contribution to `out`, whatever the scales of the blocks.
 //
-// This file: up to 16 query rows for each slot and K/V head (single tokens and
+// This file: few query rows for each slot and K/V head (single tokens and
 // short drafts; more rows go to cache_chunk.cu).  Such calls are bound by the
 // bytes of the codes, so the kernel is built around keeping many of them in
 // flight for few instructions: each warp has a ring of its own in shared
@@ -40,8 +40,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 
 // ------------------------------------------------------------ work split
-// A unit is (slot b, K/V head): the slot's n_new * group query rows (row
-// r = t * group + h) against all its keys, in tiles of kTile keys.  All tiles of
+// A unit is (slot b, K/V head, row tile): up to 8 NT of the slot's n_new * group
+// query rows (row r = t * group + h) against all its keys, in tiles of kTile
+// keys.  The row tiles of a head lie side by side, so that their codes come from
+// L2 after the first.  All tiles of
 // all units, in that order, are cut into equal shares, one for each CTA; a
 // unit that is cut leaves partial sums, joined by a second kernel in the order
 // of the CTAs.  Nothing depends on timing.  Where no slot can have more than
@@ -97,14 +99,14 @@ struct Share {
 // gives the runs' first tiles, and the thread whose run holds the share's
 // first tile walks it.
 template <int TILE>
-__device__ Share find_share(const CacheCall& c, long long* scan /* [kWarps + 2] */) {
+__device__ Share find_share(const CacheCall& c, int per_slot, long long* scan /* [kWarps + 2] */) {
   constexpr int n = kWarps * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (c.n_seqs + n - 1) / n;
   const int b0 = min(tid * per, c.n_seqs), b1 = min(b0 + per, c.n_seqs);
   long long sum = 0;
   for (int b = b0; b < b1; ++b) sum += slot_tiles<TILE>(c, b);
-  sum *= c.H_kv;
+  sum *= per_slot;
   long long upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -128,7 +130,7 @@ __device__ Share find_share(const CacheCall& c, long long* scan /* [kWarps + 2] 
     long long at = mine;
     int b = b0;
     for (; b < b1 - 1; ++b) {
-      const long long t = (long long)slot_tiles<TILE>(c, b) * c.H_kv;
+      const long long t = (long long)slot_tiles<TILE>(c, b) * per_slot;
       if (s.begin < at + t) break;
       at += t;
     }
@@ -164,9 +166,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 // CTAs on an SM, and stages of a ring: together about 190 KB.
 template <int NT>
-constexpr int kCtas = NT == 1 ? 4 : 3;
+constexpr int kCtas = NT == 1 ? 4 : 2;
 template <int NT>
-constexpr int kStages = NT == 1 ? 3 : 4;
+constexpr int kStages = NT == 1 ? 3 : 6;
 template <int D, int NT>
 constexpr int smem_bytes() {
   const int ring = kWarps * kStages<NT> * Geo<D>::kStage, merge = kWarps * 8 * NT * (D + 2) * 4;
@@ -175,7 +177,7 @@ constexpr int smem_bytes() {
 
 template <int D, int NT>  // NT: 8 query rows each
 __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
-    cache_attn_kernel(const __grid_constant__ CacheAttn p, bool whole_units) {
+    cache_attn_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool whole_units) {
   constexpr int kMR = 8 * NT;
   constexpr int kG = Geo<D>::kGroups, kStep = Geo<D>::kStep, kTile = Geo<D>::kTile;
   constexpr int kKS = D / 16;            // steps of 16 along d
@@ -196,31 +198,33 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
   // the joining kernel may be set up meanwhile; it waits for this one's end
   if (!whole_units) asm volatile("griddepcontrol.launch_dependents;");
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits without end
+  const int per_slot = c.H_kv * row_tiles;  // units of a slot
   Share sh;
   if (whole_units) {
-    sh.b = blockIdx.x / c.H_kv;
+    sh.b = blockIdx.x / per_slot;
     const int n = slot_tiles<kTile>(c, sh.b);
     if (n == 0) return;
-    sh.in_slot = (long long)n * (blockIdx.x - sh.b * c.H_kv);
+    sh.in_slot = (long long)n * (blockIdx.x - sh.b * per_slot);
     sh.begin = 0;
     sh.end = sh.size = n;
   } else {
-    sh = find_share<kTile>(c, scan);
+    sh = find_share<kTile>(c, per_slot, scan);
     if (threadIdx.x == 0) p.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (sh.begin >= sh.end) return;
   }
 
   int b = sh.b, ut = slot_tiles<kTile>(c, b);
   Rows rows = slot_rows(c, b);
-  int kv = (int)(sh.in_slot / ut), tile = (int)(sh.in_slot % ut);
+  int unit = (int)(sh.in_slot / ut), tile = (int)(sh.in_slot % ut);
   long long at = sh.begin;
 
   while (true) {
-    // ---- this segment: tiles [tile, tile_end) of unit (b, kv)
+    // ---- this segment: tiles [tile, tile_end) of the slot's unit (kv, rows r0 ..)
+    const int kv = unit / row_tiles, r0 = (unit - kv * row_tiles) * kMR;
     const int tile_end = (int)min((long long)ut, tile + (sh.end - at));
     const int ext = rows.cap;
-    const int n_rows = rows.n_new * c.group;
-    const int steps = tile_end - tile;
+    const int n_rows = min(kMR, rows.n_new * c.group - r0);  // none: a short slot's last tiles
+    const int steps = n_rows > 0 ? tile_end - tile : 0;
     const int k_head = c.k_of[kv];
     const bool any_dyn = k_head >= 0;  // a dynamic head in the group
     const int key_w = tile * kTile + warp * kStep;  // first key of this warp's step 0
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       const int r = 8 * nt + quad;
       const uint16_t* qrow = nullptr;
       if (r < n_rows && any_dyn) {
-        const int t = r / c.group, h = kv * c.group + r - t * c.group;
+        const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
         if (!c.is_static[h]) qrow = p.Q + (((size_t)b * c.H + h) * c.n_q + t) * D;
       }
 #pragma unroll
@@ -312,14 +316,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     bool ice[NT][2];
     const bool odd_rows = n_rows > 1;  // a single row leaves every lane's second one empty
     unsigned frozen = 0;               // bit 2 nt + i: row i of pair nt is frozen in some lane
-    const int pos_lo = rows.base;  // the row that sees least
+    const int pos_lo = rows.base + r0 / c.group;  // the row that sees least
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * nt + 2 * cc + i;
         const bool live = r < n_rows;
-        const int t = live ? r / c.group : 0, hh = live ? r - t * c.group : 0;
+        const int t = live ? (r0 + r) / c.group : 0, hh = live ? r0 + r - t * c.group : 0;
         head[nt][i] = kv * c.group + hh;
         pos[nt][i] = live ? rows.base + t : -1;
         ice[nt][i] = live && c.is_static[head[nt][i]];
@@ -638,7 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
         o.w = fmaf(f, x.w, o.w);
       }
       if (whole) {
-        const int t = r / c.group, h = kv * c.group + r - t * c.group;
+        const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
         const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: 0
         *reinterpret_cast<uint2*>(p.out + row * D + d) =
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     if (!whole && tile == 0 && threadIdx.x == 0) {
       // the unit begins here and ends in CTA `last`
       const int last = (int)((at + ut - 1) / sh.size);
-      p.join[blockIdx.x] = make_int4(b, kv, last, at == sh.begin ? 0 : 1);
+      p.join[blockIdx.x] = make_int4(b, unit, last, at == sh.begin ? 0 : 1);
     }
 
     // ---- the next unit
@@ -661,8 +665,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     if (at >= sh.end) break;
     __syncthreads();  // the merge buffer is free again
     tile = 0;
-    if (++kv == c.H_kv) {
-      kv = 0;
+    if (++unit == per_slot) {
+      unit = 0;
       do {
         ut = slot_tiles<kTile>(c, ++b);
       } while (ut == 0);
@@ -674,14 +678,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
 // Joins the parts of a unit that was cut: CTA x takes the unit that CTA x of
 // the first kernel left to its successors; y splits the rows.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttn p) {
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttn p, int row_tiles) {
   constexpr int kMR = 8 * NT;
   const CacheCall& c = p.c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 u = p.join[blockIdx.x];
   if (u.x < 0) return;
-  const int b = u.x, kv = u.y, last = u.z, first = 2 * blockIdx.x + u.w;
-  const int n_rows = slot_rows(c, b).n_new * c.group;
+  const int b = u.x, kv = u.y / row_tiles, r0 = (u.y - kv * row_tiles) * kMR;
+  const int last = u.z, first = 2 * blockIdx.x + u.w;
+  const int n_rows = min(kMR, slot_rows(c, b).n_new * c.group - r0);
   for (int i = blockIdx.y * 128 + threadIdx.x; i < n_rows * (D / 4); i += gridDim.y * 128) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     auto ml = [&](int part) {
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
           o.w = fmaf(f, x[k].w, o.w);
         }
     }
-    const int t = r / c.group, h = kv * c.group + r - t * c.group;
+    const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
     const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2*>(p.out + row * D + d) =
@@ -736,12 +741,13 @@ int n_ctas(int nt, int n_sms) { return n_sms * (nt == 1 ? kCtas<1> : kCtas<2>); 
 template <int D, int NT>
 cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   const bool whole = (long long)p.c.max_pages << p.c.page_shift <= kWholeKeys;
-  const int grid = whole ? p.c.n_seqs * p.c.H_kv : n_ctas(NT, n_sms);
+  const int row_tiles = (p.c.n_q * p.c.group + 8 * NT - 1) / (8 * NT);
+  const int grid = whole ? p.c.n_seqs * p.c.H_kv * row_tiles : n_ctas(NT, n_sms);
   cudaError_t e = set_max_dynamic_smem(
       reinterpret_cast<const void*>(cache_attn_kernel<D, NT>), smem_bytes<D, NT>());
   if (e != cudaSuccess) return e;
   trace_begin(s);
-  cache_attn_kernel<D, NT><<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, whole);
+  cache_attn_kernel<D, NT><<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, row_tiles, whole);
   trace_end(s, "cache_attn");
   e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
@@ -756,7 +762,7 @@ cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   trace_begin(s);
-  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, p);
+  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, p, row_tiles);
   trace_end(s, "cache_join");
   return e != cudaSuccess ? e : cudaGetLastError();
 }

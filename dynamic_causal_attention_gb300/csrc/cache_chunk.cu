@@ -31,10 +31,13 @@
 // of a tile in its place would take six times the arithmetic of converting V's
 // 128 x d_h codes.
 //
-// TMEM: S of the two row tiles (128 columns each), then their O.  P, as packed
-// f16, overwrites the first half of its own S, so the next S of a row tile
-// waits for the product that reads P; the other row tile's products and
-// softmax run meanwhile.  A frozen row writes its logits into S itself.
+// TMEM: S of the two row tiles (128 columns each), then their O.  A tile's
+// keys are taken in two halves of 64: S, softmax and P V of one half run while
+// the other half's do, and P, as packed f16, overwrites the first columns of
+// its own half of S, so the next S of a half waits only for the product that
+// reads that half's P.  (With whole tiles the chain S, softmax, P V of a row tile
+// was what a tile cost, about 4500 cycles; its links are listed in the table of
+// the measurements.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -59,8 +62,6 @@ enum : int {
   kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree,
   kSiteRaw, kSiteRawFree
 };
-
-constexpr int kBarTurn = 1;  // named barriers 1 and 2: row tile 0's and 1's turn
 
 // Instruction descriptor with f16 operands and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -322,7 +323,7 @@ struct Smem {
   static constexpr int OFF_PAT = OFF_META + 4 * 8 * 16;
   static constexpr int OFF_SCAN = OFF_PAT + 4 * 2048;
   static constexpr int OFF_BAR = OFF_SCAN + (kThreads / 32 + 4) * 8;
-  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 2 + 4 + 2 + 2;
+  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 4 + 4 + 4 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 32;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
@@ -365,12 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = r_empty + L::RST;    // [2] f16 V written (128)
   uint64_t* v_empty = v_full + 2;         // [2] its products done
   uint64_t* m_full = v_empty + 2;         // [4] a tile's scales and pattern (32)
-  uint64_t* s_full = m_full + 4;          // [2] S of a row tile done
-  uint64_t* p_full = s_full + 2;          // [2][2] half of P written, O rescaled (128)
-  // a tile's P V done: its products, and the issuing thread itself, which has
-  // seen v_full: what the converting warps wrote before is then visible
-  uint64_t* o_done = p_full + 4;          // [2] (2)
-  uint64_t* drained = o_done + 2;         // [2] every product of an issuer done
+  // of row tile g and half h of a tile, at 2 g + h
+  uint64_t* s_full = m_full + 4;          // [4] S done
+  uint64_t* p_full = s_full + 4;          // [4] P written, O rescaled (128)
+  // P V done: its products, and the issuing thread itself, which has seen
+  // v_full: what the converting warps wrote before is then visible
+  uint64_t* o_done = p_full + 4;          // [4] (2)
+  uint64_t* drained = o_done + 4;         // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [4]
@@ -382,9 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full + i, 128);
       mbar_init(v_full + i, 128);
       mbar_init(v_empty + i, 2);  // both issuers
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + 2 * i, 128);
-      mbar_init(p_full + 2 * i + 1, 128);
+      mbar_init(p_full + i, 128);
       mbar_init(o_done + i, 2);
     }
     for (int i = 0; i < L::KST; ++i) {
@@ -506,153 +509,144 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(q_full + g);
           }
           float m = -CUDART_INF_F, l = 0.f;
-          // The two row tiles take turns at the exponentials: each then has the
-          // special-function units to itself, and one's products run under the
-          // other's softmax.
-          const bool turns = unit.n > 128;
           const bool windowed = ice && one_head(w.rows, unit);
-          if (turns && g == 1) named_bar_arrive(kBarTurn, 256);
           for (int i = tile; i < tile_end; ++i) {
             const uint32_t nt = n_tile + (i - tile);
             mbar_wait(m_full + (nt & 3), (nt >> 2) & 1, wc, kSiteMeta);
-            // the P V of the tile before is done as well: this S was issued after it
-            if (!ice) {
-              mbar_wait(s_full + g, n_s & 1, wc, kSiteS);
-              ++n_s;
-            } else if (n_p > 0) {
-              mbar_wait(o_done + g, (n_p - 1) & 1, wc, kSiteO);
-            }
-            __syncwarp();
-            tc_fence_after();
-            if (warp_live) {
-              const uint32_t meta = sM + (nt & 3) * 128;
-              const int j0 = i * kTile;
-              const int lim = lim_all - j0;  // columns below it are seen
-              const bool edge = __any_sync(~0u, lim < kTile);
-              uint32_t s[128];
-              if (!ice) {
-                uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
-                uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
-                uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 64);
-                uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 96);
-                tmem_ld_x32(s_col, s0);
-                tmem_ld_x32(s_col + 32, s1);
-                tmem_ld_x32(s_col + 64, s2);
-                tmem_ld_x32(s_col + 96, s3);
-                tmem_wait_ld(s0);
-                tmem_wait_ld(s1);
-                tmem_wait_ld(s2);
-                tmem_wait_ld(s3);
-              } else if (windowed) {
-                // distance of (row, column k): entry (row of the unit) - k + 127
-                const float* pat =
-                    reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048);
-                const float* win = pat + 128 + g * 128 + r + 127;
-#pragma unroll
-                for (int k = 0; k < kTile; k += 4) {
-                  const float4 x = *reinterpret_cast<const float4*>(pat + k);
-                  s[k] = __float_as_uint(x.x + win[-k]);
-                  s[k + 1] = __float_as_uint(x.y + win[-k - 1]);
-                  s[k + 2] = __float_as_uint(x.z + win[-k - 2]);
-                  s[k + 3] = __float_as_uint(x.w + win[-k - 3]);
-                }
-              } else {
-                const float* al = p.a.alpha + (size_t)h * p.a.T_pat + j0;
-                const int d0 = pos - j0;  // distance of column 0
-                const float* rh = p.a.rho + (size_t)h * p.a.T_pat + d0;
-#pragma unroll
-                for (int k = 0; k < kTile; ++k) {
-                  const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
-                  s[k] = __float_as_uint(
-                      ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
-                }
-              }
-              if (edge) {
-#pragma unroll
-                for (int k = 0; k < kTile; ++k)
-                  if (k >= lim) s[k] = 0xff800000u;
-              }
-              float top = -CUDART_INF_F;
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {  // groups of 16 keys: one page, one scale
-                float x = fmax3(__uint_as_float(s[16 * q]), __uint_as_float(s[16 * q + 1]),
-                                __uint_as_float(s[16 * q + 2]));
-#pragma unroll
-                for (int k = 3; k < 15; k += 2)
-                  x = fmax3(x, __uint_as_float(s[16 * q + k]), __uint_as_float(s[16 * q + k + 1]));
-                x = fmaxf(x, __uint_as_float(s[16 * q + 15]));
-                const uint64_t mt = lds_f32x2(meta + 16 * q);
-                float ks, lv;
-                f2_unpack(mt, ks, lv);
-                top = fmaxf(top, fmaf(x, ice ? 1.f : fac * ks, lv));
-              }
-              // the maximum moves only when it would grow by more than 2^8:
-              // weights up to 2^8 fit f16 as well
-              const bool need = top > m + 8.f;
-              if (__any_sync(~0u, need)) {
-                const float corr = need ? fast_exp2(m - top) : 1.f;
-                if (need) m = top;
-                l *= corr;
-                if (i > tile) {
 #pragma unroll 1
-                  for (int q = 0; q < D; q += 16) {
-                    uint32_t o[16];
-                    tmem_ld_x16(o_col + q, o);
-                    tmem_wait_ld(o);
+            for (int hf = 0; hf < 2; ++hf) {
+              const int bar = 2 * g + hf;
+              // a half's P V of the tile before is done when its S is: that S was
+              // issued after it
+              if (!ice)
+                mbar_wait(s_full + bar, n_s & 1, wc, kSiteS);
+              else if (n_p > 0)
+                mbar_wait(o_done + bar, (n_p - 1) & 1, wc, kSiteO);
+              __syncwarp();
+              tc_fence_after();
+              if (warp_live) {
+                const uint32_t meta = sM + (nt & 3) * 128 + 64 * hf;
+                const uint32_t col = s_col + 64 * hf;
+                const int j0 = i * kTile + 64 * hf;
+                const int lim = lim_all - j0;  // columns below it are seen
+                const bool edge = __any_sync(~0u, lim < 64);
+                // a row of S: 4 groups of 16 keys, each of one page with one scale
+                uint32_t s[4][16];
+                float gm[4];
+                if (!ice) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                      o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                    tmem_st_x16(o_col + q, o);
+                  for (int q = 0; q < 4; ++q) tmem_ld_max_x16(col + 16 * q, s[q], gm[q]);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
+                  asm volatile("" : "+f"(gm[0]), "+f"(gm[1]), "+f"(gm[2]), "+f"(gm[3]));
+                } else if (windowed) {
+                  // distance of (row, column k): entry (row of the unit) - k + 127
+                  const float* pat =
+                      reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
+                  const float* win = pat + 128 + g * 128 + r + 127 - 128 * hf;
+#pragma unroll
+                  for (int k = 0; k < 64; k += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(pat + k);
+                    uint32_t* y = s[k / 16] + k % 16;
+                    y[0] = __float_as_uint(x.x + win[-k]);
+                    y[1] = __float_as_uint(x.y + win[-k - 1]);
+                    y[2] = __float_as_uint(x.z + win[-k - 2]);
+                    y[3] = __float_as_uint(x.w + win[-k - 3]);
+                  }
+                } else {
+                  const float* al = p.a.alpha + (size_t)h * p.a.T_pat + j0;
+                  const int d0 = pos - j0;  // distance of column 0
+                  const float* rh = p.a.rho + (size_t)h * p.a.T_pat + d0;
+#pragma unroll
+                  for (int k = 0; k < 64; ++k) {
+                    const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
+                    s[k / 16][k % 16] = __float_as_uint(
+                        ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
                   }
                 }
-              }
-              const float base = m == -CUDART_INF_F ? 0.f : m;
-              if (turns) named_bar_sync(kBarTurn + g, 256);
+                if (edge) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 mt = lds_f32x4(meta + 16 * q);
-                const float a = ice ? 1.f : fac * mt.x, b = mt.y - base;
-                const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
-                uint64_t sum = 0;
-                uint32_t pk[8];
+                  for (int k = 0; k < 64; ++k)
+                    if (k >= lim) s[k / 16][k % 16] = 0xff800000u;
+                }
+                if (edge || ice) {
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
+                  for (int q = 0; q < 4; ++q) {
+                    float x = fmax3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]),
+                                    __uint_as_float(s[q][2]));
+#pragma unroll
+                    for (int k = 3; k < 15; k += 2)
+                      x = fmax3(x, __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
+                    gm[q] = fmaxf(x, __uint_as_float(s[q][15]));
+                  }
+                }
+                float a[4], b[4], inv[4], top = -CUDART_INF_F;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float4 mt = lds_f32x4(meta + 16 * q);
+                  a[q] = ice ? 1.f : fac * mt.x;
+                  b[q] = mt.y;
+                  inv[q] = mt.z;
+                  top = fmaxf(top, fmaf(gm[q], a[q], b[q]));
+                }
+                // the maximum moves only when it would grow by more than 2^8:
+                // weights up to 2^8 fit f16 as well
+                const bool need = top > m + 8.f;
+                if (__any_sync(~0u, need)) {
+                  const float corr = need ? fast_exp2(m - top) : 1.f;
+                  if (need) m = top;
+                  l *= corr;
+                  if (i > tile || hf) {
+                    // the last product into O: the other half's
+                    mbar_wait(o_done + (bar ^ 1), (hf ? n_p : n_p - 1) & 1, wc, kSiteO);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 16) {
+                      uint32_t o[16];
+                      tmem_ld_x16(o_col + q, o);
+                      tmem_wait_ld(o);
+#pragma unroll
+                      for (int k = 0; k < 16; ++k)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                      tmem_st_x16(o_col + q, o);
+                    }
+                  }
+                }
+                const float base = m == -CUDART_INF_F ? 0.f : m;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint64_t a2 = f2_pack(a[q], a[q]), b2 = f2_pack(b[q] - base, b[q] - base);
+                  uint64_t sum = 0;
+                  uint32_t pk[8];
+#pragma unroll
+                  for (int k = 0; k < 16; k += 2) {
+                    float x, y;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][k]),
+                                             __uint_as_float(s[q][k + 1])),
+                                     a2, b2),
+                              x, y);
+                    x = fast_exp2(x);
+                    y = fast_exp2(y);
+                    sum = f2_add(sum, f2_pack(x, y));
+                    pk[k / 2] = pack_f16x2(x, y);
+                  }
                   float x, y;
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[16 * q + k]),
-                                           __uint_as_float(s[16 * q + k + 1])),
-                                   a2, b2),
-                            x, y);
-                  x = fast_exp2(x);
-                  y = fast_exp2(y);
-                  sum = f2_add(sum, f2_pack(x, y));
-                  pk[k / 2] = pack_f16x2(x, y);
+                  f2_unpack(sum, x, y);
+                  l = fmaf(x + y, inv[q], l);
+                  tmem_st_x8(col + 8 * q, pk);
                 }
-                float x, y;
-                f2_unpack(sum, x, y);
-                l = fmaf(x + y, mt.z, l);
-                tmem_st_x8(s_col + 8 * q, pk);
-                if (q == 3) {  // the first half's product may start
-                  tmem_wait_st();
-                  tc_fence_before();
-                  mbar_arrive(p_full + 2 * g);
-                }
-              }
-              if (turns && (g == 0 || i + 1 < tile_end)) named_bar_arrive(kBarTurn + 1 - g, 256);
-              tmem_wait_st();
-            } else {
-              if (turns) {
-                named_bar_sync(kBarTurn + g, 256);
-                if (g == 0 || i + 1 < tile_end) named_bar_arrive(kBarTurn + 1 - g, 256);
+                tmem_wait_st();
               }
               tc_fence_before();
-              mbar_arrive(p_full + 2 * g);
+              mbar_arrive(p_full + bar);
             }
-            tc_fence_before();
-            mbar_arrive(p_full + 2 * g + 1);
+            if (!ice) ++n_s;
             ++n_p;
           }
           // ---- results
-          mbar_wait(o_done + g, (n_p - 1) & 1, wc, kSiteO);
+          mbar_wait(o_done + 2 * g, (n_p - 1) & 1, wc, kSiteO);
+          mbar_wait(o_done + 2 * g + 1, (n_p - 1) & 1, wc, kSiteO);
           __syncwarp();
           tc_fence_after();
           const bool whole = tile == 0 && tile_end == w.ut;
@@ -803,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
       if ((warp == 12 || warp == 14) && lane == 0) {
         const int g = (warp - 12) >> 1;
-        constexpr uint32_t id_s = idesc_e4m3(128, kTile);
+        constexpr uint32_t id_s = idesc_e4m3(128, 64);
         constexpr uint32_t id_o = idesc_f16(128, D, false, true);
         const uint32_t s_col = tmem + kS + g * 128, o_col = tmem + kO + g * 128;
         const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
@@ -815,22 +809,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           // K of the next S; waited for ahead of the softmax, so that the wait
           // is not part of the row tile's chain
           auto wait_k = [&]() { mbar_poll(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK); };
-          auto issue_s = [&]() {
-            const uint32_t st = kc++ % L::KST;
-            if (mine) {
-              tc_fence_after();
-              const uint64_t kt = sdesc(sK + st * L::CODES, 16, 8 * D, swizzle_layout_code(D));
-              issue_codes<D / 32, (L::CODES >> 4)>(s_col, qt, kt, id_s);
-              mma_commit(k_empty + st);
-              mma_commit(s_full + g);
-            } else {
-              mbar_arrive(k_empty + st);
-            }
+          // S of 64 keys: the tile's first or second half
+          auto issue_s = [&](int hf) {
+            const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES + hf * 64 * D, 16, 8 * D,
+                                      swizzle_layout_code(D));
+            issue_codes<D / 32, (L::CODES >> 4)>(s_col + 64 * hf, qt, kt, id_s);
+            mma_commit(s_full + 2 * g + hf);
+          };
+          auto k_done = [&]() {
+            if (mine)
+              mma_commit(k_empty + kc % L::KST);
+            else
+              mbar_arrive(k_empty + kc % L::KST);
+            ++kc;
           };
           if (!ice) {
             wait_k();
-            if (mine) mbar_poll(q_full + g, n_q++ & 1, wc, kSiteQ);
-            issue_s();
+            if (mine) {
+              mbar_poll(q_full + g, n_q++ & 1, wc, kSiteQ);
+              tc_fence_after();
+              issue_s(0);
+              issue_s(1);
+            }
+            k_done();
           }
           for (int i = tile; i < tile_end; ++i) {
             const bool more = !ice && i + 1 < tile_end;
@@ -842,25 +843,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t vt = G::mnmajor_desc(sV + st * L::TILE, 0);
               constexpr int kVStep = 16 * G::SWZ >> 4;
 #pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
-                mbar_poll(p_full + 2 * g + half, n_p & 1, wc, kSiteP);
+              for (int hf = 0; hf < 2; ++hf) {
+                const int bar = 2 * g + hf;
+                mbar_poll(p_full + bar, n_p & 1, wc, kSiteP);
                 tc_fence_after();
-                issue_pv<kVStep>(o_col, s_col + 32 * half, vt + 4 * kVStep * half, id_o,
-                                 i > tile || half);
-              }
-              mma_commit(o_done + g);
-              mbar_arrive(o_done + g);
-              mma_commit(v_empty + st);
-              // S takes the columns of the P that these products read
-              if (more) {
-                mbar_poll(o_done + g, n_p & 1, wc, kSiteO);
-                issue_s();
+                issue_pv<kVStep>(o_col, s_col + 64 * hf, vt + 4 * kVStep * hf, id_o,
+                                 i > tile || hf);
+                mma_commit(o_done + bar);
+                mbar_arrive(o_done + bar);
+                if (hf) mma_commit(v_empty + st);
+                // S takes the columns of the P that these products read
+                if (more) {
+                  mbar_poll(o_done + bar, n_p & 1, wc, kSiteO);
+                  tc_fence_after();
+                  issue_s(hf);
+                }
               }
               ++n_p;
             } else {
               mbar_arrive(v_empty + st);
-              if (more) issue_s();
             }
+            if (more) k_done();
           }
           at += tile_end - tile;
           if (at >= sh.end) break;
@@ -873,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (warp == 13) {
         // ---------------------------------------------------------- codes and scales
         uint32_t kc = 0, vc = 0;
-        const int per = c.page_shift > 4 ? 1 << (c.page_shift - 4) : 1;  // groups of a page
+        const int per = 1 << (c.page_shift - 4);  // groups of 16 keys in a page
+        const bool issues = lane < 8 && lane % per == 0;
         for (;;) {
           const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
           const int kv = p.cls_kv[w.cls], kh = w.ice() ? -1 : c.k_of[kv];
@@ -927,12 +931,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t st = kc % L::KST;
               mbar_wait(k_empty + st, ((kc / L::KST) & 1) ^ 1, wc, kSiteKFree);
               if (lane == 0) mbar_arrive_expect_tx(k_full + st, L::CODES);
-              for (int g = 0; g < 8; g += per) {
-                const int pg = __shfl_sync(~0u, page, g);
-                if (lane == 0)
-                  tma_load_4d(smem + L::OFF_K + st * L::CODES + g * 16 * D, &tm_k, k_full + st, kh,
-                              pg);
-              }
+              __syncwarp();
+              // each page from a lane of its own: one thread gets a copy through in
+              // about 560 cycles only
+              if (issues)
+                tma_load_4d(smem + L::OFF_K + st * L::CODES + lane * 16 * D, &tm_k, k_full + st,
+                            kh, page);
               ++kc;
             }
             const uint32_t st = vc % L::RST;
@@ -952,12 +956,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(m_full + (vc & 3));
             fetch_pattern(i + 1);
             if (lane == 0) mbar_arrive_expect_tx(r_full + st, L::CODES);
-            for (int g = 0; g < 8; g += per) {
-              const int pg = __shfl_sync(~0u, page, g);
-              if (lane == 0)
-                tma_load_4d(smem + L::OFF_R + st * L::CODES + g * 16 * D, &tm_v, r_full + st, kv,
-                            pg);
-            }
+            __syncwarp();
+            if (issues)
+              tma_load_4d(smem + L::OFF_R + st * L::CODES + lane * 16 * D, &tm_v, r_full + st, kv,
+                          page);
             ++vc;
             page = page1;
             page1 = page2;

@@ -711,15 +711,15 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k0 + k < n) top = fmaxf(top, w[k].x);
-      if (top == -CUDART_INF_F) continue;  // nothing of weight yet
-      const float f0 = fast_exp2(mx - top);
+      // (a part that saw nothing holds zeros: it takes no part, but a NaN does)
+      const float f0 = top == -CUDART_INF_F ? 1.f : fast_exp2(mx - top);
       mx = top;
       sum *= f0;
       o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k0 + k < n) {
-          const float f = fast_exp2(w[k].x - mx);
+          const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(w[k].x - mx);
           sum = fmaf(f, w[k].y, sum);
           o.x = fmaf(f, x[k].x, o.x);
           o.y = fmaf(f, x[k].y, o.y);

@@ -410,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  // the joining kernel may be set up meanwhile; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;");
   const Share sh = find_share(p, reinterpret_cast<long long*>(smem + L::OFF_SCAN));
   tc_fence_before();
   __syncthreads();
@@ -447,63 +449,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool warp_live = g * 128 + (warp & 3) * 32 < unit.n;
           float fac = 1.f;
           if (!ice) {
-            // rows of Q: scaled by the least 2^-e that brings the row within
-            // e4m3's range, split into hi + lo; kL lanes take a row
-            constexpr int kL = D / 8, kR = 32 / kL;
-            const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
-            const uint16_t* qb = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
-            const int u = lane % kL;  // 8 components of a row
-            uint4 q[kL];
+            // the row of Q, scaled by the least 2^-e that brings it within e4m3's
+            // range and split into hi + lo.  Read twice, the second time from L1:
+            // rolled loops, since this runs once a unit and straight-line code
+            // would wait for its instructions.
+            const uint4* q = reinterpret_cast<const uint4*>(p.a.Q + row * D);
+            float amax = 0.f;
+            if (live) {
+#pragma unroll 8
+              for (int u = 0; u < D / 8; ++u) {
+                const uint4 x = __ldg(q + u);
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 32; i += kR) {
-              const int src = __shfl_sync(~0u, mine, i + lane / kL);
-              q[i / kR] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                               qb + (size_t)(unsigned)src * D) + u)
-                                   : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += kR) {
-              const int rl = i + lane / kL;  // row of the warp
-              const uint32_t x[4] = {q[i / kR].x, q[i / kR].y, q[i / kR].z, q[i / kR].w};
-              float y[8], amax = 0.f;
-#pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                y[v] = __uint_as_float(v & 1 ? x[v / 2] & 0xffff0000u : x[v / 2] << 16);
-                amax = fmaxf(amax, fabsf(y[v]));
+                for (int k = 0; k < 4; ++k)
+                  amax = fmax3(amax, fabsf(__uint_as_float(y[k] << 16)),
+                               fabsf(__uint_as_float(y[k] & 0xffff0000u)));
               }
-#pragma unroll
-              for (int o = kL / 2; o; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-              const int bits = __float_as_int(amax);
-              int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
-              e = amax > 0.f ? max(-126, min(120, e)) : 0;
-              const float down = pow2f(-e);
-              uint32_t hi[2], lo[2];
+            }
+            const int bits = __float_as_int(amax);
+            int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+            e = amax > 0.f ? max(-126, min(120, e)) : 0;
+            const float down = pow2f(-e);
+            fac = pow2f(e) * (rsqrtf((float)D) * kLog2e);
+            const uint32_t stage = sQ + g * L::TILE;
+#pragma unroll 2
+            for (int u = 0; u < D / 16; ++u) {
+              uint32_t hi[4], lo[4];
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
-                float z[4];
+                const uint4 x = live ? __ldg(q + 2 * u + v) : make_uint4(0, 0, 0, 0);
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  z[k] = y[4 * v + k] * down;
-                  // e4m3 has no infinity: the row becomes NaN, as its softmax would
-                  if (fabsf(z[k]) == CUDART_INF_F) z[k] = CUDART_NAN_F;
+                for (int k = 0; k < 4; k += 2) {
+                  float z[4] = {__uint_as_float(y[k] << 16), __uint_as_float(y[k] & 0xffff0000u),
+                                __uint_as_float(y[k + 1] << 16),
+                                __uint_as_float(y[k + 1] & 0xffff0000u)};
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    // e4m3 has no infinity: the row becomes NaN, as its softmax would
+                    z[j] = fabsf(z[j]) == CUDART_INF_F ? CUDART_NAN_F : z[j] * down;
+                  }
+                  const uint32_t top = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
+                  uint32_t c0, c1;
+                  e4m3x4_f16x4(top, c0, c1);
+                  const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&c0));
+                  const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
+                  hi[2 * v + k / 2] = top;
+                  lo[2 * v + k / 2] =
+                      e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
                 }
-                hi[v] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
-                uint32_t a, b;
-                e4m3x4_f16x4(hi[v], a, b);
-                const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-                const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-                lo[v] = e4m3x2(z[0] - fa.x, z[1] - fa.y) | e4m3x2(z[2] - fb.x, z[3] - fb.y) << 16;
               }
-              const uint32_t at8 =
-                  sQ + g * L::TILE + code_at<D>((warp & 3) * 32 + rl, u >> 1) + (u & 1) * 8;
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8), "r"(hi[0]), "r"(hi[1])
-                           : "memory");
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at8 + L::CODES), "r"(lo[0]),
-                           "r"(lo[1])
-                           : "memory");
-              const int back = __shfl_sync(~0u, e, (lane - i) * kL & 31);
-              if (lane >= i && lane < i + kR) fac = pow2f(back) * (rsqrtf((float)D) * kLog2e);
+              st_shared_v4(stage + code_at<D>(r, u), hi[0], hi[1], hi[2], hi[3]);
+              st_shared_v4(stage + L::CODES + code_at<D>(r, u), lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full + g);
@@ -1013,21 +1010,40 @@ __global__ void __launch_bounds__(256)
     auto ml = [&](int part) {
       return *reinterpret_cast<const float2*>(p.a.ml + ((size_t)part * kRows + r) * 2);
     };
-    float mx = ml(first).x, sum = 0.f;
-    for (int k = blockIdx.x + 1; k <= last; ++k) mx = fmaxf(mx, ml(2 * k).x);
+    // parts 0 .. n - 1, in the order of the CTAs; four at a time are in flight
+    const int n = last - blockIdx.x + 1;
+    auto part = [&](int k) { return k == 0 ? first : 2 * ((int)blockIdx.x + k); };
+    float mx = -CUDART_INF_F, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = blockIdx.x; k <= last; ++k) {
-      const int part = k == (int)blockIdx.x ? first : 2 * k;
-      const float2 x = ml(part);
-      const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(x.x - mx);
-      sum = fmaf(f, x.y, sum);
-      const float4 v =
-          *reinterpret_cast<const float4*>(p.a.acc + (size_t)part * kRows * D +
-                                           ((size_t)(d / 4) * kRows + r) * 4);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
+    for (int k0 = 0; k0 < n; k0 += 4) {
+      float2 w[4];
+      float4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k0 + k < n) {
+          w[k] = ml(part(k0 + k));
+          x[k] = *reinterpret_cast<const float4*>(p.a.acc + (size_t)part(k0 + k) * kRows * D +
+                                                  ((size_t)(d / 4) * kRows + r) * 4);
+        }
+      float top = mx;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k0 + k < n) top = fmaxf(top, w[k].x);
+      // (a part that saw nothing holds zeros: it takes no part)
+      const float f0 = top == -CUDART_INF_F ? 1.f : fast_exp2(mx - top);
+      mx = top;
+      sum *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k0 + k < n) {
+          const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(w[k].x - mx);
+          sum = fmaf(f, w[k].y, sum);
+          o.x = fmaf(f, x[k].x, o.x);
+          o.y = fmaf(f, x[k].y, o.y);
+          o.z = fmaf(f, x[k].z, o.z);
+          o.w = fmaf(f, x[k].w, o.w);
+        }
     }
     int t, idx;
     row_of(rows, unit.first + r, gk, ice, t, idx);

@@ -143,19 +143,6 @@ __device__ Share find_share(const CacheCall& c, int per_slot, long long* scan /*
   return s;
 }
 
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
-  static_assert(N == 1 || N == 2 || N == 4, "");
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(a));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
-}
-
 // The 8 x 8 block of 16-bit values of a warp (lane: row lane / 4, columns
 // 2 (lane % 4) and the next), transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {

@@ -449,55 +449,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool warp_live = g * 128 + (warp & 3) * 32 < unit.n;
           float fac = 1.f;
           if (!ice) {
-            // the row of Q, scaled by the least 2^-e that brings it within e4m3's
-            // range and split into hi + lo.  Read twice, the second time from L1:
-            // rolled loops, since this runs once a unit and straight-line code
-            // would wait for its instructions.
-            const uint4* q = reinterpret_cast<const uint4*>(p.a.Q + row * D);
+            // The row of Q, scaled by the least 2^-e that brings it within e4m3's
+            // range and split into hi + lo.  The rows come in side by side
+            // (kL lanes to a row); 8 components lie where 16 codes of hi or lo
+            // will, an even unit's in hi's place and an odd one's in lo's, so that
+            // each thread turns its row into codes where it lies.
+            constexpr int kL = D / 8, kR = 32 / kL;
+            const uint32_t stage = sQ + g * L::TILE;
+            const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
+            const uint16_t* slot_q = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
+#pragma unroll 4
+            for (int i = 0; i < 32; i += kR) {
+              const int rl = i + lane / kL, u = lane % kL;
+              const int src = __shfl_sync(~0u, mine, rl);
+              cp_async16(stage + (u & 1) * L::CODES + code_at<D>((warp & 3) * 32 + rl, u >> 1),
+                         slot_q + (size_t)(unsigned)max(src, 0) * D + u * 8, src >= 0 ? 16 : 0);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncwarp();
             float amax = 0.f;
-            if (live) {
-#pragma unroll 8
-              for (int u = 0; u < D / 8; ++u) {
-                const uint4 x = __ldg(q + u);
-                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 2
+            for (int u = 0; u < D / 16; ++u) {
+              uint32_t y[8];
+              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y), stage + code_at<D>(r, u));
+              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y + 4),
+                        stage + L::CODES + code_at<D>(r, u));
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  amax = fmax3(amax, fabsf(__uint_as_float(y[k] << 16)),
-                               fabsf(__uint_as_float(y[k] & 0xffff0000u)));
-              }
+              for (int k = 0; k < 8; ++k)
+                amax = fmax3(amax, fabsf(__uint_as_float(y[k] << 16)),
+                             fabsf(__uint_as_float(y[k] & 0xffff0000u)));
             }
             const int bits = __float_as_int(amax);
             int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
             e = amax > 0.f ? max(-126, min(120, e)) : 0;
             const float down = pow2f(-e);
             fac = pow2f(e) * (rsqrtf((float)D) * kLog2e);
-            const uint32_t stage = sQ + g * L::TILE;
 #pragma unroll 2
             for (int u = 0; u < D / 16; ++u) {
-              uint32_t hi[4], lo[4];
+              uint32_t y[8], hi[4], lo[4];
+              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y), stage + code_at<D>(r, u));
+              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y + 4),
+                        stage + L::CODES + code_at<D>(r, u));
 #pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                const uint4 x = live ? __ldg(q + 2 * u + v) : make_uint4(0, 0, 0, 0);
-                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+              for (int k = 0; k < 4; ++k) {
+                float z[4] = {__uint_as_float(y[2 * k] << 16),
+                              __uint_as_float(y[2 * k] & 0xffff0000u),
+                              __uint_as_float(y[2 * k + 1] << 16),
+                              __uint_as_float(y[2 * k + 1] & 0xffff0000u)};
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                  float z[4] = {__uint_as_float(y[k] << 16), __uint_as_float(y[k] & 0xffff0000u),
-                                __uint_as_float(y[k + 1] << 16),
-                                __uint_as_float(y[k + 1] & 0xffff0000u)};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    // e4m3 has no infinity: the row becomes NaN, as its softmax would
-                    z[j] = fabsf(z[j]) == CUDART_INF_F ? CUDART_NAN_F : z[j] * down;
-                  }
-                  const uint32_t top = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
-                  uint32_t c0, c1;
-                  e4m3x4_f16x4(top, c0, c1);
-                  const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&c0));
-                  const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
-                  hi[2 * v + k / 2] = top;
-                  lo[2 * v + k / 2] =
-                      e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
+                for (int j = 0; j < 4; ++j) {
+                  // e4m3 has no infinity: the row becomes NaN, as its softmax would
+                  z[j] = fabsf(z[j]) == CUDART_INF_F ? CUDART_NAN_F : z[j] * down;
                 }
+                hi[k] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
+                uint32_t c0, c1;
+                e4m3x4_f16x4(hi[k], c0, c1);
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&c0));
+                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
+                lo[k] = e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
               }
               st_shared_v4(stage + code_at<D>(r, u), hi[0], hi[1], hi[2], hi[3]);
               st_shared_v4(stage + L::CODES + code_at<D>(r, u), lo[0], lo[1], lo[2], lo[3]);

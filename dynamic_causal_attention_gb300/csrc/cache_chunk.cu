@@ -813,9 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
           const bool ice = w.ice();
           const bool mine = unit_rows(w.rows, w.pair, w.gk(), ice).n > g * 128;
-          // K of the next S; waited for ahead of the softmax, so that the wait
-          // is not part of the row tile's chain
-          auto wait_k = [&]() { mbar_poll(k_full + kc % L::KST, (kc / L::KST) & 1, wc, kSiteK); };
+          // K of tile i + 1 and V of tile i are waited for while a product of the
+          // tile before runs, so that the waits are not part of the row tile's chain
+          auto wait_k = [&](uint32_t n) { mbar_poll(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK); };
+          auto wait_v = [&](uint32_t n) { mbar_poll(v_full + (n & 1), (n >> 1) & 1, wc, kSiteV); };
           // S of 64 keys: the tile's first or second half
           auto issue_s = [&](int hf) {
             const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES + hf * 64 * D, 16, 8 * D,
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++kc;
           };
           if (!ice) {
-            wait_k();
+            wait_k(kc);
             if (mine) {
               mbar_poll(q_full + g, n_q++ & 1, wc, kSiteQ);
               tc_fence_after();
@@ -840,12 +841,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             k_done();
           }
+          wait_v(vc);
+          if (!ice && tile + 1 < tile_end) wait_k(kc);
           for (int i = tile; i < tile_end; ++i) {
-            const bool more = !ice && i + 1 < tile_end;
-            const uint32_t st = vc & 1;
-            mbar_poll(v_full + st, (vc >> 1) & 1, wc, kSiteV);
-            ++vc;
-            if (more) wait_k();
+            const bool next = i + 1 < tile_end, more = !ice && next;
+            const uint32_t st = vc++ & 1;
             if (mine) {
               const uint64_t vt = G::mnmajor_desc(sV + st * L::TILE, 0);
               constexpr int kVStep = 16 * G::SWZ >> 4;
@@ -858,7 +858,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  i > tile || hf);
                 mma_commit(o_done + bar);
                 mbar_arrive(o_done + bar);
-                if (hf) mma_commit(v_empty + st);
+                if (hf)
+                  mma_commit(v_empty + st);
+                else if (next) {
+                  wait_v(vc);
+                  if (!ice && i + 2 < tile_end) wait_k(kc + 1);
+                }
                 // S takes the columns of the P that these products read
                 if (more) {
                   mbar_poll(o_done + bar, n_p & 1, wc, kSiteO);
@@ -869,6 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++n_p;
             } else {
               mbar_arrive(v_empty + st);
+              if (next) wait_v(vc);
+              if (!ice && i + 2 < tile_end) wait_k(kc + 1);
             }
             if (more) k_done();
           }

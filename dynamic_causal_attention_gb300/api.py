@@ -26,6 +26,12 @@ def _stream(device=None):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _raw_stream(index):
+    """The current stream of a device as an integer (what ``_stream`` gives, without a Stream
+    object: a call on the cache is a few microseconds)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _check(st, where):
     if st != B.SAF_OK:
         raise B.SafError(st, where)
@@ -183,7 +189,7 @@ class PagedCache:
         self.H, self.d_h, self.H_kv = H, d_h, H if H_kv is None else H_kv
         self.n_seqs, self.max_pages, self.n_pages = n_seqs, max_pages, n_pages
         self.page_size, self.max_new = page_size, max_new
-        self.layouts, self.offsets, self._static = [], [], []
+        self.layouts, self.offsets, self._static, self._frozen = [], [], [], []
         geometry = (n_seqs, max_pages, n_pages, page_size, H, self.H_kv, d_h)
         at = 0
         for mask in layers:
@@ -193,6 +199,7 @@ class PagedCache:
             st, layout = B.saf_cache_layer_layout(B._cache_dims(*geometry, 0), m)
             _check(st, "saf_cache_layer_layout")
             self._static.append(m)
+            self._frozen.append(any(m))
             self.layouts.append(layout)
             self.offsets.append(at)
             at += layout.bytes
@@ -200,14 +207,19 @@ class PagedCache:
         new = lambda shape, fill: torch.full(shape, fill, dtype=torch.int32, device=self.device)
         if pool is None:
             pool = torch.zeros((n_pages, at), dtype=torch.uint8, device=self.device)
-        self.page_table = new((n_seqs, max_pages), -1) if page_table is None else page_table
-        self.seq_len = new((n_seqs,), 0) if seq_len is None else seq_len
-        self.ref = new((n_pages,), 0) if ref is None else ref
+        self._tables = (new((n_seqs, max_pages), -1) if page_table is None else page_table,
+                        new((n_seqs,), 0) if seq_len is None else seq_len,
+                        new((n_pages,), 0) if ref is None else ref)
         if not (pool.dim() == 2 and pool.shape == (n_pages, at) and pool.stride(1) == 1
                 and pool.dtype == torch.uint8 and pool.device == self.device):
             raise B.SafError(B.SAF_ERR_INVALID_ARG, f"PagedCache: pool is not [{n_pages}, {at}] bytes")
-        self.pool = pool
-        self._table_like((self.page_table, self.seq_len, self.ref), "PagedCache")
+        self._pool = pool
+        self._shapes = (torch.Size((n_seqs, max_pages)), torch.Size((n_seqs,)),
+                        torch.Size((n_pages,)))
+        # the tables and the pool stay the same tensors, so their addresses do too
+        self._at = self._table_like(self._tables, "PagedCache")
+        self._pool_at = pool.data_ptr()
+        self._layer_at = [self._pool_at + o for o in self.offsets]
         # a pool of one page may report any stride
         self.dims = B._cache_dims(*geometry, pool.stride(0) if n_pages > 1 else at)
         with torch.cuda.device(self.device):
@@ -218,6 +230,12 @@ class PagedCache:
         self.ws_bytes, self._pages_bytes = attn, pages
         self.workspace = torch.empty(attn, dtype=torch.uint8, device=self.device)
         self._pages_ws = torch.empty(pages, dtype=torch.uint8, device=self.device)
+        self._ws_at, self._pages_at = self.workspace.data_ptr(), self._pages_ws.data_ptr()
+
+    page_table = property(lambda self: self._tables[0], doc="[n_seqs, max_pages] int32")
+    seq_len = property(lambda self: self._tables[1], doc="[n_seqs] int32: tokens of each slot")
+    ref = property(lambda self: self._tables[2], doc="[n_pages] int32: rows that hold a page")
+    pool = property(lambda self: self._pool, doc="[n_pages, bytes of a page]")
 
     # ---- checks
     def _need(self, t, shape, dtype, what):
@@ -228,21 +246,20 @@ class PagedCache:
         return t.data_ptr()
 
     def _table_like(self, three, what):
-        shapes = ((self.n_seqs, self.max_pages), (self.n_seqs,), (self.n_pages,))
-        return [self._need(t, s, torch.int32, what) for t, s in zip(three, shapes)]
+        return tuple(self._need(t, s, torch.int32, what) for t, s in zip(three, self._shapes))
 
     def _per_slot(self, t, what):
-        return None if t is None else self._need(t, (self.n_seqs,), torch.int32, what)
+        return None if t is None else self._need(t, self._shapes[1], torch.int32, what)
 
-    def _call(self, name, *args):
+    def _call(self, entry, *args):
         """The C entry on this cache's device and its current stream."""
         if torch.cuda.current_device() == self.device.index:
-            st = getattr(B, name)(*args, _stream(self.device))
+            st = entry(*args, _raw_stream(self.device.index))
         else:
             with torch.cuda.device(self.device):
-                st = getattr(B, name)(*args, _stream(self.device))
+                st = entry(*args, _raw_stream(self.device.index))
         if st != B.SAF_OK:
-            raise B.SafError(st, name)
+            raise B.SafError(st, entry.__name__)
 
     # ---- tokens
     def append(self, layer: int, k, v, n_new=None):
@@ -255,11 +272,10 @@ class PagedCache:
             raise B.SafError(B.SAF_ERR_UNSUPPORTED, "append: v is neither bf16 nor fp32")
         pv = self._need(v, shape, v.dtype, "append: v")
         pk = None if k is None else self._need(k, shape, v.dtype, "append: k")
-        self._call("saf_cache_append", self.dims, self._static[layer],
-                   self.pool.data_ptr() + self.offsets[layer], pk, pv,
+        self._call(B.saf_cache_append, self.dims, self._static[layer],
+                   self._layer_at[layer], pk, pv,
                    B.SAF_F32 if v.dtype == torch.float32 else B.SAF_BF16, n,
-                   self._per_slot(n_new, "append: n_new"), self.seq_len.data_ptr(),
-                   self.page_table.data_ptr())
+                   self._per_slot(n_new, "append: n_new"), self._at[1], self._at[0])
 
     def attend(self, layer: int, q, alpha=None, rho=None, n_new=None, out=None, lse=None):
         """The hybrid attention of q [n_seqs, H, n, d_h] (bf16), the last n_new[s] (None: n)
@@ -280,15 +296,14 @@ class PagedCache:
             T = alpha.shape[-1]
             pa = self._need(alpha, (self.H, T), torch.float32, "attend: alpha")
             pr = None if rho is None else self._need(rho, (self.H, T), torch.float32, "attend: rho")
-        if any(self._static[layer]) and (alpha is None or rho is None):
+        if self._frozen[layer] and (alpha is None or rho is None):
             raise B.SafError(B.SAF_ERR_INVALID_ARG, "attend: frozen heads need alpha and rho")
-        self._call("saf_cache_attn", self.dims, self._static[layer],
-                   self.pool.data_ptr() + self.offsets[layer], pq, pa, pr, T, n,
-                   self._per_slot(n_new, "attend: n_new"), self.seq_len.data_ptr(),
-                   self.page_table.data_ptr(),
+        self._call(B.saf_cache_attn, self.dims, self._static[layer],
+                   self._layer_at[layer], pq, pa, pr, T, n,
+                   self._per_slot(n_new, "attend: n_new"), self._at[1], self._at[0],
                    self._need(out, shape, torch.bfloat16, "attend: out"),
                    self._need(lse, shape[:3], torch.float32, "attend: lse"),
-                   self.workspace.data_ptr(), self.ws_bytes)
+                   self._ws_at, self.ws_bytes)
         return out, lse
 
     def views(self, layer: int):
@@ -307,35 +322,33 @@ class PagedCache:
         seq_len advances.  Returns (granted [n_seqs], n_short [1]): what each slot got, all zero
         when n_short pages are missing.  ``into``: (page_table, seq_len, ref) to write instead of
         the cache's own."""
-        mine = self._table_like((self.page_table, self.seq_len, self.ref), "grow")
-        to = mine if into is None else self._table_like(into, "grow: into")
+        to = self._at if into is None else self._table_like(into, "grow: into")
         granted = torch.empty(self.n_seqs, dtype=torch.int32, device=self.device)
         n_short = torch.empty(1, dtype=torch.int32, device=self.device)
         if self.n_seqs == 0:
             n_short.zero_()
-        self._call("saf_cache_grow", self.dims, self.pool.data_ptr(), self.page_bytes,
-                   self._per_slot(n_new, "grow: n_new"), *mine, *to, granted.data_ptr(),
-                   n_short.data_ptr(), self._pages_ws.data_ptr(), self._pages_bytes)
+        self._call(B.saf_cache_grow, self.dims, self._pool_at, self.page_bytes,
+                   self._per_slot(n_new, "grow: n_new"), *self._at, *to, granted.data_ptr(),
+                   n_short.data_ptr(), self._pages_at, self._pages_bytes)
         return granted, n_short
 
     def fork(self, parent, into=None):
         """Slot s takes over the pages and length of slot parent[s] (int32 [n_seqs]); a parent
         outside [0, n_seqs) frees it.  ``into`` as in grow."""
-        mine = self._table_like((self.page_table, self.seq_len, self.ref), "fork")
-        to = mine if into is None else self._table_like(into, "fork: into")
-        self._call("saf_cache_fork", self.dims, self._per_slot(parent, "fork: parent"), *mine, *to)
+        to = self._at if into is None else self._table_like(into, "fork: into")
+        self._call(B.saf_cache_fork, self.dims, self._per_slot(parent, "fork: parent"), *self._at, *to)
 
     def compact(self, into=None):
         """Move the used pages into the lowest page numbers.  Returns their number (int32 [1]).
         ``into``: (page_table, ref) to write instead of the cache's own."""
-        table, _, ref = self._table_like((self.page_table, self.seq_len, self.ref), "compact")
+        table, _, ref = self._at
         to = (table, ref)
         if into is not None:
-            to = (self._need(into[0], (self.n_seqs, self.max_pages), torch.int32, "compact: into"),
-                  self._need(into[1], (self.n_pages,), torch.int32, "compact: into"))
+            to = (self._need(into[0], self._shapes[0], torch.int32, "compact: into"),
+                  self._need(into[1], self._shapes[2], torch.int32, "compact: into"))
         n_used = torch.empty(1, dtype=torch.int32, device=self.device)
-        self._call("saf_cache_compact", self.dims, self.pool.data_ptr(), self.page_bytes, table, ref,
-                   *to, n_used.data_ptr(), self._pages_ws.data_ptr(), self._pages_bytes)
+        self._call(B.saf_cache_compact, self.dims, self._pool_at, self.page_bytes, table, ref,
+                   *to, n_used.data_ptr(), self._pages_at, self._pages_bytes)
         return n_used
 
     def device_status(self):

@@ -87,14 +87,24 @@ saf_status make_call(const saf_cache_dims& d, const uint8_t* head_is_static, con
   return SAF_OK;
 }
 
-// The scratch of an attention call and the kernel that takes it: up to 16 rows
-// for each slot and K/V head go to the kernel made for single tokens.
-constexpr int kFewRows = 16;
-bool many_rows(const saf_cache_dims& d, int n_q) {
-  return (long long)n_q * (d.H / d.H_kv) > kFewRows;
-}
-CacheAttnWs attn_ws(const saf_cache_dims& d, int n_q) {
-  return many_rows(d, n_q) ? cache_chunk_ws(d.d_h, sm_count()) : cache_attn_ws(d.d_h, sm_count());
+// Which kernel takes an attention call of n_q rows.  cache_attn.cu reads a
+// head's keys once for every 16 rows (from L2 after the first); cache_chunk.cu
+// once for 256 rows of the dynamic heads and once for 256 of each frozen one.
+// Measured over 16 x 8192 tokens, d_h = 128, 2 K/V heads: 12 us plus 15 us for
+// every 16 rows against 58 us for a unit of dynamic rows (4 to 256 rows alike)
+// plus 32 us for a unit of a frozen head, so a row tile counts 10, the units 36
+// and 20.  (48 rows: 59 and 58 us; 128 rows: 129 and 61 us.)
+bool many_rows(const saf_cache_dims& d, const uint8_t* is_static, int n_q) {
+  const int g = d.H / d.H_kv;
+  const long long few = 10ll * d.H_kv * (((long long)n_q * g + 15) / 16);
+  long long many = 0;
+  for (int kv = 0; kv < d.H_kv; ++kv) {
+    int frozen = 0;
+    for (int h = kv * g; h < (kv + 1) * g; ++h) frozen += is_static[h] != 0;
+    many += 36ll * (((long long)n_q * (g - frozen) + 255) / 256);
+    many += 20ll * frozen * (((long long)n_q + 255) / 256);
+  }
+  return few > many;
 }
 
 saf_status status_of(cudaError_t e) { return e == cudaSuccess ? SAF_OK : SAF_ERR_CUDA; }
@@ -159,10 +169,10 @@ saf_status saf_cache_append(const saf_cache_dims* dims, const uint8_t* head_is_s
 
 size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q) {
   if (check_cache(dims) != SAF_OK || n_q < 0) return 0;
-  // calls with fewer rows may take either kernel
+  // which kernel runs depends on the frozen heads; 16 rows always take the first
   const size_t few = cache_attn_ws(dims->d_h, sm_count()).total;
-  const size_t all = attn_ws(*dims, n_q).total;
-  return few > all ? few : all;
+  const size_t many = cache_chunk_ws(dims->d_h, sm_count()).total;
+  return (long long)n_q * (dims->H / dims->H_kv) <= 16 || few > many ? few : many;
 }
 
 saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_static,
@@ -187,7 +197,8 @@ saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_sta
   if (any_static && T_pat > 0 && (bad16(alpha) || bad16(rho))) return SAF_ERR_INVALID_ARG;
   if (bad16(out) || (lse && !aligned16(lse)) || !workspace) return SAF_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SAF_ERR_INVALID_ARG;
-  const CacheAttnWs w = attn_ws(*dims, n_q);
+  const bool many = many_rows(*dims, p.c.is_static, n_q);
+  const CacheAttnWs w = many ? cache_chunk_ws(dims->d_h, sm_count()) : cache_attn_ws(dims->d_h, sm_count());
   if (ws_bytes < w.total) return SAF_ERR_INVALID_ARG;
   p.Q = static_cast<const uint16_t*>(Q);
   p.alpha = alpha;
@@ -200,7 +211,7 @@ saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_sta
   p.join = reinterpret_cast<int4*>(ws + w.join);
   p.ml = reinterpret_cast<float*>(ws + w.ml);
   p.acc = reinterpret_cast<float*>(ws + w.acc);
-  return status_of((many_rows(*dims, n_q) ? launch_cache_chunk : launch_cache_attn)(
+  return status_of((many ? launch_cache_chunk : launch_cache_attn)(
       p, dims->d_h, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 

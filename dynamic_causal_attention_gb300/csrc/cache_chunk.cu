@@ -6,8 +6,8 @@
 // A unit is (slot, class, row pair): a class is the dynamic or the frozen
 // query heads of one K/V head; its rows are r = t * heads + index (dynamic: the
 // last key that a unit sees is then as early as can be) or r = index * n_new + t
-// (frozen: a warp's rows share alpha and read rho side by side; from 128 new
-// tokens on each head begins a unit of its own), and a unit takes 256 of them as two tiles of 128, against the keys up to the last
+// (frozen: each head begins a unit of its own, whose rows share alpha and read
+// rho side by side), and a unit takes 256 of them as two tiles of 128, against the keys up to the last
 // position among them in tiles of 128.  Splitting a group by kind keeps every
 // warp uniform and spares frozen rows the Q K product.  All tiles of all
 // units are cut into equal shares, one for each CTA (one per SM), as in
@@ -123,11 +123,9 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// The rows of a class fall into units of up to 256.  Frozen heads with many
-// new tokens do not share a unit.
-__device__ __forceinline__ bool by_head(const Rows& r, bool ice) { return ice && r.n_new >= 128; }
+// The rows of a class fall into units of up to 256; a frozen head shares none.
 __device__ __forceinline__ int pairs_of(const Rows& r, int gk, bool ice) {
-  if (by_head(r, ice)) return (r.n_new + kRows - 1) / kRows * gk;
+  if (ice) return (r.n_new + kRows - 1) / kRows * gk;
   return (int)(((long long)r.n_new * gk + kRows - 1) / kRows);
 }
 struct UnitRows {
@@ -135,7 +133,7 @@ struct UnitRows {
 };
 __device__ __forceinline__ UnitRows unit_rows(const Rows& r, int pair, int gk, bool ice) {
   UnitRows u;
-  if (by_head(r, ice)) {
+  if (ice) {
     const int per = (r.n_new + kRows - 1) / kRows, idx = pair / per, at = (pair - idx * per) * kRows;
     u.first = idx * r.n_new + at;
     u.n = min(kRows, r.n_new - at);
@@ -155,10 +153,6 @@ __device__ __forceinline__ Span pair_span(const Rows& r, int pair, int gk, bool 
   if (ice) {
     s.lo = u.first % r.n_new;
     s.hi = s.lo + u.n;
-    if (s.hi > r.n_new) {  // the rows go on with the next head's first token
-      s.lo = 0;
-      s.hi = r.n_new;
-    }
   } else {
     s.lo = u.first / gk;
     s.hi = (u.first + u.n - 1) / gk + 1;
@@ -172,10 +166,6 @@ __device__ __forceinline__ int pair_extent(const Rows& r, int pair, int gk, bool
 __device__ __forceinline__ int pair_tiles(const Rows& r, int pair, int gk, bool ice) {
   const int n = (pair_extent(r, pair, gk, ice) + kTile - 1) / kTile;
   return n < 1 ? 1 : n;  // rows that see nothing are written too
-}
-// Whether a unit's rows are of one frozen head.
-__device__ __forceinline__ bool one_head(const Rows& r, const UnitRows& u) {
-  return u.first / r.n_new == (u.first + u.n - 1) / r.n_new;
 }
 // Row `rr` of a class as (token, index of the head).
 __device__ __forceinline__ void row_of(const Rows& r, int rr, int gk, bool ice, int& t, int& idx) {
@@ -318,7 +308,7 @@ struct Smem {
   static constexpr int OFF_K = 4 * TILE;
   static constexpr int OFF_R = OFF_K + KST * CODES;
   static constexpr int OFF_META = OFF_R + RST * CODES;  // 4 tiles x 8 groups of 16 keys x 16 bytes
-  // frozen rows of one head: 128 alphas and the 384 rhos of a tile, times
+  // frozen rows: 128 alphas and the 384 rhos of a tile, times
   // log2(e), for 4 tiles
   static constexpr int OFF_PAT = OFF_META + 4 * 8 * 16;
   static constexpr int OFF_SCAN = OFF_PAT + 4 * 2048;
@@ -516,7 +506,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(q_full + g);
           }
           float m = -CUDART_INF_F, l = 0.f;
-          const bool windowed = ice && one_head(w.rows, unit);
           for (int i = tile; i < tile_end; ++i) {
             const uint32_t nt = n_tile + (i - tile);
             mbar_wait(m_full + (nt & 3), (nt >> 2) & 1, wc, kSiteMeta);
@@ -546,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
                   asm volatile("" : "+f"(gm[0]), "+f"(gm[1]), "+f"(gm[2]), "+f"(gm[3]));
-                } else if (windowed) {
+                } else {
                   // distance of (row, column k): entry (row of the unit) - k + 127
                   const float* pat =
                       reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
@@ -559,16 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     y[1] = __float_as_uint(x.y + win[-k - 1]);
                     y[2] = __float_as_uint(x.z + win[-k - 2]);
                     y[3] = __float_as_uint(x.w + win[-k - 3]);
-                  }
-                } else {
-                  const float* al = p.a.alpha + (size_t)h * p.a.T_pat + j0;
-                  const int d0 = pos - j0;  // distance of column 0
-                  const float* rh = p.a.rho + (size_t)h * p.a.T_pat + d0;
-#pragma unroll
-                  for (int k = 0; k < 64; ++k) {
-                    const bool ok = j0 + k < p.a.T_pat && d0 - k >= 0 && d0 - k < p.a.T_pat;
-                    s[k / 16][k % 16] = __float_as_uint(
-                        ok ? (__ldg(al + k) + __ldg(rh - k)) * kLog2e : -CUDART_INF_F);
                   }
                 }
                 if (edge) {
@@ -908,12 +887,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 kh >= 0 ? __ldg(reinterpret_cast<const float*>(rec + c.off_ks) + kh) : 1.f,
                 __ldg(reinterpret_cast<const float*>(rec + c.off_vs) + kv));
           };
-          // frozen rows of one head: the lane's 4 alphas and 12 rhos of a tile
+          // frozen rows: the lane's 4 alphas and 12 rhos of a tile
           const UnitRows unit = unit_rows(w.rows, w.pair, w.gk(), w.ice());
-          const bool windowed = w.ice() && one_head(w.rows, unit);
           const float *al = nullptr, *rh = nullptr;
           int d_lo = 0;  // distance of the window's first entry, plus the tile's first key
-          if (windowed) {
+          if (w.ice()) {
             int t0, idx;
             row_of(w.rows, unit.first, w.gk(), true, t0, idx);
             const size_t h = (size_t)p.order[p.cls_first[w.cls] + idx] * p.a.T_pat;
@@ -923,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float pat[16];
           auto fetch_pattern = [&](int tl) {
-            if (!windowed || tl >= tile_end) return;
+            if (!w.ice() || tl >= tile_end) return;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int j = tl * kTile + lane + 32 * k;
@@ -962,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float4(sc.x, there ? __log2f(sc.y) : -CUDART_INF_F,
                               there ? __fdividef(1.f, sc.y) : 1.f, 0.f);
             }
-            if (windowed) {
+            if (w.ice()) {
               float* to = reinterpret_cast<float*>(smem + L::OFF_PAT + (vc & 3) * 2048) + lane;
 #pragma unroll
               for (int k = 0; k < 16; ++k) to[32 * k] = pat[k];

@@ -4,12 +4,17 @@
 // pages are taken lowest first, in the order of the slots; the only atomics
 // are integer additions, whose order does not matter.
 //
-// `grow` and `compact` each plan in one CTA (a run of the counts for each
-// thread, one block scan) and carry the plan out with the whole GPU: table
-// entries, counts and the copies of pages, which are what takes time.
+// `grow` and `compact` plan in one CTA, or for large pools in a cluster of
+// eight that exchange their sums through each other's shared memory: each walks
+// its part of the reference counts with block-wide scans.  The plan is carried
+// out with the whole GPU: table entries, counts and the copies of pages, which
+// are what takes time.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "cache_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace saf {
 namespace {
@@ -65,30 +70,114 @@ __device__ __forceinline__ Scratch scratch_of(const CachePages& p) {
   return s;
 }
 
-// The pages of one thread: a run of whole groups of four.
-struct Run {
+constexpr int kRowPages = 4 * kPlan;  // four pages for each thread
+constexpr int kPlanRows = 2;          // rows of a step of the walk, all loaded at once
+constexpr int kStepPages = kPlanRows * kRowPages;
+
+// The counts of pages base + 4 i .. base + 4 i + 3 (i: the thread); pages
+// behind the last one count as neither free nor used.
+struct Four {
+  int v[4];
+  unsigned used, exist;  // bit k: page k
+};
+__device__ __forceinline__ Four four_pages(const int32_t* ref, int n_pages, int base) {
+  Four f;
+  const int first = base + 4 * (int)threadIdx.x;
+  f.used = f.exist = 0;
+  if (first + 4 <= n_pages) {
+    const int4 x = *reinterpret_cast<const int4*>(ref + first);
+    f.v[0] = x.x, f.v[1] = x.y, f.v[2] = x.z, f.v[3] = x.w;
+    f.exist = 15;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f.v[k] = first + k < n_pages ? ref[first + k] : 0;
+      f.exist |= (first + k < n_pages ? 1u : 0u) << k;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f.used |= (f.v[k] > 0 ? 1u : 0u) << k;
+  return f;
+}
+
+// The pages of one CTA of the plan's cluster.
+struct Part {
   int begin, end;
 };
-__device__ __forceinline__ Run page_run(int n_pages) {
-  const long long per = ((((long long)n_pages + kPlan - 1) / kPlan) + 3) & ~3ll;
-  Run r;
-  r.begin = (int)min((long long)n_pages, per * threadIdx.x);
-  r.end = (int)min((long long)n_pages, per * threadIdx.x + per);
+__device__ __forceinline__ Part part_of(int n_pages) {
+  const long long n = gridDim.x, per = ((n_pages + n - 1) / n + 3) & ~3ll;
+  Part r;
+  r.begin = (int)min((long long)n_pages, per * blockIdx.x);
+  r.end = (int)min((long long)n_pages, per * blockIdx.x + per);
   return r;
 }
-// f(page, in use) over the run, counts read four at a time
-template <class F>
-__device__ __forceinline__ void each_page(const int32_t* ref, Run r, F f) {
-  int i = r.begin;
-#pragma unroll 4
-  for (; i + 4 <= r.end; i += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(ref + i);
-    f(i, v.x > 0);
-    f(i + 1, v.y > 0);
-    f(i + 2, v.z > 0);
-    f(i + 3, v.w > 0);
+
+// All threads of the plan, and what they wrote.
+__device__ __forceinline__ void plan_sync() {
+  if (gridDim.x > 1)
+    cg::this_cluster().sync();
+  else
+    __syncthreads();
+}
+
+// x summed over the CTA's threads, then over the cluster: the sum of the CTAs
+// before this one and of all.  Every thread of the cluster calls it; `box` is a
+// shared word used for nothing else.
+struct Sums {
+  long long before, all;
+};
+__device__ Sums cluster_sums(long long x, long long* warp_sums, long long* box) {
+  long long mine;
+  block_scan(x, warp_sums, mine);
+  Sums s = {0, mine};
+  if (gridDim.x == 1) return s;
+  s.all = 0;
+  if (threadIdx.x == 0) *box = mine;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (unsigned i = 0; i < gridDim.x; ++i) {
+    const long long y = *cluster.map_shared_rank(box, i);
+    if (i < blockIdx.x) s.before += y;
+    s.all += y;
   }
-  for (; i < r.end; ++i) f(i, ref[i] > 0);
+  return s;
+}
+
+// Ranks of the marked pages of a step among all marked pages of the step: of
+// the thread's first one in each row; returns the step's total.  One barrier
+// before the sums are read; the caller lets two steps use different `sums`.
+__device__ __forceinline__ int step_ranks(const unsigned (&marked)[kPlanRows],
+                                          int (*sums)[32] /* [kPlanRows] */,
+                                          int (&rank)[kPlanRows]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned before = (1u << lane) - 1;
+#pragma unroll
+  for (int j = 0; j < kPlanRows; ++j) {
+    int mine = 0;
+    rank[j] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned b = __ballot_sync(~0u, marked[j] >> k & 1);
+      rank[j] += __popc(b & before);
+      mine += __popc(b);
+    }
+    if (lane == 0) sums[j][warp] = mine;
+  }
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int j = 0; j < kPlanRows; ++j) {
+    int x = sums[j][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    const int up_to = __shfl_sync(~0u, x, warp ? warp - 1 : 0);
+    rank[j] += total + (warp ? up_to : 0);
+    total += __shfl_sync(~0u, x, 31);
+  }
+  return total;
 }
 
 // Copies pages from[k] -> to[k], k < n, in chunks over the whole grid.
@@ -130,7 +219,7 @@ __device__ __forceinline__ Need slot_need(const CachePages& p, int s) {
   d.tail = -1;
   if (d.n > 0 && (len & (size - 1))) {
     const int t = p.table[(size_t)s * p.max_pages + (len >> p.page_shift)];
-    if ((unsigned)t < (unsigned)p.n_pages && p.ref_out[t] > 1) d.tail = t;
+    if ((unsigned)t < (unsigned)p.n_pages && p.ref[t] > 1) d.tail = t;
   }
   return d;
 }
@@ -139,8 +228,11 @@ __device__ __forceinline__ Need slot_need(const CachePages& p, int s) {
 // first, then its new columns), and whether there are enough.
 __global__ void __launch_bounds__(kPlan) grow_plan_kernel(const __grid_constant__ CachePages p) {
   __shared__ long long sums[33];
+  __shared__ int ranks[2][kPlanRows][32];
+  __shared__ long long box;
+  asm volatile("griddepcontrol.launch_dependents;");
   const Scratch w = scratch_of(p);
-  // needs in the low 44 bits, copies above
+  // needs in the low 44 bits, copies above; every CTA adds up all slots
   const int per = (p.n_seqs + kPlan - 1) / kPlan;
   const int s0 = min(p.n_seqs, (int)threadIdx.x * per), s1 = min(p.n_seqs, s0 + per);
   long long mine = 0;
@@ -148,26 +240,72 @@ __global__ void __launch_bounds__(kPlan) grow_plan_kernel(const __grid_constant_
     const Need d = slot_need(p, s);
     mine += d.columns + (d.tail >= 0) + ((long long)(d.tail >= 0) << 44);
   }
-  long long all, n_free;
+  long long all;
   long long at = block_scan(mine, sums, all);
   const long long total = all & ((1ll << 44) - 1);
-  const Run run = page_run(p.n_pages);
-  long long free_mine = 0;
-  each_page(p.ref_out, run, [&](int, bool used) { free_mine += !used; });
-  long long rank = block_scan(free_mine, sums, n_free);
-  const bool ok = total <= n_free;
-  if (threadIdx.x == 0) {
+  const Part part = part_of(p.n_pages);
+  // the first row stays in registers: all there is of a small pool
+  const Four first_row = four_pages(p.ref, part.end, part.begin);
+  long long n_mine = __popc(~first_row.used & first_row.exist);
+#pragma unroll 4
+  for (int base = part.begin + kRowPages; base < part.end; base += kRowPages) {
+    const Four f = four_pages(p.ref, part.end, base);
+    n_mine += __popc(~f.used & f.exist);
+  }
+  // (also: no CTA writes before all have read the lengths)
+  const Sums free_pages = cluster_sums(n_mine, sums, &box);
+  const bool ok = total <= free_pages.all;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     w.head[0] = ok ? 1 : 0;
     w.head[1] = ok ? (int)(all >> 44) : 0;
-    const long long lack = ok ? 0 : total - n_free;
+    const long long lack = ok ? 0 : total - free_pages.all;
     *p.count = lack > 0x7fffffff ? 0x7fffffff : (int)lack;
   }
-  if (ok && free_mine > 0 && rank < total)
-    each_page(p.ref_out, run, [&](int page, bool used) {
-      if (!used && rank < total) w.list[rank] = page;
-      rank += !used;
-    });
-  __syncthreads();  // every thread reads the list
+  // the first `total` free pages go into the list and get a count of one; the
+  // other counts are copied where the call has its own output
+  const bool in_place = p.ref == p.ref_out;
+  long long rank0 = free_pages.before;
+  for (int base = part.begin, step = 0; base < part.end; base += kStepPages, ++step) {
+    if (in_place && (!ok || rank0 >= total)) break;
+    Four f[kPlanRows];
+    unsigned marked[kPlanRows];
+    int rank[kPlanRows];
+#pragma unroll
+    for (int j = 0; j < kPlanRows; ++j) {
+      f[j] = j == 0 && step == 0 ? first_row
+                                 : four_pages(p.ref, part.end, base + j * kRowPages);
+      marked[j] = ~f[j].used & f[j].exist;
+    }
+    const int n = step_ranks(marked, ranks[step & 1], rank);
+#pragma unroll
+    for (int j = 0; j < kPlanRows; ++j) {
+      const int first = base + j * kRowPages + 4 * (int)threadIdx.x;
+      long long at_rank = rank0 + rank[j];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool free = marked[j] >> k & 1, take = ok && free && at_rank < total;
+        if (take) {
+          w.list[at_rank] = first + k;
+          f[j].v[k] = 1;
+          if (in_place) p.ref_out[first + k] = 1;
+        }
+        at_rank += free;
+      }
+      if (!in_place) {
+        if (f[j].exist == 15)
+          *reinterpret_cast<int4*>(p.ref_out + first) =
+              make_int4(f[j].v[0], f[j].v[1], f[j].v[2], f[j].v[3]);
+        else
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (f[j].exist >> k & 1) p.ref_out[first + k] = f[j].v[k];
+      }
+    }
+    rank0 += n;
+  }
+  plan_sync();  // the list is whole; nobody reads a box any more
+  // each CTA writes the slots of its share of the threads
+  if ((int)(threadIdx.x * gridDim.x / kPlan) != (int)blockIdx.x) return;
   for (int s = s0; s < s1; ++s) {
     const Need d = slot_need(p, s);
     const long long base = at & ((1ll << 44) - 1);
@@ -188,20 +326,22 @@ __global__ void __launch_bounds__(kPlan) grow_plan_kernel(const __grid_constant_
 __global__ void __launch_bounds__(kCopy) grow_apply_kernel(const __grid_constant__ CachePages p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Scratch w = scratch_of(p);
-  if (!w.head[0]) return;
+  const bool in_place = p.table == p.table_out;
+  if (!w.head[0] && in_place) return;
   for (int s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
-    const int4 r = w.slots[s];
-    int32_t* row = p.table_out + (size_t)s * p.max_pages;
-    for (int i = threadIdx.x; i < r.y; i += kCopy) {
-      const int page = w.list[r.z + i];
-      row[r.x + i] = page;
-      p.ref_out[page] = 1;
+    const int4 r = w.slots[s];  // first new column, columns, place in the list, copy or -1
+    const size_t row = (size_t)s * p.max_pages;
+    const int own = r.w >= 0 ? r.x - 1 : -1;  // the column whose page becomes the slot's own
+    if (own >= 0 && threadIdx.x == 0) {
+      atomicSub(p.ref_out + p.table[row + own], 1);
+      p.table_out[row + own] = r.w;
     }
-    if (r.w >= 0 && threadIdx.x == 0) {  // the last page becomes the slot's own
-      atomicSub(p.ref_out + row[r.x - 1], 1);
-      row[r.x - 1] = r.w;
-      p.ref_out[r.w] = 1;
-    }
+    const int c0 = in_place ? r.x : 0, c1 = in_place ? r.x + r.y : p.max_pages;
+    for (int c = c0 + threadIdx.x; c < c1; c += kCopy)
+      if (c >= r.x && c < r.x + r.y)
+        p.table_out[row + c] = w.list[r.z + c - r.x];
+      else if (c != own)
+        p.table_out[row + c] = p.table[row + c];
   }
   copy_pages(p, w.from, w.to, w.head[1]);
 }
@@ -223,17 +363,23 @@ __global__ void __launch_bounds__(512)
     return;
   }
   const int c0 = blockIdx.x * width, n = min(width, p.max_pages - c0);
-  for (int i = threadIdx.x; i < p.n_seqs * n; i += blockDim.x) {
-    const int s = i / n, c = i - s * n;
-    old[s * width + c] = p.table[(size_t)s * p.max_pages + c0 + c];
+  // an element's row and column, a power of two apart
+  const int shift = width == 8 ? 3 : (width == 4 ? 2 : width - 1);
+  const int all = p.n_seqs << shift;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < all; i += 512) {
+    const int s = i >> shift, c = i & (width - 1);
+    if (c < n) old[i] = p.table[(size_t)s * p.max_pages + c0 + c];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.n_seqs * n; i += blockDim.x) {
-    const int s = i / n, c = i - s * n;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < all; i += 512) {
+    const int s = i >> shift, c = i & (width - 1);
+    if (c >= n) continue;
     const int q = p.parent[s];
-    const int was = old[s * width + c];
-    const int is = (unsigned)q < (unsigned)p.n_seqs ? old[q * width + c] : -1;
-    p.table_out[(size_t)s * p.max_pages + c0 + c] = is;
+    const int was = old[i];
+    const int is = (unsigned)q < (unsigned)p.n_seqs ? old[(q << shift) + c] : -1;
+    if (was != is || p.table != p.table_out) p.table_out[(size_t)s * p.max_pages + c0 + c] = is;
     if (was != is) {
       if ((unsigned)was < (unsigned)p.n_pages) atomicSub(p.ref_out + was, 1);
       if ((unsigned)is < (unsigned)p.n_pages) atomicAdd(p.ref_out + is, 1);
@@ -245,33 +391,81 @@ __global__ void __launch_bounds__(512)
 __global__ void __launch_bounds__(kPlan)
     compact_plan_kernel(const __grid_constant__ CachePages p) {
   __shared__ long long sums[33];
+  __shared__ int ranks[4][kPlanRows][32];
+  __shared__ long long boxes[2];
+  asm volatile("griddepcontrol.launch_dependents;");
   const Scratch w = scratch_of(p);
-  const Run run = page_run(p.n_pages);
-  long long used_mine = 0, n_used, both;
-  each_page(p.ref, run, [&](int, bool used) { used_mine += used; });
-  block_scan(used_mine, sums, n_used);
-  // used pages behind n_used in the low half, free pages before it above
-  long long mine = 0;
-  each_page(p.ref, run, [&](int page, bool used) {
-    if (used ? page >= n_used : page < n_used) mine += used ? 1 : 1ll << 32;
-  });
-  long long at = block_scan(mine, sums, both);
-  each_page(p.ref, run, [&](int page, bool used) {
-    if (used && page >= n_used) {
-      w.from[at & 0xffffffff] = page;
-      at += 1;
-    } else if (!used && page < n_used) {
-      w.to[at >> 32] = page;
-      at += 1ll << 32;
+  const Part part = part_of(p.n_pages);
+  // the first row stays in registers: all there is of a small pool
+  const Four first_row = four_pages(p.ref, part.end, part.begin);
+  long long n_mine = __popc(first_row.used);
+#pragma unroll 4
+  for (int base = part.begin + kRowPages; base < part.end; base += kRowPages)
+    n_mine += __popc(four_pages(p.ref, part.end, base).used);
+  const int n_used = (int)cluster_sums(n_mine, sums, &boxes[0]).all;
+  // free pages before n_used take the used pages behind it, in order: `front`
+  // marks the former and `back` the latter
+  auto bits = [&](const Four& f, int base, unsigned& front, unsigned& back) {
+    unsigned m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m |= (base + 4 * (int)threadIdx.x + k < n_used ? 1u : 0u) << k;
+    front = ~f.used & f.exist & m;
+    back = f.used & ~m;
+  };
+  long long both = 0;  // front in the low half, back above
+#pragma unroll 4
+  for (int base = part.begin; base < part.end; base += kRowPages) {
+    unsigned front, back;
+    bits(base == part.begin ? first_row : four_pages(p.ref, part.end, base), base, front, back);
+    both += __popc(front) + ((long long)__popc(back) << 32);
+  }
+  const Sums place = cluster_sums(both, sums, &boxes[1]);
+  int at_to = (int)(place.before & 0xffffffff), at_from = (int)(place.before >> 32);
+  for (int base = part.begin, step = 0; base < part.end; base += kStepPages, ++step) {
+    unsigned front[kPlanRows], back[kPlanRows];
+    int rank[kPlanRows];
+#pragma unroll
+    for (int j = 0; j < kPlanRows; ++j)
+      bits(j == 0 && step == 0 ? first_row
+                               : four_pages(p.ref, part.end, base + j * kRowPages),
+           base + j * kRowPages, front[j], back[j]);
+    const int first = base + 4 * (int)threadIdx.x;
+    if (base < n_used) {
+      const int n = step_ranks(front, ranks[step & 1], rank);
+#pragma unroll
+      for (int j = 0; j < kPlanRows; ++j) {
+        int k0 = at_to + rank[j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (front[j] >> k & 1) w.to[k0++] = first + j * kRowPages + k;
+      }
+      at_to += n;
     }
-    w.list[page] = page;
-  });
-  __syncthreads();
-  const int n = (int)(both & 0xffffffff);
-  for (int k = threadIdx.x; k < n; k += kPlan) w.list[w.from[k]] = w.to[k];
-  if (threadIdx.x == 0) {
+    if (base + kStepPages > n_used) {
+      const int n = step_ranks(back, ranks[2 + (step & 1)], rank);
+#pragma unroll
+      for (int j = 0; j < kPlanRows; ++j) {
+        int k0 = at_from + rank[j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int page = first + j * kRowPages + k;
+          if (back[j] >> k & 1)
+            w.from[k0++] = page;
+          else if (page >= n_used && page < part.end)
+            w.list[page] = page;  // a free page's entry, should a row hold one
+        }
+      }
+      at_from += n;
+    }
+  }
+  plan_sync();  // the lists are whole; nobody reads a box any more
+  const int n = (int)(place.all >> 32);
+  for (int k = blockIdx.x * kPlan + threadIdx.x; k < n; k += gridDim.x * kPlan)
+    w.list[w.from[k]] = w.to[k];
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     w.head[1] = n;
-    *p.count = (int)n_used;
+    w.head[2] = n_used;
+    *p.count = n_used;
   }
 }
 
@@ -279,22 +473,32 @@ __global__ void __launch_bounds__(kCopy)
     compact_apply_kernel(const __grid_constant__ CachePages p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Scratch w = scratch_of(p);
-  const int n = w.head[1];
+  const int n = w.head[1], n_used = w.head[2];
   const size_t tid = (size_t)blockIdx.x * kCopy + threadIdx.x, all = (size_t)gridDim.x * kCopy;
   for (size_t k = tid; k < (size_t)n; k += all) {
     const int from = w.from[k], to = w.to[k];
     p.ref_out[to] = p.ref[from];
-    p.ref_out[from] = 0;
+    if (p.ref == p.ref_out) p.ref_out[from] = 0;
   }
+  if (p.ref != p.ref_out)  // the places of moved pages are written above
+    for (size_t i = tid; i < (size_t)p.n_pages; i += all) {
+      const int r = p.ref[i];
+      if ((int)i >= n_used)
+        p.ref_out[i] = r > 0 ? 0 : r;
+      else if (r > 0)
+        p.ref_out[i] = r;
+    }
+  const bool in_place = p.table == p.table_out;
+#pragma unroll 4
   for (size_t i = tid; i < (size_t)p.n_seqs * p.max_pages; i += all) {
     const int page = p.table[i];
-    const int is = (unsigned)page < (unsigned)p.n_pages ? w.list[page] : page;
-    p.table_out[i] = is;
+    const int is = page >= n_used && page < p.n_pages ? w.list[page] : page;
+    if (is != page || !in_place) p.table_out[i] = is;
   }
   copy_pages(p, w.from, w.to, n);
 }
 
-// Launched while its predecessor runs; waits for the predecessor's end.
+// Launched while its predecessor runs (both plans allow it at their start); waits for the predecessor's end.
 template <class K>
 cudaError_t launch_after(K kernel, const char* name, const CachePages& p, int grid, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
@@ -303,6 +507,27 @@ cudaError_t launch_after(K kernel, const char* name, const CachePages& p, int gr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kCopy);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  trace_begin(s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  trace_end(s, name);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// One CTA plans for a pool of up to 8192 pages, a cluster of eight for more
+// (2048 pages: one CTA 6 us; 65536 pages: one CTA 25 us).
+template <class K>
+cudaError_t launch_plan(K kernel, const char* name, const CachePages& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  const unsigned n = p.n_pages > 8192 ? 8 : 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = n;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n);
+  cfg.blockDim = dim3(kPlan);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -341,25 +566,13 @@ cudaError_t launch_cache_fork(const CachePages& p, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_grow(const CachePages& p, int n_sms, cudaStream_t s) {
-  cudaError_t e = copy_words(p.ref_out, p.ref, p.n_pages, s);
-  if (e == cudaSuccess)
-    e = copy_words(p.table_out, p.table, (size_t)p.n_seqs * p.max_pages, s);
-  if (e != cudaSuccess) return e;
-  trace_begin(s);
-  grow_plan_kernel<<<1, kPlan, 0, s>>>(p);
-  trace_end(s, "cache_grow_plan");
-  e = cudaGetLastError();
+  const cudaError_t e = launch_plan(grow_plan_kernel, "cache_grow_plan", p, s);
   if (e != cudaSuccess) return e;
   return launch_after(grow_apply_kernel, "cache_grow", p, 4 * n_sms, s);
 }
 
 cudaError_t launch_cache_compact(const CachePages& p, int n_sms, cudaStream_t s) {
-  cudaError_t e = copy_words(p.ref_out, p.ref, p.n_pages, s);
-  if (e != cudaSuccess) return e;
-  trace_begin(s);
-  compact_plan_kernel<<<1, kPlan, 0, s>>>(p);
-  trace_end(s, "cache_compact_plan");
-  e = cudaGetLastError();
+  const cudaError_t e = launch_plan(compact_plan_kernel, "cache_compact_plan", p, s);
   if (e != cudaSuccess) return e;
   return launch_after(compact_apply_kernel, "cache_compact", p, 4 * n_sms, s);
 }

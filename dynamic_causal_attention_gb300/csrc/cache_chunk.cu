@@ -659,8 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // partial sums: [D / 4][row][4], so that a warp's stores are contiguous
             const size_t part = (size_t)(2 * blockIdx.x + (at == sh.begin ? 0 : 1)) * kRows;
             const int pr = g * 128 + r;
-            // results go through the row tile's Q buffer (its products are done)
+            // results go through the row's own place in the Q buffer (its products
+            // are done): other warps may be staging their rows of the next unit
             const uint32_t stage = sQ + g * L::TILE;
+            auto unit_of = [&](uint32_t row, uint32_t u) {
+              return stage + u / (D / 16) * L::CODES + code_at<D>(row, u % (D / 16));
+            };
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
               uint32_t o[32];
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (whole) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
-                  st_shared_v4(stage + unit_at<D>(r, 4 * q + k / 8),
+                  st_shared_v4(unit_of(r, 4 * q + k / 8),
                                pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
                                pack_bf16x2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
                                pack_bf16x2(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; i += kR) {
                 const int rl = i + lane / kL, u = lane % kL;
                 const int dst = __shfl_sync(~0u, mine, rl);
-                const float4 x = lds_f32x4(stage + unit_at<D>((warp & 3) * 32 + rl, u));
+                const float4 x = lds_f32x4(unit_of((warp & 3) * 32 + rl, u));
                 if (dst >= 0)
                   *(reinterpret_cast<float4*>(ob + (size_t)(unsigned)dst * D) + u) = x;
               }

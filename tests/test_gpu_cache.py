@@ -108,14 +108,14 @@ class Case:
         self.cache.attend(0, self.q, a, r, n_new=i32(self.n_new), out=out, lse=lse, **kw)
         return out, lse
 
-    def check(self, out, lse):
+    def check(self, out, lse, slots=slice(None)):
         want, want_lse, tol, lse_tol = ref.attend(
-            host(self.q.double()), self.k_codes, self.k_scales, self.v_codes, self.v_scales,
-            self.k_heads, self.alpha, self.rho, self.mask, self.table, self.lens, self.n_new,
-            self.page)
-        out, lse = host(out.double()), host(lse.double())
+            host(self.q[slots].double()), self.k_codes, self.k_scales, self.v_codes, self.v_scales,
+            self.k_heads, self.alpha, self.rho, self.mask, self.table[slots], self.lens[slots],
+            self.n_new[slots], self.page)
+        out, lse = host(out[slots].double()), host(lse[slots].double())
         n_q = self.q.shape[2]
-        live = np.arange(n_q)[None, :] < np.clip(self.n_new, 0, n_q)[:, None]
+        live = np.arange(n_q)[None, :] < np.clip(self.n_new[slots], 0, n_q)[:, None]
         live = np.broadcast_to(live[:, None], lse.shape)
         assert np.all(out[~live] == 7.0) and np.all(lse[~live] == 7.0), "rows behind n_new changed"
         got, want, tol = out[live], want[live], tol[live]
@@ -180,6 +180,14 @@ def test_prompt_chunks(api, d, page):
     # the first chunk of a prompt (nothing before it), and chunks behind a context
     c = Case(api, mask_of(8, (2, 3)), 4, d, page, [257, 700, 391], 257, n_new=[257, 130, 255], seed=9)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_many_short_prompts(api, d):
+    # several whole units of 64 rows for each CTA: half of a tile's warps have none
+    c = Case(api, mask_of(4, ()), 4, d, 64, [128 - (s * 7) % 64 for s in range(160)], 64, seed=5)
+    out, lse = c.run()
+    c.check(out, lse, slice(0, 160, 3))
 
 
 @pytest.mark.parametrize("n_q", [1, 3, 40])

@@ -60,7 +60,7 @@ constexpr long long kMinTiles = 1;
 
 enum : int {
   kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree,
-  kSiteRaw, kSiteRawFree
+  kSiteRaw, kSiteRawFree, kSiteBegin
 };
 
 // Instruction descriptor with f16 operands and fp32 sums.
@@ -313,9 +313,9 @@ struct Smem {
   static constexpr int OFF_PAT = OFF_META + 4 * 8 * 16;
   static constexpr int OFF_SCAN = OFF_PAT + 4 * 2048;
   static constexpr int OFF_BAR = OFF_SCAN + (kThreads / 32 + 4) * 8;
-  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 4 + 4 + 4 + 2;
+  static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 4 + 4 + 4 + 2 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int BYTES = OFF_MISC + 32;
+  static constexpr int BYTES = OFF_MISC + 48;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
   static_assert(ALLOC <= 232448, "shared memory budget exceeded");
 };
@@ -362,10 +362,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // P V done: its products, and the issuing thread itself, which has seen
   // v_full: what the converting warps wrote before is then visible
   uint64_t* o_done = p_full + 4;          // [4] (2)
-  uint64_t* drained = o_done + 4;         // [2] every product of an issuer done
+  // the issuer of row tile g has come to a unit in which the tile has rows: its
+  // softmax, which waits for nothing in units where it has none, may not run ahead
+  // of the ring of scales (a parity tells two neighbouring phases apart only)
+  uint64_t* begun = o_done + 4;           // [2] (1)
+  uint64_t* drained = begun + 2;          // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [4]
+  // of row tile g: the last of its units (counted from 1, at 4 g + count % 4) whose
+  // V holds NaN at an edge
+  int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [8]
   const WaitCtl wc{abort_flag, p.a.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -389,10 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(r_empty + i, 128);
     }
     for (int i = 0; i < 4; ++i) mbar_init(m_full + i, 32);
-    mbar_init(drained, 1);
-    mbar_init(drained + 1, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(begun + i, 1);
+      mbar_init(drained + i, 1);
+    }
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) nan_seg[i] = 0;
+    for (int i = 0; i < 8; ++i) nan_seg[i] = 0;
     fence_barrier_init();
     p.a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
@@ -423,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_col = trow + kS + g * 128, o_col = trow + kO + g * 128;
       uint32_t n_tile = 0, n_s = 0, n_p = 0;  // tiles of the CTA; S and P of this row tile
-      for (int seg = 0;; ++seg) {
+      uint32_t n_unit = 0;                    // units in which it has rows
+      for (;;) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
         const int gk = w.gk(), kv = p.cls_kv[w.cls];
         const bool ice = w.ice();
@@ -505,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(q_full + g);
           }
+          mbar_wait(begun + g, n_unit++ & 1, wc, kSiteBegin);
           float m = -CUDART_INF_F, l = 0.f;
           for (int i = tile; i < tile_end; ++i) {
             const uint32_t nt = n_tile + (i - tile);
@@ -640,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t nan[D / 32];
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) nan[q] = 0;
-            if (nan_seg[seg & 3] == seg + 1) {
+            if (nan_seg[4 * g + (n_unit & 3)] == (int)n_unit) {
               // V holds NaN at a key of an edge tile: rows that see it take it
               const int lo = w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo;
               const int first = max(0, lo / kTile * kTile);
@@ -734,8 +744,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that the stores of 8 lanes touch every bank
       const int ch = tid % kCh, row0 = (tid / kCh) ^ (D == 128 ? ch >> 2 : 0);
       uint32_t vc = 0;
-      for (int seg = 0;; ++seg) {
+      int n_unit[2] = {0, 0};
+      for (;;) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+        const bool both = unit_rows(w.rows, w.pair, w.gk(), w.ice()).n > 128;
+        ++n_unit[0];
+        n_unit[1] += both;
         // keys that not every row sees, and what lies behind the last key, may
         // hold NaN: 0 * NaN must not reach the other rows
         const int sure = min(w.rows.base + pair_span(w.rows, w.pair, w.gk(), w.ice()).lo + 1,
@@ -771,7 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(to + unit_at<D>(row, 2 * ch), y[0], y[1], y[2], y[3]);
             st_shared_v4(to + unit_at<D>(row, 2 * ch + 1), y[4], y[5], y[6], y[7]);
           }
-          if (bad) nan_seg[seg & 3] = seg + 1;
+          if (bad) {
+            nan_seg[n_unit[0] & 3] = n_unit[0];
+            if (both) nan_seg[4 + (n_unit[1] & 3)] = n_unit[1];
+          }
           fence_proxy_async_smem();
           mbar_arrive(v_full + st);
           mbar_arrive(r_empty + rs);
@@ -814,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(k_empty + kc % L::KST);
             ++kc;
           };
+          if (mine) mbar_arrive(begun + g);
           if (!ice) {
             wait_k(kc);
             if (mine) {

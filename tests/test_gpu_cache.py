@@ -190,6 +190,15 @@ def test_many_short_prompts(api, d):
     c.check(out, lse, slice(0, 160, 3))
 
 
+def test_frozen_heads_behind_short_units(api):
+    # 260 rows of the dynamic heads: a row of units of 256, then one of 4, whose second tile of
+    # rows is empty, then the frozen heads' units with both
+    c = Case(api, mask_of(24, range(2, 24, 3)), 8, 32, 64, [600 - 3 * s for s in range(16)], 130,
+             seed=6)
+    out, lse = c.run()
+    c.check(out, lse, slice(0, 16, 3))
+
+
 @pytest.mark.parametrize("n_q", [1, 3, 40])
 @pytest.mark.parametrize("d,page", [(128, 64), (64, 16), (32, 128)])
 def test_holes_and_dirty_pages(api, d, page, n_q):

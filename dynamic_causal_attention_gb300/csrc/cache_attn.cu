@@ -51,6 +51,7 @@ constexpr int kWarps = 4;
 // second kernel.
 constexpr int kMinTiles = 4;     // least share of a CTA
 constexpr int kWholeKeys = 512;
+constexpr int kJoinAhead = 8;    // parts that a joining thread has in flight
 
 template <int D>
 struct Geo {
@@ -164,7 +165,7 @@ constexpr int smem_bytes() {
 
 template <int D, int NT>  // NT: 8 query rows each
 __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
-    cache_attn_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool whole_units) {
+    cache_attn_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool whole_units, bool by_unit) {
   constexpr int kMR = 8 * NT;
   constexpr int kG = Geo<D>::kGroups, kStep = Geo<D>::kStep, kTile = Geo<D>::kTile;
   constexpr int kKS = D / 16;            // steps of 16 along d
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     sh.end = sh.size = n;
   } else {
     sh = find_share<kTile>(c, per_slot, scan);
-    if (threadIdx.x == 0) p.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x == 0 && !by_unit) p.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (sh.begin >= sh.end) return;
   }
 
@@ -641,10 +642,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
           *reinterpret_cast<float2*>(p.ml + ((size_t)part * kMR + r) * 2) = make_float2(mx, sum);
       }
     }
-    if (!whole && tile == 0 && threadIdx.x == 0) {
-      // the unit begins here and ends in CTA `last`
-      const int last = (int)((at + ut - 1) / sh.size);
-      p.join[blockIdx.x] = make_int4(b, unit, last, at == sh.begin ? 0 : 1);
+    if (tile == 0 && threadIdx.x == 0 && !whole_units) {
+      // the unit begins here and ends in CTA `last`; only the last that begins here
+      // can be cut
+      const int left = max(0, (int)(at + ut - sh.end));  // tiles behind this CTA's
+      const int last = blockIdx.x + cta_span(left, sh.size);
+      p.join[by_unit ? b * per_slot + unit : blockIdx.x] =
+          make_int4(tile_end < ut ? b : -1, unit, blockIdx.x, last | (at == sh.begin ? 0 : 1 << 30));
     }
 
     // ---- the next unit
@@ -662,65 +666,36 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
   }
 }
 
-// Joins the parts of a unit that was cut: CTA x takes the unit that CTA x of
-// the first kernel left to its successors; y splits the rows.
+// Joins the parts of a unit that was cut; x: the unit, or the CTA that left it
+// to its successors; y: slices of its rows.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttn p, int row_tiles) {
+__global__ void __launch_bounds__(kJoinThreads)
+    cache_join_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool by_unit, int split) {
   constexpr int kMR = 8 * NT;
   const CacheCall& c = p.c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 u = p.join[blockIdx.x];
-  if (u.x < 0) return;
+  const bool none = by_unit && slot_rows(c, blockIdx.x / (c.H_kv * row_tiles)).n_new == 0;
+  if (none || u.x < 0) return;  // (a slot without rows has no entries)
   const int b = u.x, kv = u.y / row_tiles, r0 = (u.y - kv * row_tiles) * kMR;
-  const int last = u.z, first = 2 * blockIdx.x + u.w;
+  const int cta = u.z, last = u.w & ~(1 << 30);
+  const int n = last - cta + 1, first = 2 * cta + (u.w >> 30 & 1);
   const int n_rows = min(kMR, slot_rows(c, b).n_new * c.group - r0);
-  for (int i = blockIdx.y * 128 + threadIdx.x; i < n_rows * (D / 4); i += gridDim.y * 128) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    auto ml = [&](int part) {
-      return *reinterpret_cast<const float2*>(p.ml + ((size_t)part * kMR + r) * 2);
-    };
-    // parts 0 .. n - 1, in the order of the CTAs; eight at a time are in flight
-    const int n = last - blockIdx.x + 1;
-    auto part = [&](int k) { return k == 0 ? first : 2 * ((int)blockIdx.x + k); };
-    float mx = -CUDART_INF_F, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float2 w[8];
-      float4 x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < n) {
-          w[k] = ml(part(k0 + k));
-          x[k] = *reinterpret_cast<const float4*>(p.acc +
-                                                  ((size_t)part(k0 + k) * kMR + r) * D + d);
-        }
-      float top = mx;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < n) top = fmaxf(top, w[k].x);
-      // (a part that saw nothing holds zeros: it takes no part, but a NaN does)
-      const float f0 = top == -CUDART_INF_F ? 1.f : fast_exp2(mx - top);
-      mx = top;
-      sum *= f0;
-      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < n) {
-          const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(w[k].x - mx);
-          sum = fmaf(f, w[k].y, sum);
-          o.x = fmaf(f, x[k].x, o.x);
-          o.y = fmaf(f, x[k].y, o.y);
-          o.z = fmaf(f, x[k].z, o.z);
-          o.w = fmaf(f, x[k].w, o.w);
-        }
-    }
-    const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
-    const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2*>(p.out + row * D + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (d == 0 && p.lse) p.lse[row] = (mx + log2f(sum)) * kLn2;
-  }
+  const int per = kJoinThreads / split, s = threadIdx.x / per;
+  const int i = blockIdx.y * per + threadIdx.x % per;
+  const int r = i / (D / 4), d = i % (D / 4) * 4;
+  const Part x = join_parts<kJoinAhead>(s, split, n, r < n_rows, [&](int k) {
+    const size_t at = (size_t)(k == 0 ? first : 2 * (cta + k)) * kMR + r;
+    const float2 ml = *reinterpret_cast<const float2*>(p.ml + at * 2);
+    return Part{ml.x, ml.y, *reinterpret_cast<const float4*>(p.acc + at * D + d)};
+  });
+  if (s || r >= n_rows) return;
+  const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
+  const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
+  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+  *reinterpret_cast<uint2*>(p.out + row * D + d) =
+      make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+  if (d == 0 && p.lse) p.lse[row] = (x.m + log2f(x.l)) * kLn2;
 }
 
 int n_ctas(int nt, int n_sms) { return n_sms * (nt == 1 ? kCtas<1> : kCtas<2>); }
@@ -729,12 +704,14 @@ template <int D, int NT>
 cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   const bool whole = (long long)p.c.max_pages << p.c.page_shift <= kWholeKeys;
   const int row_tiles = (p.c.n_q * p.c.group + 8 * NT - 1) / (8 * NT);
-  const int grid = whole ? p.c.n_seqs * p.c.H_kv * row_tiles : n_ctas(NT, n_sms);
+  const long long units = (long long)p.c.n_seqs * p.c.H_kv * row_tiles;
+  const bool by_unit = units <= n_ctas(NT, n_sms);
+  const int grid = whole ? (int)units : n_ctas(NT, n_sms);
   cudaError_t e = set_max_dynamic_smem(
       reinterpret_cast<const void*>(cache_attn_kernel<D, NT>), smem_bytes<D, NT>());
   if (e != cudaSuccess) return e;
   trace_begin(s);
-  cache_attn_kernel<D, NT><<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, row_tiles, whole);
+  cache_attn_kernel<D, NT><<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, row_tiles, whole, by_unit);
   trace_end(s, "cache_attn");
   e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
@@ -743,13 +720,14 @@ cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(128);
+  const int split = join_split(grid, units);
+  cfg.gridDim = dim3(by_unit ? (int)units : grid, (8 * NT * (D / 4) * split + kJoinThreads - 1) / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   trace_begin(s);
-  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, p, row_tiles);
+  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, p, row_tiles, by_unit, split);
   trace_end(s, "cache_join");
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -770,7 +748,8 @@ CacheAttnWs cache_attn_ws(int d_h, int n_sms) {
     return o;
   };
   // the larger of both row counts
-  const size_t n = (size_t)n_ctas(1, n_sms), rows = 2 * (n * 8 > (size_t)n_ctas(2, n_sms) * 16 ? n * 8 : (size_t)n_ctas(2, n_sms) * 16);
+  const size_t n = (size_t)n_ctas(1, n_sms), n2 = (size_t)n_ctas(2, n_sms);
+  const size_t rows = 2 * (n * 8 > n2 * 16 ? n * 8 : n2 * 16);
   w.status = take(256);
   w.join = take(n * sizeof(int4));
   w.ml = take(rows * 2 * 4);

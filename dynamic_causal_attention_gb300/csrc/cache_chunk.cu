@@ -57,6 +57,10 @@ constexpr int kThreads = 512;
 // registers of a thread after the split: 2 * 176 + 80 + 80 = 4 * 128
 constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsIssue = 80;
 constexpr long long kMinTiles = 1;
+// parts that a joining thread has in flight: with 4, 64 registers and 8 blocks of
+// an SM, 152 units of 2 to 4 parts take 17 us, with 8 and half the blocks 34
+constexpr int kJoinAhead = 4;
+constexpr int kStatusCtas = 64;  // status words of the CTAs, behind the call's
 
 enum : int {
   kSiteQ = 64, kSiteK, kSiteV, kSiteP, kSiteO, kSiteS, kSiteMeta, kSiteKFree, kSiteVFree,
@@ -237,6 +241,11 @@ struct Walk {
       }
     }
   }
+  // among all that the slots could have
+  __device__ int number() const {
+    return b * p.slot_units + p.group_unit[group] + pair * classes(group) + cls -
+           p.group_first[group];
+  }
   __device__ void next() {
     if (++cls == p.group_first[group + 1]) {
       if (++pair >= pairs_of(rows, gk(), ice())) {
@@ -252,6 +261,11 @@ struct Walk {
       ut = pair_tiles(rows, pair, gk(), ice());
     }
   }
+};
+
+template <bool V>
+struct Const {
+  static constexpr bool value = V;
 };
 
 struct Share {
@@ -329,11 +343,52 @@ __device__ __forceinline__ uint32_t code_at(uint32_t r, uint32_t ch) {
   return r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
 }
 
+// The first 16 of w to 64 contiguous bytes.
+__device__ __forceinline__ void st_global_words16(void* to, const uint32_t (&w)[32], bool wide) {
+  uint4* p = reinterpret_cast<uint4*>(to);
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + i / 4),
+                   "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                   "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+    } else {
+      p[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      p[i / 4 + 1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+    }
+}
+
 // Byte offset of 16-byte unit u of row r of a [128 x D] f16 tile.
 template <int D>
 __device__ __forceinline__ uint32_t unit_at(uint32_t r, uint32_t u) {
   if (D == 32) return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
   return (u >> 3) * 16384u + sw128_offset(r, u & 7);
+}
+
+// A warp fetches 32 rows of Q of a unit of dynamic heads, from row r0 of row tile
+// g, side by side (kL lanes to a row): 8 components lie where 16 codes of hi or lo
+// will, an even piece in hi's place and an odd one in lo's.
+template <int D>
+__device__ __forceinline__ void fetch_q(const CacheChunk& p, const Walk& w, const UnitRows& unit,
+                                        int g, int r0, uint32_t stage) {
+  constexpr int kL = D / 8, kR = 32 / kL;
+  const int lane = threadIdx.x & 31;
+  int mine = -1;
+  if (g * 128 + r0 + lane < unit.n) {
+    int t, idx;
+    row_of(w.rows, unit.first + g * 128 + r0 + lane, w.gk(), false, t, idx);
+    mine = (int)((size_t)p.order[p.cls_first[w.cls] + idx] * p.a.c.n_q + t);
+  }
+  const uint16_t* slot_q = p.a.Q + (size_t)w.b * p.a.c.H * p.a.c.n_q * D;
+#pragma unroll 2
+  for (int i = 0; i < 32; i += kR) {
+    const int rl = i + lane / kL, u = lane % kL;
+    const int src = __shfl_sync(~0u, mine, rl);
+    cp_async16(stage + (u & 1) * (kTile * D) + code_at<D>(r0 + rl, u >> 1),
+               slot_q + (size_t)(unsigned)max(src, 0) * D + u * 8, src >= 0 ? 16 : 0);
+  }
+  cp_async_commit();
 }
 
 template <int D>
@@ -366,13 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // softmax, which waits for nothing in units where it has none, may not run ahead
   // of the ring of scales (a parity tells two neighbouring phases apart only)
   uint64_t* begun = o_done + 4;           // [2] (1)
-  uint64_t* drained = begun + 2;          // [2] every product of an issuer done
+  uint64_t* drained = begun + 2;           // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   // of row tile g: the last of its units (counted from 1, at 4 g + count % 4) whose
   // V holds NaN at an edge
   int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [8]
-  const WaitCtl wc{abort_flag, p.a.status};
+  const WaitCtl wc{abort_flag, p.a.status + kStatusCtas + blockIdx.x};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -402,7 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) nan_seg[i] = 0;
     fence_barrier_init();
-    p.a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (!p.by_unit) p.a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    *wc.status = 0;
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
   if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
@@ -431,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_col = trow + kS + g * 128, o_col = trow + kO + g * 128;
       uint32_t n_tile = 0, n_s = 0, n_p = 0;  // tiles of the CTA; S and P of this row tile
+      bool staged = false;                    // the unit's rows of Q are on their way
       uint32_t n_unit = 0;                    // units in which it has rows
       for (;;) {
         const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
@@ -449,25 +510,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           float fac = 1.f;
           if (!ice) {
             // The row of Q, scaled by the least 2^-e that brings it within e4m3's
-            // range and split into hi + lo.  The rows come in side by side
-            // (kL lanes to a row); 8 components lie where 16 codes of hi or lo
-            // will, an even unit's in hi's place and an odd one's in lo's, so that
-            // each thread turns its row into codes where it lies.
-            constexpr int kL = D / 8, kR = 32 / kL;
+            // range and split into hi + lo: each thread turns its row into codes
+            // where it lies.  In f16, which loses nothing here: hi is at most 4 bits
+            // of the value's 8, and what f16 rounds off (2^-25) is far below e4m3's
+            // least step (2^-9).
             const uint32_t stage = sQ + g * L::TILE;
-            const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
-            const uint16_t* slot_q = p.a.Q + (size_t)w.b * c.H * c.n_q * D;
-#pragma unroll 4
-            for (int i = 0; i < 32; i += kR) {
-              const int rl = i + lane / kL, u = lane % kL;
-              const int src = __shfl_sync(~0u, mine, rl);
-              cp_async16(stage + (u & 1) * L::CODES + code_at<D>((warp & 3) * 32 + rl, u >> 1),
-                         slot_q + (size_t)(unsigned)max(src, 0) * D + u * 8, src >= 0 ? 16 : 0);
-            }
-            cp_async_commit();
+            if (!staged) fetch_q<D>(p, w, unit, g, (warp & 3) * 32, stage);
+            staged = false;
             cp_async_wait<0>();
             __syncwarp();
-            float amax = 0.f;
+            __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
 #pragma unroll 2
             for (int u = 0; u < D / 16; ++u) {
               uint32_t y[8];
@@ -476,13 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stage + L::CODES + code_at<D>(r, u));
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                amax = fmax3(amax, fabsf(__uint_as_float(y[k] << 16)),
-                             fabsf(__uint_as_float(y[k] & 0xffff0000u)));
+                top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[k])));
             }
+            const float amax = fmaxf(__low2float(top2), __high2float(top2));
             const int bits = __float_as_int(amax);
             int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
             e = amax > 0.f ? max(-126, min(120, e)) : 0;
-            const float down = pow2f(-e);
+            // e4m3 has no infinity: the row becomes NaN, as its softmax would
+            const float down = amax == CUDART_INF_F ? CUDART_NAN_F : pow2f(-e);
             fac = pow2f(e) * (rsqrtf((float)D) * kLog2e);
 #pragma unroll 2
             for (int u = 0; u < D / 16; ++u) {
@@ -492,21 +545,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stage + L::CODES + code_at<D>(r, u));
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                float z[4] = {__uint_as_float(y[2 * k] << 16),
-                              __uint_as_float(y[2 * k] & 0xffff0000u),
-                              __uint_as_float(y[2 * k + 1] << 16),
-                              __uint_as_float(y[2 * k + 1] & 0xffff0000u)};
+                uint32_t c2[2], d2[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  // e4m3 has no infinity: the row becomes NaN, as its softmax would
-                  z[j] = fabsf(z[j]) == CUDART_INF_F ? CUDART_NAN_F : z[j] * down;
+                for (int j = 0; j < 2; ++j) {
+                  const uint32_t v = y[2 * k + j];
+                  const uint32_t z = pack_f16x2(__uint_as_float(v << 16) * down,
+                                                __uint_as_float(v & 0xffff0000u) * down);
+                  c2[j] = f16x2_e4m3x2(z);
+                  const uint32_t f = e4m3x2_f16x2((uint16_t)c2[j]);
+                  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&z),
+                                               *reinterpret_cast<const __half2*>(&f));
+                  d2[j] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
                 }
-                hi[k] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
-                uint32_t c0, c1;
-                e4m3x4_f16x4(hi[k], c0, c1);
-                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&c0));
-                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
-                lo[k] = e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
+                hi[k] = c2[0] | c2[1] << 16;
+                lo[k] = d2[0] | d2[1] << 16;
               }
               st_shared_v4(stage + code_at<D>(r, u), hi[0], hi[1], hi[2], hi[3]);
               st_shared_v4(stage + L::CODES + code_at<D>(r, u), lo[0], lo[1], lo[2], lo[3]);
@@ -516,129 +568,145 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_wait(begun + g, n_unit++ & 1, wc, kSiteBegin);
           float m = -CUDART_INF_F, l = 0.f;
-          for (int i = tile; i < tile_end; ++i) {
-            const uint32_t nt = n_tile + (i - tile);
-            mbar_wait(m_full + (nt & 3), (nt >> 2) & 1, wc, kSiteMeta);
+          auto softmax = [&](auto kind) {
+            constexpr bool kIce = decltype(kind)::value;
+            for (int i = tile; i < tile_end; ++i) {
+              const uint32_t nt = n_tile + (i - tile);
+              mbar_wait(m_full + (nt & 3), (nt >> 2) & 1, wc, kSiteMeta);
 #pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-              const int bar = 2 * g + hf;
-              // a half's P V of the tile before is done when its S is: that S was
-              // issued after it
-              if (!ice)
-                mbar_wait(s_full + bar, n_s & 1, wc, kSiteS);
-              else if (n_p > 0)
-                mbar_wait(o_done + bar, (n_p - 1) & 1, wc, kSiteO);
-              __syncwarp();
-              tc_fence_after();
-              if (warp_live) {
-                const uint32_t meta = sM + (nt & 3) * 128 + 64 * hf;
-                const uint32_t col = s_col + 64 * hf;
-                const int j0 = i * kTile + 64 * hf;
-                const int lim = lim_all - j0;  // columns below it are seen
-                const bool edge = __any_sync(~0u, lim < 64);
-                // a row of S: 4 groups of 16 keys, each of one page with one scale
-                uint32_t s[4][16];
-                float gm[4];
-                if (!ice) {
+              for (int hf = 0; hf < 2; ++hf) {
+                const int bar = 2 * g + hf;
+                // a half's P V of the tile before is done when its S is: that S was
+                // issued after it
+                if (!kIce)
+                  mbar_wait(s_full + bar, n_s & 1, wc, kSiteS);
+                else if (n_p > 0)
+                  mbar_wait(o_done + bar, (n_p - 1) & 1, wc, kSiteO);
+                __syncwarp();
+                tc_fence_after();
+                if (warp_live) {
+                  const uint32_t meta = sM + (nt & 3) * 128 + 64 * hf;
+                  const uint32_t col = s_col + 64 * hf;
+                  const int j0 = i * kTile + 64 * hf;
+                  const int lim = lim_all - j0;  // columns below it are seen
+                  const bool edge = __any_sync(~0u, lim < 64);
+                  // a row of S: 4 groups of 16 keys, each of one page with one scale
+                  uint32_t s[4][16];
+                  float gm[4];
+                  if (!kIce) {
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) tmem_ld_max_x16(col + 16 * q, s[q], gm[q]);
+                    for (int q = 0; q < 4; ++q) tmem_ld_max_x16(col + 16 * q, s[q], gm[q]);
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
-                  asm volatile("" : "+f"(gm[0]), "+f"(gm[1]), "+f"(gm[2]), "+f"(gm[3]));
-                } else {
-                  // distance of (row, column k): entry (row of the unit) - k + 127
-                  const float* pat =
-                      reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
-                  const float* win = pat + 128 + g * 128 + r + 127 - 128 * hf;
+                    for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
+                    asm volatile("" : "+f"(gm[0]), "+f"(gm[1]), "+f"(gm[2]), "+f"(gm[3]));
+                  } else {
+                    // distance of (row, column k): entry (row of the unit) - k + 127
+                    const float* pat =
+                        reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
+                    const float* win = pat + 128 + g * 128 + r + 127 - 128 * hf;
 #pragma unroll
-                  for (int k = 0; k < 64; k += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(pat + k);
-                    uint32_t* y = s[k / 16] + k % 16;
-                    y[0] = __float_as_uint(x.x + win[-k]);
-                    y[1] = __float_as_uint(x.y + win[-k - 1]);
-                    y[2] = __float_as_uint(x.z + win[-k - 2]);
-                    y[3] = __float_as_uint(x.w + win[-k - 3]);
-                  }
-                }
-                if (edge) {
-#pragma unroll
-                  for (int k = 0; k < 64; ++k)
-                    if (k >= lim) s[k / 16][k % 16] = 0xff800000u;
-                }
-                if (edge || ice) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    float x = fmax3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]),
-                                    __uint_as_float(s[q][2]));
-#pragma unroll
-                    for (int k = 3; k < 15; k += 2)
-                      x = fmax3(x, __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
-                    gm[q] = fmaxf(x, __uint_as_float(s[q][15]));
-                  }
-                }
-                float a[4], b[4], inv[4], top = -CUDART_INF_F;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float4 mt = lds_f32x4(meta + 16 * q);
-                  a[q] = ice ? 1.f : fac * mt.x;
-                  b[q] = mt.y;
-                  inv[q] = mt.z;
-                  top = fmaxf(top, fmaf(gm[q], a[q], b[q]));
-                }
-                // the maximum moves only when it would grow by more than 2^8:
-                // weights up to 2^8 fit f16 as well
-                const bool need = top > m + 8.f;
-                if (__any_sync(~0u, need)) {
-                  const float corr = need ? fast_exp2(m - top) : 1.f;
-                  if (need) m = top;
-                  l *= corr;
-                  if (i > tile || hf) {
-                    // the last product into O: the other half's
-                    mbar_wait(o_done + (bar ^ 1), (hf ? n_p : n_p - 1) & 1, wc, kSiteO);
-                    __syncwarp();
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int q = 0; q < D; q += 16) {
-                      uint32_t o[16];
-                      tmem_ld_x16(o_col + q, o);
-                      tmem_wait_ld(o);
-#pragma unroll
-                      for (int k = 0; k < 16; ++k)
-                        o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                      tmem_st_x16(o_col + q, o);
+                    for (int k = 0; k < 64; k += 4) {
+                      const float4 x = *reinterpret_cast<const float4*>(pat + k);
+                      uint32_t* y = s[k / 16] + k % 16;
+                      y[0] = __float_as_uint(x.x + win[-k]);
+                      y[1] = __float_as_uint(x.y + win[-k - 1]);
+                      y[2] = __float_as_uint(x.z + win[-k - 2]);
+                      y[3] = __float_as_uint(x.w + win[-k - 3]);
                     }
                   }
-                }
-                const float base = m == -CUDART_INF_F ? 0.f : m;
+                  if (edge) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint64_t a2 = f2_pack(a[q], a[q]), b2 = f2_pack(b[q] - base, b[q] - base);
-                  uint64_t sum = 0;
-                  uint32_t pk[8];
-#pragma unroll
-                  for (int k = 0; k < 16; k += 2) {
-                    float x, y;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][k]),
-                                             __uint_as_float(s[q][k + 1])),
-                                     a2, b2),
-                              x, y);
-                    x = fast_exp2(x);
-                    y = fast_exp2(y);
-                    sum = f2_add(sum, f2_pack(x, y));
-                    pk[k / 2] = pack_f16x2(x, y);
+                    for (int k = 0; k < 64; ++k)
+                      if (k >= lim) s[k / 16][k % 16] = 0xff800000u;
                   }
-                  float x, y;
-                  f2_unpack(sum, x, y);
-                  l = fmaf(x + y, inv[q], l);
-                  tmem_st_x8(col + 8 * q, pk);
+                  if (edge || kIce) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                      float x = fmax3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]),
+                                      __uint_as_float(s[q][2]));
+#pragma unroll
+                      for (int k = 3; k < 15; k += 2)
+                        x = fmax3(x, __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
+                      gm[q] = fmaxf(x, __uint_as_float(s[q][15]));
+                    }
+                  }
+                  float a[4], b[4], inv[4], top = -CUDART_INF_F;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const float4 mt = lds_f32x4(meta + 16 * q);
+                    a[q] = kIce ? 1.f : fac * mt.x;
+                    b[q] = mt.y;
+                    inv[q] = mt.z;
+                    top = fmaxf(top, fmaf(gm[q], a[q], b[q]));
+                  }
+                  // the maximum moves only when it would grow by more than 2^8:
+                  // weights up to 2^8 fit f16 as well
+                  const bool need = top > m + 8.f;
+                  if (__any_sync(~0u, need)) {
+                    const float corr = need ? fast_exp2(m - top) : 1.f;
+                    if (need) m = top;
+                    l *= corr;
+                    if (i > tile || hf) {
+                      // the last product into O: the other half's
+                      mbar_wait(o_done + (bar ^ 1), (hf ? n_p : n_p - 1) & 1, wc, kSiteO);
+                      __syncwarp();
+                      tc_fence_after();
+#pragma unroll 1
+                      for (int q = 0; q < D; q += 16) {
+                        uint32_t o[16];
+                        tmem_ld_x16(o_col + q, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                          o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                        tmem_st_x16(o_col + q, o);
+                      }
+                    }
+                  }
+                  const float base = m == -CUDART_INF_F ? 0.f : m;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const uint64_t a2 = f2_pack(a[q], a[q]), b2 = f2_pack(b[q] - base, b[q] - base);
+                    uint64_t sum = 0;
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                      float x, y;
+                      f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][k]),
+                                               __uint_as_float(s[q][k + 1])),
+                                       a2, b2),
+                                x, y);
+                      x = fast_exp2(x);
+                      y = fast_exp2(y);
+                      sum = f2_add(sum, f2_pack(x, y));
+                      pk[k / 2] = pack_f16x2(x, y);
+                    }
+                    float x, y;
+                    f2_unpack(sum, x, y);
+                    l = fmaf(x + y, inv[q], l);
+                    tmem_st_x8(col + 8 * q, pk);
+                  }
+                  tmem_wait_st();
                 }
-                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + bar);
               }
-              tc_fence_before();
-              mbar_arrive(p_full + bar);
+              if (!kIce) ++n_s;
+              ++n_p;
             }
-            if (!ice) ++n_s;
-            ++n_p;
+          };
+          if (ice)
+            softmax(Const<true>());
+          else
+            softmax(Const<false>());
+          // ---- the next unit's rows of Q, now that no product reads this one's: they
+          // come while this one ends
+          if (at + (tile_end - tile) < sh.end) {
+            Walk x = w;
+            x.next();
+            const UnitRows u0 = unit_rows(x.rows, x.pair, x.gk(), x.ice());
+            staged = !x.ice() && g * 128 < u0.n;
+            if (staged) fetch_q<D>(p, x, u0, g, (warp & 3) * 32, sQ + g * L::TILE);
           }
           // ---- results
           mbar_wait(o_done + 2 * g, (n_p - 1) & 1, wc, kSiteO);
@@ -650,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t nan[D / 32];
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) nan[q] = 0;
-            if (nan_seg[4 * g + (n_unit & 3)] == (int)n_unit) {
+            const bool edge_nan = nan_seg[4 * g + (n_unit & 3)] == (int)n_unit;
+            if (edge_nan) {
               // V holds NaN at a key of an edge tile: rows that see it take it
               const int lo = w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo;
               const int first = max(0, lo / kTile * kTile);
@@ -669,30 +738,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             // partial sums: [D / 4][row][4], so that a warp's stores are contiguous
             const size_t part = (size_t)(2 * blockIdx.x + (at == sh.begin ? 0 : 1)) * kRows;
             const int pr = g * 128 + r;
-            // results go through the row's own place in the Q buffer (its products
-            // are done): other warps may be staging their rows of the next unit
-            const uint32_t stage = sQ + g * L::TILE;
-            auto unit_of = [&](uint32_t row, uint32_t u) {
-              return stage + u / (D / 16) * L::CODES + code_at<D>(row, u % (D / 16));
-            };
+            // a thread's row goes out in whole sectors where the base allows it: half as
+            // many accesses as 16 bytes at a time
+            uint16_t* to = p.a.out + row * D;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.a.out) & 31) == 0;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
               uint32_t o[32];
               tmem_ld_x32(o_col + 32 * q, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
-                if (nan[q] >> k & 1) o[k] = 0x7fc00000u;
-              }
-              if (whole) {
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+              if (edge_nan) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                  st_shared_v4(unit_of(r, 4 * q + k / 8),
-                               pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
-                               pack_bf16x2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
-                               pack_bf16x2(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
-                               pack_bf16x2(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
+                for (int k = 0; k < 32; ++k)
+                  if (nan[q] >> k & 1) o[k] = 0x7fc00000u;
+              }
+              if (whole && live) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                  o[k / 2] = pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1]));
+                st_global_words16(to + 32 * q, o, wide);
               } else if (live) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
@@ -701,31 +767,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                       make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
               }
             }
-            if (whole) {
-              __syncwarp();
-              constexpr int kL = D / 8, kR = 32 / kL;
-              const int mine = live ? (int)((size_t)h * c.n_q + t) : -1;
-              uint16_t* ob = p.a.out + (size_t)w.b * c.H * c.n_q * D;
-#pragma unroll 4
-              for (int i = 0; i < 32; i += kR) {
-                const int rl = i + lane / kL, u = lane % kL;
-                const int dst = __shfl_sync(~0u, mine, rl);
-                const float4 x = lds_f32x4(unit_of((warp & 3) * 32 + rl, u));
-                if (dst >= 0)
-                  *(reinterpret_cast<float4*>(ob + (size_t)(unsigned)dst * D) + u) = x;
-              }
-              __syncwarp();
-            }
             if (live && whole && p.a.lse) p.a.lse[row] = (m + log2f(l)) * kLn2;
             if (live && !whole)
               *reinterpret_cast<float2*>(p.a.ml + (part + pr) * 2) = make_float2(m, l);
           }
         }
-        if (threadIdx.x == 0 && tile == 0 && tile_end < w.ut) {
-          // the unit begins here and ends in CTA `last`
-          const int last = (int)((at + w.ut - 1) / sh.size);
-          p.a.join[blockIdx.x] =
-              make_int4(w.b, w.pair, w.cls, last | (at == sh.begin ? 0 : 1 << 30));
+        if (threadIdx.x == 0 && tile == 0) {
+          // the unit begins here and ends in CTA `last`; only the last that begins
+          // here can be cut
+          const int left = max(0, (int)(at + w.ut - sh.end));  // tiles behind this CTA's
+          const int last = blockIdx.x + cta_span(left, sh.size);
+          p.a.join[p.by_unit ? w.number() : blockIdx.x] =
+              make_int4(tile_end < w.ut ? w.b << 8 | w.cls : -1, w.pair, blockIdx.x,
+                        last | (at == sh.begin ? 0 : 1 << 30));
         }
         n_tile += tile_end - tile;
         at += tile_end - tile;
@@ -815,8 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool mine = unit_rows(w.rows, w.pair, w.gk(), ice).n > g * 128;
           // K of tile i + 1 and V of tile i are waited for while a product of the
           // tile before runs, so that the waits are not part of the row tile's chain
-          auto wait_k = [&](uint32_t n) { mbar_poll(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK); };
-          auto wait_v = [&](uint32_t n) { mbar_poll(v_full + (n & 1), (n >> 1) & 1, wc, kSiteV); };
+          auto wait_k = [&](uint32_t n) { poll_bar(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK); };
+          auto wait_v = [&](uint32_t n) { poll_bar(v_full + (n & 1), (n >> 1) & 1, wc, kSiteV); };
           // S of 64 keys: the tile's first or second half
           auto issue_s = [&](int hf) {
             const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES + hf * 64 * D, 16, 8 * D,
@@ -835,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ice) {
             wait_k(kc);
             if (mine) {
-              mbar_poll(q_full + g, n_q++ & 1, wc, kSiteQ);
+              poll_bar(q_full + g, n_q++ & 1, wc, kSiteQ);
               tc_fence_after();
               issue_s(0);
               issue_s(1);
@@ -853,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int hf = 0; hf < 2; ++hf) {
                 const int bar = 2 * g + hf;
-                mbar_poll(p_full + bar, n_p & 1, wc, kSiteP);
+                poll_bar(p_full + bar, n_p & 1, wc, kSiteP);
                 tc_fence_after();
                 issue_pv<kVStep>(o_col, s_col + 64 * hf, vt + 4 * kVStep * hf, id_o,
                                  i > tile || hf);
@@ -867,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // S takes the columns of the P that these products read
                 if (more) {
-                  mbar_poll(o_done + bar, n_p & 1, wc, kSiteO);
+                  poll_bar(o_done + bar, n_p & 1, wc, kSiteO);
                   tc_fence_after();
                   issue_s(hf);
                 }
@@ -1001,17 +1055,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of a unit that was cut (see cache_attn.cu); x: the CTA that
-// left it, y: slices of its rows.
+// Joins the parts of a unit that was cut (see cache_attn.cu); x: the unit or the
+// CTA that left it, y: slices of its rows.  One block also gathers the CTAs' status.
 template <int D>
-__global__ void __launch_bounds__(256)
-    cache_chunk_join_kernel(const __grid_constant__ CacheChunk p) {
+__global__ void __launch_bounds__(kJoinThreads, 8)
+    cache_chunk_join_kernel(const __grid_constant__ CacheChunk p, int n_ctas, int split) {
   const CacheCall& c = p.a.c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    __shared__ int worst;
+    if (threadIdx.x == 0) worst = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_ctas; i += kJoinThreads)
+      if (p.a.status[kStatusCtas + i]) worst = p.a.status[kStatusCtas + i];
+    __syncthreads();
+    if (threadIdx.x == 0) p.a.status[0] = worst;
+  }
+  if (p.by_unit) {  // a unit that the slot has no rows for has no entry
+    const int b = blockIdx.x / p.slot_units, at = blockIdx.x - b * p.slot_units;
+    int g = 0;
+    while (g + 1 < p.n_groups && at >= p.group_unit[g + 1]) ++g;
+    const int pair = (at - p.group_unit[g]) / (p.group_first[g + 1] - p.group_first[g]);
+    if (pair >= pairs_of(slot_rows(c, b), p.group_width[g], p.group_static[g])) return;
+  }
   const int4 u = p.a.join[blockIdx.x];
   if (u.x < 0) return;
-  const int b = u.x, pair = u.y, cls = u.z, last = u.w & ~(1 << 30);
-  const int first = 2 * blockIdx.x + (u.w >> 30 & 1);
+  const int b = u.x >> 8, cls = u.x & 255, pair = u.y, cta = u.z, last = u.w & ~(1 << 30);
+  const int n = last - cta + 1, first = 2 * cta + (u.w >> 30 & 1);
   const Rows rows = slot_rows(c, b);
   int gk = 0;
   bool ice = false;
@@ -1021,63 +1091,33 @@ __global__ void __launch_bounds__(256)
       ice = p.group_static[g];
     }
   const UnitRows unit = unit_rows(rows, pair, gk, ice);
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < kRows * (D / 4); i += gridDim.y * 256) {
-    const int r = i % kRows, d = i / kRows * 4;
-    if (r >= unit.n) continue;
-    auto ml = [&](int part) {
-      return *reinterpret_cast<const float2*>(p.a.ml + ((size_t)part * kRows + r) * 2);
-    };
-    // parts 0 .. n - 1, in the order of the CTAs; four at a time are in flight
-    const int n = last - blockIdx.x + 1;
-    auto part = [&](int k) { return k == 0 ? first : 2 * ((int)blockIdx.x + k); };
-    float mx = -CUDART_INF_F, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 4) {
-      float2 w[4];
-      float4 x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k0 + k < n) {
-          w[k] = ml(part(k0 + k));
-          x[k] = *reinterpret_cast<const float4*>(p.a.acc + (size_t)part(k0 + k) * kRows * D +
-                                                  ((size_t)(d / 4) * kRows + r) * 4);
-        }
-      float top = mx;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k0 + k < n) top = fmaxf(top, w[k].x);
-      // (a part that saw nothing holds zeros: it takes no part)
-      const float f0 = top == -CUDART_INF_F ? 1.f : fast_exp2(mx - top);
-      mx = top;
-      sum *= f0;
-      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k0 + k < n) {
-          const float f = mx == -CUDART_INF_F ? 1.f : fast_exp2(w[k].x - mx);
-          sum = fmaf(f, w[k].y, sum);
-          o.x = fmaf(f, x[k].x, o.x);
-          o.y = fmaf(f, x[k].y, o.y);
-          o.z = fmaf(f, x[k].z, o.z);
-          o.w = fmaf(f, x[k].w, o.w);
-        }
+  const int per = kJoinThreads / split, s = threadIdx.x / per;
+  for (int i0 = blockIdx.y * per; i0 < kRows * (D / 4); i0 += gridDim.y * per) {
+    const int i = i0 + threadIdx.x % per, r = i % kRows, d = i / kRows * 4;
+    const Part x = join_parts<kJoinAhead>(s, split, n, r < unit.n, [&](int k) {
+      const size_t at = (size_t)(k == 0 ? first : 2 * (cta + k)) * kRows;
+      const float2 ml = *reinterpret_cast<const float2*>(p.a.ml + (at + r) * 2);
+      return Part{ml.x, ml.y,
+                  *reinterpret_cast<const float4*>(p.a.acc + at * D +
+                                                   ((size_t)(d / 4) * kRows + r) * 4)};
+    });
+    if (s == 0 && r < unit.n) {
+      int t, idx;
+      row_of(rows, unit.first + r, gk, ice, t, idx);
+      const int h = p.order[p.cls_first[cls] + idx];
+      const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
+      const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+      *reinterpret_cast<uint2*>(p.a.out + row * D + d) =
+          make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+      if (d == 0 && p.a.lse) p.a.lse[row] = (x.m + log2f(x.l)) * kLn2;
     }
-    int t, idx;
-    row_of(rows, unit.first + r, gk, ice, t, idx);
-    const int h = p.order[p.cls_first[cls] + idx];
-    const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2*>(p.a.out + row * D + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (d == 0 && p.a.lse) p.a.lse[row] = (mx + log2f(sum)) * kLn2;
+    if (split > 1) __syncthreads();  // the threads' parts are read
   }
 }
 
 template <int D>
 cudaError_t launch(const CacheChunk& p, int n_sms, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(p.a.status, 0, sizeof(int), s);
-  if (e != cudaSuccess) return e;
-  e = set_max_dynamic_smem(reinterpret_cast<const void*>(cache_chunk_kernel<D>), Smem<D>::ALLOC);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(cache_chunk_kernel<D>), Smem<D>::ALLOC);
   if (e != cudaSuccess) return e;
   trace_begin(s);
   const CacheCall& c = p.a.c;
@@ -1096,13 +1136,16 @@ cudaError_t launch(const CacheChunk& p, int n_sms, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_sms, 8);
-  cfg.blockDim = dim3(256);
+  const long long units = (long long)p.slot_units * c.n_seqs;
+  const int split = join_split(n_sms, units);
+  cfg.gridDim = dim3(p.by_unit ? (int)units : n_sms,
+                     kRows * (D / 4) * split / kJoinThreads / (p.by_unit ? 1 : 2));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   trace_begin(s);
-  e = cudaLaunchKernelEx(&cfg, cache_chunk_join_kernel<D>, p);
+  e = cudaLaunchKernelEx(&cfg, cache_chunk_join_kernel<D>, p, n_sms, split);
   trace_end(s, "cache_chunk_join");
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1117,7 +1160,7 @@ CacheAttnWs cache_chunk_ws(int d_h, int n_sms) {
     off = (off + bytes + 255) & ~(size_t)255;
     return o;
   };
-  w.status = take(256);
+  w.status = take((kStatusCtas + (size_t)n_sms) * sizeof(int));
   w.join = take((size_t)n_sms * sizeof(int4));
   w.ml = take((size_t)2 * n_sms * kRows * 2 * 4);
   w.acc = take((size_t)2 * n_sms * kRows * d_h * 4);
@@ -1161,6 +1204,15 @@ cudaError_t launch_cache_chunk(const CacheAttn& a, int d_h, int n_sms, cudaStrea
       }
     }
   p.group_first[p.n_groups] = n;
+  long long units = 0;
+  for (int g = 0; g < p.n_groups; ++g) {
+    const long long w = p.group_width[g], q = c.n_q;
+    p.group_unit[g] = (int)units;
+    units += (p.group_static[g] ? (q + kRows - 1) / kRows * w : (q * w + kRows - 1) / kRows) *
+             (p.group_first[g + 1] - p.group_first[g]);
+  }
+  p.slot_units = (int)units;  // no more than rows: below 2^31
+  p.by_unit = units * c.n_seqs <= n_sms;
   switch (d_h) {
     case 32: return launch<32>(p, n_sms, s);
     case 64: return launch<64>(p, n_sms, s);

@@ -49,6 +49,13 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
+// e4m3 of two f16 values, saturating; the NaN code for NaN
+__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+
 // Two e4m3 codes (low and high byte of v) as packed f16: exact (f16 holds
 // every e4m3 value); the NaN code becomes NaN.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
@@ -63,7 +70,7 @@ __device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t&
   hi = e4m3x2_f16x2(b);
 }
 
-// e4m3 of two values, saturating; the NaN code for NaN
+// ... of two values
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -101,6 +108,32 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // 2^e as fp32 for e in [-126, 127].
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
+// A bounded wait whose rare part is a call, for a thread that a whole CTA waits on:
+// what follows the wait then lies right behind it.
+static __device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+                                              int* status, int site) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_test_wait(bar, parity)) return;
+    if (*abort) return;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+      *abort = 1;
+      atomicCAS(status, 0, site);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void poll_bar(uint64_t* bar, uint32_t parity, const WaitCtl& w,
+                                         int site) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 512; ++i)
+    if (mbar_test_wait(a, parity)) return;
+  wait_long(a, parity, w.abort, w.status, site);
+}
+
 // ------------------------------------------------------------ the rows of a call
 // Slot b takes n_new(b) of the n_q rows that the call holds for each slot;
 // row t stands at position seq_len - n_new + t.  Lengths beyond the page
@@ -129,6 +162,84 @@ __device__ __forceinline__ Rows slot_rows(const CacheCall& c, int b) {
 __device__ __forceinline__ int page_at(const CacheCall& c, int b, int col) {
   const int p = __ldg(c.page_table + (size_t)b * c.max_pages + col);
   return (unsigned)p < (unsigned)c.n_pages ? p : -1;
+}
+
+// CTAs that `tiles` more tiles take in shares of `size`; 32 bits are enough: a
+// unit has fewer than 2^27 tiles.
+__device__ __forceinline__ int cta_span(int tiles, long long size) {
+  const unsigned s = (unsigned)(size < 0x40000000 ? size : 0x40000000);
+  return (int)(((unsigned)tiles + s - 1) / s);
+}
+
+// ------------------------------------------------------------ joining parts
+// A unit of attention that was cut leaves one part per CTA: for each row the
+// maximum m of its exponents (to base 2), l = sum of the weights relative to m,
+// and the weighted sum o, of which a thread takes 4 components.  Parts are added
+// in the order of the CTAs.
+struct Part {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void add_part(Part& a, const Part& b) {
+  // (a part that saw nothing holds zeros: it takes no part, but a NaN does)
+  const float top = fmaxf(a.m, b.m);
+  const float fa = top == -INFINITY ? 1.f : fast_exp2(a.m - top);
+  const float fb = top == -INFINITY ? 1.f : fast_exp2(b.m - top);
+  a.m = top;
+  a.l = fmaf(a.l, fa, b.l * fb);
+  a.o.x = fmaf(a.o.x, fa, b.o.x * fb);
+  a.o.y = fmaf(a.o.y, fa, b.o.y * fb);
+  a.o.z = fmaf(a.o.z, fa, b.o.z * fb);
+  a.o.w = fmaf(a.o.w, fa, b.o.w * fb);
+}
+// Threads of a joining block, and what it splits them by: `split` of them take
+// every split-th part of the same 4 components.  What a unit of many parts costs
+// is the latency of its loads, so many parts want many threads; few parts want
+// few blocks.  For the same reason blocks are counted by units where there are
+// fewer of them than CTAs.  (One token against 29242, 4 K/V heads in 152 parts
+// each: 41 us with a thread for all parts of its components, 18.1 us so.)
+constexpr int kJoinThreads = 128, kJoinSplit = 8;
+inline int join_split(long long ctas, long long units) {
+  return ctas > 8 * units ? kJoinSplit : 1;
+}
+// All threads of the block call this; load(k) reads part k of the thread's
+// components.  The result is that of the threads with s = 0.
+template <int kAhead, class Load>
+__device__ __forceinline__ Part join_parts(int s, int split, int n, bool live, const Load& load) {
+  __shared__ Part others[kJoinThreads];
+  Part a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (live)
+    for (int k0 = s; k0 < n; k0 += kAhead * split) {
+      Part x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k0 + k * split < n) x[k] = load(k0 + k * split);
+      float top = a.m;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k0 + k * split < n) top = fmaxf(top, x[k].m);
+      const float f0 = top == -INFINITY ? 1.f : fast_exp2(a.m - top);
+      a.m = top;
+      a.l *= f0;
+      a.o = make_float4(a.o.x * f0, a.o.y * f0, a.o.z * f0, a.o.w * f0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k0 + k * split < n) {
+          const float f = top == -INFINITY ? 1.f : fast_exp2(x[k].m - top);
+          a.l = fmaf(f, x[k].l, a.l);
+          a.o.x = fmaf(f, x[k].o.x, a.o.x);
+          a.o.y = fmaf(f, x[k].o.y, a.o.y);
+          a.o.z = fmaf(f, x[k].o.z, a.o.z);
+          a.o.w = fmaf(f, x[k].o.w, a.o.w);
+        }
+    }
+  if (split > 1) {
+    others[threadIdx.x] = a;
+    __syncthreads();
+    if (s == 0)
+      for (int k = 1; k < split; ++k) add_part(a, others[threadIdx.x + k * (kJoinThreads / split)]);
+  }
+  return a;
 }
 
 }  // namespace saf

@@ -141,7 +141,7 @@ struct CacheAttn {
   float* lse;     // [n_seqs, H, n_q] or null
   // scratch: see cache_attn_ws
   int* status;
-  int4* join;     // [n_ctas] the unit that a CTA leaves to its successors, or none
+  int4* join;     // [n_ctas] the units that were cut, by CTA or by unit
   float* ml;      // [2 n_ctas, rows, 2]
   float* acc;     // [2 n_ctas, rows, d]
 };
@@ -161,6 +161,10 @@ struct CacheChunk {
   int group_first[kMaxHeads + 1];   // its first class
   int16_t cls_first[kMaxHeads];     // a class's heads: order[cls_first ...]
   uint8_t cls_kv[kMaxHeads], order[kMaxHeads];
+  // units that a slot can have, and of them the first of each group; whether
+  // `join` is ordered by units (no more of them than CTAs)
+  int slot_units, group_unit[kMaxHeads];
+  bool by_unit;
 };
 CacheAttnWs cache_chunk_ws(int d_h, int n_sms);
 cudaError_t launch_cache_chunk(const CacheAttn& p, int d_h, int n_sms, cudaStream_t s);

@@ -87,23 +87,28 @@ saf_status make_call(const saf_cache_dims& d, const uint8_t* head_is_static, con
   return SAF_OK;
 }
 
-// Which kernel takes an attention call of n_q rows.  cache_attn.cu reads a
-// head's keys once for every 16 rows (from L2 after the first); cache_chunk.cu
-// once for 256 rows of the dynamic heads and once for 256 of each frozen one.
-// Measured over 16 x 8192 tokens, d_h = 128, 2 K/V heads: 12 us plus 15 us for
-// every 16 rows against 58 us for a unit of dynamic rows (4 to 256 rows alike)
-// plus 32 us for a unit of a frozen head, so a row tile counts 10, the units 36
-// and 20.  (48 rows: 59 and 58 us; 128 rows: 129 and 61 us.)
+// Which kernel takes an attention call of n_q rows.  cache_attn.cu starts fast
+// and reads a head's keys once for every 8 or 16 rows (from L2 after the first);
+// cache_chunk.cu takes longer to start and reads them once for 256 rows of the
+// dynamic heads and once for 256 of each frozen one.  What the host knows of the
+// lengths is the page table's width.  The times are in nanoseconds on the whole
+// GPU for a unit of rows and for each of its keys, fitted to 220 calls drawn at
+// random that were timed with both: the choice costs 0.2% over the better one (by
+// rows alone, 8%).  E.g. 3 x 159 rows of 64 components: 8 us here and 18 us
+// there; 10 x 276 rows of 3 heads against 10471 keys: 501 and 141 us.
 bool many_rows(const saf_cache_dims& d, const uint8_t* is_static, int n_q) {
   const int g = d.H / d.H_kv;
-  const long long few = 10ll * d.H_kv * (((long long)n_q * g + 15) / 16);
-  long long many = 0;
+  const long long rows = (long long)n_q * g, tile = rows <= 8 ? 8 : 16;
+  const double keys = (double)d.max_pages * d.page_size;
+  long long units = 0;
   for (int kv = 0; kv < d.H_kv; ++kv) {
     int frozen = 0;
     for (int h = kv * g; h < (kv + 1) * g; ++h) frozen += is_static[h] != 0;
-    many += 36ll * (((long long)n_q * (g - frozen) + 255) / 256);
-    many += 20ll * frozen * (((long long)n_q + 255) / 256);
+    units += ((long long)n_q * (g - frozen) + 255) / 256 + ((long long)n_q + 255) / 256 * frozen;
   }
+  const double few_units = (double)d.n_seqs * d.H_kv * ((rows + tile - 1) / tile);
+  const double few = 5e3 + few_units * (17 + 0.05 * keys);
+  const double many = 26e3 + (double)d.n_seqs * units * (66 + 0.11 * keys);
   return few > many;
 }
 
@@ -169,7 +174,8 @@ saf_status saf_cache_append(const saf_cache_dims* dims, const uint8_t* head_is_s
 
 size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q) {
   if (check_cache(dims) != SAF_OK || n_q < 0) return 0;
-  // which kernel runs depends on the frozen heads; 16 rows always take the first
+  // which kernel runs depends on the frozen heads; 16 rows of a group always take
+  // the first: each head of K and V then is one unit there and at least one in the other
   const size_t few = cache_attn_ws(dims->d_h, sm_count()).total;
   const size_t many = cache_chunk_ws(dims->d_h, sm_count()).total;
   return (long long)n_q * (dims->H / dims->H_kv) <= 16 || few > many ? few : many;
@@ -198,7 +204,7 @@ saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_sta
   if (bad16(out) || (lse && !aligned16(lse)) || !workspace) return SAF_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SAF_ERR_INVALID_ARG;
   const bool many = many_rows(*dims, p.c.is_static, n_q);
-  const CacheAttnWs w = many ? cache_chunk_ws(dims->d_h, sm_count()) : cache_attn_ws(dims->d_h, sm_count());
+  const CacheAttnWs w = (many ? cache_chunk_ws : cache_attn_ws)(dims->d_h, sm_count());
   if (ws_bytes < w.total) return SAF_ERR_INVALID_ARG;
   p.Q = static_cast<const uint16_t*>(Q);
   p.alpha = alpha;

@@ -41,7 +41,13 @@ class Case:
     behind a slot's tokens), with host copies of everything."""
 
     def __init__(self, api, mask, H_kv, d, page, lens, n_q, seed=0, n_new=None, spare=3, holes=(),
-                 T_pat=None, wide_stride=0, cols=None, dirt=True, max_new=None):
+                 T_pat=None, wide_stride=0, cols=None, dirt=True, max_new=None, kernel=None):
+        # kernel: the one that attends.  The library chooses by sizes, the page table's width
+        # among them: wide tables (2^18 keys) make small calls take the one for many rows
+        self.kernel = kernel
+        if kernel == "cache_chunk":
+            T_pat = T_pat or max(1, -(-max(lens) // page)) * page
+            cols = 2 ** 18 // page
         rng = np.random.default_rng(seed)
         H, S = len(mask), len(lens)
         self.mask, self.H, self.H_kv, self.d, self.page = list(mask), H, H_kv, d, page
@@ -76,7 +82,7 @@ class Case:
         self.v_codes, self.v_scales = self._rows(rng, n_pages, H_kv)
         if dirt:
             for s in range(S):
-                for c in range(cols):
+                for c in range(min(cols, -(-max(int(lens[s]), 1) // page))):
                     p = self.held[s, c]
                     free = page - (max(int(lens[s]), 0) - c * page)
                     if p >= 0 and free > 0:
@@ -105,7 +111,14 @@ class Case:
         a, r = (torch.from_numpy(x).to(DEV) for x in (self.alpha, self.rho))
         out = torch.full_like(self.q, 7.0)
         lse = torch.full(self.q.shape[:3], 7.0, device=DEV)
+        from dynamic_causal_attention_gb300 import _binding as B
+        if self.kernel:
+            B.saf_trace_enable(1)
         self.cache.attend(0, self.q, a, r, n_new=i32(self.n_new), out=out, lse=lse, **kw)
+        if self.kernel:
+            names = [B.saf_trace_get(i)[1] for i in range(B.saf_trace_count())]
+            B.saf_trace_enable(0)
+            assert self.kernel in names
         return out, lse
 
     def check(self, out, lse, slots=slice(None)):
@@ -157,35 +170,41 @@ def test_single_tokens(api, H, H_kv, frozen, d, page):
 
 
 @pytest.mark.parametrize("H,H_kv,frozen,d,page", SHAPES)
-@pytest.mark.parametrize("n_q", [2, 7, 50])
-def test_several_tokens(api, H, H_kv, frozen, d, page, n_q):
+@pytest.mark.parametrize("n_q,kernel", [(2, "cache_attn"), (7, "cache_attn"), (50, None),
+                                        (50, "cache_chunk")])
+def test_several_tokens(api, H, H_kv, frozen, d, page, n_q, kernel):
     # as many new tokens as there are, fewer tokens than new ones, none, one, all but one
     lens = [n_q, max(0, n_q - 3), 77, 2 * page + 1, 260, 4]
     n_new = [n_q, n_q, 0, 1, n_q - 1, -2]
-    c = Case(api, mask_of(H, frozen), H_kv, d, page, lens, n_q, n_new=n_new, seed=n_q + d)
+    c = Case(api, mask_of(H, frozen), H_kv, d, page, lens, n_q, n_new=n_new, seed=n_q + d,
+             kernel=kernel)
     c.check(*c.run())
 
 
 @pytest.mark.parametrize("d,page,g", [(64, 64, 1), (128, 32, 4), (32, 16, 3)])
-@pytest.mark.parametrize("n_q", [1, 150])
-def test_long_sequences_are_cut_and_joined(api, d, page, g, n_q):
+@pytest.mark.parametrize("n_q,kernel", [(1, "cache_attn"), (150, None),
+                                        (150, "cache_chunk")])
+def test_long_sequences_are_cut_and_joined(api, d, page, g, n_q, kernel):
     # one long sequence next to short ones: its keys are split over many CTAs
     c = Case(api, mask_of(2 * g, (0,)), 2, d, page, [5003, 150, 900], n_q,
-             n_new=[min(n_q, 2), min(n_q, 140), n_q], seed=3)
+             n_new=[min(n_q, 2), min(n_q, 140), n_q], seed=3, kernel=kernel)
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("kernel", [None, "cache_chunk"])
 @pytest.mark.parametrize("d,page", [(128, 128), (64, 16)])
-def test_prompt_chunks(api, d, page):
+def test_prompt_chunks(api, d, page, kernel):
     # the first chunk of a prompt (nothing before it), and chunks behind a context
-    c = Case(api, mask_of(8, (2, 3)), 4, d, page, [257, 700, 391], 257, n_new=[257, 130, 255], seed=9)
+    c = Case(api, mask_of(8, (2, 3)), 4, d, page, [257, 700, 391], 257, n_new=[257, 130, 255], seed=9,
+             kernel=kernel)
     c.check(*c.run())
 
 
 @pytest.mark.parametrize("d", [32, 64, 128])
 def test_many_short_prompts(api, d):
     # several whole units of 64 rows for each CTA: half of a tile's warps have none
-    c = Case(api, mask_of(4, ()), 4, d, 64, [128 - (s * 7) % 64 for s in range(160)], 64, seed=5)
+    c = Case(api, mask_of(4, ()), 4, d, 64, [128 - (s * 7) % 64 for s in range(160)], 64, seed=5,
+             kernel="cache_chunk")
     out, lse = c.run()
     c.check(out, lse, slice(0, 160, 3))
 
@@ -194,25 +213,29 @@ def test_frozen_heads_behind_short_units(api):
     # 260 rows of the dynamic heads: a row of units of 256, then one of 4, whose second tile of
     # rows is empty, then the frozen heads' units with both
     c = Case(api, mask_of(24, range(2, 24, 3)), 8, 32, 64, [600 - 3 * s for s in range(16)], 130,
-             seed=6)
+             seed=6, kernel="cache_chunk")
     out, lse = c.run()
     c.check(out, lse, slice(0, 16, 3))
 
 
-@pytest.mark.parametrize("n_q", [1, 3, 40])
+@pytest.mark.parametrize("n_q,kernel", [(1, "cache_attn"), (3, "cache_attn"), (40, None),
+                                        (40, "cache_chunk")])
 @pytest.mark.parametrize("d,page", [(128, 64), (64, 16), (32, 128)])
-def test_holes_and_dirty_pages(api, d, page, n_q):
+def test_holes_and_dirty_pages(api, d, page, n_q, kernel):
     lens = [6 * page + 3, 2 * page, 5 * page - 1]
     holes = [(0, 0), (0, 3), (1, 0), (1, 1), (2, 4)]  # slot 1 has no page left
-    c = Case(api, mask_of(6, (1, 4)), 2, d, page, lens, n_q, holes=holes, seed=21)
+    c = Case(api, mask_of(6, (1, 4)), 2, d, page, lens, n_q, holes=holes, seed=21,
+             kernel=kernel)
     c.check(*c.run())
 
 
-@pytest.mark.parametrize("n_q", [5, 40, 200])
+@pytest.mark.parametrize("n_q,kernel", [(5, "cache_attn"), (40, None),
+                                        (40, "cache_chunk"), (200, "cache_chunk")])
 @pytest.mark.parametrize("d", [32, 64, 128])
-def test_nan_rows_reach_only_the_rows_that_see_them(api, d, n_q):
+def test_nan_rows_reach_only_the_rows_that_see_them(api, d, n_q, kernel):
     page = 32
-    c = Case(api, mask_of(4, (0,)), 2, d, page, [n_q + 90, n_q], n_q, seed=5)
+    c = Case(api, mask_of(4, (0,)), 2, d, page, [n_q + 90, n_q], n_q, seed=5,
+             kernel=kernel)
     for s, j in [(0, 90 + n_q // 2), (1, n_q - 2)]:
         p = c.table[s, j // page]
         c.v_codes[p, :, j % page, 3] = 0x7F
@@ -228,10 +251,12 @@ def test_lengths_behind_the_page_table(api):
     c.check(*c.run())
 
 
-def test_frozen_patterns(api):
+@pytest.mark.parametrize("n_q,kernel", [(4, "cache_attn"), (60, "cache_chunk")])
+def test_frozen_patterns(api, n_q, kernel):
     # vectors shorter than the sequence, entries of -inf, rows whose every weight is zero
     for T in (1, 50, 200):
-        c = Case(api, mask_of(6, (0, 1, 2, 3, 4)), 3, 64, 32, [150, 33, 1], 4, T_pat=T, seed=T)
+        c = Case(api, mask_of(6, (0, 1, 2, 3, 4)), 3, 64, 32, [150, 33, 1], n_q, T_pat=T, seed=T,
+                 kernel=kernel)
         c.alpha[1, ::2] = -np.inf
         c.rho[2, :] = -np.inf
         c.alpha[3] = -np.inf
@@ -240,9 +265,10 @@ def test_frozen_patterns(api):
         c.check(*c.run())
 
 
-def test_scales_of_any_size(api):
+@pytest.mark.parametrize("n_q,kernel", [(3, "cache_attn"), (60, "cache_chunk")])
+def test_scales_of_any_size(api, n_q, kernel):
     # block scales far apart within a sequence; queries far outside f16's range
-    c = Case(api, mask_of(4, (1,)), 2, 64, 16, [200, 130], 3, seed=4)
+    c = Case(api, mask_of(4, (1,)), 2, 64, 16, [200, 130], n_q, seed=4, kernel=kernel)
     rng = np.random.default_rng(0)
     e = rng.integers(-30, 20, size=c.v_scales.shape)
     fin = np.isfinite(c.v_scales)
@@ -253,17 +279,18 @@ def test_scales_of_any_size(api):
     c.check(*c.run())
 
 
-def test_pages_far_apart_and_layers_behind_one_another(api):
+@pytest.mark.parametrize("n_q,kernel", [(2, "cache_attn"), (70, "cache_chunk")])
+def test_pages_far_apart_and_layers_behind_one_another(api, n_q, kernel):
     # page_stride * page beyond 2^32 bytes; the layer is not the first of its page
     n_pages, page, d = 300, 16, 64
     masks = [[0, 0], [1, 0], [0, 0]]
-    small = Case(api, masks[1], 2, d, page, [70, 16], 2, seed=2)
-    n = small.cache.n_pages
-    probe = api.PagedCache(masks, 2, d, n_seqs=2, max_pages=5, n_pages=2, page_size=page, device=DEV)
+    small = Case(api, masks[1], 2, d, page, [70, 16], n_q, seed=2, kernel=kernel)
+    n, cols = small.cache.n_pages, small.table.shape[1]
+    probe = api.PagedCache(masks, 2, d, n_seqs=2, max_pages=cols, n_pages=2, page_size=page, device=DEV)
     stride = 16 << 20
     pool = torch.zeros((n_pages, stride), dtype=torch.uint8, device=DEV)
-    big = api.PagedCache(masks, 2, d, n_seqs=2, max_pages=5, n_pages=n_pages, page_size=page,
-                         max_new=2, device=DEV, pool=pool[:, :probe.page_bytes])
+    big = api.PagedCache(masks, 2, d, n_seqs=2, max_pages=cols, n_pages=n_pages, page_size=page,
+                         max_new=n_q, device=DEV, pool=pool[:, :probe.page_bytes])
     place = np.linspace(n_pages - 1, 1, n).astype(np.int32)
     big.seq_len.copy_(i32(small.lens))
     big.page_table.copy_(i32(np.where(small.table >= 0, place[small.table], -1)))
@@ -273,7 +300,7 @@ def test_pages_far_apart_and_layers_behind_one_another(api):
     a, r = (torch.from_numpy(x).to(DEV) for x in (small.alpha, small.rho))
     out, lse = big.attend(1, small.q, a, r, n_new=i32(small.n_new))
     small.check(out, lse)
-    k, v = (torch.randn((2, 2, 2, d), device=DEV) for _ in range(2))
+    k, v = (torch.randn((2, 2, n_q, d), device=DEV) for _ in range(2))
     big.append(1, k, v)
     small.cache.append(0, k, v)
     for dst, src in zip(big.views(1), small.cache.views(0)):
@@ -284,9 +311,11 @@ def test_pages_far_apart_and_layers_behind_one_another(api):
     assert int(pool[others.to(DEV)].max()) == 0 and int(pool[:, probe.page_bytes:].max()) == 0
 
 
-@pytest.mark.parametrize("n_q,lens", [(1, [3000, 10, 1200]), (64, [3000, 64, 1200])])
-def test_same_bits_again_and_on_another_stream(api, n_q, lens):
-    c = Case(api, mask_of(8, (1, 6)), 2, 128, 64, lens, n_q, seed=12)
+@pytest.mark.parametrize("n_q,lens,kernel", [
+    (1, [3000, 10, 1200], "cache_attn"), (64, [3000, 64, 1200], None),
+    (64, [3000, 64, 1200], "cache_chunk")])
+def test_same_bits_again_and_on_another_stream(api, n_q, lens, kernel):
+    c = Case(api, mask_of(8, (1, 6)), 2, 128, 64, lens, n_q, seed=12, kernel=kernel)
     out, lse = c.run()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

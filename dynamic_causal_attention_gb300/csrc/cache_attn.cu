@@ -43,14 +43,19 @@ constexpr int kWarps = 4;
 // A unit is (slot b, K/V head, row tile): up to 8 NT of the slot's n_new * group
 // query rows (row r = t * group + h) against all its keys, in tiles of kTile
 // keys.  The row tiles of a head lie side by side, so that their codes come from
-// L2 after the first.  All tiles of
-// all units, in that order, are cut into equal shares, one for each CTA; a
-// unit that is cut leaves partial sums, joined by a second kernel in the order
-// of the CTAs.  Nothing depends on timing.  Where no slot can have more than
-// kWholeKeys keys, each unit is one CTA's instead: no search for a share and no
-// second kernel.
-constexpr int kMinTiles = 4;     // least share of a CTA
-constexpr int kWholeKeys = 512;
+// L2 after the first.  All tiles of all units, in that order, are cut into equal
+// shares, one for each CTA; a unit that is cut leaves partial sums, joined by a
+// second kernel in the order of the CTAs.  Nothing depends on timing.  A share may
+// be a single tile: what a step costs a CTA without company is the latency of its
+// loads (one token against 1000, 16 heads of 4: 8.6 us; with shares of 4 tiles and
+// more, 11.3).
+//
+// Where no slot can have more than kWholeTiles tiles, each unit is one CTA's
+// instead, without a search for its share and without a second kernel: 7.6 us
+// against 8.2 for 4 units of 4 tiles, 8.8 against 12.3 for 256.  With up to
+// kWholeTilesMany that pays only where there are units for half of the SMs: 11.5
+// against 8.4 us for 4 units of 8 tiles, 11.8 and 11.4 for 64, 13.1 and 15.6 for 256.
+constexpr int kWholeTiles = 4, kWholeTilesMany = 8;
 constexpr int kJoinAhead = 8;    // parts that a joining thread has in flight
 
 template <int D>
@@ -124,7 +129,6 @@ __device__ Share find_share(const CacheCall& c, int per_slot, long long* scan /*
   }
   Share s;
   s.size = (total + gridDim.x - 1) / gridDim.x;
-  if (s.size < kMinTiles) s.size = kMinTiles;
   s.begin = min(s.size * blockIdx.x, total);
   s.end = min(s.begin + s.size, total);
   if (s.begin < s.end && mine <= s.begin && s.begin < mine + sum) {
@@ -702,9 +706,11 @@ int n_ctas(int nt, int n_sms) { return n_sms * (nt == 1 ? kCtas<1> : kCtas<2>); 
 
 template <int D, int NT>
 cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
-  const bool whole = (long long)p.c.max_pages << p.c.page_shift <= kWholeKeys;
-  const int row_tiles = (p.c.n_q * p.c.group + 8 * NT - 1) / (8 * NT);
+  const int row_tiles = (int)(((long long)p.c.n_q * p.c.group + 8 * NT - 1) / (8 * NT));
   const long long units = (long long)p.c.n_seqs * p.c.H_kv * row_tiles;
+  const long long keys = (long long)p.c.max_pages << p.c.page_shift;
+  const int whole_tiles = units >= n_sms / 2 ? kWholeTilesMany : kWholeTiles;
+  const bool whole = keys <= whole_tiles * Geo<D>::kTile && units < 1ll << 31;
   const bool by_unit = units <= n_ctas(NT, n_sms);
   const int grid = whole ? (int)units : n_ctas(NT, n_sms);
   cudaError_t e = set_max_dynamic_smem(

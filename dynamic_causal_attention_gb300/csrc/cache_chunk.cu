@@ -56,7 +56,6 @@ constexpr int kTile = 128;     // keys of a tile
 constexpr int kThreads = 512;
 // registers of a thread after the split: 2 * 176 + 80 + 80 = 4 * 128
 constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsIssue = 80;
-constexpr long long kMinTiles = 1;
 // parts that a joining thread has in flight: with 4, 64 registers and 8 blocks of
 // an SM, 152 units of 2 to 4 parts take 17 us, with 8 and half the blocks 34
 constexpr int kJoinAhead = 4;
@@ -292,7 +291,6 @@ __device__ Share find_share(const CacheChunk& p, long long* scan /* [warps + 2] 
   }
   Share s;
   s.size = (total + gridDim.x - 1) / gridDim.x;
-  if (s.size < kMinTiles) s.size = kMinTiles;
   s.begin = min(s.size * blockIdx.x, total);
   s.end = min(s.begin + s.size, total);
   if (s.begin < s.end && mine <= s.begin && s.begin < mine + sum) {

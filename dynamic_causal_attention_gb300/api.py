@@ -190,6 +190,8 @@ class PagedCache:
         self.n_seqs, self.max_pages, self.n_pages = n_seqs, max_pages, n_pages
         self.page_size, self.max_new = page_size, max_new
         self.layouts, self.offsets, self._static, self._frozen = [], [], [], []
+        if n_seqs < 1:
+            raise B.SafError(B.SAF_ERR_INVALID_ARG, f"PagedCache: {n_seqs} slots")
         geometry = (n_seqs, max_pages, n_pages, page_size, H, self.H_kv, d_h)
         at = 0
         for mask in layers:
@@ -229,6 +231,7 @@ class PagedCache:
             raise B.SafError(B.SAF_ERR_UNSUPPORTED, "saf_cache_attn_workspace_size")
         self.ws_bytes, self._pages_bytes = attn, pages
         self.workspace = torch.empty(attn, dtype=torch.uint8, device=self.device)
+        self.workspace[:256].zero_()  # the status before the first call
         self._pages_ws = torch.empty(pages, dtype=torch.uint8, device=self.device)
         self._ws_at, self._pages_at = self.workspace.data_ptr(), self._pages_ws.data_ptr()
 
@@ -325,8 +328,6 @@ class PagedCache:
         to = self._at if into is None else self._table_like(into, "grow: into")
         granted = torch.empty(self.n_seqs, dtype=torch.int32, device=self.device)
         n_short = torch.empty(1, dtype=torch.int32, device=self.device)
-        if self.n_seqs == 0:
-            n_short.zero_()
         self._call(B.saf_cache_grow, self.dims, self._pool_at, self.page_bytes,
                    self._per_slot(n_new, "grow: n_new"), *self._at, *to, granted.data_ptr(),
                    n_short.data_ptr(), self._pages_at, self._pages_bytes)

@@ -157,6 +157,7 @@ saf_status saf_cache_append(const saf_cache_dims* dims, const uint8_t* head_is_s
   const saf_status st = check_cache(dims);
   if (st != SAF_OK) return st;
   if (n_q < 0 || (dtype != SAF_BF16 && dtype != SAF_F32)) return SAF_ERR_INVALID_ARG;
+  if ((long long)n_q * dims->H >= (1ll << 31) || n_q > 1 << 30) return SAF_ERR_UNSUPPORTED;
   if (dims->n_seqs == 0 || n_q == 0) return SAF_OK;
   CacheAppend p;
   memset(&p, 0, sizeof(p));
@@ -190,7 +191,7 @@ saf_status saf_cache_attn(const saf_cache_dims* dims, const uint8_t* head_is_sta
   const saf_status st = check_cache(dims);
   if (st != SAF_OK) return st;
   if (n_q < 0 || T_pat < 0) return SAF_ERR_INVALID_ARG;
-  if ((long long)n_q * dims->H >= (1ll << 31)) return SAF_ERR_UNSUPPORTED;
+  if ((long long)n_q * dims->H >= (1ll << 31) || n_q > 1 << 30) return SAF_ERR_UNSUPPORTED;
   if (dims->n_seqs == 0 || n_q == 0) return SAF_OK;
   CacheAttn p;
   memset(&p, 0, sizeof(p));

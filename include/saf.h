@@ -305,11 +305,13 @@ SAF_API saf_status saf_calib_destroy(void* handle);
  * another in the page; a call on a layer takes the address of its record in
  * page 0 and dims->page_stride.
  *
- * Arrays of int32 are 16-byte aligned device arrays unless a call says
- * otherwise.  No call allocates, synchronises or reads device memory on the
+ * A call takes up to 2^30 rows for each slot, and fewer than 2^31 counted
+ * over the query heads.  Arrays of int32 are 16-byte aligned device arrays
+ * unless a call says otherwise.  No call allocates, synchronises or reads device memory on the
  * host; all can be captured in a CUDA graph. */
 typedef struct saf_cache_dims {
-  int n_seqs;         /* slots: rows of page_table, 0..32768               */
+  int n_seqs;         /* slots: rows of page_table, 0..32768 (0: append,  *
+                       * attn, fork and grow return and write nothing)     */
   int max_pages;      /* columns; max_pages * page_size <= 2^31 - 1024    */
   int n_pages;        /* pages of the pool, >= 1                           */
   int page_size;      /* tokens of a page: 16, 32, 64 or 128               */

@@ -74,6 +74,7 @@ def test_attn_refusals(B):
     assert call(dims(B, page_stride=1024)) == B.SAF_ERR_INVALID_ARG
     # rows beyond 31 bits
     assert call(n_q=1 << 30) == B.SAF_ERR_UNSUPPORTED
+    assert call(dims(B, H=1, H_kv=1), mask=b"\0", n_q=(1 << 30) + 1) == B.SAF_ERR_UNSUPPORTED
     # nothing to do: no pointer is looked at
     none = {k: None for k in ok if k not in ("T", "n_q", "ws_bytes", "mask")}
     assert call(dims(B, n_seqs=0), **none) == B.SAF_OK
@@ -93,6 +94,7 @@ def test_append_refusals(B):
                 dict(seq_len=None), dict(table=None), dict(table=6)):
         assert call(**bad) == B.SAF_ERR_INVALID_ARG, bad
     assert call(dims(B, page_stride=1024)) == B.SAF_ERR_INVALID_ARG
+    assert call(n_q=1 << 30) == B.SAF_ERR_UNSUPPORTED
     none = dict(layer=None, K=None, V=None, n_new=None, seq_len=None, table=None)
     assert call(dims(B, n_seqs=0), **none) == B.SAF_OK
     assert call(n_q=0, **none) == B.SAF_OK

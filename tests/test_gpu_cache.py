@@ -441,7 +441,7 @@ def random_tables(rng, S, cols, n_pages, page, share):
 
 
 PAGES = [(1, 1, 1, 16), (5, 7, 40, 16), (33, 9, 203, 32), (300, 5, 1021, 64), (64, 40, 5000, 16),
-         (7000, 3, 9001, 16)]
+         (7000, 3, 9001, 16), (90, 1100, 140003, 16)]
 
 
 @pytest.mark.parametrize("into", [False, True])
@@ -640,6 +640,32 @@ def test_captured_step_replays(api):
     assert one.device_status() == (0, 0)
 
 
+def test_two_caches_on_two_streams(api):
+    # calls of both kernels and a pool's calls at once, against the same ones one by one
+    kw = [dict(n_q=1, seed=1, kernel="cache_attn"), dict(n_q=120, seed=2, kernel="cache_chunk")]
+    cases = [Case(api, mask_of(8, (1, 6)), 2, 64, 64, [1900, 700], **k) for k in kw]
+    alone = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.run())
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        for out, lse in got[i]:
+            assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+        assert c.cache.device_status() == (0, 0)
+
+
+def test_status_of_a_fresh_cache(api):
+    junk = torch.full((1 << 24,), 255, dtype=torch.uint8, device=DEV)
+    del junk  # (what the allocator hands out next holds no zeros)
+    cache = api.PagedCache([[0, 1]], 2, 64, n_seqs=2, max_pages=2, n_pages=4, device=DEV)
+    assert cache.device_status() == (0, 0)
+
+
 def test_refusals(api):
     cache = api.PagedCache([[0, 1]], 2, 64, n_seqs=2, max_pages=2, n_pages=4, page_size=16, device=DEV)
     q = torch.zeros((2, 2, 1, 64), dtype=torch.bfloat16, device=DEV)
@@ -662,6 +688,7 @@ def test_refusals(api):
         lambda: cache.grow(torch.ones(3, dtype=torch.int32, device=DEV)),
         lambda: cache.fork(torch.ones(2, device=DEV)),
         lambda: cache.compact(into=(cache.ref, cache.ref)),
+        lambda: api.PagedCache([[0, 1]], 2, 64, n_seqs=0, max_pages=2, n_pages=4, device=DEV),
         lambda: api.PagedCache([[0]], 2, 64, n_seqs=2, max_pages=2, n_pages=4, device=DEV),
         lambda: api.PagedCache([[0, 1]], 2, 48, n_seqs=2, max_pages=2, n_pages=4, device=DEV),
         lambda: api.PagedCache([[0, 1]], 2, 64, n_seqs=2, max_pages=2, n_pages=4, device=DEV,

@@ -229,9 +229,11 @@ cudaError_t launch(const CacheAppend& p, cudaStream_t s) {
   const int groups = (D / 8) << c.page_shift;
   if (c.n_q < kManyRows || groups <= 256)
     append_few_kernel<D, F32>
-        <<<dim3((unsigned)((units + kWarps - 1) / kWarps), (unsigned)c.n_seqs), kWarps * 32, 0, s>>>(p);
+        <<<dim3((unsigned)((units + kWarps - 1) / kWarps), (unsigned)c.n_seqs), kWarps * 32, 0,
+           s>>>(p);
   else
-    append_many_kernel<D, F32><<<dim3((unsigned)units, (unsigned)c.n_seqs), groups / kGroups, 0, s>>>(p);
+    append_many_kernel<D, F32>
+        <<<dim3((unsigned)units, (unsigned)c.n_seqs), groups / kGroups, 0, s>>>(p);
   trace_end(s, "cache_append");
   return cudaGetLastError();
 }

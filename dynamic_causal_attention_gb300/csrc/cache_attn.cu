@@ -60,7 +60,7 @@ constexpr int kJoinAhead = 8;    // parts that a joining thread has in flight
 
 template <int D>
 struct Geo {
-  static constexpr int kGroups = 128 / D;           // groups of 16 keys in a warp's step: 4 KB of codes
+  static constexpr int kGroups = 128 / D;           // of 16 keys in a warp's step: 4 KB of codes
   static constexpr int kStep = 16 * kGroups;        // keys of a step
   static constexpr int kTile = kWarps * kStep;      // keys of a tile
   // ring of a warp: K codes, V codes, then for each group K scale, V scale and
@@ -148,6 +148,13 @@ __device__ Share find_share(const CacheCall& c, int per_slot, long long* scan /*
   return s;
 }
 
+// CTAs that `tiles` more tiles take in shares of `size`; 32 bits are enough: a
+// unit has fewer than 2^27 tiles.
+__device__ __forceinline__ int cta_span(int tiles, long long size) {
+  const unsigned s = (unsigned)(size < 0x40000000 ? size : 0x40000000);
+  return (int)(((unsigned)tiles + s - 1) / s);
+}
+
 // The 8 x 8 block of 16-bit values of a warp (lane: row lane / 4, columns
 // 2 (lane % 4) and the next), transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -169,7 +176,8 @@ constexpr int smem_bytes() {
 
 template <int D, int NT>  // NT: 8 query rows each
 __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
-    cache_attn_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool whole_units, bool by_unit) {
+    cache_attn_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool whole_units,
+                      bool by_unit) {
   constexpr int kMR = 8 * NT;
   constexpr int kG = Geo<D>::kGroups, kStep = Geo<D>::kStep, kTile = Geo<D>::kTile;
   constexpr int kKS = D / 16;            // steps of 16 along d
@@ -262,9 +270,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     const uint32_t to0 = chunk_at<D>(lane / (D / 16), lane % (D / 16));
     const uint32_t to1 = chunk_at<D>(lane / (D / 16) + 512 / D, lane % (D / 16));
     const uint8_t* lane_v = c.layer + c.off_v + (((size_t)kv << c.page_shift) * D) + lane * 16;
-    const uint8_t* lane_k = c.layer + (((size_t)(any_dyn ? k_head : 0) << c.page_shift) * D) + lane * 16;
-    const uint8_t* lane_m =
-        c.layer + (lane == 0 && any_dyn ? c.off_ks + 4 * (size_t)k_head : c.off_vs + 4 * (size_t)kv);
+    const uint8_t* lane_k =
+        c.layer + (((size_t)(any_dyn ? k_head : 0) << c.page_shift) * D) + lane * 16;
+    const uint8_t* lane_m = c.layer + (lane == 0 && any_dyn ? c.off_ks + 4 * (size_t)k_head
+                                                            : c.off_vs + 4 * (size_t)kv);
     const uint32_t page_stride = (uint32_t)c.page_stride;  // below 2^32: checked on the host
     auto issue = [&](int s, uint32_t st) {
       if (s < steps) {
@@ -289,8 +298,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
           const uint32_t to = st + g * 16 * D;
 #pragma unroll
           for (int i = 0; i < kChunks; ++i)
-            cp_async16(to + off_v + (i & 1 ? to1 : to0) + (i >> 1) * 1024, lane_v + in_rec + i * 512,
-                       16);
+            cp_async16(to + off_v + (i & 1 ? to1 : to0) + (i >> 1) * 1024,
+                       lane_v + in_rec + i * 512, 16);
           if (any_dyn) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i)
@@ -382,13 +391,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (frozen >> (2 * nt + i) & 1)
+          if (frozen >> (2 * nt + i) & 1) {
 #pragma unroll
-          for (int u = 0; u < 2 * kG; ++u) {
-            const int j = s * kTile + 8 * u;  // 16 (u / 2) + 8 (u % 2)
-            const bool ok = (unsigned)(j - lo[nt][i]) < (unsigned)len[nt][i];
-            pa[nt][i][u] = ok ? __ldg(al[nt][i] + j) : -CUDART_INF_F;
-            pr[nt][i][u] = ok ? __ldg(rh[nt][i] - j) : 0.f;
+            for (int u = 0; u < 2 * kG; ++u) {
+              const int j = s * kTile + 8 * u;  // 16 (u / 2) + 8 (u % 2)
+              const bool ok = (unsigned)(j - lo[nt][i]) < (unsigned)len[nt][i];
+              pa[nt][i][u] = ok ? __ldg(al[nt][i] + j) : -CUDART_INF_F;
+              pr[nt][i][u] = ok ? __ldg(rh[nt][i] - j) : 0.f;
+            }
           }
     };
     fetch_pattern(0);
@@ -674,7 +684,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
 // to its successors; y: slices of its rows.
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads)
-    cache_join_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool by_unit, int split) {
+    cache_join_kernel(const __grid_constant__ CacheAttn p, int row_tiles, bool by_unit,
+                      int split) {
   constexpr int kMR = 8 * NT;
   const CacheCall& c = p.c;
   asm volatile("griddepcontrol.wait;" ::: "memory");

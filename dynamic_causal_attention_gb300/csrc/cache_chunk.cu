@@ -7,11 +7,11 @@
 // query heads of one K/V head; its rows are r = t * heads + index (dynamic: the
 // last key that a unit sees is then as early as can be) or r = index * n_new + t
 // (frozen: each head begins a unit of its own, whose rows share alpha and read
-// rho side by side), and a unit takes 256 of them as two tiles of 128, against the keys up to the last
-// position among them in tiles of 128.  Splitting a group by kind keeps every
-// warp uniform and spares frozen rows the Q K product.  All tiles of all
-// units are cut into equal shares, one for each CTA (one per SM), as in
-// cache_attn.cu.
+// rho side by side).  A unit takes 256 of them as two tiles of 128, against the
+// keys up to the last position among them in tiles of 128.  Splitting a group by
+// kind keeps every warp uniform and spares frozen rows the Q K product.  All
+// tiles of all units are cut into shares of equal cost, one for each CTA (one per
+// SM); a unit that is cut is joined as in cache_attn.cu.
 //
 // Warp roles (512 threads; registers move to the softmax):
 //   warps 0-3, 4-7   the softmax of row tile 0 and 1: one row per thread.  They
@@ -35,9 +35,11 @@
 // keys are taken in two halves of 64: S, softmax and P V of one half run while
 // the other half's do, and P, as packed f16, overwrites the first columns of
 // its own half of S, so the next S of a half waits only for the product that
-// reads that half's P.  (With whole tiles the chain S, softmax, P V of a row tile
-// was what a tile cost, about 4500 cycles; its links are listed in the table of
-// the measurements.)
+// reads that half's P.  What a tile of keys costs is the chain S, softmax, P V
+// and its hand-offs, about 4400 cycles for 256 rows at d_h = 128, against some
+// 1800 of the tensor cores' time; 2 x 2000 rows of 16 heads against 8192 keys take
+// 267 us, 48% of the measured burst rate of products, and with 4 frozen heads,
+// whose weights are 64 loads from the window for each half a tile, 273 us (41%).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -187,32 +189,73 @@ __device__ __forceinline__ long long warp_sum(long long x) {
   return x;
 }
 
+// What a share counts, in eighths of a tile of dynamic rows (its two row tiles
+// full): the tiles of keys, and behind them the unit's own cost: Q, the first tile
+// without company, the results.  Measured with equal units, microseconds:
+//                          d_h = 128     64      32
+//   tile, dynamic             2.36      1.90    1.70     (one row tile 2.18 1.80 1.57)
+//   tile, frozen              2.59      2.51    2.40     (one row tile 2.11 1.96 1.67)
+//   unit, dynamic, frozen     11, 8.6   6.1, 4.4   4.1, 3.1
+// With tiles alone counted, 2 x 2000 rows of 16 heads, 4 of them frozen, against
+// 8192 keys took 287 us for 273 (the average SM was idle for a tenth of them), 12 x
+// 76 rows of 128 heads against 388 keys 63 for 47.
+struct Costs {
+  int tile[2][2];  // [frozen][both row tiles]
+  int unit[2];     // [frozen]
+};
+__device__ __forceinline__ constexpr Costs costs_of(int d) {
+  return d == 128  ? Costs{{{7, 8}, {7, 9}}, {37, 29}}
+         : d == 64 ? Costs{{{8, 8}, {8, 11}}, {26, 19}}
+                   : Costs{{{7, 8}, {8, 11}}, {19, 15}};
+}
+constexpr int kMaxTileCost = 11;
+
 // Walks the units in order: slots, then groups of classes (equal width and
 // kind), row pairs, classes.  seek() and the sums are taken by whole warps.
+template <int D>
 struct Walk {
   const CacheChunk& p;
   Rows rows;
-  int b, group, pair, cls, ut;
+  int b, group, pair, cls, ut, each;  // the unit's tiles and what one costs
   __device__ __forceinline__ explicit Walk(const CacheChunk& q) : p(q) {}
   __device__ __forceinline__ int gk() const { return p.group_width[group]; }
   __device__ __forceinline__ bool ice() const { return p.group_static[group]; }
   __device__ __forceinline__ int classes(int g) const {
     return p.group_first[g + 1] - p.group_first[g];
   }
-  __device__ long long slot_tiles(int slot) const {
+  static __device__ __forceinline__ int tile_cost(const Rows& r, int pair, int gk, bool ice) {
+    constexpr Costs k = costs_of(D);
+    const bool both = unit_rows(r, pair, gk, ice).n > 128;
+    return ice ? (both ? k.tile[1][1] : k.tile[1][0]) : (both ? k.tile[0][1] : k.tile[0][0]);
+  }
+  static __device__ __forceinline__ int unit_cost(bool ice) {
+    constexpr Costs k = costs_of(D);
+    return ice ? k.unit[1] : k.unit[0];
+  }
+  __device__ __forceinline__ long long cost() const {
+    return (long long)ut * each + unit_cost(ice());
+  }
+  // the tiles of the unit that begin before `upto` > 0, counted from its start
+  __device__ __forceinline__ int tiles_before(long long upto) const {
+    return upto >= (long long)ut * each ? ut : ((int)upto + each - 1) / each;
+  }
+  __device__ long long slot_cost(int slot) const {
     const Rows r = slot_rows(p.a.c, slot);
     const int lane = threadIdx.x & 31;
     long long sum = 0;
     for (int g = 0; g < p.n_groups; ++g) {
       long long mine = 0;
       const int w = p.group_width[g], n = pairs_of(r, w, p.group_static[g]);
-      for (int i = lane; i < n; i += 32) mine += pair_tiles(r, i, w, p.group_static[g]);
+      for (int i = lane; i < n; i += 32)
+        mine += (long long)pair_tiles(r, i, w, p.group_static[g]) *
+                    tile_cost(r, i, w, p.group_static[g]) +
+                unit_cost(p.group_static[g]);
       sum += mine * classes(g);
     }
     return warp_sum(sum);
   }
-  // to the unit that holds tile `at` of slot `slot`; returns the tile in it
-  __device__ int seek(int slot, long long at) {
+  // To the unit at `at` of slot `slot`; returns how far that is from its start.
+  __device__ long long seek(int slot, long long at) {
     const int lane = threadIdx.x & 31;
     b = slot;
     rows = slot_rows(p.a.c, b);
@@ -221,7 +264,8 @@ struct Walk {
       for (pair = 0; pair < n; pair += 32) {
         const int i = pair + lane;
         const int mine = i < n ? pair_tiles(rows, i, gk(), ice()) : 0;
-        long long upto = (long long)mine * n_cls;
+        const int one = i < n ? tile_cost(rows, i, gk(), ice()) : 0;
+        long long upto = i < n ? ((long long)mine * one + unit_cost(ice())) * n_cls : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(~0u, upto, o);
@@ -232,9 +276,10 @@ struct Walk {
           const int l = __ffs(over) - 1;
           pair += l;
           ut = __shfl_sync(~0u, mine, l);
-          at -= __shfl_sync(~0u, upto, l) - (long long)ut * n_cls;
-          cls = p.group_first[group] + (int)(at / ut);
-          return (int)(at % ut);
+          each = __shfl_sync(~0u, one, l);
+          at -= __shfl_sync(~0u, upto, l) - cost() * n_cls;
+          cls = p.group_first[group] + (int)(at / cost());
+          return at % cost();
         }
         at -= __shfl_sync(~0u, upto, 31);
       }
@@ -258,6 +303,7 @@ struct Walk {
       }
       cls = p.group_first[group];
       ut = pair_tiles(rows, pair, gk(), ice());
+      each = tile_cost(rows, pair, gk(), ice());
     }
   }
 };
@@ -271,17 +317,18 @@ struct Share {
   long long size, begin, end, in_slot;
   int b;
 };
-// Every CTA finds its share: each warp sums a run of slots, the sums of the
-// warps before give a run's first tile, and the warp whose run holds the
-// share's first tile walks it.
+// Every CTA finds its share, the tiles that begin in [begin, end): each warp sums a
+// run of slots, the sums of the warps before give where a run begins, and the warp
+// whose run holds the share's beginning walks it.
+template <int D>
 __device__ Share find_share(const CacheChunk& p, long long* scan /* [warps + 2] */) {
-  const Walk w(p);
+  const Walk<D> w(p);
   constexpr int kN = kThreads / 32;
   const int warp = threadIdx.x >> 5, n_seqs = p.a.c.n_seqs;
   const int per = (n_seqs + kN - 1) / kN;
   const int b0 = min(warp * per, n_seqs), b1 = min(b0 + per, n_seqs);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += w.slot_tiles(b);
+  for (int b = b0; b < b1; ++b) sum += w.slot_cost(b);
   scan[warp] = sum;
   __syncthreads();
   long long total = 0, mine = 0;
@@ -290,14 +337,15 @@ __device__ Share find_share(const CacheChunk& p, long long* scan /* [warps + 2] 
     total += scan[i];
   }
   Share s;
-  s.size = (total + gridDim.x - 1) / gridDim.x;
+  // at least a tile: every CTA that a unit passes then has one of its tiles
+  s.size = max((total + gridDim.x - 1) / gridDim.x, (long long)kMaxTileCost);
   s.begin = min(s.size * blockIdx.x, total);
   s.end = min(s.begin + s.size, total);
   if (s.begin < s.end && mine <= s.begin && s.begin < mine + sum) {
     long long at = mine;
     int b = b0;
     for (; b < b1 - 1; ++b) {
-      const long long t = w.slot_tiles(b);
+      const long long t = w.slot_cost(b);
       if (s.begin < at + t) break;
       at += t;
     }
@@ -368,7 +416,7 @@ __device__ __forceinline__ uint32_t unit_at(uint32_t r, uint32_t u) {
 // g, side by side (kL lanes to a row): 8 components lie where 16 codes of hi or lo
 // will, an even piece in hi's place and an odd one in lo's.
 template <int D>
-__device__ __forceinline__ void fetch_q(const CacheChunk& p, const Walk& w, const UnitRows& unit,
+__device__ __forceinline__ void fetch_q(const CacheChunk& p, const Walk<D>& w, const UnitRows& unit,
                                         int g, int r0, uint32_t stage) {
   constexpr int kL = D / 8, kR = 32 / kL;
   const int lane = threadIdx.x & 31;
@@ -468,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // the joining kernel may be set up meanwhile; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;");
-  const Share sh = find_share(p, reinterpret_cast<long long*>(smem + L::OFF_SCAN));
+  const Share sh = find_share<D>(p, reinterpret_cast<long long*>(smem + L::OFF_SCAN));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -478,10 +526,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                  sM = smem_u32(smem + L::OFF_META);
   constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S of row tile g at 128 g, O at 256 + 128 g
 
+  Walk<D> w(p);
+  int tile = 0;
+  long long at = sh.end;  // where the unit begins
   if (sh.begin < sh.end) {
-    Walk w(p);
-    int tile = w.seek(sh.b, sh.in_slot);
-    long long at = sh.begin;
+    const long long off = w.seek(sh.b, sh.in_slot);
+    at = sh.begin - off;
+    if (off > 0) tile = w.tiles_before(off);
+    if (tile == w.ut) {  // all its tiles begin in the shares before
+      tile = 0;
+      at += w.cost();
+      if (at < sh.end) w.next();
+    }
+  }
+  if (at < sh.end) {
     if (warp < 8) {
       // ------------------------------------------------------------ softmax
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -489,10 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_col = trow + kS + g * 128, o_col = trow + kO + g * 128;
       uint32_t n_tile = 0, n_s = 0, n_p = 0;  // tiles of the CTA; S and P of this row tile
+      bool first = true;                      // it is the CTA's first
       bool staged = false;                    // the unit's rows of Q are on their way
       uint32_t n_unit = 0;                    // units in which it has rows
       for (;;) {
-        const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+        const int tile_end = w.tiles_before(sh.end - at);
         const int gk = w.gk(), kv = p.cls_kv[w.cls];
         const bool ice = w.ice();
         const UnitRows unit = unit_rows(w.rows, w.pair, gk, ice);
@@ -699,8 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             softmax(Const<false>());
           // ---- the next unit's rows of Q, now that no product reads this one's: they
           // come while this one ends
-          if (at + (tile_end - tile) < sh.end) {
-            Walk x = w;
+          if (at + w.cost() < sh.end) {
+            Walk<D> x = w;
             x.next();
             const UnitRows u0 = unit_rows(x.rows, x.pair, x.gk(), x.ice());
             staged = !x.ice() && g * 128 < u0.n;
@@ -734,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
             // partial sums: [D / 4][row][4], so that a warp's stores are contiguous
-            const size_t part = (size_t)(2 * blockIdx.x + (at == sh.begin ? 0 : 1)) * kRows;
+            const size_t part = (size_t)(2 * blockIdx.x + (first ? 0 : 1)) * kRows;
             const int pr = g * 128 + r;
             // a thread's row goes out in whole sectors where the base allows it: half as
             // many accesses as 16 bytes at a time
@@ -773,14 +832,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0 && tile == 0) {
           // the unit begins here and ends in CTA `last`; only the last that begins
           // here can be cut
-          const int left = max(0, (int)(at + w.ut - sh.end));  // tiles behind this CTA's
-          const int last = blockIdx.x + cta_span(left, sh.size);
+          const long long end = at + (long long)(w.ut - 1) * w.each;  // its last tile
+          const int last = max((int)blockIdx.x, (int)(end / sh.size));
           p.a.join[p.by_unit ? w.number() : blockIdx.x] =
               make_int4(tile_end < w.ut ? w.b << 8 | w.cls : -1, w.pair, blockIdx.x,
-                        last | (at == sh.begin ? 0 : 1 << 30));
+                        last | (first ? 0 : 1 << 30));
         }
         n_tile += tile_end - tile;
-        at += tile_end - tile;
+        first = false;
+        at += w.cost();
         if (at >= sh.end) break;
         tile = 0;
         w.next();
@@ -798,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t vc = 0;
       int n_unit[2] = {0, 0};
       for (;;) {
-        const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+        const int tile_end = w.tiles_before(sh.end - at);
         const bool both = unit_rows(w.rows, w.pair, w.gk(), w.ice()).n > 128;
         ++n_unit[0];
         n_unit[1] += both;
@@ -846,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(r_empty + rs);
           ++vc;
         }
-        at += tile_end - tile;
+        at += w.cost();
         if (at >= sh.end) break;
         tile = 0;
         w.next();
@@ -862,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
         uint32_t kc = 0, vc = 0, n_q = 0, n_p = 0;
         for (;;) {
-          const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+          const int tile_end = w.tiles_before(sh.end - at);
           const bool ice = w.ice();
           const bool mine = unit_rows(w.rows, w.pair, w.gk(), ice).n > g * 128;
           // K of tile i + 1 and V of tile i are waited for while a product of the
@@ -932,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (more) k_done();
           }
-          at += tile_end - tile;
+          at += w.cost();
           if (at >= sh.end) break;
           tile = 0;
           w.next();
@@ -946,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int per = 1 << (c.page_shift - 4);  // groups of 16 keys in a page
         const bool issues = lane < 8 && lane % per == 0;
         for (;;) {
-          const int tile_end = (int)min((long long)w.ut, tile + (sh.end - at));
+          const int tile_end = w.tiles_before(sh.end - at);
           const int kv = p.cls_kv[w.cls], kh = w.ice() ? -1 : c.k_of[kv];
           const int ext = pair_extent(w.rows, w.pair, w.gk(), w.ice());
           // lane % 8: its group's page, two tiles ahead, and scales, one ahead
@@ -1031,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             page1 = page2;
             sc = sc1;
           }
-          at += tile_end - tile;
+          at += w.cost();
           if (at >= sh.end) break;
           tile = 0;
           w.next();

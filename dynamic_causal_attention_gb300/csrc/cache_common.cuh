@@ -164,13 +164,6 @@ __device__ __forceinline__ int page_at(const CacheCall& c, int b, int col) {
   return (unsigned)p < (unsigned)c.n_pages ? p : -1;
 }
 
-// CTAs that `tiles` more tiles take in shares of `size`; 32 bits are enough: a
-// unit has fewer than 2^27 tiles.
-__device__ __forceinline__ int cta_span(int tiles, long long size) {
-  const unsigned s = (unsigned)(size < 0x40000000 ? size : 0x40000000);
-  return (int)(((unsigned)tiles + s - 1) / s);
-}
-
 // ------------------------------------------------------------ joining parts
 // A unit of attention that was cut leaves one part per CTA: for each row the
 // maximum m of its exponents (to base 2), l = sum of the weights relative to m,

@@ -95,8 +95,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
-// mbar_wait for a thread that a whole CTA waits on: it polls (test_wait) and
-// is not suspended, so it sees the phase sooner.
+// One look at the phase: the thread is not suspended.
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -107,24 +106,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
-}
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const WaitCtl& w,
-                                          int site) {
-  const uint32_t a = smem_u32(bar);
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_test_wait(a, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-      if (mbar_test_wait(a, parity)) return true;
-    if (*w.abort) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-      wait_timed_out(w, site);
-      return false;
-    }
-  }
 }
 
 // Bounded wait that ignores the abort flag (used to drain copies in flight
@@ -140,11 +121,6 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
 // Named barrier among `nthreads` threads (a multiple of 32).
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// Arrive on a named barrier that others wait on (a multiple of 32 in all).
-__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -262,18 +238,6 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, one-byte inputs (e4m3 by the instruction
-// descriptor's formats 0), K = 32, fp32 accumulate.
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 

@@ -218,6 +218,19 @@ def test_frozen_heads_behind_short_units(api):
     c.check(out, lse, slice(0, 16, 3))
 
 
+@pytest.mark.parametrize("n_q", [64, 128, 129, 300])
+@pytest.mark.parametrize("frozen", [(0, 1, 2), (1, 3, 4, 5, 6)])
+def test_row_tiles_of_frozen_heads_come_in_pairs(api, n_q, frozen):
+    # odd and even numbers of tiles; the two of a unit are of one head or of two
+    lens = [n_q + 70, 333, n_q, 20]
+    c = Case(api, mask_of(8, frozen), 1, 64, 32, lens, n_q, n_new=[n_q, min(n_q, 201), n_q - 1, 30],
+             seed=n_q, kernel="cache_chunk")
+    for s, j in [(0, n_q + 65), (2, n_q - 3)]:
+        c.v_codes[c.table[s, j // 32], :, j % 32, 3] = 0x7F
+    c.put()
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("n_q,kernel", [(1, "cache_attn"), (3, "cache_attn"), (40, None),
                                         (40, "cache_chunk")])
 @pytest.mark.parametrize("d,page", [(128, 64), (64, 16), (32, 128)])

@@ -92,10 +92,10 @@ saf_status make_call(const saf_cache_dims& d, const uint8_t* head_is_static, con
 // cache_chunk.cu takes longer to start and reads them once for 256 rows of the
 // dynamic heads and once for 256 of each frozen one.  What the host knows of the
 // lengths is the page table's width.  The times are in nanoseconds on the whole
-// GPU for a unit of rows and for each of its keys, fitted to 220 calls drawn at
-// random that were timed with both: the choice costs 0.2% over the better one (by
-// rows alone, 8%).  E.g. 3 x 159 rows of 64 components: 8 us here and 18 us
-// there; 10 x 276 rows of 3 heads against 10471 keys: 501 and 141 us.
+// GPU for a unit of rows and for each of its keys, fitted to 300 calls drawn at
+// random that were timed with both: the choice costs 0.1% over the better one (by
+// rows alone, 11%).  E.g. 4 x 107 rows of 2 heads against 107 keys: 8 and 18 us;
+// 8 x 370 rows of 9 heads of 3 against 7973 keys: 494 and 120 us.
 bool many_rows(const saf_cache_dims& d, const uint8_t* is_static, int n_q) {
   const int g = d.H / d.H_kv;
   const long long rows = (long long)n_q * g, tile = rows <= 8 ? 8 : 16;
@@ -107,8 +107,8 @@ bool many_rows(const saf_cache_dims& d, const uint8_t* is_static, int n_q) {
     units += ((long long)n_q * (g - frozen) + 255) / 256 + ((long long)n_q + 255) / 256 * frozen;
   }
   const double few_units = (double)d.n_seqs * d.H_kv * ((rows + tile - 1) / tile);
-  const double few = 5e3 + few_units * (17 + 0.05 * keys);
-  const double many = 26e3 + (double)d.n_seqs * units * (66 + 0.11 * keys);
+  const double few = 5e3 + few_units * (10 + 0.03 * keys);
+  const double many = 18e3 + (double)d.n_seqs * units * (50 + 0.09 * keys);
   return few > many;
 }
 

@@ -43,8 +43,11 @@ constexpr int kWarps = 4;
 // A unit is (slot b, K/V head, row tile): up to 8 NT of the slot's n_new * group
 // query rows (row r = t * group + h) against all its keys, in tiles of kTile
 // keys.  The row tiles of a head lie side by side, so that their codes come from
-// L2 after the first.  All tiles of all units, in that order, are cut into equal
-// shares, one for each CTA; a unit that is cut leaves partial sums, joined by a
+// L2 after the first.  All tiles of all units, in that order, are cut into shares,
+// one for each CTA, equal when a unit counts kUnitCost tiles more for its
+// beginning and end (64 slots of up to 2500 tokens, 32 heads of 8: 55 us with none,
+// 45 with one, 42 with two, 41 with three; 16 x 2047 tokens of 12 heads of 64: 23.1,
+// 19.9, 19.4, 20.9); a unit that is cut leaves partial sums, joined by a
 // second kernel in the order of the CTAs.  Nothing depends on timing.  A share may
 // be a single tile: what a step costs a CTA without company is the latency of its
 // loads (one token against 1000, 16 heads of 4: 8.6 us; with shares of 4 tiles and
@@ -55,6 +58,7 @@ constexpr int kWarps = 4;
 // against 8.2 for 4 units of 4 tiles, 8.8 against 12.3 for 256.  With up to
 // kWholeTilesMany that pays only where there are units for half of the SMs: 11.5
 // against 8.4 us for 4 units of 8 tiles, 11.8 and 11.4 for 64, 13.1 and 15.6 for 256.
+constexpr int kUnitCost = 2;
 constexpr int kWholeTiles = 4, kWholeTilesMany = 8;
 constexpr int kJoinAhead = 8;    // parts that a joining thread has in flight
 
@@ -87,32 +91,42 @@ __device__ __forceinline__ uint32_t chunk_at(int key, int ch) {
   return (key >> 2) * 128 + (((key & 3) ^ (((key >> 2) & 1) << 1)) << 5) + (ch << 4);
 }
 
-template <int TILE>
-__device__ __forceinline__ int slot_tiles(const CacheCall& c, int b) {
-  const Rows r = slot_rows(c, b);
-  if (r.n_new == 0) return 0;
-  const int n = (r.cap + TILE - 1) / TILE;
-  return n < 1 ? 1 : n;  // rows that see nothing are written too
+// The units of a slot, n_new * group rows in row tiles of MR for each K/V head, and
+// the tiles of keys that each of them takes.
+struct SlotUnits {
+  int row_tiles, units, tiles;
+};
+template <int TILE, int MR>
+__device__ __forceinline__ SlotUnits slot_units(const CacheCall& c, const Rows& r) {
+  SlotUnits u;
+  u.row_tiles = (int)(((long long)r.n_new * c.group + MR - 1) / MR);
+  u.units = c.H_kv * u.row_tiles;
+  u.tiles = max(1, (r.cap + TILE - 1) / TILE);  // rows that see nothing are written too
+  return u;
+}
+template <int TILE, int MR>
+__device__ __forceinline__ long long slot_cost(const CacheCall& c, int b) {
+  const SlotUnits u = slot_units<TILE, MR>(c, slot_rows(c, b));
+  return (long long)u.units * (u.tiles + kUnitCost);
 }
 
 struct Share {
-  long long size, begin, end;  // tiles of a CTA
-  int b;                       // the slot of tile `begin` and that tile's index in the slot
+  long long size, begin, end;  // of a CTA: the tiles that begin there
+  int b;                       // the slot that holds `begin`, and how far behind its start
   long long in_slot;
 };
 
 // Every CTA finds its share: each thread sums a run of slots, a block scan
-// gives the runs' first tiles, and the thread whose run holds the share's
-// first tile walks it.
-template <int TILE>
-__device__ Share find_share(const CacheCall& c, int per_slot, long long* scan /* [kWarps + 2] */) {
+// gives the runs' beginnings, and the thread whose run holds the share's
+// beginning walks it.
+template <int TILE, int MR>
+__device__ Share find_share(const CacheCall& c, long long* scan /* [kWarps + 2] */) {
   constexpr int n = kWarps * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (c.n_seqs + n - 1) / n;
   const int b0 = min(tid * per, c.n_seqs), b1 = min(b0 + per, c.n_seqs);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += slot_tiles<TILE>(c, b);
-  sum *= per_slot;
+  for (int b = b0; b < b1; ++b) sum += slot_cost<TILE, MR>(c, b);
   long long upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -135,7 +149,7 @@ __device__ Share find_share(const CacheCall& c, int per_slot, long long* scan /*
     long long at = mine;
     int b = b0;
     for (; b < b1 - 1; ++b) {
-      const long long t = (long long)slot_tiles<TILE>(c, b) * per_slot;
+      const long long t = slot_cost<TILE, MR>(c, b);
       if (s.begin < at + t) break;
       at += t;
     }
@@ -198,33 +212,54 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
   // the joining kernel may be set up meanwhile; it waits for this one's end
   if (!whole_units) asm volatile("griddepcontrol.launch_dependents;");
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing here waits without end
-  const int per_slot = c.H_kv * row_tiles;  // units of a slot
+  const int per_slot = c.H_kv * row_tiles;  // units that a slot can have
   Share sh;
   if (whole_units) {
     sh.b = blockIdx.x / per_slot;
-    const int n = slot_tiles<kTile>(c, sh.b);
-    if (n == 0) return;
-    sh.in_slot = (long long)n * (blockIdx.x - sh.b * per_slot);
-    sh.begin = 0;
-    sh.end = sh.size = n;
   } else {
-    sh = find_share<kTile>(c, per_slot, scan);
+    sh = find_share<kTile, kMR>(c, scan);
     if (threadIdx.x == 0 && !by_unit) p.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (sh.begin >= sh.end) return;
   }
-
-  int b = sh.b, ut = slot_tiles<kTile>(c, b);
+  int b = sh.b;
   Rows rows = slot_rows(c, b);
-  int unit = (int)(sh.in_slot / ut), tile = (int)(sh.in_slot % ut);
-  long long at = sh.begin;
+  SlotUnits su = slot_units<kTile, kMR>(c, rows);
+  int unit = 0, tile = 0;
+  long long at;  // where the unit begins
+  auto next_unit = [&]() {
+    if (++unit < su.units) return;
+    unit = 0;
+    do {
+      rows = slot_rows(c, ++b);
+    } while (rows.n_new == 0);
+    su = slot_units<kTile, kMR>(c, rows);
+  };
+  if (whole_units) {
+    unit = blockIdx.x - sh.b * per_slot;
+    if (unit >= su.units) return;
+    tile = 0;
+    at = sh.begin = 0;
+    sh.end = sh.size = su.tiles;
+  } else {
+    const int cost = su.tiles + kUnitCost;
+    unit = (int)(sh.in_slot / cost);
+    tile = (int)(sh.in_slot - (long long)unit * cost);
+    at = sh.begin - tile;
+    if (tile >= su.tiles) {  // all its tiles begin in the shares before
+      tile = 0;
+      at += cost;
+      if (at >= sh.end) return;
+      next_unit();
+    }
+  }
 
-  while (true) {
+  for (bool first = true;; first = false) {
     // ---- this segment: tiles [tile, tile_end) of the slot's unit (kv, rows r0 ..)
-    const int kv = unit / row_tiles, r0 = (unit - kv * row_tiles) * kMR;
-    const int tile_end = (int)min((long long)ut, tile + (sh.end - at));
+    const int kv = unit / su.row_tiles, r0 = (unit - kv * su.row_tiles) * kMR;
+    const int tile_end = (int)min((long long)su.tiles, sh.end - at);
     const int ext = rows.cap;
-    const int n_rows = min(kMR, rows.n_new * c.group - r0);  // none: a short slot's last tiles
-    const int steps = n_rows > 0 ? tile_end - tile : 0;
+    const int n_rows = min(kMR, rows.n_new * c.group - r0);
+    const int steps = tile_end - tile;
     const int k_head = c.k_of[kv];
     const bool any_dyn = k_head >= 0;  // a dynamic head in the group
     const int key_w = tile * kTile + warp * kStep;  // first key of this warp's step 0
@@ -624,8 +659,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
         }
       }
     __syncthreads();
-    const bool whole = tile == 0 && tile_end == ut;
-    const int part = 2 * blockIdx.x + (at == sh.begin ? 0 : 1);
+    const bool whole = tile == 0 && tile_end == su.tiles;
+    const int part = 2 * blockIdx.x + (first ? 0 : 1);
     for (int i = threadIdx.x; i < n_rows * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float mx = -CUDART_INF_F, sum = 0.f;
@@ -659,24 +694,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
     if (tile == 0 && threadIdx.x == 0 && !whole_units) {
       // the unit begins here and ends in CTA `last`; only the last that begins here
       // can be cut
-      const int left = max(0, (int)(at + ut - sh.end));  // tiles behind this CTA's
+      const int left = max(0, (int)(at + su.tiles - sh.end));  // tiles behind this CTA's
       const int last = blockIdx.x + cta_span(left, sh.size);
       p.join[by_unit ? b * per_slot + unit : blockIdx.x] =
-          make_int4(tile_end < ut ? b : -1, unit, blockIdx.x, last | (at == sh.begin ? 0 : 1 << 30));
+          make_int4(tile_end < su.tiles ? b : -1, unit, blockIdx.x, last | (first ? 0 : 1 << 30));
     }
 
     // ---- the next unit
-    at += tile_end - tile;
+    at += su.tiles + kUnitCost;
     if (at >= sh.end) break;
     __syncthreads();  // the merge buffer is free again
     tile = 0;
-    if (++unit == per_slot) {
-      unit = 0;
-      do {
-        ut = slot_tiles<kTile>(c, ++b);
-      } while (ut == 0);
-      rows = slot_rows(c, b);
-    }
+    next_unit();
   }
 }
 
@@ -690,12 +719,19 @@ __global__ void __launch_bounds__(kJoinThreads)
   const CacheCall& c = p.c;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 u = p.join[blockIdx.x];
-  const bool none = by_unit && slot_rows(c, blockIdx.x / (c.H_kv * row_tiles)).n_new == 0;
-  if (none || u.x < 0) return;  // (a slot without rows has no entries)
-  const int b = u.x, kv = u.y / row_tiles, r0 = (u.y - kv * row_tiles) * kMR;
+  if (by_unit) {  // a unit that the slot has no rows for has no entry
+    const int per_slot = c.H_kv * row_tiles, slot = blockIdx.x / per_slot;
+    const Rows r = slot_rows(c, slot);
+    if ((int)blockIdx.x - slot * per_slot >= slot_units<1, kMR>(c, r).units) return;
+  }
+  if (u.x < 0) return;
+  const int b = u.x;
+  const Rows rows = slot_rows(c, b);
+  const int tiles = slot_units<1, kMR>(c, rows).row_tiles;  // of rows
+  const int kv = u.y / tiles, r0 = (u.y - kv * tiles) * kMR;
   const int cta = u.z, last = u.w & ~(1 << 30);
   const int n = last - cta + 1, first = 2 * cta + (u.w >> 30 & 1);
-  const int n_rows = min(kMR, slot_rows(c, b).n_new * c.group - r0);
+  const int n_rows = min(kMR, rows.n_new * c.group - r0);
   const int per = kJoinThreads / split, s = threadIdx.x / per;
   const int i = blockIdx.y * per + threadIdx.x % per;
   const int r = i / (D / 4), d = i % (D / 4) * 4;

@@ -46,8 +46,8 @@ constexpr int kWarps = 4;
 // L2 after the first.  All tiles of all units, in that order, are cut into shares,
 // one for each CTA, equal when a unit counts kUnitCost tiles more for its
 // beginning and end (64 slots of up to 2500 tokens, 32 heads of 8: 55 us with none,
-// 45 with one, 42 with two, 41 with three; 16 x 2047 tokens of 12 heads of 64: 23.1,
-// 19.9, 19.4, 20.9); a unit that is cut leaves partial sums, joined by a
+// 45 with one, 42 with two, 41 with three; 48 slots of up to 4096, 12 heads of 4, d_h
+// = 64: 23.1, 19.9, 19.4, 20.9); a unit that is cut leaves partial sums, joined by a
 // second kernel in the order of the CTAs.  Nothing depends on timing.  A share may
 // be a single tile: what a step costs a CTA without company is the latency of its
 // loads (one token against 1000, 16 heads of 4: 8.6 us; with shares of 4 tiles and

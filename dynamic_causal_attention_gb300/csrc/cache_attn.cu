@@ -177,14 +177,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// CTAs on an SM, and stages of a ring: together about 190 KB.
+// CTAs on an SM: as many as the registers allow without spills (8 rows: 166 of 168;
+// a fourth CTA's 128 cost 32 x 8192 tokens of 16 heads 162 us for 151, two CTAs 178),
+// and stages of a ring: with two it is 203 us, with four 160.
 template <int NT>
-constexpr int kCtas = NT == 1 ? 4 : 2;
-template <int NT>
-constexpr int kStages = NT == 1 ? 3 : 6;
+constexpr int kCtas = NT == 1 ? 3 : 2;
+constexpr int kStages = 3;
 template <int D, int NT>
 constexpr int smem_bytes() {
-  const int ring = kWarps * kStages<NT> * Geo<D>::kStage, merge = kWarps * 8 * NT * (D + 2) * 4;
+  const int ring = kWarps * kStages * Geo<D>::kStage, merge = kWarps * 8 * NT * (D + 2) * 4;
   return ring > merge ? ring : merge;
 }
 
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
   constexpr int kKL = kKW < 4 ? kKW : 4; // words of one load
   constexpr int kVB = D / 8;             // bytes of a V row that a lane takes
   using G = Geo<D>;
-  constexpr int kS = kStages<NT>;
+  constexpr int kS = kStages;
   extern __shared__ __align__(128) uint8_t smem[];  // the rings; then the warps' sums
   float* merge = reinterpret_cast<float*>(smem);
   __shared__ long long scan[kWarps + 2];
@@ -801,8 +802,8 @@ CacheAttnWs cache_attn_ws(int d_h, int n_sms) {
     return o;
   };
   // the larger of both row counts
-  const size_t n = (size_t)n_ctas(1, n_sms), n2 = (size_t)n_ctas(2, n_sms);
-  const size_t rows = 2 * (n * 8 > n2 * 16 ? n * 8 : n2 * 16);
+  const size_t n1 = (size_t)n_ctas(1, n_sms), n2 = (size_t)n_ctas(2, n_sms);
+  const size_t n = n1 > n2 ? n1 : n2, rows = 2 * (n1 * 8 > n2 * 16 ? n1 * 8 : n2 * 16);
   w.status = take(256);
   w.join = take(n * sizeof(int4));
   w.ml = take(rows * 2 * 4);

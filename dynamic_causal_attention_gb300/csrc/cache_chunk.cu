@@ -78,28 +78,33 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
 // k-step with the descriptors advanced by adds.  One issuing thread then gets a
 // product through in about 75 cycles in place of about 160.
 template <int N, int STEP>  // S += hi K^T, then lo K^T: N steps of 32 codes each
-__device__ __forceinline__ void issue_codes(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+__device__ __forceinline__ void issue_codes(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc,
+                                            uint32_t lead) {
   static_assert(N == 1 || N == 2 || N == 4, "");
-#define SAF_MMA8 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, "
-#define SAF_NEXT "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+#define SAF_MMA8 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, "
+#define SAF_NEXT \
+  "add.u32 p, p, 2;\n\tadd.u32 q, q, 2;\n\tmov.b64 a, {p, u};\n\tmov.b64 b, {q, v};\n\t"
 #define SAF_HEAD                                                                              \
-  "{\n\t.reg .pred f, t;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 t, 0, 0;\n\tmov.pred f, t;\n\t"    \
-  "not.pred t, f;\n\tmov.b64 a, %1;\n\tmov.b64 b, %2;\n\t"
-#define SAF_LOW "add.s64 a, %1, %4;\n\tmov.b64 b, %2;\n\t"
+  "{\n\t.reg .pred f, t, e;\n\t.reg .b64 a, b;\n\t.reg .b32 p, q, u, v;\n\t"           \
+  "setp.ne.b32 t, 0, 0;\n\tmov.pred f, t;\n\tnot.pred t, f;\n\tsetp.ne.b32 e, %5, 0;\n\t"  \
+  "mov.b64 a, %1;\n\tmov.b64 b, %2;\n\tmov.b64 {p, u}, a;\n\tmov.b64 {q, v}, b;\n\t"
+#define SAF_LOW                                                                     \
+  "mov.b64 a, %1;\n\tmov.b64 b, %2;\n\tmov.b64 {p, u}, a;\n\tmov.b64 {q, v}, b;\n\t" \
+  "add.u32 p, p, %4;\n\tmov.b64 a, {p, u};\n\t"
   if constexpr (N == 1)
     asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_LOW SAF_MMA8 "t;\n\t}" ::"r"(d), "l"(q), "l"(k),
-                 "r"(idesc), "n"(STEP)
+                 "r"(idesc), "n"(STEP), "r"(lead)
                  : "memory");
   else if constexpr (N == 2)
     asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_LOW SAF_MMA8
                  "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t}" ::"r"(d),
-                 "l"(q), "l"(k), "r"(idesc), "n"(STEP)
+                 "l"(q), "l"(k), "r"(idesc), "n"(STEP), "r"(lead)
                  : "memory");
   else
     asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8
                  "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_LOW SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8
                  "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t}" ::"r"(d),
-                 "l"(q), "l"(k), "r"(idesc), "n"(STEP)
+                 "l"(q), "l"(k), "r"(idesc), "n"(STEP), "r"(lead)
                  : "memory");
 #undef SAF_MMA8
 #undef SAF_NEXT
@@ -110,14 +115,14 @@ __device__ __forceinline__ void issue_codes(uint32_t d, uint64_t q, uint64_t k, 
 // descriptor advanced by STEP.
 template <int STEP>
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc,
-                                         uint32_t accumulate) {
-#define SAF_MMA "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, "
-#define SAF_NEXT "add.s32 a, a, 8;\n\tadd.s64 b, b, %5;\n\t"
+                                         uint32_t accumulate, uint32_t lead) {
+#define SAF_MMA "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, "
+#define SAF_NEXT "add.u32 a, a, 8;\n\tadd.u32 q, q, %5;\n\tmov.b64 b, {q, v};\n\t"
   asm volatile(
-      "{\n\t.reg .pred f, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\tsetp.ne.b32 f, %4, 0;\n\t"
-      "setp.eq.b32 t, 0, 0;\n\tmov.b32 a, %1;\n\tmov.b64 b, %2;\n\t" SAF_MMA "f;\n\t" SAF_NEXT
+      "{\n\t.reg .pred f, t, e;\n\t.reg .b64 b;\n\t.reg .b32 a, q, v;\n\tsetp.ne.b32 f, %4, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tmov.b32 a, %1;\n\tmov.b64 b, %2;\n\tmov.b64 {q, v}, b;\n\t" SAF_MMA "f;\n\t" SAF_NEXT
       SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t}" ::"r"(d),
-      "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "n"(STEP)
+      "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "n"(STEP), "r"(lead)
       : "memory");
 #undef SAF_MMA
 #undef SAF_NEXT
@@ -914,40 +919,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------ products
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-      if ((warp == 12 || warp == 14) && lane == 0) {
-        const int g = (warp - 12) >> 1;
+      // (whole warps, so that descriptors and counters stay in uniform registers)
+      const int uwarp = __shfl_sync(~0u, warp, 0);
+      if (uwarp == 12 || uwarp == 14) {
+        const int g = (uwarp - 12) >> 1;
+        const uint32_t lead = lane == 0;
+        auto commit = [&](uint64_t* bar) {
+          if (lead) mma_commit(bar);
+        };
+        auto arrive = [&](uint64_t* bar) {
+          if (lead) mbar_arrive(bar);
+        };
         constexpr uint32_t id_s = idesc_e4m3(128, 64);
         constexpr uint32_t id_o = idesc_f16(128, D, false, true);
+        auto poll = [&](uint64_t* bar, uint32_t parity, const WaitCtl& c, int site) {
+          poll_bar(bar, parity, c, site);
+          __syncwarp();
+        };
         const uint32_t s_col = tmem + kS + g * 128, o_col = tmem + kO + g * 128;
         const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
         uint32_t kc = 0, vc = 0, n_q = 0, n_p = 0;
+        tile = __shfl_sync(~0u, tile, 0);
         for (;;) {
-          const int tile_end = w.tiles_before(sh.end - at);
-          const bool ice = w.ice();
-          const bool mine = unit_rows(w.rows, w.pair, w.gk(), ice).n > g * 128;
+          const int tile_end = __shfl_sync(~0u, w.tiles_before(sh.end - at), 0);
+          const bool ice = __shfl_sync(~0u, (int)w.ice(), 0);
+          const bool mine = __shfl_sync(~0u, unit_rows(w.rows, w.pair, w.gk(), ice).n, 0) > g * 128;
           // K of tile i + 1 and V of tile i are waited for while a product of the
           // tile before runs, so that the waits are not part of the row tile's chain
-          auto wait_k = [&](uint32_t n) { poll_bar(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK); };
-          auto wait_v = [&](uint32_t n) { poll_bar(v_full + (n & 1), (n >> 1) & 1, wc, kSiteV); };
+          auto wait_k = [&](uint32_t n) { poll(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK); };
+          auto wait_v = [&](uint32_t n) { poll(v_full + (n & 1), (n >> 1) & 1, wc, kSiteV); };
           // S of 64 keys: the tile's first or second half
           auto issue_s = [&](int hf) {
             const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES + hf * 64 * D, 16, 8 * D,
                                       swizzle_layout_code(D));
-            issue_codes<D / 32, (L::CODES >> 4)>(s_col + 64 * hf, qt, kt, id_s);
-            mma_commit(s_full + 2 * g + hf);
+            issue_codes<D / 32, (L::CODES >> 4)>(s_col + 64 * hf, qt, kt, id_s, lead);
+            commit(s_full + 2 * g + hf);
           };
           auto k_done = [&]() {
             if (mine)
-              mma_commit(k_empty + kc % L::KST);
+              commit(k_empty + kc % L::KST);
             else
-              mbar_arrive(k_empty + kc % L::KST);
+              arrive(k_empty + kc % L::KST);
             ++kc;
           };
-          if (mine) mbar_arrive(begun + g);
+          if (mine) arrive(begun + g);
           if (!ice) {
             wait_k(kc);
             if (mine) {
-              poll_bar(q_full + g, n_q++ & 1, wc, kSiteQ);
+              poll(q_full + g, n_q++ & 1, wc, kSiteQ);
               tc_fence_after();
               issue_s(0);
               issue_s(1);
@@ -965,28 +984,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int hf = 0; hf < 2; ++hf) {
                 const int bar = 2 * g + hf;
-                poll_bar(p_full + bar, n_p & 1, wc, kSiteP);
+                poll(p_full + bar, n_p & 1, wc, kSiteP);
                 tc_fence_after();
                 issue_pv<kVStep>(o_col, s_col + 64 * hf, vt + 4 * kVStep * hf, id_o,
-                                 i > tile || hf);
-                mma_commit(o_done + bar);
-                mbar_arrive(o_done + bar);
+                                 i > tile || hf, lead);
+                commit(o_done + bar);
+                arrive(o_done + bar);
                 if (hf)
-                  mma_commit(v_empty + st);
+                  commit(v_empty + st);
                 else if (next) {
                   wait_v(vc);
                   if (!ice && i + 2 < tile_end) wait_k(kc + 1);
                 }
                 // S takes the columns of the P that these products read
                 if (more) {
-                  poll_bar(o_done + bar, n_p & 1, wc, kSiteO);
+                  poll(o_done + bar, n_p & 1, wc, kSiteO);
                   tc_fence_after();
                   issue_s(hf);
                 }
               }
               ++n_p;
             } else {
-              mbar_arrive(v_empty + st);
+              arrive(v_empty + st);
               if (next) wait_v(vc);
               if (!ice && i + 2 < tile_end) wait_k(kc + 1);
             }
@@ -998,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.next();
         }
         // every product has completed before TMEM is freed
-        mma_commit(drained + g);
+        commit(drained + g);
         mbar_drain(drained + g, 0);
       } else if (warp == 13) {
         // ---------------------------------------------------------- codes and scales

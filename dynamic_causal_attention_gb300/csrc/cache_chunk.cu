@@ -36,10 +36,10 @@
 // the other half's do, and P, as packed f16, overwrites the first columns of
 // its own half of S, so the next S of a half waits only for the product that
 // reads that half's P.  What a tile of keys costs is the chain S, softmax, P V
-// and its hand-offs, about 4400 cycles for 256 rows at d_h = 128, against some
+// and its hand-offs, about 4200 cycles for 256 rows at d_h = 128, against some
 // 1800 of the tensor cores' time; 2 x 2000 rows of 16 heads against 8192 keys take
-// 267 us, 48% of the measured burst rate of products, and with 4 frozen heads,
-// whose weights are 64 loads from the window for each half a tile, 273 us (41%).
+// 254 us, 50% of the measured burst rate of products, and with 4 frozen heads,
+// whose weights are 64 loads from the window for each half a tile, 261 us (43%).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>

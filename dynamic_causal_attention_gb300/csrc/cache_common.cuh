@@ -190,7 +190,7 @@ __device__ __forceinline__ void add_part(Part& a, const Part& b) {
 // is the latency of its loads, so many parts want many threads; few parts want
 // few blocks.  For the same reason blocks are counted by units where there are
 // fewer of them than CTAs.  (One token against 29242, 4 K/V heads in 152 parts
-// each: 41 us with a thread for all parts of its components, 15.9 us so.)
+// each: 41 us with a thread for all parts of its components, 14.1 us so.)
 constexpr int kJoinThreads = 128, kJoinSplit = 8;
 inline int join_split(long long ctas, long long units) {
   return ctas > 8 * units ? kJoinSplit : 1;

@@ -39,7 +39,8 @@
 // and its hand-offs, about 4200 cycles for 256 rows at d_h = 128, against some
 // 1800 of the tensor cores' time; 2 x 2000 rows of 16 heads against 8192 keys take
 // 254 us, 50% of the measured burst rate of products, and with 4 frozen heads,
-// whose weights are 64 loads from the window for each half a tile, 261 us (43%).
+// whose weights are 32 loads of two from the window for each half a tile, 258 us
+// (43%; 64 loads of one: 261, and with all heads frozen 282 for 272).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -373,10 +374,13 @@ struct Smem {
   static constexpr int OFF_K = 4 * TILE;
   static constexpr int OFF_R = OFF_K + KST * CODES;
   static constexpr int OFF_META = OFF_R + RST * CODES;  // 4 tiles x 8 groups of 16 keys x 16 bytes
-  // frozen rows: 128 alphas and the 384 rhos of a tile, times
-  // log2(e), for 4 tiles
+  // frozen rows: 128 alphas and the 384 rhos of a tile, times log2(e), and the rhos
+  // again from the second one on, 16 banks further, so that rows of either parity
+  // read two at a time; for 4 tiles
+  static constexpr int WIN0 = 128, WIN1 = WIN0 + 384 + 16;  // in floats
+  static constexpr int PAT = (WIN1 + 384) * 4;
   static constexpr int OFF_PAT = OFF_META + 4 * 8 * 16;
-  static constexpr int OFF_SCAN = OFF_PAT + 4 * 2048;
+  static constexpr int OFF_SCAN = OFF_PAT + 4 * PAT;
   static constexpr int OFF_BAR = OFF_SCAN + (kThreads / 32 + 4) * 8;
   static constexpr int NBAR = 2 + 2 * KST + 2 * RST + 4 + 4 + 4 + 4 + 4 + 2 + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -662,18 +666,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
                     asm volatile("" : "+f"(gm[0]), "+f"(gm[1]), "+f"(gm[2]), "+f"(gm[3]));
                   } else {
-                    // distance of (row, column k): entry (row of the unit) - k + 127
+                    // distance of (row, column k): entry (row of the unit) - k + 127 of
+                    // the window; entries e - k - 1 and e - k are read together
                     const float* pat =
-                        reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * 2048) + 64 * hf;
-                    const float* win = pat + 128 + g * 128 + r + 127 - 128 * hf;
+                        reinterpret_cast<const float*>(smem + L::OFF_PAT + (nt & 3) * L::PAT);
+                    const int e = g * 128 + r + 127 - 64 * hf;
+                    const float* win = pat + (e & 1 ? L::WIN0 + e - 1 : L::WIN1 + e - 2);
+                    pat += 64 * hf;
 #pragma unroll
                     for (int k = 0; k < 64; k += 4) {
                       const float4 x = *reinterpret_cast<const float4*>(pat + k);
+                      const float2 w0 = *reinterpret_cast<const float2*>(win - k);
+                      const float2 w1 = *reinterpret_cast<const float2*>(win - k - 2);
                       uint32_t* y = s[k / 16] + k % 16;
-                      y[0] = __float_as_uint(x.x + win[-k]);
-                      y[1] = __float_as_uint(x.y + win[-k - 1]);
-                      y[2] = __float_as_uint(x.z + win[-k - 2]);
-                      y[3] = __float_as_uint(x.w + win[-k - 3]);
+                      y[0] = __float_as_uint(x.x + w0.y);
+                      y[1] = __float_as_uint(x.y + w0.x);
+                      y[2] = __float_as_uint(x.z + w1.y);
+                      y[3] = __float_as_uint(x.w + w1.x);
                     }
                   }
                   if (edge) {
@@ -1094,9 +1103,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                               there ? __fdividef(1.f, sc.y) : 1.f, 0.f);
             }
             if (w.ice()) {
-              float* to = reinterpret_cast<float*>(smem + L::OFF_PAT + (vc & 3) * 2048) + lane;
+              float* to = reinterpret_cast<float*>(smem + L::OFF_PAT + (vc & 3) * L::PAT) + lane;
 #pragma unroll
               for (int k = 0; k < 16; ++k) to[32 * k] = pat[k];
+#pragma unroll
+              for (int k = 0; k < 12; ++k) to[L::WIN1 - 1 + 32 * k] = pat[4 + k];
             }
             mbar_arrive(m_full + (vc & 3));
             fetch_pattern(i + 1);

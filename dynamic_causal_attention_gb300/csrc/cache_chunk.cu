@@ -199,20 +199,22 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // full): the tiles of keys, and behind them the unit's own cost: Q, the first tile
 // without company, the results.  Measured with equal units, microseconds:
 //                          d_h = 128     64      32
-//   tile, dynamic             2.36      1.90    1.70     (one row tile 2.18 1.80 1.57)
-//   tile, frozen              2.59      2.51    2.40     (one row tile 2.11 1.96 1.67)
-//   unit, dynamic, frozen     11, 8.6   6.1, 4.4   4.1, 3.1
+//   tile, dynamic             2.22      1.78    1.56     (one row tile 1.99 1.66 1.38)
+//   tile, frozen              2.28      2.35    2.18     (one row tile 2.15 1.88 1.58)
+//   unit, dynamic, frozen     11, 8.7   6.3, 4.4   4.5, 3.3
 // With tiles alone counted, 2 x 2000 rows of 16 heads, 4 of them frozen, against
 // 8192 keys took 287 us for 273 (the average SM was idle for a tenth of them), 12 x
-// 76 rows of 128 heads against 388 keys 63 for 47.
+// 76 rows of 128 heads against 388 keys 63 for 47.  (At d_h = 128 the frozen tile
+// counts 9 and units a little less than alone: 258 us in that call, with 8, 38 and
+// 31 267.)
 struct Costs {
   int tile[2][2];  // [frozen][both row tiles]
   int unit[2];     // [frozen]
 };
 __device__ __forceinline__ constexpr Costs costs_of(int d) {
-  return d == 128  ? Costs{{{7, 8}, {7, 9}}, {37, 29}}
-         : d == 64 ? Costs{{{8, 8}, {8, 11}}, {26, 19}}
-                   : Costs{{{7, 8}, {8, 11}}, {19, 15}};
+  return d == 128  ? Costs{{{7, 8}, {8, 9}}, {34, 28}}
+         : d == 64 ? Costs{{{7, 8}, {8, 11}}, {28, 20}}
+                   : Costs{{{7, 8}, {8, 11}}, {23, 17}};
 }
 constexpr int kMaxTileCost = 11;
 

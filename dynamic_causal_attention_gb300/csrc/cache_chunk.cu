@@ -517,10 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!p.by_unit) p.a.join[blockIdx.x] = make_int4(-1, 0, 0, 0);
     *wc.status = 0;
   }
-  if (threadIdx.x == 32) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
   if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();

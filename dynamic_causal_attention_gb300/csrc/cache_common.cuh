@@ -19,6 +19,42 @@
 namespace saf {
 
 // ------------------------------------------------------------ PTX
+// One look at the phase: the thread is not suspended.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// 4-D tiled copy global -> shared, whole in the two inner dimensions.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// tmem_ld_x16 with the maximum of the 16 values as floats (a NaN does not
+// count) in `top`; valid after tmem_wait_ld as well (sm_103).
+__device__ __forceinline__ void tmem_ld_max_x16(uint32_t taddr, uint32_t (&r)[16], float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+}
+
 // 16-byte asynchronous copy global -> shared; `bytes` (0..16) are read, the
 // rest of the destination is zero-filled.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {

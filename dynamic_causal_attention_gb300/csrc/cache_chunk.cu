@@ -39,8 +39,8 @@
 // and its hand-offs, about 4200 cycles for 256 rows at d_h = 128, against some
 // 1800 of the tensor cores' time; 2 x 2000 rows of 16 heads against 8192 keys take
 // 254 us, 50% of the measured burst rate of products, and with 4 frozen heads,
-// whose weights are 32 loads of two from the window for each half a tile, 258 us
-// (43%; 64 loads of one: 261, and with all heads frozen 282 for 272).
+// whose weights are 32 loads of two from the window for each half a tile, 260 us
+// (43%; 64 loads of one: 262, and with all heads frozen 282 for 272).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>

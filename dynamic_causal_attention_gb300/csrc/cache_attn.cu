@@ -765,7 +765,8 @@ cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
       reinterpret_cast<const void*>(cache_attn_kernel<D, NT>), smem_bytes<D, NT>());
   if (e != cudaSuccess) return e;
   trace_begin(s);
-  cache_attn_kernel<D, NT><<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, row_tiles, whole, by_unit);
+  cache_attn_kernel<D, NT>
+      <<<grid, kWarps * 32, smem_bytes<D, NT>(), s>>>(p, row_tiles, whole, by_unit);
   trace_end(s, "cache_attn");
   e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
@@ -775,7 +776,8 @@ cudaError_t launch(const CacheAttn& p, int n_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const int split = join_split(grid, units);
-  cfg.gridDim = dim3(by_unit ? (int)units : grid, (8 * NT * (D / 4) * split + kJoinThreads - 1) / kJoinThreads);
+  cfg.gridDim = dim3(by_unit ? (int)units : grid,
+                     (8 * NT * (D / 4) * split + kJoinThreads - 1) / kJoinThreads);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;

@@ -121,8 +121,8 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uin
 #define SAF_NEXT "add.u32 a, a, 8;\n\tadd.u32 q, q, %5;\n\tmov.b64 b, {q, v};\n\t"
   asm volatile(
       "{\n\t.reg .pred f, t, e;\n\t.reg .b64 b;\n\t.reg .b32 a, q, v;\n\tsetp.ne.b32 f, %4, 0;\n\t"
-      "setp.ne.b32 e, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tmov.b32 a, %1;\n\tmov.b64 b, %2;\n\tmov.b64 {q, v}, b;\n\t" SAF_MMA "f;\n\t" SAF_NEXT
-      SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t}" ::"r"(d),
+      "setp.ne.b32 e, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tmov.b32 a, %1;\n\t"
+      "mov.b64 b, %2;\n\tmov.b64 {q, v}, b;\n\t" SAF_MMA "f;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t}" ::"r"(d),
       "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "n"(STEP), "r"(lead)
       : "memory");
 #undef SAF_MMA
@@ -145,7 +145,8 @@ struct UnitRows {
 __device__ __forceinline__ UnitRows unit_rows(const Rows& r, int pair, int gk, bool ice) {
   UnitRows u;
   if (ice) {
-    const int per = (r.n_new + kRows - 1) / kRows, idx = pair / per, at = (pair - idx * per) * kRows;
+    const int per = (r.n_new + kRows - 1) / kRows, idx = pair / per;
+    const int at = (pair - idx * per) * kRows;
     u.first = idx * r.n_new + at;
     u.n = min(kRows, r.n_new - at);
   } else {
@@ -953,7 +954,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool mine = __shfl_sync(~0u, unit_rows(w.rows, w.pair, w.gk(), ice).n, 0) > g * 128;
           // K of tile i + 1 and V of tile i are waited for while a product of the
           // tile before runs, so that the waits are not part of the row tile's chain
-          auto wait_k = [&](uint32_t n) { poll(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK); };
+          auto wait_k = [&](uint32_t n) {
+            poll(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK);
+          };
           auto wait_v = [&](uint32_t n) { poll(v_full + (n & 1), (n >> 1) & 1, wc, kSiteV); };
           // S of 64 keys: the tile's first or second half
           auto issue_s = [&](int hf) {
@@ -1203,7 +1206,8 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
 
 template <int D>
 cudaError_t launch(const CacheChunk& p, int n_sms, cudaStream_t s) {
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(cache_chunk_kernel<D>), Smem<D>::ALLOC);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(cache_chunk_kernel<D>),
+                                       Smem<D>::ALLOC);
   if (e != cudaSuccess) return e;
   trace_begin(s);
   const CacheCall& c = p.a.c;

@@ -498,9 +498,11 @@ __global__ void __launch_bounds__(kCopy)
   copy_pages(p, w.from, w.to, n);
 }
 
-// Launched while its predecessor runs (both plans allow it at their start); waits for the predecessor's end.
+// Launched while its predecessor runs (both plans allow it at their start); waits
+// for the predecessor's end.
 template <class K>
-cudaError_t launch_after(K kernel, const char* name, const CachePages& p, int grid, cudaStream_t s) {
+cudaError_t launch_after(K kernel, const char* name, const CachePages& p, int grid,
+                         cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

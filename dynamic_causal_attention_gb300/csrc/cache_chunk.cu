@@ -122,7 +122,8 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uin
   asm volatile(
       "{\n\t.reg .pred f, t, e;\n\t.reg .b64 b;\n\t.reg .b32 a, q, v;\n\tsetp.ne.b32 f, %4, 0;\n\t"
       "setp.ne.b32 e, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tmov.b32 a, %1;\n\t"
-      "mov.b64 b, %2;\n\tmov.b64 {q, v}, b;\n\t" SAF_MMA "f;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t}" ::"r"(d),
+      "mov.b64 b, %2;\n\tmov.b64 {q, v}, b;\n\t" SAF_MMA "f;\n\t" SAF_NEXT SAF_MMA "t;\n\t"
+      SAF_NEXT SAF_MMA "t;\n\t" SAF_NEXT SAF_MMA "t;\n\t}" ::"r"(d),
       "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "n"(STEP), "r"(lead)
       : "memory");
 #undef SAF_MMA

@@ -43,6 +43,7 @@
 // (43%; 64 loads of one: 262, and with all heads frozen 282 for 272).
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math_constants.h>
 
 #include "attn_common.cuh"
@@ -705,7 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int q = 0; q < 4; ++q) {
                     const float4 mt = lds_f32x4(meta + 16 * q);
-                    a[q] = kIce ? 1.f : fac * mt.x;
+                    // never zero: keys that the row does not see are at -inf already, and
+                    // 0 * -inf is NaN.  (The largest S, below 2^33, times the least normal
+                    // number is nothing beside a logit.)
+                    a[q] = kIce ? 1.f : fmaxf(fac * mt.x, FLT_MIN);
                     b[q] = mt.y;
                     inv[q] = mt.z;
                     top = fmaxf(top, fmaf(gm[q], a[q], b[q]));

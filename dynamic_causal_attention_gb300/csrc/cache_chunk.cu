@@ -795,8 +795,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < D / 32; ++q) nan[q] = 0;
             const bool edge_nan = nan_seg[4 * g + (n_unit & 3)] == (int)n_unit;
             if (edge_nan) {
-              // V holds NaN at a key of an edge tile: rows that see it take it
-              const int lo = w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo;
+              // V holds NaN at a key of an edge tile: rows that see it take it.  The
+              // first such tile holds the first row's position or the last key, which
+              // lies before it where the sequence is longer than the page table
+              const int lo = min(w.rows.base + pair_span(w.rows, w.pair, gk, ice).lo,
+                                 pair_extent(w.rows, w.pair, gk, ice));
               const int first = max(0, lo / kTile * kTile);
               for (int j = max(first, tile * kTile); j < min(lim_all, tile_end * kTile); ++j) {
                 const int page = page_at(c, w.b, j >> c.page_shift);

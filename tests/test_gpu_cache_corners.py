@@ -30,3 +30,20 @@ def test_small_queries_against_small_scales(api, d, e_q, e_k, n_q, kernel):
     c.q = (c.q.float() * 2.0 ** e_q).to(torch.bfloat16)
     c.put()
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("page,tail", [(64, 1), (16, 3), (32, 1)])
+def test_nan_in_a_table_that_ends_inside_a_tile(api, page, tail):
+    # seq_len lies far behind the table, whose keys are no multiple of 128: every row sees all
+    # of them, the NaN among them too
+    cols = 2 ** 18 // page + tail
+    length = cols * page + 1000
+    holes = [(0, j) for j in range(2, cols - 3)]
+    c = Case(api, mask_of(4, (1,)), 1, 32, page, [length], 80, holes=holes, cols=cols, seed=page)
+    c.kernel = "cache_chunk"
+    c.v_codes[c.table[0, cols - 1], 0, page - 5, 3] = 0x7F
+    c.v_codes[c.table[0, cols - 1], 0, 0, 30] = 0xFF
+    c.put()
+    out, lse = c.run()
+    assert bool(torch.isnan(out[0, :, :, [3, 30]].float()).all())
+    c.check(out, lse)

@@ -7,8 +7,8 @@
 // over the keys j <= i that lie on a page, with codes k_j, v_j and the scales
 // s_k, s_v of their block.  The block's V scale joins the exponent: with
 // y_j = x_j log2(e) + log2(s_v), the weights of the second product are
-// p_j = 2^{y_j - m} under a running maximum m of the y, and the sum of the
-// softmax is sum_j p_j / s_v.  So a weight is rounded to f16 relative to the
+// p_j = 2^{y_j - m} under a base m that follows the maximum of the y, and the sum
+// of the softmax is sum_j p_j / s_v.  So a weight is rounded to f16 relative to the
 // largest contribution to `out`, whatever the scales of the blocks.
 //
 // This file: few query rows for each slot and K/V head (single tokens and
@@ -525,9 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
             if ((frozen >> (2 * nt + i) & 1) && ice[nt][i])
               y = fmaf(pa[nt][i][2 * g + (u >> 1)] + pr[nt][i][2 * g + (u >> 1)], kLog2e, lv);
             if (edge && (k >= n[g] || key0 + k > pos[nt][i])) y = -CUDART_INF_F;
-            // the maximum moves only when it would grow by more than 2^8:
-            // weights up to 2^8 fit f16 as well
-            grow |= y > m[nt][i] + 8.f;
+            grow |= y > m[nt][i] + (kRoom + kLag);
           }
       }
       if (__any_sync(~0u, grow)) {
@@ -535,12 +533,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = m[nt][i];
+            float top = -CUDART_INF_F;
 #pragma unroll
             for (int g = 0; g < kG; ++g)
               if (n[g] > 0) top = fmaxf(top, fmaxf(sc[g][nt][i], sc[g][nt][2 + i]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            top = fmaxf(top - kRoom, m[nt][i]);
             const float corr = top == -CUDART_INF_F ? 1.f : fast_exp2(m[nt][i] - top);
             m[nt][i] = top;
             l[nt][i] *= corr;

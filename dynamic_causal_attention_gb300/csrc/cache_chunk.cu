@@ -714,10 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     inv[q] = mt.z;
                     top = fmaxf(top, fmaf(gm[q], a[q], b[q]));
                   }
-                  // the maximum moves only when it would grow by more than 2^8:
-                  // weights up to 2^8 fit f16 as well
-                  const bool need = top > m + 8.f;
+                  const bool need = top > m + (kRoom + kLag);
                   if (__any_sync(~0u, need)) {
+                    top -= kRoom;
                     const float corr = need ? fast_exp2(m - top) : 1.f;
                     if (need) m = top;
                     l *= corr;

@@ -141,6 +141,17 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
+// ------------------------------------------------------------ weights in f16
+// The second product takes its weights in f16, as p = 2^{y - m} for the exponents y
+// of a row and a base m that follows their maximum: m moves to kRoom below it once it
+// lies more than kRoom + kLag below.  So the largest weight is 2^11 to 2^15, in f16's
+// upper range, and a weight loses bits only where it is less than 2^-25 of the
+// largest (it is then off by at most 2^-36 of it); below 2^-36 it is lost.  The sum
+// of the softmax takes the weights in fp32.  (A base at the maximum itself loses
+// weights from 2^-14 on and all below 2^-25: 131072 keys 17.5 nats below one, a share
+// of 0.0033, came out as 0.)
+constexpr float kRoom = 11.f, kLag = 4.f;
+
 // 2^e as fp32 for e in [-126, 127].
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -202,7 +213,7 @@ __device__ __forceinline__ int page_at(const CacheCall& c, int b, int col) {
 
 // ------------------------------------------------------------ joining parts
 // A unit of attention that was cut leaves one part per CTA: for each row the
-// maximum m of its exponents (to base 2), l = sum of the weights relative to m,
+// base m of its exponents (to base 2), l = sum of the weights relative to m,
 // and the weighted sum o, of which a thread takes 4 components.  Parts are added
 // in the order of the CTAs.
 struct Part {

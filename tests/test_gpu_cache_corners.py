@@ -47,3 +47,50 @@ def test_nan_in_a_table_that_ends_inside_a_tile(api, page, tail):
     out, lse = c.run()
     assert bool(torch.isnan(out[0, :, :, [3, 30]].float()).all())
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("n_q,kernel,slots", [(1, "cache_attn", 1), (1, "cache_attn", 500),
+                                              (64, "cache_chunk", 1), (64, "cache_chunk", 80)])
+@pytest.mark.parametrize("nats,keys,at", [(16.0, 2 ** 15, 0), (17.5, 2 ** 17, 0),
+                                          (17.5, 2 ** 20, 5), (19.0, 2 ** 20, -100)])
+def test_many_keys_far_below_the_largest(api, nats, keys, at, n_q, kernel, slots):
+    """One key `nats` above all others, whose V is zero: out is their share.  With many slots (all
+    on the same pages) a warp or CTA has a long run of keys, with one the keys are cut into parts.
+
+    Tolerance: 2^-8 for bf16; the approximate exponential and the fp32 logits (2^-18); the f16
+    weight of a key, 2^-25 of at least 2^(11 - nats / ln 2), or 2^-11; two fp32 sums with 16 keys to
+    an addition.  That of the products grows evenly, and each addition is off by at most 2^-23 of
+    the sum so far: keys / 16 * 2^-24.  That of the weights holds the large one from its key on,
+    and each addition rounds by up to 2^-24 of the whole: keys / 16 * 2^-24 as well."""
+    d, page = 32, 128
+    at %= keys - n_q
+    cols = max(keys, 2 ** 18) // page
+    n_pages = keys // page
+    cache = api.PagedCache([[0, 1]], 2, d, H_kv=1, n_seqs=slots, max_pages=cols, n_pages=n_pages,
+                           page_size=page, max_new=n_q, device=DEV)
+    cache.page_table[:, :n_pages] = torch.arange(n_pages, device=DEV)
+    cache.seq_len.fill_(keys)
+    kc, vc, ks, vs = (x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x
+                      for x in cache.views(0))
+    kc.zero_(), vc.fill_(0x38), ks.fill_(1.0), vs.fill_(1.0)   # 0x38: 1.0
+    kc[at // page, 0, at % page, 0] = 0x38
+    vc[at // page, 0, at % page] = 0
+    q = torch.zeros((slots, 2, n_q, d), dtype=torch.bfloat16, device=DEV)
+    q[:, 0, :, 0] = nats * d ** 0.5
+    alpha, rho = torch.zeros((2, keys), device=DEV), torch.zeros((2, keys), device=DEV)
+    alpha[1, at] = nats
+    from dynamic_causal_attention_gb300 import _binding as B
+    B.saf_trace_enable(1)
+    out, lse = cache.attend(0, q, alpha, rho)
+    names = [B.saf_trace_get(i)[1] for i in range(B.saf_trace_count())]
+    B.saf_trace_enable(0)
+    assert kernel in names
+    n = keys - n_q + np.arange(n_q)                    # the other keys that row t sees
+    for h, x in ((0, float(q[0, 0, 0, 0]) / d ** 0.5), (1, nats)):
+        total = n + np.exp(x)
+        got = host(out[:, h].double())
+        rel = 2.0 ** -8 + 2.0 ** -18 + keys * 2.0 ** -27 + max(2.0 ** -11, 2.0 ** (-36 + nats / np.log(2)))
+        err = np.abs(got / (n / total)[None, :, None] - 1)
+        assert err.max() <= rel, (h, err.max(), rel)
+        err = np.abs(host(lse[:, h].double()) - np.log(total))
+        assert err.max() <= 2.0 ** -15 + keys * 2.0 ** -28, err.max()

@@ -681,9 +681,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<NT>)
       if (whole) {
         const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
         const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: 0
-        *reinterpret_cast<uint2*>(p.out + row * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2*>(p.out + row * D + d) = mean4(o, sum);
         if (d == 0 && p.lse) p.lse[row] = (mx + log2f(sum)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(p.acc + ((size_t)part * kMR + r) * D + d) = o;
@@ -743,9 +741,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (s || r >= n_rows) return;
   const int t = (r0 + r) / c.group, h = kv * c.group + r0 + r - t * c.group;
   const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
-  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-  *reinterpret_cast<uint2*>(p.out + row * D + d) =
-      make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+  *reinterpret_cast<uint2*>(p.out + row * D + d) = mean4(x.o, x.l);
   if (d == 0 && p.lse) p.lse[row] = (x.m + log2f(x.l)) * kLn2;
 }
 

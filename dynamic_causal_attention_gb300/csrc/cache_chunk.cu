@@ -811,7 +811,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if ((v[q] >> (8 * k) & 0x7f) == 0x7f) nan[q / 8] |= 1u << (q % 8 * 4 + k);
               }
             }
-            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // a row without weight: 0, even if a key that it sees holds NaN (a part's sum
+            // goes out as it is: another part may have weight)
+            const float inv = whole ? 1.f / l : 1.f;
+            const bool none = whole && l == 0.f;
             // partial sums: [D / 4][row][4], so that a warp's stores are contiguous
             const size_t part = (size_t)(2 * blockIdx.x + (first ? 0 : 1)) * kRows;
             const int pr = g * 128 + r;
@@ -834,7 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (whole && live) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 2)
-                  o[k / 2] = pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1]));
+                  o[k / 2] = none ? 0u
+                                  : pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1]));
                 st_global_words16(to + 32 * q, o, wide);
               } else if (live) {
 #pragma unroll
@@ -1202,9 +1206,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
       row_of(rows, unit.first + r, gk, ice, t, idx);
       const int h = p.order[p.cls_first[cls] + idx];
       const size_t row = ((size_t)b * c.H + h) * c.n_q + t;
-      const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-      *reinterpret_cast<uint2*>(p.a.out + row * D + d) =
-          make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+      *reinterpret_cast<uint2*>(p.a.out + row * D + d) = mean4(x.o, x.l);
       if (d == 0 && p.a.lse) p.a.lse[row] = (x.m + log2f(x.l)) * kLn2;
     }
     if (split > 1) __syncthreads();  // the threads' parts are read

@@ -211,6 +211,14 @@ __device__ __forceinline__ int page_at(const CacheCall& c, int b, int col) {
   return (unsigned)p < (unsigned)c.n_pages ? p : -1;
 }
 
+// 4 components of a row's mean as bf16: o over the sum l of its weights.  A row
+// without weight gets 0 even where a key that it sees holds NaN.
+__device__ __forceinline__ uint2 mean4(const float4& o, float l) {
+  if (l == 0.f) return make_uint2(0u, 0u);
+  const float inv = 1.f / l;
+  return make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
 // ------------------------------------------------------------ joining parts
 // A unit of attention that was cut leaves one part per CTA: for each row the
 // base m of its exponents (to base 2), l = sum of the weights relative to m,

@@ -94,3 +94,34 @@ def test_many_keys_far_below_the_largest(api, nats, keys, at, n_q, kernel, slots
         assert err.max() <= rel, (h, err.max(), rel)
         err = np.abs(host(lse[:, h].double()) - np.log(total))
         assert err.max() <= 2.0 ** -15 + keys * 2.0 ** -28, err.max()
+
+
+@pytest.mark.parametrize("n_q,kernel,lens", [(3, "cache_attn", [150, 40]), (70, "cache_chunk", [150, 75]),
+                                             (2, "cache_attn", [5003, 40]),
+                                             (70, "cache_chunk", [5003, 75])])
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16), (32, 64)])
+def test_rows_without_weight_that_see_nan(api, d, page, n_q, kernel, lens):
+    # out = 0 and lse = -inf where every weight is zero, whatever V holds; a row with weight
+    # takes the NaN as 0 * NaN does
+    c = Case(api, mask_of(6, (0, 1, 2, 3, 4)), 3, d, page, lens, n_q, T_pat=max(lens), seed=d,
+             kernel=kernel)
+    c.alpha[0] = -np.inf
+    c.rho[1] = -np.inf
+    c.alpha[2, :30] = -np.inf
+    for s, j in [(0, 3), (0, lens[0] // 2), (0, lens[0] - 1), (1, 20), (1, lens[1] - 2)]:
+        c.v_codes[c.table[s, j // page], :, j % page, 5] = 0x7F
+    c.put()
+    out, lse = c.run()
+    assert bool((out[:, :2] == 0).all()) and bool((lse[:, :2] == -np.inf).all())
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("n_q,kernel", KERNELS)
+def test_patterns_shorter_than_the_distance_and_nan(api, n_q, kernel):
+    # keys behind the vectors' end weigh nothing: rows that see only such keys are empty
+    c = Case(api, mask_of(4, (0, 1, 2, 3)), 2, 64, 16, [260, 75], n_q, T_pat=2, seed=1, kernel=kernel)
+    c.alpha[:2, :] = -np.inf
+    c.v_codes[c.table[0, 1], :, 3, 7] = 0xFF
+    c.v_codes[c.table[0, 15], :, 9, 7] = 0xFF
+    c.put()
+    c.check(*c.run())

@@ -22,25 +22,33 @@
 //   warp 13          looks up pages, fetches K and V codes by TMA (a page that is
 //                    missing reads as zeros) and writes the scales of each tile.
 //
-// K needs no conversion: Q K^T runs on e4m3 operands at twice f16's rate, with
-// the row of q split into two e4m3 parts, q = hi + lo.  The row is scaled by a
-// power of two into e4m3's range; hi is q rounded to 4 bits, and what is left
-// of a bf16 value (8 bits) has at most 4: the sum is exact for components down
-// to 2^-10 of the row's largest, and below them it is off by at most 2^-18 of
-// the largest.  V is turned into f16 (exact): splitting the 256 x 128 weights
-// of a tile in its place would take six times the arithmetic of converting V's
-// 128 x d_h codes.
+// K needs no conversion: Q K^T runs on 8-bit operands at twice f16's rate, K as e4m3
+// and the row of q as a sum of parts, each the rounded rest of the ones before.  Two
+// do for most rows: scaled by a power of two to a largest component of 224 to 448,
+// the first is e4m3 and leaves at most 4 of a bf16 value's 8 bits (and no more than 8
+// units of its last place), the second e5m2, whose 3 bits hold that.  This is exact for
+// components down to 2^-6, where e4m3 becomes subnormal: 2^-14 of the row's largest;
+// below, they are off by at most 2^-14, 2^-21 of it.  A row tile with an infinity, or
+// with a row of more than two such components, takes three e5m2 parts of rows scaled to
+// a largest component of 2^14 to 2^15.8: they leave 5, 2 and no bits, exact down to
+// 2^-24 of the largest, below off by 2^-31 of it.  (Of 128 normal components, 0.013 lie
+// below 2^-6: in a call of 256 row tiles more than two of one row hardly ever do.  The
+// call below takes 263 us, 302 if all have three parts.  Two e4m3 parts are exact down
+// to 2^-10: beside a component 1000 times the others they left logits off by 2^-7.)  V
+// is turned into f16 (exact): splitting the 256 x 128 weights of a tile in its place
+// would take six times the arithmetic of converting V's 128 x d_h codes.
 //
 // TMEM: S of the two row tiles (128 columns each), then their O.  A tile's
 // keys are taken in two halves of 64: S, softmax and P V of one half run while
 // the other half's do, and P, as packed f16, overwrites the first columns of
 // its own half of S, so the next S of a half waits only for the product that
 // reads that half's P.  What a tile of keys costs is the chain S, softmax, P V
-// and its hand-offs, about 4200 cycles for 256 rows at d_h = 128, against some
+// and its hand-offs, about 4300 cycles for 256 rows at d_h = 128, against some
 // 1800 of the tensor cores' time; 2 x 2000 rows of 16 heads against 8192 keys take
-// 254 us, 50% of the measured burst rate of products, and with 4 frozen heads,
-// whose weights are 32 loads of two from the window for each half a tile, 260 us
-// (43%; 64 loads of one: 262, and with all heads frozen 282 for 272).
+// 263 us, 48% of the measured burst rate of products, and with 4 frozen heads,
+// whose weights are 32 loads of two from the window for each half a tile, 268 us
+// (41%; with all heads frozen 285, of which 8 for the single stage of V's codes that
+// Q's third part leaves room for).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <float.h>
@@ -79,40 +87,63 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
 // A chain of products into one accumulator from one statement: k-step after
 // k-step with the descriptors advanced by adds.  One issuing thread then gets a
 // product through in about 75 cycles in place of about 160.
-template <int N, int STEP>  // S += hi K^T, then lo K^T: N steps of 32 codes each
-__device__ __forceinline__ void issue_codes(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc,
-                                            uint32_t lead) {
-  static_assert(N == 1 || N == 2 || N == 4, "");
-#define SAF_MMA8 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, "
-#define SAF_NEXT \
-  "add.u32 p, p, 2;\n\tadd.u32 q, q, 2;\n\tmov.b64 a, {p, u};\n\tmov.b64 b, {q, v};\n\t"
-#define SAF_HEAD                                                                              \
-  "{\n\t.reg .pred f, t, e;\n\t.reg .b64 a, b;\n\t.reg .b32 p, q, u, v;\n\t"           \
-  "setp.ne.b32 t, 0, 0;\n\tmov.pred f, t;\n\tnot.pred t, f;\n\tsetp.ne.b32 e, %5, 0;\n\t"  \
-  "mov.b64 a, %1;\n\tmov.b64 b, %2;\n\tmov.b64 {p, u}, a;\n\tmov.b64 {q, v}, b;\n\t"
-#define SAF_LOW                                                                     \
+#define SAF_HEAD                                                                \
+  "{\n\t.reg .pred f, t, e;\n\t.reg .b64 a, b;\n\t.reg .b32 p, q, u, v;\n\t"  \
+  "setp.ne.b32 t, 0, 0;\n\tmov.pred f, t;\n\tnot.pred t, f;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+#define SAF_PART(AT)                                                                   \
   "mov.b64 a, %1;\n\tmov.b64 b, %2;\n\tmov.b64 {p, u}, a;\n\tmov.b64 {q, v}, b;\n\t" \
-  "add.u32 p, p, %4;\n\tmov.b64 a, {p, u};\n\t"
+  "add.u32 p, p, " AT ";\n\tmov.b64 a, {p, u};\n\t"
+#define SAF_MMA8(IDESC, ACC) \
+  "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, " IDESC ", " ACC ";\n\t"
+#define SAF_MORE(IDESC)                                                                         \
+  "add.u32 p, p, 2;\n\tadd.u32 q, q, 2;\n\tmov.b64 a, {p, u};\n\tmov.b64 b, {q, v};\n\t" SAF_MMA8( \
+      IDESC, "t")
+#define SAF_REST1(IDESC) ""
+#define SAF_REST2(IDESC) SAF_MORE(IDESC)
+#define SAF_REST4(IDESC) SAF_MORE(IDESC) SAF_MORE(IDESC) SAF_MORE(IDESC)
+
+// S = q0 K^T + q1 K^T: N steps of 32 codes each, the parts STEP apart
+template <int N, int STEP>
+__device__ __forceinline__ void issue_codes(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc0,
+                                            uint32_t idesc1, uint32_t lead) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+#define SAF_PARTS(REST) \
+  SAF_HEAD SAF_PART("0") SAF_MMA8("%3", "f") REST("%3") SAF_PART("%4") SAF_MMA8("%6", "t") REST("%6") "}"
+#define SAF_ARGS \
+  ::"r"(d), "l"(q), "l"(k), "r"(idesc0), "n"(STEP), "r"(lead), "r"(idesc1) : "memory"
   if constexpr (N == 1)
-    asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_LOW SAF_MMA8 "t;\n\t}" ::"r"(d), "l"(q), "l"(k),
-                 "r"(idesc), "n"(STEP), "r"(lead)
-                 : "memory");
+    asm volatile(SAF_PARTS(SAF_REST1) SAF_ARGS);
   else if constexpr (N == 2)
-    asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_LOW SAF_MMA8
-                 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t}" ::"r"(d),
-                 "l"(q), "l"(k), "r"(idesc), "n"(STEP), "r"(lead)
-                 : "memory");
+    asm volatile(SAF_PARTS(SAF_REST2) SAF_ARGS);
   else
-    asm volatile(SAF_HEAD SAF_MMA8 "f;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8
-                 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_LOW SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8
-                 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t" SAF_NEXT SAF_MMA8 "t;\n\t}" ::"r"(d),
-                 "l"(q), "l"(k), "r"(idesc), "n"(STEP), "r"(lead)
-                 : "memory");
-#undef SAF_MMA8
-#undef SAF_NEXT
-#undef SAF_HEAD
-#undef SAF_LOW
+    asm volatile(SAF_PARTS(SAF_REST4) SAF_ARGS);
+#undef SAF_PARTS
+#undef SAF_ARGS
 }
+// S += q2 K^T, for rows of Q that need a third part.  A call, so that what follows the
+// first two lies right behind them: issued under a predicate in their chain the third
+// costs 8% where it is not needed.
+template <int N, int STEP>
+__device__ __noinline__ void issue_third(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc,
+                                         uint32_t lead) {
+#define SAF_PARTS(REST) SAF_HEAD SAF_PART("%4") SAF_MMA8("%3", "t") REST("%3") "}"
+#define SAF_ARGS ::"r"(d), "l"(q), "l"(k), "r"(idesc), "n"(2 * STEP), "r"(lead) : "memory"
+  if constexpr (N == 1)
+    asm volatile(SAF_PARTS(SAF_REST1) SAF_ARGS);
+  else if constexpr (N == 2)
+    asm volatile(SAF_PARTS(SAF_REST2) SAF_ARGS);
+  else
+    asm volatile(SAF_PARTS(SAF_REST4) SAF_ARGS);
+#undef SAF_PARTS
+#undef SAF_ARGS
+}
+#undef SAF_HEAD
+#undef SAF_PART
+#undef SAF_MMA8
+#undef SAF_MORE
+#undef SAF_REST1
+#undef SAF_REST2
+#undef SAF_REST4
 // O (+)= P V for 64 keys: 4 steps of 16, P in TMEM (8 columns a step), V's
 // descriptor advanced by STEP.
 template <int STEP>
@@ -131,9 +162,9 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uin
 #undef SAF_NEXT
 }
 
-// ... with e4m3 operands (K-major both).
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// ... with e4m3 or e5m2 A and e4m3 B (K-major both).
+__host__ __device__ constexpr uint32_t idesc_codes(int M, int N, uint32_t e5m2) {
+  return (1u << 4) | (e5m2 << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // The rows of a class fall into units of up to 256; a frozen head shares none.
@@ -202,14 +233,14 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // full): the tiles of keys, and behind them the unit's own cost: Q, the first tile
 // without company, the results.  Measured with equal units, microseconds:
 //                          d_h = 128     64      32
-//   tile, dynamic             2.22      1.78    1.56     (one row tile 1.99 1.66 1.38)
-//   tile, frozen              2.28      2.35    2.18     (one row tile 2.15 1.88 1.58)
+//   tile, dynamic             2.26      1.80    1.57     (one row tile 2.02 1.63 1.47)
+//   tile, frozen              2.33      2.31    2.14     (one row tile 2.13 1.73 1.58)
 //   unit, dynamic, frozen     11, 8.7   6.3, 4.4   4.5, 3.3
 // With tiles alone counted, 2 x 2000 rows of 16 heads, 4 of them frozen, against
-// 8192 keys took 287 us for 273 (the average SM was idle for a tenth of them), 12 x
-// 76 rows of 128 heads against 388 keys 63 for 47.  (At d_h = 128 the frozen tile
-// counts 9 and units a little less than alone: 258 us in that call, with 8, 38 and
-// 31 267.)
+// 8192 keys took 5% longer (the average SM was idle for a tenth of them), 12 x 76
+// rows of 128 heads against 388 keys 34%.  (At d_h = 128 the frozen tile counts 9
+// and units a little less than alone: 268 us in that call, with 8 for both kinds of
+// tile 281.)
 struct Costs {
   int tile[2][2];  // [frozen][both row tiles]
   int unit[2];     // [frozen]
@@ -372,11 +403,16 @@ __device__ Share find_share(const CacheChunk& p, long long* scan /* [warps + 2] 
 template <int D>
 struct Smem {
   static constexpr int CODES = kTile * D;     // e4m3
-  static constexpr int TILE = 2 * CODES;      // f16, or Q's two parts
-  static constexpr int KST = 3, RST = 2;      // stages of K codes and of V codes
+  static constexpr int TILE = 2 * CODES;      // f16
+  static constexpr int QTILE = 3 * CODES;     // Q's three parts
+  // stages of K codes and of V codes.  V's is free again as soon as its codes lie in
+  // registers (two stages are no faster); tile n's scales and pattern, written behind
+  // that, then find those of tile n - 4 read: the codes of n - 1 are read when n - 2
+  // has been converted, which waits for the products of n - 4
+  static constexpr int KST = D == 128 ? 2 : 3, RST = 1;
   static constexpr int OFF_Q = 0;             // two row tiles
-  static constexpr int OFF_V = 2 * TILE;      // two stages of f16 V
-  static constexpr int OFF_K = 4 * TILE;
+  static constexpr int OFF_V = 2 * QTILE;     // two stages of f16 V
+  static constexpr int OFF_K = OFF_V + 2 * TILE;
   static constexpr int OFF_R = OFF_K + KST * CODES;
   static constexpr int OFF_META = OFF_R + RST * CODES;  // 4 tiles x 8 groups of 16 keys x 16 bytes
   // frozen rows: 128 alphas and the 384 rhos of a tile, times log2(e), and the rhos
@@ -451,6 +487,114 @@ __device__ __forceinline__ void fetch_q(const CacheChunk& p, const Walk<D>& w, c
   cp_async_commit();
 }
 
+// Whether `x` holds in one of the 128 threads that share named barrier `id`.
+__device__ __forceinline__ bool any_of_128(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// The threads of row tile g turn its rows of Q into codes, where they lie, row r each:
+// two parts or, if a row asks for it, three (see the top).  Returns the factor of the
+// row's logits.  The arithmetic is in f16, which loses nothing here: a part is the
+// rounded rest of the ones before, and what f16 rounds off (2^-25) is far below the
+// least step of e5m2 (2^-16).
+template <int D>
+__device__ __noinline__ float q_codes(uint32_t stage, uint32_t r, int g, int* three_parts) {
+  constexpr int kCodes = Smem<D>::CODES;
+  auto load = [&](int u, uint32_t(&y)[8]) {
+    lds_words(*reinterpret_cast<uint32_t(*)[4]>(y), stage + code_at<D>(r, u));
+    lds_words(*reinterpret_cast<uint32_t(*)[4]>(y + 4), stage + kCodes + code_at<D>(r, u));
+  };
+  __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
+#pragma unroll 2
+  for (int u = 0; u < D / 16; ++u) {
+    uint32_t y[8];
+    load(u, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[k])));
+  }
+  const float amax = fmaxf(__low2float(top2), __high2float(top2));
+  const bool inf = amax == CUDART_INF_F;  // e4m3 has none
+  const int bits = __float_as_int(amax);
+  // amax 2^-e in (224, 448]
+  int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  // components that e4m3 holds as a subnormal number: the first part keeps less of
+  // them than 4 bits, and the second may round the rest
+  int small = 0;
+  const __nv_bfloat162 limit = __float2bfloat162_rn(pow2f(max(-126, min(120, e) - 6)));
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll 2
+  for (int u = 0; u < D / 16; ++u) {
+    uint32_t y[8];
+    load(u, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const __nv_bfloat162 x = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[k]));
+      small += __popc(__hlt2_mask(x, limit) & __hgt2_mask(x, zero));
+    }
+  }
+  const bool three = any_of_128(1 + g, inf || small > 2 * 16);  // 16 bits for each
+  if (r == 0) *three_parts = three;
+  e = amax > 0.f ? max(-126, three ? min(113, e - 7) : min(120, e)) : 0;
+  const float down = pow2f(-e);
+  auto convert = [&](auto kind) {
+    constexpr int kParts = decltype(kind)::value ? 3 : 2;
+#pragma unroll 2
+    for (int u = 0; u < D / 16; ++u) {
+      uint32_t y[8], parts[kParts][4];
+      load(u, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t codes[kParts][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t v = y[2 * k + j];
+          uint32_t rest = pack_f16x2(__uint_as_float(v << 16) * down,
+                                     __uint_as_float(v & 0xffff0000u) * down);
+#pragma unroll
+          for (int n = 0; n < kParts; ++n) {
+            const bool e4m3 = kParts == 2 && n == 0;
+            uint32_t code = e4m3 ? f16x2_e4m3x2(rest) : f16x2_e5m2x2(rest);
+            const uint32_t f = e4m3 ? e4m3x2_f16x2((uint16_t)code) : e5m2x2_f16x2(code);
+            const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&rest),
+                                      *reinterpret_cast<const __half2*>(&f));
+            rest = *reinterpret_cast<const uint32_t*>(&x);
+            if (kParts == 3 && n == 0 && inf) {  // saturated infinities: their code, no rest
+              if ((rest & 0x7fffu) == 0x7c00u) {
+                code = (code & 0xff00u) | (rest >> 8 & 0xffu);
+                rest &= 0xffff0000u;
+              }
+              if ((rest & 0x7fff0000u) == 0x7c000000u) {
+                code = (code & 0xffu) | (rest >> 16 & 0xff00u);
+                rest &= 0xffffu;
+              }
+            }
+            codes[n][j] = code;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) parts[n][k] = codes[n][0] | codes[n][1] << 16;
+      }
+#pragma unroll
+      for (int n = 0; n < kParts; ++n)
+        st_shared_v4(stage + n * kCodes + code_at<D>(r, u), parts[n][0], parts[n][1],
+                     parts[n][2], parts[n][3]);
+    }
+  };
+  if (three)
+    convert(Const<true>());
+  else
+    convert(Const<false>());
+  return pow2f(e) * (rsqrtf((float)D) * kLog2e);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -467,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_full = q_full + 2;          // [KST] codes of K have landed
   uint64_t* k_empty = k_full + L::KST;    // [KST] their products done
   uint64_t* r_full = k_empty + L::KST;    // [RST] codes of V have landed
-  uint64_t* r_empty = r_full + L::RST;    // [RST] converted (128 arrivals)
+  uint64_t* r_empty = r_full + L::RST;    // [RST] in registers (128 arrivals)
   uint64_t* v_full = r_empty + L::RST;    // [2] f16 V written (128)
   uint64_t* v_empty = v_full + 2;         // [2] its products done
   uint64_t* m_full = v_empty + 2;         // [4] a tile's scales and pattern (32)
@@ -484,6 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drained = begun + 2;           // [2] every product of an issuer done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  // of row tile g: whether its rows of Q are in three parts
+  int* three_parts = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);  // [2]
   // of row tile g: the last of its units (counted from 1, at 4 g + count % 4) whose
   // V holds NaN at an edge
   int* nan_seg = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [8]
@@ -576,60 +722,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool warp_live = g * 128 + (warp & 3) * 32 < unit.n;
           float fac = 1.f;
           if (!ice) {
-            // The row of Q, scaled by the least 2^-e that brings it within e4m3's
-            // range and split into hi + lo: each thread turns its row into codes
-            // where it lies.  In f16, which loses nothing here: hi is at most 4 bits
-            // of the value's 8, and what f16 rounds off (2^-25) is far below e4m3's
-            // least step (2^-9).
-            const uint32_t stage = sQ + g * L::TILE;
+            const uint32_t stage = sQ + g * L::QTILE;
             if (!staged) fetch_q<D>(p, w, unit, g, (warp & 3) * 32, stage);
             staged = false;
             cp_async_wait<0>();
             __syncwarp();
-            __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
-#pragma unroll 2
-            for (int u = 0; u < D / 16; ++u) {
-              uint32_t y[8];
-              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y), stage + code_at<D>(r, u));
-              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y + 4),
-                        stage + L::CODES + code_at<D>(r, u));
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[k])));
-            }
-            const float amax = fmaxf(__low2float(top2), __high2float(top2));
-            const int bits = __float_as_int(amax);
-            int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
-            e = amax > 0.f ? max(-126, min(120, e)) : 0;
-            // e4m3 has no infinity: the row becomes NaN, as its softmax would
-            const float down = amax == CUDART_INF_F ? CUDART_NAN_F : pow2f(-e);
-            fac = pow2f(e) * (rsqrtf((float)D) * kLog2e);
-#pragma unroll 2
-            for (int u = 0; u < D / 16; ++u) {
-              uint32_t y[8], hi[4], lo[4];
-              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y), stage + code_at<D>(r, u));
-              lds_words(*reinterpret_cast<uint32_t(*)[4]>(y + 4),
-                        stage + L::CODES + code_at<D>(r, u));
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t c2[2], d2[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const uint32_t v = y[2 * k + j];
-                  const uint32_t z = pack_f16x2(__uint_as_float(v << 16) * down,
-                                                __uint_as_float(v & 0xffff0000u) * down);
-                  c2[j] = f16x2_e4m3x2(z);
-                  const uint32_t f = e4m3x2_f16x2((uint16_t)c2[j]);
-                  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&z),
-                                               *reinterpret_cast<const __half2*>(&f));
-                  d2[j] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
-                }
-                hi[k] = c2[0] | c2[1] << 16;
-                lo[k] = d2[0] | d2[1] << 16;
-              }
-              st_shared_v4(stage + code_at<D>(r, u), hi[0], hi[1], hi[2], hi[3]);
-              st_shared_v4(stage + L::CODES + code_at<D>(r, u), lo[0], lo[1], lo[2], lo[3]);
-            }
+            fac = q_codes<D>(stage, r, g, three_parts + g);
             fence_proxy_async_smem();
             mbar_arrive(q_full + g);
           }
@@ -780,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.next();
             const UnitRows u0 = unit_rows(x.rows, x.pair, x.gk(), x.ice());
             staged = !x.ice() && g * 128 < u0.n;
-            if (staged) fetch_q<D>(p, x, u0, g, (warp & 3) * 32, sQ + g * L::TILE);
+            if (staged) fetch_q<D>(p, x, u0, g, (warp & 3) * 32, sQ + g * L::QTILE);
           }
           // ---- results
           mbar_wait(o_done + 2 * g, (n_p - 1) & 1, wc, kSiteO);
@@ -899,6 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 y = lds_f32x4(sR + rs * L::CODES + code_at<D>(row0 + n * kStep, ch));
             x[n] = *reinterpret_cast<const uint4*>(&y);
           }
+          mbar_arrive(r_empty + rs);
           mbar_wait(v_empty + st, ((vc >> 1) & 1) ^ 1, wc, kSiteVFree);
           const bool clean = (i + 1) * kTile > sure;
           bool bad = false;
@@ -927,7 +1026,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           mbar_arrive(v_full + st);
-          mbar_arrive(r_empty + rs);
           ++vc;
         }
         at += w.cost();
@@ -949,22 +1047,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto arrive = [&](uint64_t* bar) {
           if (lead) mbar_arrive(bar);
         };
-        constexpr uint32_t id_s = idesc_e4m3(128, 64);
         constexpr uint32_t id_o = idesc_f16(128, D, false, true);
         auto poll = [&](uint64_t* bar, uint32_t parity, const WaitCtl& c, int site) {
           poll_bar(bar, parity, c, site);
           __syncwarp();
         };
         const uint32_t s_col = tmem + kS + g * 128, o_col = tmem + kO + g * 128;
-        const uint64_t qt = sdesc(sQ + g * L::TILE, 16, 8 * D, swizzle_layout_code(D));
+        const uint64_t qt = sdesc(sQ + g * L::QTILE, 16, 8 * D, swizzle_layout_code(D));
         uint32_t kc = 0, vc = 0, n_q = 0, n_p = 0;
+        uint32_t id_s = 0;  // of the first part of the unit's rows of Q
         tile = __shfl_sync(~0u, tile, 0);
         for (;;) {
           const int tile_end = __shfl_sync(~0u, w.tiles_before(sh.end - at), 0);
           const bool ice = __shfl_sync(~0u, (int)w.ice(), 0);
           const bool mine = __shfl_sync(~0u, unit_rows(w.rows, w.pair, w.gk(), ice).n, 0) > g * 128;
-          // K of tile i + 1 and V of tile i are waited for while a product of the
-          // tile before runs, so that the waits are not part of the row tile's chain
+          // K and V of tile i + 1 are waited for while a product of tile i runs, so
+          // that the waits are not part of the row tile's chain
           auto wait_k = [&](uint32_t n) {
             poll(k_full + n % L::KST, (n / L::KST) & 1, wc, kSiteK);
           };
@@ -973,7 +1071,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto issue_s = [&](int hf) {
             const uint64_t kt = sdesc(sK + kc % L::KST * L::CODES + hf * 64 * D, 16, 8 * D,
                                       swizzle_layout_code(D));
-            issue_codes<D / 32, (L::CODES >> 4)>(s_col + 64 * hf, qt, kt, id_s, lead);
+            constexpr uint32_t id1 = idesc_codes(128, 64, 1);
+            issue_codes<D / 32, (L::CODES >> 4)>(s_col + 64 * hf, qt, kt, id_s, id1, lead);
+            if (id_s == id1) issue_third<D / 32, (L::CODES >> 4)>(s_col + 64 * hf, qt, kt, id1, lead);
             commit(s_full + 2 * g + hf);
           };
           auto k_done = [&]() {
@@ -988,6 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_k(kc);
             if (mine) {
               poll(q_full + g, n_q++ & 1, wc, kSiteQ);
+              id_s = idesc_codes(128, 64, __shfl_sync(~0u, *(volatile int*)(three_parts + g), 0));
               tc_fence_after();
               issue_s(0);
               issue_s(1);
@@ -995,7 +1096,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             k_done();
           }
           wait_v(vc);
-          if (!ice && tile + 1 < tile_end) wait_k(kc);
           for (int i = tile; i < tile_end; ++i) {
             const bool next = i + 1 < tile_end, more = !ice && next;
             const uint32_t st = vc++ & 1;
@@ -1015,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   commit(v_empty + st);
                 else if (next) {
                   wait_v(vc);
-                  if (!ice && i + 2 < tile_end) wait_k(kc + 1);
+                  if (!ice) wait_k(kc);
                 }
                 // S takes the columns of the P that these products read
                 if (more) {
@@ -1028,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               arrive(v_empty + st);
               if (next) wait_v(vc);
-              if (!ice && i + 2 < tile_end) wait_k(kc + 1);
+              if (more) wait_k(kc);
             }
             if (more) k_done();
           }

@@ -85,11 +85,20 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
-// e4m3 of two f16 values, saturating; the NaN code for NaN
+// e4m3 and e5m2 of two f16 values, saturating; the NaN code for NaN
 __device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t v) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
   return r;
+}
+__device__ __forceinline__ uint32_t f16x2_e5m2x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+// Two e5m2 codes as packed f16 (e5m2 is f16's upper byte).
+__device__ __forceinline__ uint32_t e5m2x2_f16x2(uint32_t v) {
+  return __byte_perm(v, 0, 0x1404);
 }
 
 // Two e4m3 codes (low and high byte of v) as packed f16: exact (f16 holds

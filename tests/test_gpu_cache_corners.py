@@ -125,3 +125,33 @@ def test_patterns_shorter_than_the_distance_and_nan(api, n_q, kernel):
     c.v_codes[c.table[0, 15], :, 9, 7] = 0xFF
     c.put()
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("n_q,kernel", KERNELS)
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("times", [30.0, 300.0, 1000.0, 30000.0])
+def test_queries_with_an_outlying_channel(api, d, times, n_q, kernel):
+    # a channel of q far above the others, whose K is small: the others make the logits
+    c = Case(api, mask_of(4, ()), 2, d, 16, [200, n_q + 60], n_q, seed=d, kernel=kernel)
+    with np.errstate(invalid="ignore"):
+        small = ref.encode(ref.E4M3[c.k_codes[..., 3]] / times)
+    c.k_codes[..., 3] = np.where((c.k_codes[..., 3] & 0x7F) == 0x7F, c.k_codes[..., 3], small)
+    c.q[..., 3] *= times
+    c.put()
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("n_q,kernel", KERNELS)
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_queries_of_every_size(api, d, n_q, kernel):
+    # components 2^-16 to 2^0 of the largest, each with 8 bits, against K of the inverse sizes
+    # as far as a code reaches
+    c = Case(api, mask_of(4, ()), 4, d, 32, [150, n_q + 7], n_q, seed=d, kernel=kernel)
+    rng = np.random.default_rng(d)
+    e = rng.integers(0, 17, d)
+    q = rng.uniform(0.5, 1.0, c.q.shape) * rng.choice([-1.0, 1.0], c.q.shape) * 2.0 ** -e
+    c.q = torch.tensor(q, dtype=torch.bfloat16, device=DEV)
+    k = rng.uniform(0.5, 1.0, c.k_codes.shape) * rng.choice([-1.0, 1.0], c.k_codes.shape) * 2.0 ** (e - 8.0)
+    c.k_codes, c.k_scales = ref.encode(k), np.ones_like(c.k_scales)
+    c.put()
+    c.check(*c.run())

@@ -487,6 +487,14 @@ __device__ __forceinline__ void fetch_q(const CacheChunk& p, const Walk<D>& w, c
   cp_async_commit();
 }
 
+// The lowest n bits (none for n < 1, all from 32 on), and 16 for each of 2 bits.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n < 1 ? 0u : ~0u >> (n < 32 ? 32 - n : 0);
+}
+__device__ __forceinline__ uint32_t spread16(uint32_t x) {
+  return (x & 1 ? 0xffffu : 0u) | (x & 2 ? 0xffff0000u : 0u);
+}
+
 // Whether `x` holds in one of the 128 threads that share named barrier `id`.
 __device__ __forceinline__ bool any_of_128(int id, bool x) {
   uint32_t r;
@@ -754,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t col = s_col + 64 * hf;
                   const int j0 = i * kTile + 64 * hf;
                   const int lim = lim_all - j0;  // columns below it are seen
-                  const bool edge = __any_sync(~0u, lim < 64);
+                  const uint32_t holes = lds_word(meta + 12) >> 4 * hf & 15u;
+                  const bool edge = __any_sync(~0u, lim < 64 || holes);
                   // a row of S: 4 groups of 16 keys, each of one page with one scale
                   uint32_t s[4][16];
                   float gm[4];
@@ -785,9 +794,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                   }
                   if (edge) {
+                    // behind the row, or without a page: such a key weighs nothing, whatever
+                    // a q or a pattern that is not finite makes of the zeros read for it
+                    const uint32_t seen[2] = {low_bits(lim) & ~spread16(holes),
+                                              low_bits(lim - 32) & ~spread16(holes >> 2)};
 #pragma unroll
                     for (int k = 0; k < 64; ++k)
-                      if (k >= lim) s[k / 16][k % 16] = 0xff800000u;
+                      if (!(seen[k / 32] >> (k % 32) & 1)) s[k / 16][k % 16] = 0xff800000u;
                   }
                   if (edge || kIce) {
 #pragma unroll
@@ -1207,12 +1220,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t st = vc % L::RST;
             mbar_wait(r_empty + st, ((vc / L::RST) & 1) ^ 1, wc, kSiteRawFree);
+            const uint32_t holes = __ballot_sync(~0u, page < 0);
             if (lane < 8) {
               // a group without a page: every logit -inf
               const bool there = page >= 0;
               *reinterpret_cast<float4*>(smem + L::OFF_META + (vc & 3) * 128 + lane * 16) =
                   make_float4(sc.x, there ? __log2f(sc.y) : -CUDART_INF_F,
-                              there ? __fdividef(1.f, sc.y) : 1.f, 0.f);
+                              there ? __fdividef(1.f, sc.y) : 1.f, __uint_as_float(holes & 255u));
             }
             if (w.ice()) {
               float* to = reinterpret_cast<float*>(smem + L::OFF_PAT + (vc & 3) * L::PAT) + lane;

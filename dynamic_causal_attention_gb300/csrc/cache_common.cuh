@@ -85,6 +85,12 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
 
+__device__ __forceinline__ uint32_t lds_word(uint32_t a) {
+  uint32_t w[1];
+  lds_words(w, a);
+  return w[0];
+}
+
 // e4m3 and e5m2 of two f16 values, saturating; the NaN code for NaN
 __device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t v) {
   uint16_t r;

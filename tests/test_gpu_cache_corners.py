@@ -155,3 +155,55 @@ def test_queries_of_every_size(api, d, n_q, kernel):
     c.k_codes, c.k_scales = ref.encode(k), np.ones_like(c.k_scales)
     c.put()
     c.check(*c.run())
+
+
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")  # (the reference's sums of infinities)
+@pytest.mark.parametrize("n_q,kernel", [(3, "cache_attn"), (70, "cache_chunk"), (300, "cache_chunk")])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_queries_that_are_not_finite(api, d, n_q, kernel):
+    # NaN reaches the rows that see a key, and only those; of an infinite component against K of
+    # one sign the logits are all -inf (no weight) or +inf (NaN)
+    lens = [n_q + 90, n_q + 90, n_q + 90, n_q, n_q + 90]
+    holes = [(0, j) for j in range(40)] + [(1, 1), (1, 2), (2, 0), (2, 3)]
+    holes = [(s, j) for s, j in holes if j < -(-lens[s] // 16)]
+    c = Case(api, mask_of(4, (3,)), 2, d, 16, lens, n_q, holes=holes, seed=d, kernel=kernel)
+    rng = np.random.default_rng(d)
+    fin = (c.k_codes[..., 2] & 0x7F) != 0x7F
+    down = ref.encode(-rng.uniform(1.0, 100.0, c.k_codes.shape[:-1]))
+    c.k_codes[..., 2] = np.where(fin, down, c.k_codes[..., 2])
+    c.put()
+    c.q[0] = float("nan")                        # a slot without a page
+    c.q[1, :, 0, 1] = float("nan")
+    c.q[1, 0, n_q - 1] = float("nan")
+    c.q[2, :, 1, 2] = float("inf")
+    c.q[2, 1, n_q - 1, 2] = float("-inf")
+    c.q[3, 0, 0, 2] = float("inf")
+    c.q[3, 1, n_q // 2, 2] = float("inf")
+    c.q[4] = 3.38e38                             # bf16's largest are finite
+    c.q[4, :, :, 1::2] = 0.0
+    c.q[4, :, :, 2] = 0.0
+    c.k_codes[:] = np.where(((c.k_codes & 0x7F) != 0x7F) & (np.arange(d) % 2 == 0) & (np.arange(d) != 2),
+                            0, c.k_codes)        # ... against K of zeros
+    c.put()
+    out, lse = c.run()
+    assert bool((out[0, :3] == 0).all()) and bool((lse[0, :3] == -np.inf).all())
+    assert bool((out[2, :3, 1] == 0).all()) and bool((lse[2, :3, 1] == -np.inf).all())
+    assert bool(torch.isnan(out[2, 1, n_q - 1].float()).all())
+    c.check(out, lse)
+
+
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")
+@pytest.mark.parametrize("n_q,kernel", KERNELS)
+@pytest.mark.parametrize("d", [32, 128])
+def test_patterns_that_are_not_finite(api, d, n_q, kernel):
+    # an alpha of NaN or +inf reaches the rows that see its key, not those that have a hole there
+    # or stand before it
+    holes = [(0, 1), (0, 2), (1, 2)]
+    c = Case(api, mask_of(4, (0, 2, 3)), 2, d, 16, [n_q + 90, n_q + 60, n_q + 2], n_q, holes=holes,
+             seed=d, kernel=kernel)
+    c.alpha[0, 16:48] = np.nan
+    c.alpha[2, 33] = np.inf
+    c.alpha[3, n_q + 50] = np.nan
+    out, lse = c.run()
+    assert not bool(torch.isnan(out[0, 0].float()).any()) and bool(torch.isnan(out[1, 0].float()).all())
+    c.check(out, lse)

@@ -322,7 +322,8 @@ class PagedCache:
     # ---- pages
     def grow(self, n_new, into=None):
         """Room for n_new[s] more tokens in every slot (copying a last page that is shared);
-        seq_len advances.  Returns (granted [n_seqs], n_short [1]): what each slot got, all zero
+        seq_len advances.  To take tokens back lower seq_len: the row keeps its pages, and grow
+        uses them again where no other row holds them.  Returns (granted [n_seqs], n_short [1]): what each slot got, all zero
         when n_short pages are missing.  ``into``: (page_table, seq_len, ref) to write instead of
         the cache's own."""
         to = self._at if into is None else self._table_like(into, "grow: into")

@@ -52,8 +52,8 @@ __device__ long long block_scan(long long x, long long* warp_sums /* [33] */, lo
 // Scratch of one call: a header, a record for each slot, two page lists and a
 // page map.
 struct Scratch {
-  int* head;     // [16] total, copies, used
-  int4* slots;   // [n_seqs] first column, columns, first of its pages in the list, -
+  int* head;     // [16] grow: goes through, copies, pages taken; compact: -, copies, used
+  int4* slots;   // [n_seqs] first column, columns, first of its pages in the list, copy or -1
   int* from;     // [max(n_seqs, n_pages)] pages to copy
   int* to;       // [max(n_seqs, n_pages)]
   int* list;     // [n_pages] grow: free pages; compact: new place of a page
@@ -223,6 +223,23 @@ __device__ __forceinline__ Need slot_need(const CachePages& p, int s) {
   }
   return d;
 }
+// A row may hold pages behind its length: tokens were taken back.  New columns, from
+// the first on, that hold a page which no other row holds need none; returns their
+// number.  To be asked before the counts change.
+__device__ __forceinline__ int held_columns(const CachePages& p, int s, const Need& d) {
+  const int32_t* row = p.table + (size_t)s * p.max_pages + d.begin;
+  for (int c = 0; c < d.columns; c += 4) {  // four loads in flight
+    int t[4], r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = c + k < d.columns ? row[c + k] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = (unsigned)t[k] < (unsigned)p.n_pages ? p.ref[t[k]] : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r[k] != 1) return c + k;
+  }
+  return d.columns;
+}
 
 // The plan: each slot's share of the free pages (a copy of its last page
 // first, then its new columns), and whether there are enough.
@@ -235,10 +252,14 @@ __global__ void __launch_bounds__(kPlan) grow_plan_kernel(const __grid_constant_
   // needs in the low 44 bits, copies above; every CTA adds up all slots
   const int per = (p.n_seqs + kPlan - 1) / kPlan;
   const int s0 = min(p.n_seqs, (int)threadIdx.x * per), s1 = min(p.n_seqs, s0 + per);
+  // each CTA writes the slots of its share of the threads
+  const bool owner = (int)(threadIdx.x * gridDim.x / kPlan) == (int)blockIdx.x;
   long long mine = 0;
   for (int s = s0; s < s1; ++s) {
     const Need d = slot_need(p, s);
-    mine += d.columns + (d.tail >= 0) + ((long long)(d.tail >= 0) << 44);
+    const int held = held_columns(p, s, d);
+    if (owner) w.slots[s].x = held;
+    mine += d.columns - held + (d.tail >= 0) + ((long long)(d.tail >= 0) << 44);
   }
   long long all;
   long long at = block_scan(mine, sums, all);
@@ -258,6 +279,7 @@ __global__ void __launch_bounds__(kPlan) grow_plan_kernel(const __grid_constant_
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     w.head[0] = ok ? 1 : 0;
     w.head[1] = ok ? (int)(all >> 44) : 0;
+    w.head[2] = ok ? (int)total : 0;
     const long long lack = ok ? 0 : total - free_pages.all;
     *p.count = lack > 0x7fffffff ? 0x7fffffff : (int)lack;
   }
@@ -304,23 +326,36 @@ __global__ void __launch_bounds__(kPlan) grow_plan_kernel(const __grid_constant_
     rank0 += n;
   }
   plan_sync();  // the list is whole; nobody reads a box any more
-  // each CTA writes the slots of its share of the threads
-  if ((int)(threadIdx.x * gridDim.x / kPlan) != (int)blockIdx.x) return;
+  if (!owner) return;
   for (int s = s0; s < s1; ++s) {
     const Need d = slot_need(p, s);
+    const int held = w.slots[s].x, columns = d.columns - held;
     const long long base = at & ((1ll << 44) - 1);
     const bool copy = d.tail >= 0;
-    int4 rec = make_int4(d.begin, ok ? d.columns : 0, (int)base + copy, -1);
+    int4 rec = make_int4(d.begin + held, ok ? columns : 0, (int)base + copy, -1);
     if (ok && copy) {
       w.from[at >> 44] = d.tail;
       w.to[at >> 44] = w.list[base];
       rec.w = w.list[base];
     }
     w.slots[s] = rec;
-    at += d.columns + copy + ((long long)copy << 44);
+    at += columns + copy + ((long long)copy << 44);
     p.granted[s] = ok ? d.n : 0;
     p.seq_len_out[s] = max(0, p.seq_len[s]) + (ok ? d.n : 0);
   }
+}
+
+// Whether x is among the n ascending pages of the list.
+__device__ __forceinline__ bool in_list(const int* list, int n, int x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (list[mid] < x)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo < n && list[lo] == x;
 }
 
 __global__ void __launch_bounds__(kCopy) grow_apply_kernel(const __grid_constant__ CachePages p) {
@@ -331,16 +366,24 @@ __global__ void __launch_bounds__(kCopy) grow_apply_kernel(const __grid_constant
   for (int s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
     const int4 r = w.slots[s];  // first new column, columns, place in the list, copy or -1
     const size_t row = (size_t)s * p.max_pages;
-    const int own = r.w >= 0 ? r.x - 1 : -1;  // the column whose page becomes the slot's own
+    // the column whose page becomes the slot's own: that of its length before
+    const int own = r.w >= 0 ? p.seq_len_out[s] - p.granted[s] >> p.page_shift : -1;
     if (own >= 0 && threadIdx.x == 0) {
       atomicSub(p.ref_out + p.table[row + own], 1);
       p.table_out[row + own] = r.w;
     }
     const int c0 = in_place ? r.x : 0, c1 = in_place ? r.x + r.y : p.max_pages;
     for (int c = c0 + threadIdx.x; c < c1; c += kCopy)
-      if (c >= r.x && c < r.x + r.y)
+      if (c >= r.x && c < r.x + r.y) {
+        // a page that the row holds here, with others or behind a column that needed one,
+        // is given up.  (One that was free when the call began is nobody's, whatever the
+        // entry says, or was taken in this call.)
+        const int was = p.table[row + c];
         p.table_out[row + c] = w.list[r.z + c - r.x];
-      else if (c != own)
+        if ((unsigned)was < (unsigned)p.n_pages && !in_list(w.list, w.head[2], was) &&
+            *(volatile int32_t*)(p.ref_out + was) > 0)
+          atomicSub(p.ref_out + was, 1);
+      } else if (c != own)
         p.table_out[row + c] = p.table[row + c];
   }
   copy_pages(p, w.from, w.to, w.head[1]);

@@ -355,7 +355,9 @@ SAF_API saf_status saf_cache_layer_layout(const saf_cache_dims* dims,
  * tokens raise the scale of a block that older tokens began, the older codes
  * are rounded again under the new scale, which changes only those that sink
  * below e4m3's normal range; an older block's scale must be a power of two
- * (this call writes no other).  Position 0 of a page starts its block over.
+ * (this call writes no other).  Position 0 of a page starts its block over;
+ * until then a scale never falls, also where the token that raised it was taken
+ * back.
  * Infinities are stored as the largest value of the block's scale (448 s), NaN
  * as NaN.  Writing the same rows to the same positions again changes nothing.
  *
@@ -417,7 +419,13 @@ SAF_API size_t saf_cache_pages_workspace_size(const saf_cache_dims* dims);
 /* Makes room for n_new[s] more tokens in every slot and advances seq_len.
  * Free pages (ref <= 0) are taken lowest first, slot by slot; a slot whose
  * last page is begun and shared (ref > 1 before the call) first gets a copy of
- * it.  granted[s] receives the tokens that slot s may append: n_new[s], or 0
+ * it (every such slot that grows, so the page itself may end up free: the call
+ * counts on pages that are free when it begins).
+ * Tokens are taken back (rejected drafts) by lowering seq_len; the row keeps
+ * its pages.  New columns, from the first on, that hold a page of the row's own
+ * (ref == 1) use it again; behind them, and where a page is shared, the row
+ * gives up what it holds (ref falls by one) and takes a free page.
+ * granted[s] receives the tokens that slot s may append: n_new[s], or 0
  * where they would pass the end of the page table (the slot is left alone) or
  * n_new[s] <= 0.  When the pool has too few free pages nothing changes, every
  * granted[s] is 0 and n_short [1] says how many are missing; otherwise it is

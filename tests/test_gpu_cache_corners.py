@@ -207,3 +207,125 @@ def test_patterns_that_are_not_finite(api, d, n_q, kernel):
     out, lse = c.run()
     assert not bool(torch.isnan(out[0, 0].float()).any()) and bool(torch.isnan(out[1, 0].float()).all())
     c.check(out, lse)
+
+
+def grow_over_held(table, seq_len, counts, n_new, page):
+    """cache_reference.grow for rows that hold pages behind their length: those that no other
+    row holds, from the first new column on, are used again; behind them, and where a page is
+    shared, the row gives its page up and takes a free one."""
+    S, cols = table.shape
+    n = len(counts)
+    keep = np.zeros(S, dtype=int)
+    lens = np.maximum(seq_len, 0)
+    for s in range(S):
+        if n_new[s] <= 0 or lens[s] + int(n_new[s]) > cols * page:
+            continue
+        begin, end = -(-int(lens[s]) // page), -(-(int(lens[s]) + int(n_new[s])) // page)
+        while begin + keep[s] < end:
+            t = table[s, begin + keep[s]]
+            if not 0 <= t < n or counts[t] != 1:
+                break
+            keep[s] += 1
+    free = [p for p in range(n) if counts[p] <= 0]
+    out, out_ref, out_len = table.copy(), counts.copy(), lens.copy()
+    granted, copies, at = np.zeros(S, dtype=np.int32), [], 0
+
+    def take():
+        nonlocal at
+        at += 1
+        if at > len(free):
+            return -1
+        out_ref[free[at - 1]] = 1
+        return free[at - 1]
+    for s in range(S):
+        k = int(n_new[s])
+        if k <= 0 or lens[s] + k > cols * page:
+            continue
+        granted[s] = k
+        if lens[s] % page:
+            held = table[s, lens[s] // page]
+            if 0 <= held < n and counts[held] > 1:
+                new = take()
+                copies.append((held, new))
+                out_ref[held] -= 1
+                out[s, lens[s] // page] = new
+        begin, end = -(-int(lens[s]) // page), -(-(int(lens[s]) + k) // page)
+        for c in range(begin + keep[s], end):
+            t = table[s, c]
+            out[s, c] = take()
+            if 0 <= t < n and counts[t] > 0:
+                out_ref[t] -= 1
+        out_len[s] += k
+    if at > len(free):
+        return table, seq_len, counts, np.zeros(S, dtype=np.int32), at - len(free), []
+    return out, out_len, out_ref, granted, 0, copies
+
+
+TAKEN_BACK = [(1, 4, 9, 16), (6, 9, 90, 16), (40, 30, 2600, 16), (300, 12, 9001, 16),
+              (2000, 6, 30000, 16), (3, 700, 9000, 16)]
+
+
+@pytest.mark.parametrize("into", [False, True])
+@pytest.mark.parametrize("S,cols,n_pages,page", TAKEN_BACK)
+def test_grow_after_tokens_were_taken_back(api, S, cols, n_pages, page, into):
+    from test_gpu_cache import page_cache, random_tables
+    rng = np.random.default_rng(S + cols)
+    for seed, most in enumerate((1, 2 * page, cols * page)):
+        table, lens = random_tables(rng, S, cols, n_pages, page, 0.3)
+        # lengths go down, pages stay; some entries behind are holes or no pages
+        lens = (lens * rng.random(S) ** 0.5).astype(np.int32)
+        lens[rng.random(S) < 0.1] = 0
+        counts = np.bincount(table[table >= 0].flatten(), minlength=n_pages).astype(np.int32)
+        cache, got_counts, pool = page_cache(api, table, lens, n_pages, page, seed)
+        assert np.array_equal(counts, got_counts)
+        n_new = rng.integers(-1, most + 1, S).astype(np.int32)
+        before = host(pool)
+        w_table, w_lens, w_ref, granted, short, copies = grow_over_held(table, lens, counts, n_new, page)
+        to = tuple(torch.full_like(t, -7) for t in (cache.page_table, cache.seq_len, cache.ref)) \
+            if into else None
+        got_granted, got_short = cache.grow(i32(n_new), into=to)
+        got = [host(t) for t in (to or (cache.page_table, cache.seq_len, cache.ref))]
+        assert int(got_short) == short and np.array_equal(host(got_granted), granted)
+        for g, w in zip(got, (w_table, w_lens, w_ref)):
+            assert np.array_equal(g, w)
+        # nothing is lost: every page is counted as often as it is held
+        held = np.bincount(got[0][got[0] >= 0].flatten(), minlength=n_pages)
+        assert np.array_equal(held, got[2])
+        for a, b in copies:
+            before[b] = before[a]
+        assert np.array_equal(host(pool), before)
+
+
+def test_drafts_taken_back_again_and_again(api):
+    # a pool with no page to spare: every draft fits into the pages that the row holds already
+    cache = api.PagedCache([[0, 0]], 2, 32, n_seqs=2, max_pages=4, n_pages=7, page_size=16,
+                           max_new=20, device=DEV)
+    cache.grow(i32([45, 45]))
+    for i in range(12):
+        granted, short = cache.grow(i32([19, 3]))
+        assert int(short) == 0 and host(granted).tolist() == [19, 3]
+        cache.seq_len.sub_(i32([18, 3]) if i % 2 else i32([19, 3]))
+        if i == 5:
+            cache.seq_len.copy_(i32([45, 45]))
+        held = host(cache.page_table)
+        assert np.array_equal(np.bincount(held[held >= 0], minlength=7), host(cache.ref))
+        cache.seq_len.clamp_(max=45)
+    assert int((cache.ref > 0).sum()) == 7
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_entries_that_no_count_knows_are_overwritten(api, into):
+    # a caller that starts over by clearing lengths and counts, not the table
+    cache = api.PagedCache([[0, 0]], 2, 32, n_seqs=3, max_pages=4, n_pages=12, page_size=16,
+                           device=DEV)
+    cache.grow(i32([64, 64, 64]))
+    cache.seq_len.zero_()
+    cache.ref.zero_()
+    cache.page_table.copy_(cache.page_table.flip(0))
+    to = tuple(torch.zeros_like(t) for t in (cache.page_table, cache.seq_len, cache.ref)) if into else None
+    granted, short = cache.grow(i32([40, 64, 16]), into=to)
+    table, lens, counts = to or (cache.page_table, cache.seq_len, cache.ref)
+    assert int(short) == 0 and host(granted).tolist() == [40, 64, 16]
+    got = host(table)
+    assert got[0, :3].tolist() == [0, 1, 2] and got[1].tolist() == [3, 4, 5, 6] and got[2, 0] == 7
+    assert host(counts).tolist() == [1] * 8 + [0] * 4

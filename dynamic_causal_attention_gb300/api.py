@@ -186,6 +186,7 @@ class PagedCache:
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.H, self.d_h, self.H_kv = H, d_h, H if H_kv is None else H_kv
         self.n_seqs, self.max_pages, self.n_pages = n_seqs, max_pages, n_pages
         self.page_size, self.max_new = page_size, max_new
@@ -218,10 +219,8 @@ class PagedCache:
         self._pool = pool
         self._shapes = (torch.Size((n_seqs, max_pages)), torch.Size((n_seqs,)),
                         torch.Size((n_pages,)))
-        # the tables and the pool stay the same tensors, so their addresses do too
-        self._at = self._table_like(self._tables, "PagedCache")
-        self._pool_at = pool.data_ptr()
-        self._layer_at = [self._pool_at + o for o in self.offsets]
+        self._table_like(self._tables, "PagedCache")
+        self._pool_shape, self._strides = pool.shape, pool.stride()
         # a pool of one page may report any stride
         self.dims = B._cache_dims(*geometry, pool.stride(0) if n_pages > 1 else at)
         with torch.cuda.device(self.device):
@@ -233,7 +232,6 @@ class PagedCache:
         self.workspace = torch.empty(attn, dtype=torch.uint8, device=self.device)
         self.workspace[:256].zero_()  # the status before the first call
         self._pages_ws = torch.empty(pages, dtype=torch.uint8, device=self.device)
-        self._ws_at, self._pages_at = self.workspace.data_ptr(), self._pages_ws.data_ptr()
 
     page_table = property(lambda self: self._tables[0], doc="[n_seqs, max_pages] int32")
     seq_len = property(lambda self: self._tables[1], doc="[n_seqs] int32: tokens of each slot")
@@ -242,8 +240,8 @@ class PagedCache:
 
     # ---- checks
     def _need(self, t, shape, dtype, what):
-        if (t.shape != shape or t.dtype != dtype or t.device != self.device
-                or not t.is_contiguous()):
+        if (t.dtype is not dtype or not t.is_cuda or t.get_device() != self._index
+                or t.shape != shape or not t.is_contiguous()):
             raise B.SafError(B.SAF_ERR_INVALID_ARG,
                              f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on {self.device}")
         return t.data_ptr()
@@ -251,16 +249,32 @@ class PagedCache:
     def _table_like(self, three, what):
         return tuple(self._need(t, s, torch.int32, what) for t, s in zip(three, self._shapes))
 
+    # The tables and the pool belong to the caller, who may give them other storage: every call
+    # takes their addresses anew, and checks them like its other arguments.
+    def _table_at(self, i):
+        return self._need(self._tables[i], self._shapes[i], torch.int32, "PagedCache: its tables")
+
+    def _tables_at(self):
+        return self._table_at(0), self._table_at(1), self._table_at(2)
+
+    def _pool_at(self):
+        p = self._pool
+        if (p.dtype is not torch.uint8 or not p.is_cuda or p.get_device() != self._index
+                or p.shape != self._pool_shape or p.stride() != self._strides):
+            raise B.SafError(B.SAF_ERR_INVALID_ARG,
+                             "PagedCache: the pool has another shape, type, device or stride now")
+        return p.data_ptr()
+
     def _per_slot(self, t, what):
         return None if t is None else self._need(t, self._shapes[1], torch.int32, what)
 
     def _call(self, entry, *args):
         """The C entry on this cache's device and its current stream."""
-        if torch.cuda.current_device() == self.device.index:
-            st = entry(*args, _raw_stream(self.device.index))
+        if torch.cuda.current_device() == self._index:
+            st = entry(*args, _raw_stream(self._index))
         else:
             with torch.cuda.device(self.device):
-                st = entry(*args, _raw_stream(self.device.index))
+                st = entry(*args, _raw_stream(self._index))
         if st != B.SAF_OK:
             raise B.SafError(st, entry.__name__)
 
@@ -276,9 +290,9 @@ class PagedCache:
         pv = self._need(v, shape, v.dtype, "append: v")
         pk = None if k is None else self._need(k, shape, v.dtype, "append: k")
         self._call(B.saf_cache_append, self.dims, self._static[layer],
-                   self._layer_at[layer], pk, pv,
+                   self._pool_at() + self.offsets[layer], pk, pv,
                    B.SAF_F32 if v.dtype == torch.float32 else B.SAF_BF16, n,
-                   self._per_slot(n_new, "append: n_new"), self._at[1], self._at[0])
+                   self._per_slot(n_new, "append: n_new"), self._table_at(1), self._table_at(0))
 
     def attend(self, layer: int, q, alpha=None, rho=None, n_new=None, out=None, lse=None):
         """The hybrid attention of q [n_seqs, H, n, d_h] (bf16), the last n_new[s] (None: n)
@@ -302,11 +316,11 @@ class PagedCache:
         if self._frozen[layer] and (alpha is None or rho is None):
             raise B.SafError(B.SAF_ERR_INVALID_ARG, "attend: frozen heads need alpha and rho")
         self._call(B.saf_cache_attn, self.dims, self._static[layer],
-                   self._layer_at[layer], pq, pa, pr, T, n,
-                   self._per_slot(n_new, "attend: n_new"), self._at[1], self._at[0],
+                   self._pool_at() + self.offsets[layer], pq, pa, pr, T, n,
+                   self._per_slot(n_new, "attend: n_new"), self._table_at(1), self._table_at(0),
                    self._need(out, shape, torch.bfloat16, "attend: out"),
                    self._need(lse, shape[:3], torch.float32, "attend: lse"),
-                   self._ws_at, self.ws_bytes)
+                   self.workspace.data_ptr(), self.ws_bytes)
         return out, lse
 
     def views(self, layer: int):
@@ -326,31 +340,33 @@ class PagedCache:
         uses them again where no other row holds them.  Returns (granted [n_seqs], n_short [1]): what each slot got, all zero
         when n_short pages are missing.  ``into``: (page_table, seq_len, ref) to write instead of
         the cache's own."""
-        to = self._at if into is None else self._table_like(into, "grow: into")
+        at = self._tables_at()
+        to = at if into is None else self._table_like(into, "grow: into")
         granted = torch.empty(self.n_seqs, dtype=torch.int32, device=self.device)
         n_short = torch.empty(1, dtype=torch.int32, device=self.device)
-        self._call(B.saf_cache_grow, self.dims, self._pool_at, self.page_bytes,
-                   self._per_slot(n_new, "grow: n_new"), *self._at, *to, granted.data_ptr(),
-                   n_short.data_ptr(), self._pages_at, self._pages_bytes)
+        self._call(B.saf_cache_grow, self.dims, self._pool_at(), self.page_bytes,
+                   self._per_slot(n_new, "grow: n_new"), *at, *to, granted.data_ptr(),
+                   n_short.data_ptr(), self._pages_ws.data_ptr(), self._pages_bytes)
         return granted, n_short
 
     def fork(self, parent, into=None):
         """Slot s takes over the pages and length of slot parent[s] (int32 [n_seqs]); a parent
         outside [0, n_seqs) frees it.  ``into`` as in grow."""
-        to = self._at if into is None else self._table_like(into, "fork: into")
-        self._call(B.saf_cache_fork, self.dims, self._per_slot(parent, "fork: parent"), *self._at, *to)
+        at = self._tables_at()
+        to = at if into is None else self._table_like(into, "fork: into")
+        self._call(B.saf_cache_fork, self.dims, self._per_slot(parent, "fork: parent"), *at, *to)
 
     def compact(self, into=None):
         """Move the used pages into the lowest page numbers.  Returns their number (int32 [1]).
         ``into``: (page_table, ref) to write instead of the cache's own."""
-        table, _, ref = self._at
+        table, ref = self._table_at(0), self._table_at(2)
         to = (table, ref)
         if into is not None:
             to = (self._need(into[0], self._shapes[0], torch.int32, "compact: into"),
                   self._need(into[1], self._shapes[2], torch.int32, "compact: into"))
         n_used = torch.empty(1, dtype=torch.int32, device=self.device)
-        self._call(B.saf_cache_compact, self.dims, self._pool_at, self.page_bytes, table, ref,
-                   *to, n_used.data_ptr(), self._pages_at, self._pages_bytes)
+        self._call(B.saf_cache_compact, self.dims, self._pool_at(), self.page_bytes, table, ref,
+                   *to, n_used.data_ptr(), self._pages_ws.data_ptr(), self._pages_bytes)
         return n_used
 
     def device_status(self):

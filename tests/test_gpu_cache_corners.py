@@ -329,3 +329,43 @@ def test_entries_that_no_count_knows_are_overwritten(api, into):
     got = host(table)
     assert got[0, :3].tolist() == [0, 1, 2] and got[1].tolist() == [3, 4, 5, 6] and got[2, 0] == 7
     assert host(counts).tolist() == [1] * 8 + [0] * 4
+
+
+def test_tensors_that_change_under_the_cache(api):
+    # the cache looks at its tensors on every call: new storage is used, another shape refused
+    c = Case(api, mask_of(4, (2,)), 2, 64, 16, [40, 25], 2, seed=6)
+    k = c.cache
+    out, lse = c.run()
+    old = [k.page_table.data, k.seq_len.data, k.pool.data]   # (the old memory stays alive)
+    pool = torch.zeros((k.n_pages, old[2].stride(0)), dtype=torch.uint8, device=DEV)
+    pool[:, :k.page_bytes].copy_(old[2])
+    k.pool.data = pool[:, :k.page_bytes]
+    k.page_table.data = old[0].clone()
+    k.seq_len.data = old[1].clone()
+    for t in old:
+        t.zero_()
+    out2, lse2 = c.run()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    table, lens = k.page_table.clone(), k.seq_len.clone()
+    k.grow(i32([0, 0]))
+    k.fork(i32([1, 0]))
+    assert torch.equal(k.page_table, table.flip(0)) and torch.equal(k.seq_len, lens.flip(0))
+    v = torch.zeros((2, 2, 1, 64), device=DEV)
+    q = c.q[:, :, :1].contiguous()
+    pat = torch.zeros((4, 64), device=DEV)
+    calls = [lambda: k.append(0, v, v), lambda: k.attend(0, q, pat, pat), lambda: k.grow(i32([1, 1])),
+             lambda: k.fork(i32([0, 1])), lambda: k.compact()]
+    for name in ("page_table", "seq_len", "ref", "pool"):
+        t = getattr(k, name)
+        was = t.data
+        for other in (was[:-1].clone(), was.float(), was.cpu()):
+            t.data = other if other.dtype == t.dtype else other.to(torch.int64)
+            for i, call in enumerate(calls):
+                if name == "ref" and i < 2 or name == "seq_len" and i == 4 or name == "pool" and i == 3:
+                    continue                                  # these do not look at it
+                with pytest.raises(api.SafError):
+                    call()
+                    pytest.fail(f"{name}: call {i} was taken")
+            t.data = was
+    for call in calls:
+        call()

@@ -7,6 +7,8 @@ non-OK status.  All arithmetic runs in libsaf's kernels.
 
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import torch
 
@@ -297,16 +299,21 @@ class PagedCache:
     def attend(self, layer: int, q, alpha=None, rho=None, n_new=None, out=None, lse=None):
         """The hybrid attention of q [n_seqs, H, n, d_h] (bf16), the last n_new[s] (None: n)
         tokens of each slot, over the cache.  alpha, rho [H, T] are needed where the layer has
-        frozen heads.  Returns (out, lse); rows behind n_new are left as they were."""
+        frozen heads.  Returns (out, lse); rows behind n_new are left as they were in buffers that
+        are given, and 0 and -inf in those that the call makes (two small launches more)."""
         n = q.shape[2] if q.dim() == 4 else -1
         shape = (self.n_seqs, self.H, n, self.d_h)
         pq = self._need(q, shape, torch.bfloat16, "attend: q")
         if n > self.max_new:
             raise B.SafError(B.SAF_ERR_INVALID_ARG, f"attend: {n} rows, max_new is {self.max_new}")
+        # what is made here and may keep rows that no slot takes starts as the results of rows
+        # without a key
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty_like(q) if n_new is None else torch.zeros_like(q)
         if lse is None:
             lse = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
+            if n_new is not None:
+                lse.fill_(-math.inf)
         pa = pr = None
         T = 0
         if alpha is not None:

@@ -369,3 +369,21 @@ def test_tensors_that_change_under_the_cache(api):
             t.data = was
     for call in calls:
         call()
+
+
+def test_outputs_that_the_call_makes_hold_no_old_memory(api):
+    # rows behind n_new of buffers that attend itself allocates: no token, so out = 0, lse = -inf
+    for n_q, kernel in KERNELS:
+        c = Case(api, mask_of(4, (2,)), 2, 64, 16, [120, n_q, 90], n_q, n_new=[n_q, 0, 2], seed=6,
+                 kernel=kernel)
+        want, want_lse = c.run()
+        a, r = (torch.from_numpy(x).to(DEV) for x in (c.alpha, c.rho))
+        for _ in range(3):
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+                    for n in (c.q.nbytes, want_lse.nbytes) for _ in range(8)]
+            del junk  # (what the allocator hands out next holds NaN)
+            out, lse = c.cache.attend(0, c.q, a, r, n_new=i32(c.n_new))
+            for s, n in enumerate(c.n_new):
+                assert torch.equal(out[s, :, :n], want[s, :, :n])
+                assert torch.equal(lse[s, :, :n], want_lse[s, :, :n])
+                assert bool((out[s, :, n:] == 0).all()) and bool((lse[s, :, n:] == -np.inf).all())

@@ -27,11 +27,11 @@
 // do for most rows: scaled by a power of two to a largest component of 224 to 448,
 // the first is e4m3 and leaves at most 4 of a bf16 value's 8 bits (and no more than 8
 // units of its last place), the second e5m2, whose 3 bits hold that.  This is exact for
-// components down to 2^-6, where e4m3 becomes subnormal: 2^-14 of the row's largest;
+// components down to 2^-6, where e4m3 becomes subnormal: 2^-13 of the row's largest;
 // below, they are off by at most 2^-14, 2^-21 of it.  A row tile with an infinity, or
 // with a row of more than two such components, takes three e5m2 parts of rows scaled to
 // a largest component of 2^14 to 2^15.8: they leave 5, 2 and no bits, exact down to
-// 2^-24 of the largest, below off by 2^-31 of it.  (Of 128 normal components, 0.013 lie
+// 2^-23 of the largest, below off by 2^-31 of it.  (Of 128 normal components, 0.013 lie
 // below 2^-6: in a call of 256 row tiles more than two of one row hardly ever do.  The
 // call below takes 263 us, 302 if all have three parts.  Two e4m3 parts are exact down
 // to 2^-10: beside a component 1000 times the others they left logits off by 2^-7.)  V

@@ -228,15 +228,16 @@ __device__ __forceinline__ Need slot_need(const CachePages& p, int s) {
 // number.  To be asked before the counts change.
 __device__ __forceinline__ int held_columns(const CachePages& p, int s, const Need& d) {
   const int32_t* row = p.table + (size_t)s * p.max_pages + d.begin;
-  for (int c = 0; c < d.columns; c += 4) {  // four loads in flight
-    int t[4], r[4];
+  constexpr int kAhead = 4;  // loads in flight
+  for (int c = 0; c < d.columns; c += kAhead) {
+    int t[kAhead], r[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t[k] = c + k < d.columns ? row[c + k] : -1;
+    for (int k = 0; k < kAhead; ++k) t[k] = c + k < d.columns ? row[c + k] : -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = (unsigned)t[k] < (unsigned)p.n_pages ? p.ref[t[k]] : 0;
+    for (int k = 0; k < kAhead; ++k) r[k] = (unsigned)t[k] < (unsigned)p.n_pages ? p.ref[t[k]] : 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (r[k] != 1) return c + k;
+    for (int k = 0; k < kAhead; ++k)
+      if (r[k] != 1) return min(c + k, d.columns);
   }
   return d.columns;
 }

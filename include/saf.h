@@ -382,14 +382,21 @@ SAF_API size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q
  *   Q           bf16 [n_seqs, H, n_q, d_h]; rows of frozen heads and rows
  *               t >= n_new are never read (Q may be NULL when H_k = 0).
  *   alpha, rho  fp32 [H, T_pat]; only rows of frozen heads are read.  Keys and
- *               distances at or behind T_pat count as -inf.
+ *               distances at or behind T_pat count as -inf, and so do values
+ *               below -2.3e38 (float's lowest, as a mask).
  *   n_new, seq_len, page_table: as in saf_cache_append.  Scales must be
- *               positive normal numbers.
+ *               positive normal numbers, those of V between 2^-80 and 2^120 and
+ *               those of one slot and head at most 2^100 apart.
  *   out         bf16 [n_seqs, H, n_q, d_h]; lse fp32 [n_seqs, H, n_q] or NULL:
  *               log sum_j exp(.).  A row that sees no key, or none of nonzero
  *               weight, gets out = 0 and lse = -inf.  Rows t >= n_new are left
  *               as they were.
  *   workspace   256-byte aligned; saf_get_device_status reads its status.
+ * Both products have fp32 sums.  Weights are rounded to f16, relative to the
+ * largest of the row times its V scale: 2^-11 of each, and of one below 2^-25 of
+ * the largest 2^-36 of that (so keys that far below it are lost).  Q is exact but
+ * for components far below the largest of their row: with few rows 2^-28 of it;
+ * with many 2^-13, of which up to two in a row may be off by 2^-21 of the largest.
  * What lies on a page behind a slot's last token, or at keys that a row does
  * not see, has no part in the row's result, NaN codes included.  Results do
  * not depend on timing: the same call gives the same bits. */

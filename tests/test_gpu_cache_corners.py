@@ -387,3 +387,33 @@ def test_outputs_that_the_call_makes_hold_no_old_memory(api):
                 assert torch.equal(out[s, :, :n], want[s, :, :n])
                 assert torch.equal(lse[s, :, :n], want_lse[s, :, :n])
                 assert bool((out[s, :, n:] == 0).all()) and bool((lse[s, :, n:] == -np.inf).all())
+
+
+@pytest.mark.parametrize("n_q,kernel", KERNELS)
+def test_masks_of_the_lowest_value_are_masks_of_minus_infinity(api, n_q, kernel):
+    c = Case(api, mask_of(6, (0, 1, 2, 3)), 3, 64, 32, [150, 75], n_q, seed=2, kernel=kernel)
+    got = []
+    for low in (-np.inf, np.finfo(np.float32).min):
+        c.alpha[0, ::3] = low
+        c.rho[1, 2:50] = low
+        c.alpha[2] = low
+        c.rho[3] = low
+        got.append(c.run())
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool((got[1][0][:, 2:4] == 0).all()) and bool((got[1][1][:, 2:4] == -np.inf).all())
+
+
+@pytest.mark.parametrize("n_q,kernel", KERNELS)
+@pytest.mark.parametrize("d", [32, 128])
+def test_scales_of_v_at_the_ends_of_their_range(api, d, n_q, kernel):
+    # blocks of zeros (scale 2^-64) beside large ones: their keys count in the sums all the same
+    c = Case(api, mask_of(4, (1,)), 2, d, 16, [300, n_q + 40], n_q, seed=d, kernel=kernel)
+    rng = np.random.default_rng(d)
+    small = rng.random(c.v_scales.shape) < 0.5
+    fin = np.isfinite(c.v_scales)
+    c.v_scales = np.where(fin, np.where(small, 2.0 ** -64, 2.0 ** 36), c.v_scales).astype(np.float32)
+    zero = np.broadcast_to((small & fin)[:, :, None, None], c.v_codes.shape)
+    c.v_codes = np.where(zero & ((c.v_codes & 0x7F) != 0x7F), 0, c.v_codes)
+    c.put()
+    c.check(*c.run())

@@ -90,12 +90,15 @@ saf_status make_call(const saf_cache_dims& d, const uint8_t* head_is_static, con
 // Which kernel takes an attention call of n_q rows.  cache_attn.cu starts fast
 // and reads a head's keys once for every 8 or 16 rows (from L2 after the first);
 // cache_chunk.cu takes longer to start and reads them once for 256 rows of the
-// dynamic heads and once for 256 of each frozen one.  What the host knows of the
-// lengths is the page table's width.  The times are in nanoseconds on the whole
-// GPU for a unit of rows and for each of its keys, fitted to 300 calls drawn at
-// random that were timed with both: the choice costs 0.1% over the better one (by
-// rows alone, 11%).  E.g. 4 x 107 rows of 2 heads against 107 keys: 8 and 18 us;
-// 8 x 370 rows of 9 heads of 3 against 7973 keys: 494 and 120 us.
+// dynamic heads and once for 256 of each frozen one.  The times are in nanoseconds
+// on the whole GPU for a unit of rows and for each of its keys, fitted to 300 calls
+// drawn at random that were timed with both, in tables as wide as their longest
+// sequence: there the choice cost 0.1% over the better one (by rows alone, 11%).
+// (Both kernels have changed by up to 5% since.)  All that the host knows of the
+// lengths is the page table's width, so short sequences in wide tables may get the
+// slower kernel: 4 x 107 rows of 2 heads against 107 keys take 6 us in a table of 128
+// or 512 keys, 8 in one of 4096 (units may then be cut), 14 from 32768 on; a prompt of
+// 512 tokens, 16 heads of 4, 28 us in a table of 512 keys and 26 in wider ones.
 bool many_rows(const saf_cache_dims& d, const uint8_t* is_static, int n_q) {
   const int g = d.H / d.H_kv;
   const long long rows = (long long)n_q * g, tile = rows <= 8 ? 8 : 16;

@@ -45,19 +45,21 @@ constexpr int kWarps = 4;
 // keys.  The row tiles of a head lie side by side, so that their codes come from
 // L2 after the first.  All tiles of all units, in that order, are cut into shares,
 // one for each CTA, equal when a unit counts kUnitCost tiles more for its
-// beginning and end (64 slots of up to 2500 tokens, 32 heads of 8: 55 us with none,
-// 45 with one, 42 with two, 41 with three; 48 slots of up to 4096, 12 heads of 4, d_h
-// = 64: 23.1, 19.9, 19.4, 20.9); a unit that is cut leaves partial sums, joined by a
-// second kernel in the order of the CTAs.  Nothing depends on timing.  A share may
-// be a single tile: what a step costs a CTA without company is the latency of its
-// loads (one token against 1000, 16 heads of 4: 8.6 us; with shares of 4 tiles and
-// more, 11.3).
+// beginning and end (64 slots of up to 2500 tokens, 32 heads of 8: 39 us; with none
+// 31% more, with one 7%, with three 2% less; 48 slots of up to 4096, 12 heads of 4,
+// d_h = 64: 18 us, 19%, 3% and 8% more); a unit that is cut leaves partial sums,
+// joined by a second kernel in the order of the CTAs.  Nothing depends on timing.  A
+// share may be a single tile: what a step costs a CTA without company is the latency
+// of its loads (one token against 1000, 16 heads of 4: 7.9 us; with shares of 4 tiles
+// and more a third longer).
 //
 // Where no slot can have more than kWholeTiles tiles, each unit is one CTA's
-// instead, without a search for its share and without a second kernel: 7.6 us
-// against 8.2 for 4 units of 4 tiles, 8.8 against 12.3 for 256.  With up to
-// kWholeTilesMany that pays only where there are units for half of the SMs: 11.5
+// instead, without a search for its share and without a second kernel: when that was
+// chosen, 7.6 us against 8.2 for 4 units of 4 tiles, 8.8 against 12.3 for 256.  With up
+// to kWholeTilesMany it pays only where there are units for half of the SMs: 11.5
 // against 8.4 us for 4 units of 8 tiles, 11.8 and 11.4 for 64, 13.1 and 15.6 for 256.
+// (What a slot can have is the page table's width; what it has is on the GPU.  12
+// heads against 100 tokens: 4.1 us in a table of 128 keys, 6.4 in one of 4096.)
 constexpr int kUnitCost = 2;
 constexpr int kWholeTiles = 4, kWholeTilesMany = 8;
 constexpr int kJoinAhead = 8;    // parts that a joining thread has in flight
@@ -178,7 +180,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // CTAs on an SM: as many as the registers allow without spills (8 rows: 166 of 168;
-// a fourth CTA's 128 cost 32 x 8192 tokens of 16 heads 162 us for 151, two CTAs 178),
+// a fourth CTA's 128 cost 32 x 8192 tokens of 16 heads 162 us for 150, two CTAs 178),
 // and stages of a ring: with two it is 203 us, with four 160.
 template <int NT>
 constexpr int kCtas = NT == 1 ? 3 : 2;

@@ -33,7 +33,7 @@
 // a largest component of 2^14 to 2^15.8: they leave 5, 2 and no bits, exact down to
 // 2^-23 of the largest, below off by 2^-31 of it.  (Of 128 normal components, 0.013 lie
 // below 2^-6: in a call of 256 row tiles more than two of one row hardly ever do.  The
-// call below takes 263 us, 302 if all have three parts.  Two e4m3 parts are exact down
+// call below takes 15% longer if all have three parts.  Two e4m3 parts are exact down
 // to 2^-10: beside a component 1000 times the others they left logits off by 2^-7.)  V
 // is turned into f16 (exact): splitting the 256 x 128 weights of a tile in its place
 // would take six times the arithmetic of converting V's 128 x d_h codes.
@@ -45,9 +45,9 @@
 // reads that half's P.  What a tile of keys costs is the chain S, softmax, P V
 // and its hand-offs, about 4300 cycles for 256 rows at d_h = 128, against some
 // 1800 of the tensor cores' time; 2 x 2000 rows of 16 heads against 8192 keys take
-// 263 us, 48% of the measured burst rate of products, and with 4 frozen heads,
-// whose weights are 32 loads of two from the window for each half a tile, 268 us
-// (41%; with all heads frozen 285, of which 8 for the single stage of V's codes that
+// 265 us, 48% of the measured burst rate of products, and with 4 frozen heads,
+// whose weights are 32 loads of two from the window for each half a tile, 271 us
+// (41%; with all heads frozen 287, of which 8 for the single stage of V's codes that
 // Q's third part leaves room for).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -239,8 +239,8 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // With tiles alone counted, 2 x 2000 rows of 16 heads, 4 of them frozen, against
 // 8192 keys took 5% longer (the average SM was idle for a tenth of them), 12 x 76
 // rows of 128 heads against 388 keys 34%.  (At d_h = 128 the frozen tile counts 9
-// and units a little less than alone: 268 us in that call, with 8 for both kinds of
-// tile 281.)
+// and units a little less than alone; with 8 for both kinds of tile that call takes
+// 5% longer.)
 struct Costs {
   int tile[2][2];  // [frozen][both row tiles]
   int unit[2];     // [frozen]

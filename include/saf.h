@@ -394,9 +394,11 @@ SAF_API size_t saf_cache_attn_workspace_size(const saf_cache_dims* dims, int n_q
  *   workspace   256-byte aligned; saf_get_device_status reads its status.
  * Both products have fp32 sums.  Weights are rounded to f16, relative to the
  * largest of the row times its V scale: 2^-11 of each, and of one below 2^-25 of
- * the largest 2^-36 of that (so keys that far below it are lost).  Q is exact but
- * for components far below the largest of their row: with few rows 2^-28 of it;
- * with many 2^-13, of which up to two in a row may be off by 2^-21 of the largest.
+ * the largest 2^-36 of that (so keys that far below it are lost).  lse is off by up
+ * to 2^-23 of a logit plus the logarithm of its V scale.  Q is exact but for
+ * components far below the largest of their row: with few rows 2^-28 of it; with
+ * many 2^-13, and then off by at most 2^-21 of the largest, or 2^-31 where a row has
+ * more than two of them.
  * What lies on a page behind a slot's last token, or at keys that a row does
  * not see, has no part in the row's result, NaN codes included.  Results do
  * not depend on timing: the same call gives the same bits. */

@@ -27,6 +27,10 @@ SAF_F32 = 1
 
 SAF_CALIB_TRACK_KL = 1
 
+SAF_ROTARY_INTERLEAVED = 1
+SAF_ROTARY_INVERSE = 2
+SAF_CLEAR_REST = 4
+
 EXPORTED = (
     "saf_hybrid_attn_workspace_size",
     "saf_hybrid_attn_fwd",
@@ -57,6 +61,10 @@ EXPORTED = (
     "saf_cache_pages_workspace_size",
     "saf_cache_grow",
     "saf_cache_compact",
+    "saf_rotary_turns",
+    "saf_rotary",
+    "saf_beam_workspace_size",
+    "saf_beam_step",
 )
 
 
@@ -74,6 +82,23 @@ class saf_cache_dims(ctypes.Structure):
 class saf_cache_layout(ctypes.Structure):
     _fields_ = [("H_k", ctypes.c_int), ("v", ctypes.c_size_t), ("k_scale", ctypes.c_size_t),
                 ("v_scale", ctypes.c_size_t), ("bytes", ctypes.c_size_t)]
+
+
+class saf_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("seq", ctypes.c_int64), ("row", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class saf_rotary_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("H_k", ctypes.c_int), ("d_h", ctypes.c_int), ("rot", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class saf_beam_dims(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int), ("beams", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int), ("end", ctypes.c_int),
+                ("max_tokens", ctypes.c_int)]
 
 
 class SafError(RuntimeError):
@@ -161,6 +186,17 @@ _lib.saf_cache_grow.argtypes = [_cd, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp
 _lib.saf_cache_grow.restype = _i
 _lib.saf_cache_compact.argtypes = [_cd, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.saf_cache_compact.restype = _i
+_rp = ctypes.POINTER(saf_rows)
+_lib.saf_rotary_turns.argtypes = [_vp, _i, _vp]
+_lib.saf_rotary_turns.restype = _i
+_lib.saf_rotary.argtypes = [ctypes.POINTER(saf_rotary_dims), _rp, _rp, _rp, _rp, _vp,
+                            ctypes.c_float, _vp, _vp, _i, _vp, _vp, ctypes.c_uint, _vp]
+_lib.saf_rotary.restype = _i
+_lib.saf_beam_workspace_size.argtypes = [ctypes.POINTER(saf_beam_dims)]
+_lib.saf_beam_workspace_size.restype = _sz
+_lib.saf_beam_step.argtypes = [ctypes.POINTER(saf_beam_dims), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.saf_beam_step.restype = _i
 
 
 def lib():
@@ -325,3 +361,30 @@ def saf_cache_compact(dims, pool, page_bytes, page_table, ref, page_table_out, r
                       workspace, ws_bytes, stream) -> int:
     return _lib.saf_cache_compact(ctypes.byref(dims), pool, page_bytes, page_table, ref,
                                   page_table_out, ref_out, n_used, workspace, ws_bytes, stream)
+
+
+def saf_rotary_turns(radians):
+    """(status, turns): a host sequence of radians a token, as saf_rotary takes it (a list of
+    whole numbers below 2^64)."""
+    n = len(radians)
+    src, dst = (ctypes.c_double * n)(*radians), (ctypes.c_uint64 * n)()
+    st = _lib.saf_rotary_turns(src, n, dst)
+    return st, list(dst)
+
+
+def saf_rotary(dims, q, k, q_out, k_out, turns, scale, positions, cu_seqlens, n_seqs, seq_len,
+               n_new, flags, stream) -> int:
+    ref = lambda r: None if r is None else ctypes.byref(r)
+    return _lib.saf_rotary(ref(dims), ref(q), ref(k), ref(q_out), ref(k_out), turns, scale,
+                           positions, cu_seqlens, n_seqs, seq_len, n_new, flags, stream)
+
+
+def saf_beam_workspace_size(dims) -> int:
+    return _lib.saf_beam_workspace_size(ctypes.byref(dims))
+
+
+def saf_beam_step(dims, logits, scores, finished, history, n_tokens, parent, token, score_out,
+                  finished_out, history_out, workspace, ws_bytes, stream) -> int:
+    return _lib.saf_beam_step(ctypes.byref(dims), logits, scores, finished, history, n_tokens,
+                              parent, token, score_out, finished_out, history_out, workspace,
+                              ws_bytes, stream)

@@ -14,8 +14,8 @@ import torch
 
 from . import _binding as B
 
-__all__ = ["HybridAttention", "Calibration", "PagedCache", "fit_compact", "num_select",
-           "SafError"]
+__all__ = ["HybridAttention", "Calibration", "PagedCache", "Rotary", "rotary_frequencies",
+           "BeamSearch", "fit_compact", "num_select", "SafError"]
 
 SafError = B.SafError
 
@@ -378,6 +378,236 @@ class PagedCache:
 
     def device_status(self):
         return B.saf_get_device_status(_ptr(self.workspace), 0, _stream(self.device))
+
+
+class _OnDevice:
+    """What the classes below share: their device, checks of arguments, the call itself."""
+
+    def _place(self, device):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
+
+    def _bad(self, what):
+        return B.SafError(B.SAF_ERR_INVALID_ARG, what)
+
+    def _need(self, t, shape, dtype, what):
+        """The address of a contiguous tensor of this shape, type and device."""
+        if (t.dtype is not dtype or not t.is_cuda or t.get_device() != self._index
+                or t.shape != shape or not t.is_contiguous()):
+            raise self._bad(f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on "
+                            f"{self.device}")
+        return t.data_ptr()
+
+    def _rows(self, t, shape, dtype, what):
+        """saf_rows of [total, heads, d] or [B, heads, T, d] rows in any order."""
+        if (t.dtype is not dtype or not t.is_cuda or t.get_device() != self._index
+                or t.shape != shape or (t.stride(-1) != 1 and shape[-1] > 1)):
+            raise self._bad(f"{what}: want a {dtype} tensor {tuple(shape)} on {self.device} "
+                            "whose rows are contiguous")
+        st = t.stride()
+        if len(st) == 3:
+            return B.saf_rows(t.data_ptr(), 0, st[0], st[1])
+        return B.saf_rows(t.data_ptr(), st[0], st[2], st[1])
+
+    def _call(self, entry, *args):
+        """The C entry on this object's device and its current stream."""
+        if torch.cuda.current_device() == self._index:
+            st = entry(*args, _raw_stream(self._index))
+        else:
+            with torch.cuda.device(self.device):
+                st = entry(*args, _raw_stream(self._index))
+        if st != B.SAF_OK:
+            raise B.SafError(st, entry.__name__)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, stretch: float = 1.0,
+                       kind: str = "ramp", trained: int = 4096, slow: float = 1.0,
+                       fast: float = 32.0):
+    """Radians a token of each of the rot_dim / 2 turned pairs, in 64 bits: base^(-2 j / rot_dim),
+    for contexts ``stretch`` times longer than the ``trained`` one changed by ``kind``:
+
+    * ``linear``  every frequency divided by ``stretch``
+    * ``base``    a larger base, so that the slowest pair is divided by ``stretch`` and the
+                  fastest stays
+    * ``ramp``    pairs with at least ``fast`` turns over the trained context stay, those with at
+                  most ``slow`` are divided by ``stretch``, those between are mixed
+    """
+    if rot_dim < 2 or rot_dim % 2 or base <= 0 or stretch <= 0 or trained < 1 or fast <= slow:
+        raise B.SafError(B.SAF_ERR_INVALID_ARG, "rotary_frequencies")
+    if kind == "base" and stretch != 1.0:
+        if rot_dim < 4:
+            raise B.SafError(B.SAF_ERR_INVALID_ARG, "rotary_frequencies: one pair has no base")
+        base = base * stretch ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2.0 * np.arange(rot_dim // 2, dtype=np.float64) / rot_dim)
+    if kind == "linear":
+        return f / stretch
+    if kind == "ramp":
+        keep = np.clip((trained * f / (2.0 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
+        return f * keep + f / stretch * (1.0 - keep)
+    if kind != "base":
+        raise B.SafError(B.SAF_ERR_INVALID_ARG, f"rotary_frequencies: kind {kind!r}")
+    return f
+
+
+class Rotary(_OnDevice):
+    """Rotary positions for Q and K: pairs of components turned by position times frequency.
+
+    ``freqs`` are the frequencies (radians a token, one for each turned pair: see
+    rotary_frequencies); without it they are those of ``rot_dim`` (default: d_h) and ``base``.
+    The first 2 * len(freqs) components of a row are turned, the rest copied.  ``layout`` is
+    "half" (pairs j, j + rot_dim / 2) or "interleaved" (2 j, 2 j + 1); the turned pairs are
+    multiplied by ``scale``.  Angles are exact modulo a turn at any position.
+    """
+
+    def __init__(self, d_h: int, *, rot_dim=None, base: float = 10000.0, freqs=None,
+                 layout: str = "half", scale: float = 1.0, device="cuda"):
+        self._place(device)
+        if freqs is None:
+            freqs = rotary_frequencies(d_h if rot_dim is None else rot_dim, base)
+        freqs = [float(f) for f in freqs]
+        if rot_dim is not None and rot_dim != 2 * len(freqs):
+            raise self._bad(f"Rotary: {len(freqs)} frequencies for rot_dim {rot_dim}")
+        if layout not in ("half", "interleaved"):
+            raise self._bad(f"Rotary: layout {layout!r}")
+        if not freqs or 2 * len(freqs) > d_h:
+            raise self._bad(f"Rotary: {len(freqs)} pairs in {d_h} components")
+        st, turns = B.saf_rotary_turns(freqs)
+        _check(st, "saf_rotary_turns")
+        self.d_h, self.rot_dim, self.layout, self.scale = d_h, 2 * len(freqs), layout, scale
+        self.turns = torch.from_numpy(np.array(turns, dtype=np.uint64).view(np.int64)).to(
+            self.device)
+
+    def apply(self, q, k=None, *, positions=None, cu_seqlens=None, seq_len=None, n_new=None,
+              out=None, inverse=False):
+        """q [total, H, d_h] (packed rows) or [B, H, T, d_h] (as the layer and the cache take
+        them), k the same with its own heads or None, bf16 or fp32, rows in any order.  Row t of
+        a sequence is at position t; or as ``positions`` ([total] or [B, T] int32) says; or
+        counted from its sequence's start in ``cu_seqlens`` [n + 1] (packed rows); or at
+        seq_len - n_new + t as in PagedCache.append.  Returns (q, k) turned, in new tensors or in
+        ``out`` (a pair; (q, k) itself for in place).  Rows of no sequence and rows behind n_new
+        are left as they were in ``out``, 0 in new tensors.  ``inverse`` turns back: applied to
+        the gradients of the results it gives those of q and k."""
+        if q.dim() not in (3, 4):
+            raise self._bad("apply: q is neither [total, H, d_h] nor [B, H, T, d_h]")
+        if q.dtype not in (torch.bfloat16, torch.float32):
+            raise B.SafError(B.SAF_ERR_UNSUPPORTED, "apply: q is neither bf16 nor fp32")
+        packed = q.dim() == 3
+        B_, T = (1, q.shape[0]) if packed else (q.shape[0], q.shape[2])
+        H, H_k = q.shape[1], 0
+
+        def shape(heads):
+            return torch.Size((T, heads, self.d_h) if packed else (B_, heads, T, self.d_h))
+        rows = [self._rows(q, shape(H), q.dtype, "apply: q"), None]
+        if k is not None:
+            if k.dim() != q.dim():
+                raise self._bad("apply: k has another number of dimensions than q")
+            H_k = k.shape[1]
+            rows[1] = self._rows(k, shape(H_k), q.dtype, "apply: k")
+        flags = ((B.SAF_ROTARY_INTERLEAVED if self.layout == "interleaved" else 0)
+                 | (B.SAF_ROTARY_INVERSE if inverse else 0))
+        if out is None:
+            out = (torch.empty(q.shape, dtype=q.dtype, device=self.device),
+                   None if k is None else torch.empty(k.shape, dtype=q.dtype, device=self.device))
+            flags |= B.SAF_CLEAR_REST
+        elif (out[1] is None) != (k is None):
+            raise self._bad("apply: out is not a pair like (q, k)")
+        rows.append(self._rows(out[0], shape(H), q.dtype, "apply: out"))
+        rows.append(None if k is None else self._rows(out[1], shape(H_k), q.dtype, "apply: out"))
+        if (positions is not None) + (cu_seqlens is not None) + (seq_len is not None) > 1:
+            raise self._bad("apply: positions are given in more than one way")
+        at = cu = lens = new = None
+        n = 0
+        if positions is not None:
+            at = self._need(positions, torch.Size((T,) if packed else (B_, T)), torch.int32,
+                            "apply: positions")
+        elif cu_seqlens is not None:
+            if not packed or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+                raise self._bad("apply: cu_seqlens [n + 1] goes with packed rows")
+            n = cu_seqlens.shape[0] - 1
+            cu = self._need(cu_seqlens, cu_seqlens.shape, torch.int32, "apply: cu_seqlens")
+        elif seq_len is not None:
+            lens = self._need(seq_len, torch.Size((B_,)), torch.int32, "apply: seq_len")
+        if n_new is not None:
+            new = self._need(n_new, torch.Size((B_,)), torch.int32, "apply: n_new")
+        dims = B.saf_rotary_dims(B_, T, H, H_k, self.d_h, self.rot_dim,
+                                 B.SAF_F32 if q.dtype == torch.float32 else B.SAF_BF16)
+        self._call(B.saf_rotary, dims, *rows, self.turns.data_ptr(), self.scale, at, cu, n, lens,
+                   new, flags)
+        return out
+
+
+class BeamSearch(_OnDevice):
+    """Beam search over ``n_groups`` sequences with ``beams`` slots each (slot g * beams + b).
+
+        parent, token, scores, finished, history = search.step(
+            logits, scores, finished, history=history, n_tokens=n)
+        cache.fork(parent)
+
+    ``end`` is the token that ends a sequence (None: no token does).  Calls share the object's
+    workspace, so they belong on one stream at a time.
+    """
+
+    def __init__(self, n_groups: int, beams: int, vocab: int, *, end=None, device="cuda"):
+        self._place(device)
+        self.n_groups, self.beams, self.vocab = n_groups, beams, vocab
+        self.end, self.slots = end, n_groups * beams
+        if n_groups < 1:
+            raise self._bad(f"BeamSearch: {n_groups} groups")
+        with torch.cuda.device(self.device):
+            self.ws_bytes = B.saf_beam_workspace_size(self._dims(vocab, B.SAF_F32, 0))
+        if self.ws_bytes == 0:
+            raise B.SafError(B.SAF_ERR_UNSUPPORTED, "saf_beam_workspace_size")
+        self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def _dims(self, stride, dtype, max_tokens):
+        return B.saf_beam_dims(self.n_groups, self.beams, self.vocab, stride, dtype,
+                               -1 if self.end is None else self.end, max_tokens)
+
+    def step(self, logits, scores, finished=None, *, history=None, n_tokens=None,
+             history_out=None):
+        """logits [slots, vocab] (bf16 or fp32, rows any distance apart), scores [slots] fp32,
+        finished [slots] bool or None, history [slots, columns] int32 with ``n_tokens`` [1] int32
+        columns filled.  Returns (parent, token, scores, finished, history): the new slots, best
+        first in each group; finished is None without an ending token, history None without one.
+        The history is written to ``history_out`` (not the same tensor), as far as it is filled."""
+        n = (self.slots,)
+        if logits.dtype not in (torch.bfloat16, torch.float32):
+            raise B.SafError(B.SAF_ERR_UNSUPPORTED, "step: logits are neither bf16 nor fp32")
+        if (logits.shape != (self.slots, self.vocab) or logits.get_device() != self._index
+                or not logits.is_cuda or (self.vocab > 1 and logits.stride(1) != 1)
+                or (self.slots > 1 and logits.stride(0) < self.vocab)):
+            raise self._bad(f"step: want logits [{self.slots}, {self.vocab}] on {self.device} "
+                            "whose rows are contiguous and apart")
+        ps = self._need(scores, n, torch.float32, "step: scores")
+        pf = None if finished is None else self._need(finished, n, torch.bool, "step: finished")
+        if finished is not None and self.end is None:
+            raise self._bad("step: finished slots without an ending token")
+        ph = pn = po = None
+        columns = 0
+        if history is not None:
+            if n_tokens is None or history.dim() != 2:
+                raise self._bad("step: history [slots, columns] needs n_tokens")
+            columns = history.shape[1]
+            shape = (self.slots, columns)
+            if history_out is None:
+                history_out = torch.full_like(history, -1)
+            ph = self._need(history, shape, torch.int32, "step: history")
+            po = self._need(history_out, shape, torch.int32, "step: history_out")
+            pn = self._need(n_tokens, (1,), torch.int32, "step: n_tokens")
+        elif history_out is not None:
+            raise self._bad("step: history_out without a history")
+        new = torch.empty((2, self.slots), dtype=torch.int32, device=self.device)
+        parent, token = new[0], new[1]
+        score = torch.empty(n, dtype=torch.float32, device=self.device)
+        done = None if self.end is None else torch.empty(n, dtype=torch.bool, device=self.device)
+        dims = self._dims(logits.stride(0) if self.slots > 1 else self.vocab,
+                          B.SAF_F32 if logits.dtype == torch.float32 else B.SAF_BF16, columns)
+        self._call(B.saf_beam_step, dims, logits.data_ptr(), ps, pf, ph, pn, parent.data_ptr(),
+                   token.data_ptr(), score.data_ptr(), _ptr(done), po, self.workspace.data_ptr(),
+                   self.ws_bytes)
+        return parent, token, score, done, history_out
 
 
 def fit_compact(A_hat, candidates, k, kl_max=0.2, steps=400, lr=1e-2):

@@ -188,4 +188,54 @@ cudaError_t launch_cache_fork(const CachePages& p, cudaStream_t s);
 cudaError_t launch_cache_grow(const CachePages& p, int n_sms, cudaStream_t s);
 cudaError_t launch_cache_compact(const CachePages& p, int n_sms, cudaStream_t s);
 
+// ------------------------------------------------------------ rotary positions
+struct FastDiv {
+  uint32_t m;
+  int s;
+};
+struct RotaryRows {
+  void* p;
+  int64_t seq, row, head;  // elements from one sequence, row, head to the next
+};
+struct RotaryParams {
+  RotaryRows x[4];           // q, k, q_out, k_out
+  int B, T, H, H_k, d, rot;
+  const uint64_t* turns;     // [rot / 2] turns a token, in 2^-64
+  float scale, scale_sin;    // of the cosines and of the sines (negative: backwards)
+  const int32_t *positions, *cu, *seq_len, *n_new;
+  int n_seqs;
+  bool clear, copy_rest;
+  // set by launch_rotary
+  int tokens, pair_units, units;
+  uint32_t row_units;
+  FastDiv by_T, by_half, by_row, by_units;
+};
+cudaError_t launch_rotary(RotaryParams& p, bool f32, bool interleaved, int n_sms, cudaStream_t s);
+
+// ------------------------------------------------------------ beam step
+struct BeamParams {
+  int n_groups, beams, vocab, end, max_tokens, splits;
+  int64_t row_stride;
+  const void* logits;       // [n_groups * beams, vocab]
+  const float* scores;
+  const uint8_t* finished;  // or null
+  const int32_t *history, *n_tokens;  // or null
+  int32_t *parent, *token;
+  float* score_out;
+  uint8_t* finished_out;    // or null
+  int32_t* history_out;     // or null
+  // scratch: see beam_ws
+  size_t part_bytes;
+  int *row_count, *group_count, *row_n;
+  double* row_lse;
+  uint8_t *row_best, *parts;
+};
+struct BeamWs {
+  int held, splits;  // elements of a thread, blocks of a row
+  size_t part_bytes;
+  size_t row_count, group_count, row_n, row_lse, row_best, parts, total;
+};
+BeamWs beam_ws(int n_groups, int beams, int vocab, int n_sms);
+cudaError_t launch_beam(const BeamParams& p, bool f32, int held, cudaStream_t s);
+
 }  // namespace saf

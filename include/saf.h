@@ -454,6 +454,110 @@ SAF_API saf_status saf_cache_compact(const saf_cache_dims* dims, void* pool, siz
                              int32_t* page_table_out, int32_t* ref_out, int32_t* n_used,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions: Q and K on their way into the layer or the cache. */
+
+/* Rows of a tensor [B, T, heads, d_h] in any order of B, T and heads: element
+ * c of row t of sequence b under head h lies at p + b * seq + t * row + h * head
+ * + c.  Strides count elements and are not negative; a row's d_h elements lie
+ * next to one another. */
+typedef struct saf_rows {
+  void* p;
+  int64_t seq, row, head;
+} saf_rows;
+
+typedef struct saf_rotary_dims {
+  int B, T;         /* sequences and rows of each, B * T < 2^31 - 63            */
+  int H, H_k;       /* heads of q and of k (either may be 0), up to 256         */
+  int d_h;          /* 1..256                                                   */
+  int rot;          /* components that are turned, the first of each row: even, *
+                     * 2..d_h                                                   */
+  saf_dtype dtype;
+} saf_rotary_dims;
+
+/* Pair j is (x[2j], x[2j + 1]); without this flag (x[j], x[rot / 2 + j]). */
+#define SAF_ROTARY_INTERLEAVED 1u
+/* Turn back: the gradient of the call without this flag (the same scale). */
+#define SAF_ROTARY_INVERSE 2u
+/* Rows that a call does not work on (of no sequence, or behind a slot's new
+ * ones) become 0, lse -inf, instead of being left as they were. */
+#define SAF_CLEAR_REST 4u
+
+/* Frequencies in the form that saf_rotary takes: turns[i] = radians[i] / 2 pi modulo
+ * one turn, in units of 2^-64.  Host arrays; radians must be finite. */
+SAF_API saf_status saf_rotary_turns(const double* radians, int n, uint64_t* turns);
+
+/* Turns pair j of every row at position p by the angle p * radians[j] and multiplies
+ * it by `scale`; components from rot on are copied.
+ *
+ *   q, k, q_out, k_out   device rows; an output may be its input (the same saf_rows),
+ *               and must not overlap one otherwise.  k, k_out are not looked at when
+ *               H_k = 0 (q, q_out when H = 0).  16-byte vectors are used where all
+ *               pointers and strides allow it and rot / 2 and d_h are multiples of a
+ *               vector, single elements elsewhere.
+ *   turns       device [rot / 2], 8-byte aligned.
+ * At most one of the three ways to give positions:
+ *   positions   [B, T] int32; negative ones turn back.
+ *   cu_seqlens  [n_seqs + 1] int32 (B = 1): rows cu[s] <= t < cu[s + 1] are sequence
+ *               s, at positions t - cu[s]; other rows are not worked on.
+ *   seq_len, n_new   [B] int32 as in saf_cache_append: row t of slot b is at position
+ *               seq_len - n_new + t; rows t >= n_new are not worked on.  n_new NULL:
+ *               T for every slot.
+ * None: row t is at position t.
+ * The angle is exact modulo one turn for every position; sines and cosines are formed
+ * and applied in fp32. */
+SAF_API saf_status saf_rotary(const saf_rotary_dims* dims, const saf_rows* q, const saf_rows* k,
+                      const saf_rows* q_out, const saf_rows* k_out, const uint64_t* turns,
+                      float scale, const int32_t* positions, const int32_t* cu_seqlens,
+                      int n_seqs, const int32_t* seq_len, const int32_t* n_new, unsigned flags,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * Beam search: which tokens follow, and which slots go on (saf_cache_fork takes
+ * the parents that come out). */
+typedef struct saf_beam_dims {
+  int n_groups;        /* searches, each with `beams` consecutive slots       */
+  int beams;           /* 1..32                                               */
+  int vocab;           /* 1..2^22                                             */
+  int64_t row_stride;  /* elements from one slot's logits to the next, >= vocab */
+  saf_dtype dtype;     /* of the logits                                       */
+  int end;             /* the token that ends a sequence, or -1 for none      */
+  int max_tokens;      /* columns of the histories                            */
+} saf_beam_dims;
+
+/* Bytes of device workspace for saf_beam_step; 0 for dims that it does not take.
+ * The workspace must be zero before its first use (a call leaves its counters at
+ * zero again); calls that share one must not overlap, nor may their dims differ. */
+SAF_API size_t saf_beam_workspace_size(const saf_beam_dims* dims);
+
+/* One step.  Slot b of a group offers every token v with the score
+ *     scores(b) + x(b, v) - log sum_w exp x(b, w)
+ * over the slot's logits x, in which NaN, +inf and values below -2.3e38 (the type's lowest, as a
+ * mask) count as -inf; a finished slot offers the token `end` at its own score;
+ * a slot whose score is -inf (or as above) offers nothing.  The group's best
+ * `beams` offers, best first, become its slots; offers without weight (-inf) never
+ * do.  Scores are compared in 64 bits, offers of one slot by their logits; equal
+ * ones go to the lower slot, then the lower token.
+ *
+ *   logits      [n_groups * beams, vocab], rows row_stride apart; rows of finished
+ *               and dead slots are not read.
+ *   scores      [slots] fp32; finished [slots] bytes or NULL (none).
+ *   history     [slots, max_tokens] int32 or NULL, n_tokens [1] of its columns filled.
+ *   parent      [slots]: the slot (counted over all groups) that this one continues,
+ *               -1 where the group has fewer offers than slots (token -1, score -inf).
+ *   token, score_out, finished_out (or NULL)   [slots]; finished: token == end.
+ *               score_out and finished_out may be scores and finished.
+ *   history_out [slots, max_tokens]: the parent's first n_tokens columns, then the
+ *               token (as far as there are columns); -1 for free slots.  Columns
+ *               behind are left as they were.  Not the same array as history.
+ * Arrays are device arrays, aligned to their elements.  The same call gives the same
+ * bits. */
+SAF_API saf_status saf_beam_step(const saf_beam_dims* dims, const void* logits, const float* scores,
+                         const uint8_t* finished, const int32_t* history,
+                         const int32_t* n_tokens, int32_t* parent, int32_t* token,
+                         float* score_out, uint8_t* finished_out, int32_t* history_out,
+                         void* workspace, size_t ws_bytes, void* stream);
+
 /* Reads (and clears) the device status word kept in an attention workspace
  * (`is_calib_handle` = 0) or in a calibration handle (`is_calib_handle` = 1).
  * Every saf_hybrid_attn_fwd / _bwd call clears the word of its workspace when

@@ -63,6 +63,9 @@ EXPORTED = (
     "saf_cache_compact",
     "saf_rotary_turns",
     "saf_rotary",
+    "saf_packed_attn_workspace_size",
+    "saf_packed_attn_fwd",
+    "saf_packed_attn_bwd",
     "saf_beam_workspace_size",
     "saf_beam_step",
 )
@@ -93,6 +96,12 @@ class saf_rotary_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("H_k", ctypes.c_int), ("d_h", ctypes.c_int), ("rot", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+
+
+class saf_packed_dims(ctypes.Structure):
+    _fields_ = [("total", ctypes.c_int), ("n_seqs", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("d_h", ctypes.c_int),
+                ("T_pat", ctypes.c_int)]
 
 
 class saf_beam_dims(ctypes.Structure):
@@ -192,6 +201,15 @@ _lib.saf_rotary_turns.restype = _i
 _lib.saf_rotary.argtypes = [ctypes.POINTER(saf_rotary_dims), _rp, _rp, _rp, _rp, _vp,
                             ctypes.c_float, _vp, _vp, _i, _vp, _vp, ctypes.c_uint, _vp]
 _lib.saf_rotary.restype = _i
+_pd = ctypes.POINTER(saf_packed_dims)
+_lib.saf_packed_attn_workspace_size.argtypes = [_pd, _i]
+_lib.saf_packed_attn_workspace_size.restype = _sz
+_lib.saf_packed_attn_fwd.argtypes = [_pd, _rp, _rp, _rp, _vp, _vp, _vp, ctypes.c_char_p, _rp, _vp,
+                                     ctypes.c_uint, _vp, _sz, _vp]
+_lib.saf_packed_attn_fwd.restype = _i
+_lib.saf_packed_attn_bwd.argtypes = [_pd, _rp, _rp, _rp, _rp, _vp, _rp, _vp, _vp, _vp,
+                                     ctypes.c_char_p, _rp, _rp, _rp, ctypes.c_uint, _vp, _sz, _vp]
+_lib.saf_packed_attn_bwd.restype = _i
 _lib.saf_beam_workspace_size.argtypes = [ctypes.POINTER(saf_beam_dims)]
 _lib.saf_beam_workspace_size.restype = _sz
 _lib.saf_beam_step.argtypes = [ctypes.POINTER(saf_beam_dims), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -377,6 +395,27 @@ def saf_rotary(dims, q, k, q_out, k_out, turns, scale, positions, cu_seqlens, n_
     ref = lambda r: None if r is None else ctypes.byref(r)
     return _lib.saf_rotary(ref(dims), ref(q), ref(k), ref(q_out), ref(k_out), turns, scale,
                            positions, cu_seqlens, n_seqs, seq_len, n_new, flags, stream)
+
+
+def saf_packed_attn_workspace_size(dims, backward) -> int:
+    return _lib.saf_packed_attn_workspace_size(ctypes.byref(dims), int(backward))
+
+
+def saf_packed_attn_fwd(dims, Q, K, V, cu_seqlens, alpha, rho, head_is_static: bytes, out, lse,
+                        flags, workspace, ws_bytes, stream) -> int:
+    ref = lambda r: None if r is None else ctypes.byref(r)
+    return _lib.saf_packed_attn_fwd(ref(dims), ref(Q), ref(K), ref(V), cu_seqlens, alpha, rho,
+                                    head_is_static, ref(out), lse, flags, workspace, ws_bytes,
+                                    stream)
+
+
+def saf_packed_attn_bwd(dims, Q, K, V, out, lse, dout, cu_seqlens, alpha, rho,
+                        head_is_static: bytes, dQ, dK, dV, flags, workspace, ws_bytes,
+                        stream) -> int:
+    ref = lambda r: None if r is None else ctypes.byref(r)
+    return _lib.saf_packed_attn_bwd(ref(dims), ref(Q), ref(K), ref(V), ref(out), lse, ref(dout),
+                                    cu_seqlens, alpha, rho, head_is_static, ref(dQ), ref(dK),
+                                    ref(dV), flags, workspace, ws_bytes, stream)
 
 
 def saf_beam_workspace_size(dims) -> int:

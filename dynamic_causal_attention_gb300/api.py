@@ -14,7 +14,7 @@ import torch
 
 from . import _binding as B
 
-__all__ = ["HybridAttention", "Calibration", "PagedCache", "Rotary", "rotary_frequencies",
+__all__ = ["HybridAttention", "Calibration", "PackedAttention", "PagedCache", "Rotary", "rotary_frequencies",
            "BeamSearch", "fit_compact", "num_select", "SafError"]
 
 SafError = B.SafError
@@ -536,6 +536,107 @@ class Rotary(_OnDevice):
         self._call(B.saf_rotary, dims, *rows, self.turns.data_ptr(), self.scale, at, cu, n, lens,
                    new, flags)
         return out
+
+
+class PackedAttention(_OnDevice):
+    """The hybrid causal attention layer on sequences of different lengths laid end to end.
+
+    Rows cu_seqlens[s] <= i < cu_seqlens[s + 1] (int32 [n + 1] on the GPU) of q [total, H, d_h]
+    and k, v [total, H_kv, d_h] (bf16, rows in any order: views of one projection's output will
+    do) are sequence s; frozen heads (``head_is_static``, host booleans) count their pattern's
+    positions from its first row.  A call has at most ``max_total`` rows and ``max_seqs``
+    sequences of at most ``max_len`` rows; with ``backward`` the workspace has room for the
+    gradients' sums.  Nothing synchronises, and every call can be captured in a CUDA graph.
+    Calls share the object's workspace, so they belong on one stream at a time.
+    """
+
+    def __init__(self, H: int, d_h: int, head_is_static, *, max_total: int, max_seqs: int,
+                 max_len: int, H_kv=None, backward: bool = True, device="cuda"):
+        self._place(device)
+        self.H, self.d_h, self.H_kv = H, d_h, H if H_kv is None else H_kv
+        self.max_total, self.max_seqs, self.max_len = max_total, max_seqs, max_len
+        self.head_is_static = bytes(int(bool(x)) for x in head_is_static)
+        if len(self.head_is_static) != H:
+            raise self._bad(f"PackedAttention: a mask of {len(self.head_is_static)} heads")
+        self._frozen = any(self.head_is_static)
+        self.ws_bytes = B.saf_packed_attn_workspace_size(
+            B.saf_packed_dims(max_total, max_seqs, max_len, H, self.H_kv, d_h, max_len), backward)
+        if self.ws_bytes == 0:
+            raise B.SafError(B.SAF_ERR_UNSUPPORTED, "saf_packed_attn_workspace_size")
+        self._backward = backward
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.workspace[:256].zero_()  # the status before the first call
+
+    def _common(self, q, cu_seqlens, alpha, rho, what):
+        if q.dim() != 3 or q.shape[0] > self.max_total:
+            raise self._bad(f"{what}: q is not [total, H, d_h] with total <= {self.max_total}")
+        total = q.shape[0]
+        if cu_seqlens.dim() != 1 or not 1 <= cu_seqlens.shape[0] <= self.max_seqs + 1:
+            raise self._bad(f"{what}: want cu_seqlens [n + 1], n <= {self.max_seqs}")
+        n = cu_seqlens.shape[0] - 1
+        cu = self._need(cu_seqlens, cu_seqlens.shape, torch.int32, f"{what}: cu_seqlens")
+        pa = pr = None
+        T = 0
+        if self._frozen:
+            if alpha is None or rho is None:
+                raise self._bad(f"{what}: frozen heads need alpha and rho")
+            T = alpha.shape[-1]
+            if T < self.max_len:
+                raise self._bad(f"{what}: alpha has {T} columns, max_len is {self.max_len}")
+            pa = self._need(alpha, (self.H, T), torch.float32, f"{what}: alpha")
+            pr = self._need(rho, (self.H, T), torch.float32, f"{what}: rho")
+        dims = B.saf_packed_dims(total, n, self.max_len, self.H, self.H_kv, self.d_h, T)
+        wide, narrow = (total, self.H, self.d_h), (total, self.H_kv, self.d_h)
+
+        def rows(t, shape, name):
+            return self._rows(t, shape, torch.bfloat16, f"{what}: {name}")
+        return total, dims, cu, pa, pr, wide, narrow, rows
+
+    def forward(self, q, k, v, cu_seqlens, alpha=None, rho=None, out=None, lse=None):
+        """(out [total, H, d_h], lse [H, total] fp32).  Rows of no sequence are left as they were
+        in buffers that are given, 0 and -inf if the call makes both.  alpha, rho
+        [H, >= max_len] fp32 are needed where heads are frozen."""
+        total, dims, cu, pa, pr, wide, narrow, rows = self._common(q, cu_seqlens, alpha, rho,
+                                                                   "forward")
+        flags = 0
+        if out is None and lse is None:
+            flags = B.SAF_CLEAR_REST
+        if out is None:
+            make = torch.empty if flags else torch.zeros
+            out = make(wide, dtype=torch.bfloat16, device=self.device)
+        if lse is None:
+            lse = torch.empty((self.H, total), dtype=torch.float32, device=self.device)
+            if not flags:
+                lse.fill_(-math.inf)
+        self._call(B.saf_packed_attn_fwd, dims, rows(q, wide, "q"), rows(k, narrow, "k"),
+                   rows(v, narrow, "v"), cu, pa, pr, self.head_is_static, rows(out, wide, "out"),
+                   self._need(lse, (self.H, total), torch.float32, "forward: lse"), flags,
+                   self.workspace.data_ptr(), self.ws_bytes)
+        return out, lse
+
+    def backward(self, q, k, v, out, lse, dout, cu_seqlens, alpha=None, rho=None, grads=None):
+        """(dq, dk, dv) for the gradient dout of out; out and lse are the forward's.  Written to
+        ``grads`` (a triple; rows of no sequence are left as they were) or to new tensors."""
+        if not self._backward:
+            raise B.SafError(B.SAF_ERR_STATE, "backward: made with backward=False")
+        total, dims, cu, pa, pr, wide, narrow, rows = self._common(q, cu_seqlens, alpha, rho,
+                                                                   "backward")
+        flags = 0
+        if grads is None:
+            flags = B.SAF_CLEAR_REST
+            grads = tuple(torch.empty(s, dtype=torch.bfloat16, device=self.device)
+                          for s in (wide, narrow, narrow))
+        dq, dk, dv = grads
+        self._call(B.saf_packed_attn_bwd, dims, rows(q, wide, "q"), rows(k, narrow, "k"),
+                   rows(v, narrow, "v"), rows(out, wide, "out"),
+                   self._need(lse, (self.H, total), torch.float32, "backward: lse"),
+                   rows(dout, wide, "dout"), cu, pa, pr, self.head_is_static,
+                   rows(dq, wide, "dq"), rows(dk, narrow, "dk"), rows(dv, narrow, "dv"), flags,
+                   self.workspace.data_ptr(), self.ws_bytes)
+        return dq, dk, dv
+
+    def device_status(self):
+        return B.saf_get_device_status(_ptr(self.workspace), 0, _stream(self.device))
 
 
 class BeamSearch(_OnDevice):

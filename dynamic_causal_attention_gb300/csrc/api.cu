@@ -136,6 +136,24 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, int d) {
   return r == CUDA_SUCCESS;
 }
 
+// 3-D view [heads, rows, d] of bf16 rows at any distance, box of 128 rows of a head x
+// one swizzle chunk; rows outside read zeros.
+bool encode_heads(CUtensorMap* m, const void* base, int rows, int heads, int d, int64_t row_bytes,
+                  int64_t head_bytes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int swz = d >= 64 ? 128 : 64;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)head_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)(swz / 2), 128u, 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // 4-D view [n_pages, heads, page, d] of the codes of a cache layer, box of one
 // page's block of one head; a page number outside the pool reads zeros.
 bool encode_pages(CUtensorMap* m, const void* base, int d, int page, int heads, int n_pages,
@@ -156,7 +174,6 @@ bool encode_pages(CUtensorMap* m, const void* base, int d, int page, int heads, 
   return r == CUDA_SUCCESS;
 }
 
-namespace {
 // 2-D view [rows, d] of an fp32 tensor, box of 128 rows x 32 columns (128 B,
 // 128-byte swizzle): the staging layout of the backward's dQ reduction.
 bool encode_rows_f32(CUtensorMap* m, const void* base, uint64_t rows, int d) {
@@ -173,6 +190,7 @@ bool encode_rows_f32(CUtensorMap* m, const void* base, uint64_t rows, int d) {
   return r == CUDA_SUCCESS;
 }
 
+namespace {
 // ------------------------------------------------------------ workspace
 struct WsLayout {
   size_t status, a_tab, r_tab, row_tab, logZ, mode;

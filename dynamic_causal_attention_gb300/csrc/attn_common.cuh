@@ -45,6 +45,15 @@ struct TileGeom {
     const uint32_t a = tile_saddr + (uint32_t)kk * 16u * SWZ;
     return sdesc(a, (uint32_t)CHUNK_BYTES, 8u * SWZ, LAYOUT);
   }
+  // Rows valid .. 127 of a tile become zero (the swizzle moves bytes inside a row
+  // only); by one warp.
+  __device__ static __forceinline__ void zero_rows(uint32_t tile_saddr, int valid, int lane) {
+    const int units = (128 - valid) * SWZ / 16;  // of 16 bytes, in each chunk
+    for (int c = 0; c < NCHUNK; ++c)
+      for (int u = lane; u < units; u += 32)
+        st_shared_v4(tile_saddr + (uint32_t)(c * CHUNK_BYTES + valid * SWZ + 16 * u), 0u, 0u, 0u,
+                     0u);
+  }
 };
 
 // Square [128 x 128] bf16 tile written by the kernels (two 64-col chunks,

@@ -46,6 +46,22 @@ inline int static_group(int d_h, int B, bool transposed = false) {
   return g < B ? g : B;
 }
 
+// The same for sequences laid end to end: T is the length of the tables, and items
+// come from a plan that the preparing kernel makes on the device.
+struct PackedFwdParams : FwdParams {
+  const int* hdr;        // {tiles, groups of static forward items}
+  const int4* tiles;     // (row0, len, X, tile0), most steps first
+  const int2* groups;    // forward: (first record, records) that share X
+  int total;             // rows of lse and out_acc
+  int nt_max;            // tiles that row_vals has for each head
+  int64_t out_row, out_head;
+  // transposed: the frozen heads (as slots of the tables) by K/V head
+  int n_kv_st;
+  const float* row_vals; // [n_static, nt_max * 128]
+  uint8_t kv_list[kMaxHeads], kv_has_dyn[kMaxHeads], st_by_kv[kMaxHeads];
+  uint16_t st_begin[kMaxHeads], st_count[kMaxHeads];
+};
+
 struct FwdLaunch {
   // bf16 views [B*H*T, d_h] (Q) and [B*H_kv*T, d_h] (K, V); tm_v = dO
   // ([B*H*T, d_h]) when transposed
@@ -103,6 +119,15 @@ struct BwdParams {
   __nv_bfloat16* dV;
   int* status;
 };
+// The same for sequences laid end to end (lse2 and Dvec lie by tiles: [H, nt_max * 128],
+// dq_acc and dv_acc by rows: [H or H_kv, total, d_h]; pairs_per_group counts K/V heads).
+struct PackedBwdParams : BwdParams {
+  const int* hdr;      // {tiles, ...}
+  const int4* tiles;   // (row0, len, J, tile0), most query tiles first
+  int total, nt_max;
+  int64_t dk_row, dk_head, dv_row, dv_head;
+};
+
 struct BwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;
   CUtensorMap tm_dq;             // fp32 [B*H*T, d_h] view of dq_acc (d_h <= 64)
@@ -111,6 +136,20 @@ struct BwdLaunch {
   int num_sms;
 };
 cudaError_t launch_bwd_dynamic(const BwdLaunch& L, cudaStream_t s);
+
+struct PackedFwdLaunch {
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;  // 3-D views [heads, rows, d_h] (tm_o is not used)
+  PackedFwdParams p;
+  int d_h, num_sms;
+};
+cudaError_t launch_packed_fwd(const PackedFwdLaunch& L, bool transposed, cudaStream_t s);
+struct PackedBwdLaunch {
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;  // 3-D views [heads, rows, d_h]
+  CUtensorMap tm_dq;                    // fp32 [H * total, d_h] view of dq_acc
+  PackedBwdParams p;
+  int d_h, num_sms;
+};
+cudaError_t launch_packed_bwd(const PackedBwdLaunch& L, cudaStream_t s);
 
 // Static-head alpha/rho gradients.
 struct ParamGradParams {

@@ -50,6 +50,14 @@ void fill_fwd_params(FwdParams& p, const saf_attn_dims& d, const HeadSplit& hs,
 // 2-D view [rows, d] of a bf16 tensor, box of 128 rows x one swizzle chunk.
 bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, int d);
 
+// 3-D view [heads, rows, d] of bf16 rows at any distance, box of 128 rows of a head x
+// one swizzle chunk.
+bool encode_heads(CUtensorMap* m, const void* base, int rows, int heads, int d, int64_t row_bytes,
+                  int64_t head_bytes);
+
+// 2-D view [rows, d] of an fp32 tensor, box of 128 rows x 32 columns.
+bool encode_rows_f32(CUtensorMap* m, const void* base, uint64_t rows, int d);
+
 // 4-D view [n_pages, heads, page, d] of the codes of a cache layer, box of one
 // page's block of one head.
 bool encode_pages(CUtensorMap* m, const void* base, int d, int page, int heads, int n_pages,

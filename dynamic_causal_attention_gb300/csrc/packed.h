@@ -1,0 +1,64 @@
+// packed.h — the small kernels around the packed attention: the plan and the tables that
+// precede it, and the backward's row passes.
+#pragma once
+
+#include "attn_kernels.h"
+
+namespace saf {
+
+constexpr int kMaxPackedLen = 131072;             // longest sequence
+constexpr int kMaxPackedTiles = kMaxPackedLen / 128;
+
+// bf16 rows [total, heads, d] of which those of no sequence are cleared.
+struct ClearRows {
+  __nv_bfloat16* p;
+  int64_t row, head;
+  int heads;
+};
+
+struct PackedPrep {
+  int total, n_seqs, max_len, max_tiles;  // max_tiles = ceil(max_len / 128)
+  int group;                 // tiles of a static forward item
+  const int32_t* cu;         // [n_seqs + 1]
+  int* status;
+  int* hdr;                  // {tiles, static groups}
+  int4 *by_key, *by_query;   // records by falling X + 1 and by falling query tiles
+  int2* groups;
+  int4* seqs;                // [n_seqs] scratch
+  // tables of the frozen heads, T = 128 * max_tiles entries a head (see static_prep_kernel)
+  int T, T_pat, n_static;
+  const float *alpha, *rho;
+  float *a_tab, *r_tab, *row_tab, *logZ, *shift;
+  int* mode;
+  // rows of no sequence: cleared where `clear`
+  bool clear;
+  ClearRows rows[3];
+  int n_rows, d;
+  float* lse;                // or null
+  int H;
+  uint8_t static_heads[kMaxHeads];
+};
+cudaError_t launch_packed_prep(const PackedPrep& p, cudaStream_t s);
+
+struct PackedRows {
+  int nt_max, total, H, group_kv, d_h;
+  const int* hdr;
+  const int4* tiles;
+  const __nv_bfloat16 *out, *dout;
+  int64_t out_row, out_head, do_row, do_head;
+  const float* lse;          // [H, total]
+  float *Dvec, *lse2;        // [H, nt_max * 128]
+  float* row_vals;           // [n_static, nt_max * 128]
+  const int* mode;
+  const float* shift;
+  float* dq_acc;             // [H, total, d]
+  __nv_bfloat16 *dQ, *dK;
+  int64_t dq_row, dq_head, dk_row, dk_head;
+  float scale;
+  uint8_t static_slot[kMaxHeads];  // 255: dynamic
+  uint8_t kv_has_dyn[kMaxHeads];
+};
+cudaError_t launch_packed_pre(const PackedRows& p, cudaStream_t s);
+cudaError_t launch_packed_post(const PackedRows& p, cudaStream_t s);
+
+}  // namespace saf

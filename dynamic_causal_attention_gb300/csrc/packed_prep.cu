@@ -1,0 +1,386 @@
+// packed_prep.cu — what precedes and follows the packed attention's kernels.
+//
+// packed_prep_kernel, one launch ahead of the forward and of the backward:
+//   block 0      the plan: a record (first row of the sequence, its rows, tile X, the
+//                sequence's first tile) for every tile of 128 rows, sorted by falling X
+//                (steps of the forward) and by falling number of query tiles (steps of
+//                the backward).  A sequence of n tiles has one tile with every key
+//                1..n in either order, so with the sequences sorted by falling n those that have
+//                key k are the first cnt[k], and a record's place is start[k] + place
+//                of its sequence: one counting sort of the sequences gives both.
+//   then         the frozen heads' generator tables, 128 entries a block
+//   the last     rows of no sequence, cleared where asked
+// packed_pre / packed_post: the backward's row passes (D = rowsum(dO o O), -lse log2 e,
+// zeros of dQ's accumulator; dQ from it), by tiles and heads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "packed.h"
+#include "ptx.cuh"
+
+namespace saf {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMasked = -2.3e38f;              // below: as -inf
+constexpr float kMaxFactoredRange = 80.0f;       // as for batches of one length
+constexpr int kPrepThreads = 512, kPrepWarps = kPrepThreads / 32;
+constexpr int kClearBlocks = 64;
+
+struct PlanShared {
+  int hist[kMaxPackedTiles + 2];    // sequences of n tiles, then the next place of such a one
+  int cnt[kMaxPackedTiles + 2];     // sequences of at least k tiles
+  int start[kMaxPackedTiles + 2];   // records of keys above k
+  int gstart[kMaxPackedTiles + 2];  // groups of keys above k
+  int warp_max[kPrepWarps], warp_sum[kPrepWarps];
+  int end, tiles;
+};
+
+// Inclusive suffix sums of v[0 .. n) into out[i] = sum of v[j], j >= i (or j > i), by one warp.
+template <class F>
+__device__ int warp_suffix(int n, int* out, bool exclusive, F value) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int base = (n - 1) / 32 * 32; base >= 0; base -= 32) {
+    const int i = base + lane;
+    const int v = i < n ? value(i) : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int t = __shfl_down_sync(0xffffffffu, s, o);
+      if (lane + o < 32) s += t;
+    }
+    if (i < n) out[i] = carry + s - (exclusive ? v : 0);
+    carry += __shfl_sync(0xffffffffu, s, 0);
+  }
+  return carry;
+}
+
+__device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = p.n_seqs, m = p.max_tiles;
+  if (tid == 0) {
+    *p.status = 0;
+    sh.end = max(0, min(p.cu[0], p.total));
+    sh.tiles = 0;
+  }
+  for (int i = tid; i < m + 2; i += kPrepThreads) sh.hist[i] = 0;
+  __syncthreads();
+  // Ends of the sequences (never falling, whatever cu holds, so that no row is in two
+  // of them), their tiles, and the sum of the tiles before.
+  for (int b0 = 0; b0 < n; b0 += kPrepThreads) {
+    const int b = b0 + tid;
+    const int carry_end = sh.end, carry_tiles = sh.tiles;
+    int e = b < n ? max(0, min(p.cu[b + 1], p.total)) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int t = __shfl_up_sync(0xffffffffu, e, o);
+      if (lane >= o) e = max(e, t);
+    }
+    if (lane == 31) sh.warp_max[warp] = e;
+    __syncthreads();
+    int before = carry_end;
+    for (int w = 0; w < warp; ++w) before = max(before, sh.warp_max[w]);
+    e = max(e, before);
+    const int prev = __shfl_up_sync(0xffffffffu, e, 1);
+    const int a = lane > 0 ? prev : before;
+    const int len = b < n ? min(e - a, p.max_len) : 0;
+    const int nt = (len + 127) / 128;
+    int s = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += t;
+    }
+    if (lane == 31) sh.warp_sum[warp] = s;
+    __syncthreads();
+    int tile0 = carry_tiles + s - nt;
+    for (int w = 0; w < warp; ++w) tile0 += sh.warp_sum[w];
+    if (b < n) {
+      p.seqs[b] = make_int4(a, len, tile0, 0);
+      atomicAdd(&sh.hist[nt], 1);
+    }
+    __syncthreads();
+    if (tid == kPrepThreads - 1) {
+      sh.end = e;
+      sh.tiles = tile0 + nt;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    warp_suffix(m + 2, sh.cnt, false, [&](int i) { return sh.hist[i]; });
+    __syncwarp();
+    const int tiles = warp_suffix(m + 2, sh.start, true, [&](int i) { return i ? sh.cnt[i] : 0; });
+    const int groups = warp_suffix(m + 2, sh.gstart, true, [&](int i) {
+      return i ? (sh.cnt[i] + p.group - 1) / p.group : 0;
+    });
+    if (lane == 0) {
+      p.hdr[0] = tiles;
+      p.hdr[1] = groups;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i <= m; i += kPrepThreads) sh.hist[i] = sh.cnt[i + 1];
+  __syncthreads();
+  for (int b = warp; b < n; b += kPrepWarps) {
+    const int4 q = p.seqs[b];
+    const int nt = (q.y + 127) / 128;
+    int place = 0;
+    if (lane == 0 && nt > 0) place = atomicAdd(&sh.hist[nt], 1);
+    place = __shfl_sync(0xffffffffu, place, 0);
+    for (int X = lane; X < nt; X += 32) {
+      const int4 rec = make_int4(q.x, q.y, X, q.z);
+      const int kf = X + 1, kb = nt - X;
+      p.by_key[sh.start[kf] + place] = rec;
+      p.by_query[sh.start[kb] + place] = rec;
+      if (place % p.group == 0)
+        p.groups[sh.gstart[kf] + place / p.group] =
+            make_int2(sh.start[kf] + place, min(p.group, sh.cnt[kf] - place));
+    }
+  }
+}
+
+// Entry t of alpha or rho: -inf behind the longest sequence and for masks.
+__device__ __forceinline__ float entry(const float* v, int t, int n) {
+  const float x = t < n ? __ldg(v + t) : -INFINITY;
+  return x < kMasked ? -INFINITY : x;
+}
+
+// Entries row0 .. row0 + 127 of a frozen head's tables (the formulas of static_prep_kernel).
+__device__ void make_tables(const PackedPrep& p, int hs, int row0, float* red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int T = p.T, h = p.static_heads[hs], n = p.max_len;
+  const float* alpha = p.alpha + (size_t)h * p.T_pat;
+  const float* rho = p.rho + (size_t)h * p.T_pat;
+  // finite ranges of the whole head (every block agrees)
+  float amax = -INFINITY, amin = INFINITY, rmax = -INFINITY, rmin = INFINITY;
+#pragma unroll 4
+  for (int t = tid; t < n; t += kPrepThreads) {
+    const float a = entry(alpha, t, n), r = entry(rho, t, n);
+    if (isfinite(a)) { amax = fmaxf(amax, a); amin = fminf(amin, a); }
+    if (isfinite(r)) { rmax = fmaxf(rmax, r); rmin = fminf(rmin, r); }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    amin = fminf(amin, __shfl_xor_sync(0xffffffffu, amin, o));
+    rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
+    rmin = fminf(rmin, __shfl_xor_sync(0xffffffffu, rmin, o));
+  }
+  if (lane == 0) {
+    red[warp] = amax;
+    red[kPrepWarps + warp] = amin;
+    red[2 * kPrepWarps + warp] = rmax;
+    red[3 * kPrepWarps + warp] = rmin;
+  }
+  __syncthreads();
+  for (int w = 0; w < kPrepWarps; ++w) {
+    amax = fmaxf(amax, red[w]);
+    amin = fminf(amin, red[kPrepWarps + w]);
+    rmax = fmaxf(rmax, red[2 * kPrepWarps + w]);
+    rmin = fminf(rmin, red[3 * kPrepWarps + w]);
+  }
+  const bool none = !(amax > -INFINITY) || !(rmax > -INFINITY);
+  const bool exact = !none && (amax - amin) + (rmax - rmin) > kMaxFactoredRange;
+  float* a_tab = p.a_tab + (size_t)hs * T;
+  float* r_tab = p.r_tab + (size_t)hs * (T + 128);
+  if (row0 == 0 && tid == 0) {
+    p.mode[hs] = exact ? 1 : 0;
+    p.shift[hs] = exact || none ? 0.f : amax + rmax;
+  }
+  if (row0 == 0 && tid < 128) r_tab[tid < 127 ? tid : T + 127] = exact ? -INFINITY : 0.f;
+  if (tid < 128) {
+    const int t = row0 + tid;
+    const float a = entry(alpha, t, n), r = entry(rho, t, n);
+    a_tab[t] = exact ? a * kLog2e : none ? 0.f : expf(a - amax);
+    r_tab[127 + t] = exact ? r * kLog2e : none ? 0.f : expf(r - rmax);
+  }
+  if (!exact) return;
+  // log Z of each row: an online log-sum-exp per lane, merged in a fixed order
+  for (int k0 = 0; k0 < 128 / kPrepWarps; ++k0) {
+    const int i = row0 + warp * (128 / kPrepWarps) + k0;
+    float mx = -INFINITY, sm = 0.f;
+    for (int k = lane; k <= i && k < n; k += 32) {
+      const float t = entry(alpha, k, n) + entry(rho, i - k, n);
+      if (t > mx) {
+        sm = sm * expf(mx - t) + 1.f;
+        mx = t;
+      } else if (t > -INFINITY) {
+        sm += expf(t - mx);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, mx, o);
+      const float so = __shfl_xor_sync(0xffffffffu, sm, o);
+      const float mn = fmaxf(mx, mo);
+      if (mn > -INFINITY) {
+        sm = sm * expf(mx - mn) + so * expf(mo - mn);
+        mx = mn;
+      }
+    }
+    if (lane == 0) {
+      const float lz = mx > -INFINITY ? mx + logf(sm) : -INFINITY;
+      p.logZ[(size_t)hs * T + i] = lz;
+      p.row_tab[(size_t)hs * T + i] = mx > -INFINITY ? -lz * kLog2e : -INFINITY;
+    }
+  }
+}
+
+__device__ void clear_rows(const PackedPrep& p, int block) {
+  const int first = max(0, min(p.cu[0], p.total));
+  const int last = max(first, min(p.cu[p.n_seqs], p.total));
+  const long long rest = first + (p.total - last);
+  const long long t0 = (long long)block * kPrepThreads + threadIdx.x;
+  const long long step = (long long)kClearBlocks * kPrepThreads;
+  if (rest == 0) return;
+  for (int i = 0; i < p.n_rows; ++i) {
+    const ClearRows& x = p.rows[i];
+    const int units = p.d / 8;
+    for (long long j = t0; j < rest * x.heads * units; j += step) {
+      const int u = (int)(j % units);
+      const long long hr = j / units;
+      const int h = (int)(hr % x.heads);
+      const long long k = hr / x.heads;
+      const long long row = k < first ? k : last + (k - first);
+      *reinterpret_cast<uint4*>(x.p + row * x.row + (int64_t)h * x.head + 8 * u) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if (p.lse)
+    for (long long j = t0; j < rest * p.H; j += step) {
+      const long long h = j / rest, k = j - h * rest;
+      p.lse[h * p.total + (k < first ? k : last + (k - first))] = -INFINITY;
+    }
+}
+
+// Grid: 1 + tables * n_static + (clear ? kClearBlocks : 0).
+__global__ void __launch_bounds__(kPrepThreads)
+    packed_prep_kernel(const __grid_constant__ PackedPrep p) {
+  __shared__ PlanShared plan;
+  const int chunks = p.max_tiles;
+  const int b = (int)blockIdx.x - 1;
+  if (b < 0) make_plan(p, plan);
+  else if (b < chunks * p.n_static)
+    make_tables(p, b / chunks, (b % chunks) * 128, reinterpret_cast<float*>(plan.hist));
+  else clear_rows(p, b - chunks * p.n_static);
+}
+
+// A tile's rows under one head: D/8 lanes a row, 8 elements each.
+template <int D>
+__global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__ PackedRows p) {
+  constexpr int LPR = D / 8;
+  if ((int)blockIdx.x >= p.hdr[0]) return;
+  const int4 t = p.tiles[blockIdx.x];
+  const int h = blockIdx.y, hs = p.static_slot[h], kv = h / p.group_kv;
+  const int tile = t.w + t.z, valid = min(128, t.y - t.z * 128);
+  const bool zero_k = h == kv * p.group_kv && !p.kv_has_dyn[kv];
+  const int sub = threadIdx.x % LPR;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+  for (int r = threadIdx.x / LPR; r < 128; r += 256 / LPR) {
+    const int64_t row = t.x + t.z * 128 + r;
+    const bool mine = r < valid;
+    if (zero_k && mine)
+      *reinterpret_cast<uint4*>(p.dK + row * p.dk_row + (int64_t)kv * p.dk_head + sub * 8) = zero;
+    if (hs != 255) {
+      if (mine)
+        *reinterpret_cast<uint4*>(p.dQ + row * p.dq_row + (int64_t)h * p.dq_head + sub * 8) = zero;
+      if (sub == 0) {
+        // the weight of a query's row: 1 / Z', or -log2 Z (exact); none behind the end
+        const float l = mine ? p.lse[(int64_t)h * p.total + row] : -INFINITY;
+        const bool some = l > -INFINITY;
+        const float v = p.mode[hs] ? (some ? -l * kLog2e : -INFINITY)
+                                   : (some ? expf(p.shift[hs] - l) : 0.f);
+        p.row_vals[((size_t)hs * p.nt_max + tile) * 128 + r] = v;
+      }
+      continue;
+    }
+    float acc = 0.f;
+    if (mine) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p.out + row * p.out_row +
+                                                      (int64_t)h * p.out_head + sub * 8);
+      const uint4 b = *reinterpret_cast<const uint4*>(p.dout + row * p.do_row +
+                                                      (int64_t)h * p.do_head + sub * 8);
+      const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
+      const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = __bfloat1622float2(a2[k]), y = __bfloat1622float2(b2[k]);
+        acc = fmaf(x.x, y.x, acc);
+        acc = fmaf(x.y, y.y, acc);
+      }
+      float4* z = reinterpret_cast<float4*>(p.dq_acc + ((int64_t)h * p.total + row) * D + sub * 8);
+      z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (sub == 0) {
+      const size_t at = ((size_t)h * p.nt_max + tile) * 128 + r;
+      p.Dvec[at] = mine ? -acc : 0.f;
+      p.lse2[at] = mine ? -p.lse[(int64_t)h * p.total + row] * kLog2e : -INFINITY;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) packed_post_kernel(const __grid_constant__ PackedRows p) {
+  constexpr int LPR = D / 8;
+  const int h = blockIdx.y;
+  if ((int)blockIdx.x >= p.hdr[0] || p.static_slot[h] != 255) return;
+  const int4 t = p.tiles[blockIdx.x];
+  const int valid = min(128, t.y - t.z * 128), sub = threadIdx.x % LPR;
+  for (int r = threadIdx.x / LPR; r < valid; r += 256 / LPR) {
+    const int64_t row = t.x + t.z * 128 + r;
+    const float* src = p.dq_acc + ((int64_t)h * p.total + row) * D + sub * 8;
+    const float4 a = *reinterpret_cast<const float4*>(src);
+    const float4 b = *reinterpret_cast<const float4*>(src + 4);
+    uint4 q;
+    q.x = pack_bf16x2(a.x * p.scale, a.y * p.scale);
+    q.y = pack_bf16x2(a.z * p.scale, a.w * p.scale);
+    q.z = pack_bf16x2(b.x * p.scale, b.y * p.scale);
+    q.w = pack_bf16x2(b.z * p.scale, b.w * p.scale);
+    *reinterpret_cast<uint4*>(p.dQ + row * p.dq_row + (int64_t)h * p.dq_head + sub * 8) = q;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_packed_prep(const PackedPrep& p, cudaStream_t s) {
+  const int grid = 1 + p.max_tiles * p.n_static + (p.clear ? kClearBlocks : 0);
+  trace_begin(s);
+  packed_prep_kernel<<<grid, kPrepThreads, 0, s>>>(p);
+  trace_end(s, "packed_prep");
+  return cudaGetLastError();
+}
+
+cudaError_t launch_packed_pre(const PackedRows& p, cudaStream_t s) {
+  const dim3 grid(p.nt_max, p.H);
+  trace_begin(s);
+  switch (p.d_h) {
+    case 32: packed_pre_kernel<32><<<grid, 256, 0, s>>>(p); break;
+    case 64: packed_pre_kernel<64><<<grid, 256, 0, s>>>(p); break;
+    case 128: packed_pre_kernel<128><<<grid, 256, 0, s>>>(p); break;
+    default: return cudaErrorInvalidValue;
+  }
+  trace_end(s, "packed_pre");
+  return cudaGetLastError();
+}
+
+cudaError_t launch_packed_post(const PackedRows& p, cudaStream_t s) {
+  const dim3 grid(p.nt_max, p.H);
+  trace_begin(s);
+  switch (p.d_h) {
+    case 32: packed_post_kernel<32><<<grid, 256, 0, s>>>(p); break;
+    case 64: packed_post_kernel<64><<<grid, 256, 0, s>>>(p); break;
+    case 128: packed_post_kernel<128><<<grid, 256, 0, s>>>(p); break;
+    default: return cudaErrorInvalidValue;
+  }
+  trace_end(s, "packed_post");
+  return cudaGetLastError();
+}
+
+}  // namespace saf

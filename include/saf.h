@@ -513,6 +513,67 @@ SAF_API saf_status saf_rotary(const saf_rotary_dims* dims, const saf_rows* q, co
                       void* stream);
 
 /* ------------------------------------------------------------------------
+ * The hybrid layer on sequences of different lengths laid end to end: prompts that
+ * arrive together, or documents packed into a training batch, without padding. */
+typedef struct saf_packed_dims {
+  int total;    /* rows of every tensor, (total + 256) * H < 2^31               */
+  int n_seqs;   /* sequences, up to 2^20                                        */
+  int max_len;  /* no sequence has more rows, up to 131072                      */
+  int H, H_kv;  /* query heads 1..256, K/V heads (a divisor of H)               */
+  int d_h;      /* 32, 64 or 128                                                */
+  int T_pat;    /* columns of alpha and rho, >= max_len where heads are frozen  */
+} saf_packed_dims;
+
+/* Bytes of device workspace for the forward, or with backward != 0 for both; 0 for
+ * dims that they do not take.  Fewer rows, sequences or a smaller max_len never
+ * need more. */
+SAF_API size_t saf_packed_attn_workspace_size(const saf_packed_dims* dims, int backward);
+
+/* Forward.  Rows cu_seqlens[s] <= i < cu_seqlens[s + 1] are sequence s; row i stands
+ * at position i - cu_seqlens[s] and sees the rows of its sequence up to itself:
+ * softmax attention under a dynamic head, weights exp(alpha(j) + rho(i - j)) / Z(i) by
+ * positions under a frozen one, as in saf_hybrid_attn_fwd.
+ *
+ *   Q, out      [total, H, d_h], K, V [total, H_kv, d_h] bf16 as saf_rows (seq is not
+ *               looked at): 16-byte aligned, strides multiples of 8 and >= d_h.  Q of
+ *               frozen heads, and K of K/V heads that serve no dynamic head, are not
+ *               read.
+ *   cu_seqlens  device [n_seqs + 1] int32, not falling, within 0..total.  Empty
+ *               sequences are allowed.  Rows before the first and behind the last
+ *               sequence, and rows of a sequence from max_len on, are not worked on; they
+ *               may hold anything.
+ *   alpha, rho  [H, T_pat] fp32, rows of frozen heads; values below -2.3e38 count as
+ *               -inf (no weight).  NULL without frozen heads.
+ *   lse         [H, total] fp32 or NULL (4-byte aligned): log sum_j exp(.); -inf where
+ *               a frozen head's row has no weight, whose out is 0.
+ *   flags       SAF_CLEAR_REST: rows of no sequence become 0, their lse -inf.
+ *   workspace   256-byte aligned; saf_get_device_status reads its status.
+ * Both products have fp32 sums; the weights are rounded to bf16 for the second (as the
+ * rows that they weigh).  An infinity or NaN in a row of V reaches rows of its own sequence
+ * only: those after it, and those up to 127 rows before it.  The same call gives the
+ * same bits. */
+SAF_API saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_rows* Q,
+                               const saf_rows* K, const saf_rows* V, const int32_t* cu_seqlens,
+                               const float* alpha, const float* rho,
+                               const uint8_t* head_is_static, const saf_rows* out, float* lse,
+                               unsigned flags, void* workspace, size_t ws_bytes, void* stream);
+
+/* Backward, for the gradient dout of out.  out and lse are the forward's (out is not
+ * looked at without dynamic heads); dQ [total, H, d_h], dK and dV [total, H_kv, d_h]
+ * are overwritten in the rows of the sequences: dK and dV sum over the query heads of
+ * their group, dQ of frozen heads and dK that serve frozen heads only are 0.  alpha and
+ * rho are constants here (saf_hybrid_attn_bwd has their gradients).  dQ is summed in
+ * fp32 in the order in which its parts arrive, so its last bit may differ from call to
+ * call; dK and dV do not. */
+SAF_API saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q,
+                               const saf_rows* K, const saf_rows* V, const saf_rows* out,
+                               const float* lse, const saf_rows* dout,
+                               const int32_t* cu_seqlens, const float* alpha, const float* rho,
+                               const uint8_t* head_is_static, const saf_rows* dQ,
+                               const saf_rows* dK, const saf_rows* dV, unsigned flags,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Beam search: which tokens follow, and which slots go on (saf_cache_fork takes
  * the parents that come out). */
 typedef struct saf_beam_dims {

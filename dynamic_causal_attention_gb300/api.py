@@ -436,19 +436,19 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, stretch: float = 
     """
     if rot_dim < 2 or rot_dim % 2 or base <= 0 or stretch <= 0 or trained < 1 or fast <= slow:
         raise B.SafError(B.SAF_ERR_INVALID_ARG, "rotary_frequencies")
+    if kind not in ("linear", "base", "ramp"):
+        raise B.SafError(B.SAF_ERR_INVALID_ARG, f"rotary_frequencies: kind {kind!r}")
     if kind == "base" and stretch != 1.0:
         if rot_dim < 4:
             raise B.SafError(B.SAF_ERR_INVALID_ARG, "rotary_frequencies: one pair has no base")
         base = base * stretch ** (rot_dim / (rot_dim - 2))
     f = base ** (-2.0 * np.arange(rot_dim // 2, dtype=np.float64) / rot_dim)
+    if kind == "base" or stretch == 1.0:
+        return f
     if kind == "linear":
         return f / stretch
-    if kind == "ramp":
-        keep = np.clip((trained * f / (2.0 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
-        return f * keep + f / stretch * (1.0 - keep)
-    if kind != "base":
-        raise B.SafError(B.SAF_ERR_INVALID_ARG, f"rotary_frequencies: kind {kind!r}")
-    return f
+    keep = np.clip((trained * f / (2.0 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
+    return np.where(keep == 1.0, f, f * keep + f / stretch * (1.0 - keep))
 
 
 class Rotary(_OnDevice):

@@ -6,20 +6,21 @@
 // offers of a group become its slots; equal scores go to the lower b * vocab + v.
 //
 // The logits are read once, and that is what bounds the call.  A row is cut into
-// blocks' parts; a block holds its part in registers, so that every load is in flight
-// at once, the maximum is known before the first exponential, and the best few are
-// found by a threshold: the K-th largest of the threads' maxima has at least K
-// elements at or above it, and few more.  A block leaves its sum and its K best; the
-// last block of a row joins the row's parts, the last row of a group chooses
-// (a counter each, which its last block sets back to zero for the next call).
+// blocks' parts; a block goes through its part in tiles, the next one's loads in
+// flight while a tile is summed.  The K-th largest of the threads' maxima of the first
+// tile is a threshold that at least K elements reach, and of later tiles few more; they
+// are listed, and the best K of the list are the part's.  The last block of a row joins
+// the row's parts, the last row of a group chooses (a counter each, which its last
+// block sets back to zero for the next call).
 //
 // Which of two offers is better must not hang on the rounding of a sum of 10^5
-// exponentials.  So an exponential is formed in base two against the block's
+// exponentials.  So an exponential is formed in base two against the thread's
 // exponent E = ceil(max x log2 e): with n = round(x log2 e) and the rest f, both
 // from x itself (no difference to the maximum is rounded), 2^(n - E) (1 + f q(f)),
-// q of degree 5 fitted by the author to 2e-9; a thread's sum is rounded to 2^-44 and
-// added to the others' in integers, so the sum does not depend on the order, and parts
-// are joined by exact powers of two in fp64.  Scores are compared in fp64.
+// q of degree 5 fitted by the author to 2e-9; a thread's sum is rounded to 2^-44 of the
+// block's scale and added to the others' in integers, so the sum does not depend on the
+// order, and parts are joined by exact powers of two in fp64.  Scores are compared in
+// fp64.  (Logits beyond 2^20 take a second pass against their maximum.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -71,93 +72,91 @@ __device__ __forceinline__ bool dead(const BeamParams& p, int slot) {
   return !(s >= kMasked && s < INFINITY);
 }
 
-// The row's elements that a thread holds: NV vectors of 16 bytes and one more (the
-// row's unaligned ends).
-template <typename T, int NV>
-struct Held {
-  static constexpr int PER = 16 / (int)sizeof(T);
-  uint4 vec[NV];
-  float extra;
-  __device__ __forceinline__ float get(int k, int e) const {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&vec[k]);
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
-    else return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-  }
-};
+__device__ __forceinline__ Best best_of(unsigned long long key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return Best{__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o), (int)~(uint32_t)key};
+}
+
+// How many of keys[0 .. n) are above `key`.
+__device__ __forceinline__ int count_above(const unsigned long long* keys, int n,
+                                           unsigned long long key) {
+  int above = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; ++j) above += keys[j] > key;
+  return above;
+}
 
 // Joins a row's parts and writes its log sum and its K best; every thread of the block.
-template <typename T>
-__device__ void join_row(const BeamParams& p, int slot, double* sh_d, unsigned long long* sh_k) {
-  const int S = p.splits, K = p.beams, tid = threadIdx.x;
-  const Part* parts = reinterpret_cast<const Part*>(p.parts + (size_t)slot * S * p.part_bytes);
-  auto part = [&](int s) -> const Part& {
-    return *reinterpret_cast<const Part*>(reinterpret_cast<const uint8_t*>(parts) +
-                                          (size_t)s * p.part_bytes);
-  };
-  double* row_lse = p.row_lse + slot;
-  Best* row_best = reinterpret_cast<Best*>(p.row_best) + (size_t)slot * K;
-  int* row_n = p.row_n + slot;
-  // the largest element, and the part that holds it: its base and exponent are the sum's
-  float top = -INFINITY;
-  int at = 0;
-  for (int s = 0; s < S; ++s) {
-    const float t = __ldcg(&part(s).top);
-    if (t > top) {
-      top = t;
-      at = s;
+__device__ void join_row(const BeamParams& p, int slot, unsigned long long* keys) {
+  const int S = p.splits, K = p.beams, tid = threadIdx.x, lane = tid & 31, n = S * K;
+  const uint8_t* parts = p.parts + (size_t)slot * S * p.part_bytes;
+  auto part = [&](int s) { return reinterpret_cast<const Part*>(parts + (size_t)s * p.part_bytes); };
+  for (int i = tid; i < n; i += kThreads) {
+    const int s = i / K, j = i - s * K;
+    const int2 x = __ldcg(reinterpret_cast<const int2*>(part(s) + 1) + j);
+    keys[i] = j < __ldcg(&part(s)->n) ? key_of(__int_as_float(x.x), x.y) : 0;
+  }
+  if (tid >= kThreads - 32) {
+    // the largest element, and the part that holds it: its base and exponent are the sum's
+    float top = -INFINITY;
+    int at = 0;
+    for (int s = lane; s < S; s += 32) {
+      const float t = __ldcg(&part(s)->top);
+      if (t > top) {
+        top = t;
+        at = s;
+      }
     }
-  }
-  if (!(top > -INFINITY)) {
-    if (tid == 0) *row_n = 0;
-    return;
-  }
-  const float base = __ldcg(&part(at).base);
-  const int e = __ldcg(&part(at).e);
-  double sum = 0.0;
-  if (tid < 32) {
-    for (int s = tid; s < S; s += 32) {
-      const Part& q = part(s);
-      if (!(__ldcg(&q.top) > -INFINITY)) continue;
-      const double x = (double)__ldcg(&q.sum) * (1.0 / kUnit);
-      const float b = __ldcg(&q.base);
-      const int de = __ldcg(&q.e) - (b == base ? e : 0);
-      // parts of another base: one of them holds logits beyond 2^20
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, top, o);
+      const int a = __shfl_xor_sync(0xffffffffu, at, o);
+      if (t > top || (t == top && a < at)) {
+        top = t;
+        at = a;
+      }
+    }
+    const float base = __ldcg(&part(at)->base);
+    const int e = __ldcg(&part(at)->e);
+    double sum = 0.0;
+    for (int s = lane; s < S; s += 32) {
+      const Part* q = part(s);
+      const float b = __ldcg(&q->base);
+      const double x = (double)__ldcg(&q->sum) * (1.0 / kUnit);
+      const int de = __ldcg(&q->e) - e;
+      if (!(__ldcg(&q->top) > -INFINITY)) continue;
       if (b == base) {
         if (de > -1000) sum += x * pow2(de);
-      } else {
-        const double d = ((double)b - (double)base) + (double)(de - e) * 0.6931471805599453;
+      } else {  // one of the two holds logits beyond 2^20
+        const double d = ((double)b - (double)base) + (double)de * 0.6931471805599453;
         if (d > -700.0) sum += x * exp(d);
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (tid == 0) *row_lse = (double)base + ((double)e * 0.6931471805599453 + log(sum));
-  }
-  // the K best of the parts' K best: each entry counts those above it
-  const int n = S * K;
-  for (int i = tid; i < n; i += kThreads) {
-    const int s = i / K, j = i - s * K;
-    const Best* list = reinterpret_cast<const Best*>(&part(s) + 1);
-    unsigned long long key = 0;
-    if (j < __ldcg(&part(s).n)) key = key_of(__ldcg(&list[j].x), __ldcg(&list[j].v));
-    sh_k[i] = key;
+    if (lane == 0)
+      p.row_lse[slot] = top > -INFINITY
+                            ? (double)base + ((double)e * 0.6931471805599453 + log(sum))
+                            : 0.0;
   }
   __syncthreads();
-  int valid = 0;
-  for (int s = 0; s < S; ++s) valid += __ldcg(&part(s).n);
+  Best* row_best = reinterpret_cast<Best*>(p.row_best) + (size_t)slot * K;
+  int mine = 0;
   for (int i = tid; i < n; i += kThreads) {
-    const unsigned long long key = sh_k[i];
+    const unsigned long long key = keys[i];
     if (key == 0) continue;
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += sh_k[j] > key;
-    if (above < K) {
-      const uint32_t o = (uint32_t)(key >> 32);
-      row_best[above] = Best{__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o),
-                             (int)~(uint32_t)key};
-    }
+    ++mine;
+    const int above = count_above(keys, n, key);
+    if (above < K) row_best[above] = best_of(key);
   }
-  if (tid == 0) *row_n = min(valid, K);
-  (void)sh_d;
+  const int valid = __syncthreads_count(mine > 0) >= K ? K : -1;
+  if (valid == K) {
+    if (tid == 0) p.row_n[slot] = K;
+  } else if (tid == 0) {
+    int c = 0;
+    for (int i = 0; i < n; ++i) c += keys[i] != 0;
+    p.row_n[slot] = min(c, K);
+  }
 }
 
 // Chooses a group's new slots; every thread of the block.
@@ -195,6 +194,7 @@ __device__ void choose(const BeamParams& p, int group, uint8_t* scratch) {
     if (key == 0) continue;
     const int f = flat[i];
     int above = 0;
+#pragma unroll 4
     for (int j = 0; j < K * K; ++j) {
       const unsigned long long other = score[j];
       above += other > key || (other == key && flat[j] < f);
@@ -220,25 +220,25 @@ __device__ void choose(const BeamParams& p, int group, uint8_t* scratch) {
       if (p.finished_out) p.finished_out[slot0 + i] = 0;
     }
   if (p.history_out) {
-    const int n = max(0, min(*p.n_tokens, p.max_tokens));
-    for (int b = 0; b < K; ++b) {
-      const int from = chosen[b];
-      int32_t* to = p.history_out + (size_t)(slot0 + b) * p.max_tokens;
-      const int32_t* src = p.history + (size_t)max(from, 0) * p.max_tokens;
-      for (int c = tid; c < n; c += kThreads) to[c] = from >= 0 ? src[c] : -1;
-      if (tid == 0 && n < p.max_tokens) to[n] = from >= 0 ? token_of[b] : -1;
+    const int n = max(0, min(*p.n_tokens, p.max_tokens)), cols = min(n + 1, p.max_tokens);
+#pragma unroll 4
+    for (int i = tid; i < K * cols; i += kThreads) {
+      const int b = i / cols, c = i - b * cols, from = chosen[b];
+      int v = -1;
+      if (from >= 0)
+        v = c < n ? __ldg(p.history + (size_t)from * p.max_tokens + c) : token_of[b];
+      p.history_out[(size_t)(slot0 + b) * p.max_tokens + c] = v;
     }
   }
 }
 
-// Grid: slots * splits blocks.  Dynamic shared memory holds what joining and choosing
-// need (the lists of a block lie in it before).
+// Grid: slots * splits blocks.  A thread takes NV vectors of 16 bytes of every tile.  Dynamic
+// shared memory holds what joining and choosing need.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ BeamParams p) {
-  using H = Held<T, NV>;
-  constexpr int PER = H::PER;
+__global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant__ BeamParams p) {
+  constexpr int PER = 16 / (int)sizeof(T);  // elements of a vector
   extern __shared__ __align__(16) uint8_t scratch[];
-  __shared__ float tops[kThreads];       // the best K maxima of each warp
+  __shared__ __align__(16) float tops[kThreads];  // the best K maxima of each warp
   __shared__ unsigned long long sums[kWarps];
   __shared__ unsigned long long list[kList];
   __shared__ float sh_top[kWarps];
@@ -256,49 +256,62 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
     const int nvec = (p.vocab - head) / PER, tail = p.vocab - head - nvec * PER;
     const uint4* vecs = reinterpret_cast<const uint4*>(row + head);
     const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-    H x;
-    int v_extra = 0;
-    const int v0 = split * (kThreads * NV) + tid;
+    const int first = split * p.tiles * (kThreads * NV);
+    const int end = min(nvec, first + p.tiles * (kThreads * NV));
+    uint4 x[NV];
+    auto load = [&](uint4 (&to)[NV], int tile) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = v0 + k * kThreads;
-      x.vec[k] = v < nvec ? __ldcs(vecs + v) : make_uint4(none, none, none, none);
-    }
-    x.extra = -INFINITY;
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + (tile * NV + k) * kThreads + tid;
+        to[k] = v < end ? __ldcs(vecs + v) : make_uint4(none, none, none, none);
+      }
+    };
+    load(x, 0);
+    auto get = [&](int k, int e) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(&x[k])[sizeof(T) == 4 ? e : e >> 1];
+      if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+      else return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+    };
+    // the row's unaligned ends, an element a thread of its first part
+    float extra = -INFINITY;
+    int v_extra = 0;
     if (split == 0 && tid < head + tail) {
       v_extra = tid < head ? tid : p.vocab - tail + (tid - head);
-      x.extra = (float)row[v_extra];
+      extra = (float)row[v_extra];
+      if (!(extra < INFINITY)) extra = -INFINITY;
     }
     if (tid == 0) n_list = 0;
-    // the maximum (NaN is passed over); +inf counts as masked, found and cleared here
-    auto thread_top = [&]() {
-      float m = x.extra;
+    // The maximum of the tile: NaN is passed over, +inf (which counts as masked) cleared.
+    auto tile_top = [&]() {
+      float m = -INFINITY;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) m = fmax3(m, x.get(k, e), x.get(k, e + 1));
+        for (int e = 0; e < PER; e += 2) m = fmax3(m, get(k, e), get(k, e + 1));
       return m;
     };
-    if (!(x.extra < INFINITY)) x.extra = -INFINITY;
-    float m = thread_top();
-    if (!(m < INFINITY)) {  // +inf (a NaN would have to be all that there is)
+    auto clean_top = [&]() {
+      float m = tile_top();
+      if (!(m < INFINITY)) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x.vec[k]);
+        for (int k = 0; k < NV; ++k) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(T) == 4) {
-            if (!(__uint_as_float(w[i]) < INFINITY)) w[i] = 0xff800000u;
-          } else {
-            if (!(__uint_as_float(w[i] << 16) < INFINITY)) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
-            if (!(__uint_as_float(w[i] & 0xffff0000u) < INFINITY))
-              w[i] = (w[i] & 0xffffu) | 0xff800000u;
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+              if (!(__uint_as_float(w[i]) < INFINITY)) w[i] = 0xff800000u;
+            } else {
+              if (!(__uint_as_float(w[i] << 16) < INFINITY)) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+              if (!(__uint_as_float(w[i] & 0xffff0000u) < INFINITY))
+                w[i] = (w[i] & 0xffffu) | 0xff800000u;
+            }
           }
         }
+        m = tile_top();
       }
-      m = thread_top();
-    }
-    if (!(m >= kMasked)) m = -INFINITY;
+      return m >= kMasked ? m : -INFINITY;
+    };
+    float m = fmaxf(clean_top(), extra >= kMasked ? extra : -INFINITY);
     // the warp's maxima, sorted downwards (bitonic)
     float srt = m;
 #pragma unroll
@@ -310,59 +323,70 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
         srt = (up == low) ? fminf(srt, o) : fmaxf(srt, o);
       }
     if (lane < K) tops[warp * K + lane] = srt;
-    if (lane == 0) sh_top[warp] = srt;
     __syncthreads();
-    float top = sh_top[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh_top[w]);
     // the K-th largest of the threads' maxima: at least K elements are not below it
     float floor_k = -INFINITY;
-    {
+    if (warp * 32 < kWarps * K) {
       const float mine = tid < kWarps * K ? tops[tid] : -INFINITY;
-      int above = 0, ties = 0;
-      if (mine > -INFINITY)
-        for (int j = 0; j < kWarps * K; ++j) {
-          above += tops[j] > mine;
-          ties += tops[j] == mine;
-        }
-      if (mine > -INFINITY && above < K && above + ties >= K) floor_k = mine;
+      int above = 0, not_below = 0;
+#pragma unroll 4
+      for (int j = 0; j < kWarps * K / 4; ++j) {
+        const float4 t = reinterpret_cast<const float4*>(tops)[j];
+        above += (t.x > mine) + (t.y > mine) + (t.z > mine) + (t.w > mine);
+        not_below += (t.x >= mine) + (t.y >= mine) + (t.z >= mine) + (t.w >= mine);
+      }
+      if (mine > -INFINITY && above < K && not_below >= K) floor_k = mine;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         floor_k = fmaxf(floor_k, __shfl_xor_sync(0xffffffffu, floor_k, o));
-      __syncthreads();
-      if (lane == 0) sh_top[warp] = floor_k;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) floor_k = fmaxf(floor_k, sh_top[w]);
     }
+    if (lane == 0) sh_top[warp] = floor_k;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) floor_k = fmaxf(floor_k, sh_top[w]);
     floor_k = fmaxf(floor_k, kMasked);  // fewer than K maxima: every element that counts
 
-    // the sum of exponentials
-    unsigned long long fixed = 0;
-    const float base = fabsf(top) <= kPlain ? 0.f : top;
-    const int e_top = (int)ceilf((top - base) * kLog2e);
-    if (top > -INFINITY) {
-      const float low = (top - base) - 80.f;  // exp of less adds nothing that counts
-      const uint64_t l2 = f2_pack(kLog2e, kLog2e), ll2 = f2_pack(kLog2eLo, kLog2eLo);
-      const uint64_t magic = f2_pack(12582912.f, 12582912.f);  // 1.5 * 2^23: rounds to integers
-      const uint64_t nmagic = f2_pack(-12582912.f, -12582912.f);
-      const uint64_t c6 = f2_pack(0.00015353362f, 0.00015353362f);
-      const uint64_t c5 = f2_pack(0.0013398874f, 0.0013398874f);
-      const uint64_t c4 = f2_pack(0.009618437f, 0.009618437f);
-      const uint64_t c3 = f2_pack(0.055503324f, 0.055503324f);
-      const uint64_t c2 = f2_pack(0.24022648f, 0.24022648f);
-      const uint64_t c1 = f2_pack(0.6931472f, 0.6931472f);
-      const uint64_t one = f2_pack(1.f, 1.f), minus1 = f2_pack(-1.f, -1.f);
-      const uint64_t nbase = f2_pack(-base, -base);
-      const int shift = 0x4b400000 + e_top;  // the magic number's bits, and E
+    // The sum of exponentials, 2^e times `sum`, and the elements that reach the threshold.
+    // Logits below -2^20 are taken as -2^20: that counts only where the part has no
+    // larger ones, and then the second pass below does.
+    float top = -INFINITY, sum = 0.f;
+    int e_run = (int)(-kPlain * kLog2e);
+    const uint64_t l2 = f2_pack(kLog2e, kLog2e), ll2 = f2_pack(kLog2eLo, kLog2eLo);
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f);  // 1.5 * 2^23: rounds to integers
+    const uint64_t nmagic = f2_pack(-12582912.f, -12582912.f);
+    const uint64_t c6 = f2_pack(0.00015353362f, 0.00015353362f);
+    const uint64_t c5 = f2_pack(0.0013398874f, 0.0013398874f);
+    const uint64_t c4 = f2_pack(0.009618437f, 0.009618437f);
+    const uint64_t c3 = f2_pack(0.055503324f, 0.055503324f);
+    const uint64_t c2 = f2_pack(0.24022648f, 0.24022648f);
+    const uint64_t c1 = f2_pack(0.6931472f, 0.6931472f);
+    const uint64_t one = f2_pack(1.f, 1.f);
+    auto offer = [&](float v, int at) {
+      if (v >= floor_k) {
+        const int i = atomicAdd(&n_list, 1);
+        if (i < kList) list[i] = key_of(v, at);
+      }
+    };
+    for (int tile = 0; tile < p.tiles; ++tile) {
+      uint4 next[NV];
+      if (tile + 1 < p.tiles) load(next, tile + 1);
+      if (tile > 0) m = clean_top();
+      if (m > top) {
+        top = m;
+        const int e = (int)ceilf(fminf(fmaxf(m, -kPlain), kPlain) * kLog2e);
+        if (e > e_run) {
+          sum = e - e_run > 120 ? 0.f : sum * __uint_as_float((uint32_t)(127 - (e - e_run)) << 23);
+          e_run = e;
+        }
+      }
+      const float low = fmaxf(top - 80.f, -kPlain);  // exp of less adds nothing that counts
+      const int shift = 0x4b400000 + e_run;          // the magic number's bits, and E
       uint64_t acc[2] = {0ull, 0ull};
       auto add = [&](float x0, float x1, int w) {
-        float y0, y1;
-        f2_unpack(f2_add(f2_pack(x0, x1), nbase), y0, y1);  // exact: base 0 or close by
-        const uint64_t y = f2_pack(fmaxf(y0, low), fmaxf(y1, low));
+        const uint64_t y = f2_pack(fmaxf(x0, low), fmaxf(x1, low));
         const uint64_t t = f2_fma(y, l2, magic);
-        const uint64_t n = f2_add(t, nmagic);
-        uint64_t f = f2_fma(y, l2, f2_mul(n, minus1));
+        const uint64_t n = f2_add(t, nmagic) ^ 0x8000000080000000ull;  // -n
+        uint64_t f = f2_fma(y, l2, n);
         f = f2_fma(y, ll2, f);
         uint64_t q = f2_fma(c6, f, c5);
         q = f2_fma(q, f, c4);
@@ -381,54 +405,74 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) add(x.get(k, e), x.get(k, e + 1), (e >> 1) & 1);
-      if (split == 0 && warp * 32 < head + tail) add(x.extra, -INFINITY, 0);
+        for (int e = 0; e < PER; e += 2) add(get(k, e), get(k, e + 1), (e >> 1) & 1);
+      if (tile == 0 && split == 0 && warp == 0) add(extra, -INFINITY, 0);
       float s0, s1;
       f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
-      fixed = __double2ull_rn((double)(s0 + s1) * kUnit);
+      sum += s0 + s1;
+      if (m >= floor_k) {
+        const int at = head + (first + tile * NV * kThreads + tid) * PER;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
-      if (lane == 0) sums[warp] = fixed;
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int e = 0; e < PER; ++e) offer(get(k, e), at + k * kThreads * PER + e);
+        if (tile == 0) offer(extra, v_extra);
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) x[k] = next[k];
     }
-    // the elements at or above the threshold
-    if (m >= floor_k) {
-      auto offer = [&](float v, int at) {
-        if (v >= floor_k) {
-          const int i = atomicAdd(&n_list, 1);
-          if (i < kList) list[i] = key_of(v, at);
+    // the block's maximum, then the threads' sums against its exponent
+    float block_top = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      block_top = fmaxf(block_top, __shfl_xor_sync(0xffffffffu, block_top, o));
+    __syncthreads();
+    if (lane == 0) sh_top[warp] = block_top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) block_top = fmaxf(block_top, sh_top[w]);
+    const bool far = !(fabsf(block_top) <= kPlain);  // (also: no element)
+    const float base = far ? block_top : 0.f;
+    const int e_top = far ? 0 : (int)ceilf(block_top * kLog2e);
+    unsigned long long fixed = 0;
+    // an element of this thread's part, read again
+    auto again = [&](auto&& f) {
+      for (int v = first + tid; v < end; v += kThreads) {
+        const T* q = reinterpret_cast<const T*>(vecs + v);
+        for (int e = 0; e < PER; ++e) {
+          const float y = (float)q[e];
+          if (y >= kMasked && y < INFINITY) f(y, head + v * PER + e);
         }
-      };
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-          offer(x.get(k, e), head + (v0 + k * kThreads) * PER + e);
-      offer(x.extra, v_extra);
+      }
+      if (extra >= kMasked) f(extra, v_extra);
+    };
+    if (!far) {
+      if (top > -INFINITY && e_run - e_top > -100)
+        fixed = __double2ull_rn((double)sum * (kUnit * pow2(e_run - e_top)));
+    } else if (block_top > -INFINITY) {
+      float s = 0.f;
+      again([&](float y, int) { s += expf(y - block_top); });
+      fixed = __double2ull_rn((double)s * kUnit);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+    if (lane == 0) sums[warp] = fixed;
     __syncthreads();
     Part* part = reinterpret_cast<Part*>(p.parts +
                                          ((size_t)slot * p.splits + split) * p.part_bytes);
     Best* best = reinterpret_cast<Best*>(part + 1);
     const int n = n_list;
     if (n > kList) {
-      // many equal ones: the K best one after another, each the best below the one before
+      // too many to list (equal ones, or rising ones): the K best one after another, each
+      // the best below the one before
       unsigned long long before = ~0ull;
       for (int r = 0; r < K; ++r) {
         unsigned long long mine = 0;
-        if (m >= floor_k) {
-          auto see = [&](float v, int at) {
-            if (v >= floor_k) {
-              const unsigned long long key = key_of(v, at);
-              if (key < before && key > mine) mine = key;
-            }
-          };
-#pragma unroll
-          for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int e = 0; e < PER; ++e)
-              see(x.get(k, e), head + (v0 + k * kThreads) * PER + e);
-          see(x.extra, v_extra);
-        }
+        if (top >= floor_k)
+          again([&](float y, int at) {
+            const unsigned long long key = key_of(y, at);
+            if (key < before && key > mine) mine = key;
+          });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const unsigned long long other = __shfl_xor_sync(0xffffffffu, mine, o);
@@ -439,36 +483,21 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
         __syncthreads();
         before = list[0];
         for (int w = 1; w < kWarps; ++w) before = list[w] > before ? list[w] : before;
-        __syncthreads();
-        if (tid == 0) list[kWarps + r] = before;
-      }
-      __syncthreads();
-      if (tid < K) {
-        const unsigned long long key = list[kWarps + tid];
-        const uint32_t o = (uint32_t)(key >> 32);
-        best[tid] = Best{__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o),
-                         (int)~(uint32_t)key};
+        if (tid == 0) best[r] = best_of(before);
       }
     } else {
       for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = list[i];
-        int above = 0;
-        for (int j = 0; j < n; ++j) above += list[j] > key;
-        if (above < K) {
-          const uint32_t o = (uint32_t)(key >> 32);
-          best[above] = Best{__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o),
-                             (int)~(uint32_t)key};
-        }
+        const int above = count_above(list, n, list[i]);
+        if (above < K) best[above] = best_of(list[i]);
       }
     }
     if (tid == 0) {
       unsigned long long all = 0;
-      if (top > -INFINITY)
-        for (int w = 0; w < kWarps; ++w) all += sums[w];
+      for (int w = 0; w < kWarps; ++w) all += sums[w];
       part->sum = all;
       part->e = e_top;
       part->base = base;
-      part->top = top;
+      part->top = block_top;
       part->n = min(n, K);
     }
   }
@@ -483,8 +512,7 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
   __syncthreads();
   if (!last_of) return;
   __threadfence();
-  if (!skip)
-    join_row<T>(p, slot, nullptr, reinterpret_cast<unsigned long long*>(scratch));
+  if (!skip) join_row(p, slot, reinterpret_cast<unsigned long long*>(scratch));
   __threadfence();
   __syncthreads();
   const int group = slot / K;
@@ -499,12 +527,6 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
   choose(p, group, scratch);
 }
 
-// Elements a thread holds: 32 (as many as its registers take); 8 where that leaves SMs
-// without a block.
-int elements_held(long long slots, int vocab, int n_sms) {
-  return slots * ((vocab + 32 * kThreads - 1) / (32 * kThreads)) < n_sms ? 8 : 32;
-}
-
 size_t take(size_t& off, size_t bytes) {
   const size_t o = off;
   off = (off + bytes + 255) & ~(size_t)255;
@@ -516,10 +538,18 @@ size_t take(size_t& off, size_t bytes) {
 BeamWs beam_ws(int n_groups, int beams, int vocab, int n_sms) {
   BeamWs w;
   const size_t slots = (size_t)n_groups * beams;
-  w.held = elements_held((long long)slots, vocab, n_sms);
-  // whole vectors are counted from the row's first 16-byte boundary: never more than
-  // vocab elements' worth
-  w.splits = (vocab + w.held * kThreads - 1) / (w.held * kThreads);
+  // A thread takes 16 elements of a tile, 8 where that leaves SMs without a block; a
+  // block up to 8 tiles, as long as every SM gets its three blocks four times over.
+  auto blocks = [&](int elements, int tiles) {
+    return (long long)slots * ((vocab + elements * tiles * kThreads - 1) /
+                               (elements * tiles * kThreads));
+  };
+  w.held = blocks(16, 1) < n_sms ? 8 : 16;
+  w.tiles = 1;
+  while (w.tiles < 8 && blocks(w.held, 2 * w.tiles) >= 12ll * n_sms) w.tiles *= 2;
+  // (whole vectors are counted from the row's first 16-byte boundary: never more than
+  // vocab elements' worth)
+  w.splits = (int)(blocks(w.held, w.tiles) / (long long)slots);
   if (w.splits < 1) w.splits = 1;
   w.part_bytes = sizeof(Part) + (sizeof(Best) * beams + 15) / 16 * 16;
   size_t off = 0;
@@ -549,8 +579,8 @@ cudaError_t launch_beam(const BeamParams& p, bool f32, int held, cudaStream_t s)
     trace_end(s, "beam");
     return cudaGetLastError();
   };
-  if (f32) return held == 32 ? go(beam_kernel<float, 8>) : go(beam_kernel<float, 2>);
-  return held == 32 ? go(beam_kernel<__nv_bfloat16, 4>) : go(beam_kernel<__nv_bfloat16, 1>);
+  if (f32) return held == 16 ? go(beam_kernel<float, 4>) : go(beam_kernel<float, 2>);
+  return held == 16 ? go(beam_kernel<__nv_bfloat16, 2>) : go(beam_kernel<__nv_bfloat16, 1>);
 }
 
 }  // namespace saf

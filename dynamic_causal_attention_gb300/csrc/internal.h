@@ -214,7 +214,7 @@ cudaError_t launch_rotary(RotaryParams& p, bool f32, bool interleaved, int n_sms
 
 // ------------------------------------------------------------ beam step
 struct BeamParams {
-  int n_groups, beams, vocab, end, max_tokens, splits;
+  int n_groups, beams, vocab, end, max_tokens, tiles, splits;
   int64_t row_stride;
   const void* logits;       // [n_groups * beams, vocab]
   const float* scores;
@@ -231,7 +231,7 @@ struct BeamParams {
   uint8_t *row_best, *parts;
 };
 struct BeamWs {
-  int held, splits;  // elements of a thread, blocks of a row
+  int held, tiles, splits;  // elements of a thread's tile, tiles of a block, blocks of a row
   size_t part_bytes;
   size_t row_count, group_count, row_n, row_lse, row_best, parts, total;
 };

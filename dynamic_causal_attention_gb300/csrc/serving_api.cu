@@ -165,6 +165,7 @@ saf_status saf_beam_step(const saf_beam_dims* dims, const void* logits, const fl
   p.score_out = score_out;
   p.finished_out = finished_out;
   p.history_out = history_out;
+  p.tiles = w.tiles;
   p.splits = w.splits;
   p.part_bytes = w.part_bytes;
   p.row_count = reinterpret_cast<int*>(ws + w.row_count);

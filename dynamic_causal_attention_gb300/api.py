@@ -392,21 +392,22 @@ class _OnDevice:
     def _bad(self, what):
         return B.SafError(B.SAF_ERR_INVALID_ARG, what)
 
+    # (get_device of a CPU tensor is -1: no device of ours)
     def _need(self, t, shape, dtype, what):
         """The address of a contiguous tensor of this shape, type and device."""
-        if (t.dtype is not dtype or not t.is_cuda or t.get_device() != self._index
-                or t.shape != shape or not t.is_contiguous()):
+        if (t.dtype is not dtype or t.get_device() != self._index or t.shape != shape
+                or not t.is_contiguous()):
             raise self._bad(f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on "
                             f"{self.device}")
         return t.data_ptr()
 
     def _rows(self, t, shape, dtype, what):
         """saf_rows of [total, heads, d] or [B, heads, T, d] rows in any order."""
-        if (t.dtype is not dtype or not t.is_cuda or t.get_device() != self._index
-                or t.shape != shape or (t.stride(-1) != 1 and shape[-1] > 1)):
+        st = t.stride()
+        if (t.dtype is not dtype or t.get_device() != self._index or t.shape != shape
+                or (st[-1] != 1 and shape[-1] != 1)):
             raise self._bad(f"{what}: want a {dtype} tensor {tuple(shape)} on {self.device} "
                             "whose rows are contiguous")
-        st = t.stride()
         if len(st) == 3:
             return B.saf_rows(t.data_ptr(), 0, st[0], st[1])
         return B.saf_rows(t.data_ptr(), st[0], st[2], st[1])
@@ -476,6 +477,7 @@ class Rotary(_OnDevice):
         st, turns = B.saf_rotary_turns(freqs)
         _check(st, "saf_rotary_turns")
         self.d_h, self.rot_dim, self.layout, self.scale = d_h, 2 * len(freqs), layout, scale
+        self._flags = B.SAF_ROTARY_INTERLEAVED if layout == "interleaved" else 0
         self.turns = torch.from_numpy(np.array(turns, dtype=np.uint64).view(np.int64)).to(
             self.device)
 
@@ -489,52 +491,62 @@ class Rotary(_OnDevice):
         ``out`` (a pair; (q, k) itself for in place).  Rows of no sequence and rows behind n_new
         are left as they were in ``out``, 0 in new tensors.  ``inverse`` turns back: applied to
         the gradients of the results it gives those of q and k."""
-        if q.dim() not in (3, 4):
+        shape, dtype = q.shape, q.dtype
+        packed = len(shape) == 3
+        if not packed and len(shape) != 4:
             raise self._bad("apply: q is neither [total, H, d_h] nor [B, H, T, d_h]")
-        if q.dtype not in (torch.bfloat16, torch.float32):
+        if dtype is torch.bfloat16:
+            code = B.SAF_BF16
+        elif dtype is torch.float32:
+            code = B.SAF_F32
+        else:
             raise B.SafError(B.SAF_ERR_UNSUPPORTED, "apply: q is neither bf16 nor fp32")
-        packed = q.dim() == 3
-        B_, T = (1, q.shape[0]) if packed else (q.shape[0], q.shape[2])
-        H, H_k = q.shape[1], 0
-
-        def shape(heads):
-            return torch.Size((T, heads, self.d_h) if packed else (B_, heads, T, self.d_h))
-        rows = [self._rows(q, shape(H), q.dtype, "apply: q"), None]
+        d = self.d_h
+        if packed:
+            B_, (T, H, last) = 1, shape
+        else:
+            B_, H, T, last = shape
+        if last != d:
+            raise self._bad(f"apply: rows of {last} components, d_h is {d}")
+        rq = self._rows(q, shape, dtype, "apply: q")
+        rk = k_shape = None
+        H_k = 0
         if k is not None:
-            if k.dim() != q.dim():
+            k_shape = k.shape
+            if len(k_shape) != len(shape):
                 raise self._bad("apply: k has another number of dimensions than q")
-            H_k = k.shape[1]
-            rows[1] = self._rows(k, shape(H_k), q.dtype, "apply: k")
-        flags = ((B.SAF_ROTARY_INTERLEAVED if self.layout == "interleaved" else 0)
-                 | (B.SAF_ROTARY_INVERSE if inverse else 0))
+            H_k = k_shape[1]
+            rk = self._rows(k, (T, H_k, d) if packed else (B_, H_k, T, d), dtype, "apply: k")
+        flags = self._flags | B.SAF_ROTARY_INVERSE if inverse else self._flags
         if out is None:
-            out = (torch.empty(q.shape, dtype=q.dtype, device=self.device),
-                   None if k is None else torch.empty(k.shape, dtype=q.dtype, device=self.device))
+            out = (torch.empty(shape, dtype=dtype, device=self.device),
+                   None if k is None else torch.empty(k_shape, dtype=dtype, device=self.device))
             flags |= B.SAF_CLEAR_REST
         elif (out[1] is None) != (k is None):
             raise self._bad("apply: out is not a pair like (q, k)")
-        rows.append(self._rows(out[0], shape(H), q.dtype, "apply: out"))
-        rows.append(None if k is None else self._rows(out[1], shape(H_k), q.dtype, "apply: out"))
-        if (positions is not None) + (cu_seqlens is not None) + (seq_len is not None) > 1:
-            raise self._bad("apply: positions are given in more than one way")
+        oq = self._rows(out[0], shape, dtype, "apply: out")
+        ok = None if k is None else self._rows(out[1], k_shape, dtype, "apply: out")
         at = cu = lens = new = None
         n = 0
         if positions is not None:
-            at = self._need(positions, torch.Size((T,) if packed else (B_, T)), torch.int32,
+            if cu_seqlens is not None or seq_len is not None:
+                raise self._bad("apply: positions are given in more than one way")
+            at = self._need(positions, (T,) if packed else (B_, T), torch.int32,
                             "apply: positions")
         elif cu_seqlens is not None:
-            if not packed or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            if seq_len is not None:
+                raise self._bad("apply: positions are given in more than one way")
+            cu_shape = cu_seqlens.shape
+            if not packed or len(cu_shape) != 1 or cu_shape[0] < 1:
                 raise self._bad("apply: cu_seqlens [n + 1] goes with packed rows")
-            n = cu_seqlens.shape[0] - 1
-            cu = self._need(cu_seqlens, cu_seqlens.shape, torch.int32, "apply: cu_seqlens")
+            n = cu_shape[0] - 1
+            cu = self._need(cu_seqlens, cu_shape, torch.int32, "apply: cu_seqlens")
         elif seq_len is not None:
-            lens = self._need(seq_len, torch.Size((B_,)), torch.int32, "apply: seq_len")
+            lens = self._need(seq_len, (B_,), torch.int32, "apply: seq_len")
         if n_new is not None:
-            new = self._need(n_new, torch.Size((B_,)), torch.int32, "apply: n_new")
-        dims = B.saf_rotary_dims(B_, T, H, H_k, self.d_h, self.rot_dim,
-                                 B.SAF_F32 if q.dtype == torch.float32 else B.SAF_BF16)
-        self._call(B.saf_rotary, dims, *rows, self.turns.data_ptr(), self.scale, at, cu, n, lens,
-                   new, flags)
+            new = self._need(n_new, (B_,), torch.int32, "apply: n_new")
+        self._call(B.saf_rotary, B.saf_rotary_dims(B_, T, H, H_k, d, self.rot_dim, code), rq, rk,
+                   oq, ok, self.turns.data_ptr(), self.scale, at, cu, n, lens, new, flags)
         return out
 
 
@@ -567,49 +579,48 @@ class PackedAttention(_OnDevice):
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self.workspace[:256].zero_()  # the status before the first call
 
-    def _common(self, q, cu_seqlens, alpha, rho, what):
-        if q.dim() != 3 or q.shape[0] > self.max_total:
-            raise self._bad(f"{what}: q is not [total, H, d_h] with total <= {self.max_total}")
-        total = q.shape[0]
-        if cu_seqlens.dim() != 1 or not 1 <= cu_seqlens.shape[0] <= self.max_seqs + 1:
-            raise self._bad(f"{what}: want cu_seqlens [n + 1], n <= {self.max_seqs}")
-        n = cu_seqlens.shape[0] - 1
-        cu = self._need(cu_seqlens, cu_seqlens.shape, torch.int32, f"{what}: cu_seqlens")
+    def _common(self, q, cu_seqlens, alpha, rho):
+        """(dims, cu_seqlens, alpha, rho) as the C entries take them."""
+        shape, n = q.shape, cu_seqlens.shape
+        if len(shape) != 3 or shape[0] > self.max_total:
+            raise self._bad(f"PackedAttention: q is not [total, H, d_h], total <= {self.max_total}")
+        if len(n) != 1 or not 1 <= n[0] <= self.max_seqs + 1:
+            raise self._bad(f"PackedAttention: want cu_seqlens [n + 1], n <= {self.max_seqs}")
+        cu = self._need(cu_seqlens, n, torch.int32, "PackedAttention: cu_seqlens")
         pa = pr = None
         T = 0
         if self._frozen:
             if alpha is None or rho is None:
-                raise self._bad(f"{what}: frozen heads need alpha and rho")
+                raise self._bad("PackedAttention: frozen heads need alpha and rho")
             T = alpha.shape[-1]
             if T < self.max_len:
-                raise self._bad(f"{what}: alpha has {T} columns, max_len is {self.max_len}")
-            pa = self._need(alpha, (self.H, T), torch.float32, f"{what}: alpha")
-            pr = self._need(rho, (self.H, T), torch.float32, f"{what}: rho")
-        dims = B.saf_packed_dims(total, n, self.max_len, self.H, self.H_kv, self.d_h, T)
-        wide, narrow = (total, self.H, self.d_h), (total, self.H_kv, self.d_h)
-
-        def rows(t, shape, name):
-            return self._rows(t, shape, torch.bfloat16, f"{what}: {name}")
-        return total, dims, cu, pa, pr, wide, narrow, rows
+                raise self._bad(f"PackedAttention: {T} columns of alpha, max_len {self.max_len}")
+            pa = self._need(alpha, (self.H, T), torch.float32, "PackedAttention: alpha")
+            pr = self._need(rho, (self.H, T), torch.float32, "PackedAttention: rho")
+        return B.saf_packed_dims(shape[0], n[0] - 1, self.max_len, self.H, self.H_kv, self.d_h,
+                                 T), cu, pa, pr
 
     def forward(self, q, k, v, cu_seqlens, alpha=None, rho=None, out=None, lse=None):
         """(out [total, H, d_h], lse [H, total] fp32).  Rows of no sequence are left as they were
-        in buffers that are given, 0 and -inf if the call makes both.  alpha, rho
+        in buffers that are given, 0 and -inf in those that the call makes.  alpha, rho
         [H, >= max_len] fp32 are needed where heads are frozen."""
-        total, dims, cu, pa, pr, wide, narrow, rows = self._common(q, cu_seqlens, alpha, rho,
-                                                                   "forward")
+        dims, cu, pa, pr = self._common(q, cu_seqlens, alpha, rho)
+        total, bf16 = dims.total, torch.bfloat16
+        wide, narrow = (total, self.H, self.d_h), (total, self.H_kv, self.d_h)
         flags = 0
         if out is None and lse is None:
+            # both are new: the call itself clears what it does not work on
             flags = B.SAF_CLEAR_REST
-        if out is None:
-            make = torch.empty if flags else torch.zeros
-            out = make(wide, dtype=torch.bfloat16, device=self.device)
-        if lse is None:
+            out = torch.empty(wide, dtype=bf16, device=self.device)
             lse = torch.empty((self.H, total), dtype=torch.float32, device=self.device)
-            if not flags:
-                lse.fill_(-math.inf)
-        self._call(B.saf_packed_attn_fwd, dims, rows(q, wide, "q"), rows(k, narrow, "k"),
-                   rows(v, narrow, "v"), cu, pa, pr, self.head_is_static, rows(out, wide, "out"),
+        elif out is None:
+            out = torch.zeros(wide, dtype=bf16, device=self.device)
+        elif lse is None:
+            lse = torch.full((self.H, total), -math.inf, device=self.device)
+        rows = self._rows
+        self._call(B.saf_packed_attn_fwd, dims, rows(q, wide, bf16, "forward: q"),
+                   rows(k, narrow, bf16, "forward: k"), rows(v, narrow, bf16, "forward: v"), cu,
+                   pa, pr, self.head_is_static, rows(out, wide, bf16, "forward: out"),
                    self._need(lse, (self.H, total), torch.float32, "forward: lse"), flags,
                    self.workspace.data_ptr(), self.ws_bytes)
         return out, lse
@@ -619,20 +630,25 @@ class PackedAttention(_OnDevice):
         ``grads`` (a triple; rows of no sequence are left as they were) or to new tensors."""
         if not self._backward:
             raise B.SafError(B.SAF_ERR_STATE, "backward: made with backward=False")
-        total, dims, cu, pa, pr, wide, narrow, rows = self._common(q, cu_seqlens, alpha, rho,
-                                                                   "backward")
+        dims, cu, pa, pr = self._common(q, cu_seqlens, alpha, rho)
+        total, bf16 = dims.total, torch.bfloat16
+        wide, narrow = (total, self.H, self.d_h), (total, self.H_kv, self.d_h)
         flags = 0
         if grads is None:
             flags = B.SAF_CLEAR_REST
-            grads = tuple(torch.empty(s, dtype=torch.bfloat16, device=self.device)
-                          for s in (wide, narrow, narrow))
+            grads = (torch.empty(wide, dtype=bf16, device=self.device),
+                     torch.empty(narrow, dtype=bf16, device=self.device),
+                     torch.empty(narrow, dtype=bf16, device=self.device))
         dq, dk, dv = grads
-        self._call(B.saf_packed_attn_bwd, dims, rows(q, wide, "q"), rows(k, narrow, "k"),
-                   rows(v, narrow, "v"), rows(out, wide, "out"),
+        rows = self._rows
+        self._call(B.saf_packed_attn_bwd, dims, rows(q, wide, bf16, "backward: q"),
+                   rows(k, narrow, bf16, "backward: k"), rows(v, narrow, bf16, "backward: v"),
+                   rows(out, wide, bf16, "backward: out"),
                    self._need(lse, (self.H, total), torch.float32, "backward: lse"),
-                   rows(dout, wide, "dout"), cu, pa, pr, self.head_is_static,
-                   rows(dq, wide, "dq"), rows(dk, narrow, "dk"), rows(dv, narrow, "dv"), flags,
-                   self.workspace.data_ptr(), self.ws_bytes)
+                   rows(dout, wide, bf16, "backward: dout"), cu, pa, pr, self.head_is_static,
+                   rows(dq, wide, bf16, "backward: dq"), rows(dk, narrow, bf16, "backward: dk"),
+                   rows(dv, narrow, bf16, "backward: dv"), flags, self.workspace.data_ptr(),
+                   self.ws_bytes)
         return dq, dk, dv
 
     def device_status(self):
@@ -657,14 +673,13 @@ class BeamSearch(_OnDevice):
         if n_groups < 1:
             raise self._bad(f"BeamSearch: {n_groups} groups")
         with torch.cuda.device(self.device):
-            self.ws_bytes = B.saf_beam_workspace_size(self._dims(vocab, B.SAF_F32, 0))
+            self.ws_bytes = B.saf_beam_workspace_size(
+                B.saf_beam_dims(n_groups, beams, vocab, vocab, B.SAF_F32,
+                                -1 if end is None else end, 0))
         if self.ws_bytes == 0:
             raise B.SafError(B.SAF_ERR_UNSUPPORTED, "saf_beam_workspace_size")
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
-
-    def _dims(self, stride, dtype, max_tokens):
-        return B.saf_beam_dims(self.n_groups, self.beams, self.vocab, stride, dtype,
-                               -1 if self.end is None else self.end, max_tokens)
+        self._whole = torch.empty(self.slots, dtype=torch.int32, device=self.device)  # a shape
 
     def step(self, logits, scores, finished=None, *, history=None, n_tokens=None,
              history_out=None):
@@ -673,25 +688,31 @@ class BeamSearch(_OnDevice):
         columns filled.  Returns (parent, token, scores, finished, history): the new slots, best
         first in each group; finished is None without an ending token, history None without one.
         The history is written to ``history_out`` (not the same tensor), as far as it is filled."""
-        n = (self.slots,)
-        if logits.dtype not in (torch.bfloat16, torch.float32):
+        slots, dtype, st = self.slots, logits.dtype, logits.stride()
+        n = (slots,)
+        if dtype is torch.float32:
+            code = B.SAF_F32
+        elif dtype is torch.bfloat16:
+            code = B.SAF_BF16
+        else:
             raise B.SafError(B.SAF_ERR_UNSUPPORTED, "step: logits are neither bf16 nor fp32")
-        if (logits.shape != (self.slots, self.vocab) or logits.get_device() != self._index
-                or not logits.is_cuda or (self.vocab > 1 and logits.stride(1) != 1)
-                or (self.slots > 1 and logits.stride(0) < self.vocab)):
-            raise self._bad(f"step: want logits [{self.slots}, {self.vocab}] on {self.device} "
-                            "whose rows are contiguous and apart")
+        if (logits.shape != (slots, self.vocab) or logits.get_device() != self._index
+                or (st[1] != 1 and self.vocab > 1) or (st[0] < self.vocab and slots > 1)):
+            raise self._bad(f"step: want logits [{slots}, {self.vocab}] on {self.device} whose "
+                            "rows are contiguous and apart")
         ps = self._need(scores, n, torch.float32, "step: scores")
-        pf = None if finished is None else self._need(finished, n, torch.bool, "step: finished")
-        if finished is not None and self.end is None:
-            raise self._bad("step: finished slots without an ending token")
+        pf = None
+        if finished is not None:
+            if self.end is None:
+                raise self._bad("step: finished slots without an ending token")
+            pf = self._need(finished, n, torch.bool, "step: finished")
         ph = pn = po = None
         columns = 0
         if history is not None:
-            if n_tokens is None or history.dim() != 2:
+            shape = history.shape
+            if n_tokens is None or len(shape) != 2 or shape[0] != slots:
                 raise self._bad("step: history [slots, columns] needs n_tokens")
-            columns = history.shape[1]
-            shape = (self.slots, columns)
+            columns = shape[1]
             if history_out is None:
                 history_out = torch.full_like(history, -1)
             ph = self._need(history, shape, torch.int32, "step: history")
@@ -699,14 +720,18 @@ class BeamSearch(_OnDevice):
             pn = self._need(n_tokens, (1,), torch.int32, "step: n_tokens")
         elif history_out is not None:
             raise self._bad("step: history_out without a history")
-        new = torch.empty((2, self.slots), dtype=torch.int32, device=self.device)
-        parent, token = new[0], new[1]
-        score = torch.empty(n, dtype=torch.float32, device=self.device)
-        done = None if self.end is None else torch.empty(n, dtype=torch.bool, device=self.device)
-        dims = self._dims(logits.stride(0) if self.slots > 1 else self.vocab,
-                          B.SAF_F32 if logits.dtype == torch.float32 else B.SAF_BF16, columns)
+        parent, token = torch.empty_like(self._whole), torch.empty_like(self._whole)
+        score = torch.empty_like(scores)
+        done = pd = None
+        end = -1
+        if self.end is not None:
+            end = self.end
+            done = torch.empty(n, dtype=torch.bool, device=self.device)
+            pd = done.data_ptr()
+        dims = B.saf_beam_dims(self.n_groups, self.beams, self.vocab,
+                               st[0] if slots > 1 else self.vocab, code, end, columns)
         self._call(B.saf_beam_step, dims, logits.data_ptr(), ps, pf, ph, pn, parent.data_ptr(),
-                   token.data_ptr(), score.data_ptr(), _ptr(done), po, self.workspace.data_ptr(),
+                   token.data_ptr(), score.data_ptr(), pd, po, self.workspace.data_ptr(),
                    self.ws_bytes)
         return parent, token, score, done, history_out
 

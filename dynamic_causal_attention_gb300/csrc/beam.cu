@@ -13,14 +13,16 @@
 // the row's parts, the last row of a group chooses (a counter each, which its last
 // block sets back to zero for the next call).
 //
-// Which of two offers is better must not hang on the rounding of a sum of 10^5
-// exponentials.  So an exponential is formed in base two against the thread's
-// exponent E = ceil(max x log2 e): with n = round(x log2 e) and the rest f, both
-// from x itself (no difference to the maximum is rounded), 2^(n - E) (1 + f q(f)),
-// q of degree 5 fitted by the author to 2e-9; a thread's sum is rounded to 2^-44 of the
-// block's scale and added to the others' in integers, so the sum does not depend on the
-// order, and parts are joined by exact powers of two in fp64.  Scores are compared in
-// fp64.  (Logits beyond 2^20 take a second pass against their maximum.)
+// Which of two offers is better should not hang on the rounding of a sum of 10^5
+// exponentials.  An exponential is 2^(x log2 e - E) with the thread's exponent
+// E = ceil(max x log2 e): the argument from x itself, by a multiplication that is
+// rounded after E is subtracted, and the part of log2 e that fp32 does not hold; so it is
+// exact to 2^-24 of what is left, and the function to 2^-22.  A thread's sum is rounded to
+// 2^-40 of the block's scale and added to the others' in integers, so it does not
+// depend on the order, and parts are joined by exact powers of two in fp64.  Scores are
+// compared in fp64.  (Logits beyond 2^20 take a second pass against their maximum.)
+// A polynomial in place of the function (2e-9) cost 18 more instructions for each pair
+// of logits and twice the time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -33,15 +35,16 @@ namespace saf {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kStages = 3;              // tiles of a block's ring
 constexpr int kList = 512;             // candidates of a block before the K best are picked
 constexpr float kMasked = -2.3e38f;    // below: as -inf
 constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-08f;
 constexpr float kPlain = 1048576.f;    // |logits| up to here are reduced without a base
-constexpr double kUnit = 17592186044416.0;  // 2^44: a block's sum in integers
+constexpr int kUnit = 40;              // sums in integers count 2^-40: those of 2^22 ones fit
 
 // What a block (then a row) leaves behind, followed by its K best as (value, token).
 struct __align__(16) Part {
-  unsigned long long sum;  // in 2^-44
+  unsigned long long sum;  // in 2^-40
   int e;                   // sum * 2^e * exp(base), or no element where top = -inf
   float base, top;
   int n;                   // best ones that follow
@@ -63,18 +66,70 @@ __device__ __forceinline__ unsigned long long key_of(double x) {
   return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
-__device__ __forceinline__ double pow2(int e) {  // 2^e, -1022 <= e <= 1023
-  return __longlong_as_double((long long)(e + 1023) << 52);
+// x 2^e in units of 2^-40, rounded down (x >= 0 and finite; fp64 has 1/64 of fp32's rate
+// here, so this is done in integers).
+__device__ __forceinline__ unsigned long long in_units(float x, int e) {
+  const uint32_t u = __float_as_uint(x);
+  const int sh = (int)(u >> 23) - 127 - 23 + kUnit + e;
+  const unsigned long long m = (u & 0x7fffffu) | 0x800000u;
+  return u < 0x800000u || sh < -23 ? 0 : sh >= 0 ? m << sh : m >> -sh;
 }
 
-__device__ __forceinline__ bool dead(const BeamParams& p, int slot) {
-  const float s = p.scores[slot];
-  return !(s >= kMasked && s < INFINITY);
+// 16 bytes global -> shared, past the L1 cache, in groups that a thread waits for.
+__device__ __forceinline__ void copy_async_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
 }
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The maximum of three, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Whether a score is one (not -inf, masked or NaN).
+__device__ __forceinline__ bool alive(float score) { return score >= kMasked && score < INFINITY; }
 
 __device__ __forceinline__ Best best_of(unsigned long long key) {
   const uint32_t o = (uint32_t)(key >> 32);
   return Best{__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o), (int)~(uint32_t)key};
+}
+
+// (top, base, e, sum) takes in another part of the row: of two sums the one with the smaller
+// exponent is shifted; the part with the larger element keeps its base.
+__device__ __forceinline__ void join_sum(float& top, float& base, int& e, unsigned long long& sum,
+                                         float t, float b, int ex, unsigned long long x) {
+  if (!(t > -INFINITY)) return;
+  if (!(top > -INFINITY)) {
+    top = t;
+    base = b;
+    e = ex;
+    sum = x;
+    return;
+  }
+  if (b != base) {
+    // one of the two holds logits beyond 2^20
+    const bool other = t > top;
+    const double from = other ? (double)base - b : (double)b - base;
+    const double d = from + (double)(other ? e - ex : ex - e) * 0.6931471805599453;
+    const unsigned long long small = other ? sum : x, large = other ? x : sum;
+    sum = large + (d > -40.0 ? (unsigned long long)((double)small * exp(d)) : 0);
+    if (other) {
+      base = b;
+      e = ex;
+    }
+  } else {
+    const int up = max(e, ex);
+    sum = (up - e < 64 ? sum >> (up - e) : 0) + (up - ex < 64 ? x >> (up - ex) : 0);
+    e = up;
+  }
+  top = fmaxf(top, t);
 }
 
 // How many of keys[0 .. n) are above `key`.
@@ -86,124 +141,126 @@ __device__ __forceinline__ int count_above(const unsigned long long* keys, int n
   return above;
 }
 
-// Joins a row's parts and writes its log sum and its K best; every thread of the block.
-__device__ void join_row(const BeamParams& p, int slot, unsigned long long* keys) {
-  const int S = p.splits, K = p.beams, tid = threadIdx.x, lane = tid & 31, n = S * K;
-  const uint8_t* parts = p.parts + (size_t)slot * S * p.part_bytes;
-  auto part = [&](int s) { return reinterpret_cast<const Part*>(parts + (size_t)s * p.part_bytes); };
-  for (int i = tid; i < n; i += kThreads) {
-    const int s = i / K, j = i - s * K;
-    const int2 x = __ldcg(reinterpret_cast<const int2*>(part(s) + 1) + j);
-    keys[i] = j < __ldcg(&part(s)->n) ? key_of(__int_as_float(x.x), x.y) : 0;
-  }
-  if (tid >= kThreads - 32) {
-    // the largest element, and the part that holds it: its base and exponent are the sum's
-    float top = -INFINITY;
-    int at = 0;
-    for (int s = lane; s < S; s += 32) {
-      const float t = __ldcg(&part(s)->top);
-      if (t > top) {
-        top = t;
-        at = s;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float t = __shfl_xor_sync(0xffffffffu, top, o);
-      const int a = __shfl_xor_sync(0xffffffffu, at, o);
-      if (t > top || (t == top && a < at)) {
-        top = t;
-        at = a;
-      }
-    }
-    const float base = __ldcg(&part(at)->base);
-    const int e = __ldcg(&part(at)->e);
-    double sum = 0.0;
-    for (int s = lane; s < S; s += 32) {
-      const Part* q = part(s);
-      const float b = __ldcg(&q->base);
-      const double x = (double)__ldcg(&q->sum) * (1.0 / kUnit);
-      const int de = __ldcg(&q->e) - e;
-      if (!(__ldcg(&q->top) > -INFINITY)) continue;
-      if (b == base) {
-        if (de > -1000) sum += x * pow2(de);
-      } else {  // one of the two holds logits beyond 2^20
-        const double d = ((double)b - (double)base) + (double)de * 0.6931471805599453;
-        if (d > -700.0) sum += x * exp(d);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0)
-      p.row_lse[slot] = top > -INFINITY
-                            ? (double)base + ((double)e * 0.6931471805599453 + log(sum))
-                            : 0.0;
-  }
-  __syncthreads();
-  Best* row_best = reinterpret_cast<Best*>(p.row_best) + (size_t)slot * K;
-  int mine = 0;
-  for (int i = tid; i < n; i += kThreads) {
-    const unsigned long long key = keys[i];
-    if (key == 0) continue;
-    ++mine;
-    const int above = count_above(keys, n, key);
-    if (above < K) row_best[above] = best_of(key);
-  }
-  const int valid = __syncthreads_count(mine > 0) >= K ? K : -1;
-  if (valid == K) {
-    if (tid == 0) p.row_n[slot] = K;
-  } else if (tid == 0) {
-    int c = 0;
-    for (int i = 0; i < n; ++i) c += keys[i] != 0;
-    p.row_n[slot] = min(c, K);
-  }
+// What the last blocks work on, in dynamic shared memory.
+struct Joined {
+  unsigned long long *keys, *best, *score;  // [R * S * K], [K * K], [K * K]
+  double* lse;                              // [K]
+  int *flat, *chosen, *token;               // [K * K], [K], [K]
+};
+
+// Whether a slot offers tokens of its own.
+__device__ __forceinline__ bool offers(const BeamParams& p, int slot) {
+  // (scores may be score_out, and finished its output: no read-only loads)
+  const uint8_t done = p.finished ? p.finished[slot] : 0;
+  return alive(p.scores[slot]) && !done;
 }
 
-// Chooses a group's new slots; every thread of the block.
-__device__ void choose(const BeamParams& p, int group, uint8_t* scratch) {
-  const int K = p.beams, tid = threadIdx.x, slot0 = group * K;
-  unsigned long long* score = reinterpret_cast<unsigned long long*>(scratch);  // [K * K] keys
-  int* flat = reinterpret_cast<int*>(score + K * K);                           // [K * K]
-  int* chosen = flat + K * K;                                                  // [K] parents
-  int* token_of = chosen + K;                                                  // [K]
-  for (int i = tid; i < K * K; i += kThreads) {
-    const int b = i / K, j = i - b * K, slot = slot0 + b;
-    unsigned long long key = 0;
-    int f = 0;
-    if (!dead(p, slot)) {
-      if (p.finished && p.finished[slot]) {
-        if (j == 0) {
-          key = key_of((double)p.scores[slot]);
-          f = b * p.vocab + p.end;
-        }
-      } else if (j < __ldcg(p.row_n + slot)) {
-        const Best* best = reinterpret_cast<const Best*>(p.row_best) + (size_t)slot * K + j;
-        const double x = (double)p.scores[slot] +
-                         ((double)__ldcg(&best->x) - __ldcg(p.row_lse + slot));
-        key = key_of(x);
-        f = b * p.vocab + __ldcg(&best->v);
+// Joins the parts of R rows from slot0 on: log sums and, best first, K keys of each row
+// (0: none); every thread of the block.
+__device__ void join_rows(const BeamParams& p, int slot0, int R, const Joined& j) {
+  const int S = p.splits, K = p.beams, tid = threadIdx.x, lane = tid & 31, n = S * K;
+  auto part = [&](int r, int s) {
+    return reinterpret_cast<const int4*>(p.parts + ((size_t)(slot0 + r) * S + s) * p.part_bytes);
+  };
+  for (int i = tid; i < R * K; i += kThreads) j.best[i] = 0;
+  // a warp to a row: its largest element, and against the exponent of that part the
+  // sum (j.score, j.flat and j.chosen hold sums, exponents and bases until the row's
+  // logarithm is taken)
+  for (int r = tid >> 5; r < R; r += kWarps) {
+    float top = -INFINITY, base = 0.f;
+    int e = 0;
+    unsigned long long sum = 0;
+    if (offers(p, slot0 + r)) {
+      // (a lane's parts one after another; 32 of them and more are rare)
+      for (int s = lane; s < S; s += 32) {
+        const int4 a = __ldcg(part(r, s)), b = __ldcg(part(r, s) + 1);
+        const unsigned long long x =
+            (unsigned long long)(uint32_t)a.x | (unsigned long long)(uint32_t)a.y << 32;
+        const float t = __int_as_float(b.x), bs = __int_as_float(a.w);
+        join_sum(top, base, e, sum, t, bs, a.z, x);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float t = __shfl_xor_sync(0xffffffffu, top, o);
+        const float bs = __shfl_xor_sync(0xffffffffu, base, o);
+        const int ex = __shfl_xor_sync(0xffffffffu, e, o);
+        const unsigned long long x = __shfl_xor_sync(0xffffffffu, sum, o);
+        join_sum(top, base, e, sum, t, bs, ex, x);
       }
     }
-    score[i] = key;
-    flat[i] = f;
+    if (lane == 0) {
+      j.score[r] = top > -INFINITY ? sum : 0;
+      j.flat[r] = e;
+      j.chosen[r] = __float_as_int(base);
+    }
   }
-  for (int i = tid; i < K; i += kThreads) chosen[i] = -1;
+#pragma unroll 2
+  for (int i = tid; i < R * n; i += kThreads) {
+    const int r = i / n, k = i - r * n, s = k / K, at = k - s * K;
+    const int2 x = __ldcg(reinterpret_cast<const int2*>(part(r, s) + 2) + at);
+    const int count = __ldcg(&reinterpret_cast<const Part*>(part(r, s))->n);
+    j.keys[i] = offers(p, slot0 + r) && at < count ? key_of(__int_as_float(x.x), x.y) : 0;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    // all rows' logarithms by one warp: fp64 instructions take as long for one lane as for 32
+    for (int r = lane; r < R; r += 32) {
+      const unsigned long long sum = j.score[r];
+      const double e = (double)(j.flat[r] - kUnit) * 0.6931471805599453;
+      j.lse[r] = sum == 0 ? 0.0 : (double)__int_as_float(j.chosen[r]) + (e + log((double)sum));
+    }
+  }
+  for (int i = tid; i < R * n; i += kThreads) {
+    const unsigned long long key = j.keys[i];
+    if (key == 0) continue;
+    const int r = i / n, above = count_above(j.keys + r * n, n, key);
+    if (above < K) j.best[r * K + above] = key;
+  }
+  __syncthreads();
+}
+
+// Chooses a group's new slots from its rows' best; every thread of the block.
+__device__ void choose(const BeamParams& p, int group, const Joined& j) {
+  const int K = p.beams, tid = threadIdx.x, slot0 = group * K;
+  const int filled = p.history_out ? max(0, min(__ldg(p.n_tokens), p.max_tokens)) : 0;
+  for (int i = tid; i < K * K; i += kThreads) {
+    const int b = i / K, slot = slot0 + b;
+    unsigned long long key = 0;
+    int f = 0;
+    const float start = p.scores[slot];  // (scores may be score_out: no read-only load)
+    const uint8_t done = p.finished ? p.finished[slot] : 0;
+    if (alive(start)) {
+      if (done) {
+        if (i == b * K) {
+          key = key_of((double)start);
+          f = b * p.vocab + p.end;
+        }
+      } else if (j.best[i] != 0) {
+        const Best best = best_of(j.best[i]);
+        key = key_of((double)start + ((double)best.x - j.lse[b]));
+        f = b * p.vocab + best.v;
+      }
+    }
+    j.score[i] = key;
+    j.flat[i] = f;
+  }
+  for (int i = tid; i < K; i += kThreads) j.chosen[i] = -1;
   __syncthreads();
   for (int i = tid; i < K * K; i += kThreads) {
-    const unsigned long long key = score[i];
+    const unsigned long long key = j.score[i];
     if (key == 0) continue;
-    const int f = flat[i];
+    const int f = j.flat[i];
     int above = 0;
 #pragma unroll 4
-    for (int j = 0; j < K * K; ++j) {
-      const unsigned long long other = score[j];
-      above += other > key || (other == key && flat[j] < f);
+    for (int k = 0; k < K * K; ++k) {
+      const unsigned long long other = j.score[k];
+      above += other > key || (other == key && j.flat[k] < f);
     }
     if (above < K) {
       const int b = f / p.vocab, v = f - b * p.vocab, s = slot0 + above;
       const unsigned long long u = key >> 63 ? key & 0x7fffffffffffffffull : ~key;
-      chosen[above] = slot0 + b;
-      token_of[above] = v;
+      j.chosen[above] = slot0 + b;
+      j.token[above] = v;
       p.parent[s] = slot0 + b;
       p.token[s] = v;
       p.score_out[s] = (float)__longlong_as_double((long long)u);
@@ -212,7 +269,7 @@ __device__ void choose(const BeamParams& p, int group, uint8_t* scratch) {
   }
   __syncthreads();
   for (int i = tid; i < K; i += kThreads)
-    if (chosen[i] < 0) {
+    if (j.chosen[i] < 0) {
       // fewer offers than slots: the slot is free
       p.parent[slot0 + i] = -1;
       p.token[slot0 + i] = -1;
@@ -220,22 +277,49 @@ __device__ void choose(const BeamParams& p, int group, uint8_t* scratch) {
       if (p.finished_out) p.finished_out[slot0 + i] = 0;
     }
   if (p.history_out) {
-    const int n = max(0, min(*p.n_tokens, p.max_tokens)), cols = min(n + 1, p.max_tokens);
-#pragma unroll 4
-    for (int i = tid; i < K * cols; i += kThreads) {
-      const int b = i / cols, c = i - b * cols, from = chosen[b];
-      int v = -1;
-      if (from >= 0)
-        v = c < n ? __ldg(p.history + (size_t)from * p.max_tokens + c) : token_of[b];
-      p.history_out[(size_t)(slot0 + b) * p.max_tokens + c] = v;
+    // a warp to a row, eight columns of each lane in flight
+    const int cols = min(filled + 1, p.max_tokens), lane = tid & 31;
+    for (int b = tid >> 5; b < K; b += kWarps) {
+      const int from = j.chosen[b], last = from >= 0 ? j.token[b] : -1;
+      const int32_t* src = p.history + (size_t)max(from, 0) * p.max_tokens;
+      int32_t* dst = p.history_out + (size_t)(slot0 + b) * p.max_tokens;
+      for (int c0 = lane; c0 < cols; c0 += 256) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = c0 + 32 * i;
+          v[i] = c >= filled ? last : from >= 0 ? __ldg(src + c) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + 32 * i < cols) dst[c0 + 32 * i] = v[i];
+      }
     }
   }
 }
 
+// Whether this block is the last of `of` to come here (what the others wrote before is then
+// visible to it); the counter is zero again afterwards.
+__device__ __forceinline__ bool last_here(int* counter, int of, int* flag) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // the barrier and this fence order the whole block's writes before the count
+    __threadfence();
+    const bool last = atomicAdd(counter, 1) == of - 1;
+    if (last) {
+      *counter = 0;
+      __threadfence();
+    }
+    *flag = last;
+  }
+  __syncthreads();
+  return *flag != 0;
+}
+
 // Grid: slots * splits blocks.  A thread takes NV vectors of 16 bytes of every tile.  Dynamic
-// shared memory holds what joining and choosing need.
+// shared memory holds the ring of tiles, then what joining and choosing need.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant__ BeamParams p) {
+__global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant__ BeamParams p) {
   constexpr int PER = 16 / (int)sizeof(T);  // elements of a vector
   extern __shared__ __align__(16) uint8_t scratch[];
   __shared__ __align__(16) float tops[kThreads];  // the best K maxima of each warp
@@ -246,8 +330,7 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = blockIdx.x / p.splits, split = blockIdx.x - slot * p.splits;
   const int K = p.beams;
-  const bool skip = dead(p, slot) || (p.finished && p.finished[slot]);
-  if (!skip) {
+  if (offers(p, slot)) {
     const T* row = static_cast<const T*>(p.logits) + (size_t)slot * (size_t)p.row_stride;
     // elements ahead of the first 16-byte boundary, whole vectors, elements behind them
     const int head = min(
@@ -258,15 +341,41 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
     const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
     const int first = split * p.tiles * (kThreads * NV);
     const int end = min(nvec, first + p.tiles * (kThreads * NV));
-    uint4 x[NV];
-    auto load = [&](uint4 (&to)[NV], int tile) {
+    // Tiles come through a ring in shared memory in which each thread has places of its own:
+    // it copies what it reads itself, so no barrier is needed, and no registers
+    // hold what is in flight.
+    uint4* ring = reinterpret_cast<uint4*>(scratch) + tid;
+    constexpr int kTile = kThreads * NV;  // vectors
+    auto whole = [&](int tile) { return first + (tile + 1) * kTile <= end; };
+    auto issue = [&](int tile) {
+      if (tile < p.tiles) {
+        uint4* to = ring + tile % kStages * kTile;
+        const uint4* from = vecs + (first + tile * kTile + tid);
+        if (whole(tile)) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int v = first + (tile * NV + k) * kThreads + tid;
-        to[k] = v < end ? __ldcs(vecs + v) : make_uint4(none, none, none, none);
+          for (int k = 0; k < NV; ++k) copy_async_16(to + k * kThreads, from + k * kThreads);
+        } else {
+          for (int k = 0; k < NV; ++k)
+            if (first + tile * kTile + k * kThreads + tid < end)
+              copy_async_16(to + k * kThreads, from + k * kThreads);
+        }
+      }
+      commit_copies();
+    };
+    for (int t = 0; t < kStages - 1; ++t) issue(t);
+    uint4 x[NV];
+    auto fetch = [&](int tile) {
+      wait_copies<kStages - 2>();  // (one group a tile: this tile's is done)
+      const uint4* from = ring + tile % kStages * kTile;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) x[k] = from[k * kThreads];
+      if (!whole(tile)) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (first + tile * kTile + k * kThreads + tid >= end)
+            x[k] = make_uint4(none, none, none, none);
       }
     };
-    load(x, 0);
     auto get = [&](int k, int e) {
       const uint32_t w = reinterpret_cast<const uint32_t*>(&x[k])[sizeof(T) == 4 ? e : e >> 1];
       if constexpr (sizeof(T) == 4) return __uint_as_float(w);
@@ -281,13 +390,19 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
       if (!(extra < INFINITY)) extra = -INFINITY;
     }
     if (tid == 0) n_list = 0;
-    // The maximum of the tile: NaN is passed over, +inf (which counts as masked) cleared.
+    fetch(0);
+    // The maximum of the tile, in which NaN and +inf (both count as masked) are cleared.
+    float vec_top[NV];
     auto tile_top = [&]() {
       float m = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k) {
+        float t = get(k, 0);
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) m = fmax3(m, get(k, e), get(k, e + 1));
+        for (int e = 1; e + 1 < PER; e += 2) t = max3_nan(t, get(k, e), get(k, e + 1));
+        vec_top[k] = max3_nan(t, t, get(k, PER - 1));
+        m = max3_nan(m, m, vec_top[k]);
+      }
       return m;
     };
     auto clean_top = [&]() {
@@ -347,20 +462,11 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
     floor_k = fmaxf(floor_k, kMasked);  // fewer than K maxima: every element that counts
 
     // The sum of exponentials, 2^e times `sum`, and the elements that reach the threshold.
-    // Logits below -2^20 are taken as -2^20: that counts only where the part has no
-    // larger ones, and then the second pass below does.
+    // (Against the first exponent, 2^-(2^20 log2 e), logits below -2^20 add nothing: where a part
+    // has no larger ones, the second pass below sums them.)
     float top = -INFINITY, sum = 0.f;
     int e_run = (int)(-kPlain * kLog2e);
     const uint64_t l2 = f2_pack(kLog2e, kLog2e), ll2 = f2_pack(kLog2eLo, kLog2eLo);
-    const uint64_t magic = f2_pack(12582912.f, 12582912.f);  // 1.5 * 2^23: rounds to integers
-    const uint64_t nmagic = f2_pack(-12582912.f, -12582912.f);
-    const uint64_t c6 = f2_pack(0.00015353362f, 0.00015353362f);
-    const uint64_t c5 = f2_pack(0.0013398874f, 0.0013398874f);
-    const uint64_t c4 = f2_pack(0.009618437f, 0.009618437f);
-    const uint64_t c3 = f2_pack(0.055503324f, 0.055503324f);
-    const uint64_t c2 = f2_pack(0.24022648f, 0.24022648f);
-    const uint64_t c1 = f2_pack(0.6931472f, 0.6931472f);
-    const uint64_t one = f2_pack(1.f, 1.f);
     auto offer = [&](float v, int at) {
       if (v >= floor_k) {
         const int i = atomicAdd(&n_list, 1);
@@ -368,9 +474,11 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
       }
     };
     for (int tile = 0; tile < p.tiles; ++tile) {
-      uint4 next[NV];
-      if (tile + 1 < p.tiles) load(next, tile + 1);
-      if (tile > 0) m = clean_top();
+      if (tile > 0) {
+        fetch(tile);
+        m = clean_top();
+      }
+      issue(tile + kStages - 1);
       if (m > top) {
         top = m;
         const int e = (int)ceilf(fminf(fmaxf(m, -kPlain), kPlain) * kLog2e);
@@ -379,28 +487,13 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
           e_run = e;
         }
       }
-      const float low = fmaxf(top - 80.f, -kPlain);  // exp of less adds nothing that counts
-      const int shift = 0x4b400000 + e_run;          // the magic number's bits, and E
+      const uint64_t ne = f2_pack(-(float)e_run, -(float)e_run);
       uint64_t acc[2] = {0ull, 0ull};
       auto add = [&](float x0, float x1, int w) {
-        const uint64_t y = f2_pack(fmaxf(x0, low), fmaxf(x1, low));
-        const uint64_t t = f2_fma(y, l2, magic);
-        const uint64_t n = f2_add(t, nmagic) ^ 0x8000000080000000ull;  // -n
-        uint64_t f = f2_fma(y, l2, n);
-        f = f2_fma(y, ll2, f);
-        uint64_t q = f2_fma(c6, f, c5);
-        q = f2_fma(q, f, c4);
-        q = f2_fma(q, f, c3);
-        q = f2_fma(q, f, c2);
-        q = f2_fma(q, f, c1);
-        q = f2_fma(q, f, one);
-        float t0, t1, q0, q1;
-        f2_unpack(t, t0, t1);
-        f2_unpack(q, q0, q1);
-        // 2^(n - E) goes into the exponent: n - E lies in [-118, 1]
-        q0 = __uint_as_float(__float_as_uint(q0) + ((__float_as_uint(t0) - shift) << 23));
-        q1 = __uint_as_float(__float_as_uint(q1) + ((__float_as_uint(t1) - shift) << 23));
-        acc[w] = f2_add(acc[w], f2_pack(q0, q1));
+        const uint64_t y = f2_pack(x0, x1);
+        float t0, t1;
+        f2_unpack(f2_fma(y, ll2, f2_fma(y, l2, ne)), t0, t1);
+        acc[w] = f2_add(acc[w], f2_pack(fast_exp2(t0), fast_exp2(t1)));
       };
 #pragma unroll
       for (int k = 0; k < NV; ++k)
@@ -414,23 +507,23 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
         const int at = head + (first + tile * NV * kThreads + tid) * PER;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
+          if (vec_top[k] >= floor_k) {
 #pragma unroll
-          for (int e = 0; e < PER; ++e) offer(get(k, e), at + k * kThreads * PER + e);
+            for (int e = 0; e < PER; ++e) offer(get(k, e), at + k * kThreads * PER + e);
+          }
         if (tile == 0) offer(extra, v_extra);
       }
-#pragma unroll
-      for (int k = 0; k < NV; ++k) x[k] = next[k];
     }
+    wait_copies<0>();
     // the block's maximum, then the threads' sums against its exponent
     float block_top = top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       block_top = fmaxf(block_top, __shfl_xor_sync(0xffffffffu, block_top, o));
-    __syncthreads();
-    if (lane == 0) sh_top[warp] = block_top;
+    if (lane == 0) tops[warp] = block_top;  // (the maxima there have been read)
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) block_top = fmaxf(block_top, sh_top[w]);
+    for (int w = 0; w < kWarps; ++w) block_top = fmaxf(block_top, tops[w]);
     const bool far = !(fabsf(block_top) <= kPlain);  // (also: no element)
     const float base = far ? block_top : 0.f;
     const int e_top = far ? 0 : (int)ceilf(block_top * kLog2e);
@@ -447,12 +540,11 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
       if (extra >= kMasked) f(extra, v_extra);
     };
     if (!far) {
-      if (top > -INFINITY && e_run - e_top > -100)
-        fixed = __double2ull_rn((double)sum * (kUnit * pow2(e_run - e_top)));
+      if (top > -INFINITY) fixed = in_units(sum, max(e_run - e_top, -200));
     } else if (block_top > -INFINITY) {
       float s = 0.f;
       again([&](float y, int) { s += expf(y - block_top); });
-      fixed = __double2ull_rn((double)s * kUnit);
+      fixed = in_units(s, 0);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
@@ -501,30 +593,32 @@ __global__ void __launch_bounds__(kThreads, 3) beam_kernel(const __grid_constant
       part->n = min(n, K);
     }
   }
-  // the last block of the row joins its parts, the last row's of the group chooses
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    const bool last = atomicAdd(p.row_count + slot, 1) == p.splits - 1;
-    if (last) p.row_count[slot] = 0;
-    last_of = last;
+  // The last block joins and chooses: of the group where its rows' parts are few, else
+  // of each row, and then of the group's rows.
+  const int group = slot / K, slot0 = group * K, R = p.one_join ? K : 1;
+  Joined j;
+  j.keys = reinterpret_cast<unsigned long long*>(scratch);
+  j.best = j.keys + R * p.splits * K;
+  j.score = j.best + K * K;
+  j.lse = reinterpret_cast<double*>(j.score + K * K);
+  j.flat = reinterpret_cast<int*>(j.lse + K);
+  j.chosen = j.flat + K * K;
+  j.token = j.chosen + K;
+  if (p.one_join) {
+    if (!last_here(p.group_count + group, K * p.splits, &last_of)) return;
+    join_rows(p, slot0, K, j);
+  } else {
+    if (!last_here(p.row_count + slot, p.splits, &last_of)) return;
+    join_rows(p, slot, 1, j);
+    for (int i = tid; i < K; i += kThreads) p.row_best[(size_t)slot * K + i] = j.best[i];
+    if (tid == 0) p.row_lse[slot] = j.lse[0];
+    if (!last_here(p.group_count + group, K, &last_of)) return;
+    for (int i = tid; i < K * K; i += kThreads)
+      j.best[i] = __ldcg(p.row_best + (size_t)slot0 * K + i);
+    for (int i = tid; i < K; i += kThreads) j.lse[i] = __ldcg(p.row_lse + slot0 + i);
+    __syncthreads();
   }
-  __syncthreads();
-  if (!last_of) return;
-  __threadfence();
-  if (!skip) join_row(p, slot, reinterpret_cast<unsigned long long*>(scratch));
-  __threadfence();
-  __syncthreads();
-  const int group = slot / K;
-  if (tid == 0) {
-    const bool last = atomicAdd(p.group_count + group, 1) == K - 1;
-    if (last) p.group_count[group] = 0;
-    last_of = last;
-  }
-  __syncthreads();
-  if (!last_of) return;
-  __threadfence();
-  choose(p, group, scratch);
+  choose(p, group, j);
 }
 
 size_t take(size_t& off, size_t bytes) {
@@ -550,23 +644,26 @@ BeamWs beam_ws(int n_groups, int beams, int vocab, int n_sms) {
   // (whole vectors are counted from the row's first 16-byte boundary: never more than
   // vocab elements' worth)
   w.splits = (int)(blocks(w.held, w.tiles) / (long long)slots);
+  // all parts of a group are joined at once where each thread has but a few of their
+  // best (an entry counts those of its row)
+  w.one_join = (long long)beams * beams * w.splits <= 4 * kThreads;
   if (w.splits < 1) w.splits = 1;
   w.part_bytes = sizeof(Part) + (sizeof(Best) * beams + 15) / 16 * 16;
   size_t off = 0;
   w.row_count = take(off, slots * 4);
   w.group_count = take(off, (size_t)n_groups * 4);
-  w.row_n = take(off, slots * 4);
   w.row_lse = take(off, slots * 8);
-  w.row_best = take(off, slots * beams * sizeof(Best));
+  w.row_best = take(off, slots * beams * 8);
   w.parts = take(off, slots * w.splits * w.part_bytes);
   w.total = off;
   return w;
 }
 
 cudaError_t launch_beam(const BeamParams& p, bool f32, int held, cudaStream_t s) {
-  const size_t join = (size_t)p.splits * p.beams * 8;
-  const size_t pick = (size_t)p.beams * p.beams * 12 + 8 * (size_t)p.beams;
-  const size_t smem = join > pick ? join : pick;
+  const size_t K = p.beams;
+  const size_t join = (p.one_join ? K : 1) * p.splits * K * 8 + K * K * 20 + K * 16;
+  const size_t ring = (size_t)kStages * held * (f32 ? 4 : 2) * kThreads;  // join follows it
+  const size_t smem = join > ring ? join : ring;
   const unsigned grid = (unsigned)(p.n_groups * p.beams) * (unsigned)p.splits;
   auto go = [&](auto kern) -> cudaError_t {
     if (smem > 40 * 1024) {

@@ -206,9 +206,8 @@ struct RotaryParams {
   int n_seqs;
   bool clear, copy_rest;
   // set by launch_rotary
-  int tokens, pair_units, units;
-  uint32_t row_units;
-  FastDiv by_T, by_half, by_row, by_units;
+  int pair_units, units, split;
+  FastDiv by_T, by_units, by_split;
 };
 cudaError_t launch_rotary(RotaryParams& p, bool f32, bool interleaved, int n_sms, cudaStream_t s);
 
@@ -226,14 +225,17 @@ struct BeamParams {
   int32_t* history_out;     // or null
   // scratch: see beam_ws
   size_t part_bytes;
-  int *row_count, *group_count, *row_n;
+  bool one_join;            // all rows of a group joined by one block
+  int *row_count, *group_count;
   double* row_lse;
-  uint8_t *row_best, *parts;
+  unsigned long long* row_best;
+  uint8_t* parts;
 };
 struct BeamWs {
   int held, tiles, splits;  // elements of a thread's tile, tiles of a block, blocks of a row
   size_t part_bytes;
-  size_t row_count, group_count, row_n, row_lse, row_best, parts, total;
+  bool one_join;
+  size_t row_count, group_count, row_lse, row_best, parts, total;
 };
 BeamWs beam_ws(int n_groups, int beams, int vocab, int n_sms);
 cudaError_t launch_beam(const BeamParams& p, bool f32, int held, cudaStream_t s);

@@ -9,10 +9,11 @@
 // signed fraction of half a turn, go to sincospif: off by 2^-32 of a turn from the
 // cut and 2^-24 of itself from the conversion.
 //
-// The rows are read once and written once, so the kernel is bound by memory.  A block
-// takes a few tokens, forms their cosines and sines once in shared memory and uses
-// them for every head of Q and K; a thread moves 16-byte vectors, four units of two
-// vectors in flight.
+// The rows are read once and written once, so the kernel is bound by memory.  A thread
+// has a token and two vectors of 16 bytes of its rows (the two parts of eight pairs), forms
+// their cosines and sines once in registers and goes through the heads of Q and K with
+// them, four heads' loads in flight; no shared memory, no barrier.  With few tokens the
+// heads are shared out over several threads, which then form the same sines.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,8 +24,7 @@ namespace saf {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // tokens of a block
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 4;  // heads in flight
 
 template <int BYTES>
 struct Raw;
@@ -69,139 +69,129 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
   return (__umulhi(n, f.m) + n) >> f.s;
 }
 
-template <typename T, int W, bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
-  extern __shared__ float tab[];  // [tokens][half] cosines, then as many sines
-  __shared__ int64_t row_at[4][kMaxTokens];  // q, k, q_out, k_out: where a token's row starts
-  __shared__ int pos_of[kMaxTokens], state_of[kMaxTokens];  // 0: left alone, 1: turned, 2: cleared
-  const int half = p.rot / 2;
-  float* cosv = tab;
-  float* sinv = tab + p.tokens * half;
-  const long long n0 = (long long)blockIdx.x * p.tokens;
-  const int nt = (int)min((long long)p.tokens, (long long)p.B * p.T - n0);
-  if ((int)threadIdx.x < nt) {
-    const uint32_t n = (uint32_t)(n0 + threadIdx.x);
-    const uint32_t b = fast_div(n, p.by_T), t = n - b * (uint32_t)p.T;
-    int pos = (int)t;
-    bool live = true;
-    if (p.positions) {
-      pos = p.positions[n];
-    } else if (p.cu) {
-      // the last sequence that starts at or before the row, and holds it
-      int lo = 0, hi = p.n_seqs;  // cu[lo] <= t for lo > 0 or t >= cu[0]; cu[hi] > t or hi = n_seqs
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu[mid] <= (int)t) lo = mid;
-        else hi = mid;
-      }
-      const int a = p.n_seqs > 0 ? p.cu[lo] : 0;
-      live = p.n_seqs > 0 && a <= (int)t && (int)t < p.cu[lo + 1];
-      pos = (int)t - a;
-    } else if (p.seq_len) {
-      const int fresh = p.n_new ? max(0, min(p.n_new[b], p.T)) : p.T;
-      live = (int)t < fresh;
-      pos = p.seq_len[b] - fresh + (int)t;
+// The position of row t of sequence b; false where the row is not worked on.
+__device__ __forceinline__ bool position(const RotaryParams& p, uint32_t n, uint32_t b, uint32_t t,
+                                         int& pos) {
+  pos = (int)t;
+  if (p.positions) {
+    pos = __ldg(p.positions + n);
+  } else if (p.cu) {
+    // the last sequence that starts at or before the row holds it, if any does
+    int lo = 0, hi = p.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu + mid) <= (int)t) lo = mid;
+      else hi = mid;
     }
-    pos_of[threadIdx.x] = pos;
-    state_of[threadIdx.x] = live ? 1 : p.clear ? 2 : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      row_at[i][threadIdx.x] = (int64_t)b * p.x[i].seq + (int64_t)t * p.x[i].row;
+    if (p.n_seqs == 0) return false;
+    const int a = __ldg(p.cu + lo);
+    pos = (int)t - a;
+    return a <= (int)t && (int)t < __ldg(p.cu + lo + 1);
+  } else if (p.seq_len) {
+    const int fresh = p.n_new ? max(0, min(__ldg(p.n_new + b), p.T)) : p.T;
+    pos = __ldg(p.seq_len + b) - fresh + (int)t;
+    return (int)t < fresh;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int tok = (int)fast_div((uint32_t)i, p.by_half), j = i - tok * half;
-    const uint64_t phase = (uint64_t)(int64_t)pos_of[tok] * p.turns[j];  // modulo one turn
-    float s, c;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    cosv[i] = c * p.scale;
-    sinv[i] = s * p.scale_sin;
-  }
-  __syncthreads();
-  const int total = nt * (int)p.row_units;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kUnroll) {
-    Vec<T, W> a[kUnroll], b[kUnroll];
-    T *to_a[kUnroll], *to_b[kUnroll];
-    int at[kUnroll];  // >= 0: offset of the pair's cosines; -1: copied; -2: cleared; -3: nothing
+  return true;
+}
+
+// Turns (TURN) or copies two vectors of every head h0, h0 + step, ... of one tensor.
+template <typename T, int W, bool HALF, bool TURN>
+__device__ __forceinline__ void heads(const RotaryRows& in, const RotaryRows& out, uint32_t b,
+                                      uint32_t t, int n_heads, int h0, int step, int ea, int eb,
+                                      bool has_b, const float (&c)[W], const float (&s)[W]) {
+  using V = Vec<T, W>;
+  const T* src = static_cast<const T*>(in.p) + (int64_t)b * in.seq + (int64_t)t * in.row;
+  T* dst = static_cast<T*>(out.p) + (int64_t)b * out.seq + (int64_t)t * out.row;
+  for (int h = h0; h < n_heads; h += kUnroll * step) {
+    V x[kUnroll], y[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int i = i0 + k * kThreads;
-      at[k] = -3;
-      to_a[k] = to_b[k] = nullptr;
-      if (i >= total) continue;
-      const int tok = (int)fast_div((uint32_t)i, p.by_row);
-      const int r = i - tok * (int)p.row_units;
-      const int h = (int)fast_div((uint32_t)r, p.by_units), u = r - h * p.units;
-      const int st = state_of[tok];
-      if (st == 0) continue;
-      const bool isk = h >= p.H;
-      const int hh = isk ? h - p.H : h;
-      const RotaryRows& in = p.x[isk ? 1 : 0];
-      const RotaryRows& out = p.x[isk ? 3 : 2];
-      const T* src = static_cast<const T*>(in.p) + row_at[isk ? 1 : 0][tok] + (int64_t)hh * in.head;
-      T* dst = static_cast<T*>(out.p) + row_at[isk ? 3 : 2][tok] + (int64_t)hh * out.head;
-      int ea, eb;
-      if (u < p.pair_units) {
-        ea = HALF ? u * W : 2 * u * W;
-        eb = HALF ? half + u * W : ea + W;
-        at[k] = tok * half + u * W;
-      } else {
-        ea = p.rot + 2 * (u - p.pair_units) * W;
-        eb = ea + W;
-        at[k] = -1;
-      }
-      if (st == 2) at[k] = -2;
-      to_a[k] = dst + ea;
-      to_b[k] = eb < p.d ? dst + eb : nullptr;
-      if (st == 2) {
-        a[k].raw = {};
-        b[k].raw = {};
-      } else {
-        a[k].raw = *reinterpret_cast<const decltype(a[k].raw)*>(src + ea);
-        if (eb < p.d) b[k].raw = *reinterpret_cast<const decltype(b[k].raw)*>(src + eb);
-      }
+      if (h + k * step >= n_heads) continue;
+      const T* q = src + (int64_t)(h + k * step) * in.head;
+      x[k].raw = *reinterpret_cast<const decltype(x[k].raw)*>(q + ea);
+      if (TURN || has_b) y[k].raw = *reinterpret_cast<const decltype(x[k].raw)*>(q + eb);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      if (at[k] >= 0) {
-        const float* c = cosv + at[k];
-        const float* s = sinv + at[k];
-        if constexpr (HALF) {
-          if constexpr (W == 1) {
-            const float x = a[k].get(0), y = b[k].get(0);
-            a[k].set1(x * c[0] - y * s[0]);
-            b[k].set1(y * c[0] + x * s[0]);
-          } else {
+      if (h + k * step >= n_heads) continue;
+      if constexpr (TURN) {
+        V& a = x[k];
+        V& d = y[k];
+        if constexpr (W == 1) {
+          const float p = a.get(0), q = d.get(0);
+          a.set1(p * c[0] - q * s[0]);
+          d.set1(q * c[0] + p * s[0]);
+        } else if constexpr (HALF) {
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
-              const float x0 = a[k].get(e), x1 = a[k].get(e + 1);
-              const float y0 = b[k].get(e), y1 = b[k].get(e + 1);
-              a[k].set2(e, x0 * c[e] - y0 * s[e], x1 * c[e + 1] - y1 * s[e + 1]);
-              b[k].set2(e, y0 * c[e] + x0 * s[e], y1 * c[e + 1] + x1 * s[e + 1]);
-            }
+          for (int e = 0; e < W; e += 2) {
+            const float p0 = a.get(e), p1 = a.get(e + 1), q0 = d.get(e), q1 = d.get(e + 1);
+            a.set2(e, p0 * c[e] - q0 * s[e], p1 * c[e + 1] - q1 * s[e + 1]);
+            d.set2(e, q0 * c[e] + p0 * s[e], q1 * c[e + 1] + p1 * s[e + 1]);
           }
         } else {
-          if constexpr (W == 1) {
-            const float x = a[k].get(0), y = b[k].get(0);
-            a[k].set1(x * c[0] - y * s[0]);
-            b[k].set1(y * c[0] + x * s[0]);
-          } else {
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
-              const float x0 = a[k].get(e), y0 = a[k].get(e + 1);
-              const float x1 = b[k].get(e), y1 = b[k].get(e + 1);
-              const int q0 = e / 2, q1 = W / 2 + e / 2;
-              a[k].set2(e, x0 * c[q0] - y0 * s[q0], y0 * c[q0] + x0 * s[q0]);
-              b[k].set2(e, x1 * c[q1] - y1 * s[q1], y1 * c[q1] + x1 * s[q1]);
-            }
+          for (int e = 0; e < W; e += 2) {
+            const float p0 = a.get(e), q0 = a.get(e + 1), p1 = d.get(e), q1 = d.get(e + 1);
+            const int i = e / 2, j = W / 2 + e / 2;
+            a.set2(e, p0 * c[i] - q0 * s[i], q0 * c[i] + p0 * s[i]);
+            d.set2(e, p1 * c[j] - q1 * s[j], q1 * c[j] + p1 * s[j]);
           }
         }
       }
-      if (at[k] > -3) {
-        *reinterpret_cast<decltype(a[k].raw)*>(to_a[k]) = a[k].raw;
-        if (to_b[k]) *reinterpret_cast<decltype(b[k].raw)*>(to_b[k]) = b[k].raw;
+      T* q = dst + (int64_t)(h + k * step) * out.head;
+      *reinterpret_cast<decltype(x[k].raw)*>(q + ea) = x[k].raw;
+      if (TURN || has_b) *reinterpret_cast<decltype(x[k].raw)*>(q + eb) = y[k].raw;
+    }
+  }
+}
+
+template <typename T, int W, bool HALF>
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
+  const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
+  const uint32_t r = fast_div(i, p.by_units), u = i - r * (uint32_t)p.units;
+  const uint32_t n = fast_div(r, p.by_split);           // the row of B * T
+  const int g = (int)(r - n * (uint32_t)p.split);       // the first of its heads
+  if (n >= (uint32_t)p.B * (uint32_t)p.T) return;
+  const uint32_t b = fast_div(n, p.by_T), t = n - b * (uint32_t)p.T;
+  int pos;
+  const bool live = position(p, n, b, t, pos);
+  if (!live && !p.clear) return;
+  const int half = p.rot / 2;
+  const bool pair = u < (uint32_t)p.pair_units;
+  const int ea = pair ? (HALF ? (int)u * W : 2 * (int)u * W)
+                      : p.rot + 2 * ((int)u - p.pair_units) * W;
+  const int eb = pair && HALF ? half + (int)u * W : ea + W;
+  const bool has_b = eb < p.d;
+  // heads are counted over Q and K: this thread's first of K
+  const int k0 = ((g - p.H) % p.split + p.split) % p.split;
+  float c[W], s[W];
+  if (!live) {
+    Vec<T, W> zero;
+    zero.raw = {};
+    for (int x = 0; x < 2; ++x) {
+      const RotaryRows& out = p.x[2 + x];
+      T* dst = static_cast<T*>(out.p) + (int64_t)b * out.seq + (int64_t)t * out.row;
+      for (int h = x ? k0 : g; h < (x ? p.H_k : p.H); h += p.split) {
+        *reinterpret_cast<decltype(zero.raw)*>(dst + (int64_t)h * out.head + ea) = zero.raw;
+        if (has_b)
+          *reinterpret_cast<decltype(zero.raw)*>(dst + (int64_t)h * out.head + eb) = zero.raw;
       }
     }
+  } else if (pair) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      // the phase modulo one turn, in 2^-64
+      const uint64_t phase = (uint64_t)(int64_t)pos * __ldg(p.turns + u * W + e);
+      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[e], &c[e]);
+      c[e] *= p.scale;
+      s[e] *= p.scale_sin;
+    }
+    heads<T, W, HALF, true>(p.x[0], p.x[2], b, t, p.H, g, p.split, ea, eb, true, c, s);
+    heads<T, W, HALF, true>(p.x[1], p.x[3], b, t, p.H_k, k0, p.split, ea, eb, true, c, s);
+  } else {
+    heads<T, W, HALF, false>(p.x[0], p.x[2], b, t, p.H, g, p.split, ea, eb, has_b, c, s);
+    heads<T, W, HALF, false>(p.x[1], p.x[3], b, t, p.H_k, k0, p.split, ea, eb, has_b, c, s);
   }
 }
 
@@ -214,13 +204,13 @@ FastDiv make_div(uint32_t d) {
 }
 
 template <typename T>
-cudaError_t launch(RotaryParams& p, int W, bool half, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch(const RotaryParams& p, int W, bool half, unsigned grid, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   trace_begin(s);
-  if (W == V && half) rotary_kernel<T, V, true><<<grid, kThreads, smem, s>>>(p);
-  else if (W == V) rotary_kernel<T, V, false><<<grid, kThreads, smem, s>>>(p);
-  else if (half) rotary_kernel<T, 1, true><<<grid, kThreads, smem, s>>>(p);
-  else rotary_kernel<T, 1, false><<<grid, kThreads, smem, s>>>(p);
+  if (W == V && half) rotary_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
+  else if (W == V) rotary_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p);
+  else if (half) rotary_kernel<T, 1, true><<<grid, kThreads, 0, s>>>(p);
+  else rotary_kernel<T, 1, false><<<grid, kThreads, 0, s>>>(p);
   trace_end(s, "rotary");
   return cudaGetLastError();
 }
@@ -234,27 +224,27 @@ cudaError_t launch_rotary(RotaryParams& p, bool f32, bool interleaved, int n_sms
   bool wide = half % V == 0 && p.d % V == 0;
   for (int i = 0; i < 4; ++i) {
     const RotaryRows& x = p.x[i];
-    if (p.H_k == 0 && (i & 1)) continue;
+    if ((i & 1 ? p.H_k : p.H) == 0) continue;
     wide &= reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.seq % V == 0 && x.row % V == 0 &&
             x.head % V == 0;
   }
   const int W = wide ? V : 1;
   p.pair_units = half / W;
   p.units = p.pair_units + (p.copy_rest ? ((p.d - p.rot) / W + 1) / 2 : 0);
-  p.row_units = (uint32_t)p.units * (p.H + p.H_k);
-  // tokens of a block: as many as keep four blocks for each SM (fewer sines to form
-  // and more bytes in flight per block against an idle part of the GPU)
-  const long long n = (long long)p.B * p.T;
-  p.tokens = kMaxTokens;
-  while (p.tokens > 1 && (n + p.tokens - 1) / p.tokens < 4ll * n_sms) p.tokens /= 2;
+  // Threads of a token's unit: one, as long as that fills every SM twice (768 threads
+  // each); up to one for each head where there are few tokens.
+  const long long n = (long long)p.B * p.T, want = 2ll * 768 * n_sms;
+  const long long fits = ((1ll << 31) - kThreads) / (n * p.units);
+  long long split = (want + n * p.units - 1) / (n * p.units);
+  if (split > p.H + p.H_k) split = p.H + p.H_k;
+  p.split = (int)(split > fits ? fits : split);
+  if (p.split < 1) return cudaErrorInvalidValue;
   p.by_T = make_div((uint32_t)p.T);
-  p.by_half = make_div((uint32_t)half);
-  p.by_row = make_div(p.row_units);
   p.by_units = make_div((uint32_t)p.units);
-  const int grid = (int)((n + p.tokens - 1) / p.tokens);
-  const size_t smem = (size_t)p.tokens * half * 2 * sizeof(float);
-  return f32 ? launch<float>(p, W, !interleaved, grid, smem, s)
-             : launch<__nv_bfloat16>(p, W, !interleaved, grid, smem, s);
+  p.by_split = make_div((uint32_t)p.split);
+  const unsigned grid = (unsigned)((n * p.units * p.split + kThreads - 1) / kThreads);
+  return f32 ? launch<float>(p, W, !interleaved, grid, s)
+             : launch<__nv_bfloat16>(p, W, !interleaved, grid, s);
 }
 
 }  // namespace saf

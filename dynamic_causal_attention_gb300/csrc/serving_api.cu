@@ -67,8 +67,9 @@ saf_status saf_rotary(const saf_rotary_dims* dims, const saf_rows* q, const saf_
   if ((positions != nullptr) + (cu_seqlens != nullptr) + (seq_len != nullptr) > 1 ||
       (n_new && !seq_len) || n_seqs < 0 || (cu_seqlens && d.B > 1))
     return SAF_ERR_INVALID_ARG;
+  // pairs and copied parts of all rows are counted in 31 bits
   if (d.d_h > 256 || d.H > kMaxHeads || d.H_k > kMaxHeads ||
-      (long long)d.B * d.T > (1ll << 31) - 64)
+      (long long)d.B * d.T > ((1ll << 31) - 1024) / d.d_h)
     return SAF_ERR_UNSUPPORTED;
   if (d.B == 0 || d.T == 0 || d.H + d.H_k == 0) return SAF_OK;
   if (!turns || !aligned(turns, 8) || !isfinite(scale)) return SAF_ERR_INVALID_ARG;
@@ -165,14 +166,14 @@ saf_status saf_beam_step(const saf_beam_dims* dims, const void* logits, const fl
   p.score_out = score_out;
   p.finished_out = finished_out;
   p.history_out = history_out;
+  p.one_join = w.one_join;
   p.tiles = w.tiles;
   p.splits = w.splits;
   p.part_bytes = w.part_bytes;
   p.row_count = reinterpret_cast<int*>(ws + w.row_count);
   p.group_count = reinterpret_cast<int*>(ws + w.group_count);
-  p.row_n = reinterpret_cast<int*>(ws + w.row_n);
   p.row_lse = reinterpret_cast<double*>(ws + w.row_lse);
-  p.row_best = ws + w.row_best;
+  p.row_best = reinterpret_cast<unsigned long long*>(ws + w.row_best);
   p.parts = ws + w.parts;
   return status_of(launch_beam(p, f32, w.held, static_cast<cudaStream_t>(stream)));
 }

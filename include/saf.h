@@ -467,7 +467,7 @@ typedef struct saf_rows {
 } saf_rows;
 
 typedef struct saf_rotary_dims {
-  int B, T;         /* sequences and rows of each, B * T < 2^31 - 63            */
+  int B, T;         /* sequences and rows of each, B * T * d_h <= 2^31 - 1024   */
   int H, H_k;       /* heads of q and of k (either may be 0), up to 256         */
   int d_h;          /* 1..256                                                   */
   int rot;          /* components that are turned, the first of each row: even, *

@@ -122,25 +122,35 @@ __device__ __forceinline__ BItem decode_bwd(const BwdParams& p, int it) {
   return r;
 }
 
-// The same for sequences laid end to end: the plan's records of key tiles (most query
-// tiles first) under the K/V heads, in groups of p.pairs_per_group K/V heads.
+// The same for sequences laid end to end (packed_prep.cu makes the items; few rounds of them are
+// shared out there, entry round * grid + cta, many go by the snake order).
 __device__ __forceinline__ BItem decode_bwd(const PackedBwdParams& p, int it) {
   BItem r;
-  const int nt = p.hdr[0], G = p.pairs_per_group;
-  const int g = it / (G * nt);                       // the last group may be smaller
-  const int gs = min(G, p.n_kv - g * G), w = it - g * G * nt;
-  const int rank = w / gs;
-  const int4 t = p.tiles[rank];
+  const int4 t = p.hdr[0] * p.n_kv <= kOrderRounds * (int)gridDim.x
+                     ? __ldg(p.order + it)
+                     : packed_bwd_item(p.items, p.hdr[0], it);
   r.b = 0;
-  r.kv = p.kv_list[g * G + (w - rank * gs)];
+  r.kv = t.z >> 16;
+  r.J = t.z & 0xffff;
   r.row0 = t.x;
   r.len = t.y;
-  r.J = t.z;
   r.tile0 = t.w;
   r.span = (r.len + 127) / 128 - r.J;
   r.db = p.dyn_begin[r.kv];
   r.nsteps = p.dyn_count[r.kv] * r.span;
   return r;
+}
+
+// Item of round k of this CTA, or one behind the last.
+__device__ __forceinline__ int bwd_item(const BwdParams&, int k, int) {
+  return snake_item(k, blockIdx.x, gridDim.x);
+}
+__device__ __forceinline__ int bwd_item(const PackedBwdParams& p, int k, int n_items) {
+  if (p.hdr[0] * p.n_kv > kOrderRounds * (int)gridDim.x)
+    return snake_item(k, blockIdx.x, gridDim.x);
+  // (the list ends with a round of empty entries)
+  const int it = k * (int)gridDim.x + (int)blockIdx.x;
+  return __ldg(&p.order[it].y) > 0 ? it : n_items;
 }
 
 template <bool PACKED>
@@ -268,9 +278,19 @@ __global__ void __launch_bounds__(512, 1)
   const uint32_t sDST = smem_u32(smem + L::OFF_DST);
   const int H = p.H, T = p.T;
   const int n_items = [&] {
-    if constexpr (PACKED) return p.hdr[0] * p.n_kv;
-    else return p.n_items;
+    if constexpr (PACKED) {
+      // (shared out: entries of the list lie anywhere below its length)
+      const int n = p.hdr[0] * p.n_kv, listed = kOrderRounds * (int)gridDim.x;
+      return n > listed ? n : listed + (int)gridDim.x;
+    } else {
+      return p.n_items;
+    }
   }();
+
+  // The next item of a role, n_items or more behind the last: by the snake order, or
+  // (packed) as the pre-pass has shared them out.
+  int round = 0;
+  auto next_item = [&] { return bwd_item(p, round++, n_items); };
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
@@ -278,8 +298,7 @@ __global__ void __launch_bounds__(512, 1)
     // per tile chunk issues its copy (one issuing thread moves about 29 bytes
     // per clock from L2, four about 74) and two more the -lse/-D vectors.
     uint32_t kvc = 0, qc = 0;
-    for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+    for (int it = next_item(); it < n_items; it = next_item()) {
       const BItem w = decode_bwd(p, it);
       const int kvrow0 = PACKED ? w.row0 : (w.b * p.H_kv + w.kv) * T;
       uint64_t* kv_bar = PACKED && w.len - w.J * 128 < 128 ? kv_tail : kv_full;
@@ -338,8 +357,7 @@ __global__ void __launch_bounds__(512, 1)
     // ---------------------------------------------------------- ends of sequences
     if constexpr (PACKED) {
       uint32_t qc = 0, kvt = 0, used = 0, par = 0;  // by stage: ever used, the next parity
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-           it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = next_item(); it < n_items; it = next_item()) {
         const BItem w = decode_bwd(p, it);
         const int keys = w.len - w.J * 128;
         if (keys < 128) {
@@ -426,8 +444,7 @@ __global__ void __launch_bounds__(512, 1)
       uint32_t sfc = 0;
       if constexpr (L::PS) {
         // S^T and dP^T only; warp 3 issues dV, dK and dQ.
-        for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+        for (int it = next_item(); it < n_items; it = next_item()) {
           const BItem w = decode_bwd(p, it);
           mbar_wait(kv_full, kvc & 1, wc, kSiteBMmaKV);
           ++kvc;
@@ -457,8 +474,7 @@ __global__ void __launch_bounds__(512, 1)
       // TMEM; the reduce-adds of dQ then run while the next step computes.
       constexpr uint32_t id_dq = idesc_bf16(128, 128, true, true);
       uint32_t dkc = 0;
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); !L::PS && it < n_items;
-           it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = L::PS ? n_items : next_item(); it < n_items; it = next_item()) {
         const BItem w = decode_bwd(p, it);
         mbar_wait(kv_full, kvc & 1, wc, kSiteBMmaKV);
         ++kvc;
@@ -528,8 +544,7 @@ __global__ void __launch_bounds__(512, 1)
       constexpr uint32_t id_acc = idesc_bf16(128, D, false, true);
       constexpr uint32_t id_dq = idesc_bf16(128, D, true, true);
       uint32_t kvc = 0, qc = 0, pc = 0, dqc = 0, kdc = 0;
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = next_item(); it < n_items; it = next_item()) {
         const BItem w = decode_bwd(p, it);
         mbar_wait(kv_full, kvc & 1, wc, kSiteBMmaKV);  // K_J is the B operand of dQ
         ++kvc;
@@ -577,8 +592,7 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t qc = 0, sc = 0, pc = 0, kdc = 0;
-    for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+    for (int it = next_item(); it < n_items; it = next_item()) {
       const BItem w = decode_bwd(p, it);
       for (int t = 0; t < w.nsteps; ++t) {
         const int qs = qc % L::QST;
@@ -794,8 +808,7 @@ __global__ void __launch_bounds__(512, 1)
     const int r = (warp & 3) * 32 + lane;  // query row i within the tile == TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t dqc = 0;
-    for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+    for (int it = next_item(); it < n_items; it = next_item()) {
       const BItem w = decode_bwd(p, it);
       for (int t = 0; t < w.nsteps; ++t) {
         int hq, I;

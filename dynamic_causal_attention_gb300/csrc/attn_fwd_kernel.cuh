@@ -57,9 +57,10 @@ struct FwdSmem {
   static constexpr int OFF_AUX = OFF_X + 3 * 2 * 128 * 4;
   static constexpr int OFF_BAR = OFF_AUX + AST * AUX_SLOT;
   static constexpr int NBAR =
-      2 * QST + 2 * KST + 2 * VST + 3 * NBUF + 2 + 2 + 2 * AST + 2 + 1;  // NBUF >= NBUF_T
+      2 * QST + 2 * KST + 2 * VST + 3 * NBUF + 2 + 2 + 2 * AST + 2 + 1 + 2 * kItemSlots;  // NBUF >= NBUF_T
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int OFF_ITEM = OFF_MISC + 16;
+  static constexpr int BYTES = OFF_ITEM + 4 * kItemSlots;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
   static_assert(ALLOC <= 232448, "shared memory budget exceeded");
   // a table slot (static items): 128 column values then a 256-entry distance
@@ -137,7 +138,8 @@ __device__ __forceinline__ uint32_t p_col(int kk) {
 
 enum : int {
   kSiteProdQ = 1, kSiteProdK, kSiteProdV, kSiteMmaQ, kSiteMmaK, kSiteMmaS, kSiteMmaV,
-  kSiteMmaP, kSiteMmaO, kSiteCmpS, kSiteCmpP, kSiteCmpPV, kSiteCmpO, kSiteCmpAux
+  kSiteMmaP, kSiteMmaO, kSiteCmpS, kSiteCmpP, kSiteCmpPV, kSiteCmpO, kSiteCmpAux,
+  kSiteItem
 };
 
 struct Item {
@@ -317,6 +319,8 @@ __global__ void __launch_bounds__(384, 1)
   // per MMA-issuing warp (1, 3): all its products done, before TMEM is freed
   uint64_t* mma_drained = aux_empty + L::AST;
   uint64_t* tail_full = mma_drained + 2;    // PACKED: a V tile that ends a sequence landed
+  const ItemRing ring{tail_full + 1, tail_full + 1 + kItemSlots,
+                      reinterpret_cast<volatile int*>(smem + L::OFF_ITEM)};
   float* xmax = reinterpret_cast<float*>(smem + L::OFF_X);  // [2 parity][2 halves][128]
   float* xsum = xmax + 2 * 2 * 128;                         // [2 halves][128]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -342,6 +346,10 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(mma_drained + 1, 1);
     mbar_init(o_empty, 256);
     mbar_init(tail_full, 1);
+    for (int s = 0; s < kItemSlots; ++s) {
+      mbar_init(ring.full + s, 1);
+      mbar_init(ring.empty + s, 11);  // warps 1, 2, 3 and the eight compute warps
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -369,13 +377,30 @@ __global__ void __launch_bounds__(384, 1)
       return p.n_items;
   }();
 
+  // The next item of this role: by the snake order, or (packed) as they are handed out.
+  int round = 0;
+  ItemFeed items_fed;
+  ItemTake<true> lane_items;
+  ItemTake<false> warp_items;
+  auto feed = [&] {
+    if constexpr (PACKED) return items_fed.next(ring, n_items, wc, kSiteItem);
+    else return 0;
+  };
+  auto take_lane = [&] {
+    if constexpr (PACKED) return lane_items.next(ring, n_items, wc, kSiteItem);
+    else return snake_item(round++, blockIdx.x, gridDim.x);
+  };
+  auto take_warp = [&] {
+    if constexpr (PACKED) return warp_items.next(ring, n_items, wc, kSiteItem);
+    else return snake_item(round++, blockIdx.x, gridDim.x);
+  };
+
   if (PACKED && warp == 0) {
     // ------------------------------------------- Q, K and tables of packed sequences
     if constexpr (PACKED) {
       if (lane == 0) {
         uint32_t qc = 0, kc = 0, ac = 0, kn0 = 0, kn1 = 0;
-        for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-             it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+        for (int it = feed(); it < n_items; it = feed()) {
           const Item w = decode_item<TRANSPOSED>(p, it);
           if (!w.is_static) {
             const int qs = qc % L::QST;
@@ -397,6 +422,7 @@ __global__ void __launch_bounds__(384, 1)
                 kpar = ((kc / L::KST) & 1) ^ 1;
                 ++kc;
               }
+              if (j == w.nsteps - 1) items_fed.claim(p.counter);
               mbar_wait(k_empty + ks, kpar, wc, kSiteProdK);
               mbar_arrive_expect_tx(k_full + ks, G::TILE_BYTES);
               for (int c = 0; c < G::NCHUNK; ++c)
@@ -406,6 +432,7 @@ __global__ void __launch_bounds__(384, 1)
           } else {
             for (int step = 0; step < w.nsteps; ++step) {
               const int as = ac % L::AST;
+              if (step == w.nsteps - 1) items_fed.claim(p.counter);
               mbar_wait(aux_empty + as, ((ac / L::AST) & 1) ^ 1, wc, kSiteProdK);
               ++ac;
               mbar_arrive_expect_tx(aux_full + as, L::AUX_BYTES);
@@ -473,8 +500,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         ++vc;
       };
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-           it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = take_warp(); it < n_items; it = take_warp()) {
         const Item w = decode_item<TRANSPOSED>(p, it);
         for (int step = 0; step < w.nsteps; ++step) {
           if (TRANSPOSED) {
@@ -518,8 +544,7 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t qc = 0, kc = 0, vc = 0, ac = 0;
       uint32_t kn0 = 0, kn1 = 0;  // SPLIT: uses of each issuer's K ring
       bool held_q = false;        // the first Q tile was withheld (testing)
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = take_lane(); it < n_items; it = take_lane()) {
         const Item w = decode_item<TRANSPOSED>(p, it);
         if (!w.is_static) {
           const int row0 = (w.b * H + w.h) * T;                           // Q rows
@@ -653,8 +678,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_pair = idesc_bf16(128, 2 * D, false, true);
       uint32_t qc = 0, vc = 0, sc = 0, oc = 0;
       uint32_t kn = 0, sn = 0;  // uses of this issuer's K ring and of S buffer g
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-           it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = take_lane(); it < n_items; it = take_lane()) {
         const Item w = decode_item<TRANSPOSED>(p, it);
         // before the first product into O: the previous item's O has been
         // read out (an issuer without products waits too, so that its
@@ -782,8 +806,7 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
       uint32_t qc = 0, kc = 0, sc = 0;
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = take_lane(); it < n_items; it = take_lane()) {
         const Item w = decode_item<TRANSPOSED>(p, it);
         const uint32_t sc0 = sc;
         if (!w.is_static) {
@@ -829,8 +852,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
       constexpr uint32_t idesc_pair = idesc_bf16(128, 2 * D, false, true);
       uint32_t vc = 0, sc = 0, oc = 0;
-      for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+      for (int it = take_lane(); it < n_items; it = take_lane()) {
         const Item w = decode_item<TRANSPOSED>(p, it);
         const uint32_t sc0 = sc;
         if (!w.is_static) {
@@ -917,8 +939,7 @@ __global__ void __launch_bounds__(384, 1)
     const int pair_bar = 2 + q4;                 // the two warps that share these rows
     uint32_t ac = 0, sc = 0, oc = 0;  // static tables, P ring uses (all steps), items
     uint32_t sn = 0;  // SPLIT: this half's dynamic tiles (uses of S buffer hf)
-    for (int kr = 0, it = snake_item(0, blockIdx.x, gridDim.x); it < n_items;
-         it = snake_item(++kr, blockIdx.x, gridDim.x)) {
+    for (int it = take_warp(); it < n_items; it = take_warp()) {
       const Item w = decode_item<TRANSPOSED>(p, it);
       const uint32_t sc0 = sc;
       if (!w.is_static && SPLIT) {

@@ -50,6 +50,7 @@ inline int static_group(int d_h, int B, bool transposed = false) {
 // come from a plan that the preparing kernel makes on the device.
 struct PackedFwdParams : FwdParams {
   const int* hdr;        // {tiles, groups of static forward items}
+  int* counter;          // items handed out, zero at the start
   const int4* tiles;     // (row0, len, X, tile0), most steps first
   const int2* groups;    // forward: (first record, records) that share X
   int total;             // rows of lse and out_acc
@@ -119,11 +120,26 @@ struct BwdParams {
   __nv_bfloat16* dV;
   int* status;
 };
+// Items of the packed backward, key tiles (most query tiles first) under K/V heads that serve a
+// dynamic query head, in groups of as many K/V heads as keep dQ's sums in L2.
+struct PackedBwdItems {
+  const int4* tiles;   // (row0, len, J, tile0)
+  int n_kv, per_group;
+  int most_steps;      // of an item
+  bool even;           // every K/V head of kv_list serves as many dynamic query heads
+  uint8_t kv_list[kMaxHeads];
+  uint16_t dyn_count[kMaxHeads];
+};
+// Up to so many rounds of the grid are shared out by cost; with more the snake order is
+// as good (the last rounds are a small part).
+constexpr int kOrderRounds = 64;
+
 // The same for sequences laid end to end (lse2 and Dvec lie by tiles: [H, nt_max * 128],
 // dq_acc and dv_acc by rows: [H or H_kv, total, d_h]; pairs_per_group counts K/V heads).
 struct PackedBwdParams : BwdParams {
   const int* hdr;      // {tiles, ...}
-  const int4* tiles;   // (row0, len, J, tile0), most query tiles first
+  const int4* order;   // [kOrderRounds + 1, grid] (row0, len, J | kv << 16, tile0), len 0: none
+  PackedBwdItems items;
   int total, nt_max;
   int64_t dk_row, dk_head, dv_row, dv_head;
 };

@@ -21,7 +21,7 @@ struct PackedPrep {
   int group;                 // tiles of a static forward item
   const int32_t* cu;         // [n_seqs + 1]
   int* status;
-  int* hdr;                  // {tiles, static groups}
+  int* hdr;                  // {tiles, static groups, two counters of items handed out}
   int4 *by_key, *by_query;   // records by falling X + 1 and by falling query tiles
   int2* groups;
   int4* seqs;                // [n_seqs] scratch
@@ -55,6 +55,10 @@ struct PackedRows {
   __nv_bfloat16 *dQ, *dK;
   int64_t dq_row, dq_head, dk_row, dk_head;
   float scale;
+  // the dynamic pass's items, shared out over its CTAs
+  int4* order;               // or null: no such pass
+  int n_ctas;                // up to 256
+  PackedBwdItems items;
   uint8_t static_slot[kMaxHeads];  // 255: dynamic
   uint8_t kv_has_dyn[kMaxHeads];
 };

@@ -42,7 +42,7 @@ int max_tiles(const saf_packed_dims& d) {
 struct PackedWs {
   size_t status, hdr, by_key, by_query, groups, seqs;
   size_t a_tab, r_tab, row_tab, logZ, mode, shift;
-  size_t Dvec, lse2, row_vals, dq_acc, dv_acc, total;
+  size_t Dvec, lse2, row_vals, dq_acc, dv_acc, order, total;
 };
 
 PackedWs packed_ws(const saf_packed_dims& d, bool backward) {
@@ -55,7 +55,7 @@ PackedWs packed_ws(const saf_packed_dims& d, bool backward) {
   };
   const size_t nt = max_tiles(d), H = d.H, T = (size_t)tiles_of(d.max_len) * 128;
   w.status = take(256);
-  w.hdr = take(16);
+  w.hdr = take(32);
   w.by_key = take(nt * 16);
   w.by_query = take(nt * 16);
   w.groups = take(nt * 8);
@@ -72,6 +72,7 @@ PackedWs packed_ws(const saf_packed_dims& d, bool backward) {
   w.row_vals = take(b * H * nt * 512);
   w.dq_acc = take(b * H * d.total * d.d_h * 4);
   w.dv_acc = take(b * d.H_kv * d.total * d.d_h * 4);
+  w.order = take(b * (kOrderRounds + 1) * 256 * 16);
   w.total = off;
   return w;
 }
@@ -169,6 +170,7 @@ void fill_fwd(PackedFwdParams& p, const Call& c) {
   p.shift = c.at<float>(c.w.shift);
   p.status = c.at<int>(c.w.status);
   p.hdr = c.at<int>(c.w.hdr);
+  p.counter = c.at<int>(c.w.hdr) + 2;
   p.groups = c.at<int2>(c.w.groups);
   p.total = c.d.total;
   p.nt_max = c.nt;
@@ -337,6 +339,45 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
   memset(r.static_slot, 255, sizeof(r.static_slot));
   for (int i = 0; i < c.hs.n_static; ++i) r.static_slot[c.hs.st[i]] = (uint8_t)i;
   for (int h = 0; h < d.H; ++h) r.kv_has_dyn[h / c.g] |= !c.hs.is_static[h];
+
+  // the dynamic pass: query heads by K/V head, and its items
+  PackedBwdLaunch bl;
+  memset(&bl, 0, sizeof(bl));
+  if (dyn) {
+    PackedBwdParams& p = bl.p;
+    int n = 0;
+    for (int kv = 0; kv < c.Hkv; ++kv) {
+      p.dyn_begin[kv] = (uint16_t)n;
+      for (int h = kv * c.g; h < (kv + 1) * c.g; ++h)
+        if (!c.hs.is_static[h]) p.dyn_by_kv[n++] = (uint8_t)h;
+      p.dyn_count[kv] = (uint16_t)(n - p.dyn_begin[kv]);
+      if (p.dyn_count[kv] > 0) p.kv_list[p.n_kv++] = (uint8_t)kv;
+    }
+    // K/V heads of a group of items.  The CTAs add into dQ's sums, and read Q and dO, of one
+    // query head of each K/V head of the group at a time; half of L2 and a little more
+    // holds them (80 MB).  Up to 160 MB one group is better all the same, as items
+    // share out better: 352 us against 368 with two (9 heads of 64, 33k rows); with 245 MB
+    // three groups take 340 us, one 370 (16 heads of 64, 30k rows).
+    int heads = 1;
+    for (int i = 0; i < p.n_kv; ++i)
+      heads = p.dyn_count[p.kv_list[i]] > heads ? p.dyn_count[p.kv_list[i]] : heads;
+    const double mb = (double)p.n_kv * d.total * d.d_h * 8.0 / 1e6;
+    int groups = mb <= 160.0 ? 1 : (int)ceil(mb / 80.0);
+    if (groups > p.n_kv) groups = p.n_kv;
+    p.items.tiles = c.at<int4>(c.w.by_query);
+    p.items.n_kv = p.n_kv;
+    p.items.per_group = (p.n_kv + groups - 1) / groups;
+    p.items.most_steps = heads * tiles_of(d.max_len);
+    p.items.even = n == heads * p.n_kv;
+    memcpy(p.items.kv_list, p.kv_list, sizeof(p.kv_list));
+    memcpy(p.items.dyn_count, p.dyn_count, sizeof(p.dyn_count));
+    p.n_items = items_for(c, p.n_kv);
+    bl.num_sms = sm_count() < 256 ? sm_count() : 256;
+    p.order = c.at<int4>(c.w.order);
+    r.order = c.at<int4>(c.w.order);
+    r.n_ctas = p.n_items < bl.num_sms ? p.n_items : bl.num_sms;
+    r.items = p.items;
+  }
   SAF_TRY(launch_packed_pre(r, c.s));
 
   float* dv_acc = c.at<float>(c.w.dv_acc);
@@ -348,6 +389,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     PackedFwdLaunch L;
     memset(&L, 0, sizeof(L));
     fill_fwd(L.p, c);
+    L.p.counter = c.at<int>(c.w.hdr) + 3;
     L.p.tiles = c.at<int4>(c.w.by_query);
     L.p.out = static_cast<__nv_bfloat16*>(dV->p);
     L.p.out_row = row_of(*dV, d);
@@ -371,32 +413,11 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     SAF_TRY(launch_packed_fwd(L, true, c.s));
   }
   if (dyn) {
-    PackedBwdLaunch L;
-    memset(&L, 0, sizeof(L));
+    PackedBwdLaunch& L = bl;
     PackedBwdParams& p = L.p;
     p.H = d.H;
     p.H_kv = c.Hkv;
-    int n = 0;
-    for (int kv = 0; kv < c.Hkv; ++kv) {
-      p.dyn_begin[kv] = (uint16_t)n;
-      for (int h = kv * c.g; h < (kv + 1) * c.g; ++h)
-        if (!c.hs.is_static[h]) p.dyn_by_kv[n++] = (uint8_t)h;
-      p.dyn_count[kv] = (uint16_t)(n - p.dyn_begin[kv]);
-      if (p.dyn_count[kv] > 0) p.kv_list[p.n_kv++] = (uint8_t)kv;
-      p.kv_has_static[kv] = kv_has_static[kv];
-    }
-    p.n_items = items_for(c, p.n_kv);
-    {
-      // K/V heads of a group of items: as for batches of one length, about five rounds
-      // of the grid where dQ's accumulator, Q and dO of all heads exceed half of L2
-      int heads = 1;
-      for (int i = 0; i < p.n_kv; ++i)
-        heads = p.dyn_count[p.kv_list[i]] > heads ? p.dyn_count[p.kv_list[i]] : heads;
-      const double bytes = (double)p.n_kv * heads * d.total * d.d_h * 8.0;
-      int G = (int)(5.0 * sm_count() / tiles_of(d.total) + 0.5);
-      if (bytes <= 64.0 * 1024 * 1024 || G >= p.n_kv) G = p.n_kv;
-      p.pairs_per_group = G < 1 ? 1 : G;
-    }
+    memcpy(p.kv_has_static, kv_has_static, sizeof(p.kv_has_static));
     p.scale = r.scale;
     p.scale_log2 = 1.4426950408889634f * r.scale;
     p.dv_acc = dv_acc;
@@ -411,7 +432,6 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     p.dv_head = head_of(*dV, c.Hkv);
     p.status = c.at<int>(c.w.status);
     p.hdr = r.hdr;
-    p.tiles = c.at<int4>(c.w.by_query);
     p.total = d.total;
     p.nt_max = c.nt;
     if (!encode(&L.tm_q, *Q, d, d.H) || !encode(&L.tm_k, *K, d, c.Hkv) ||
@@ -419,7 +439,6 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
         !encode_rows_f32(&L.tm_dq, r.dq_acc, (uint64_t)d.H * d.total, d.d_h))
       return SAF_ERR_CUDA;
     L.d_h = d.d_h;
-    L.num_sms = sm_count();
     SAF_TRY(launch_packed_bwd(L, c.s));
     SAF_TRY(launch_packed_post(r, c.s));
   }

@@ -17,6 +17,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "attn_common.cuh"
 #include "packed.h"
 #include "ptx.cuh"
 
@@ -63,6 +64,7 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
   const int n = p.n_seqs, m = p.max_tiles;
   if (tid == 0) {
     *p.status = 0;
+    p.hdr[2] = p.hdr[3] = 0;
     sh.end = max(0, min(p.cu[0], p.total));
     sh.tiles = 0;
   }
@@ -268,13 +270,80 @@ __global__ void __launch_bounds__(kPrepThreads)
   else clear_rows(p, b - chunks * p.n_static);
 }
 
+// Place of a key among the block's keys (all different, those behind n the largest).
+__device__ __forceinline__ int place_of(uint32_t key, const uint32_t* keys, int n) {
+  int below = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; i += 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+    below += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+  }
+  return below;
+}
+
+// The dynamic pass's items shared out over its CTAs, by one block beside the row pass: round by
+// round the costliest item of a round goes to the CTA with the least to do so far.  A
+// step costs 2, an item's beginning and end 1.  (By the snake order 16 % of the SMs' time was
+// idle with 16 documents of up to 4096 tokens and 9 heads of 64, 17 % with 3 of up to 8192 and
+// 8 K/V heads: 397 and 793 us against 368 and 695.  Items handed out as CTAs come free,
+// through a ring in shared memory to the five roles, cost each step 9 %.)
+__device__ void share_out(const PackedRows& p) {
+  __shared__ __align__(16) uint32_t by_load[256], by_cost[256];
+  __shared__ int load_of[256], cta_at[256];
+  const int tid = threadIdx.x, n_ctas = p.n_ctas, nt = p.hdr[0], n = nt * p.items.n_kv;
+  const int rounds = (n + n_ctas - 1) / n_ctas;
+  if (rounds > kOrderRounds) return;
+  auto record = [&](int r) {
+    const int it = r * n_ctas + tid;
+    return tid < n_ctas && it < n ? packed_bwd_item(p.items, nt, it) : make_int4(0, 0, 0, 0);
+  };
+  // costs in units that keep a CTA's sum below 2^24
+  int shift = 0;
+  while (((long long)rounds * (1 + 2 * p.items.most_steps)) >> shift >= 1 << 24) ++shift;
+  load_of[tid] = 0;
+  by_load[tid] = by_cost[tid] = 0xffffffffu;  // (what is behind the last CTA stays so)
+  int4 rec = record(0);
+  for (int r = 0; r < rounds; ++r) {
+    const int4 next = record(r + 1);
+    const int cost = rec.y > 0 ? (1 + 2 * (int)p.items.dyn_count[rec.z >> 16] *
+                                          ((rec.y + 127) / 128 - (rec.z & 0xffff))) >> shift
+                               : 0;
+    const uint32_t lk = (uint32_t)load_of[tid] << 8 | tid, ck = (0xffffffu - cost) << 8 | tid;
+    if (tid < n_ctas) {
+      by_load[tid] = lk;
+      by_cost[tid] = ck;
+    }
+    __syncthreads();
+    // (records come by falling steps: they need no ranking where every K/V head
+    // serves as many query heads)
+    int place = tid;
+    if (tid < n_ctas) {
+      cta_at[place_of(lk, by_load, n_ctas)] = tid;
+      if (!p.items.even) place = place_of(ck, by_cost, n_ctas);
+    }
+    __syncthreads();
+    if (tid < n_ctas) {
+      const int cta = cta_at[place];
+      p.order[r * n_ctas + cta] = rec;
+      load_of[cta] += cost;
+    }
+    rec = next;
+    __syncthreads();
+  }
+  if (tid < n_ctas) p.order[rounds * n_ctas + tid] = make_int4(0, 0, 0, 0);
+}
+
 // A tile's rows under one head: D/8 lanes a row, 8 elements each.
 template <int D>
 __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__ PackedRows p) {
   constexpr int LPR = D / 8;
+  if ((int)blockIdx.y == 0 && p.order) {
+    if (blockIdx.x == 0) share_out(p);
+    return;
+  }
   if ((int)blockIdx.x >= p.hdr[0]) return;
   const int4 t = p.tiles[blockIdx.x];
-  const int h = blockIdx.y, hs = p.static_slot[h], kv = h / p.group_kv;
+  const int h = (int)blockIdx.y - (p.order ? 1 : 0), hs = p.static_slot[h], kv = h / p.group_kv;
   const int tile = t.w + t.z, valid = min(128, t.y - t.z * 128);
   const bool zero_k = h == kv * p.group_kv && !p.kv_has_dyn[kv];
   const int sub = threadIdx.x % LPR;
@@ -358,7 +427,7 @@ cudaError_t launch_packed_prep(const PackedPrep& p, cudaStream_t s) {
 }
 
 cudaError_t launch_packed_pre(const PackedRows& p, cudaStream_t s) {
-  const dim3 grid(p.nt_max, p.H);
+  const dim3 grid(p.nt_max, p.H + (p.order ? 1 : 0));
   trace_begin(s);
   switch (p.d_h) {
     case 32: packed_pre_kernel<32><<<grid, 256, 0, s>>>(p); break;

@@ -99,17 +99,28 @@ struct ItemRing {
   volatile int* item;      // [kItemSlots]
 };
 
+// A CTA's first item is its own number; with no more items than CTAs that is all, and
+// the ring is not used.
+//
 // The handing thread.  The counter is zero before the launch.  claim() is called as the
 // item's last loads go out: the number is there when the item ends, and no CTA holds one
 // while it still has much to do (claimed as an item began, the order was as bad as
 // a fixed one).
 struct ItemFeed {
-  uint32_t n = 0;
+  uint32_t n = 0;  // items handed out after the first
+  bool begun = false;
   int ahead = 0;
-  __device__ __forceinline__ void claim(int* counter) { ahead = atomicAdd(counter, 1); }
+  __device__ __forceinline__ void claim(int* counter, int n_items) {
+    if (n_items > (int)gridDim.x) ahead = atomicAdd(counter, 1);
+  }
   __device__ __forceinline__ int next(const ItemRing& r, int n_items, const WaitCtl& wc,
                                       int site) {
-    int it = n == 0 ? (int)blockIdx.x : (int)gridDim.x + ahead;
+    if (!begun) {
+      begun = true;
+      return min((int)blockIdx.x, n_items);
+    }
+    if (n_items <= (int)gridDim.x) return n_items;
+    int it = (int)gridDim.x + ahead;
     const uint32_t s = n % kItemSlots;
     if (!mbar_wait(r.empty + s, ((n / kItemSlots) & 1) ^ 1, wc, site) || it > n_items) it = n_items;
     r.item[s] = it;
@@ -123,8 +134,14 @@ struct ItemFeed {
 template <bool ALONE>
 struct ItemTake {
   uint32_t n = 0;
+  bool begun = false;
   __device__ __forceinline__ int next(const ItemRing& r, int n_items, const WaitCtl& wc,
                                       int site) {
+    if (!begun) {
+      begun = true;
+      return min((int)blockIdx.x, n_items);
+    }
+    if (n_items <= (int)gridDim.x) return n_items;
     const uint32_t s = n % kItemSlots;
     int it = n_items;
     if (mbar_wait(r.full + s, (n / kItemSlots) & 1, wc, site)) it = r.item[s];

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(384, 1)
                 kpar = ((kc / L::KST) & 1) ^ 1;
                 ++kc;
               }
-              if (j == w.nsteps - 1) items_fed.claim(p.counter);
+              if (j == w.nsteps - 1) items_fed.claim(p.counter, n_items);
               mbar_wait(k_empty + ks, kpar, wc, kSiteProdK);
               mbar_arrive_expect_tx(k_full + ks, G::TILE_BYTES);
               for (int c = 0; c < G::NCHUNK; ++c)
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(384, 1)
           } else {
             for (int step = 0; step < w.nsteps; ++step) {
               const int as = ac % L::AST;
-              if (step == w.nsteps - 1) items_fed.claim(p.counter);
+              if (step == w.nsteps - 1) items_fed.claim(p.counter, n_items);
               mbar_wait(aux_empty + as, ((ac / L::AST) & 1) ^ 1, wc, kSiteProdK);
               ++ac;
               mbar_arrive_expect_tx(aux_full + as, L::AUX_BYTES);

@@ -101,6 +101,14 @@ __device__ __forceinline__ Best best_of(unsigned long long key) {
   return Best{__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o), (int)~(uint32_t)key};
 }
 
+// Of two parts of a row one holds logits beyond 2^20: the sum of the one with the smaller
+// element in units of the other's.
+__device__ __noinline__ unsigned long long far_sum(float from, float to, int e,
+                                                   unsigned long long x) {
+  const double d = (double)from - (double)to + (double)e * 0.6931471805599453;
+  return d > -40.0 ? (unsigned long long)((double)x * exp(d)) : 0;
+}
+
 // (top, base, e, sum) takes in another part of the row: of two sums the one with the smaller
 // exponent is shifted; the part with the larger element keeps its base.
 __device__ __forceinline__ void join_sum(float& top, float& base, int& e, unsigned long long& sum,
@@ -114,15 +122,12 @@ __device__ __forceinline__ void join_sum(float& top, float& base, int& e, unsign
     return;
   }
   if (b != base) {
-    // one of the two holds logits beyond 2^20
-    const bool other = t > top;
-    const double from = other ? (double)base - b : (double)b - base;
-    const double d = from + (double)(other ? e - ex : ex - e) * 0.6931471805599453;
-    const unsigned long long small = other ? sum : x, large = other ? x : sum;
-    sum = large + (d > -40.0 ? (unsigned long long)((double)small * exp(d)) : 0);
-    if (other) {
+    if (t > top) {
+      sum = x + far_sum(base, b, e - ex, sum);
       base = b;
       e = ex;
+    } else {
+      sum += far_sum(b, base, ex - e, x);
     }
   } else {
     const int up = max(e, ex);
@@ -170,16 +175,18 @@ __device__ void join_rows(const BeamParams& p, int slot0, int R, const Joined& j
     float top = -INFINITY, base = 0.f;
     int e = 0;
     unsigned long long sum = 0;
-    if (offers(p, slot0 + r)) {
-      // (a lane's parts one after another; 32 of them and more are rare)
-      for (int s = lane; s < S; s += 32) {
-        const int4 a = __ldcg(part(r, s)), b = __ldcg(part(r, s) + 1);
-        const unsigned long long x =
-            (unsigned long long)(uint32_t)a.x | (unsigned long long)(uint32_t)a.y << 32;
-        const float t = __int_as_float(b.x), bs = __int_as_float(a.w);
-        join_sum(top, base, e, sum, t, bs, a.z, x);
-      }
-#pragma unroll
+    // (parts of a slot that offers nothing hold anything: they are read, not used)
+    const bool some = offers(p, slot0 + r);
+#pragma unroll 1
+    for (int s = lane; s < S; s += 32) {
+      const int4 a = __ldcg(part(r, s)), b = __ldcg(part(r, s) + 1);
+      const unsigned long long x =
+          (unsigned long long)(uint32_t)a.x | (unsigned long long)(uint32_t)a.y << 32;
+      const float t = some ? __int_as_float(b.x) : -INFINITY, bs = __int_as_float(a.w);
+      join_sum(top, base, e, sum, t, bs, a.z, x);
+    }
+    if (some) {
+#pragma unroll 1
       for (int o = 16; o > 0; o >>= 1) {
         const float t = __shfl_xor_sync(0xffffffffu, top, o);
         const float bs = __shfl_xor_sync(0xffffffffu, base, o);
@@ -202,8 +209,9 @@ __device__ void join_rows(const BeamParams& p, int slot0, int R, const Joined& j
     j.keys[i] = offers(p, slot0 + r) && at < count ? key_of(__int_as_float(x.x), x.y) : 0;
   }
   __syncthreads();
-  if (tid < 32) {
-    // all rows' logarithms by one warp: fp64 instructions take as long for one lane as for 32
+  if (tid >= kThreads - 32) {
+    // all rows' logarithms by one warp (the one with the fewest entries below): fp64
+    // instructions take as long for one lane as for 32
     for (int r = lane; r < R; r += 32) {
       const unsigned long long sum = j.score[r];
       const double e = (double)(j.flat[r] - kUnit) * 0.6931471805599453;
@@ -277,21 +285,21 @@ __device__ void choose(const BeamParams& p, int group, const Joined& j) {
       if (p.finished_out) p.finished_out[slot0 + i] = 0;
     }
   if (p.history_out) {
-    // a warp to a row, eight columns of each lane in flight
+    // a warp to a row, 16 columns of each lane in flight
     const int cols = min(filled + 1, p.max_tokens), lane = tid & 31;
     for (int b = tid >> 5; b < K; b += kWarps) {
       const int from = j.chosen[b], last = from >= 0 ? j.token[b] : -1;
       const int32_t* src = p.history + (size_t)max(from, 0) * p.max_tokens;
       int32_t* dst = p.history_out + (size_t)(slot0 + b) * p.max_tokens;
-      for (int c0 = lane; c0 < cols; c0 += 256) {
-        int v[8];
+      for (int c0 = lane; c0 < cols; c0 += 512) {
+        int v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
           const int c = c0 + 32 * i;
           v[i] = c >= filled ? last : from >= 0 ? __ldg(src + c) : -1;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
           if (c0 + 32 * i < cols) dst[c0 + 32 * i] = v[i];
       }
     }

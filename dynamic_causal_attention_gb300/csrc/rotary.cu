@@ -12,7 +12,7 @@
 // The rows are read once and written once, so the kernel is bound by memory.  A thread
 // has a token and two vectors of 16 bytes of its rows (the two parts of eight pairs), forms
 // their cosines and sines once in registers and goes through the heads of Q and K with
-// them, four heads' loads in flight; no shared memory, no barrier.  With few tokens the
+// them, three heads' loads in flight; no shared memory, no barrier.  With few tokens the
 // heads are shared out over several threads, which then form the same sines.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,7 +24,7 @@ namespace saf {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // heads in flight
+constexpr int kUnroll = 3;  // heads in flight
 
 template <int BYTES>
 struct Raw;
@@ -147,7 +147,7 @@ __device__ __forceinline__ void heads(const RotaryRows& in, const RotaryRows& ou
 }
 
 template <typename T, int W, bool HALF>
-__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
   const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
   const uint32_t r = fast_div(i, p.by_units), u = i - r * (uint32_t)p.units;
   const uint32_t n = fast_div(r, p.by_split);           // the row of B * T

@@ -592,7 +592,7 @@ class PackedAttention(_OnDevice):
         if self._frozen:
             if alpha is None or rho is None:
                 raise self._bad("PackedAttention: frozen heads need alpha and rho")
-            T = alpha.shape[-1]
+            T = alpha.shape[-1] if alpha.dim() == 2 else -1
             if T < self.max_len:
                 raise self._bad(f"PackedAttention: {T} columns of alpha, max_len {self.max_len}")
             pa = self._need(alpha, (self.H, T), torch.float32, "PackedAttention: alpha")

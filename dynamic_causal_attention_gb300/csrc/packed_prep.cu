@@ -231,31 +231,38 @@ __device__ void make_tables(const PackedPrep& p, int hs, int row0, float* red) {
   }
 }
 
-__device__ void clear_rows(const PackedPrep& p, int block) {
-  const int first = max(0, min(p.cu[0], p.total));
-  const int last = max(first, min(p.cu[p.n_seqs], p.total));
-  const long long rest = first + (p.total - last);
-  const long long t0 = (long long)block * kPrepThreads + threadIdx.x;
-  const long long step = (long long)kClearBlocks * kPrepThreads;
-  if (rest == 0) return;
+// Rows row0 .. row0 + n - 1, by threads t0, t0 + step, ...
+__device__ void clear_range(const PackedPrep& p, long long row0, long long n, long long t0,
+                            long long step) {
   for (int i = 0; i < p.n_rows; ++i) {
     const ClearRows& x = p.rows[i];
     const int units = p.d / 8;
-    for (long long j = t0; j < rest * x.heads * units; j += step) {
+    for (long long j = t0; j < n * x.heads * units; j += step) {
       const int u = (int)(j % units);
       const long long hr = j / units;
       const int h = (int)(hr % x.heads);
-      const long long k = hr / x.heads;
-      const long long row = k < first ? k : last + (k - first);
-      *reinterpret_cast<uint4*>(x.p + row * x.row + (int64_t)h * x.head + 8 * u) =
+      *reinterpret_cast<uint4*>(x.p + (row0 + hr / x.heads) * x.row + (int64_t)h * x.head + 8 * u) =
           make_uint4(0u, 0u, 0u, 0u);
     }
   }
   if (p.lse)
-    for (long long j = t0; j < rest * p.H; j += step) {
-      const long long h = j / rest, k = j - h * rest;
-      p.lse[h * p.total + (k < first ? k : last + (k - first))] = -INFINITY;
-    }
+    for (long long j = t0; j < n * p.H; j += step)
+      p.lse[j / n * p.total + row0 + j % n] = -INFINITY;
+}
+
+// What is not worked on: rows before the first and behind the last sequence, and rows of a
+// sequence from max_len on.
+__device__ void clear_rows(const PackedPrep& p, int block) {
+  const int first = max(0, min(p.cu[0], p.total));
+  const int last = max(first, min(p.cu[p.n_seqs], p.total));
+  const long long t0 = (long long)block * kPrepThreads + threadIdx.x;
+  const long long step = (long long)kClearBlocks * kPrepThreads;
+  clear_range(p, 0, first, t0, step);
+  clear_range(p, last, p.total - last, t0, step);
+  for (int b = block; b < p.n_seqs; b += kClearBlocks) {
+    const int a = max(0, min(p.cu[b], p.total)), e = max(0, min(p.cu[b + 1], p.total));
+    if (e - a > p.max_len) clear_range(p, a + p.max_len, e - a - p.max_len, threadIdx.x, kPrepThreads);
+  }
 }
 
 // Grid: 1 + tables * n_static + (clear ? kClearBlocks : 0).

@@ -541,14 +541,15 @@ SAF_API size_t saf_packed_attn_workspace_size(const saf_packed_dims* dims, int b
  *   cu_seqlens  device [n_seqs + 1] int32, not falling, within 0..total.  Empty
  *               sequences are allowed.  Rows before the first and behind the last
  *               sequence, and rows of a sequence from max_len on, are not worked on; they
- *               may hold anything.
+ *               may hold anything.  (Offsets that fall or lie outside are cut so that no
+ *               row is in two sequences; nothing outside the tensors is touched.)
  *   alpha, rho  [H, T_pat] fp32, rows of frozen heads; values below -2.3e38 count as
  *               -inf (no weight).  NULL without frozen heads.
  *   lse         [H, total] fp32 or NULL (4-byte aligned): log sum_j exp(.); -inf where
  *               a frozen head's row has no weight, whose out is 0.
- *   flags       SAF_CLEAR_REST: rows of no sequence become 0, their lse -inf.
+ *   flags       SAF_CLEAR_REST: rows that are not worked on become 0, their lse -inf.
  *   workspace   256-byte aligned; saf_get_device_status reads its status.
- * Both products have fp32 sums; the weights are rounded to bf16 for the second (as the
+ * Outputs must not overlap inputs or one another.  Both products have fp32 sums; the weights are rounded to bf16 for the second (as the
  * rows that they weigh).  An infinity or NaN in a row of V reaches rows of its own sequence
  * only: those after it, and those up to 127 rows before it.  The same call gives the
  * same bits. */
@@ -562,9 +563,10 @@ SAF_API saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_ro
  * looked at without dynamic heads); dQ [total, H, d_h], dK and dV [total, H_kv, d_h]
  * are overwritten in the rows of the sequences: dK and dV sum over the query heads of
  * their group, dQ of frozen heads and dK that serve frozen heads only are 0.  alpha and
- * rho are constants here (saf_hybrid_attn_bwd has their gradients).  dQ is summed in
- * fp32 in the order in which its parts arrive, so its last bit may differ from call to
- * call; dK and dV do not. */
+ * rho are constants here (saf_hybrid_attn_bwd has their gradients).  P and dS are rounded
+ * to bf16 for their products, and rowsum(dout o out) is formed from out as it is rounded.  dQ is
+ * summed in fp32 in the order in which its parts arrive, so its last bit may differ from
+ * call to call; dK and dV do not. */
 SAF_API saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q,
                                const saf_rows* K, const saf_rows* V, const saf_rows* out,
                                const float* lse, const saf_rows* dout,

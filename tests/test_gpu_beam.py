@@ -160,6 +160,24 @@ def test_first_step_and_in_place_scores(api):
     check(api, x, s, K=K)
 
 
+def test_scores_in_their_own_place(api):
+    from dynamic_causal_attention_gb300 import _binding as B
+    G, K, V = 7, 4, 3000
+    x, s = inputs(G, K, V, seed=4)
+    done = (torch.arange(G * K, device="cuda") % 5 == 0)
+    search = api.BeamSearch(G, K, V, end=2)
+    want = search.step(x, s, done)
+    parent, token = (torch.zeros(G * K, dtype=torch.int32, device="cuda") for _ in range(2))
+    dims = B.saf_beam_dims(G, K, V, V, B.SAF_F32, 2, 0)
+    st = B.saf_beam_step(dims, x.data_ptr(), s.data_ptr(), done.data_ptr(), None, None,
+                         parent.data_ptr(), token.data_ptr(), s.data_ptr(), done.data_ptr(), None,
+                         search.workspace.data_ptr(), search.ws_bytes,
+                         torch.cuda.current_stream().cuda_stream)
+    assert st == B.SAF_OK
+    for a, b in zip((parent, token, s, done), want):
+        assert torch.equal(a, b)
+
+
 def test_histories_follow_their_parents(api):
     G, K, V, cols = 5, 3, 4000, 70
     search = api.BeamSearch(G, K, V, end=1)

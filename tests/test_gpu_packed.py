@@ -260,3 +260,70 @@ def test_other_stream_and_strided_inputs(api):
     side.synchronize()
     want = ref.packed(q, k, v, lens, starts, frozen, alpha, rho)
     ref.check("out", out, *want["out"])
+
+
+def test_more_items_than_are_shared_out(api):
+    """Short sequences by the thousand: the backward's items go by the fixed order then."""
+    lens = [(7 * i) % 12 for i in range(1400)]
+    run(api, lens, 8, 8, 32, [0] * 8)
+
+
+def test_rows_behind_the_longest_length(api):
+    """A sequence longer than max_len: its first max_len rows are as if it ended there, the rest is
+    left alone in given buffers and cleared in new ones."""
+    d, H, n = 64, 2, 200
+    q, k, v, do, alpha, rho, cu, _ = inputs([n, 90], H, H, d)
+    layer = api.PackedAttention(H, d, [0, 1], max_total=290, max_seqs=2, max_len=130)
+    want = ref.packed(q, k, v, [130, 90], [0, n], [0, 1], alpha, rho, do)
+    out, lse = layer.forward(q, k, v, cu, alpha, rho)
+    grads = layer.backward(q, k, v, out, lse, do, cu, alpha, rho)
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        ref.check(name, t, *want[name])
+    given = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    layer.forward(q, k, v, cu, alpha, rho, out=given[0], lse=given[1])
+    assert (given[0][130:n] == 7).all() and (given[1][:, 130:n] == 7).all()
+    assert torch.equal(given[0][:130], out[:130]) and torch.equal(given[0][n:], out[n:])
+
+
+def test_gradients_into_one_projection(api):
+    """dq, dk, dv as views of one tensor, as a projection's backward wants them."""
+    lens, H, Hkv, d, frozen = [77, 200], 4, 2, 64, [0, 1, 0, 0]
+    q, k, v, do, alpha, rho, cu, starts = inputs(lens, H, Hkv, d, layout="fused", tail=3)
+    layer = api.PackedAttention(H, d, frozen, max_total=280, max_seqs=2, max_len=200, H_kv=Hkv)
+    out, lse = layer.forward(q, k, v, cu, alpha, rho)
+    whole = torch.full((280, H + 2 * Hkv, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    parts = whole[:, :H], whole[:, H:H + Hkv], whole[:, H + Hkv:]
+    layer.backward(q, k, v, out, lse, do, cu, alpha, rho, grads=parts)
+    want = ref.packed(q, k, v, lens, starts, frozen, alpha, rho, do)
+    for name, t in zip(("dq", "dk", "dv"), parts):
+        ref.check(name, t[:277], want[name][0][:277], want[name][1][:277])
+    assert (whole[277:] == 5).all()
+
+
+def test_refusals(api):
+    d, H = 64, 4
+    q, k, v, do, alpha, rho, cu, _ = inputs([50, 14], H, 2, d, layout="fused")
+    layer = api.PackedAttention(H, d, [0, 0, 0, 1], max_total=64, max_seqs=2, max_len=50, H_kv=2,
+                                backward=False)
+    ok = dict(q=q, k=k, v=v, cu_seqlens=cu, alpha=alpha, rho=rho)
+    layer.forward(**ok)
+    more = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q[:, :3]), dict(q=q[0]), dict(k=q), dict(v=v[:63]),
+                dict(k=k.cpu()), dict(cu_seqlens=cu.long()), dict(cu_seqlens=more),
+                dict(cu_seqlens=cu[:0]), dict(cu_seqlens=cu.cpu()), dict(alpha=None),
+                dict(rho=rho[:, :49]), dict(alpha=alpha[:, :49], rho=rho[:, :49]),
+                dict(alpha=alpha[0]), dict(rho=rho.double()), dict(out=q[:, :, :32]),
+                dict(lse=torch.empty(64, H, device="cuda")),
+                dict(q=torch.zeros((H, d, 64), device="cuda").bfloat16().permute(2, 0, 1)),
+                dict(q=torch.zeros((65, H, d), device="cuda").bfloat16()),
+                # rows that lie on no 16-byte boundary, and all in one place
+                dict(q=torch.zeros((64, H * d + 1), device="cuda").bfloat16()[:, 1:].unflatten(1, (H, d))),
+                dict(k=k[:1].expand(64, 2, d))):
+        with pytest.raises(api.SafError):
+            layer.forward(**{**ok, **bad})
+    with pytest.raises(api.SafError):
+        layer.backward(q, k, v, *layer.forward(**ok), do, cu, alpha, rho)
+    for bad in (dict(d_h=48), dict(H_kv=3), dict(max_len=200000), dict(head_is_static=[0])):
+        with pytest.raises(api.SafError):
+            api.PackedAttention(**{**dict(H=4, d_h=64, head_is_static=[0] * 4, max_total=64, max_seqs=2,
+                                          max_len=64), **bad})

@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kStages = 3;              // tiles of a block's ring
-constexpr int kList = 512;             // candidates of a block before the K best are picked
+constexpr int kHits = 184;             // vectors of a part that reach its threshold
 constexpr float kMasked = -2.3e38f;    // below: as -inf
 constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-08f;
 constexpr float kPlain = 1048576.f;    // |logits| up to here are reduced without a base
@@ -84,13 +84,6 @@ __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// The maximum of three, NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // Whether a score is one (not -inf, masked or NaN).
@@ -324,6 +317,42 @@ __device__ __forceinline__ bool last_here(int* counter, int of, int* flag) {
   return *flag != 0;
 }
 
+// The K-th largest of the threads' values m (kMasked if fewer count): at least K elements of
+// which the m are maxima are not below it.
+__device__ __noinline__ float kth_largest(float m, int K, float* tops, float* sh_top) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // each warp's, sorted downwards (bitonic)
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2) {
+      const float o = __shfl_xor_sync(0xffffffffu, m, step);
+      const bool up = (lane & size) != 0, low = (lane & step) == 0;
+      m = (up == low) ? fminf(m, o) : fmaxf(m, o);
+    }
+  if (lane < K) tops[warp * K + lane] = m;
+  __syncthreads();
+  float kth = -INFINITY;
+  if (warp * 32 < kWarps * K) {
+    const float mine = tid < kWarps * K ? tops[tid] : -INFINITY;
+    int above = 0, not_below = 0;
+#pragma unroll 4
+    for (int j = 0; j < kWarps * K / 4; ++j) {
+      const float4 t = reinterpret_cast<const float4*>(tops)[j];
+      above += (t.x > mine) + (t.y > mine) + (t.z > mine) + (t.w > mine);
+      not_below += (t.x >= mine) + (t.y >= mine) + (t.z >= mine) + (t.w >= mine);
+    }
+    if (mine > -INFINITY && above < K && not_below >= K) kth = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) kth = fmaxf(kth, __shfl_xor_sync(0xffffffffu, kth, o));
+  }
+  if (lane == 0) sh_top[warp] = kth;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) kth = fmaxf(kth, sh_top[w]);
+  return fmaxf(kth, kMasked);
+}
+
 // Grid: slots * splits blocks.  A thread takes NV vectors of 16 bytes of every tile.  Dynamic
 // shared memory holds the ring of tiles, then what joining and choosing need.
 template <typename T, int NV>
@@ -332,9 +361,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
   extern __shared__ __align__(16) uint8_t scratch[];
   __shared__ __align__(16) float tops[kThreads];  // the best K maxima of each warp
   __shared__ unsigned long long sums[kWarps];
-  __shared__ unsigned long long list[kList];
+  __shared__ uint4 hit[kHits];
+  __shared__ int hit_at[kHits];
   __shared__ float sh_top[kWarps];
-  __shared__ int n_list, last_of;
+  __shared__ int n_hits, n_list, last_of;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = blockIdx.x / p.splits, split = blockIdx.x - slot * p.splits;
   const int K = p.beams;
@@ -395,79 +425,25 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
     if (split == 0 && tid < head + tail) {
       v_extra = tid < head ? tid : p.vocab - tail + (tid - head);
       extra = (float)row[v_extra];
-      if (!(extra < INFINITY)) extra = -INFINITY;
+      if (!(extra >= kMasked && extra < INFINITY)) extra = -INFINITY;
     }
-    if (tid == 0) n_list = 0;
+    if (tid == 0) n_hits = n_list = 0;
     fetch(0);
-    // The maximum of the tile, in which NaN and +inf (both count as masked) are cleared.
+    // The maximum of the tile (NaN is passed over; it shows in the sum).
     float vec_top[NV];
     auto tile_top = [&]() {
       float m = -INFINITY;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        float t = get(k, 0);
+        vec_top[k] = fmaxf(get(k, 0), get(k, 1));
 #pragma unroll
-        for (int e = 1; e + 1 < PER; e += 2) t = max3_nan(t, get(k, e), get(k, e + 1));
-        vec_top[k] = max3_nan(t, t, get(k, PER - 1));
-        m = max3_nan(m, m, vec_top[k]);
-      }
-      return m;
-    };
-    auto clean_top = [&]() {
-      float m = tile_top();
-      if (!(m < INFINITY)) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-              if (!(__uint_as_float(w[i]) < INFINITY)) w[i] = 0xff800000u;
-            } else {
-              if (!(__uint_as_float(w[i] << 16) < INFINITY)) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
-              if (!(__uint_as_float(w[i] & 0xffff0000u) < INFINITY))
-                w[i] = (w[i] & 0xffffu) | 0xff800000u;
-            }
-          }
-        }
-        m = tile_top();
+        for (int e = 2; e < PER; e += 2) vec_top[k] = fmax3(vec_top[k], get(k, e), get(k, e + 1));
+        m = fmaxf(m, vec_top[k]);
       }
       return m >= kMasked ? m : -INFINITY;
     };
-    float m = fmaxf(clean_top(), extra >= kMasked ? extra : -INFINITY);
-    // the warp's maxima, sorted downwards (bitonic)
-    float srt = m;
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-      for (int step = size / 2; step > 0; step /= 2) {
-        const float o = __shfl_xor_sync(0xffffffffu, srt, step);
-        const bool up = (lane & size) != 0, low = (lane & step) == 0;
-        srt = (up == low) ? fminf(srt, o) : fmaxf(srt, o);
-      }
-    if (lane < K) tops[warp * K + lane] = srt;
-    __syncthreads();
-    // the K-th largest of the threads' maxima: at least K elements are not below it
-    float floor_k = -INFINITY;
-    if (warp * 32 < kWarps * K) {
-      const float mine = tid < kWarps * K ? tops[tid] : -INFINITY;
-      int above = 0, not_below = 0;
-#pragma unroll 4
-      for (int j = 0; j < kWarps * K / 4; ++j) {
-        const float4 t = reinterpret_cast<const float4*>(tops)[j];
-        above += (t.x > mine) + (t.y > mine) + (t.z > mine) + (t.w > mine);
-        not_below += (t.x >= mine) + (t.y >= mine) + (t.z >= mine) + (t.w >= mine);
-      }
-      if (mine > -INFINITY && above < K && not_below >= K) floor_k = mine;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        floor_k = fmaxf(floor_k, __shfl_xor_sync(0xffffffffu, floor_k, o));
-    }
-    if (lane == 0) sh_top[warp] = floor_k;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) floor_k = fmaxf(floor_k, sh_top[w]);
-    floor_k = fmaxf(floor_k, kMasked);  // fewer than K maxima: every element that counts
+    float m = fmaxf(tile_top(), extra);
+    const float floor_k = kth_largest(m, K, tops, sh_top);
 
     // The sum of exponentials, 2^e times `sum`, and the elements that reach the threshold.
     // (Against the first exponent, 2^-(2^20 log2 e), logits below -2^20 add nothing: where a part
@@ -475,16 +451,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
     float top = -INFINITY, sum = 0.f;
     int e_run = (int)(-kPlain * kLog2e);
     const uint64_t l2 = f2_pack(kLog2e, kLog2e), ll2 = f2_pack(kLog2eLo, kLog2eLo);
-    auto offer = [&](float v, int at) {
-      if (v >= floor_k) {
-        const int i = atomicAdd(&n_list, 1);
-        if (i < kList) list[i] = key_of(v, at);
-      }
-    };
     for (int tile = 0; tile < p.tiles; ++tile) {
       if (tile > 0) {
         fetch(tile);
-        m = clean_top();
+        m = tile_top();
       }
       issue(tile + kStages - 1);
       if (m > top) {
@@ -516,10 +486,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < NV; ++k)
           if (vec_top[k] >= floor_k) {
-#pragma unroll
-            for (int e = 0; e < PER; ++e) offer(get(k, e), at + k * kThreads * PER + e);
+            const int i = atomicAdd(&n_hits, 1);
+            if (i < kHits) {
+              hit[i] = x[k];
+              hit_at[i] = at + k * kThreads * PER;
+            }
           }
-        if (tile == 0) offer(extra, v_extra);
       }
     }
     wait_copies<0>();
@@ -529,50 +501,89 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
     for (int o = 16; o > 0; o >>= 1)
       block_top = fmaxf(block_top, __shfl_xor_sync(0xffffffffu, block_top, o));
     if (lane == 0) tops[warp] = block_top;  // (the maxima there have been read)
-    __syncthreads();
+    // NaN or +inf among the logits (they count as masked), or some beyond 2^20: all of the
+    // part is gone through again, element by element
+    const bool slow = __syncthreads_or(!(sum < INFINITY) || !(top < INFINITY)) != 0;
+    auto again = [&](auto&& f) {
+      for (int v = first + tid; v < end; v += kThreads) {
+        const T* q = reinterpret_cast<const T*>(vecs + v);
+#pragma unroll 1
+        for (int e = 0; e < PER; ++e) {
+          const float y = (float)q[e];
+          if (y >= kMasked && y < INFINITY) f(y, head + v * PER + e);
+        }
+      }
+      if (extra > -INFINITY) f(extra, v_extra);
+    };
+    if (slow) {
+      top = -INFINITY;
+      again([&](float y, int) { top = fmaxf(top, y); });
+      block_top = top;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        block_top = fmaxf(block_top, __shfl_xor_sync(0xffffffffu, block_top, o));
+      if (lane == 0) tops[warp] = block_top;
+      __syncthreads();
+    }
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) block_top = fmaxf(block_top, tops[w]);
     const bool far = !(fabsf(block_top) <= kPlain);  // (also: no element)
     const float base = far ? block_top : 0.f;
     const int e_top = far ? 0 : (int)ceilf(block_top * kLog2e);
     unsigned long long fixed = 0;
-    // an element of this thread's part, read again
-    auto again = [&](auto&& f) {
-      for (int v = first + tid; v < end; v += kThreads) {
-        const T* q = reinterpret_cast<const T*>(vecs + v);
-        for (int e = 0; e < PER; ++e) {
-          const float y = (float)q[e];
-          if (y >= kMasked && y < INFINITY) f(y, head + v * PER + e);
-        }
-      }
-      if (extra >= kMasked) f(extra, v_extra);
-    };
-    if (!far) {
+    if (!far && !slow) {
       if (top > -INFINITY) fixed = in_units(sum, max(e_run - e_top, -200));
     } else if (block_top > -INFINITY) {
       float s = 0.f;
-      again([&](float y, int) { s += expf(y - block_top); });
+      again([&](float y, int) {
+        y -= base;
+        s += fast_exp2(fmaf(y, kLog2eLo, fmaf(y, kLog2e, -(float)e_top)));
+      });
       fixed = in_units(s, 0);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
     if (lane == 0) sums[warp] = fixed;
-    __syncthreads();
     Part* part = reinterpret_cast<Part*>(p.parts +
                                          ((size_t)slot * p.splits + split) * p.part_bytes);
     Best* best = reinterpret_cast<Best*>(part + 1);
-    const int n = n_list;
-    if (n > kList) {
-      // too many to list (equal ones, or rising ones): the K best one after another, each
-      // the best below the one before
+    // the elements that reach the threshold, in the ring's place (no tile is needed any more)
+    unsigned long long* list = reinterpret_cast<unsigned long long*>(scratch);
+    constexpr int list_size = kStages * kTile * 16 / 8;
+    static_assert(list_size >= kHits * PER + 16, "what the hits hold, and the ends, fits");
+    int n = n_hits;
+    bool listed = !slow && n <= kHits;
+    if (!listed) {
+      // too many reach the threshold of the first tile (or NaN spoiled it): that of
+      // the whole part, and another pass for what reaches it
+      const float floor_all = kth_largest(top, K, tops, sh_top);
+      __syncthreads();
+      again([&](float y, int at) {
+        if (y >= floor_all) {
+          const int i = atomicAdd(&n_list, 1);
+          if (i < list_size) list[i] = key_of(y, at);
+        }
+      });
+    } else {
+      for (int i = tid; i < n * PER; i += kThreads) {
+        const int v = i / PER, e = i % PER;
+        const float y = (float)reinterpret_cast<const T*>(&hit[v])[e];
+        if (y >= floor_k) list[atomicAdd(&n_list, 1)] = key_of(y, hit_at[v] + e);
+      }
+      if (extra >= floor_k) list[atomicAdd(&n_list, 1)] = key_of(extra, v_extra);
+    }
+    __syncthreads();
+    n = n_list;
+    listed = n <= list_size;
+    if (!listed) {
+      // so many equal ones: the K best one after another, each the best below the one before
       unsigned long long before = ~0ull;
-      for (int r = 0; r < K; ++r) {
+      for (n = 0; n < K; ++n) {
         unsigned long long mine = 0;
-        if (top >= floor_k)
-          again([&](float y, int at) {
-            const unsigned long long key = key_of(y, at);
-            if (key < before && key > mine) mine = key;
-          });
+        again([&](float y, int at) {
+          const unsigned long long key = key_of(y, at);
+          if (key < before && key > mine) mine = key;
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const unsigned long long other = __shfl_xor_sync(0xffffffffu, mine, o);
@@ -583,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
         __syncthreads();
         before = list[0];
         for (int w = 1; w < kWarps; ++w) before = list[w] > before ? list[w] : before;
-        if (tid == 0) best[r] = best_of(before);
+        if (before == 0) break;  // fewer than K
+        if (tid == 0) best[n] = best_of(before);
       }
     } else {
       for (int i = tid; i < n; i += kThreads) {
@@ -591,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
         if (above < K) best[above] = best_of(list[i]);
       }
     }
+    __syncthreads();
     if (tid == 0) {
       unsigned long long all = 0;
       for (int w = 0; w < kWarps; ++w) all += sums[w];
@@ -648,7 +661,11 @@ BeamWs beam_ws(int n_groups, int beams, int vocab, int n_sms) {
   };
   w.held = blocks(16, 1) < n_sms ? 8 : 16;
   w.tiles = 1;
-  while (w.tiles < 8 && blocks(w.held, 2 * w.tiles) >= 12ll * n_sms) w.tiles *= 2;
+  // (of each tile about as many vectors as beams reach the first one's threshold: half of
+  // the places for them are left for chance)
+  while (w.tiles < 8 && 2 * w.tiles * beams <= kHits / 2 &&
+         blocks(w.held, 2 * w.tiles) >= 12ll * n_sms)
+    w.tiles *= 2;
   // (whole vectors are counted from the row's first 16-byte boundary: never more than
   // vocab elements' worth)
   w.splits = (int)(blocks(w.held, w.tiles) / (long long)slots);

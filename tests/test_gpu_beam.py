@@ -140,6 +140,24 @@ def test_equal_scores_go_to_the_lowest(api):
     check(api, x, s, K=K)                     # -0 is 0
 
 
+@pytest.mark.parametrize("K,V", [(8, 128003), (32, 70001), (1, 200000), (16, 33000)])
+def test_parts_whose_first_logits_are_the_smallest(api, K, V):
+    """Far more logits above the first tile's than the places for them: rising along the vocabulary,
+    in steps of 4096, in bf16's coarse steps, with NaN and infinities on the way."""
+    G = max(1, 512 // K)
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    ramp = torch.arange(V, device="cuda", dtype=torch.float32) / V
+    noise = torch.randn((G * K, V), device="cuda", generator=gen)
+    s = -10 * torch.rand(G * K, device="cuda", generator=gen)
+    search = check(api, 30 * ramp + noise, s, K=K)
+    check(api, 5 * torch.floor(ramp * V / 4096) + noise, s, K=K, search=search)
+    check(api, (30 * ramp + noise).bfloat16(), s, K=K, search=search)
+    x = 30 * ramp + noise
+    x[:, 5::4097] = math.nan
+    x[:, 7::9001] = math.inf
+    check(api, x, s, K=K, search=search)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_finished_slots_stand_still(api, dtype):
     K, V, end = 4, 5000, 7

@@ -10,6 +10,7 @@
 //                of its sequence: one counting sort of the sequences gives both.
 //   then         the frozen heads' generator tables, 128 entries a block
 //   the last     rows of no sequence, cleared where asked
+// 7 us for 16 sequences: a chain of scans by one block, beside tables of 4096 entries.
 // packed_pre / packed_post: the backward's row passes (D = rowsum(dO o O), -lse log2 e,
 // zeros of dQ's accumulator; dQ from it), by tiles and heads.
 #include <cuda_bf16.h>

@@ -14,6 +14,10 @@
 // their cosines and sines once in registers and goes through the heads of Q and K with
 // them, three heads' loads in flight; no shared memory, no barrier.  With few tokens the
 // heads are shared out over several threads, which then form the same sines.
+// Measured: Q and K (bf16, parts of one projection) of 33.4k tokens, 12 + 12 heads of 64, 38 us,
+// 5.3 TB/s or 80 % of the copy rate; fp32, 2 x 8190 tokens, 16 + 4 heads of 128, 58 us, 86 %;
+// one token of 64 sequences 6 us (launch, position, sine, row: one latency after another).
+// With the sines of 16 tokens in shared memory and a barrier the first took 48 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -57,7 +57,8 @@ struct FwdSmem {
   static constexpr int OFF_AUX = OFF_X + 3 * 2 * 128 * 4;
   static constexpr int OFF_BAR = OFF_AUX + AST * AUX_SLOT;
   static constexpr int NBAR =
-      2 * QST + 2 * KST + 2 * VST + 3 * NBUF + 2 + 2 + 2 * AST + 2 + 1 + 2 * kItemSlots;  // NBUF >= NBUF_T
+      2 * QST + 2 * KST + 2 * VST + 3 * NBUF + 2 + 2 + 2 * AST + 2 + 1 +
+      2 * kItemSlots;  // NBUF >= NBUF_T
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_ITEM = OFF_MISC + 16;
   static constexpr int BYTES = OFF_ITEM + 4 * kItemSlots;
@@ -154,7 +155,8 @@ struct Item {
   // sequences, the records from `rank` on):
   int row0, len;   // the sequence's first row and its rows
   int rank;        // of the (first) tile's record
-  int span, tile0; // transposed: inner tiles of one head; the sequence's first tile
+  int span;        // transposed: inner tiles of one head
+  int more[3];     // transposed: query tiles of the group's other sequences (0: none), falling
 };
 
 // Longest first: forward items in descending query tile; for each tile the
@@ -186,10 +188,11 @@ __device__ __forceinline__ Item decode_item(const FwdParams& p, int it) {
   return r;
 }
 
-// The same for sequences laid end to end, from the plan's records (row0, len, X, tile0),
-// sorted by falling steps: the static items first (forward: groups of tiles that
-// share X; transposed: a tile under a K/V head, all frozen heads of which one item
-// goes through), then the dynamic ones, the heads of a tile next to one another.
+// The same for sequences laid end to end, from the plan's records (row0, len, X, -),
+// sorted by falling steps: the static items first (groups of tiles of different sequences
+// that share X, the longest sequence first; transposed under a K/V head, all frozen heads of
+// which one item goes through), then the dynamic ones, the heads of a tile next to one
+// another.
 template <bool TRANSPOSED>
 __device__ __forceinline__ Item decode_item(const PackedFwdParams& p, int it) {
   Item r;
@@ -199,8 +202,13 @@ __device__ __forceinline__ Item decode_item(const PackedFwdParams& p, int it) {
   const int n_st = TRANSPOSED ? 0 : p.hdr[1] * p.n_static;
   if (TRANSPOSED) {
     r.is_static = true;
-    r.rank = it / p.n_kv_st;
-    r.h = p.kv_list[it - r.rank * p.n_kv_st];  // the K/V head
+    const int g = it / p.n_kv_st;
+    r.h = p.kv_list[it - g * p.n_kv_st];  // the K/V head
+    const int2 grp = p.groups[g];
+    r.rank = grp.x;
+    r.nb = grp.y;
+#pragma unroll
+    for (int k = 1; k < 4; ++k) r.more[k - 1] = k < r.nb ? (p.tiles[r.rank + k].y + 127) / 128 : 0;
   } else if (it < n_st) {
     r.is_static = true;
     const int g = it / p.n_static;
@@ -218,10 +226,14 @@ __device__ __forceinline__ Item decode_item(const PackedFwdParams& p, int it) {
   r.row0 = t.x;
   r.len = t.y;
   r.X = t.z;
-  r.tile0 = t.w;
   r.span = (r.len + 127) / 128 - r.X;
   r.nsteps = TRANSPOSED ? p.st_count[r.h] * r.span : r.X + 1;
   return r;
+}
+
+// Sequences of a transposed item's group that have query tile I (the longest ones).
+__device__ __forceinline__ int with_tile(const Item& w, int I) {
+  return 1 + (w.more[0] > I) + (w.more[1] > I) + (w.more[2] > I);
 }
 
 // Row `row` of head `h` of the output.
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(384, 1)
   const int H = p.H, T = p.T;
   const int n_items = [&] {
     if constexpr (PACKED)
-      return TRANSPOSED ? p.hdr[0] * p.n_kv_st
+      return TRANSPOSED ? p.hdr[1] * p.n_kv_st
                         : p.hdr[1] * p.n_static + p.hdr[0] * p.n_dynamic;
     else
       return p.n_items;
@@ -443,7 +455,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int q = step / w.span;
                 dist0 = step - q * w.span;
                 hs = p.st_by_kv[p.st_begin[w.h] + q];
-                col_src = p.row_vals + ((size_t)hs * p.nt_max + w.tile0 + w.X + dist0) * 128;
+                col_src = p.row_vals + (size_t)hs * T + (w.X + dist0) * 128;
               } else {
                 col_src = p.a_tab + (size_t)hs * T + step * 128;
               }
@@ -500,26 +512,34 @@ __global__ void __launch_bounds__(384, 1)
         }
         ++vc;
       };
+      auto skip_odd = [&](int nb) {
+        if (!(L::PAIR_V && nb == 2 && (vc & 1))) return;
+        // the pair must start at an even slot: one slot carries nothing
+        if (lane == 0) {
+          const int vs = vc % L::VST;
+          mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
+          mbar_arrive(v_full + vs);
+        }
+        __syncwarp();
+        ++vc;
+      };
       for (int it = take_warp(); it < n_items; it = take_warp()) {
         const Item w = decode_item<TRANSPOSED>(p, it);
         for (int step = 0; step < w.nsteps; ++step) {
           if (TRANSPOSED) {
             const int q = step / w.span, I = w.X + (step - q * w.span);
-            const int hs = p.st_by_kv[p.st_begin[w.h] + q];
-            load_v(w.row0 + I * 128, p.static_heads[hs], w.len - I * 128);
+            const int h = p.static_heads[p.st_by_kv[p.st_begin[w.h] + q]];
+            const int nb = with_tile(w, I);
+            skip_odd(nb);
+            load_v(w.row0 + I * 128, h, w.len - I * 128);
+            for (int bb = 1; bb < nb; ++bb) {
+              const int4 t = p.tiles[w.rank + bb];
+              load_v(t.x + I * 128, h, t.y - I * 128);
+            }
           } else if (!w.is_static) {
             load_v(w.row0 + step * 128, w.h / p.group_kv, w.len - step * 128);
           } else {
-            if (L::PAIR_V && w.nb == 2 && (vc & 1)) {
-              // the pair must start at an even slot: one slot carries nothing
-              if (lane == 0) {
-                const int vs = vc % L::VST;
-                mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
-                mbar_arrive(v_full + vs);
-              }
-              __syncwarp();
-              ++vc;
-            }
+            skip_odd(w.nb);
             for (int bb = 0; bb < w.nb; ++bb) {
               const int4 t = p.tiles[w.rank + bb];
               load_v(t.x + step * 128, w.h / p.group_kv, t.y - step * 128);
@@ -536,133 +556,133 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (!PACKED && (warp == 0 || warp == 2)) {
     if constexpr (!PACKED) {
-    // ---------------------------------------------------------- producers
-    // warp 0: Q, K (and a static step's tables); warp 2 (after the TMEM
-    // allocation): V, so that neither ring waits behind the other
-    const bool kprod = (warp == 0);
-    if (lane == 0) {
-      uint32_t qc = 0, kc = 0, vc = 0, ac = 0;
-      uint32_t kn0 = 0, kn1 = 0;  // SPLIT: uses of each issuer's K ring
-      bool held_q = false;        // the first Q tile was withheld (testing)
-      for (int it = take_lane(); it < n_items; it = take_lane()) {
-        const Item w = decode_item<TRANSPOSED>(p, it);
-        if (!w.is_static) {
-          const int row0 = (w.b * H + w.h) * T;                           // Q rows
-          const int kv0 = (w.b * p.H_kv + w.h / p.group_kv) * T;          // K/V rows
-          if (kprod) {
-            const int qs = qc % L::QST;
-            mbar_wait(q_empty + qs, ((qc / L::QST) & 1) ^ 1, wc, kSiteProdQ);
-            // failure-path testing: CTA 0 withholds its first Q tile, so that
-            // the waits on it run out (it is then not drained either)
-            const bool hold = p.hold_first_q && blockIdx.x == 0 && qc == 0;
-            held_q |= hold;
-            ++qc;
-            if (!hold) {
-              mbar_arrive_expect_tx(q_full + qs, G::TILE_BYTES);
-              for (int c = 0; c < G::NCHUNK; ++c)
-                tma_load_2d(smem + L::OFF_Q + qs * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_q,
-                            q_full + qs, c * G::CHUNK, row0 + w.X * 128);
-            }
-            for (int j = 0; j < w.nsteps; ++j) {
-              int ks;
-              uint32_t kpar;
-              if (SPLIT) {
-                const uint32_t n = (j & 1) ? kn1++ : kn0++;
-                ks = 2 * (j & 1) + (int)(n & 1);
-                kpar = ((n >> 1) & 1) ^ 1;
-              } else {
-                ks = kc % L::KST;
-                kpar = ((kc / L::KST) & 1) ^ 1;
-                ++kc;
+      // ---------------------------------------------------------- producers
+      // warp 0: Q, K (and a static step's tables); warp 2 (after the TMEM
+      // allocation): V, so that neither ring waits behind the other
+      const bool kprod = (warp == 0);
+      if (lane == 0) {
+        uint32_t qc = 0, kc = 0, vc = 0, ac = 0;
+        uint32_t kn0 = 0, kn1 = 0;  // SPLIT: uses of each issuer's K ring
+        bool held_q = false;        // the first Q tile was withheld (testing)
+        for (int it = take_lane(); it < n_items; it = take_lane()) {
+          const Item w = decode_item<TRANSPOSED>(p, it);
+          if (!w.is_static) {
+            const int row0 = (w.b * H + w.h) * T;                           // Q rows
+            const int kv0 = (w.b * p.H_kv + w.h / p.group_kv) * T;          // K/V rows
+            if (kprod) {
+              const int qs = qc % L::QST;
+              mbar_wait(q_empty + qs, ((qc / L::QST) & 1) ^ 1, wc, kSiteProdQ);
+              // failure-path testing: CTA 0 withholds its first Q tile, so that
+              // the waits on it run out (it is then not drained either)
+              const bool hold = p.hold_first_q && blockIdx.x == 0 && qc == 0;
+              held_q |= hold;
+              ++qc;
+              if (!hold) {
+                mbar_arrive_expect_tx(q_full + qs, G::TILE_BYTES);
+                for (int c = 0; c < G::NCHUNK; ++c)
+                  tma_load_2d(smem + L::OFF_Q + qs * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_q,
+                              q_full + qs, c * G::CHUNK, row0 + w.X * 128);
               }
-              mbar_wait(k_empty + ks, kpar, wc, kSiteProdK);
-              mbar_arrive_expect_tx(k_full + ks, G::TILE_BYTES);
-              for (int c = 0; c < G::NCHUNK; ++c)
-                tma_load_2d(smem + L::OFF_K + ks * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_k,
-                            k_full + ks, c * G::CHUNK, kv0 + j * 128);
-            }
-          } else {
-            for (int j = 0; j < w.nsteps; ++j) {
-              const int vs = vc % L::VST;
-              mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
-              ++vc;
-              mbar_arrive_expect_tx(v_full + vs, G::TILE_BYTES);
-              for (int c = 0; c < G::NCHUNK; ++c)
-                tma_load_2d(smem + L::OFF_V + vs * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_v,
-                            v_full + vs, c * G::CHUNK, kv0 + j * 128);
-            }
-          }
-        } else {
-          // A static step's tables go into the table ring (warp 0), its V
-          // tiles into the V ring (warp 2).
-          auto load_aux = [&](int step) {
-            // inner tile Y: J (forward) or I (transposed)
-            const int Y = TRANSPOSED ? (w.X + step) : step;
-            const int dist0 = TRANSPOSED ? (Y - w.X) : (w.X - Y);  // (I - J) in tiles
-            const int as = ac % L::AST;
-            mbar_wait(aux_empty + as, ((ac / L::AST) & 1) ^ 1, wc, kSiteProdK);
-            ++ac;
-            mbar_arrive_expect_tx(aux_full + as, L::AUX_BYTES);
-            uint8_t* aux = smem + L::OFF_AUX + as * L::AUX_SLOT;
-            // column values: a(j) for j in tile J (forward) or row values of
-            // tile I (transposed)
-            const float* col_src = TRANSPOSED ? (p.row_tab + (size_t)w.hs * T + Y * 128)
-                                              : (p.a_tab + (size_t)w.hs * T + Y * 128);
-            bulk_load(aux + L::AUX_COL, col_src, 512, aux_full + as);
-            bulk_load(aux + L::AUX_WIN, p.r_tab + (size_t)w.hs * (T + 128) + dist0 * 128, 1024,
-                      aux_full + as);
-          };
-          if (kprod) {
-            for (int step = 0; step < w.nsteps; ++step) load_aux(step);
-          } else {
-            for (int step = 0; step < w.nsteps; ++step) {
-              const int Y = TRANSPOSED ? (w.X + step) : step;
-              if (L::PAIR_V && w.nb == 2 && (vc & 1)) {
-                // the pair must start at an even slot: one slot carries nothing
-                const int vs = vc % L::VST;
-                mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
-                ++vc;
-                mbar_arrive(v_full + vs);
+              for (int j = 0; j < w.nsteps; ++j) {
+                int ks;
+                uint32_t kpar;
+                if (SPLIT) {
+                  const uint32_t n = (j & 1) ? kn1++ : kn0++;
+                  ks = 2 * (j & 1) + (int)(n & 1);
+                  kpar = ((n >> 1) & 1) ^ 1;
+                } else {
+                  ks = kc % L::KST;
+                  kpar = ((kc / L::KST) & 1) ^ 1;
+                  ++kc;
+                }
+                mbar_wait(k_empty + ks, kpar, wc, kSiteProdK);
+                mbar_arrive_expect_tx(k_full + ks, G::TILE_BYTES);
+                for (int c = 0; c < G::NCHUNK; ++c)
+                  tma_load_2d(smem + L::OFF_K + ks * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_k,
+                              k_full + ks, c * G::CHUNK, kv0 + j * 128);
               }
-              for (int bb = 0; bb < w.nb; ++bb) {
+            } else {
+              for (int j = 0; j < w.nsteps; ++j) {
                 const int vs = vc % L::VST;
                 mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
                 ++vc;
                 mbar_arrive_expect_tx(v_full + vs, G::TILE_BYTES);
-                // forward: V of the head's K/V group; transposed: dO of the head
-                const int row0 = TRANSPOSED ? ((w.b + bb) * H + w.h) * T
-                                            : ((w.b + bb) * p.H_kv + w.h / p.group_kv) * T;
                 for (int c = 0; c < G::NCHUNK; ++c)
                   tma_load_2d(smem + L::OFF_V + vs * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_v,
-                              v_full + vs, c * G::CHUNK, row0 + Y * 128);
+                              v_full + vs, c * G::CHUNK, kv0 + j * 128);
+              }
+            }
+          } else {
+            // A static step's tables go into the table ring (warp 0), its V
+            // tiles into the V ring (warp 2).
+            auto load_aux = [&](int step) {
+              // inner tile Y: J (forward) or I (transposed)
+              const int Y = TRANSPOSED ? (w.X + step) : step;
+              const int dist0 = TRANSPOSED ? (Y - w.X) : (w.X - Y);  // (I - J) in tiles
+              const int as = ac % L::AST;
+              mbar_wait(aux_empty + as, ((ac / L::AST) & 1) ^ 1, wc, kSiteProdK);
+              ++ac;
+              mbar_arrive_expect_tx(aux_full + as, L::AUX_BYTES);
+              uint8_t* aux = smem + L::OFF_AUX + as * L::AUX_SLOT;
+              // column values: a(j) for j in tile J (forward) or row values of
+              // tile I (transposed)
+              const float* col_src = TRANSPOSED ? (p.row_tab + (size_t)w.hs * T + Y * 128)
+                                                : (p.a_tab + (size_t)w.hs * T + Y * 128);
+              bulk_load(aux + L::AUX_COL, col_src, 512, aux_full + as);
+              bulk_load(aux + L::AUX_WIN, p.r_tab + (size_t)w.hs * (T + 128) + dist0 * 128, 1024,
+                        aux_full + as);
+            };
+            if (kprod) {
+              for (int step = 0; step < w.nsteps; ++step) load_aux(step);
+            } else {
+              for (int step = 0; step < w.nsteps; ++step) {
+                const int Y = TRANSPOSED ? (w.X + step) : step;
+                if (L::PAIR_V && w.nb == 2 && (vc & 1)) {
+                  // the pair must start at an even slot: one slot carries nothing
+                  const int vs = vc % L::VST;
+                  mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
+                  ++vc;
+                  mbar_arrive(v_full + vs);
+                }
+                for (int bb = 0; bb < w.nb; ++bb) {
+                  const int vs = vc % L::VST;
+                  mbar_wait(v_empty + vs, ((vc / L::VST) & 1) ^ 1, wc, kSiteProdV);
+                  ++vc;
+                  mbar_arrive_expect_tx(v_full + vs, G::TILE_BYTES);
+                  // forward: V of the head's K/V group; transposed: dO of the head
+                  const int row0 = TRANSPOSED ? ((w.b + bb) * H + w.h) * T
+                                              : ((w.b + bb) * p.H_kv + w.h / p.group_kv) * T;
+                  for (int c = 0; c < G::NCHUNK; ++c)
+                    tma_load_2d(smem + L::OFF_V + vs * G::TILE_BYTES + c * G::CHUNK_BYTES, &tm_v,
+                                v_full + vs, c * G::CHUNK, row0 + Y * 128);
+                }
               }
             }
           }
         }
-      }
-      // Drain: every copy issued must have landed before the CTA exits (a
-      // withheld Q tile, use 0 of slot 0, was never issued).
-      for (int s = 0; s < L::QST; ++s)
-        if (qc > (uint32_t)s && !(held_q && s == 0 && (qc - 1) / L::QST == 0))
-          mbar_drain(q_full + s, ((qc - 1 - s) / L::QST) & 1);
-      if (SPLIT) {
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t n = g ? kn1 : kn0;
-          for (uint32_t i = 0; i < 2; ++i)
-            if (n > i) {
-              const uint32_t m = n - 1 - i;  // the last use of slot 2g + (m & 1)
-              mbar_drain(k_full + 2 * g + (int)(m & 1), (m >> 1) & 1);
-            }
+        // Drain: every copy issued must have landed before the CTA exits (a
+        // withheld Q tile, use 0 of slot 0, was never issued).
+        for (int s = 0; s < L::QST; ++s)
+          if (qc > (uint32_t)s && !(held_q && s == 0 && (qc - 1) / L::QST == 0))
+            mbar_drain(q_full + s, ((qc - 1 - s) / L::QST) & 1);
+        if (SPLIT) {
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t n = g ? kn1 : kn0;
+            for (uint32_t i = 0; i < 2; ++i)
+              if (n > i) {
+                const uint32_t m = n - 1 - i;  // the last use of slot 2g + (m & 1)
+                mbar_drain(k_full + 2 * g + (int)(m & 1), (m >> 1) & 1);
+              }
+          }
+        } else {
+          for (int s = 0; s < L::KST; ++s)
+            if (kc > (uint32_t)s) mbar_drain(k_full + s, ((kc - 1 - s) / L::KST) & 1);
         }
-      } else {
-        for (int s = 0; s < L::KST; ++s)
-          if (kc > (uint32_t)s) mbar_drain(k_full + s, ((kc - 1 - s) / L::KST) & 1);
+        for (int s = 0; s < L::AST; ++s)
+          if (ac > (uint32_t)s) mbar_drain(aux_full + s, ((ac - 1 - s) / L::AST) & 1);
+        for (int s = 0; s < L::VST; ++s)
+          if (vc > (uint32_t)s) mbar_drain(v_full + s, ((vc - 1 - s) / L::VST) & 1);
       }
-      for (int s = 0; s < L::AST; ++s)
-        if (ac > (uint32_t)s) mbar_drain(aux_full + s, ((ac - 1 - s) / L::AST) & 1);
-      for (int s = 0; s < L::VST; ++s)
-        if (vc > (uint32_t)s) mbar_drain(v_full + s, ((vc - 1 - s) / L::VST) & 1);
-    }
     }  // !PACKED
   } else if (SPLIT && (warp == 1 || warp == 3)) {
     // ---------------------------------------------------------- MMA issuers
@@ -883,7 +903,9 @@ __global__ void __launch_bounds__(384, 1)
             mbar_wait(p_full + pb, (u / NB) & 1, wc, kSiteMmaP);
             if (step == 0) mbar_wait(o_empty, (oc & 1) ^ 1, wc, kSiteMmaO);
             const uint32_t ga = tmem + kTmemS + pb * 128;
-            if (L::PAIR_V && w.nb == 2) {
+            int nb = w.nb;
+            if constexpr (PACKED && TRANSPOSED) nb = with_tile(w, w.X + step % w.span);
+            if (L::PAIR_V && nb == 2) {
               // Two sequences' V tiles in adjacent slots form one [128 x 2 d_h]
               // MN-major operand (the slot stride is the chunk stride), so one
               // N = 2 d_h product fills O_b0 | O_b1.
@@ -906,7 +928,7 @@ __global__ void __launch_bounds__(384, 1)
               mma_commit(v_empty + vs + 1);
               vc += 2;
             } else {
-              for (int bb = 0; bb < w.nb; ++bb) {
+              for (int bb = 0; bb < nb; ++bb) {
                 const int vs = vc % L::VST;
                 mbar_wait(v_full + vs, (vc / L::VST) & 1, wc, kSiteMmaV);
                 tc_fence_after();
@@ -1392,35 +1414,35 @@ __global__ void __launch_bounds__(384, 1)
             continue;
           }
           if constexpr (!PACKED) {
-          const size_t orow = ((size_t)((w.b + bb) * H + w.h) * T + trow_i);
-          if (TRANSPOSED && p.out_acc) {
-            // grouped K/V: several query heads add into one K/V head's dV
-            const size_t arow =
-                ((size_t)((w.b + bb) * p.H_kv + w.h / p.group_kv) * T + trow_i);
-            float* dst = p.out_acc + arow * D + hf * DH;
+            const size_t orow = ((size_t)((w.b + bb) * H + w.h) * T + trow_i);
+            if (TRANSPOSED && p.out_acc) {
+              // grouped K/V: several query heads add into one K/V head's dV
+              const size_t arow =
+                  ((size_t)((w.b + bb) * p.H_kv + w.h / p.group_kv) * T + trow_i);
+              float* dst = p.out_acc + arow * D + hf * DH;
+#pragma unroll
+              for (int c0 = 0; c0 < DH; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(trow + kTmemO + bb * D + hf * DH + c0, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                  atomicAdd(reinterpret_cast<float4*>(dst + c0 + e),
+                            make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])));
+              }
+              continue;
+            }
+            __nv_bfloat16* dst = p.out + orow * D + hf * DH;
 #pragma unroll
             for (int c0 = 0; c0 < DH; c0 += 16) {
               uint32_t o[16];
               tmem_ld_x16(trow + kTmemO + bb * D + hf * DH + c0, o);
               tmem_wait_ld(o);
-#pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                atomicAdd(reinterpret_cast<float4*>(dst + c0 + e),
-                          make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                      __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])));
+              store_row16(dst + c0, o, oscale);
             }
-            continue;
-          }
-          __nv_bfloat16* dst = p.out + orow * D + hf * DH;
-#pragma unroll
-          for (int c0 = 0; c0 < DH; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld_x16(trow + kTmemO + bb * D + hf * DH + c0, o);
-            tmem_wait_ld(o);
-            store_row16(dst + c0, o, oscale);
-          }
-          if (!TRANSPOSED && hf == 0 && p.lse)
-            p.lse[orow] = exact ? p.logZ[(size_t)w.hs * T + trow_i] : lse_i;
+            if (!TRANSPOSED && hf == 0 && p.lse)
+              p.lse[orow] = exact ? p.logZ[(size_t)w.hs * T + trow_i] : lse_i;
           }
         }
         tc_fence_before();

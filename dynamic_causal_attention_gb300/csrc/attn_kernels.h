@@ -49,16 +49,15 @@ inline int static_group(int d_h, int B, bool transposed = false) {
 // The same for sequences laid end to end: T is the length of the tables, and items
 // come from a plan that the preparing kernel makes on the device.
 struct PackedFwdParams : FwdParams {
-  const int* hdr;        // {tiles, groups of static forward items}
+  const int* hdr;        // {tiles, groups of static items}
   int* counter;          // items handed out, zero at the start
-  const int4* tiles;     // (row0, len, X, tile0), most steps first
-  const int2* groups;    // forward: (first record, records) that share X
+  const int4* tiles;     // (row0, len, X, -), most steps first
+  const int2* groups;    // (first record, records) that share X
   int total;             // rows of lse and out_acc
-  int nt_max;            // tiles that row_vals has for each head
   int64_t out_row, out_head;
   // transposed: the frozen heads (as slots of the tables) by K/V head
   int n_kv_st;
-  const float* row_vals; // [n_static, nt_max * 128]
+  const float* row_vals; // [n_static, T]: the weights of a query's row, at its position
   uint8_t kv_list[kMaxHeads], kv_has_dyn[kMaxHeads], st_by_kv[kMaxHeads];
   uint16_t st_begin[kMaxHeads], st_count[kMaxHeads];
 };

@@ -18,12 +18,16 @@ struct ClearRows {
 
 struct PackedPrep {
   int total, n_seqs, max_len, max_tiles;  // max_tiles = ceil(max_len / 128)
-  int group;                 // tiles of a static forward item
+  bool backward;             // groups are of the transposed form
+  int group;                 // most tiles of a static item
+  int per_tile;              // work items of a tile that shares nothing
+  int num_sms;
   const int32_t* cu;         // [n_seqs + 1]
   int* status;
-  int* hdr;                  // {tiles, static groups, two counters of items handed out}
+  int* hdr;                  // {tiles, groups, two counters of items handed out, first tile of the
+                             // longest sequence (backward)}
   int4 *by_key, *by_query;   // records by falling X + 1 and by falling query tiles
-  int2* groups;
+  int2* groups;              // (first record of by_key, records) that share X
   int4* seqs;                // [n_seqs] scratch
   // tables of the frozen heads, T = 128 * max_tiles entries a head (see static_prep_kernel)
   int T, T_pat, n_static;
@@ -48,7 +52,8 @@ struct PackedRows {
   int64_t out_row, out_head, do_row, do_head;
   const float* lse;          // [H, total]
   float *Dvec, *lse2;        // [H, nt_max * 128]
-  float* row_vals;           // [n_static, nt_max * 128]
+  float* row_vals;           // [n_static, T], by the position in a sequence
+  int T;
   const int* mode;
   const float* shift;
   float* dq_acc;             // [H, total, d]

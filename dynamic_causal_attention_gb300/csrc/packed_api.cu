@@ -69,7 +69,7 @@ PackedWs packed_ws(const saf_packed_dims& d, bool backward) {
   const size_t b = backward ? 1 : 0;
   w.Dvec = take(b * H * nt * 512);
   w.lse2 = take(b * H * nt * 512);
-  w.row_vals = take(b * H * nt * 512);
+  w.row_vals = take(b * H * T * 4);
   w.dq_acc = take(b * H * d.total * d.d_h * 4);
   w.dv_acc = take(b * d.H_kv * d.total * d.d_h * 4);
   w.order = take(b * (kOrderRounds + 1) * 256 * 16);
@@ -113,14 +113,27 @@ struct Call {
 };
 
 PackedPrep make_prep(const Call& c, const int32_t* cu, const float* alpha, const float* rho,
-                     bool clear) {
+                     bool backward, bool clear) {
   PackedPrep p;
   memset(&p, 0, sizeof(p));
   p.total = c.d.total;
   p.n_seqs = c.d.n_seqs;
   p.max_len = c.d.max_len;
   p.max_tiles = tiles_of(c.d.max_len);
-  p.group = 128 / c.d.d_h;
+  // (the accumulators that fit beside the tiles of weights: static_group)
+  p.backward = backward;
+  p.group = static_group(c.d.d_h, 4, backward);
+  p.per_tile = c.d.H;
+  if (backward) {
+    // dV of the K/V heads that frozen heads read
+    p.per_tile = 0;
+    for (int kv = 0; kv < c.Hkv; ++kv) {
+      int frozen = 0;
+      for (int h = kv * c.g; h < (kv + 1) * c.g; ++h) frozen |= c.hs.is_static[h];
+      p.per_tile += frozen;
+    }
+  }
+  p.num_sms = sm_count();
   p.cu = cu;
   p.status = c.at<int>(c.w.status);
   p.hdr = c.at<int>(c.w.hdr);
@@ -173,7 +186,6 @@ void fill_fwd(PackedFwdParams& p, const Call& c) {
   p.counter = c.at<int>(c.w.hdr) + 2;
   p.groups = c.at<int2>(c.w.groups);
   p.total = c.d.total;
-  p.nt_max = c.nt;
 }
 
 // Blocks for `n` items per tile: the plan may hold fewer.
@@ -243,7 +255,7 @@ saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_rows* Q, c
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return SAF_ERR_INVALID_ARG;
   if (ws_bytes < c.w.total) return SAF_ERR_INVALID_ARG;
 
-  PackedPrep prep = make_prep(c, cu_seqlens, alpha, rho, (flags & SAF_CLEAR_REST) != 0);
+  PackedPrep prep = make_prep(c, cu_seqlens, alpha, rho, false, (flags & SAF_CLEAR_REST) != 0);
   clear_too(prep, *out, d, d.H);
   prep.lse = lse;
   SAF_TRY(launch_packed_prep(prep, c.s));
@@ -298,7 +310,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return SAF_ERR_INVALID_ARG;
   if (ws_bytes < c.w.total) return SAF_ERR_INVALID_ARG;
 
-  PackedPrep prep = make_prep(c, cu_seqlens, alpha, rho, (flags & SAF_CLEAR_REST) != 0);
+  PackedPrep prep = make_prep(c, cu_seqlens, alpha, rho, true, (flags & SAF_CLEAR_REST) != 0);
   clear_too(prep, *dQ, d, d.H);
   clear_too(prep, *dK, d, d.H_kv);
   clear_too(prep, *dV, d, d.H_kv);
@@ -326,6 +338,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
   r.Dvec = c.at<float>(c.w.Dvec);
   r.lse2 = c.at<float>(c.w.lse2);
   r.row_vals = c.at<float>(c.w.row_vals);
+  r.T = tiles_of(d.max_len) * 128;
   r.mode = c.at<int>(c.w.mode);
   r.shift = c.at<float>(c.w.shift);
   r.dq_acc = c.at<float>(c.w.dq_acc);
@@ -390,7 +403,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     memset(&L, 0, sizeof(L));
     fill_fwd(L.p, c);
     L.p.counter = c.at<int>(c.w.hdr) + 3;
-    L.p.tiles = c.at<int4>(c.w.by_query);
+    L.p.tiles = c.at<int4>(c.w.by_key);
     L.p.out = static_cast<__nv_bfloat16*>(dV->p);
     L.p.out_row = row_of(*dV, d);
     L.p.out_head = head_of(*dV, c.Hkv);

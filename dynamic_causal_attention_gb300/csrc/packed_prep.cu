@@ -8,6 +8,7 @@
 //                1..n in either order, so with the sequences sorted by falling n those that have
 //                key k are the first cnt[k], and a record's place is start[k] + place
 //                of its sequence: one counting sort of the sequences gives both.
+//                Neighbours in the first order share X and a frozen head's weights.
 //   then         the frozen heads' generator tables, 128 entries a block
 //   the last     rows of no sequence, cleared where asked
 // 7 us for 16 sequences: a chain of scans by one block, beside tables of 4096 entries.
@@ -37,7 +38,8 @@ struct PlanShared {
   int start[kMaxPackedTiles + 2];   // records of keys above k
   int gstart[kMaxPackedTiles + 2];  // groups of keys above k
   int warp_max[kPrepWarps], warp_sum[kPrepWarps];
-  int end, tiles;
+  int end, tiles, group;
+  unsigned long long longest;       // (rows, first tile) of the longest sequence
 };
 
 // Inclusive suffix sums of v[0 .. n) into out[i] = sum of v[j], j >= i (or j > i), by one warp.
@@ -68,6 +70,7 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
     p.hdr[2] = p.hdr[3] = 0;
     sh.end = max(0, min(p.cu[0], p.total));
     sh.tiles = 0;
+    sh.longest = 0;
   }
   for (int i = tid; i < m + 2; i += kPrepThreads) sh.hist[i] = 0;
   __syncthreads();
@@ -104,6 +107,7 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
     if (b < n) {
       p.seqs[b] = make_int4(a, len, tile0, 0);
       atomicAdd(&sh.hist[nt], 1);
+      if (p.backward) atomicMax(&sh.longest, (unsigned long long)len << 32 | (unsigned)tile0);
     }
     __syncthreads();
     if (tid == kPrepThreads - 1) {
@@ -116,17 +120,25 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
     warp_suffix(m + 2, sh.cnt, false, [&](int i) { return sh.hist[i]; });
     __syncwarp();
     const int tiles = warp_suffix(m + 2, sh.start, true, [&](int i) { return i ? sh.cnt[i] : 0; });
+    // Tiles share generated weights where there are more items than SMs; with fewer, an
+    // item that carries several tiles only takes longer (dV of a K/V head of 32 and 40
+    // documents of up to 300 tokens: 16.4 us shared, 11 not; of 3 of 64 and 16 documents of
+    // up to 4096: 49.7 and 62.9).
+    const int g = tiles * p.per_tile > p.num_sms ? p.group : 1;
     const int groups = warp_suffix(m + 2, sh.gstart, true, [&](int i) {
-      return i ? (sh.cnt[i] + p.group - 1) / p.group : 0;
+      return i ? (sh.cnt[i] + g - 1) / g : 0;
     });
     if (lane == 0) {
+      sh.group = g;
       p.hdr[0] = tiles;
       p.hdr[1] = groups;
+      p.hdr[4] = (int)(unsigned)sh.longest;
     }
   }
   __syncthreads();
   for (int i = tid; i <= m; i += kPrepThreads) sh.hist[i] = sh.cnt[i + 1];
   __syncthreads();
+  const int g = sh.group;
   for (int b = warp; b < n; b += kPrepWarps) {
     const int4 q = p.seqs[b];
     const int nt = (q.y + 127) / 128;
@@ -138,9 +150,11 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
       const int kf = X + 1, kb = nt - X;
       p.by_key[sh.start[kf] + place] = rec;
       p.by_query[sh.start[kb] + place] = rec;
-      if (place % p.group == 0)
-        p.groups[sh.gstart[kf] + place / p.group] =
-            make_int2(sh.start[kf] + place, min(p.group, sh.cnt[kf] - place));
+      // (groups come by falling steps: of the transposed form by the query tiles of their
+      // first sequence, which has the most)
+      if (place % g == 0)
+        p.groups[sh.gstart[p.backward ? kb : kf] + place / g] =
+            make_int2(sh.start[kf] + place, min(g, sh.cnt[kf] - place));
     }
   }
 }
@@ -262,7 +276,8 @@ __device__ void clear_rows(const PackedPrep& p, int block) {
   clear_range(p, last, p.total - last, t0, step);
   for (int b = block; b < p.n_seqs; b += kClearBlocks) {
     const int a = max(0, min(p.cu[b], p.total)), e = max(0, min(p.cu[b + 1], p.total));
-    if (e - a > p.max_len) clear_range(p, a + p.max_len, e - a - p.max_len, threadIdx.x, kPrepThreads);
+    if (e - a > p.max_len)
+      clear_range(p, a + p.max_len, e - a - p.max_len, threadIdx.x, kPrepThreads);
   }
 }
 
@@ -352,7 +367,7 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__
   if ((int)blockIdx.x >= p.hdr[0]) return;
   const int4 t = p.tiles[blockIdx.x];
   const int h = (int)blockIdx.y - (p.order ? 1 : 0), hs = p.static_slot[h], kv = h / p.group_kv;
-  const int tile = t.w + t.z, valid = min(128, t.y - t.z * 128);
+  const int tile = t.w + t.z, valid = min(128, t.y - t.z * 128), longest = p.hdr[4];
   const bool zero_k = h == kv * p.group_kv && !p.kv_has_dyn[kv];
   const int sub = threadIdx.x % LPR;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -365,13 +380,14 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__
     if (hs != 255) {
       if (mine)
         *reinterpret_cast<uint4*>(p.dQ + row * p.dq_row + (int64_t)h * p.dq_head + sub * 8) = zero;
-      if (sub == 0) {
-        // the weight of a query's row: 1 / Z', or -log2 Z (exact); none behind the end
+      if (sub == 0 && t.w == longest) {
+        // the weight of a query's row: 1 / Z', or -log2 Z (exact); none behind the end.  A
+        // frozen head's depends on the position alone, so the longest sequence's serve all.
         const float l = mine ? p.lse[(int64_t)h * p.total + row] : -INFINITY;
         const bool some = l > -INFINITY;
         const float v = p.mode[hs] ? (some ? -l * kLog2e : -INFINITY)
                                    : (some ? expf(p.shift[hs] - l) : 0.f);
-        p.row_vals[((size_t)hs * p.nt_max + tile) * 128 + r] = v;
+        p.row_vals[(size_t)hs * p.T + t.z * 128 + r] = v;
       }
       continue;
     }

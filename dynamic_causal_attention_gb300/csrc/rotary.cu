@@ -151,7 +151,8 @@ __device__ __forceinline__ void heads(const RotaryRows& in, const RotaryRows& ou
 }
 
 template <typename T, int W, bool HALF>
-__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, 4)
+    rotary_kernel(const __grid_constant__ RotaryParams p) {
   const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
   const uint32_t r = fast_div(i, p.by_units), u = i - r * (uint32_t)p.units;
   const uint32_t n = fast_div(r, p.by_split);           // the row of B * T

@@ -151,6 +151,37 @@ def test_many_sequences_and_items(api, d):
     run(api, lens, 8, 4, d, [0, 1, 0, 0, 1, 1, 0, 0])
 
 
+# more work items than the GPU has SMs, so that sequences share a frozen head's weights
+SHARED = [[384] * 6, [700, 1, 130, 0, 129, 385, 384, 128, 257, 40], [900, 520, 512, 641, 300],
+          [2, 1] * 45]
+
+
+@pytest.mark.parametrize("lens", SHARED, ids=str)
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sequences_share_weights(api, lens, d):
+    def change(q, k, v, alpha, rho):
+        alpha[0, :5] = -math.inf                    # the first rows see nothing
+        alpha[1] *= 60                              # exact exponentials
+        rho[2, 60:] = torch.finfo(torch.float32).min
+        rho[3, 1:] = -math.inf
+    got = run(api, lens, 20, 20, d, [1] * 19 + [0], head=1, tail=5, change=change)
+    # sequences that share agree with one alone to the bit (with the same longest length: the
+    # tables are against the largest entries up to it)
+    q, k, v, do, alpha, rho, cu, starts = inputs(lens, 20, 20, d, head=1, tail=5)
+    change(q, k, v, alpha, rho)
+    b = max(range(len(lens)), key=lambda i: (lens[i] % 128, lens[i]))
+    rows = slice(starts[b], starts[b] + lens[b])
+    layer = api.PackedAttention(20, d, [1] * 19 + [0], max_total=lens[b], max_seqs=1,
+                                max_len=max(lens), H_kv=20)
+    one = [t[rows].contiguous() for t in (q, k, v, do)]
+    cu1 = torch.tensor([0, lens[b]], dtype=torch.int32, device="cuda")
+    out, lse = layer.forward(*one[:3], cu1, alpha, rho)
+    dv = layer.backward(*one[:3], out, lse, one[3], cu1, alpha, rho)[2]
+    assert torch.equal(got["out"][rows, :19], out[:, :19])
+    assert torch.equal(got["lse"][:19, rows], lse[:19])
+    assert torch.equal(got["dv"][rows, :19], dv[:, :19])
+
+
 def test_long_sequence(api):
     run(api, [4000, 3, 1100], 2, 1, 128, [0, 1])
 

@@ -64,7 +64,7 @@ struct PackedRows {
   int4* order;               // or null: no such pass
   int n_ctas;                // up to 256
   PackedBwdItems items;
-  uint8_t static_slot[kMaxHeads];  // 255: dynamic
+  int16_t static_slot[kMaxHeads];  // -1: dynamic
   uint8_t kv_has_dyn[kMaxHeads];
 };
 cudaError_t launch_packed_pre(const PackedRows& p, cudaStream_t s);

@@ -349,8 +349,8 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
   r.dk_row = row_of(*dK, d);
   r.dk_head = head_of(*dK, c.Hkv);
   r.scale = 1.0f / sqrtf((float)d.d_h);
-  memset(r.static_slot, 255, sizeof(r.static_slot));
-  for (int i = 0; i < c.hs.n_static; ++i) r.static_slot[c.hs.st[i]] = (uint8_t)i;
+  memset(r.static_slot, 0xff, sizeof(r.static_slot));  // -1
+  for (int i = 0; i < c.hs.n_static; ++i) r.static_slot[c.hs.st[i]] = (int16_t)i;
   for (int h = 0; h < d.H; ++h) r.kv_has_dyn[h / c.g] |= !c.hs.is_static[h];
 
   // the dynamic pass: query heads by K/V head, and its items
@@ -414,7 +414,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     for (int kv = 0; kv < c.Hkv; ++kv) {
       L.p.st_begin[kv] = (uint16_t)n;
       for (int h = kv * c.g; h < (kv + 1) * c.g; ++h)
-        if (c.hs.is_static[h]) L.p.st_by_kv[n++] = r.static_slot[h];
+        if (c.hs.is_static[h]) L.p.st_by_kv[n++] = (uint8_t)r.static_slot[h];
       L.p.st_count[kv] = (uint16_t)(n - L.p.st_begin[kv]);
       if (L.p.st_count[kv] > 0) L.p.kv_list[L.p.n_kv_st++] = (uint8_t)kv;
     }

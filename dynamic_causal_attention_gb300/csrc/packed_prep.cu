@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__
     const bool mine = r < valid;
     if (zero_k && mine)
       *reinterpret_cast<uint4*>(p.dK + row * p.dk_row + (int64_t)kv * p.dk_head + sub * 8) = zero;
-    if (hs != 255) {
+    if (hs >= 0) {
       if (mine)
         *reinterpret_cast<uint4*>(p.dQ + row * p.dq_row + (int64_t)h * p.dq_head + sub * 8) = zero;
       if (sub == 0 && t.w == longest) {
@@ -423,7 +423,7 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_post_kernel(const __grid_constant__ PackedRows p) {
   constexpr int LPR = D / 8;
   const int h = blockIdx.y;
-  if ((int)blockIdx.x >= p.hdr[0] || p.static_slot[h] != 255) return;
+  if ((int)blockIdx.x >= p.hdr[0] || p.static_slot[h] >= 0) return;
   const int4 t = p.tiles[blockIdx.x];
   const int valid = min(128, t.y - t.z * 128), sub = threadIdx.x % LPR;
   for (int r = threadIdx.x / LPR; r < valid; r += 256 / LPR) {

@@ -151,6 +151,12 @@ def test_many_sequences_and_items(api, d):
     run(api, lens, 8, 4, d, [0, 1, 0, 0, 1, 1, 0, 0])
 
 
+@pytest.mark.parametrize("Hkv", [256, 1])
+@pytest.mark.parametrize("dynamic", [(), (255,), (0,), (7, 8)])
+def test_as_many_heads_as_there_can_be(api, Hkv, dynamic):
+    run(api, [130, 3], 256, Hkv, 32, [h not in dynamic for h in range(256)])
+
+
 # more work items than the GPU has SMs, so that sequences share a frozen head's weights
 SHARED = [[384] * 6, [700, 1, 130, 0, 129, 385, 384, 128, 257, 40], [900, 520, 512, 641, 300],
           [2, 1] * 45]

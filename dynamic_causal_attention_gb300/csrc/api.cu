@@ -586,8 +586,8 @@ saf_status saf_hybrid_attn_bwd(const saf_attn_dims* dims, const void* Q, const v
   pre.lse2 = reinterpret_cast<float*>(ws + L.lse2);
   pre.Dsum = dalpha_k ? reinterpret_cast<float*>(ws + L.Dsum) : nullptr;
   pre.n_static = hs.n_static;
-  memset(pre.static_slot, 255, sizeof(pre.static_slot));
-  for (int i = 0; i < hs.n_static; ++i) pre.static_slot[hs.st[i]] = (uint8_t)i;
+  memset(pre.static_slot, 0xff, sizeof(pre.static_slot));  // -1
+  for (int i = 0; i < hs.n_static; ++i) pre.static_slot[hs.st[i]] = (int16_t)i;
   if (hs.n_static > 0) {
     pre.row_tab = reinterpret_cast<float*>(ws + L.row_tab);
     pre.mode = reinterpret_cast<const int*>(ws + L.mode);

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(BwdPre p) {
   for (int bh = blockIdx.y; bh < n_bh; bh += gridDim.y) {
     const int h = bh % p.H;
     const int hs = p.static_slot[h];
-    const bool need_d = (hs == 255) || (p.Dsum != nullptr);
+    const bool need_d = (hs < 0) || (p.Dsum != nullptr);
     for (uint32_t t = blockIdx.x * blockDim.x + threadIdx.x; t < (uint32_t)p.T * LPR;
          t += gridDim.x * blockDim.x) {
       const int i = (int)(t / LPR), sub = (int)(t % LPR);
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(BwdPre p) {
         for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
       }
       // the accumulator rows of frozen heads are never added to or read
-      if (hs == 255 && p.dq_acc) {
+      if (hs < 0 && p.dq_acc) {
         float4* z = reinterpret_cast<float4*>(p.dq_acc + row * D + sub * 8);
         z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
         z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(BwdPre p) {
           p.Dvec[row] = -acc;
           p.lse2[row] = -l * 1.4426950408889634f;
         }
-        if (hs != 255 && p.row_tab && bh < p.H) {  // sequence 0: rows (h, i)
+        if (hs >= 0 && p.row_tab && bh < p.H) {  // sequence 0: rows (h, i)
           float v;
           if (p.mode[hs]) v = -l * 1.4426950408889634f;
           else v = (l > -INFINITY) ? expf(p.shift[hs] - l) : 0.f;

@@ -92,7 +92,7 @@ struct BwdPre {
   float* row_tab;     // [n_static, T]
   const int* mode;
   const float* shift;
-  uint8_t static_slot[kMaxHeads];  // head -> index among the frozen heads, 255 if dynamic
+  int16_t static_slot[kMaxHeads];  // head -> index among the frozen heads, -1 if dynamic
 };
 cudaError_t launch_bwd_pre(const BwdPre& p, cudaStream_t s);
 

@@ -231,3 +231,11 @@ def test_masked_keys_and_fully_masked_head(api):
     assert np.all(da[1][0::2] == 0)
     assert_close(da[1][1::2], ra[1::2], "masked-keys dalpha")
     assert_close(dr[1], rr, "masked-keys drho")
+
+
+def test_as_many_frozen_heads_as_there_can_be(api):
+    cfg = AttnConfig("heads", B=1, H=256, T=256, d_h=32, dtype="bf16",
+                     static_heads=tuple(range(256)))
+    inp = attn_inputs(cfg, seed=53)
+    got = gpu_fwd_bwd(api, inp, cfg.head_is_static, False)
+    compare(got, oracle_bwd(inp, cfg.head_is_static, False), cfg.head_is_static, "256 heads", False)

@@ -14,8 +14,8 @@ import torch
 
 from . import _binding as B
 
-__all__ = ["HybridAttention", "Calibration", "PackedAttention", "PagedCache", "Rotary", "rotary_frequencies",
-           "BeamSearch", "fit_compact", "num_select", "SafError"]
+__all__ = ["HybridAttention", "Calibration", "PackedAttention", "PagedCache", "Rotary",
+           "rotary_frequencies", "BeamSearch", "fit_compact", "num_select", "SafError"]
 
 SafError = B.SafError
 
@@ -392,6 +392,12 @@ class _OnDevice:
     def _bad(self, what):
         return B.SafError(B.SAF_ERR_INVALID_ARG, what)
 
+    def _counts(self, what, *counts):
+        """Refuses what the C structs' ints do not hold (ctypes would cut it)."""
+        for n in counts:
+            if not 0 <= n < 1 << 31:
+                raise self._bad(f"{what}: {n} is out of range")
+
     # (get_device of a CPU tensor is -1: no device of ours)
     def _need(self, t, shape, dtype, what):
         """The address of a contiguous tensor of this shape, type and device."""
@@ -508,6 +514,7 @@ class Rotary(_OnDevice):
             B_, H, T, last = shape
         if last != d:
             raise self._bad(f"apply: rows of {last} components, d_h is {d}")
+        self._counts("apply: rows", B_, T, H)
         rq = self._rows(q, shape, dtype, "apply: q")
         rk = k_shape = None
         H_k = 0
@@ -540,6 +547,7 @@ class Rotary(_OnDevice):
             if not packed or len(cu_shape) != 1 or cu_shape[0] < 1:
                 raise self._bad("apply: cu_seqlens [n + 1] goes with packed rows")
             n = cu_shape[0] - 1
+            self._counts("apply: sequences", n)
             cu = self._need(cu_seqlens, cu_shape, torch.int32, "apply: cu_seqlens")
         elif seq_len is not None:
             lens = self._need(seq_len, (B_,), torch.int32, "apply: seq_len")
@@ -566,6 +574,7 @@ class PackedAttention(_OnDevice):
                  max_len: int, H_kv=None, backward: bool = True, device="cuda"):
         self._place(device)
         self.H, self.d_h, self.H_kv = H, d_h, H if H_kv is None else H_kv
+        self._counts("PackedAttention", max_total, max_seqs, max_len, H, self.H_kv, d_h)
         self.max_total, self.max_seqs, self.max_len = max_total, max_seqs, max_len
         self.head_is_static = bytes(int(bool(x)) for x in head_is_static)
         if len(self.head_is_static) != H:
@@ -593,7 +602,7 @@ class PackedAttention(_OnDevice):
             if alpha is None or rho is None:
                 raise self._bad("PackedAttention: frozen heads need alpha and rho")
             T = alpha.shape[-1] if alpha.dim() == 2 else -1
-            if T < self.max_len:
+            if not self.max_len <= T < 1 << 31:
                 raise self._bad(f"PackedAttention: {T} columns of alpha, max_len {self.max_len}")
             pa = self._need(alpha, (self.H, T), torch.float32, "PackedAttention: alpha")
             pr = self._need(rho, (self.H, T), torch.float32, "PackedAttention: rho")
@@ -670,6 +679,7 @@ class BeamSearch(_OnDevice):
         self._place(device)
         self.n_groups, self.beams, self.vocab = n_groups, beams, vocab
         self.end, self.slots = end, n_groups * beams
+        self._counts("BeamSearch", n_groups, beams, vocab, 0 if end is None else end)
         if n_groups < 1:
             raise self._bad(f"BeamSearch: {n_groups} groups")
         with torch.cuda.device(self.device):
@@ -713,6 +723,7 @@ class BeamSearch(_OnDevice):
             if n_tokens is None or len(shape) != 2 or shape[0] != slots:
                 raise self._bad("step: history [slots, columns] needs n_tokens")
             columns = shape[1]
+            self._counts("step: columns", columns)
             if history_out is None:
                 history_out = torch.full_like(history, -1)
             ph = self._need(history, shape, torch.int32, "step: history")

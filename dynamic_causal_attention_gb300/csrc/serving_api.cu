@@ -4,6 +4,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <utility>
+
 #include "../../include/saf.h"
 #include "host_common.h"
 #include "internal.h"
@@ -14,6 +16,25 @@ namespace {
 saf_status status_of(cudaError_t e) { return e == cudaSuccess ? SAF_OK : SAF_ERR_CUDA; }
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Whether rows run into one another: by rising strides, each must pass what lies below it.
+bool overlap(const saf_rows& r, int B, int T, int heads, int d) {
+  int64_t stride[3] = {r.head, r.row, r.seq};
+  int n[3] = {heads, T, B};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (stride[j] > stride[j + 1]) {
+        std::swap(stride[j], stride[j + 1]);
+        std::swap(n[j], n[j + 1]);
+      }
+  __int128 span = d;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] < 2) continue;
+    if (stride[i] < span) return true;
+    span += (__int128)stride[i] * (n[i] - 1);
+  }
+  return false;
+}
 
 constexpr int kMaxBeams = 32;
 constexpr int kMaxVocab = 1 << 22;
@@ -87,10 +108,7 @@ saf_status saf_rotary(const saf_rotary_dims* dims, const saf_rows* q, const saf_
     const saf_rows* r = rows[i];
     if (!r || !r->p || !aligned(r->p, size) || r->seq < 0 || r->row < 0 || r->head < 0)
       return SAF_ERR_INVALID_ARG;
-    // two rows of an output must not be one
-    if (i >= 2 && ((d.B > 1 && r->seq < d.d_h) || (d.T > 1 && r->row < d.d_h) ||
-                   (heads > 1 && r->head < d.d_h)))
-      return SAF_ERR_INVALID_ARG;
+    if (i >= 2 && overlap(*r, d.B, d.T, heads, d.d_h)) return SAF_ERR_INVALID_ARG;
     p.x[i] = RotaryRows{r->p, r->seq, r->row, r->head};
     if (i >= 2) {
       const saf_rows* in = rows[i - 2];

@@ -491,10 +491,10 @@ SAF_API saf_status saf_rotary_turns(const double* radians, int n, uint64_t* turn
  * it by `scale`; components from rot on are copied.
  *
  *   q, k, q_out, k_out   device rows; an output may be its input (the same saf_rows),
- *               and must not overlap one otherwise.  k, k_out are not looked at when
- *               H_k = 0 (q, q_out when H = 0).  16-byte vectors are used where all
- *               pointers and strides allow it and rot / 2 and d_h are multiples of a
- *               vector, single elements elsewhere.
+ *               and must not overlap one otherwise, nor may its own rows overlap.  k,
+ *               k_out are not looked at when H_k = 0 (q, q_out when H = 0).  16-byte
+ *               vectors are used where all pointers and strides allow it and rot / 2
+ *               and d_h are multiples of a vector, single elements elsewhere.
  *   turns       device [rot / 2], 8-byte aligned.
  * At most one of the three ways to give positions:
  *   positions   [B, T] int32; negative ones turn back.
@@ -549,10 +549,10 @@ SAF_API size_t saf_packed_attn_workspace_size(const saf_packed_dims* dims, int b
  *               a frozen head's row has no weight, whose out is 0.
  *   flags       SAF_CLEAR_REST: rows that are not worked on become 0, their lse -inf.
  *   workspace   256-byte aligned; saf_get_device_status reads its status.
- * Outputs must not overlap inputs or one another.  Both products have fp32 sums; the weights are rounded to bf16 for the second (as the
- * rows that they weigh).  An infinity or NaN in a row of V reaches rows of its own sequence
- * only: those after it, and those up to 127 rows before it.  The same call gives the
- * same bits. */
+ * Outputs must not overlap inputs or one another.  Both products have fp32 sums; the
+ * weights are rounded to bf16 for the second (as the rows that they weigh).  An
+ * infinity or NaN in a row of V reaches rows of its own sequence only: those after
+ * it, and those up to 127 rows before it.  The same call gives the same bits. */
 SAF_API saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_rows* Q,
                                const saf_rows* K, const saf_rows* V, const int32_t* cu_seqlens,
                                const float* alpha, const float* rho,

@@ -86,6 +86,33 @@ def test_rotary_refusals(B):
         assert call(dims=d, q=None, k=None, q_out=None, k_out=None, turns=None) == B.SAF_OK
 
 
+def test_rotary_outputs_must_not_run_into_themselves(B):
+    rows = lambda **kw: B.saf_rows(**{**dict(p=1 << 20, seq=4096, row=256, head=64), **kw})
+    dims = B.saf_rotary_dims(2, 8, 4, 0, 64, 64, 0)
+    call = lambda out: B.saf_rotary(dims, rows(p=16), None, out, None, 16, 1.0, None, None, 0, None,
+                                    None, 0, None)
+    for bad in (dict(row=64), dict(row=192), dict(head=256), dict(seq=64), dict(seq=1984),
+                dict(row=64, head=448), dict(seq=64, row=128, head=1023), dict(row=1 << 62, seq=1 << 62)):
+        assert call(rows(**bad)) == B.SAF_ERR_INVALID_ARG, bad
+
+
+def test_counts_beyond_an_int_are_refused(api):
+    big = (1 << 32) + 8
+    for bad in (dict(max_total=big), dict(max_seqs=big), dict(max_len=big), dict(max_total=-1)):
+        with pytest.raises(api.SafError, match="out of range"):
+            api.PackedAttention(2, 64, [0, 0], **{**dict(max_total=8, max_seqs=1, max_len=8), **bad},
+                                device="cpu")
+    for n in ((big, 1, 100), (1, big, 100), (1, 1, big)):
+        with pytest.raises(api.SafError, match="out of range"):
+            api.BeamSearch(*n, device="cpu")
+    with pytest.raises(api.SafError, match="out of range"):
+        api.BeamSearch(1, 1, 100, end=big, device="cpu")
+    import torch
+    turn = api.Rotary(2, device="cpu")
+    with pytest.raises(api.SafError, match="out of range"):
+        turn.apply(torch.zeros(1, 1, 2).expand(big, 1, 2))
+
+
 def test_rotary_objects_refuse(api):
     for bad in (dict(layout="pairs"), dict(freqs=[]), dict(freqs=[1.0] * 40), dict(rot_dim=62, freqs=[1.0]),
                 dict(freqs=[math.inf])):

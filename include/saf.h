@@ -560,7 +560,8 @@ SAF_API saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_ro
                                unsigned flags, void* workspace, size_t ws_bytes, void* stream);
 
 /* Backward, for the gradient dout of out.  out and lse are the forward's (out is not
- * looked at without dynamic heads); dQ [total, H, d_h], dK and dV [total, H_kv, d_h]
+ * looked at without dynamic heads; a frozen head's lse depends on the position alone, and
+ * the longest sequence's is read); dQ [total, H, d_h], dK and dV [total, H_kv, d_h]
  * are overwritten in the rows of the sequences: dK and dV sum over the query heads of
  * their group, dQ of frozen heads and dK that serve frozen heads only are 0.  alpha and
  * rho are constants here (saf_hybrid_attn_bwd has their gradients).  P and dS are rounded

@@ -525,14 +525,28 @@ class Rotary(_OnDevice):
             H_k = k_shape[1]
             rk = self._rows(k, (T, H_k, d) if packed else (B_, H_k, T, d), dtype, "apply: k")
         flags = self._flags | B.SAF_ROTARY_INVERSE if inverse else self._flags
+        ok = None
         if out is None:
-            out = (torch.empty(shape, dtype=dtype, device=self.device),
-                   None if k is None else torch.empty(k_shape, dtype=dtype, device=self.device))
             flags |= B.SAF_CLEAR_REST
+            new_q, new_k = torch.empty(shape, dtype=dtype, device=self.device), None
+            if k is not None:
+                new_k = torch.empty(k_shape, dtype=dtype, device=self.device)
+            # (rows of new tensors need no checks: they are a third of the call's host part)
+            if packed:
+                oq = B.saf_rows(new_q.data_ptr(), 0, H * d, d)
+                if k is not None:
+                    ok = B.saf_rows(new_k.data_ptr(), 0, H_k * d, d)
+            else:
+                oq = B.saf_rows(new_q.data_ptr(), H * T * d, d, T * d)
+                if k is not None:
+                    ok = B.saf_rows(new_k.data_ptr(), H_k * T * d, d, T * d)
+            out = new_q, new_k
         elif (out[1] is None) != (k is None):
             raise self._bad("apply: out is not a pair like (q, k)")
-        oq = self._rows(out[0], shape, dtype, "apply: out")
-        ok = None if k is None else self._rows(out[1], k_shape, dtype, "apply: out")
+        else:
+            oq = self._rows(out[0], shape, dtype, "apply: out")
+            if k is not None:
+                ok = self._rows(out[1], k_shape, dtype, "apply: out")
         at = cu = lens = new = None
         n = 0
         if positions is not None:

@@ -77,14 +77,20 @@ struct SqTile {
   }
 };
 
-// Item `it` of the packed backward: (row0, len, J | kv << 16, tile0).
+// Item `it` of the packed backward: the place of its tile's record, and the K/V head.
 template <class Items>
-__device__ __forceinline__ int4 packed_bwd_item(const Items& p, int n_tiles, int it) {
+__device__ __forceinline__ int2 packed_bwd_place(const Items& p, int n_tiles, int it) {
   const int per = p.per_group * n_tiles, g = it / per;
   const int kvs = min(p.per_group, p.n_kv - g * p.per_group);  // the last group may be smaller
   const int w = it - g * per, rank = w / kvs;
-  int4 t = p.tiles[rank];
-  t.z |= (int)p.kv_list[g * p.per_group + (w - rank * kvs)] << 16;
+  return make_int2(rank, p.kv_list[g * p.per_group + (w - rank * kvs)]);
+}
+// The item itself: (row0, len, J | kv << 16, tile0).
+template <class Items>
+__device__ __forceinline__ int4 packed_bwd_item(const Items& p, int n_tiles, int it) {
+  const int2 at = packed_bwd_place(p, n_tiles, it);
+  int4 t = p.tiles[at.x];
+  t.z |= at.y << 16;
   return t;
 }
 

@@ -79,19 +79,6 @@ __device__ __forceinline__ unsigned long long in_units(float x, int e) {
   return u < 0x800000u || sh < -23 ? 0 : sh >= 0 ? m << sh : m >> -sh;
 }
 
-// 16 bytes global -> shared, past the L1 cache, in groups that a thread waits for.
-__device__ __forceinline__ void copy_async_16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void commit_copies() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Whether a score is one (not -inf, masked or NaN).
 __device__ __forceinline__ bool alive(float score) { return score >= kMasked && score < INFINITY; }
 

@@ -311,23 +311,36 @@ __device__ __forceinline__ int place_of(uint32_t key, const uint32_t* keys, int 
 // 8 K/V heads: 397 and 793 us against 368 and 695.  Items handed out as CTAs come free,
 // through a ring in shared memory to the five roles, cost each step 9 %.)
 __device__ void share_out(const PackedRows& p) {
+  constexpr int AHEAD = 4;  // rounds whose records are on their way
+  __shared__ __align__(16) int4 ring[AHEAD][256];
   __shared__ __align__(16) uint32_t by_load[256], by_cost[256];
   __shared__ int load_of[256], cta_at[256];
   const int tid = threadIdx.x, n_ctas = p.n_ctas, nt = p.hdr[0], n = nt * p.items.n_kv;
   const int rounds = (n + n_ctas - 1) / n_ctas;
   if (rounds > kOrderRounds) return;
-  auto record = [&](int r) {
+  // A thread's record of round r, by a copy of its own into its place of the ring (beside the row
+  // pass a load takes 1.5 us: one round ahead, 16 rounds took 33 us, longer than all rows)
+  auto issue = [&](int r) {
     const int it = r * n_ctas + tid;
-    return tid < n_ctas && it < n ? packed_bwd_item(p.items, nt, it) : make_int4(0, 0, 0, 0);
+    if (tid < n_ctas && it < n)
+      copy_async_16(&ring[r % AHEAD][tid], p.items.tiles + packed_bwd_place(p.items, nt, it).x);
+    commit_copies();
   };
   // costs in units that keep a CTA's sum below 2^24
   int shift = 0;
   while (((long long)rounds * (1 + 2 * p.items.most_steps)) >> shift >= 1 << 24) ++shift;
   load_of[tid] = 0;
   by_load[tid] = by_cost[tid] = 0xffffffffu;  // (what is behind the last CTA stays so)
-  int4 rec = record(0);
+  for (int r = 0; r < AHEAD - 1; ++r) issue(r);
   for (int r = 0; r < rounds; ++r) {
-    const int4 next = record(r + 1);
+    wait_copies<AHEAD - 2>();
+    int4 rec = make_int4(0, 0, 0, 0);
+    const int it = r * n_ctas + tid;
+    if (tid < n_ctas && it < n) {
+      rec = ring[r % AHEAD][tid];
+      rec.z |= packed_bwd_place(p.items, nt, it).y << 16;
+    }
+    issue(r + AHEAD - 1);
     const int cost = rec.y > 0 ? (1 + 2 * (int)p.items.dyn_count[rec.z >> 16] *
                                           ((rec.y + 127) / 128 - (rec.z & 0xffff))) >> shift
                                : 0;
@@ -350,9 +363,9 @@ __device__ void share_out(const PackedRows& p) {
       p.order[r * n_ctas + cta] = rec;
       load_of[cta] += cost;
     }
-    rec = next;
     __syncthreads();
   }
+  wait_copies<0>();
   if (tid < n_ctas) p.order[rounds * n_ctas + tid] = make_int4(0, 0, 0, 0);
 }
 

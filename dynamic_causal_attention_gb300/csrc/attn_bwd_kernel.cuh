@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(512, 1)
     tma_prefetch_desc(&tm_v);
     tma_prefetch_desc(&tm_do);
   }
+  if constexpr (PACKED) wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -931,10 +932,15 @@ cudaError_t launch_dyn(const Launch& L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (L.p.n_items == 0) return cudaSuccess;
   const int grid = L.p.n_items < L.num_sms ? L.p.n_items : L.num_sms;
-  trace_begin(s);
-  kern<<<grid, 512, BwdSmem<D>::ALLOC, s>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_do, L.tm_dq, L.p);
-  trace_end(s, PACKED ? "packed_bwd" : "bwd_dynamic");
-  return cudaGetLastError();
+  if constexpr (PACKED) {
+    return launch_behind(kern, grid, 512, BwdSmem<D>::ALLOC, s, "packed_bwd", L.tm_q, L.tm_k,
+                         L.tm_v, L.tm_do, L.tm_dq, L.p);
+  } else {
+    trace_begin(s);
+    kern<<<grid, 512, BwdSmem<D>::ALLOC, s>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_do, L.tm_dq, L.p);
+    trace_end(s, "bwd_dynamic");
+    return cudaGetLastError();
+  }
 }
 
 }  // namespace

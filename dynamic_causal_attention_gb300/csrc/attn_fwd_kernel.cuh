@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  if constexpr (PACKED) wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1471,11 +1472,16 @@ cudaError_t launch_fused(const Launch& L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (L.p.n_items == 0) return cudaSuccess;
   const int grid = L.p.n_items < L.num_sms ? L.p.n_items : L.num_sms;
-  trace_begin(s);
-  kern<<<grid, 384, S::ALLOC, s>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_o, L.p);
-  trace_end(s, PACKED ? (TRANSPOSED ? "packed_static_dv" : "packed_fwd")
-                      : (TRANSPOSED ? "static_dv" : "hybrid_fwd"));
-  return cudaGetLastError();
+  if constexpr (PACKED) {
+    return launch_behind(kern, grid, 384, S::ALLOC, s,
+                         TRANSPOSED ? "packed_static_dv" : "packed_fwd", L.tm_q, L.tm_k, L.tm_v,
+                         L.tm_o, L.p);
+  } else {
+    trace_begin(s);
+    kern<<<grid, 384, S::ALLOC, s>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_o, L.p);
+    trace_end(s, TRANSPOSED ? "static_dv" : "hybrid_fwd");
+    return cudaGetLastError();
+  }
 }
 
 }  // namespace

@@ -373,6 +373,7 @@ __device__ void share_out(const PackedRows& p) {
 template <int D>
 __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__ PackedRows p) {
   constexpr int LPR = D / 8;
+  wait_for_previous();
   if ((int)blockIdx.y == 0 && p.order) {
     if (blockIdx.x == 0) share_out(p);
     return;
@@ -436,6 +437,7 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_post_kernel(const __grid_constant__ PackedRows p) {
   constexpr int LPR = D / 8;
   const int h = blockIdx.y;
+  wait_for_previous();
   if ((int)blockIdx.x >= p.hdr[0] || p.static_slot[h] >= 0) return;
   const int4 t = p.tiles[blockIdx.x];
   const int valid = min(128, t.y - t.z * 128), sub = threadIdx.x % LPR;
@@ -465,28 +467,24 @@ cudaError_t launch_packed_prep(const PackedPrep& p, cudaStream_t s) {
 
 cudaError_t launch_packed_pre(const PackedRows& p, cudaStream_t s) {
   const dim3 grid(p.nt_max, p.H + (p.order ? 1 : 0));
-  trace_begin(s);
+  auto go = [&](auto kernel) { return launch_behind(kernel, grid, 256, 0, s, "packed_pre", p); };
   switch (p.d_h) {
-    case 32: packed_pre_kernel<32><<<grid, 256, 0, s>>>(p); break;
-    case 64: packed_pre_kernel<64><<<grid, 256, 0, s>>>(p); break;
-    case 128: packed_pre_kernel<128><<<grid, 256, 0, s>>>(p); break;
+    case 32: return go(packed_pre_kernel<32>);
+    case 64: return go(packed_pre_kernel<64>);
+    case 128: return go(packed_pre_kernel<128>);
     default: return cudaErrorInvalidValue;
   }
-  trace_end(s, "packed_pre");
-  return cudaGetLastError();
 }
 
 cudaError_t launch_packed_post(const PackedRows& p, cudaStream_t s) {
   const dim3 grid(p.nt_max, p.H);
-  trace_begin(s);
+  auto go = [&](auto kernel) { return launch_behind(kernel, grid, 256, 0, s, "packed_post", p); };
   switch (p.d_h) {
-    case 32: packed_post_kernel<32><<<grid, 256, 0, s>>>(p); break;
-    case 64: packed_post_kernel<64><<<grid, 256, 0, s>>>(p); break;
-    case 128: packed_post_kernel<128><<<grid, 256, 0, s>>>(p); break;
+    case 32: return go(packed_post_kernel<32>);
+    case 64: return go(packed_post_kernel<64>);
+    case 128: return go(packed_post_kernel<128>);
     default: return cudaErrorInvalidValue;
   }
-  trace_end(s, "packed_post");
-  return cudaGetLastError();
 }
 
 }  // namespace saf

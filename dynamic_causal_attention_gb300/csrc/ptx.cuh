@@ -139,6 +139,12 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// A kernel launched behind another one of its call (launch_behind) waits for that one's end and
+// for what it wrote before it touches memory; every thread of every block.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // 16 bytes global -> shared, past the L1 cache, in groups that a thread waits for.
 __device__ __forceinline__ void copy_async_16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)

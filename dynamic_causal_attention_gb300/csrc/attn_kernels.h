@@ -46,30 +46,6 @@ inline int static_group(int d_h, int B, bool transposed = false) {
   return g < B ? g : B;
 }
 
-// A launch behind another kernel of the same call, set up before that one has ended (it
-// waits: wait_for_previous).  The gaps between the launches of a training step on 16 documents
-// go from 15 us to 3 (672 -> 656 us).  Allowed to start as early as there is room,
-// the kernels get in one another's way: 685 us where the backward's CTAs take the SMs in the order
-// in which the frozen heads' dV leaves them, 662 where only the two small kernels allow it.
-template <class... P, class... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
-                          cudaStream_t s, const char* name, const A&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  trace_begin(s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  trace_end(s, name);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // The same for sequences laid end to end: T is the length of the tables, and items
 // come from a plan that the preparing kernel makes on the device.
 struct PackedFwdParams : FwdParams {

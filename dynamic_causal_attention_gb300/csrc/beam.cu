@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = blockIdx.x / p.splits, split = blockIdx.x - slot * p.splits;
   const int K = p.beams;
+  wait_for_previous();
   if (offers(p, slot)) {
     const T* row = static_cast<const T*>(p.logits) + (size_t)slot * (size_t)p.row_stride;
     // elements ahead of the first 16-byte boundary, whole vectors, elements behind them
@@ -689,10 +690,7 @@ cudaError_t launch_beam(const BeamParams& p, bool f32, int held, cudaStream_t s)
           set_max_dynamic_smem(reinterpret_cast<const void*>(kern), 200 * 1024);
       if (e != cudaSuccess) return e;
     }
-    trace_begin(s);
-    kern<<<grid, kThreads, smem, s>>>(p);
-    trace_end(s, "beam");
-    return cudaGetLastError();
+    return launch_first(kern, grid, kThreads, smem, s, "beam", p);
   };
   if (f32) return held == 16 ? go(beam_kernel<float, 4>) : go(beam_kernel<float, 2>);
   return held == 16 ? go(beam_kernel<__nv_bfloat16, 2>) : go(beam_kernel<__nv_bfloat16, 1>);

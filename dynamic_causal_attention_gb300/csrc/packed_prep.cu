@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   __shared__ PlanShared plan;
   const int chunks = p.max_tiles;
   const int b = (int)blockIdx.x - 1;
+  wait_for_previous();
   if (b < 0) make_plan(p, plan);
   else if (b < chunks * p.n_static)
     make_tables(p, b / chunks, (b % chunks) * 128, reinterpret_cast<float*>(plan.hist));
@@ -459,10 +460,7 @@ __global__ void __launch_bounds__(256) packed_post_kernel(const __grid_constant_
 
 cudaError_t launch_packed_prep(const PackedPrep& p, cudaStream_t s) {
   const int grid = 1 + p.max_tiles * p.n_static + (p.clear ? kClearBlocks : 0);
-  trace_begin(s);
-  packed_prep_kernel<<<grid, kPrepThreads, 0, s>>>(p);
-  trace_end(s, "packed_prep");
-  return cudaGetLastError();
+  return launch_first(packed_prep_kernel, grid, kPrepThreads, 0, s, "packed_prep", p);
 }
 
 cudaError_t launch_packed_pre(const PackedRows& p, cudaStream_t s) {

@@ -14,8 +14,8 @@
 // their cosines and sines once in registers and goes through the heads of Q and K with
 // them, three heads' loads in flight; no shared memory, no barrier.  With few tokens the
 // heads are shared out over several threads, which then form the same sines.
-// Measured: Q and K (bf16, parts of one projection) of 33.4k tokens, 12 + 12 heads of 64, 38 us,
-// 5.3 TB/s or 80 % of the copy rate; fp32, 2 x 8190 tokens, 16 + 4 heads of 128, 58 us, 86 %;
+// Measured: Q and K (bf16, parts of one projection) of 33.4k tokens, 12 + 12 heads of 64, 37 us,
+// 5.5 TB/s or 83 % of the copy rate; fp32, 2 x 8190 tokens, 16 + 4 heads of 128, 57 us, 87 %;
 // one token of 64 sequences 6 us (launch, position, sine, row: one latency after another).
 // With the sines of 16 tokens in shared memory and a barrier the first took 48 us.
 #include <cuda_bf16.h>
@@ -23,11 +23,12 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace saf {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;  // (256: the last blocks leave more SMs idle, 38.8 us for 37.7)
 constexpr int kUnroll = 3;  // heads in flight
 
 template <int BYTES>
@@ -151,9 +152,10 @@ __device__ __forceinline__ void heads(const RotaryRows& in, const RotaryRows& ou
 }
 
 template <typename T, int W, bool HALF>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 16)
     rotary_kernel(const __grid_constant__ RotaryParams p) {
   const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
+  wait_for_previous();
   const uint32_t r = fast_div(i, p.by_units), u = i - r * (uint32_t)p.units;
   const uint32_t n = fast_div(r, p.by_split);           // the row of B * T
   const int g = (int)(r - n * (uint32_t)p.split);       // the first of its heads
@@ -211,13 +213,9 @@ FastDiv make_div(uint32_t d) {
 template <typename T>
 cudaError_t launch(const RotaryParams& p, int W, bool half, unsigned grid, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
-  trace_begin(s);
-  if (W == V && half) rotary_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p);
-  else if (W == V) rotary_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p);
-  else if (half) rotary_kernel<T, 1, true><<<grid, kThreads, 0, s>>>(p);
-  else rotary_kernel<T, 1, false><<<grid, kThreads, 0, s>>>(p);
-  trace_end(s, "rotary");
-  return cudaGetLastError();
+  auto go = [&](auto kernel) { return launch_first(kernel, grid, kThreads, 0, s, "rotary", p); };
+  if (W == V) return half ? go(rotary_kernel<T, V, true>) : go(rotary_kernel<T, V, false>);
+  return half ? go(rotary_kernel<T, 1, true>) : go(rotary_kernel<T, 1, false>);
 }
 
 }  // namespace
@@ -236,9 +234,9 @@ cudaError_t launch_rotary(RotaryParams& p, bool f32, bool interleaved, int n_sms
   const int W = wide ? V : 1;
   p.pair_units = half / W;
   p.units = p.pair_units + (p.copy_rest ? ((p.d - p.rot) / W + 1) / 2 : 0);
-  // Threads of a token's unit: one, as long as that fills every SM twice (768 threads
+  // Threads of a token's unit: one, as long as that fills every SM four times (768 threads
   // each); up to one for each head where there are few tokens.
-  const long long n = (long long)p.B * p.T, want = 2ll * 768 * n_sms;
+  const long long n = (long long)p.B * p.T, want = 4ll * 768 * n_sms;
   const long long fits = ((1ll << 31) - kThreads) / (n * p.units);
   long long split = (want + n * p.units - 1) / (n * p.units);
   if (split > p.H + p.H_k) split = p.H + p.H_k;

@@ -113,3 +113,59 @@ def test_prompts_to_beams(api):
         # (frozen heads see K in neither: only V is rounded there)
         assert cache.device_status() == (0, 0) and packed.device_status() == (0, 0)
         logits = (got[:, :, 0].float().flatten(1) @ head).contiguous()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_wait_for_what_writes_their_inputs(api, captured):
+    """Inputs written by a long kernel just before the call, and right behind it overwritten: the
+    same bits as with synchronised ones (in a graph behind a join of two streams too)."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    draw = lambda *s: torch.randn(s, device="cuda", generator=gen)
+    total, H, d, cu = 700, 4, 64, torch.tensor([0, 300, 700], dtype=torch.int32, device="cuda")
+    src = draw(total, 3 * H, d).bfloat16()
+    alpha, rho = draw(H, 400), draw(H, 400)
+    logits = draw(8, 50000)
+    scores = torch.zeros(8, device="cuda")
+    turn = api.Rotary(d)
+    layer = api.PackedAttention(H, d, [0, 1, 0, 0], max_total=total, max_seqs=2, max_len=400)
+    search = api.BeamSearch(2, 4, 50000)
+    big = draw(4096, 4096)
+    x, y = torch.zeros_like(src), torch.zeros_like(logits)
+
+    def fill(slow):
+        # 4096^3 products ahead of the copy keep the calls' predecessors running
+        z = (big @ big @ big)[:1, :1] * 0 if slow else torch.zeros(1, 1, device="cuda")
+        x.copy_(src + z.nan_to_num(0.0).bfloat16())
+        y.copy_(logits + z.nan_to_num(0.0))
+
+    def calls(slow, behind=None):
+        res = []
+        for call in (lambda: turn.apply(x[:, :H], x[:, H:2 * H], cu_seqlens=cu),
+                     lambda: layer.forward(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], cu, alpha, rho),
+                     lambda: search.step(y, scores)[:3]):
+            fill(slow)
+            if behind is not None:
+                behind.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(behind):
+                    y.add_(0.0)
+                torch.cuda.current_stream().wait_stream(behind)
+            res += call()
+            x.fill_(9.0)
+            y.fill_(9.0)
+        return res
+    want = calls(False)
+    torch.cuda.synchronize()
+    if not captured:
+        got = calls(True)
+    else:
+        other = torch.cuda.Stream()
+        calls(True, other)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = calls(True, other)
+        for _ in range(2):
+            graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)

@@ -418,6 +418,12 @@ class _OnDevice:
             return B.saf_rows(t.data_ptr(), 0, st[0], st[1])
         return B.saf_rows(t.data_ptr(), st[0], st[2], st[1])
 
+    def _fresh(self, shape):
+        """New bf16 rows [total, heads, d] and their saf_rows (which need no checks: those of three
+        tensors take 2 us of a call)."""
+        t = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        return t, B.saf_rows(t.data_ptr(), 0, shape[1] * shape[2], shape[2])
+
     def _call(self, entry, *args):
         """The C entry on this object's device and its current stream."""
         if torch.cuda.current_device() == self._index:
@@ -634,18 +640,21 @@ class PackedAttention(_OnDevice):
         if out is None and lse is None:
             # both are new: the call itself clears what it does not work on
             flags = B.SAF_CLEAR_REST
-            out = torch.empty(wide, dtype=bf16, device=self.device)
+            out, po = self._fresh(wide)
             lse = torch.empty((self.H, total), dtype=torch.float32, device=self.device)
-        elif out is None:
-            out = torch.zeros(wide, dtype=bf16, device=self.device)
-        elif lse is None:
-            lse = torch.full((self.H, total), -math.inf, device=self.device)
+            pl = lse.data_ptr()
+        else:
+            if out is None:
+                out = torch.zeros(wide, dtype=bf16, device=self.device)
+            if lse is None:
+                lse = torch.full((self.H, total), -math.inf, device=self.device)
+            po = self._rows(out, wide, bf16, "forward: out")
+            pl = self._need(lse, (self.H, total), torch.float32, "forward: lse")
         rows = self._rows
         self._call(B.saf_packed_attn_fwd, dims, rows(q, wide, bf16, "forward: q"),
                    rows(k, narrow, bf16, "forward: k"), rows(v, narrow, bf16, "forward: v"), cu,
-                   pa, pr, self.head_is_static, rows(out, wide, bf16, "forward: out"),
-                   self._need(lse, (self.H, total), torch.float32, "forward: lse"), flags,
-                   self.workspace.data_ptr(), self.ws_bytes)
+                   pa, pr, self.head_is_static, po, pl, flags, self.workspace.data_ptr(),
+                   self.ws_bytes)
         return out, lse
 
     def backward(self, q, k, v, out, lse, dout, cu_seqlens, alpha=None, rho=None, grads=None):
@@ -656,22 +665,21 @@ class PackedAttention(_OnDevice):
         dims, cu, pa, pr = self._common(q, cu_seqlens, alpha, rho)
         total, bf16 = dims.total, torch.bfloat16
         wide, narrow = (total, self.H, self.d_h), (total, self.H_kv, self.d_h)
-        flags = 0
+        rows, flags = self._rows, 0
         if grads is None:
             flags = B.SAF_CLEAR_REST
-            grads = (torch.empty(wide, dtype=bf16, device=self.device),
-                     torch.empty(narrow, dtype=bf16, device=self.device),
-                     torch.empty(narrow, dtype=bf16, device=self.device))
-        dq, dk, dv = grads
-        rows = self._rows
+            (dq, pq), (dk, pk), (dv, pv) = self._fresh(wide), self._fresh(narrow), self._fresh(narrow)
+        else:
+            dq, dk, dv = grads
+            pq = rows(dq, wide, bf16, "backward: dq")
+            pk = rows(dk, narrow, bf16, "backward: dk")
+            pv = rows(dv, narrow, bf16, "backward: dv")
         self._call(B.saf_packed_attn_bwd, dims, rows(q, wide, bf16, "backward: q"),
                    rows(k, narrow, bf16, "backward: k"), rows(v, narrow, bf16, "backward: v"),
                    rows(out, wide, bf16, "backward: out"),
                    self._need(lse, (self.H, total), torch.float32, "backward: lse"),
                    rows(dout, wide, bf16, "backward: dout"), cu, pa, pr, self.head_is_static,
-                   rows(dq, wide, bf16, "backward: dq"), rows(dk, narrow, bf16, "backward: dk"),
-                   rows(dv, narrow, bf16, "backward: dv"), flags, self.workspace.data_ptr(),
-                   self.ws_bytes)
+                   pq, pk, pv, flags, self.workspace.data_ptr(), self.ws_bytes)
         return dq, dk, dv
 
     def device_status(self):

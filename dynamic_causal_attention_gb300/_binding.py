@@ -381,10 +381,6 @@ def saf_cache_compact(dims, pool, page_bytes, page_table, ref, page_table_out, r
                                   page_table_out, ref_out, n_used, workspace, ws_bytes, stream)
 
 
-def _ref(struct):
-    return None if struct is None else ctypes.byref(struct)
-
-
 def saf_rotary_turns(radians):
     """(status, turns): a host sequence of radians a token, as saf_rotary takes it (a list of
     whole numbers below 2^64)."""
@@ -394,10 +390,11 @@ def saf_rotary_turns(radians):
     return st, list(dst)
 
 
+# (structs are passed as they are: ctypes makes the pointer, at half of byref's price)
 def saf_rotary(dims, q, k, q_out, k_out, turns, scale, positions, cu_seqlens, n_seqs, seq_len,
                n_new, flags, stream) -> int:
-    return _lib.saf_rotary(_ref(dims), _ref(q), _ref(k), _ref(q_out), _ref(k_out), turns, scale,
-                           positions, cu_seqlens, n_seqs, seq_len, n_new, flags, stream)
+    return _lib.saf_rotary(dims, q, k, q_out, k_out, turns, scale, positions, cu_seqlens, n_seqs,
+                           seq_len, n_new, flags, stream)
 
 
 def saf_packed_attn_workspace_size(dims, backward) -> int:
@@ -406,17 +403,15 @@ def saf_packed_attn_workspace_size(dims, backward) -> int:
 
 def saf_packed_attn_fwd(dims, Q, K, V, cu_seqlens, alpha, rho, head_is_static: bytes, out, lse,
                         flags, workspace, ws_bytes, stream) -> int:
-    return _lib.saf_packed_attn_fwd(_ref(dims), _ref(Q), _ref(K), _ref(V), cu_seqlens, alpha, rho,
-                                    head_is_static, _ref(out), lse, flags, workspace, ws_bytes,
-                                    stream)
+    return _lib.saf_packed_attn_fwd(dims, Q, K, V, cu_seqlens, alpha, rho, head_is_static, out,
+                                    lse, flags, workspace, ws_bytes, stream)
 
 
 def saf_packed_attn_bwd(dims, Q, K, V, out, lse, dout, cu_seqlens, alpha, rho,
                         head_is_static: bytes, dQ, dK, dV, flags, workspace, ws_bytes,
                         stream) -> int:
-    return _lib.saf_packed_attn_bwd(_ref(dims), _ref(Q), _ref(K), _ref(V), _ref(out), lse, _ref(dout),
-                                    cu_seqlens, alpha, rho, head_is_static, _ref(dQ), _ref(dK),
-                                    _ref(dV), flags, workspace, ws_bytes, stream)
+    return _lib.saf_packed_attn_bwd(dims, Q, K, V, out, lse, dout, cu_seqlens, alpha, rho,
+                                    head_is_static, dQ, dK, dV, flags, workspace, ws_bytes, stream)
 
 
 def saf_beam_workspace_size(dims) -> int:
@@ -425,6 +420,6 @@ def saf_beam_workspace_size(dims) -> int:
 
 def saf_beam_step(dims, logits, scores, finished, history, n_tokens, parent, token, score_out,
                   finished_out, history_out, workspace, ws_bytes, stream) -> int:
-    return _lib.saf_beam_step(ctypes.byref(dims), logits, scores, finished, history, n_tokens,
+    return _lib.saf_beam_step(dims, logits, scores, finished, history, n_tokens,
                               parent, token, score_out, finished_out, history_out, workspace,
                               ws_bytes, stream)

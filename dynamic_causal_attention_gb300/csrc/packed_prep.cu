@@ -11,7 +11,8 @@
 //                Neighbours in the first order share X and a frozen head's weights.
 //   then         the frozen heads' generator tables, 128 entries a block
 //   the last     rows of no sequence, cleared where asked
-// 7 us for 16 sequences: a chain of scans by one block, beside tables of 4096 entries.
+// 7 us for 16 sequences with its launch: of that a chain of scans by one block 3, beside tables of
+// 4096 entries (2).
 // packed_pre / packed_post: the backward's row passes (D = rowsum(dO o O), -lse log2 e,
 // zeros of dQ's accumulator; dQ from it), by tiles and heads.
 #include <cuda_bf16.h>

@@ -118,7 +118,7 @@ def test_prompts_to_beams(api):
 @pytest.mark.parametrize("captured", [False, True])
 def test_calls_wait_for_what_writes_their_inputs(api, captured):
     """Inputs written by a long kernel just before the call, and right behind it overwritten: the
-    same bits as with synchronised ones (in a graph behind a join of two streams too)."""
+    same bits as with synchronised ones (behind a join of two streams too, and that in a graph)."""
     gen = torch.Generator(device="cuda").manual_seed(3)
     draw = lambda *s: torch.randn(s, device="cuda", generator=gen)
     total, H, d, cu = 700, 4, 64, torch.tensor([0, 300, 700], dtype=torch.int32, device="cuda")
@@ -155,10 +155,11 @@ def test_calls_wait_for_what_writes_their_inputs(api, captured):
         return res
     want = calls(False)
     torch.cuda.synchronize()
+    other = torch.cuda.Stream()
     if not captured:
         got = calls(True)
+        want, got = want + want, got + calls(True, other)
     else:
-        other = torch.cuda.Stream()
         calls(True, other)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()

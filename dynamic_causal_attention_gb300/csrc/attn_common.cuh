@@ -94,75 +94,6 @@ __device__ __forceinline__ int4 packed_bwd_item(const Items& p, int n_tiles, int
   return t;
 }
 
-// Items of a plan made on the device, handed out as CTAs come free: one thread of a CTA
-// (the first producer) takes the next number and passes it on to the other roles
-// through a ring in shared memory.  Sequences of different lengths make items of
-// very different cost: the forward of 4 prompts of up to 8192 tokens (16 heads of 128) took
-// 444 us by the snake order below, 427 this way.
-constexpr int kItemSlots = 4;
-struct ItemRing {
-  uint64_t *full, *empty;  // [kItemSlots]; empty counts the taking roles
-  volatile int* item;      // [kItemSlots]
-};
-
-// A CTA's first item is its own number; with no more items than CTAs that is all, and
-// the ring is not used.
-//
-// The handing thread.  The counter is zero before the launch.  claim() is called as the
-// item's last loads go out: the number is there when the item ends, and no CTA holds one
-// while it still has much to do (claimed as an item began, the order was as bad as
-// a fixed one).
-struct ItemFeed {
-  uint32_t n = 0;  // items handed out after the first
-  bool begun = false;
-  int ahead = 0;
-  __device__ __forceinline__ void claim(int* counter, int n_items) {
-    if (n_items > (int)gridDim.x) ahead = atomicAdd(counter, 1);
-  }
-  __device__ __forceinline__ int next(const ItemRing& r, int n_items, const WaitCtl& wc,
-                                      int site) {
-    if (!begun) {
-      begun = true;
-      return min((int)blockIdx.x, n_items);
-    }
-    if (n_items <= (int)gridDim.x) return n_items;
-    int it = (int)gridDim.x + ahead;
-    const uint32_t s = n % kItemSlots;
-    if (!mbar_wait(r.empty + s, ((n / kItemSlots) & 1) ^ 1, wc, site) || it > n_items) it = n_items;
-    r.item[s] = it;
-    mbar_arrive(r.full + s);
-    ++n;
-    return it;
-  }
-};
-
-// A role that takes them: a whole warp, or (ALONE) one lane of it.
-template <bool ALONE>
-struct ItemTake {
-  uint32_t n = 0;
-  bool begun = false;
-  __device__ __forceinline__ int next(const ItemRing& r, int n_items, const WaitCtl& wc,
-                                      int site) {
-    if (!begun) {
-      begun = true;
-      return min((int)blockIdx.x, n_items);
-    }
-    if (n_items <= (int)gridDim.x) return n_items;
-    const uint32_t s = n % kItemSlots;
-    int it = n_items;
-    if (mbar_wait(r.full + s, (n / kItemSlots) & 1, wc, site)) it = r.item[s];
-    ++n;
-    if (ALONE) {
-      mbar_arrive(r.empty + s);
-    } else {
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(r.empty + s);
-    }
-    // (from one lane: the warp agrees on the item, and the compiler knows it)
-    return __shfl_sync(ALONE ? 1u : 0xffffffffu, it, 0);
-  }
-};
-
 // Item of round k for CTA `cta` of a persistent grid of `grid` CTAs: even
 // rounds run forwards, odd rounds backwards, so that with items sorted
 // longest first the CTA that drew one of the longest items in one round

@@ -22,6 +22,9 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kItemSlots = 4;  // of the ring that hands out packed items
+constexpr int kClaim = 3;      // loads ahead of an item's end that the next is claimed
+
 template <int D>
 struct FwdSmem {
   using G = TileGeom<D>;
@@ -60,8 +63,8 @@ struct FwdSmem {
       2 * QST + 2 * KST + 2 * VST + 3 * NBUF + 2 + 2 + 2 * AST + 2 + 1 +
       2 * kItemSlots;  // NBUF >= NBUF_T
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_ITEM = OFF_MISC + 16;
-  static constexpr int BYTES = OFF_ITEM + 4 * kItemSlots;
+  static constexpr int OFF_ITEM = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int BYTES = OFF_ITEM + 32 * kItemSlots;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 B
   static_assert(ALLOC <= 232448, "shared memory budget exceeded");
   // a table slot (static items): 128 column values then a 256-entry distance
@@ -231,6 +234,111 @@ __device__ __forceinline__ Item decode_item(const PackedFwdParams& p, int it) {
   return r;
 }
 
+// Items of a plan made on the device, handed out as CTAs come free: one thread of a CTA
+// (the first producer) takes the next number, reads the item's records and passes it on to the
+// other roles through a ring in shared memory.  Sequences of different lengths make items of
+// very different cost: the forward of 4 prompts of up to 8192 tokens (16 heads of 128) took
+// 444 us by the snake order, 427 this way; and with every role reading the records itself RINGOLD.
+struct ItemRing {
+  uint64_t *full, *empty;  // [kItemSlots]; empty counts the taking roles
+  uint32_t rec;            // shared address of two int4 for each slot
+};
+
+// A CTA's first item is its own number; with no more items than CTAs that is all, and
+// the ring is not used.
+//
+// The handing thread.  The counter is zero before the launch.  claim() is called a few loads ahead
+// of the item's last: the number is there when the item ends, and no CTA holds one
+// while it still has much to do (claimed as an item began, the order was as bad as
+// a fixed one).
+template <bool TRANSPOSED>
+struct ItemFeed {
+  uint32_t n = 0;  // items handed out after the first
+  bool begun = false;
+  int ahead = 0;
+  __device__ __forceinline__ void claim(int* counter, int n_items) {
+    if (n_items > (int)gridDim.x) ahead = atomicAdd(counter, 1);
+  }
+  // The next item, n_items behind the last.
+  __device__ __forceinline__ int next(const ItemRing& r, const PackedFwdParams& p, int n_items,
+                                      Item& w, const WaitCtl& wc, int site) {
+    int it;
+    if (!begun) {
+      begun = true;
+      it = min((int)blockIdx.x, n_items);
+      if (it < n_items) w = decode_item<TRANSPOSED>(p, it);
+      return it;
+    }
+    if (n_items <= (int)gridDim.x) return n_items;
+    it = min((int)gridDim.x + ahead, n_items);
+    if (it < n_items) w = decode_item<TRANSPOSED>(p, it);
+    const uint32_t s = n % kItemSlots;
+    if (!mbar_wait(r.empty + s, ((n / kItemSlots) & 1) ^ 1, wc, site)) it = n_items;
+    const uint32_t to = r.rec + 32 * s;
+    st_shared_v4(to, (uint32_t)w.row0, (uint32_t)w.len,
+                 (uint32_t)(w.X | w.nb << 16 | (int)w.is_static << 24),
+                 (uint32_t)(w.h | (w.hs & 0xffff) << 16));
+    st_shared_v4(to + 16, (uint32_t)it, (uint32_t)w.rank,
+                 TRANSPOSED ? (uint32_t)(w.more[0] | w.more[1] << 16) : 0u,
+                 TRANSPOSED ? (uint32_t)w.more[2] : 0u);
+    mbar_arrive(r.full + s);
+    ++n;
+    return it;
+  }
+};
+
+// A role that takes them: a whole warp, or (ALONE) one lane of it.
+template <bool TRANSPOSED, bool ALONE>
+struct ItemTake {
+  uint32_t n = 0;
+  bool begun = false;
+  __device__ __forceinline__ int next(const ItemRing& r, const PackedFwdParams& p, int n_items,
+                                      Item& w, const WaitCtl& wc, int site) {
+    if (!begun) {
+      begun = true;
+      const int it = min((int)blockIdx.x, n_items);
+      if (it < n_items) w = decode_item<TRANSPOSED>(p, it);
+      return it;
+    }
+    if (n_items <= (int)gridDim.x) return n_items;
+    const uint32_t s = n % kItemSlots, from = r.rec + 32 * s;
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = make_uint4((uint32_t)n_items, 0u, 0u, 0u);
+    if (mbar_wait(r.full + s, (n / kItemSlots) & 1, wc, site)) {
+      a = lds_u32x4(from);
+      b = lds_u32x4(from + 16);
+    }
+    ++n;
+    if (ALONE) {
+      mbar_arrive(r.empty + s);
+    } else {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(r.empty + s);
+    }
+    // (from one lane: the warp agrees on the item, and the compiler knows it)
+    auto one = [](uint32_t x) { return (int)__shfl_sync(ALONE ? 1u : 0xffffffffu, x, 0); };
+    w.row0 = one(a.x);
+    w.len = one(a.y);
+    const int kind = one(a.z), head = one(a.w);
+    w.X = kind & 0xffff;
+    w.nb = (kind >> 16) & 0xff;
+    w.is_static = TRANSPOSED || (kind >> 24) != 0;
+    w.h = head & 0xffff;
+    w.hs = head >> 16;
+    w.rank = one(b.y);
+    if (TRANSPOSED) {
+      const int more = one(b.z);
+      w.more[0] = more & 0xffff;
+      w.more[1] = more >> 16;
+      w.more[2] = one(b.w);
+      w.span = (w.len + 127) / 128 - w.X;
+      w.nsteps = p.st_count[w.h] * w.span;
+    } else {
+      w.nsteps = w.X + 1;
+    }
+    return one(b.x);
+  }
+};
+
 // Sequences of a transposed item's group that have query tile I (the longest ones).
 __device__ __forceinline__ int with_tile(const Item& w, int I) {
   return 1 + (w.more[0] > I) + (w.more[1] > I) + (w.more[2] > I);
@@ -332,7 +440,7 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* mma_drained = aux_empty + L::AST;
   uint64_t* tail_full = mma_drained + 2;    // PACKED: a V tile that ends a sequence landed
   const ItemRing ring{tail_full + 1, tail_full + 1 + kItemSlots,
-                      reinterpret_cast<volatile int*>(smem + L::OFF_ITEM)};
+                      smem_u32(smem + L::OFF_ITEM)};
   float* xmax = reinterpret_cast<float*>(smem + L::OFF_X);  // [2 parity][2 halves][128]
   float* xsum = xmax + 2 * 2 * 128;                         // [2 halves][128]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -392,20 +500,25 @@ __global__ void __launch_bounds__(384, 1)
 
   // The next item of this role: by the snake order, or (packed) as they are handed out.
   int round = 0;
-  ItemFeed items_fed;
-  ItemTake<true> lane_items;
-  ItemTake<false> warp_items;
+  ItemFeed<TRANSPOSED> items_fed;
+  ItemTake<TRANSPOSED, true> lane_items;
+  ItemTake<TRANSPOSED, false> warp_items;
+  Item handed;
   auto feed = [&] {
-    if constexpr (PACKED) return items_fed.next(ring, n_items, wc, kSiteItem);
+    if constexpr (PACKED) return items_fed.next(ring, p, n_items, handed, wc, kSiteItem);
     else return 0;
   };
   auto take_lane = [&] {
-    if constexpr (PACKED) return lane_items.next(ring, n_items, wc, kSiteItem);
+    if constexpr (PACKED) return lane_items.next(ring, p, n_items, handed, wc, kSiteItem);
     else return snake_item(round++, blockIdx.x, gridDim.x);
   };
   auto take_warp = [&] {
-    if constexpr (PACKED) return warp_items.next(ring, n_items, wc, kSiteItem);
+    if constexpr (PACKED) return warp_items.next(ring, p, n_items, handed, wc, kSiteItem);
     else return snake_item(round++, blockIdx.x, gridDim.x);
+  };
+  auto item = [&](int it) {
+    if constexpr (PACKED) return handed;
+    else return decode_item<TRANSPOSED>(p, it);
   };
 
   if (PACKED && warp == 0) {
@@ -414,7 +527,7 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) {
         uint32_t qc = 0, kc = 0, ac = 0, kn0 = 0, kn1 = 0;
         for (int it = feed(); it < n_items; it = feed()) {
-          const Item w = decode_item<TRANSPOSED>(p, it);
+          const Item w = item(it);
           if (!w.is_static) {
             const int qs = qc % L::QST;
             mbar_wait(q_empty + qs, ((qc / L::QST) & 1) ^ 1, wc, kSiteProdQ);
@@ -435,7 +548,7 @@ __global__ void __launch_bounds__(384, 1)
                 kpar = ((kc / L::KST) & 1) ^ 1;
                 ++kc;
               }
-              if (j == w.nsteps - 1) items_fed.claim(p.counter, n_items);
+              if (j == max(w.nsteps - kClaim, 0)) items_fed.claim(p.counter, n_items);
               mbar_wait(k_empty + ks, kpar, wc, kSiteProdK);
               mbar_arrive_expect_tx(k_full + ks, G::TILE_BYTES);
               for (int c = 0; c < G::NCHUNK; ++c)
@@ -445,7 +558,7 @@ __global__ void __launch_bounds__(384, 1)
           } else {
             for (int step = 0; step < w.nsteps; ++step) {
               const int as = ac % L::AST;
-              if (step == w.nsteps - 1) items_fed.claim(p.counter, n_items);
+              if (step == max(w.nsteps - kClaim, 0)) items_fed.claim(p.counter, n_items);
               mbar_wait(aux_empty + as, ((ac / L::AST) & 1) ^ 1, wc, kSiteProdK);
               ++ac;
               mbar_arrive_expect_tx(aux_full + as, L::AUX_BYTES);
@@ -525,7 +638,7 @@ __global__ void __launch_bounds__(384, 1)
         ++vc;
       };
       for (int it = take_warp(); it < n_items; it = take_warp()) {
-        const Item w = decode_item<TRANSPOSED>(p, it);
+        const Item w = item(it);
         for (int step = 0; step < w.nsteps; ++step) {
           if (TRANSPOSED) {
             const int q = step / w.span, I = w.X + (step - q * w.span);
@@ -566,7 +679,7 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t kn0 = 0, kn1 = 0;  // SPLIT: uses of each issuer's K ring
         bool held_q = false;        // the first Q tile was withheld (testing)
         for (int it = take_lane(); it < n_items; it = take_lane()) {
-          const Item w = decode_item<TRANSPOSED>(p, it);
+          const Item w = item(it);
           if (!w.is_static) {
             const int row0 = (w.b * H + w.h) * T;                           // Q rows
             const int kv0 = (w.b * p.H_kv + w.h / p.group_kv) * T;          // K/V rows
@@ -700,7 +813,7 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t qc = 0, vc = 0, sc = 0, oc = 0;
       uint32_t kn = 0, sn = 0;  // uses of this issuer's K ring and of S buffer g
       for (int it = take_lane(); it < n_items; it = take_lane()) {
-        const Item w = decode_item<TRANSPOSED>(p, it);
+        const Item w = item(it);
         // before the first product into O: the previous item's O has been
         // read out (an issuer without products waits too, so that its
         // o_full arrival falls into this item's phase)
@@ -828,7 +941,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
       uint32_t qc = 0, kc = 0, sc = 0;
       for (int it = take_lane(); it < n_items; it = take_lane()) {
-        const Item w = decode_item<TRANSPOSED>(p, it);
+        const Item w = item(it);
         const uint32_t sc0 = sc;
         if (!w.is_static) {
           const int qs = qc % L::QST;
@@ -874,7 +987,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_pair = idesc_bf16(128, 2 * D, false, true);
       uint32_t vc = 0, sc = 0, oc = 0;
       for (int it = take_lane(); it < n_items; it = take_lane()) {
-        const Item w = decode_item<TRANSPOSED>(p, it);
+        const Item w = item(it);
         const uint32_t sc0 = sc;
         if (!w.is_static) {
           for (int j = 0; j < w.nsteps; ++j) {
@@ -963,7 +1076,7 @@ __global__ void __launch_bounds__(384, 1)
     uint32_t ac = 0, sc = 0, oc = 0;  // static tables, P ring uses (all steps), items
     uint32_t sn = 0;  // SPLIT: this half's dynamic tiles (uses of S buffer hf)
     for (int it = take_warp(); it < n_items; it = take_warp()) {
-      const Item w = decode_item<TRANSPOSED>(p, it);
+      const Item w = item(it);
       const uint32_t sc0 = sc;
       if (!w.is_static && SPLIT) {
         // this half's key tiles: j = hf, hf + 2, ...; a thread holds a whole

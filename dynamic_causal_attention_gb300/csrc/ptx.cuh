@@ -411,6 +411,13 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
                : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint4 lds_u32x4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t pack_bf16x2_f2(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);

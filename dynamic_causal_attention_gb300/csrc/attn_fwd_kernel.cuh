@@ -23,7 +23,7 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kItemSlots = 4;  // of the ring that hands out packed items
-constexpr int kClaim = 3;      // loads ahead of an item's end that the next is claimed
+constexpr int kClaim = 2;      // loads ahead of an item's end that the next is claimed
 
 template <int D>
 struct FwdSmem {

@@ -127,7 +127,7 @@ __device__ __forceinline__ BItem decode_bwd(const BwdParams& p, int it) {
 __device__ __forceinline__ BItem decode_bwd(const PackedBwdParams& p, int it) {
   BItem r;
   const int4 t = p.hdr[0] * p.n_kv <= kOrderRounds * (int)gridDim.x
-                     ? __ldg(p.order + it)
+                     ? p.order[it]
                      : packed_bwd_item(p.items, p.hdr[0], it);
   r.b = 0;
   r.kv = t.z >> 16;
@@ -150,7 +150,7 @@ __device__ __forceinline__ int bwd_item(const PackedBwdParams& p, int k, int n_i
     return snake_item(k, blockIdx.x, gridDim.x);
   // (the list ends with a round of empty entries)
   const int it = k * (int)gridDim.x + (int)blockIdx.x;
-  return __ldg(&p.order[it].y) > 0 ? it : n_items;
+  return p.order[it].y > 0 ? it : n_items;
 }
 
 template <bool PACKED>

@@ -216,7 +216,7 @@ __device__ void join_rows(const BeamParams& p, int slot0, int R, const Joined& j
 // Chooses a group's new slots from its rows' best; every thread of the block.
 __device__ void choose(const BeamParams& p, int group, const Joined& j) {
   const int K = p.beams, tid = threadIdx.x, slot0 = group * K;
-  const int filled = p.history_out ? max(0, min(__ldg(p.n_tokens), p.max_tokens)) : 0;
+  const int filled = p.history_out ? max(0, min(*p.n_tokens, p.max_tokens)) : 0;
   for (int i = tid; i < K * K; i += kThreads) {
     const int b = i / K, slot = slot0 + b;
     unsigned long long key = 0;
@@ -282,7 +282,7 @@ __device__ void choose(const BeamParams& p, int group, const Joined& j) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int c = c0 + 32 * i;
-          v[i] = c >= filled ? last : from >= 0 ? __ldg(src + c) : -1;
+          v[i] = c >= filled ? last : from >= 0 ? src[c] : -1;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)

@@ -162,7 +162,7 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
 
 // Entry t of alpha or rho: -inf behind the longest sequence and for masks.
 __device__ __forceinline__ float entry(const float* v, int t, int n) {
-  const float x = t < n ? __ldg(v + t) : -INFINITY;
+  const float x = t < n ? v[t] : -INFINITY;
   return x < kMasked ? -INFINITY : x;
 }
 

@@ -139,8 +139,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// A kernel launched behind another one of its call (launch_behind) waits for that one's end and
-// for what it wrote before it touches memory; every thread of every block.
+// A kernel that is set up while the one ahead runs (launch_behind, launch_first) waits for that
+// one's end and for what it wrote before it touches memory; every thread of every block.  No load
+// of such a kernel may be a read-only one (__ldg, const __restrict__): the compiler moves those
+// ahead of this.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

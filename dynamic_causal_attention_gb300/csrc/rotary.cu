@@ -79,22 +79,22 @@ __device__ __forceinline__ bool position(const RotaryParams& p, uint32_t n, uint
                                          int& pos) {
   pos = (int)t;
   if (p.positions) {
-    pos = __ldg(p.positions + n);
+    pos = p.positions[n];
   } else if (p.cu) {
     // the last sequence that starts at or before the row holds it, if any does
     int lo = 0, hi = p.n_seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu + mid) <= (int)t) lo = mid;
+      if (p.cu[mid] <= (int)t) lo = mid;
       else hi = mid;
     }
     if (p.n_seqs == 0) return false;
-    const int a = __ldg(p.cu + lo);
+    const int a = p.cu[lo];
     pos = (int)t - a;
-    return a <= (int)t && (int)t < __ldg(p.cu + lo + 1);
+    return a <= (int)t && (int)t < p.cu[lo + 1];
   } else if (p.seq_len) {
-    const int fresh = p.n_new ? max(0, min(__ldg(p.n_new + b), p.T)) : p.T;
-    pos = __ldg(p.seq_len + b) - fresh + (int)t;
+    const int fresh = p.n_new ? max(0, min(p.n_new[b], p.T)) : p.T;
+    pos = p.seq_len[b] - fresh + (int)t;
     return (int)t < fresh;
   }
   return true;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 16)
 #pragma unroll
     for (int e = 0; e < W; ++e) {
       // the phase modulo one turn, in 2^-64
-      const uint64_t phase = (uint64_t)(int64_t)pos * __ldg(p.turns + u * W + e);
+      const uint64_t phase = (uint64_t)(int64_t)pos * p.turns[u * W + e];
       sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[e], &c[e]);
       c[e] *= p.scale;
       s[e] *= p.scale_sin;

@@ -122,36 +122,45 @@ def test_calls_wait_for_what_writes_their_inputs(api, captured):
     gen = torch.Generator(device="cuda").manual_seed(3)
     draw = lambda *s: torch.randn(s, device="cuda", generator=gen)
     total, H, d, cu = 700, 4, 64, torch.tensor([0, 300, 700], dtype=torch.int32, device="cuda")
-    src = draw(total, 3 * H, d).bfloat16()
-    alpha, rho = draw(H, 400), draw(H, 400)
-    logits = draw(8, 50000)
-    scores = torch.zeros(8, device="cuda")
     turn = api.Rotary(d)
     layer = api.PackedAttention(H, d, [0, 1, 0, 0], max_total=total, max_seqs=2, max_len=400)
     search = api.BeamSearch(2, 4, 50000)
     big = draw(4096, 4096)
-    x, y = torch.zeros_like(src), torch.zeros_like(logits)
+    ints = lambda *s: torch.randint(0, 400, s, device="cuda", generator=gen, dtype=torch.int32)
+    # every input, and what the calls see until it is written
+    src = dict(x=draw(total, 3 * H, d).bfloat16(), cu=cu, alpha=draw(H, 400), rho=draw(H, 400),
+               at=ints(total), logits=draw(8, 50000), scores=torch.zeros(8, device="cuda"),
+               history=ints(8, 20), n=torch.tensor([7], dtype=torch.int32, device="cuda"))
+    now = {k: torch.zeros_like(t) for k, t in src.items()}
 
     def fill(slow):
-        # 4096^3 products ahead of the copy keep the calls' predecessors running
-        z = (big @ big @ big)[:1, :1] * 0 if slow else torch.zeros(1, 1, device="cuda")
-        x.copy_(src + z.nan_to_num(0.0).bfloat16())
-        y.copy_(logits + z.nan_to_num(0.0))
+        # 4096^3 products ahead of the copies keep the calls' predecessors running
+        z = (big @ big @ big)[0, 0] * 0 if slow else torch.zeros((), device="cuda")
+        z = z.nan_to_num(0.0)
+        for k, t in src.items():
+            now[k].copy_(t + z.to(t.dtype))
 
     def calls(slow, behind=None):
-        res = []
-        for call in (lambda: turn.apply(x[:, :H], x[:, H:2 * H], cu_seqlens=cu),
-                     lambda: layer.forward(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], cu, alpha, rho),
-                     lambda: search.step(y, scores)[:3]):
+        res, w = [], now
+        q, k, v = w["x"][:, :H], w["x"][:, H:2 * H], w["x"][:, 2 * H:]
+        for call in (lambda: turn.apply(q, k, cu_seqlens=w["cu"]),
+                     lambda: turn.apply(q, k, positions=w["at"]),
+                     lambda: layer.forward(q, k, v, w["cu"], w["alpha"], w["rho"]),
+                     lambda: search.step(w["logits"], w["scores"], history=w["history"],
+                                         n_tokens=w["n"])):
             fill(slow)
             if behind is not None:
                 behind.wait_stream(torch.cuda.current_stream())
                 with torch.cuda.stream(behind):
-                    y.add_(0.0)
+                    w["logits"].add_(0.0)
                 torch.cuda.current_stream().wait_stream(behind)
-            res += call()
-            x.fill_(9.0)
-            y.fill_(9.0)
+            res += [t for t in call() if t is not None]
+            for t in w.values():
+                t.zero_()
+        # (and the kernels of the backward one another)
+        fill(slow)
+        out, lse = layer.forward(q, k, v, w["cu"], w["alpha"], w["rho"])
+        res += layer.backward(q, k, v, out, lse, out, w["cu"], w["alpha"], w["rho"])[1:]
         return res
     want = calls(False)
     torch.cuda.synchronize()

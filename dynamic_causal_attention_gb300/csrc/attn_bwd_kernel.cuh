@@ -19,7 +19,7 @@ namespace {
 
 constexpr uint32_t kTmemCols = 512;
 
-template <int D>
+template <int D, bool PACKED = false>
 struct BwdSmem {
   using G = TileGeom<D>;
   // d_h = 128 leaves no free TMEM columns: dQ goes over the dP^T columns once
@@ -51,7 +51,10 @@ struct BwdSmem {
   static constexpr int OFF_BAR = OFF_DQS + DQS_BYTES;
   static constexpr int NBAR = 2 + 2 * QST + 16 + QST + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int BYTES = OFF_MISC + 16;
+  // PACKED: the CTA's items, where they are shared out (read from memory by every role, they
+  // cost 16 documents of up to 4096 tokens and 9 heads of 64 354 us in place of 336)
+  static constexpr int OFF_LIST = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int BYTES = PACKED ? OFF_LIST + (kOrderRounds + 1) * 16 : OFF_MISC + 16;
   static constexpr int SLACK = (BYTES + 1024 <= 232448) ? 1024 : 0;
   static constexpr int ALLOC = BYTES + SLACK;
   static_assert(ALLOC <= 232448, "shared memory budget exceeded");
@@ -97,7 +100,7 @@ struct BItem {
 // a few groups only, a working set that stays in L2 (the TMA reduce-adds run
 // at about half speed once their target falls out of L2); across the whole
 // list the item lengths still cycle from long to short for the snake order.
-__device__ __forceinline__ BItem decode_bwd(const BwdParams& p, int it) {
+__device__ __forceinline__ BItem decode_bwd(const BwdParams& p, int it, uint32_t) {
   BItem r;
   const int n_pairs = p.B * p.n_kv;
   const int G = p.pairs_per_group;
@@ -123,12 +126,16 @@ __device__ __forceinline__ BItem decode_bwd(const BwdParams& p, int it) {
 }
 
 // The same for sequences laid end to end (packed_prep.cu makes the items; few rounds of them are
-// shared out there, entry round * grid + cta, many go by the snake order).
-__device__ __forceinline__ BItem decode_bwd(const PackedBwdParams& p, int it) {
+// shared out there, and lie in shared memory at `list`; many go by the snake order, list 0).
+__device__ __forceinline__ BItem decode_bwd(const PackedBwdParams& p, int it, uint32_t list) {
   BItem r;
-  const int4 t = p.hdr[0] * p.n_kv <= kOrderRounds * (int)gridDim.x
-                     ? p.order[it]
-                     : packed_bwd_item(p.items, p.hdr[0], it);
+  int4 t;
+  if (list) {
+    const uint4 x = lds_u32x4(list + 16 * it);
+    t = make_int4((int)x.x, (int)x.y, (int)x.z, (int)x.w);
+  } else {
+    t = packed_bwd_item(p.items, p.hdr[0], it);
+  }
   r.b = 0;
   r.kv = t.z >> 16;
   r.J = t.z & 0xffff;
@@ -142,15 +149,14 @@ __device__ __forceinline__ BItem decode_bwd(const PackedBwdParams& p, int it) {
 }
 
 // Item of round k of this CTA, or one behind the last.
-__device__ __forceinline__ int bwd_item(const BwdParams&, int k, int) {
+__device__ __forceinline__ int bwd_item(const BwdParams&, int k, int, uint32_t) {
   return snake_item(k, blockIdx.x, gridDim.x);
 }
-__device__ __forceinline__ int bwd_item(const PackedBwdParams& p, int k, int n_items) {
-  if (p.hdr[0] * p.n_kv > kOrderRounds * (int)gridDim.x)
-    return snake_item(k, blockIdx.x, gridDim.x);
-  // (the list ends with a round of empty entries)
-  const int it = k * (int)gridDim.x + (int)blockIdx.x;
-  return p.order[it].y > 0 ? it : n_items;
+__device__ __forceinline__ int bwd_item(const PackedBwdParams&, int k, int n_items,
+                                        uint32_t list) {
+  if (!list) return snake_item(k, blockIdx.x, gridDim.x);
+  // (the list ends with an empty entry)
+  return (int)lds_u32(list + 16 * k + 4) > 0 ? k : n_items;
 }
 
 template <bool PACKED>
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(512, 1)
                        const __grid_constant__ CUtensorMap tm_dq,
                        const std::conditional_t<PACKED, PackedBwdParams, BwdParams> p) {
   using G = TileGeom<D>;
-  using L = BwdSmem<D>;
+  using L = BwdSmem<D, PACKED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -269,7 +275,16 @@ __global__ void __launch_bounds__(512, 1)
     tma_prefetch_desc(&tm_v);
     tma_prefetch_desc(&tm_do);
   }
-  if constexpr (PACKED) wait_for_previous();
+  uint32_t list = 0;
+  if constexpr (PACKED) {
+    wait_for_previous();
+    if (p.hdr[0] * p.n_kv <= kOrderRounds * (int)gridDim.x) {
+      list = smem_u32(smem + L::OFF_LIST);
+      if (threadIdx.x <= kOrderRounds)
+        reinterpret_cast<int4*>(smem + L::OFF_LIST)[threadIdx.x] =
+            p.order[threadIdx.x * gridDim.x + blockIdx.x];
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -280,9 +295,7 @@ __global__ void __launch_bounds__(512, 1)
   const int H = p.H, T = p.T;
   const int n_items = [&] {
     if constexpr (PACKED) {
-      // (shared out: entries of the list lie anywhere below its length)
-      const int n = p.hdr[0] * p.n_kv, listed = kOrderRounds * (int)gridDim.x;
-      return n > listed ? n : listed + (int)gridDim.x;
+      return list ? kOrderRounds + 1 : p.hdr[0] * p.n_kv;
     } else {
       return p.n_items;
     }
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(512, 1)
   // The next item of a role, n_items or more behind the last: by the snake order, or
   // (packed) as the pre-pass has shared them out.
   int round = 0;
-  auto next_item = [&] { return bwd_item(p, round++, n_items); };
+  auto next_item = [&] { return bwd_item(p, round++, n_items, list); };
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
@@ -300,7 +313,7 @@ __global__ void __launch_bounds__(512, 1)
     // per clock from L2, four about 74) and two more the -lse/-D vectors.
     uint32_t kvc = 0, qc = 0;
     for (int it = next_item(); it < n_items; it = next_item()) {
-      const BItem w = decode_bwd(p, it);
+      const BItem w = decode_bwd(p, it, list);
       const int kvrow0 = PACKED ? w.row0 : (w.b * p.H_kv + w.kv) * T;
       uint64_t* kv_bar = PACKED && w.len - w.J * 128 < 128 ? kv_tail : kv_full;
       if (lane == 0) {
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(512, 1)
     if constexpr (PACKED) {
       uint32_t qc = 0, kvt = 0, used = 0, par = 0;  // by stage: ever used, the next parity
       for (int it = next_item(); it < n_items; it = next_item()) {
-        const BItem w = decode_bwd(p, it);
+        const BItem w = decode_bwd(p, it, list);
         const int keys = w.len - w.J * 128;
         if (keys < 128) {
           mbar_wait(kv_tail, kvt & 1, wc, kSiteBProdKV);
@@ -446,11 +459,11 @@ __global__ void __launch_bounds__(512, 1)
       if constexpr (L::PS) {
         // S^T and dP^T only; warp 3 issues dV, dK and dQ.
         for (int it = next_item(); it < n_items; it = next_item()) {
-          const BItem w = decode_bwd(p, it);
+          const BItem w = decode_bwd(p, it, list);
           mbar_wait(kv_full, kvc & 1, wc, kSiteBMmaKV);
           ++kvc;
           // the previous item's last S^T/dP^T must have been loaded
-          if (it != (int)blockIdx.x) {
+          if (PACKED ? round > 1 : it != (int)blockIdx.x) {
             mbar_wait(s_free, sfc & 1, wc, kSiteBMmaS);
             ++sfc;
           }
@@ -476,7 +489,7 @@ __global__ void __launch_bounds__(512, 1)
       constexpr uint32_t id_dq = idesc_bf16(128, 128, true, true);
       uint32_t dkc = 0;
       for (int it = L::PS ? n_items : next_item(); it < n_items; it = next_item()) {
-        const BItem w = decode_bwd(p, it);
+        const BItem w = decode_bwd(p, it, list);
         mbar_wait(kv_full, kvc & 1, wc, kSiteBMmaKV);
         ++kvc;
         if (dkc > 0) mbar_wait(dk_done, (dkc - 1) & 1, wc, kSiteBMmaTS);
@@ -546,7 +559,7 @@ __global__ void __launch_bounds__(512, 1)
       constexpr uint32_t id_dq = idesc_bf16(128, D, true, true);
       uint32_t kvc = 0, qc = 0, pc = 0, dqc = 0, kdc = 0;
       for (int it = next_item(); it < n_items; it = next_item()) {
-        const BItem w = decode_bwd(p, it);
+        const BItem w = decode_bwd(p, it, list);
         mbar_wait(kv_full, kvc & 1, wc, kSiteBMmaKV);  // K_J is the B operand of dQ
         ++kvc;
         for (int t = 0; t < w.nsteps; ++t) {
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(512, 1)
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t qc = 0, sc = 0, pc = 0, kdc = 0;
     for (int it = next_item(); it < n_items; it = next_item()) {
-      const BItem w = decode_bwd(p, it);
+      const BItem w = decode_bwd(p, it, list);
       for (int t = 0; t < w.nsteps; ++t) {
         const int qs = qc % L::QST;
         mbar_wait(q_full + qs, (qc / L::QST) & 1, wc, kSiteBCmpQ);
@@ -810,7 +823,7 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t dqc = 0;
     for (int it = next_item(); it < n_items; it = next_item()) {
-      const BItem w = decode_bwd(p, it);
+      const BItem w = decode_bwd(p, it, list);
       for (int t = 0; t < w.nsteps; ++t) {
         int hq, I;
         step_of(p, w, t, hq, I);
@@ -928,12 +941,12 @@ template <int D, bool PACKED = false, class Launch>
 cudaError_t launch_dyn(const Launch& L, cudaStream_t s) {
   auto kern = bwd_dynamic_kernel<D, PACKED>;
   cudaError_t e =
-      set_max_dynamic_smem(reinterpret_cast<const void*>(kern), BwdSmem<D>::ALLOC);
+      set_max_dynamic_smem(reinterpret_cast<const void*>(kern), BwdSmem<D, PACKED>::ALLOC);
   if (e != cudaSuccess) return e;
   if (L.p.n_items == 0) return cudaSuccess;
   const int grid = L.p.n_items < L.num_sms ? L.p.n_items : L.num_sms;
   if constexpr (PACKED) {
-    return launch_behind(kern, grid, 512, BwdSmem<D>::ALLOC, s, "packed_bwd", L.tm_q, L.tm_k,
+    return launch_behind(kern, grid, 512, BwdSmem<D, true>::ALLOC, s, "packed_bwd", L.tm_q, L.tm_k,
                          L.tm_v, L.tm_do, L.tm_dq, L.p);
   } else {
     trace_begin(s);

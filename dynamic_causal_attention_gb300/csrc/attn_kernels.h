@@ -129,9 +129,9 @@ struct PackedBwdItems {
   uint8_t kv_list[kMaxHeads];
   uint16_t dyn_count[kMaxHeads];
 };
-// Up to so many rounds of the grid are shared out by cost; with more the snake order is
-// as good (the last rounds are a small part).
-constexpr int kOrderRounds = 64;
+// Up to so many rounds of the grid are shared out by cost (as many records as d_h = 128 leaves
+// shared memory for); with more the snake order is as good (the last rounds are a small part).
+constexpr int kOrderRounds = 48;
 
 // The same for sequences laid end to end (lse2 and Dvec lie by tiles: [H, nt_max * 128],
 // dq_acc and dv_acc by rows: [H or H_kv, total, d_h]; pairs_per_group counts K/V heads).

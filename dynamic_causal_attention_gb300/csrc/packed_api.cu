@@ -368,14 +368,16 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     }
     // K/V heads of a group of items.  The CTAs add into dQ's sums, and read Q and dO, of one
     // query head of each K/V head of the group at a time; half of L2 and a little more
-    // holds them (80 MB).  Up to 160 MB one group is better all the same, as items
-    // share out better: 352 us against 368 with two (9 heads of 64, 33k rows); with 245 MB
-    // three groups take 340 us, one 370 (16 heads of 64, 30k rows).
+    // holds them, about 82 MB.  Up to 160 MB one group is better all the same, as items
+    // share out better: 352 us against 368 with two (9 heads of 64, 33k rows).  With 245 MB three
+    // groups take 340 us, one 370 (16 heads of 64, 30k rows); with 201 MB two 924, three
+    // 1002 (12 heads of 128, 2 x 8192 rows); with 268 three 2370, two 2446, four 2419 (16 heads of
+    // 128, 16384 rows).
     int heads = 1;
     for (int i = 0; i < p.n_kv; ++i)
       heads = p.dyn_count[p.kv_list[i]] > heads ? p.dyn_count[p.kv_list[i]] : heads;
     const double mb = (double)p.n_kv * d.total * d.d_h * 8.0 / 1e6;
-    int groups = mb <= 160.0 ? 1 : (int)ceil(mb / 80.0);
+    int groups = mb <= 160.0 ? 1 : (int)(mb / 82.0 + 0.5);
     if (groups > p.n_kv) groups = p.n_kv;
     p.items.tiles = c.at<int4>(c.w.by_query);
     p.items.n_kv = p.n_kv;

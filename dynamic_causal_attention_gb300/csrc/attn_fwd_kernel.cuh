@@ -1223,14 +1223,16 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         const size_t orow = ((size_t)(w.b * H + w.h) * T + (size_t)w.X * 128 + r);
-        if constexpr (PACKED) {
-          const int row = w.X * 128 + r;
-          if (row < w.len) {
-            __nv_bfloat16* dst = packed_row(p, w.row0 + row, w.h) + hf * DH;
+        // (packed: a tile that ends a sequence is written row by row)
+        const bool whole = !PACKED || (L::OSTAGE && w.len - w.X * 128 >= 128);
+        if (PACKED && !whole) {
+          if constexpr (PACKED) {
+            const int row = w.X * 128 + r;
+            if (row < w.len) {
+              __nv_bfloat16* dst = packed_row(p, w.row0 + row, w.h) + hf * DH;
 #pragma unroll
-            for (int c = 0; c < DH / 16; ++c) store_row16(dst + 16 * c, o[c], 1.0f);
-            if (hf == 0 && p.lse)
-              p.lse[(size_t)w.h * p.total + w.row0 + row] = (mm + log2f(l_tot)) * kLn2;
+              for (int c = 0; c < DH / 16; ++c) store_row16(dst + 16 * c, o[c], 1.0f);
+            }
           }
         } else if constexpr (L::OSTAGE) {
           // bf16 into the staging tile, then one tensor store
@@ -1250,7 +1252,10 @@ __global__ void __launch_bounds__(384, 1)
           fence_proxy_async_smem();
           named_bar_sync(1, 256);
           if (warp == 4 && lane == 0) {
-            tma_store_2d(&tm_o, smem + L::OFF_OS, 0, (w.b * H + w.h) * T + w.X * 128);
+            if constexpr (PACKED)
+              tma_store_3d(&tm_o, smem + L::OFF_OS, 0, w.row0 + w.X * 128, w.h);
+            else
+              tma_store_2d(&tm_o, smem + L::OFF_OS, 0, (w.b * H + w.h) * T + w.X * 128);
             bulk_commit_group();
           }
         } else {
@@ -1258,7 +1263,13 @@ __global__ void __launch_bounds__(384, 1)
           for (int c = 0; c < DH / 16; ++c)
             store_row16(p.out + orow * D + hf * DH + 16 * c, o[c], 1.0f);
         }
-        if (!PACKED && hf == 0 && p.lse) p.lse[orow] = (mm + log2f(l_tot)) * kLn2;
+        if constexpr (PACKED) {
+          const int row = w.X * 128 + r;
+          if (hf == 0 && p.lse && row < w.len)
+            p.lse[(size_t)w.h * p.total + w.row0 + row] = (mm + log2f(l_tot)) * kLn2;
+        } else {
+          if (hf == 0 && p.lse) p.lse[orow] = (mm + log2f(l_tot)) * kLn2;
+        }
         tc_fence_before();
         mbar_arrive(o_empty);
         ++oc;

@@ -153,7 +153,7 @@ struct BwdLaunch {
 cudaError_t launch_bwd_dynamic(const BwdLaunch& L, cudaStream_t s);
 
 struct PackedFwdLaunch {
-  CUtensorMap tm_q, tm_k, tm_v, tm_o;  // 3-D views [heads, rows, d_h] (tm_o is not used)
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;  // 3-D views [heads, rows, d_h] (tm_o: d_h = 64)
   PackedFwdParams p;
   int d_h, num_sms;
 };

@@ -275,7 +275,9 @@ saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_rows* Q, c
   if (!encode(&L.tm_q, dyn ? *Q : *V, d, dyn ? d.H : d.H_kv) ||
       !encode(&L.tm_k, dyn ? *K : *V, d, d.H_kv) || !encode(&L.tm_v, *V, d, d.H_kv))
     return SAF_ERR_CUDA;
-  L.tm_o = L.tm_v;
+  // (the map of out is used where a tile is staged in shared memory)
+  if (d.d_h != 64) L.tm_o = L.tm_v;
+  else if (!encode(&L.tm_o, *out, d, d.H)) return SAF_ERR_CUDA;
   L.d_h = d.d_h;
   L.num_sms = sm_count();
   SAF_TRY(launch_packed_fwd(L, false, c.s));

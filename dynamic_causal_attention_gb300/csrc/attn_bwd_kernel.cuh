@@ -54,7 +54,7 @@ struct BwdSmem {
   // PACKED: the CTA's items, where they are shared out (read from memory by every role, they
   // cost 16 documents of up to 4096 tokens and 9 heads of 64 354 us in place of 336)
   static constexpr int OFF_LIST = (OFF_MISC + 16 + 15) / 16 * 16;
-  static constexpr int BYTES = PACKED ? OFF_LIST + (kOrderRounds + 1) * 16 : OFF_MISC + 16;
+  static constexpr int BYTES = PACKED ? OFF_LIST + (order_rounds(D) + 1) * 16 : OFF_MISC + 16;
   static constexpr int SLACK = (BYTES + 1024 <= 232448) ? 1024 : 0;
   static constexpr int ALLOC = BYTES + SLACK;
   static_assert(ALLOC <= 232448, "shared memory budget exceeded");
@@ -278,9 +278,9 @@ __global__ void __launch_bounds__(512, 1)
   uint32_t list = 0;
   if constexpr (PACKED) {
     wait_for_previous();
-    if (p.hdr[0] * p.n_kv <= kOrderRounds * (int)gridDim.x) {
+    if (p.hdr[0] * p.n_kv <= order_rounds(D) * (int)gridDim.x) {
       list = smem_u32(smem + L::OFF_LIST);
-      if (threadIdx.x <= kOrderRounds)
+      if (threadIdx.x <= order_rounds(D))
         reinterpret_cast<int4*>(smem + L::OFF_LIST)[threadIdx.x] =
             p.order[threadIdx.x * gridDim.x + blockIdx.x];
     }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(512, 1)
   const int H = p.H, T = p.T;
   const int n_items = [&] {
     if constexpr (PACKED) {
-      return list ? kOrderRounds + 1 : p.hdr[0] * p.n_kv;
+      return list ? order_rounds(D) + 1 : p.hdr[0] * p.n_kv;
     } else {
       return p.n_items;
     }

@@ -129,15 +129,15 @@ struct PackedBwdItems {
   uint8_t kv_list[kMaxHeads];
   uint16_t dyn_count[kMaxHeads];
 };
-// Up to so many rounds of the grid are shared out by cost (as many records as d_h = 128 leaves
-// shared memory for); with more the snake order is as good (the last rounds are a small part).
-constexpr int kOrderRounds = 48;
+// Up to so many rounds of the grid a CTA's records lie in its shared memory (d_h = 128 leaves room
+// for 49); with more they go by the snake order and are read from memory.
+constexpr int order_rounds(int d_h) { return d_h == 128 ? 48 : 192; }
 
 // The same for sequences laid end to end (lse2 and Dvec lie by tiles: [H, nt_max * 128],
 // dq_acc and dv_acc by rows: [H or H_kv, total, d_h]; pairs_per_group counts K/V heads).
 struct PackedBwdParams : BwdParams {
   const int* hdr;      // {tiles, ...}
-  const int4* order;   // [kOrderRounds + 1, grid] (row0, len, J | kv << 16, tile0), len 0: none
+  const int4* order;   // [order_rounds + 1, grid] (row0, len, J | kv << 16, tile0), len 0: none
   PackedBwdItems items;
   int total, nt_max;
   int64_t dk_row, dk_head, dv_row, dv_head;

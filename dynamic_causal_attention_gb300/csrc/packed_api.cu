@@ -72,7 +72,7 @@ PackedWs packed_ws(const saf_packed_dims& d, bool backward) {
   w.row_vals = take(b * H * T * 4);
   w.dq_acc = take(b * H * d.total * d.d_h * 4);
   w.dv_acc = take(b * d.H_kv * d.total * d.d_h * 4);
-  w.order = take(b * (kOrderRounds + 1) * 256 * 16);
+  w.order = take(b * (order_rounds(d.d_h) + 1) * 256 * 16);
   w.total = off;
   return w;
 }

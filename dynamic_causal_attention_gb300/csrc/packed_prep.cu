@@ -311,7 +311,10 @@ __device__ __forceinline__ int place_of(uint32_t key, const uint32_t* keys, int 
 // step costs 2, an item's beginning and end 1.  (By the snake order 16 % of the SMs' time was
 // idle with 16 documents of up to 4096 tokens and 9 heads of 64, 17 % with 3 of up to 8192 and
 // 8 K/V heads: 397 and 793 us against 368 and 695.  Items handed out as CTAs come free,
-// through a ring in shared memory to the five roles, cost each step 9 %.)
+// through a ring in shared memory to the five roles, cost each step 9 %.)  A round takes 1.5 us
+// beside the row pass; where there are many, the snake order shares out as well (400 documents
+// of up to 300 tokens and 16 heads of 64, 65 rounds: the row pass would take 135 us in place of 89).
+constexpr int kRankedRounds = 48;
 __device__ void share_out(const PackedRows& p) {
   constexpr int AHEAD = 4;  // rounds whose records are on their way
   __shared__ __align__(16) int4 ring[AHEAD][256];
@@ -319,7 +322,16 @@ __device__ void share_out(const PackedRows& p) {
   __shared__ int load_of[256], cta_at[256];
   const int tid = threadIdx.x, n_ctas = p.n_ctas, nt = p.hdr[0], n = nt * p.items.n_kv;
   const int rounds = (n + n_ctas - 1) / n_ctas;
-  if (rounds > kOrderRounds) return;
+  if (rounds > order_rounds(p.d_h)) return;
+  if (rounds > kRankedRounds) {
+#pragma unroll 4
+    for (int r = 0; r <= rounds; ++r) {
+      const int it = snake_item(r, tid, n_ctas);
+      if (tid < n_ctas)
+        p.order[r * n_ctas + tid] = it < n ? packed_bwd_item(p.items, nt, it) : make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
   // A thread's record of round r, by a copy of its own into its place of the ring (beside the row
   // pass a load takes 1.5 us: one round ahead, 16 rounds took 33 us, longer than all rows)
   auto issue = [&](int r) {

@@ -305,6 +305,13 @@ def test_more_items_than_are_shared_out(api):
     run(api, lens, 8, 8, 32, [0] * 8)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_items_than_are_ranked_or_listed(api, d):
+    """Up to 48 rounds of items are ranked by cost, up to 192 listed in shared memory (48 at 128)."""
+    lens = [(7 * i) % 12 for i in range(1100)] + [150, 300]
+    run(api, lens, 8, 8, d, [0] * 7 + [1])
+
+
 def test_rows_behind_the_longest_length(api):
     """A sequence longer than max_len: its first max_len rows are as if it ended there, the rest is
     left alone in given buffers and cleared in new ones."""

@@ -238,7 +238,7 @@ __device__ __forceinline__ Item decode_item(const PackedFwdParams& p, int it) {
 // (the first producer) takes the next number, reads the item's records and passes it on to the
 // other roles through a ring in shared memory.  Sequences of different lengths make items of
 // very different cost: the forward of 4 prompts of up to 8192 tokens (16 heads of 128) took
-// 444 us by the snake order, 427 this way; and with every role reading the records itself RINGOLD.
+// 444 us by the snake order, 424 by numbers whose records every role read itself, 417 this way.
 struct ItemRing {
   uint64_t *full, *empty;  // [kItemSlots]; empty counts the taking roles
   uint32_t rec;            // shared address of two int4 for each slot

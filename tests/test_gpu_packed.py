@@ -308,7 +308,7 @@ def test_more_items_than_are_shared_out(api):
 @pytest.mark.parametrize("d", [64, 128])
 def test_more_items_than_are_ranked_or_listed(api, d):
     """Up to 48 rounds of items are ranked by cost, up to 192 listed in shared memory (48 at 128)."""
-    lens = [(7 * i) % 12 for i in range(1100)] + [150, 300]
+    lens = [(7 * i) % 12 for i in range(1300)] + [150, 300]
     run(api, lens, 8, 8, d, [0] * 7 + [1])
 
 

@@ -1,11 +1,11 @@
 // packed_bwd.cu — the dynamic heads' backward on sequences of different lengths laid end
 // to end: the kernel of attn_bwd_kernel.cuh on the items of a plan that packed_prep.cu
 // makes on the device, shared out by cost (share_out in packed_prep.cu).  Measured: 16
-// documents of up to 4096 tokens (9 dynamic heads of 64) 353 us, 610 TFLOP/s or 31 % of the burst
-// rate; 3 of up to 8192 (12 dynamic heads of 128 over 8) 700 us, 850 TFLOP/s.  With equal lengths as
-// fast as the kernel for those.  Shorter sequences make shorter items, and K_J and V_J of
-// an item cannot come before the last products of the one before have read theirs: no
-// shared memory is left for a second pair.
+// documents of up to 4096 tokens (9 dynamic heads of 64) 336 us, 640 TFLOP/s or 33 % of the
+// burst rate; 3 of up to 8192 (12 dynamic heads of 128 over 8) 692 us, 860 TFLOP/s.  With equal
+// lengths as fast as the kernel for those or 2 % faster.  Shorter sequences make shorter items,
+// and K_J and V_J of an item cannot come before the last products of the one before have read
+// theirs (its beginning and end cost about 3 steps).
 #include "attn_bwd_kernel.cuh"
 
 namespace saf {

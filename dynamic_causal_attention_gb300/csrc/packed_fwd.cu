@@ -1,11 +1,10 @@
 // packed_fwd.cu — the forward of the hybrid layer on sequences of different lengths laid
 // end to end, and the frozen heads' dV: the fused kernel of attn_fwd_kernel.cuh on
 // the items of a plan that packed_prep.cu makes on the device, handed out as CTAs come
-// free.  Measured: 4 prompts of up to 8192 tokens (16 heads of 128 over 4, 4 frozen) 424 us,
-// 1230 TFLOP/s or 63 % of the burst rate; 16 of up to 4096 (12 heads of 64, 3 frozen) 151 us,
-// 590 TFLOP/s.
-// With equal lengths it takes 2 to 8 % longer than the kernel for those: a tile's record is
-// read from memory, and a frozen head's tile serves two sequences only where both have it.
+// free.  Measured: 4 prompts of up to 8192 tokens (16 heads of 128 over 4, 4 frozen) 415 us,
+// 1256 TFLOP/s or 64 % of the burst rate; 16 of up to 4096 (12 heads of 64, 3 frozen) 144 us,
+// 617 TFLOP/s.  With equal lengths it takes up to 3 % longer than the kernel for those: an item
+// is claimed and passed on before it begins.
 // The frozen heads' dV takes 49 us of the latter's documents; 63 with a tile for one sequence.
 #include "attn_fwd_kernel.cuh"
 

@@ -313,7 +313,7 @@ __device__ __forceinline__ int place_of(uint32_t key, const uint32_t* keys, int 
 // 8 K/V heads: 397 and 793 us against 368 and 695.  Items handed out as CTAs come free,
 // through a ring in shared memory to the five roles, cost each step 9 %.)  A round takes 1.5 us
 // beside the row pass; where there are many, the snake order shares out as well (400 documents
-// of up to 300 tokens and 16 heads of 64, 65 rounds: the row pass would take 135 us in place of 89).
+// of up to 300 tokens and 16 heads of 64: the row pass would take 135 us in place of 89).
 constexpr int kRankedRounds = 48;
 __device__ void share_out(const PackedRows& p) {
   constexpr int AHEAD = 4;  // rounds whose records are on their way
@@ -328,7 +328,8 @@ __device__ void share_out(const PackedRows& p) {
     for (int r = 0; r <= rounds; ++r) {
       const int it = snake_item(r, tid, n_ctas);
       if (tid < n_ctas)
-        p.order[r * n_ctas + tid] = it < n ? packed_bwd_item(p.items, nt, it) : make_int4(0, 0, 0, 0);
+        p.order[r * n_ctas + tid] =
+            it < n ? packed_bwd_item(p.items, nt, it) : make_int4(0, 0, 0, 0);
     }
     return;
   }

@@ -1,5 +1,5 @@
 // attn_fwd_kernel.cuh — the fused forward kernel of the hybrid layer (K2): a
-// template that attn_fwd.cu builds for batches of one length and packed_attn.cu
+// template that attn_fwd.cu builds for batches of one length and packed_fwd.cu
 // for sequences of different lengths laid end to end.
 #pragma once
 

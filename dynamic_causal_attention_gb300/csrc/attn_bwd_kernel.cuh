@@ -1,5 +1,5 @@
 // attn_bwd_kernel.cuh — the dynamic heads' backward kernel (K4): a template that
-// attn_bwd.cu builds for batches of one length and packed_attn.cu for sequences of
+// attn_bwd.cu builds for batches of one length and packed_bwd.cu for sequences of
 // different lengths laid end to end.  attn_bwd.cu describes it.
 #pragma once
 

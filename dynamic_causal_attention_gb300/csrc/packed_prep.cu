@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 // Place of a key among the block's keys (all different, those behind n the largest).
 __device__ __forceinline__ int place_of(uint32_t key, const uint32_t* keys, int n) {
   int below = 0;
-#pragma unroll 4
+#pragma unroll 19  // (half of 152 CTAs' keys in flight: 16 rounds 4 us shorter than by fours)
   for (int i = 0; i < n; i += 4) {
     const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
     below += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);

@@ -43,22 +43,28 @@ struct PlanShared {
   unsigned long long longest;       // (rows, first tile) of the longest sequence
 };
 
-// Inclusive suffix sums of v[0 .. n) into out[i] = sum of v[j], j >= i (or j > i), by one warp.
-template <class F>
-__device__ int warp_suffix(int n, int* out, bool exclusive, F value) {
+// Suffix sums of value(0 .. n - 1), two at a time: put(i, sums of j >= i, value(i)), by one
+// warp.  The sums of all come back.
+template <class F, class G>
+__device__ int2 warp_suffix(int n, F value, G put) {
   const int lane = threadIdx.x & 31;
-  int carry = 0;
+  int2 carry = make_int2(0, 0);
   for (int base = (n - 1) / 32 * 32; base >= 0; base -= 32) {
     const int i = base + lane;
-    const int v = i < n ? value(i) : 0;
-    int s = v;
+    const int2 v = i < n ? value(i) : make_int2(0, 0);
+    int2 s = v;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const int t = __shfl_down_sync(0xffffffffu, s, o);
-      if (lane + o < 32) s += t;
+      const int tx = __shfl_down_sync(0xffffffffu, s.x, o);
+      const int ty = __shfl_down_sync(0xffffffffu, s.y, o);
+      if (lane + o < 32) {
+        s.x += tx;
+        s.y += ty;
+      }
     }
-    if (i < n) out[i] = carry + s - (exclusive ? v : 0);
-    carry += __shfl_sync(0xffffffffu, s, 0);
+    if (i < n) put(i, make_int2(carry.x + s.x, carry.y + s.y), v);
+    carry.x += __shfl_sync(0xffffffffu, s.x, 0);
+    carry.y += __shfl_sync(0xffffffffu, s.y, 0);
   }
   return carry;
 }
@@ -118,21 +124,27 @@ __device__ void make_plan(const PackedPrep& p, PlanShared& sh) {
     __syncthreads();
   }
   if (warp == 0) {
-    warp_suffix(m + 2, sh.cnt, false, [&](int i) { return sh.hist[i]; });
+    warp_suffix(m + 2, [&](int i) { return make_int2(sh.hist[i], 0); },
+                [&](int i, int2 s, int2) { sh.cnt[i] = s.x; });
     __syncwarp();
-    const int tiles = warp_suffix(m + 2, sh.start, true, [&](int i) { return i ? sh.cnt[i] : 0; });
+    const int tiles = sh.tiles;
     // Tiles share generated weights where there are more items than SMs; with fewer, an
     // item that carries several tiles only takes longer (dV of a K/V head of 32 and 40
     // documents of up to 300 tokens: 16.4 us shared, 11 not; of 3 of 64 and 16 documents of
     // up to 4096: 49.7 and 62.9).
     const int g = tiles * p.per_tile > p.num_sms ? p.group : 1;
-    const int groups = warp_suffix(m + 2, sh.gstart, true, [&](int i) {
-      return i ? (sh.cnt[i] + g - 1) / g : 0;
-    });
+    // places of the records and of the groups of a key: as many as larger keys have
+    const int2 all = warp_suffix(
+        m + 2,
+        [&](int i) { return i ? make_int2(sh.cnt[i], (sh.cnt[i] + g - 1) / g) : make_int2(0, 0); },
+        [&](int i, int2 s, int2 v) {
+          sh.start[i] = s.x - v.x;
+          sh.gstart[i] = s.y - v.y;
+        });
     if (lane == 0) {
       sh.group = g;
       p.hdr[0] = tiles;
-      p.hdr[1] = groups;
+      p.hdr[1] = all.y;
       p.hdr[4] = (int)(unsigned)sh.longest;
     }
   }

@@ -48,8 +48,8 @@ struct PackedRows {
   int nt_max, total, H, group_kv, d_h;
   const int* hdr;
   const int4* tiles;
-  const __nv_bfloat16 *out, *dout;
-  int64_t out_row, out_head, do_row, do_head;
+  const __nv_bfloat16 *out, *dout, *q, *k, *v;
+  int64_t out_row, out_head, do_row, do_head, q_row, q_head, k_row, k_head, v_row, v_head;
   const float* lse;          // [H, total]
   float *Dvec, *lse2;        // [H, nt_max * 128]
   float* row_vals;           // [n_static, T], by the position in a sequence

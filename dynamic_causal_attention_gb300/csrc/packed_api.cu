@@ -332,6 +332,15 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     r.out = static_cast<const __nv_bfloat16*>(out->p);
     r.out_row = row_of(*out, d);
     r.out_head = head_of(*out, d.H);
+    r.q = static_cast<const __nv_bfloat16*>(Q->p);
+    r.q_row = row_of(*Q, d);
+    r.q_head = head_of(*Q, d.H);
+    r.k = static_cast<const __nv_bfloat16*>(K->p);
+    r.k_row = row_of(*K, d);
+    r.k_head = head_of(*K, c.Hkv);
+    r.v = static_cast<const __nv_bfloat16*>(V->p);
+    r.v_row = row_of(*V, d);
+    r.v_head = head_of(*V, c.Hkv);
   }
   r.dout = static_cast<const __nv_bfloat16*>(dout->p);
   r.do_row = row_of(*dout, d);

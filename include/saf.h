@@ -565,7 +565,8 @@ SAF_API saf_status saf_packed_attn_fwd(const saf_packed_dims* dims, const saf_ro
  * are overwritten in the rows of the sequences: dK and dV sum over the query heads of
  * their group, dQ of frozen heads and dK that serve frozen heads only are 0.  alpha and
  * rho are constants here (saf_hybrid_attn_bwd has their gradients).  P and dS are rounded
- * to bf16 for their products, and rowsum(dout o out) is formed from out as it is rounded.  dQ is
+ * to bf16 for their products, and rowsum(dout o out) is formed from out as it is rounded (for a
+ * sequence's first 8 rows, where little of it would be left, from P and dP).  dQ is
  * summed in fp32 in the order in which its parts arrive, so its last bit may differ from
  * call to call; dK and dV do not. */
 SAF_API saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q,

@@ -312,6 +312,23 @@ def test_more_items_than_are_ranked_or_listed(api, d):
     run(api, lens, 8, 8, d, [0] * 7 + [1])
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("layout", ["rows", "fused", "heads"])
+def test_first_rows_see_themselves_only(api, d, layout):
+    """dQ of a sequence's first row is zero: its weight is 1 whatever Q is.  What is left of
+    P (dP - D) are fp32 sums of d products on either side (d 2^-24 of their sizes each, d <= 128)
+    and exp's 2^-20: less than 2^-15 of sum |dO| |V|, times |K| / sqrt(d) and a bf16 rounding."""
+    lens, H, Hkv = [1, 3, 200, 1, 2, 130], 4, 2
+    q, k, v, do, alpha, rho, cu, starts = inputs(lens, H, Hkv, d, layout=layout)
+    layer = api.PackedAttention(H, d, [0] * H, max_total=sum(lens), max_seqs=6, max_len=200,
+                                H_kv=Hkv)
+    out, lse = layer.forward(q, k, v, cu)
+    dq = layer.backward(q, k, v, out, lse, do, cu)[0]
+    kk, vv = (t[starts].double().repeat_interleave(2, 1) for t in (k, v))
+    size = (do[starts].double().abs() * vv.abs()).sum(-1, keepdim=True)
+    assert (dq[starts].double().abs() <= 1.01 * 2.0 ** -15 * size * kk.abs() / math.sqrt(d)).all()
+
+
 def test_rows_behind_the_longest_length(api):
     """A sequence longer than max_len: its first max_len rows are as if it ended there, the rest is
     left alone in given buffers and cleared in new ones."""

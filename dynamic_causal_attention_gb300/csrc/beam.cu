@@ -353,6 +353,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
   constexpr int PER = 16 / (int)sizeof(T);  // elements of a vector
   extern __shared__ __align__(16) uint8_t scratch[];
   __shared__ __align__(16) float tops[kThreads];  // the best K maxima of each warp
+  // The warps' maxima have a place of their own: the second pass's threshold writes `tops`
+  // while slower warps may still read them, no barrier lying between.
+  __shared__ float warp_top[kWarps];
   __shared__ unsigned long long sums[kWarps];
   __shared__ uint4 hit[kHits];
   __shared__ int hit_at[kHits];
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       block_top = fmaxf(block_top, __shfl_xor_sync(0xffffffffu, block_top, o));
-    if (lane == 0) tops[warp] = block_top;  // (the maxima there have been read)
+    if (lane == 0) warp_top[warp] = block_top;
     // NaN or +inf among the logits (they count as masked), or some beyond 2^20: all of the
     // part is gone through again, element by element
     const bool slow = __syncthreads_or(!(sum < INFINITY) || !(top < INFINITY)) != 0;
@@ -516,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         block_top = fmaxf(block_top, __shfl_xor_sync(0xffffffffu, block_top, o));
-      if (lane == 0) tops[warp] = block_top;
+      if (lane == 0) warp_top[warp] = block_top;
       __syncthreads();
     }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) block_top = fmaxf(block_top, tops[w]);
+    for (int w = 0; w < kWarps; ++w) block_top = fmaxf(block_top, warp_top[w]);
     const bool far = !(fabsf(block_top) <= kPlain);  // (also: no element)
     const float base = far ? block_top : 0.f;
     const int e_top = far ? 0 : (int)ceilf(block_top * kLog2e);

@@ -1,0 +1,74 @@
+"""The beam step where a part of a row is gone through twice: more logits than places reach the first
+tile's threshold, or NaN, infinities and logits beyond 2^20 are among them."""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    from dynamic_causal_attention_gb300 import api
+    return api
+
+
+def best(logits, scores, K):
+    """(parent, token, score in 64 bits) by score, slot, logit and token, on the GPU."""
+    x = logits.double()
+    x = torch.where((x >= -2.3e38) & (x < math.inf), x, -math.inf)
+    lse = torch.logsumexp(x, 1, keepdim=True)
+    lse = torch.where(lse == -math.inf, 0.0, lse)
+    # a slot's K best: by logit, then token (sorting keeps the order of equal ones)
+    top, token = torch.sort(x, dim=1, descending=True, stable=True)
+    top, token = top[:, :K], token[:, :K]
+    s = scores.double()
+    s = torch.where((s >= -2.3e38) & (s < math.inf), s, -math.inf)
+    score = torch.where(top == -math.inf, -math.inf, s[:, None] + (top - lse))
+    # (no offer: the fp32 score is none)
+    score = torch.where(score.float() < -2.3e38, -math.inf, score)
+    wide = score.shape[1]
+    score = score.view(-1, K * wide)
+    score, at = torch.sort(score, dim=1, descending=True, stable=True)
+    score, at = score[:, :K], at[:, :K]
+    slot = at // wide + torch.arange(score.shape[0], device=x.device)[:, None] * K
+    token = token.reshape(score.shape[0], -1).gather(1, at)
+    none = score == -math.inf
+    out = (torch.where(none, -1, slot), torch.where(none, -1, token), score)
+    if wide < K:
+        pad = lambda t, v: torch.nn.functional.pad(t, (0, K - t.shape[1]), value=v)
+        out = tuple(pad(t, v) for t, v in zip(out, (-1, -1, -math.inf)))
+    return tuple(t.flatten() for t in out)
+
+
+def rows(kind, G, K, V):
+    gen = torch.Generator().manual_seed(G + K)
+    ramp = torch.arange(V, dtype=torch.float32) / V
+    x = 30 * ramp + torch.randn((G * K, V), generator=gen)
+    if kind == "equal":
+        x = torch.zeros_like(x)
+    elif kind == "nan":
+        x[:, 5::4097] = math.nan
+        x[:, 7::9001] = math.inf
+    elif kind == "far":
+        x = torch.round(4 * x) / 4 + 2.0 ** 21
+    # (scores of different slots are 4e-6 apart or more for these seeds, but for equal rows)
+    return x.cuda(), (-7.0 * torch.arange(G * K) / K).cuda()
+
+
+@pytest.mark.parametrize("kind", ["rising", "equal", "nan", "far"])
+@pytest.mark.parametrize("G,K,V", [(64, 8, 128003), (8, 2, 50001), (16, 32, 70001)])
+def test_a_second_pass_gives_the_same_bits_every_time(api, kind, G, K, V):
+    x, s = rows(kind, G, K, V)
+    search = api.BeamSearch(G, K, V)
+    parent, token, score = search.step(x, s)[:3]
+    wp, wt, ws = best(x, s, K)
+    assert torch.equal(parent.long(), wp)
+    assert torch.equal(token.long(), wt)
+    assert ((score.double() - ws).abs() <= 2.0 ** -24 * ws.abs() + 2.0 ** -19.3).all()
+    for i in range(60):
+        again = search.step(x, s)
+        for a, b in zip((parent, token, score), again):
+            assert torch.equal(a, b), i

@@ -3,7 +3,8 @@
 // Slot b of a group offers, for every token v, the score
 //     score(b) + x(b, v) - log sum_w exp x(b, w);
 // a finished slot offers one: its score, with the ending token.  The best `beams`
-// offers of a group become its slots; equal scores go to the lower b * vocab + v.
+// offers of a group become its slots; a slot's own offers go by their logits, equal scores of
+// different slots to the lower one, equal logits to the lower token.
 //
 // The logits are read once, and that is what bounds the call.  A row is cut into
 // blocks' parts; a block goes through its part in tiles, the next one's loads in
@@ -240,18 +241,20 @@ __device__ void choose(const BeamParams& p, int group, const Joined& j) {
   }
   for (int i = tid; i < K; i += kThreads) j.chosen[i] = -1;
   __syncthreads();
+  // Equal scores go to the lower slot, and of a slot, whose offers lie here best first, to the
+  // larger logit, then the lower token: to the lower place.  (64 bits can round different logits
+  // of a slot to one score, far from 0 or beside a large log sum.)
   for (int i = tid; i < K * K; i += kThreads) {
     const unsigned long long key = j.score[i];
     if (key == 0) continue;
-    const int f = j.flat[i];
     int above = 0;  // (without branches: 64 rounds took 5 us with them)
 #pragma unroll 8
     for (int k = 0; k < K * K; ++k) {
       const unsigned long long other = j.score[k];
-      above += (int)(other > key) | ((int)(other == key) & (int)(j.flat[k] < f));
+      above += (int)(other > key) | ((int)(other == key) & (int)(k < i));
     }
     if (above < K) {
-      const int b = f / p.vocab, v = f - b * p.vocab, s = slot0 + above;
+      const int f = j.flat[i], b = f / p.vocab, v = f - b * p.vocab, s = slot0 + above;
       const unsigned long long u = key >> 63 ? key & 0x7fffffffffffffffull : ~key;
       j.chosen[above] = slot0 + b;
       j.token[above] = v;

@@ -72,3 +72,30 @@ def test_a_second_pass_gives_the_same_bits_every_time(api, kind, G, K, V):
         again = search.step(x, s)
         for a, b in zip((parent, token, score), again):
             assert torch.equal(a, b), i
+
+
+def collapse(kind, K, V):
+    gen = torch.Generator(device="cuda").manual_seed(K + V)
+    x = torch.rand((3 * K, V), device="cuda", generator=gen)
+    s = torch.full((3 * K,), -math.inf, device="cuda")
+    if kind == "far scores":          # 64 bits hold multiples of 128 there
+        s[:] = -1e18
+    elif kind == "one slot":
+        s[::K] = -1e18
+    else:                             # logits that vanish beside their log sum
+        x *= 1e-20
+        s[::K] = -1.0
+    return x, s
+
+
+@pytest.mark.parametrize("kind", ["far scores", "one slot", "tiny logits"])
+@pytest.mark.parametrize("K,V", [(1, 500), (4, 1000), (8, 40000), (32, 3001)])
+def test_offers_of_a_slot_go_by_their_logits(api, kind, K, V):
+    """Also where 64 bits give them the same score: the larger logit first, then the lower token."""
+    x, s = collapse(kind, K, V)
+    for y in (x, x.flip(1).contiguous(), x.bfloat16()):
+        parent, token, score = api.BeamSearch(3, K, V).step(y, s)[:3]
+        wp, wt, ws = best(y, s, K)
+        assert torch.equal(parent.long(), wp)
+        assert torch.equal(token.long(), wt)
+        assert ((score.double() - ws).abs() <= 2.0 ** -24 * ws.abs() + 2.0 ** -19.3).all()

@@ -534,12 +534,20 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const __grid_constant
     if (!far && !slow) {
       if (top > -INFINITY) fixed = in_units(sum, max(e_run - e_top, -200));
     } else if (block_top > -INFINITY) {
+      // sixteen terms in fp32, as in a tile, then in integers: one after another the roundings
+      // of a thread's 136 would add up to 2^-19
       float s = 0.f;
+      int n = 0;
       again([&](float y, int) {
         y -= base;
         s += fast_exp2(fmaf(y, kLog2eLo, fmaf(y, kLog2e, -(float)e_top)));
+        if (++n == 16) {
+          fixed += in_units(s, 0);
+          s = 0.f;
+          n = 0;
+        }
       });
-      fixed = in_units(s, 0);
+      fixed += in_units(s, 0);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);

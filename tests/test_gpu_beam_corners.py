@@ -99,3 +99,30 @@ def test_offers_of_a_slot_go_by_their_logits(api, kind, K, V):
         assert torch.equal(parent.long(), wp)
         assert torch.equal(token.long(), wt)
         assert ((score.double() - ws).abs() <= 2.0 ** -24 * ws.abs() + 2.0 ** -19.3).all()
+
+
+def test_sums_of_a_second_pass_are_as_exact(api):
+    """Rows of equal logits with a NaN: a thread adds 128 terms of the same value, whose roundings
+    go the same way (one after another they would add up to 2^-19).  In sixteens: 15 roundings of
+    2^-24, the function's 2^-22, its argument's 1.4 x 2^-24; scores near 0 add nothing."""
+    n, V = 1900, 32768                # one part of eight tiles a row
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    c = 6 * torch.rand((n, 1), device="cuda", generator=gen) - 3
+    x = c.expand(n, V).contiguous()
+    x[:, 777] = math.nan
+    want = math.log(V - 1)            # of the row without its logit's value
+    s = torch.full((n,), want, device="cuda")
+    parent, token, score = api.BeamSearch(n, 1, V).step(x, s)[:3]
+    assert torch.equal(parent.long(), torch.arange(n, device="cuda")) and not token.any()
+    off = (score.double() - (s.double() - want)).abs()
+    assert off.max() <= 2.0 ** -22 + 16.5 * 2.0 ** -24, float(off.max())
+    # beyond 2^20, against the largest logit
+    step = 0.25 * (1 + torch.arange(n, device="cuda") % 12)
+    x = (2.0 ** 21 - step)[:, None].expand(n, V).contiguous()
+    x[:, 0] = 2.0 ** 21
+    want = torch.log1p((V - 1) * torch.exp(-step.double()))
+    s = want.float()
+    _, token, score = api.BeamSearch(n, 1, V).step(x, s)[:3]
+    assert not token.any()
+    off = (score.double() - (s.double() - want)).abs()
+    assert off.max() <= 2.0 ** -22 + 16.5 * 2.0 ** -24, float(off.max())

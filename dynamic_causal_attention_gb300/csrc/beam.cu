@@ -231,8 +231,10 @@ __device__ void choose(const BeamParams& p, int group, const Joined& j) {
           f = b * p.vocab + p.end;
         }
       } else if (j.best[i] != 0) {
+        // (an offer whose score is none in fp32 would be a slot that never goes on)
         const Best best = best_of(j.best[i]);
-        key = key_of((double)start + ((double)best.x - j.lse[b]));
+        const double score = (double)start + ((double)best.x - j.lse[b]);
+        key = alive((float)score) ? key_of(score) : 0;
         f = b * p.vocab + best.v;
       }
     }

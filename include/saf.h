@@ -600,9 +600,9 @@ SAF_API size_t saf_beam_workspace_size(const saf_beam_dims* dims);
  * over the slot's logits x, in which NaN, +inf and values below -2.3e38 (the type's lowest, as a
  * mask) count as -inf; a finished slot offers the token `end` at its own score;
  * a slot whose score is -inf (or as above) offers nothing.  The group's best
- * `beams` offers, best first, become its slots; offers without weight (-inf) never
- * do.  Scores are compared in 64 bits, offers of one slot by their logits; equal
- * ones go to the lower slot, then the lower token.
+ * `beams` offers, best first, become its slots; offers without weight (-inf, or a score
+ * that comes out below -2.3e38) never do.  Scores are compared in 64 bits, offers of one
+ * slot by their logits; equal ones go to the lower slot, then the lower token.
  *
  *   logits      [n_groups * beams, vocab], rows row_stride apart; rows of finished
  *               and dead slots are not read.

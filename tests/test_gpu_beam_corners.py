@@ -126,3 +126,26 @@ def test_sums_of_a_second_pass_are_as_exact(api):
     assert not token.any()
     off = (score.double() - (s.double() - want)).abs()
     assert off.max() <= 2.0 ** -22 + 16.5 * 2.0 ** -24, float(off.max())
+
+
+def test_scores_that_leave_the_type_are_no_offers(api):
+    """An offer whose score would be -inf in fp32, or below what a score counts from, is none: the
+    slot would have a parent but never go on."""
+    x = torch.tensor([[0.0, -1e37, -2e38, -1e38], [0.0, -2.2e38, -2e38, -2e38]], device="cuda")
+    s = torch.tensor([-2e38, -2.25e38], device="cuda")
+    parent, token, score = api.BeamSearch(1, 2, 4).step(x, s)[:3]
+    assert parent.tolist() == [0, 0] and token.tolist() == [0, 1]
+    x[0, 1] = -1.5e38
+    parent, token, score = api.BeamSearch(1, 2, 4).step(x, s)[:3]
+    assert parent.tolist() == [0, 1] and token.tolist() == [0, 0]
+    s[1] = -math.inf
+    parent, token, score = api.BeamSearch(1, 2, 4).step(x, s)[:3]
+    assert parent.tolist() == [0, -1] and token.tolist() == [0, -1]
+    assert score[1] == -math.inf
+    x = torch.where(x == 0, 0.0, -2.2e38)
+    K = 4
+    x, s = x[:1].expand(2 * K, 4).contiguous(), torch.full((2 * K,), -2e38, device="cuda")
+    parent, token, score = api.BeamSearch(2, K, 4).step(x, s)[:3]
+    wp, wt, ws = best(x, s, K)
+    assert torch.equal(parent.long(), wp) and torch.equal(token.long(), wt)
+    assert torch.equal(score == -math.inf, wp < 0)

@@ -134,7 +134,8 @@ struct PackedBwdItems {
 constexpr int order_rounds(int d_h) { return d_h == 128 ? 48 : 192; }
 
 // The same for sequences laid end to end (lse2 and Dvec lie by tiles: [H, nt_max * 128],
-// dq_acc and dv_acc by rows: [H or H_kv, total, d_h]; pairs_per_group counts K/V heads).
+// dq_acc and dv_acc by rows: [H or H_kv, total, d_h]).  The K/V heads and the size of their groups
+// are those of `items`; pairs_per_group and kv_list of the base are not set.
 struct PackedBwdParams : BwdParams {
   const int* hdr;      // {tiles, ...}
   const int4* order;   // [order_rounds + 1, grid] (row0, len, J | kv << 16, tile0), len 0: none

@@ -375,7 +375,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
       for (int h = kv * c.g; h < (kv + 1) * c.g; ++h)
         if (!c.hs.is_static[h]) p.dyn_by_kv[n++] = (uint8_t)h;
       p.dyn_count[kv] = (uint16_t)(n - p.dyn_begin[kv]);
-      if (p.dyn_count[kv] > 0) p.kv_list[p.n_kv++] = (uint8_t)kv;
+      if (p.dyn_count[kv] > 0) p.items.kv_list[p.n_kv++] = (uint8_t)kv;
     }
     // K/V heads of a group of items.  The CTAs add into dQ's sums, and read Q and dO, of one
     // query head of each K/V head of the group at a time; half of L2 and a little more
@@ -386,7 +386,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     // 128, 16384 rows).
     int heads = 1;
     for (int i = 0; i < p.n_kv; ++i)
-      heads = p.dyn_count[p.kv_list[i]] > heads ? p.dyn_count[p.kv_list[i]] : heads;
+      heads = p.dyn_count[p.items.kv_list[i]] > heads ? p.dyn_count[p.items.kv_list[i]] : heads;
     const double mb = (double)p.n_kv * d.total * d.d_h * 8.0 / 1e6;
     int groups = mb <= 160.0 ? 1 : (int)(mb / 82.0 + 0.5);
     if (groups > p.n_kv) groups = p.n_kv;
@@ -395,7 +395,6 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     p.items.per_group = (p.n_kv + groups - 1) / groups;
     p.items.most_steps = heads * tiles_of(d.max_len);
     p.items.even = n == heads * p.n_kv;
-    memcpy(p.items.kv_list, p.kv_list, sizeof(p.kv_list));
     memcpy(p.items.dyn_count, p.dyn_count, sizeof(p.dyn_count));
     p.n_items = items_for(c, p.n_kv);
     bl.num_sms = sm_count() < 256 ? sm_count() : 256;

@@ -371,11 +371,16 @@ __global__ void __launch_bounds__(512, 1)
     // ---------------------------------------------------------- ends of sequences
     if constexpr (PACKED) {
       uint32_t qc = 0, kvt = 0, used = 0, par = 0;  // by stage: ever used, the next parity
+      // This warp passes over whole tiles without a wait, so its next wait may take as long as all
+      // the steps in between (a short sequence's items come behind all others').  Each of
+      // those is bounded by the other roles' waits, which abort the CTA.
+      unsigned long long passed = 1;
       for (int it = next_item(); it < n_items; it = next_item()) {
         const BItem w = decode_bwd(p, it, list);
         const int keys = w.len - w.J * 128;
         if (keys < 128) {
-          mbar_wait(kv_tail, kvt & 1, wc, kSiteBProdKV);
+          mbar_wait(kv_tail, kvt & 1, wc, kSiteBProdKV, passed * kWaitTimeoutNs);
+          passed = 1;
           ++kvt;
           G::zero_rows(sK, keys, lane);
           G::zero_rows(sV, keys, lane);
@@ -388,9 +393,11 @@ __global__ void __launch_bounds__(512, 1)
           step_of(p, w, t, hq, I);
           const uint32_t qs = qc % L::QST;
           ++qc;
+          ++passed;
           const int rows = w.len - I * 128;
           if (rows >= 128) continue;
-          mbar_wait(q_tail + qs, (par >> qs) & 1, wc, kSiteBProdQ);
+          mbar_wait(q_tail + qs, (par >> qs) & 1, wc, kSiteBProdQ, passed * kWaitTimeoutNs);
+          passed = 1;
           par ^= 1u << qs;
           used |= 1u << qs;
           const uint32_t st = smem_u32(smem + L::OFF_Q + qs * L::STAGE);

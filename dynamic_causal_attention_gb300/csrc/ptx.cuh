@@ -79,7 +79,8 @@ static __device__ __noinline__ void wait_timed_out(const WaitCtl& w, int site) {
 // Wait until the phase with parity `parity` of `bar` has completed.  Returns
 // false if the wait was abandoned (timeout or CTA abort).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w,
-                                          int site) {
+                                          int site,
+                                          unsigned long long limit_ns = kWaitTimeoutNs) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = global_timer_ns();
@@ -88,7 +89,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(a, parity)) return true;
     if (*w.abort) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+    if (global_timer_ns() - t0 > limit_ns) {
       wait_timed_out(w, site);
       return false;
     }

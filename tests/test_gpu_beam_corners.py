@@ -149,3 +149,21 @@ def test_scores_that_leave_the_type_are_no_offers(api):
     wp, wt, ws = best(x, s, K)
     assert torch.equal(parent.long(), wp) and torch.equal(token.long(), wt)
     assert torch.equal(score == -math.inf, wp < 0)
+
+
+# ---- limits
+@pytest.mark.parametrize("G,K,V,dtype", [(1, 32, 1 << 22, torch.bfloat16), (2, 2, 1 << 22, torch.float32),
+                                         (1, 1, 1 << 22, torch.float32), (3, 23, (1 << 21) + 5, torch.float32),
+                                         (30000, 3, 40, torch.float32), (100000, 1, 7, torch.bfloat16)])
+def test_largest_vocabulary_and_many_groups(api, G, K, V, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn((G * K, V), device="cuda", generator=gen).to(dtype)
+    s = -40.0 * (torch.arange(G * K, device="cuda") % K)   # (the slots' offers do not meet)
+    x[:, V // 2] += 3.0
+    search = api.BeamSearch(G, K, V)
+    for i in range(2):
+        parent, token, score = search.step(x, s)[:3]
+    wp, wt, ws = best(x, s, K)
+    assert torch.equal(parent.long(), wp)
+    assert torch.equal(token.long(), wt)
+    assert ((score.double() - ws).abs() <= 2.0 ** -24 * ws.abs() + 2.0 ** -19.3).all()

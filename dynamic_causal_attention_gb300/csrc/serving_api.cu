@@ -118,6 +118,10 @@ saf_status saf_rotary(const saf_rotary_dims* dims, const saf_rows* q, const saf_
       in_place &= same;
     }
   }
+  // one tensor's output in the place of the other (x: q, k, q_out, k_out)
+  if (d.H > 0 && d.H_k > 0 &&
+      (p.x[2].p == p.x[1].p || p.x[3].p == p.x[0].p || p.x[2].p == p.x[3].p))
+    return SAF_ERR_INVALID_ARG;
   p.B = d.B;
   p.T = d.T;
   p.H = d.H;

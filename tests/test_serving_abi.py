@@ -228,3 +228,17 @@ def test_packed_workspace_never_grows_with_less(B):
         for less in (dict(total=4999), dict(total=100), dict(n_seqs=39), dict(n_seqs=0),
                      dict(max_len=2872), dict(max_len=1), dict(total=0)):
             assert 0 < size(back, **less) <= full, less
+
+
+def test_rotary_outputs_in_the_place_of_the_other_tensor(B):
+    """q_out where k or k_out lies, and the other way round: threads of other heads would read what
+    is written."""
+    rows = lambda p: B.saf_rows(p, 4096, 256, 64)
+    q, k, a, b = rows(1 << 20), rows(1 << 21), rows(1 << 22), rows(1 << 23)
+    dims = B.saf_rotary_dims(2, 8, 4, 4, 64, 64, 0)
+    for out_q, out_k in ((a, a), (q, q), (k, q), (k, k), (k, b), (a, q)):
+        assert B.saf_rotary(dims, q, k, out_q, out_k, 16, 1.0, None, None, 0, None, None, 0,
+                            None) == B.SAF_ERR_INVALID_ARG
+    # one tensor for both, each in its own place
+    assert B.saf_rotary(dims, q, q, q, q, 16, 1.0, None, None, 0, None, None, 0,
+                        None) == B.SAF_ERR_INVALID_ARG

@@ -120,11 +120,12 @@ def roofline_of(cfg, kernels, region_s, peaks, sm_mhz=None):
 
 # Source files that define each timed kernel: a recorded DRAM-traffic figure
 # counts only while these are unchanged.
+_SHARED = ("attn_common.cuh", "ptx.cuh", "attn_kernels.h")
 KERNEL_SOURCES = {
-    "hybrid_fwd": ("attn_fwd.cu", "attn_common.cuh", "ptx.cuh", "attn_kernels.h"),
-    "static_dv": ("attn_fwd.cu", "attn_common.cuh", "ptx.cuh", "attn_kernels.h"),
-    "bwd_dynamic": ("attn_bwd.cu", "attn_common.cuh", "ptx.cuh", "attn_kernels.h"),
-    "param_grad": ("attn_bwd.cu", "attn_common.cuh", "ptx.cuh", "attn_kernels.h"),
+    "hybrid_fwd": ("attn_fwd.cu", "attn_fwd_kernel.cuh", *_SHARED),
+    "static_dv": ("attn_fwd.cu", "attn_fwd_kernel.cuh", *_SHARED),
+    "bwd_dynamic": ("attn_bwd.cu", "attn_bwd_kernel.cuh", *_SHARED),
+    "param_grad": ("attn_bwd.cu", "attn_bwd_kernel.cuh", *_SHARED),
 }
 
 

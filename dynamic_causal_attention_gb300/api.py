@@ -586,7 +586,10 @@ class PackedAttention(_OnDevice):
     do) are sequence s; frozen heads (``head_is_static``, host booleans) count their pattern's
     positions from its first row.  A call has at most ``max_total`` rows and ``max_seqs``
     sequences of at most ``max_len`` rows; with ``backward`` the workspace has room for the
-    gradients' sums.  Nothing synchronises, and every call can be captured in a CUDA graph.
+    gradients' sums.  Every call makes the frozen heads' tables for ``max_len`` rows, so it had
+    better be near the longest sequence (with it at 4096 they take 2 us beside the rest; at 131072 a
+    call on short prompts takes 0.3 ms, and 33 where alpha + rho range over more than 80).
+    Nothing synchronises, and every call can be captured in a CUDA graph.
     Calls share the object's workspace, so they belong on one stream at a time.
     """
 

@@ -13,10 +13,12 @@
 // are listed, and the best K of the list are the part's.  The last block of a row joins
 // the row's parts, the last row of a group chooses (a counter each, which its last
 // block sets back to zero for the next call).
-// Measured: 64 groups of 8 beams over 128003 fp32 logits (a fifth of the slots finished), 56 us:
-// about 40 at the rate at which the other slots' 214 MB come (5.3 TB/s), the last blocks'
-// join and choice 8, their histories of 1000 tokens 4.  12 x 4 beams over 50001 15 us, 1 x 4 over
-// 32000 12 us: a chain of latencies (tile 2 us, join 4, choice 2, two fences and counters).
+// Measured: 64 groups of 8 beams over 128003 fp32 logits (a fifth of the slots finished), 55 us
+// where the other slots' 210 MB take 32 at the copy rate: about 40 until they have come (5.3 TB/s),
+// the last blocks' join and choice 8, their histories of 1000 tokens 4.  The same in bf16 52 us, of
+// 105 MB (16 us): as many logits at half the bytes, so it is bound by its instructions (65 % of the
+// issue slots, 53 in fp32).  12 x 4 beams over 50001 15 us, 1 x 4 over 32000 12 us: a chain of
+// latencies (tile 2 us, join 4, choice 2, two fences and counters).
 //
 // Which of two offers is better should not hang on the rounding of a sum of 10^5
 // exponentials.  An exponential is 2^(x log2 e - E) with the thread's exponent

@@ -383,7 +383,7 @@ saf_status saf_packed_attn_bwd(const saf_packed_dims* dims, const saf_rows* Q, c
     // share out better: 352 us against 368 with two (9 heads of 64, 33k rows).  With 245 MB three
     // groups take 340 us, one 370 (16 heads of 64, 30k rows); with 201 MB two 924, three
     // 1002 (12 heads of 128, 2 x 8192 rows); with 268 three 2370, two 2446, four 2419 (16 heads of
-    // 128, 16384 rows).
+    // 128, 16384 rows).  (Nothing was measured between 154 and 201 MB.)
     int heads = 1;
     for (int i = 0; i < p.n_kv; ++i)
       heads = p.dyn_count[p.items.kv_list[i]] > heads ? p.dyn_count[p.items.kv_list[i]] : heads;

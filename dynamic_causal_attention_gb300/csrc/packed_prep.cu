@@ -12,7 +12,10 @@
 //   then         the frozen heads' generator tables, 128 entries a block
 //   the last     rows of no sequence, cleared where asked
 // 7 us for 16 sequences with its launch: of that a chain of scans by one block 3, beside tables of
-// 4096 entries (2).
+// 4096 entries (2).  The tables are made for max_len, whatever the batch's longest sequence: each
+// block looks for the range over all of it, and a head whose range needs the exact exponentials
+// forms log Z of every row.  Forward of six prompts of up to 100 tokens, 12 heads (3 frozen): 12 us with
+// max_len 4096, 34 with 32768, 270 with 131072; with such heads 126 us, 3.1 and 33 ms.
 // packed_pre / packed_post: the backward's row passes (D = rowsum(dO o O), -lse log2 e,
 // zeros of dQ's accumulator; dQ from it), by tiles and heads.
 #include <cuda_bf16.h>

@@ -592,7 +592,8 @@ typedef struct saf_beam_dims {
 
 /* Bytes of device workspace for saf_beam_step; 0 for dims that it does not take.
  * The workspace must be zero before its first use (a call leaves its counters at
- * zero again); calls that share one must not overlap, nor may their dims differ. */
+ * zero again); calls that share one must not overlap, nor may their n_groups, beams
+ * or vocab differ. */
 SAF_API size_t saf_beam_workspace_size(const saf_beam_dims* dims);
 
 /* One step.  Slot b of a group offers every token v with the score
